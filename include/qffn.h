@@ -74,7 +74,8 @@ int qffn_abi_version(void);
 qffn_status qffn_check_status(qffn_stream_t stream);
 
 /* Measurement aid (no counterpart on the pages).  Synchronises `stream`, then
- * writes, for the most recent GEMM launch on the current device, the SM clock
+ * writes, for the most recent launch of the FP8 GEMMs on the current device
+ * (qffn_linear* and qffn_gated_linear* record none), the SM clock
  * cycles (%clock64) and the nanoseconds (%globaltimer) that its first CTA
  * spent from its start to its end: out[0] / out[1] is the mean SM clock of
  * that launch in GHz.  With the tensor cores' dense FP8 rate of 16384 FLOP
@@ -336,6 +337,136 @@ qffn_status qffn_ffn_backward(uint16_t* d_ln2, uint16_t* dw1, uint16_t* dw2, flo
                               const uint8_t* w1, const float* w1_scale, const uint8_t* w2,
                               const float* w2_scale, int64_t N, int64_t C, int64_t H, int accumulate,
                               void* workspace, size_t workspace_bytes, qffn_stream_t stream);
+
+/* ---- Layer norm and the norms' backward -------------------------------------
+ * The layer norm beside qffn_rmsnorm_absmax, and the step of [llmq-model]
+ * _backward_block that follows the gradients of the projections: the fused
+ * residual norm's backward (rmsnorm_backward there).  All sums are fp32. */
+
+/* Fused residual add + layer norm + abs-max, with r = bf16(res_in + x) (or x
+ * when res_in == NULL):
+ *   res_out[N,C] = r                                       (skipped if res_in == NULL)
+ *   mean[N] = sum_C(r) / C;  rstd[N] = 1 / sqrt(sum_C((r - mean)^2) / C + eps)
+ *   y[N,C]  = bf16((r - mean) * rstd * gain + shift)       (shift == NULL: no shift)
+ *   stats[0] = max |y|   (zeroed first; stats == NULL records nothing)
+ * res_out may alias res_in or x.  N >= 0, C % 8 == 0, 8 <= C <= 16384; eps >= 0
+ * and finite. */
+qffn_status qffn_layernorm_absmax(uint16_t* res_out, uint16_t* y, float* mean, float* rstd,
+                                  float* stats, const uint16_t* res_in, const uint16_t* x,
+                                  const uint16_t* gain, const uint16_t* shift, float eps, int64_t N,
+                                  int64_t C, qffn_stream_t stream);
+
+/* Backward of qffn_layernorm_absmax, for the gradient dy of y and (optional)
+ * the gradient dres that reaches r along the residual stream.  r, mean and
+ * rstd are those of the forward.  With xhat = (r - mean) * rstd, w = dy * gain:
+ *   dx[N,C]   = bf16(dres + rstd * (w - sum_C(w) / C - xhat * sum_C(w * xhat) / C))
+ *   dgain[C]  = sum_N(dy * xhat);  dshift[C] = sum_N(dy)   (fp32; added to the
+ *               previous contents when accumulate != 0; dshift may be NULL)
+ *   stats[0]  = max |dx|   (zeroed first; NULL records nothing), the abs-max
+ *               that qffn_backward_qmm of the layer before quantises dx with
+ * dx is the gradient of both inputs of the residual sum.  dx may alias dy or
+ * dres.  The column sums are added in a fixed order (no atomics): the same
+ * bits in every run.  workspace: >= qffn_norm_backward_workspace_size() bytes,
+ * 256-byte aligned, any content.  Two launches.  Shape rules of
+ * qffn_layernorm_absmax. */
+size_t qffn_norm_backward_workspace_size(int64_t N, int64_t C);
+qffn_status qffn_layernorm_backward(uint16_t* dx, float* dgain, float* dshift, float* stats,
+                                    const uint16_t* dy, const uint16_t* dres, const uint16_t* r,
+                                    const float* mean, const float* rstd, const uint16_t* gain,
+                                    int64_t N, int64_t C, int accumulate, void* workspace,
+                                    size_t workspace_bytes, qffn_stream_t stream);
+
+/* Backward of qffn_rmsnorm_absmax (r = its res_out, or its x without a
+ * residual; rstd as it wrote it): xhat = r * rstd,
+ *   dx = bf16(dres + rstd * (w - xhat * sum_C(w * xhat) / C)),  dgain as above.
+ * It completes qffn_ffn_backward, whose d_ln2 is the dy of this call.
+ * Arguments, workspace and rules as in qffn_layernorm_backward. */
+qffn_status qffn_rmsnorm_backward(uint16_t* dx, float* dgain, float* stats, const uint16_t* dy,
+                                  const uint16_t* dres, const uint16_t* r, const float* rstd,
+                                  const uint16_t* gain, int64_t N, int64_t C, int accumulate,
+                                  void* workspace, size_t workspace_bytes, qffn_stream_t stream);
+
+/* ---- Linear layers with bias, activation and residual -------------------------
+ * The unquantised (bf16) and FP8 matmul of a feed-forward layer with its
+ * epilogue fused.  Activations: */
+#define QFFN_ACT_NONE 0       /* z */
+#define QFFN_ACT_RELU 1       /* max(z, 0) */
+#define QFFN_ACT_GELU 2       /* z * Phi(z), Phi the normal distribution function */
+#define QFFN_ACT_GELU_TANH 3  /* z / 2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))) */
+#define QFFN_ACT_SILU 4       /* z / (1 + exp(-z)) */
+
+/*   z[M,N]   = x[M,K] . w[N,K]^T + bias[N]
+ *   out[M,N] = bf16(residual + act(z))
+ * with x and w bf16 and fp32 sums; z stays in fp32 for out.  bias and residual
+ * [M,N] (bf16) may be NULL.  z (bf16 [M,N], may be NULL) receives the rounded
+ * pre-activation that qffn_linear_backward needs when act != QFFN_ACT_NONE.
+ * out may alias residual.  M >= 0, N % 8 == 0, K % 8 == 0, N, K >= 8;
+ * M <= 2^30, N, K <= 2^20 and at most 2^28 tiles of 256 x 256 outputs.
+ * workspace: >= qffn_linear_workspace_size() bytes, 256-byte aligned, any
+ * content (the partial sums of the split of K that fills the GPU when there
+ * are few outputs; an unsupported shape gives 0). */
+size_t qffn_linear_workspace_size(int64_t M, int64_t N, int64_t K);
+qffn_status qffn_linear(uint16_t* out, uint16_t* z, const uint16_t* x, const uint16_t* w,
+                        const uint16_t* bias, const uint16_t* residual, int act, int64_t M, int64_t N,
+                        int64_t K, void* workspace, size_t workspace_bytes, qffn_stream_t stream);
+
+/* The same with x and w in E4M3 and their scales (one device float each):
+ *   z = x_scale * w_scale * (x . w^T) + bias
+ * K % 16 == 0, K >= 16; the other rules as above.  With bias, residual and z
+ * NULL and QFFN_ACT_NONE it computes qffn_fp8_gemm_scaled (the fp32 sums may
+ * be split over K in another way). */
+size_t qffn_linear_fp8_workspace_size(int64_t M, int64_t N, int64_t K);
+qffn_status qffn_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, const float* x_scale,
+                            const uint8_t* w, const float* w_scale, const uint16_t* bias,
+                            const uint16_t* residual, int act, int64_t M, int64_t N, int64_t K,
+                            void* workspace, size_t workspace_bytes, qffn_stream_t stream);
+
+/* Backward of qffn_linear for the gradient dout [M,N] of its out (which is
+ * also the gradient of its residual):
+ *   dz        = dout * act'(z), z the bf16 pre-activation of the forward (may be
+ *               NULL for QFFN_ACT_NONE, where dz = dout); rounded to bf16 for the
+ *               two products, as the tensor cores take it
+ *   dx[M,K]   = bf16(dz . w)                       (dx may be NULL)
+ *   dw[N,K]   = bf16(dz^T . x (+ dw))
+ *   dbias[N]  = sum_M(dz) (+ dbias), fp32, from dz before its rounding
+ *                                                  (dbias may be NULL)
+ * The terms in parentheses are added when accumulate != 0.  dx and dw must not
+ * overlap any input or each other.  workspace: >=
+ * qffn_linear_backward_workspace_size() bytes, 256-byte aligned, any content.
+ * Shape rules of qffn_linear, for each of the three products. */
+size_t qffn_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K);
+qffn_status qffn_linear_backward(uint16_t* dx, uint16_t* dw, float* dbias, const uint16_t* dout,
+                                 const uint16_t* z, const uint16_t* x, const uint16_t* w, int act,
+                                 int64_t M, int64_t N, int64_t K, int accumulate, void* workspace,
+                                 size_t workspace_bytes, qffn_stream_t stream);
+
+/* ---- Gated feed-forward layer, bf16 -------------------------------------------
+ * The unquantised form of qffn_gate_up_swiglu with a choice of activation:
+ * both projections, the activation and the product in one kernel.
+ *   g = x . w1[0:H]^T, u = x . w1[H:2H]^T     (w1 [2H,C] bf16, gate rows first)
+ *   h[N,H] = bf16(act(g) * u)
+ * g and u stay in fp32 and are not written.  N >= 0, C % 8 == 0, H % 8 == 0;
+ * C, H >= 8; N <= 2^30, C <= 2^20, H <= 2^19, at most 2^28 tiles.  workspace as in
+ * qffn_linear, of qffn_gated_linear_workspace_size() bytes. */
+size_t qffn_gated_linear_workspace_size(int64_t N, int64_t C, int64_t H);
+qffn_status qffn_gated_linear(uint16_t* h, const uint16_t* x, const uint16_t* w1, int act, int64_t N,
+                              int64_t C, int64_t H, void* workspace, size_t workspace_bytes,
+                              qffn_stream_t stream);
+
+/* Its backward for the gradient dh [N,H] of h: g and u are recomputed from x
+ * and w1, and their gradient formed in the same kernel,
+ *   d_gu[N,2H] = (dh * u * act'(g) | dh * act(g))   (bf16, in the workspace)
+ *   dx[N,C]    = bf16(d_gu . w1)                    (dx may be NULL)
+ *   dw1[2H,C]  = bf16(d_gu^T . x (+ dw1 when accumulate != 0))
+ * dx and dw1 must not overlap any input or each other.  workspace: >=
+ * qffn_gated_linear_backward_workspace_size() bytes, 256-byte aligned; d_gu is
+ * at its start after the call.  Shape rules of qffn_gated_linear, for each
+ * product. */
+size_t qffn_gated_linear_backward_workspace_size(int64_t N, int64_t C, int64_t H);
+qffn_status qffn_gated_linear_backward(uint16_t* dx, uint16_t* dw1, const uint16_t* dh,
+                                       const uint16_t* x, const uint16_t* w1, int act, int64_t N,
+                                       int64_t C, int64_t H, int accumulate, void* workspace,
+                                       size_t workspace_bytes, qffn_stream_t stream);
 
 /* ---- Step A6: dual row-scaled FP8 GEMV ------------------------------------
  * [metrale] w8a16_gemv_dual: one pass over x for two weight matrices.

@@ -3,7 +3,9 @@
 Argument marshalling only: each function here has the name of a C entry
 point of ``include/qffn.h``, turns torch tensors (or raw integer device
 addresses) into pointers, passes the current torch CUDA stream unless one is
-given, and raises ``QffnError`` on a non-zero status.  Every step of the
+given, and raises ``QffnError`` on a non-zero status.  The norm, linear and
+gated-linear functions also refuse tensors that are too small, not contiguous
+or not on the current device.  Every step of the
 block runs in the CUDA kernels of ``libqffn.so``; there is no fallback.  If
 the library is missing the import fails (run ``build()`` first).
 """
@@ -26,12 +28,19 @@ __all__ = [
     "qffn_forward_recompute", "qffn_transpose_e4m3", "qffn_swiglu_backward",
     "qffn_backward_qmm_workspace_size", "qffn_backward_qmm", "qffn_ffn_backward_workspace_size",
     "qffn_ffn_backward_workspace_offsets", "qffn_ffn_backward", "qffn_gate_up_swiglu_backward",
+    "qffn_layernorm_absmax", "qffn_norm_backward_workspace_size", "qffn_layernorm_backward",
+    "qffn_rmsnorm_backward", "qffn_linear_workspace_size", "qffn_linear", "qffn_linear_fp8_workspace_size",
+    "qffn_linear_fp8", "qffn_linear_backward_workspace_size", "qffn_linear_backward",
+    "qffn_gated_linear_workspace_size", "qffn_gated_linear", "qffn_gated_linear_backward_workspace_size",
+    "qffn_gated_linear_backward", "QFFN_ACT_NONE", "QFFN_ACT_RELU", "QFFN_ACT_GELU", "QFFN_ACT_GELU_TANH",
+    "QFFN_ACT_SILU",
     "qffn_gemv_dual", "qffn_gemv", "qffn_gemv_silu_input", "qffn_silu_mul", "qffn_decode_workspace_size",
     "qffn_decode_workspace_offsets", "qffn_decode_forward", "qffn_decode_forward_ex", "qffn_decode_forward_gu",
     "qffn_decode_forward_noalloc", "QFFN_DECODE_WEIGHTS_STABLE",
 ]
 
 QFFN_DECODE_WEIGHTS_STABLE = 1
+QFFN_ACT_NONE, QFFN_ACT_RELU, QFFN_ACT_GELU, QFFN_ACT_GELU_TANH, QFFN_ACT_SILU = range(5)
 
 STATUS = {0: "QFFN_OK", 1: "QFFN_ERR_INVALID_ARG", 2: "QFFN_ERR_UNSUPPORTED_SHAPE",
           3: "QFFN_ERR_MISALIGNED", 4: "QFFN_ERR_CUDA", 5: "QFFN_ERR_TIMEOUT"}
@@ -80,6 +89,20 @@ _SIGS = {
     "qffn_ffn_backward_workspace_offsets": ([_I64, _I64, _I64, ctypes.POINTER(_SZ)], _S),
     "qffn_ffn_backward": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                            _I64, _I64, _I64, _S, _P, _SZ, _P], _S),
+    "qffn_layernorm_absmax": ([_P] * 9 + [_F, _I64, _I64, _P], _S),
+    "qffn_norm_backward_workspace_size": ([_I64, _I64], _SZ),
+    "qffn_layernorm_backward": ([_P] * 10 + [_I64, _I64, _S, _P, _SZ, _P], _S),
+    "qffn_rmsnorm_backward": ([_P] * 8 + [_I64, _I64, _S, _P, _SZ, _P], _S),
+    "qffn_linear_workspace_size": ([_I64] * 3, _SZ),
+    "qffn_linear": ([_P] * 6 + [_S, _I64, _I64, _I64, _P, _SZ, _P], _S),
+    "qffn_linear_fp8_workspace_size": ([_I64] * 3, _SZ),
+    "qffn_linear_fp8": ([_P] * 8 + [_S, _I64, _I64, _I64, _P, _SZ, _P], _S),
+    "qffn_linear_backward_workspace_size": ([_I64] * 3, _SZ),
+    "qffn_linear_backward": ([_P] * 7 + [_S, _I64, _I64, _I64, _S, _P, _SZ, _P], _S),
+    "qffn_gated_linear_workspace_size": ([_I64] * 3, _SZ),
+    "qffn_gated_linear": ([_P] * 3 + [_S, _I64, _I64, _I64, _P, _SZ, _P], _S),
+    "qffn_gated_linear_backward_workspace_size": ([_I64] * 3, _SZ),
+    "qffn_gated_linear_backward": ([_P] * 5 + [_S, _I64, _I64, _I64, _S, _P, _SZ, _P], _S),
     "qffn_gemv_dual": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _P], _S),
     "qffn_gemv": ([_P, _P, _P, _P, _I64, _I64, _P], _S),
     "qffn_gemv_silu_input": ([_P, _P, _P, _P, _P, _I64, _I64, _P], _S),
@@ -98,9 +121,9 @@ for _name, (_args, _res) in _SIGS.items():
 
 
 class QffnError(RuntimeError):
-    def __init__(self, fn: str, status: int):
+    def __init__(self, fn: str, status: int, detail: str = ""):
         self.status = status
-        super().__init__(f"{fn}: {STATUS.get(status, status)} ({qffn_status_string(status)})")
+        super().__init__(f"{fn}: {STATUS.get(status, status)} ({detail or qffn_status_string(status)})")
 
 
 def _ptr(t):
@@ -110,6 +133,32 @@ def _ptr(t):
     if isinstance(t, int):
         return t
     return t.data_ptr()
+
+
+def _buf(fn, device, name, t, size, n):
+    """_ptr of a tensor after the checks that a bare address cannot have: ``n`` elements of
+    ``size`` bytes at least, contiguous, on the current device."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.element_size() != size or t.numel() < n or not t.is_contiguous() or (n and t.get_device() != device):
+        raise QffnError(fn, 1, f"{name}: expected {n} contiguous elements of {size} bytes on cuda:{device}, got "
+                               f"{tuple(t.shape)} {t.dtype} on {t.device}"
+                               f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+def _current_device():
+    import torch
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+
+def _workspace(fn, device, workspace, workspace_bytes):
+    if isinstance(workspace, int) or workspace is None:
+        return workspace, int(workspace_bytes or 0)
+    nbytes = workspace.numel() * workspace.element_size()
+    if workspace_bytes is not None:
+        nbytes = min(nbytes, int(workspace_bytes))
+    return _buf(fn, device, "workspace", workspace, workspace.element_size(), 1), nbytes
 
 
 def _stream(stream):
@@ -287,6 +336,109 @@ def qffn_ffn_backward(d_ln2, dw1, dw2, stats_dout, stats_dgu, dout, yq, y_scale,
         _ptr(d_ln2), _ptr(dw1), _ptr(dw2), _ptr(stats_dout), _ptr(stats_dgu), _ptr(dout), _ptr(yq),
         _ptr(y_scale), _ptr(hq), _ptr(h_scale), _ptr(w1), _ptr(w1_scale), _ptr(w2), _ptr(w2_scale),
         int(N), int(C), int(H), int(bool(accumulate)), _ptr(workspace), int(workspace_bytes),
+        _stream(stream)))
+
+
+def qffn_layernorm_absmax(res_out, y, mean, rstd, stats, res_in, x, gain, shift, eps, N, C, stream=None):
+    fn, d, n = "qffn_layernorm_absmax", _current_device(), N * C
+    _check(fn, lib.qffn_layernorm_absmax(
+        _buf(fn, d, "res_out", res_out, 2, n), _buf(fn, d, "y", y, 2, n), _buf(fn, d, "mean", mean, 4, N),
+        _buf(fn, d, "rstd", rstd, 4, N), _buf(fn, d, "stats", stats, 4, 1), _buf(fn, d, "res_in", res_in, 2, n),
+        _buf(fn, d, "x", x, 2, n), _buf(fn, d, "gain", gain, 2, C), _buf(fn, d, "shift", shift, 2, C),
+        eps, N, C, _stream(stream)))
+
+
+def qffn_norm_backward_workspace_size(N, C) -> int:
+    return int(lib.qffn_norm_backward_workspace_size(int(N), int(C)))
+
+
+def qffn_layernorm_backward(dx, dgain, dshift, stats, dy, dres, r, mean, rstd, gain, N, C, accumulate, workspace,
+                            workspace_bytes=None, stream=None):
+    fn, d, n = "qffn_layernorm_backward", _current_device(), N * C
+    ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
+    _check(fn, lib.qffn_layernorm_backward(
+        _buf(fn, d, "dx", dx, 2, n), _buf(fn, d, "dgain", dgain, 4, C), _buf(fn, d, "dshift", dshift, 4, C),
+        _buf(fn, d, "stats", stats, 4, 1), _buf(fn, d, "dy", dy, 2, n), _buf(fn, d, "dres", dres, 2, n),
+        _buf(fn, d, "r", r, 2, n), _buf(fn, d, "mean", mean, 4, N), _buf(fn, d, "rstd", rstd, 4, N),
+        _buf(fn, d, "gain", gain, 2, C), N, C, bool(accumulate), ws, nbytes, _stream(stream)))
+
+
+def qffn_rmsnorm_backward(dx, dgain, stats, dy, dres, r, rstd, gain, N, C, accumulate, workspace,
+                          workspace_bytes=None, stream=None):
+    fn, d, n = "qffn_rmsnorm_backward", _current_device(), N * C
+    ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
+    _check(fn, lib.qffn_rmsnorm_backward(
+        _buf(fn, d, "dx", dx, 2, n), _buf(fn, d, "dgain", dgain, 4, C), _buf(fn, d, "stats", stats, 4, 1),
+        _buf(fn, d, "dy", dy, 2, n), _buf(fn, d, "dres", dres, 2, n), _buf(fn, d, "r", r, 2, n),
+        _buf(fn, d, "rstd", rstd, 4, N), _buf(fn, d, "gain", gain, 2, C), N, C, bool(accumulate), ws, nbytes,
+        _stream(stream)))
+
+
+def qffn_linear_workspace_size(M, N, K) -> int:
+    return int(lib.qffn_linear_workspace_size(int(M), int(N), int(K)))
+
+
+def qffn_linear(out, z, x, w, bias, residual, act, M, N, K, workspace, workspace_bytes=None, stream=None):
+    fn, d = "qffn_linear", _current_device()
+    ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
+    _check(fn, lib.qffn_linear(
+        _buf(fn, d, "out", out, 2, M * N), _buf(fn, d, "z", z, 2, M * N), _buf(fn, d, "x", x, 2, M * K),
+        _buf(fn, d, "w", w, 2, N * K), _buf(fn, d, "bias", bias, 2, N), _buf(fn, d, "residual", residual, 2, M * N),
+        act, M, N, K, ws, nbytes, _stream(stream)))
+
+
+def qffn_linear_fp8_workspace_size(M, N, K) -> int:
+    return int(lib.qffn_linear_fp8_workspace_size(int(M), int(N), int(K)))
+
+
+def qffn_linear_fp8(out, z, x, x_scale, w, w_scale, bias, residual, act, M, N, K, workspace, workspace_bytes=None,
+                    stream=None):
+    fn, d = "qffn_linear_fp8", _current_device()
+    ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
+    _check(fn, lib.qffn_linear_fp8(
+        _buf(fn, d, "out", out, 2, M * N), _buf(fn, d, "z", z, 2, M * N), _buf(fn, d, "x", x, 1, M * K),
+        _buf(fn, d, "x_scale", x_scale, 4, 1), _buf(fn, d, "w", w, 1, N * K), _buf(fn, d, "w_scale", w_scale, 4, 1),
+        _buf(fn, d, "bias", bias, 2, N), _buf(fn, d, "residual", residual, 2, M * N), act, M, N, K, ws, nbytes,
+        _stream(stream)))
+
+
+def qffn_linear_backward_workspace_size(M, N, K) -> int:
+    return int(lib.qffn_linear_backward_workspace_size(int(M), int(N), int(K)))
+
+
+def qffn_linear_backward(dx, dw, dbias, dout, z, x, w, act, M, N, K, accumulate, workspace, workspace_bytes=None,
+                         stream=None):
+    fn, d = "qffn_linear_backward", _current_device()
+    ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
+    _check(fn, lib.qffn_linear_backward(
+        _buf(fn, d, "dx", dx, 2, M * K), _buf(fn, d, "dw", dw, 2, N * K), _buf(fn, d, "dbias", dbias, 4, N),
+        _buf(fn, d, "dout", dout, 2, M * N), _buf(fn, d, "z", z, 2, M * N), _buf(fn, d, "x", x, 2, M * K),
+        _buf(fn, d, "w", w, 2, N * K), act, M, N, K, bool(accumulate), ws, nbytes, _stream(stream)))
+
+
+def qffn_gated_linear_workspace_size(N, C, H) -> int:
+    return int(lib.qffn_gated_linear_workspace_size(int(N), int(C), int(H)))
+
+
+def qffn_gated_linear(h, x, w1, act, N, C, H, workspace, workspace_bytes=None, stream=None):
+    fn, d = "qffn_gated_linear", _current_device()
+    ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
+    _check(fn, lib.qffn_gated_linear(
+        _buf(fn, d, "h", h, 2, N * H), _buf(fn, d, "x", x, 2, N * C), _buf(fn, d, "w1", w1, 2, 2 * H * C), act, N, C, H,
+        ws, nbytes, _stream(stream)))
+
+
+def qffn_gated_linear_backward_workspace_size(N, C, H) -> int:
+    return int(lib.qffn_gated_linear_backward_workspace_size(int(N), int(C), int(H)))
+
+
+def qffn_gated_linear_backward(dx, dw1, dh, x, w1, act, N, C, H, accumulate, workspace, workspace_bytes=None,
+                               stream=None):
+    fn, d = "qffn_gated_linear_backward", _current_device()
+    ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
+    _check(fn, lib.qffn_gated_linear_backward(
+        _buf(fn, d, "dx", dx, 2, N * C), _buf(fn, d, "dw1", dw1, 2, 2 * H * C), _buf(fn, d, "dh", dh, 2, N * H),
+        _buf(fn, d, "x", x, 2, N * C), _buf(fn, d, "w1", w1, 2, 2 * H * C), act, N, C, H, bool(accumulate), ws, nbytes,
         _stream(stream)))
 
 

@@ -126,6 +126,40 @@ qffn_status check_forward_shape(int64_t B, int64_t T, int64_t C, int64_t H) {
   return QFFN_OK;
 }
 
+// linear and gated layers: sizes every product of a call must have
+constexpr int64_t kMaxLinearRows = int64_t(1) << 30;
+bool product_fits(int64_t M, int64_t N) { return (M + 255) / 256 * ((N + 255) / 256) <= (int64_t(1) << 28); }
+
+qffn_status check_linear_shape(int64_t M, int64_t N, int64_t K, int64_t k_step) {
+  QFFN_REQUIRE(M >= 0 && N >= 0 && K >= 0, QFFN_ERR_INVALID_ARG);
+  QFFN_REQUIRE(M <= kMaxLinearRows, QFFN_ERR_UNSUPPORTED_SHAPE);
+  QFFN_REQUIRE(N % 8 == 0 && N >= 8 && N <= kMaxDim, QFFN_ERR_UNSUPPORTED_SHAPE);
+  QFFN_REQUIRE(K % k_step == 0 && K >= k_step && K <= kMaxDim, QFFN_ERR_UNSUPPORTED_SHAPE);
+  QFFN_REQUIRE(product_fits(M, N), QFFN_ERR_UNSUPPORTED_SHAPE);
+  return QFFN_OK;
+}
+// the backward's products: [M,K], [N,K]
+qffn_status check_linear_backward_shape(int64_t M, int64_t N, int64_t K) {
+  const qffn_status st = check_linear_shape(M, N, K, 8);
+  if (st != QFFN_OK) return st;
+  QFFN_REQUIRE(product_fits(M, K) && product_fits(N, K), QFFN_ERR_UNSUPPORTED_SHAPE);
+  return QFFN_OK;
+}
+qffn_status check_gated_shape(int64_t N, int64_t C, int64_t H, bool backward) {
+  QFFN_REQUIRE(N >= 0 && C >= 0 && H >= 0, QFFN_ERR_INVALID_ARG);
+  QFFN_REQUIRE(H % 8 == 0 && H >= 8 && H <= kMaxDim / 2, QFFN_ERR_UNSUPPORTED_SHAPE);
+  return backward ? check_linear_backward_shape(N, 2 * H, C) : check_linear_shape(N, 2 * H, C, 8);
+}
+bool valid_act(int act) { return act >= QFFN_ACT_NONE && act <= QFFN_ACT_SILU; }
+size_t at_least_256(size_t v) { return v < 256 ? 256 : v; }
+
+qffn_status check_norm_shape(int64_t N, int64_t C) {
+  QFFN_REQUIRE(N >= 0 && C >= 0, QFFN_ERR_INVALID_ARG);
+  QFFN_REQUIRE(N <= kMaxRows, QFFN_ERR_UNSUPPORTED_SHAPE);
+  QFFN_REQUIRE(C % 8 == 0 && C >= 8 && C <= 16384, QFFN_ERR_UNSUPPORTED_SHAPE);
+  return QFFN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -146,10 +180,11 @@ int qffn_abi_version(void) { return kAbiVersion; }
 
 qffn_status qffn_check_status(qffn_stream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return QFFN_ERR_CUDA;
-  unsigned int st = 0, sd = 0;
+  unsigned int st = 0, sd = 0, sl = 0;
   if (qffn::gemm_take_status(&st) != cudaSuccess) return QFFN_ERR_CUDA;
   if (qffn::decode_take_status(&sd) != cudaSuccess) return QFFN_ERR_CUDA;
-  return (st | sd) != 0 ? QFFN_ERR_TIMEOUT : QFFN_OK;
+  if (qffn::linear_take_status(&sl) != cudaSuccess) return QFFN_ERR_CUDA;
+  return (st | sd | sl) != 0 ? QFFN_ERR_TIMEOUT : QFFN_OK;
 }
 
 qffn_status qffn_gemm_clock_sample(uint64_t* out, qffn_stream_t stream) {
@@ -530,6 +565,170 @@ qffn_status qffn_ffn_backward(uint16_t* d_ln2, uint16_t* dw1, uint16_t* dw2, flo
   // up projection: d_ln2, dW1
   return from_cuda(run_backward_qmm(d_ln2, dw1, stats_dgu, dgu, yq, y_scale, w1, w1_scale, N, C,
                                     2 * H, acc, bq, stream));
+}
+
+qffn_status qffn_layernorm_absmax(uint16_t* res_out, uint16_t* y, float* mean, float* rstd,
+                                  float* stats, const uint16_t* res_in, const uint16_t* x,
+                                  const uint16_t* gain, const uint16_t* shift, float eps, int64_t N,
+                                  int64_t C, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR(y); QFFN_PTR(mean); QFFN_PTR(rstd); QFFN_PTR(x); QFFN_PTR(gain);
+  if (res_in != nullptr) QFFN_PTR(res_out);
+  QFFN_REQUIRE(isfinite(eps) && eps >= 0.0f, QFFN_ERR_INVALID_ARG);
+  const qffn_status st = check_norm_shape(N, C);
+  if (st != QFFN_OK) return st;
+  QFFN_ALIGNED(y); QFFN_ALIGNED4(mean); QFFN_ALIGNED4(rstd); QFFN_ALIGNED4(stats);
+  QFFN_ALIGNED(x); QFFN_ALIGNED(gain); QFFN_ALIGNED(shift);
+  if (res_in != nullptr) { QFFN_ALIGNED(res_in); QFFN_ALIGNED(res_out); }
+  return from_cuda(qffn::launch_layernorm(res_out, y, mean, rstd, stats, res_in, x, gain, shift, eps, N,
+                                          int(C), stream));
+}
+
+size_t qffn_norm_backward_workspace_size(int64_t N, int64_t C) {
+  if (check_norm_shape(N, C) != QFFN_OK) return 0;
+  // one partial row of dgain and dshift per block
+  return at_least_256(round_up(size_t(qffn::norm_backward_blocks(N, int(C))) * 2 * size_t(C) * sizeof(float), 256));
+}
+
+qffn_status qffn_layernorm_backward(uint16_t* dx, float* dgain, float* dshift, float* stats,
+                                    const uint16_t* dy, const uint16_t* dres, const uint16_t* r,
+                                    const float* mean, const float* rstd, const uint16_t* gain,
+                                    int64_t N, int64_t C, int accumulate, void* workspace,
+                                    size_t workspace_bytes, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR(dx); QFFN_PTR(dgain); QFFN_PTR(dy); QFFN_PTR(r); QFFN_PTR(mean); QFFN_PTR(rstd); QFFN_PTR(gain);
+  QFFN_PTR(workspace);
+  const qffn_status st = check_norm_shape(N, C);
+  if (st != QFFN_OK) return st;
+  QFFN_REQUIRE(workspace_bytes >= qffn_norm_backward_workspace_size(N, C), QFFN_ERR_INVALID_ARG);
+  QFFN_REQUIRE(aligned256(workspace), QFFN_ERR_MISALIGNED);
+  QFFN_ALIGNED(dx); QFFN_ALIGNED4(dgain); QFFN_ALIGNED4(dshift); QFFN_ALIGNED4(stats); QFFN_ALIGNED(dy);
+  QFFN_ALIGNED(dres); QFFN_ALIGNED(r); QFFN_ALIGNED4(mean); QFFN_ALIGNED4(rstd); QFFN_ALIGNED(gain);
+  return from_cuda(qffn::launch_norm_backward(dx, dgain, dshift, stats, dy, dres, r, mean, rstd, gain, N, int(C),
+                                              true, accumulate != 0, static_cast<float*>(workspace), stream));
+}
+
+qffn_status qffn_rmsnorm_backward(uint16_t* dx, float* dgain, float* stats, const uint16_t* dy,
+                                  const uint16_t* dres, const uint16_t* r, const float* rstd,
+                                  const uint16_t* gain, int64_t N, int64_t C, int accumulate,
+                                  void* workspace, size_t workspace_bytes, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR(dx); QFFN_PTR(dgain); QFFN_PTR(dy); QFFN_PTR(r); QFFN_PTR(rstd); QFFN_PTR(gain);
+  QFFN_PTR(workspace);
+  const qffn_status st = check_norm_shape(N, C);
+  if (st != QFFN_OK) return st;
+  QFFN_REQUIRE(workspace_bytes >= qffn_norm_backward_workspace_size(N, C), QFFN_ERR_INVALID_ARG);
+  QFFN_REQUIRE(aligned256(workspace), QFFN_ERR_MISALIGNED);
+  QFFN_ALIGNED(dx); QFFN_ALIGNED4(dgain); QFFN_ALIGNED4(stats); QFFN_ALIGNED(dy);
+  QFFN_ALIGNED(dres); QFFN_ALIGNED(r); QFFN_ALIGNED4(rstd); QFFN_ALIGNED(gain);
+  return from_cuda(qffn::launch_norm_backward(dx, dgain, nullptr, stats, dy, dres, r, nullptr, rstd, gain, N,
+                                              int(C), false, accumulate != 0, static_cast<float*>(workspace),
+                                              stream));
+}
+
+size_t qffn_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (check_linear_shape(M, N, K, 8) != QFFN_OK) return 0;
+  return at_least_256(qffn::linear_workspace(M, N, K, false));
+}
+
+qffn_status qffn_linear(uint16_t* out, uint16_t* z, const uint16_t* x, const uint16_t* w,
+                        const uint16_t* bias, const uint16_t* residual, int act, int64_t M, int64_t N,
+                        int64_t K, void* workspace, size_t workspace_bytes, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR(out); QFFN_PTR(x); QFFN_PTR(w); QFFN_PTR(workspace);
+  QFFN_REQUIRE(valid_act(act), QFFN_ERR_INVALID_ARG);
+  const qffn_status st = check_linear_shape(M, N, K, 8);
+  if (st != QFFN_OK) return st;
+  QFFN_REQUIRE(workspace_bytes >= qffn_linear_workspace_size(M, N, K), QFFN_ERR_INVALID_ARG);
+  QFFN_REQUIRE(aligned256(workspace), QFFN_ERR_MISALIGNED);
+  QFFN_ALIGNED(out); QFFN_ALIGNED(z); QFFN_ALIGNED(x); QFFN_ALIGNED(w); QFFN_ALIGNED(bias); QFFN_ALIGNED(residual);
+  return from_cuda(qffn::launch_linear(out, z, x, w, bias, residual, act, M, N, K, static_cast<float*>(workspace),
+                                       stream));
+}
+
+size_t qffn_linear_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (check_linear_shape(M, N, K, 16) != QFFN_OK) return 0;
+  return at_least_256(qffn::linear_workspace(M, N, K, true));
+}
+
+qffn_status qffn_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, const float* x_scale,
+                            const uint8_t* w, const float* w_scale, const uint16_t* bias,
+                            const uint16_t* residual, int act, int64_t M, int64_t N, int64_t K,
+                            void* workspace, size_t workspace_bytes, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR(out); QFFN_PTR(x); QFFN_PTR(x_scale); QFFN_PTR(w); QFFN_PTR(w_scale); QFFN_PTR(workspace);
+  QFFN_REQUIRE(valid_act(act), QFFN_ERR_INVALID_ARG);
+  const qffn_status st = check_linear_shape(M, N, K, 16);
+  if (st != QFFN_OK) return st;
+  QFFN_REQUIRE(workspace_bytes >= qffn_linear_fp8_workspace_size(M, N, K), QFFN_ERR_INVALID_ARG);
+  QFFN_REQUIRE(aligned256(workspace), QFFN_ERR_MISALIGNED);
+  QFFN_ALIGNED(out); QFFN_ALIGNED(z); QFFN_ALIGNED(x); QFFN_ALIGNED4(x_scale); QFFN_ALIGNED(w);
+  QFFN_ALIGNED4(w_scale); QFFN_ALIGNED(bias); QFFN_ALIGNED(residual);
+  return from_cuda(qffn::launch_linear_fp8(out, z, x, x_scale, w, w_scale, bias, residual, act, M, N, K,
+                                           static_cast<float*>(workspace), stream));
+}
+
+size_t qffn_linear_backward_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (check_linear_backward_shape(M, N, K) != QFFN_OK) return 0;
+  return at_least_256(qffn::linear_backward_workspace(M, N, K));
+}
+
+qffn_status qffn_linear_backward(uint16_t* dx, uint16_t* dw, float* dbias, const uint16_t* dout,
+                                 const uint16_t* z, const uint16_t* x, const uint16_t* w, int act,
+                                 int64_t M, int64_t N, int64_t K, int accumulate, void* workspace,
+                                 size_t workspace_bytes, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR(dw); QFFN_PTR(dout); QFFN_PTR(x); QFFN_PTR(w); QFFN_PTR(workspace);
+  QFFN_REQUIRE(valid_act(act), QFFN_ERR_INVALID_ARG);
+  if (act != QFFN_ACT_NONE) QFFN_PTR(z);
+  const qffn_status st = check_linear_backward_shape(M, N, K);
+  if (st != QFFN_OK) return st;
+  QFFN_REQUIRE(workspace_bytes >= qffn_linear_backward_workspace_size(M, N, K), QFFN_ERR_INVALID_ARG);
+  QFFN_REQUIRE(aligned256(workspace), QFFN_ERR_MISALIGNED);
+  QFFN_ALIGNED(dx); QFFN_ALIGNED(dw); QFFN_ALIGNED4(dbias); QFFN_ALIGNED(dout); QFFN_ALIGNED(z);
+  QFFN_ALIGNED(x); QFFN_ALIGNED(w);
+  return from_cuda(qffn::launch_linear_backward(dx, dw, dbias, dout, z, x, w, act, M, N, K, accumulate != 0,
+                                                static_cast<uint8_t*>(workspace), stream));
+}
+
+size_t qffn_gated_linear_workspace_size(int64_t N, int64_t C, int64_t H) {
+  if (check_gated_shape(N, C, H, false) != QFFN_OK) return 0;
+  return at_least_256(qffn::gated_workspace(N, C, H));
+}
+
+qffn_status qffn_gated_linear(uint16_t* h, const uint16_t* x, const uint16_t* w1, int act, int64_t N,
+                              int64_t C, int64_t H, void* workspace, size_t workspace_bytes,
+                              qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR(h); QFFN_PTR(x); QFFN_PTR(w1); QFFN_PTR(workspace);
+  QFFN_REQUIRE(valid_act(act), QFFN_ERR_INVALID_ARG);
+  const qffn_status st = check_gated_shape(N, C, H, false);
+  if (st != QFFN_OK) return st;
+  QFFN_REQUIRE(workspace_bytes >= qffn_gated_linear_workspace_size(N, C, H), QFFN_ERR_INVALID_ARG);
+  QFFN_REQUIRE(aligned256(workspace), QFFN_ERR_MISALIGNED);
+  QFFN_ALIGNED(h); QFFN_ALIGNED(x); QFFN_ALIGNED(w1);
+  return from_cuda(qffn::launch_gated(h, x, w1, act, N, C, H, static_cast<float*>(workspace), stream));
+}
+
+size_t qffn_gated_linear_backward_workspace_size(int64_t N, int64_t C, int64_t H) {
+  if (check_gated_shape(N, C, H, true) != QFFN_OK) return 0;
+  return at_least_256(qffn::gated_backward_workspace(N, C, H));
+}
+
+qffn_status qffn_gated_linear_backward(uint16_t* dx, uint16_t* dw1, const uint16_t* dh,
+                                       const uint16_t* x, const uint16_t* w1, int act, int64_t N,
+                                       int64_t C, int64_t H, int accumulate, void* workspace,
+                                       size_t workspace_bytes, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR(dw1); QFFN_PTR(dh); QFFN_PTR(x); QFFN_PTR(w1); QFFN_PTR(workspace);
+  QFFN_REQUIRE(valid_act(act), QFFN_ERR_INVALID_ARG);
+  const qffn_status st = check_gated_shape(N, C, H, true);
+  if (st != QFFN_OK) return st;
+  QFFN_REQUIRE(workspace_bytes >= qffn_gated_linear_backward_workspace_size(N, C, H), QFFN_ERR_INVALID_ARG);
+  QFFN_REQUIRE(aligned256(workspace), QFFN_ERR_MISALIGNED);
+  QFFN_ALIGNED(dx); QFFN_ALIGNED(dw1); QFFN_ALIGNED(dh); QFFN_ALIGNED(x); QFFN_ALIGNED(w1);
+  return from_cuda(qffn::launch_gated_backward(dx, dw1, dh, x, w1, act, N, C, H, accumulate != 0,
+                                               static_cast<uint8_t*>(workspace), stream));
 }
 
 qffn_status qffn_gemv_dual(uint16_t* g, uint16_t* u, const uint16_t* x, const uint8_t* w_gate,

@@ -106,6 +106,44 @@ cudaError_t launch_decode(uint16_t* out, const uint16_t* x, const uint8_t* w_gat
                           const float* s_gate, const uint8_t* w_up, const float* s_up,
                           const uint8_t* w_down, const float* s_down, int64_t C, int64_t H,
                           uint16_t* g, uint16_t* u, bool early, cudaStream_t s);
+// ---- layer norm and the norms' backward (norm.cu)
+cudaError_t launch_layernorm(uint16_t* res_out, uint16_t* y, float* mean, float* rstd, float* stats,
+                             const uint16_t* res_in, const uint16_t* x, const uint16_t* gain,
+                             const uint16_t* shift, float eps, int64_t N, int C, cudaStream_t s);
+// Blocks of the backward, each of which writes one partial row of dgain (and
+// of dshift, for the layer norm) into `partial`.
+int norm_backward_blocks(int64_t N, int C);
+cudaError_t launch_norm_backward(uint16_t* dx, float* dgain, float* dshift, float* stats, const uint16_t* dy,
+                                 const uint16_t* dres, const uint16_t* r, const float* mean, const float* rstd,
+                                 const uint16_t* gain, int64_t N, int C, bool centred, bool accumulate,
+                                 float* partial, cudaStream_t s);
+// out0 [cols0], out1 [cols - cols0] (+)= the sum of the rows of partial [parts, cols],
+// in a fixed order; either output may be NULL.  A programmatic dependent launch.
+cudaError_t launch_column_sum(float* out0, float* out1, const float* partial, int parts, int64_t cols0,
+                              int64_t cols, bool accumulate, cudaStream_t s);
+
+// ---- linear and gated layers (linear.cu).  The *_workspace functions give the
+// bytes `ws` must hold (0: none); shapes are checked by the caller.
+size_t linear_workspace(int64_t M, int64_t N, int64_t K, bool fp8);
+size_t gated_workspace(int64_t M, int64_t C, int64_t H);
+size_t linear_backward_workspace(int64_t M, int64_t N, int64_t K);
+size_t gated_backward_workspace(int64_t M, int64_t C, int64_t H);
+cudaError_t launch_linear(uint16_t* out, uint16_t* z, const uint16_t* x, const uint16_t* w, const uint16_t* bias,
+                          const uint16_t* res, int act, int64_t M, int64_t N, int64_t K, float* ws, cudaStream_t s);
+cudaError_t launch_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, const float* x_scale, const uint8_t* w,
+                              const float* w_scale, const uint16_t* bias, const uint16_t* res, int act, int64_t M,
+                              int64_t N, int64_t K, float* ws, cudaStream_t s);
+cudaError_t launch_linear_backward(uint16_t* dx, uint16_t* dw, float* dbias, const uint16_t* dout, const uint16_t* z,
+                                   const uint16_t* x, const uint16_t* w, int act, int64_t M, int64_t N, int64_t K,
+                                   bool accumulate, uint8_t* ws, cudaStream_t s);
+cudaError_t launch_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int act, int64_t M, int64_t C, int64_t H,
+                         float* ws, cudaStream_t s);
+cudaError_t launch_gated_backward(uint16_t* dx, uint16_t* dw1, const uint16_t* dh, const uint16_t* x,
+                                  const uint16_t* w1, int act, int64_t M, int64_t C, int64_t H, bool accumulate,
+                                  uint8_t* ws, cudaStream_t s);
+// Reads and clears the linear kernels' device status word of the current device.
+cudaError_t linear_take_status(unsigned int* status);
+
 // Reads and clears the decode kernels' device status word of the current device.
 cudaError_t decode_take_status(unsigned int* status);
 

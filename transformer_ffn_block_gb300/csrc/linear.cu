@@ -1,0 +1,1050 @@
+// Linear layers on the 5th-generation tensor cores (tcgen05, sm_103a) with
+// bf16 or E4M3 operands and a fused epilogue:
+//
+//   EPI_LINEAR     out[M,N] = bf16(res + act(z)),  z = s * A[M,K] . W[N,K]^T + bias,
+//                  z also stored (bf16) on request; s = 1 for bf16 operands
+//   EPI_GATED      h[M,H]   = bf16(act(g) * u),  g / u the products with rows
+//                  [0,H) / [H,2H) of W1, kept in fp32
+//   EPI_GATED_BWD  d_gu[M,2H] = (dh * u * act'(g) | dh * act(g)) for the
+//                  recomputed g, u and dh [M,H] read in the epilogue
+//   EPI_PARTIAL    fp32 sums over one part of K, joined by join_kernel, which
+//                  then applies one of the epilogues above
+//
+// The matmul and the epilogues of a transformer block's feed-forward half
+// (llmq "llama_model.cpp", LLamaModel::_forward_block and _backward_block) in
+// unquantised form; the gradients use EPI_LINEAR with MN-major operands
+// (dx = dz . W, dW = dz^T . x read dz, W and x where they lie).
+//
+// Pipeline: SM pairs (2-CTA clusters), persistent over 256 x 256 tiles, one
+// tcgen05.mma.cta_group::2 (M = 256, N = 256) chain per tile; CTA r of a pair
+// stages rows [128 r, 128 r + 128) of A and of the tile's 256 weight rows,
+// 256 bytes of K per stage and row, three stages.  One warp loads (TMA,
+// 128-byte swizzle), one thread of the leader issues the MMAs, four warps per
+// CTA run the epilogue out of one of two TMEM accumulators while the next tile
+// accumulates in the other.  Per SM and byte of K this loads 16 + 16 KB per
+// 128 x 256 outputs; a bf16 MMA takes twice the cycles of an E4M3 one over the
+// same bytes of shared memory, so the operand feed has room to spare.
+//
+// Every mbarrier wait is bounded; see gemm_fp8.cu for how a wait that runs out
+// ends the kernel (abort flag, status word, drained copies and MMAs).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "act.cuh"
+#include "common.cuh"
+#include "launch.h"
+#include "pipeline.cuh"
+#include "umma.cuh"
+
+namespace qffn {
+namespace {
+
+constexpr int BM = 128;                    // rows of A per CTA (256 per pair)
+constexpr int BN = 256;                    // accumulator columns
+constexpr int ROW_BYTES = 128;             // one swizzle atom row
+constexpr int BOX_BYTES = 128 * ROW_BYTES; // one TMA box: 128 rows
+constexpr int KBOX = 2;                    // boxes per operand and stage
+constexpr int STAGES = 3;
+constexpr int OP_BYTES = KBOX * BOX_BYTES; // one operand's share of a stage
+constexpr int STAGE_BYTES = 2 * OP_BYTES;
+constexpr int STEPS = 8;                   // MMAs per stage (32 bytes of K each)
+constexpr int NUM_THREADS = 192;
+constexpr int TMEM_COLS = 2 * BN;
+constexpr int NUM_BARS = 2 * STAGES + 5 + 8;
+constexpr int STAGE_BOX_BYTES = 32 * 128;  // epilogue staging box: 32 rows x 128 bytes
+constexpr int STAGING_BYTES = 4 * 2 * STAGE_BOX_BYTES;
+constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 + NUM_BARS * 8 + 16;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
+constexpr int GROUP_M = 8;
+constexpr uint16_t kBothCtas = 0x3;
+constexpr uint16_t kLeaderOnly = 0x1;
+constexpr unsigned long long kWaitLimitNs = 2000000000ull;
+constexpr unsigned long long kDrainLimitNs = 200000000ull;
+
+constexpr int OP_BF16 = 0, OP_E4M3 = 1;
+// elements of K per box row, and per stage
+constexpr int box_k(int op) { return op == OP_BF16 ? 64 : 128; }
+constexpr int stage_k(int op) { return KBOX * box_k(op); }
+
+constexpr int EPI_LINEAR = 0, EPI_GATED = 1, EPI_GATED_BWD = 2, EPI_PARTIAL = 3;
+
+// Instruction descriptor: D fp32 (bits 4-5 = 1); A and B formats at bits 7-9
+// and 10-12 (kind::f16: 1 = bf16; kind::f8f6f4: 0 = E4M3); bits 15 / 16: A / B
+// MN-major; N >> 3 at bits 17-22, M >> 4 at bits 24-28 (M = 256 over the pair).
+constexpr uint32_t idesc_for(int op, bool a_mn, bool b_mn, int n) {
+  return (1u << 4) | (op == OP_BF16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
+         (b_mn ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) | (uint32_t((2 * BM) >> 4) << 24);
+}
+
+__device__ unsigned int g_status;
+
+struct LinArgs {
+  const float* a_scale;     // E4M3 operands: one float each; NULL: no scaling
+  const float* w_scale;
+  const uint16_t* bias;     // EPI_LINEAR, optional
+  int has_in;               // EPI_LINEAR: add the bf16 tensor of the input map
+  int save_z;               // EPI_LINEAR: store z by the second output map
+  int M, N;                 // output rows and columns (gated: columns = H)
+  int up_row;               // gated: first up row of W1 (= H)
+  int tiles_m, tiles_n, num_units, num_kb;
+  int band_n;               // N-blocks per raster band
+  int split_from;           // units from here on are 128-column halves of the last tiles
+  int splits, kb_per_split, m_pad;   // EPI_PARTIAL
+};
+
+// D(tmem, both CTAs) (+)= A(smem, both CTAs) . B(smem, both CTAs)^T
+template <int OP>
+QFFN_DEVI void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  if (OP == OP_BF16)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Shared-memory descriptor of MMA step i of a stage's operand.
+// K-major: box i/4 (64 or 128 elements of K), 32 bytes along its 128-byte rows
+// per step.  MN-major (16-bit types): the operand's 128 M (N) values lie in two
+// boxes of 64 values x 128 K rows; a step is 16 K rows of 128 bytes (8-row
+// groups 1024 bytes apart) in both boxes, whose distance is the leading byte
+// offset.
+template <bool MN>
+QFFN_DEVI uint64_t step_desc(uint32_t base, int i) {
+  if (!MN) return sdesc_sw128(base + uint32_t(i >> 2) * BOX_BYTES + uint32_t(i & 3) * 32u);
+  const uint64_t d = sdesc_sw128(base + uint32_t(i) * 16u * ROW_BYTES);
+  return (d & ~(uint64_t(0x3FFF) << 16)) | (uint64_t(BOX_BYTES >> 4) << 16);
+}
+
+QFFN_DEVI bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, bool honour_abort = true,
+                         unsigned long long limit = kWaitLimitNs) {
+  return mbar_wait_bounded(bar, parity, abort_flag, &g_status, honour_abort, limit);
+}
+
+struct Unit {
+  int mb, nb;      // pair M-block (256 rows), N-block
+  int half;        // -1: whole tile; 0 / 1: first / second 128 accumulator columns of a split one
+  int sp;          // EPI_PARTIAL: part of K
+};
+
+template <int EPI>
+QFFN_DEVI Unit unit_coords(int u, const LinArgs& a) {
+  Unit r;
+  r.half = -1;
+  r.sp = 0;
+  int tile = u;
+  if (EPI == EPI_PARTIAL) {
+    tile = u / a.splits;
+    r.sp = u - tile * a.splits;
+  } else if (u >= a.split_from) {
+    tile = a.split_from + ((u - a.split_from) >> 1);
+    r.half = (u - a.split_from) & 1;
+  }
+  // bands of band_n N-blocks; within a band, groups of GROUP_M M-blocks sweep
+  // the band's N-blocks, M fastest, odd groups backwards
+  const int band_tiles = a.tiles_m * a.band_n;
+  const int band = tile / band_tiles;
+  const int n0 = band * a.band_n;
+  const int wb = min(a.band_n, a.tiles_n - n0);
+  const int t = tile - band * band_tiles;
+  const int per_group = GROUP_M * wb;
+  const int group = t / per_group;
+  const int first_m = group * GROUP_M;
+  const int gsize = min(a.tiles_m - first_m, GROUP_M);
+  const int k = t - group * per_group;
+  r.mb = first_m + k % gsize;
+  r.nb = n0 + ((group & 1) ? wb - 1 - k / gsize : k / gsize);
+  return r;
+}
+
+// tmO / tmZ: first and second output (EPI_LINEAR: out, z; GATED_BWD: dg, du);
+// tmI: tensor read in the epilogue (EPI_LINEAR: residual or previous output;
+// GATED_BWD: dh); tmBh: B with 64-row boxes for the half tiles.
+template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmO,
+                  const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ CUtensorMap tmI,
+                  const LinArgs args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + STAGES * OP_BYTES;
+  uint8_t* sStaging = smem + STAGES * STAGE_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sStaging + STAGING_BYTES);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t bar0 = smem_u32(bars);
+  // full[s] (leader): both CTAs' loads of stage s landed; empty[s]: the MMAs
+  // reading stage s are done; tfull[a]: accumulator a is complete; tempty[a]
+  // (leader): both CTAs' epilogue warps have read it; drain: all MMAs done;
+  // ld[q][b]: the TMA load into staging box b of epilogue warp q has landed
+  auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
+  auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * uint32_t(2 * STAGES + 4);
+  auto ld_bar = [&](int q, int b) { return bar0 + 8u * uint32_t(2 * STAGES + 5 + 2 * q + b); };
+
+  constexpr bool GATED = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = int(cluster_id_x()), num_pairs = int(num_clusters_x());
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 8);
+    }
+    mbar_init(drain_bar, 1);
+    for (int q = 0; q < 4; ++q) {
+      mbar_init(ld_bar(q, 0), 1);
+      mbar_init(ld_bar(q, 1), 1);
+    }
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmO);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  cluster_sync_all();      // both CTAs' barriers exist before either signals the other's
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();              // nothing in global memory is touched before the preceding kernel is done
+  pdl_trigger();
+
+  // K blocks of a unit
+  auto kb_begin = [&](const Unit& u) { return EPI == EPI_PARTIAL ? u.sp * args.kb_per_split : 0; };
+  auto kb_end = [&](const Unit& u) {
+    return EPI == EPI_PARTIAL ? min(args.num_kb, (u.sp + 1) * args.kb_per_split) : args.num_kb;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer
+      uint32_t issued = 0, issued_parity = 0;
+      int it = 0;
+      bool ok = true;
+      for (int un = pair; ok && un < args.num_units; un += num_pairs) {
+        const Unit u = unit_coords<EPI>(un, args);
+        const int rowA = u.mb * (2 * BM) + int(rank) * BM;
+        // this CTA's weight rows: half of the tile's 256 (of a half tile's
+        // 128); gated: CTA 0 the gate rows, CTA 1 the matching up rows
+        const int rowB = GATED ? (rank == 0 ? 0 : args.up_row) + u.nb * 128 + (u.half < 0 ? 0 : u.half * 64)
+                         : u.half < 0 ? u.nb * BN + int(rank) * 128
+                                      : u.nb * BN + u.half * 128 + int(rank) * 64;
+        const uint32_t stage_tx = u.half < 0 ? 2 * STAGE_BYTES : 2 * (OP_BYTES + OP_BYTES / 2);
+        const int kb1 = kb_end(u);
+        for (int kb = kb_begin(u); kb < kb1; ++kb, ++it) {
+          const int s = it % STAGES;
+          const uint32_t ph = uint32_t(it / STAGES) & 1u;
+          if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) { ok = false; break; }
+          if (rank == 0) mbar_expect_tx(full_bar(s), stage_tx);
+          const uint32_t fb = map_to_rank(full_bar(s), 0);
+          const int k0 = kb * stage_k(OP);
+#pragma unroll
+          for (int bx = 0; bx < KBOX; ++bx) {
+            const uint32_t da = smem_u32(sA + s * OP_BYTES + bx * BOX_BYTES);
+            const uint32_t db = smem_u32(sB + s * OP_BYTES + bx * BOX_BYTES);
+            if (A_MN) tma_load_2d_pair(da, &tmA, fb, rowA + bx * 64, k0);
+            else tma_load_2d_pair(da, &tmA, fb, k0 + bx * box_k(OP), rowA);
+            if (B_MN) {
+              // a half tile's 64 rows are one box
+              if (u.half < 0 || bx == 0) tma_load_2d_pair(db, &tmB, fb, rowB + bx * 64, k0);
+            } else {
+              tma_load_2d_pair(db, u.half < 0 ? &tmB : &tmBh, fb, k0 + bx * box_k(OP), rowB);
+            }
+          }
+          issued |= 1u << s;
+          issued_parity = (issued_parity & ~(1u << s)) | (ph << s);
+        }
+      }
+      // every phase the leader armed completes before shared memory is released
+      if (rank == 0)
+        for (int s = 0; s < STAGES; ++s)
+          if (issued & (1u << s))
+            mbar_wait(full_bar(s), (issued_parity >> s) & 1u, abort_flag, false, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ------------------------------------------------------------ MMA issuer (leader)
+      int it = 0, local = 0;
+      bool ok = true;
+      for (int un = pair; ok && un < args.num_units; un += num_pairs, ++local) {
+        const int acc = local & 1;
+        const uint32_t aph = uint32_t(local >> 1) & 1u;
+        if (!mbar_wait_cluster_bounded(tempty_bar(acc), aph ^ 1u, abort_flag, &g_status, kWaitLimitNs)) break;
+        tc_fence_after();
+        const Unit u = unit_coords<EPI>(un, args);
+        const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
+        const uint32_t idesc = u.half < 0 ? idesc_for(OP, A_MN, B_MN, BN) : idesc_for(OP, A_MN, B_MN, BN / 2);
+        const int kb0 = kb_begin(u), kb1 = kb_end(u);
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = it % STAGES;
+          const uint32_t ph = uint32_t(it / STAGES) & 1u;
+          if (!mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(sA + s * OP_BYTES);
+          const uint32_t b0 = smem_u32(sB + s * OP_BYTES);
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i)
+            mma_pair<OP>(d_tmem, step_desc<A_MN>(a0, i), step_desc<B_MN>(b0, i), idesc, uint32_t((kb - kb0) | i));
+          mma_commit_mc(empty_bar(s), kBothCtas);
+        }
+        if (!ok) break;
+        mma_commit_mc(tfull_bar(acc), kBothCtas);
+      }
+      mma_commit_mc(drain_bar, kLeaderOnly);
+      mbar_wait(drain_bar, 0, abort_flag, false, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int q = warp & 3;                  // TMEM lane quarter: rows 32 q .. 32 q + 31 of the CTA's 128
+    const float scale = args.a_scale != nullptr ? args.a_scale[0] * args.w_scale[0] : 1.0f;
+    uint8_t* const box0 = sStaging + (q * 2) * STAGE_BOX_BYTES;
+    auto box = [&](int b) { return box0 + b * STAGE_BOX_BYTES; };
+    const uint32_t lane_off = uint32_t(lane) * 128u;
+    auto chunk_off = [&](int chunk) { return lane_off + (uint32_t(chunk ^ (lane & 7)) << 4); };
+    // Two ways to use the two staging boxes (32 rows x 64 bf16 columns):
+    //  alternating: successive groups go out of the two boxes in turn; with an
+    //    input tensor (an even number of groups per unit, the first in box 0)
+    //    a box is filled by a TMA load first, the next group's load in flight
+    //    while a group is summed, and the result replaces it in place
+    //  paired (two outputs): box 0 holds the input and then the first output,
+    //    box 1 the second output
+    const bool paired = EPI == EPI_GATED_BWD || (EPI == EPI_LINEAR && args.save_z != 0);
+    const bool has_in = EPI == EPI_GATED_BWD || (EPI == EPI_LINEAR && args.has_in != 0);
+    uint32_t ld_par = 0u;                    // bit b: parity of the next load into box b
+    uint32_t ld_pending = 0u;                // lane 0, bit b: a load has been issued and not waited for
+    int flip = 0;
+    auto first_col = [&](const Unit& u) {    // output column of the unit's first group
+      return GATED ? u.nb * 128 + (u.half < 0 ? 0 : u.half * 64) : u.nb * BN + (u.half < 0 ? 0 : u.half * 128);
+    };
+    auto first_row = [&](const Unit& u) { return u.mb * (2 * BM) + int(rank) * BM + q * 32; };
+    auto load_in = [&](const Unit& u, int g, int b) {   // lane 0
+      mbar_expect_tx(ld_bar(q, b), STAGE_BOX_BYTES);
+      tma_load_2d(smem_u32(box(b)), &tmI, ld_bar(q, b), first_col(u) + g * 64, first_row(u));
+      ld_pending |= 1u << b;
+    };
+    if (has_in && lane == 0 && pair < args.num_units) load_in(unit_coords<EPI>(pair, args), 0, 0);
+    int local = 0;
+    for (int un = pair; un < args.num_units; un += num_pairs, ++local) {
+      const int acc = local & 1;
+      const uint32_t aph = uint32_t(local >> 1) & 1u;
+      if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) break;
+      tc_fence_after();
+      const Unit u = unit_coords<EPI>(un, args);
+      const int row0 = first_row(u);
+      const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * BN);
+      const int acc_cols = u.half < 0 ? BN : BN / 2;
+      if (EPI == EPI_PARTIAL) {
+        // fp32 boxes of 32 rows x 32 columns, rows padded per part of K
+#pragma unroll 1
+        for (int c0 = 0; c0 < BN; c0 += 32) {
+          uint32_t v[32];
+          tmem_ld32(tbase + uint32_t(c0), v);
+          uint8_t* b = box((c0 >> 5) & 1);
+          if (lane == 0) bulk_wait_read_1();
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(b + chunk_off(k)) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int x = u.nb * BN + c0;
+          if (lane == 0) {
+            if (row0 < args.M && x < args.N) tma_store_2d(&tmO, smem_u32(b), x, u.sp * args.m_pad + row0);
+            bulk_commit();
+          }
+        }
+      } else {
+        const int groups = GATED ? acc_cols / 128 : acc_cols / 64;
+        bool ok = true;
+        for (int g = 0; g < groups; ++g) {
+          const int b = paired ? 0 : flip;
+          flip ^= 1;
+          if (has_in) {
+            if (!paired && g + 1 < groups) {
+              if (lane == 0) {
+                bulk_wait_read_0();          // the store that last read the other box is done
+                load_in(u, g + 1, b ^ 1);
+              }
+              __syncwarp();
+            }
+            if (!mbar_wait(ld_bar(q, b), (ld_par >> b) & 1u, abort_flag)) { ok = false; break; }
+            ld_par ^= 1u << b;
+            ld_pending &= ~(1u << b);
+          } else {
+            if (lane == 0) {
+              if (paired) bulk_wait_read_0();
+              else bulk_wait_read_1();
+            }
+            __syncwarp();
+          }
+          const int col0 = first_col(u) + g * 64;
+          if (!GATED) {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              const int col = col0 + h * 32;
+              uint4 bias[4];
+              if (args.bias != nullptr) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  bias[k] = col + 8 * k < args.N ? ld16_ro(args.bias + col + 8 * k) : make_uint4(0, 0, 0, 0);
+              }
+              uint32_t v[32];
+              tmem_ld32(tbase + uint32_t(g * 64 + h * 32), v);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t off = chunk_off(h * 4 + k);
+                float z[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[j] = __uint_as_float(v[8 * k + j]);
+                if (OP == OP_E4M3) {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) z[j] *= scale;
+                }
+                if (args.bias != nullptr) {
+                  const uint32_t bw[4] = {bias[k].x, bias[k].y, bias[k].z, bias[k].w};
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    z[2 * j] += bf16_lo(bw[j]);
+                    z[2 * j + 1] += bf16_hi(bw[j]);
+                  }
+                }
+                if (args.save_z)
+                  *reinterpret_cast<uint4*>(box(1) + off) =
+                      make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
+                                 pack_bf16x2(z[6], z[7]));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[j] = act_f32<ACT>(z[j]);
+                if (args.has_in) {
+                  const uint4 o4 = *reinterpret_cast<const uint4*>(box(b) + off);
+                  const uint32_t ow[4] = {o4.x, o4.y, o4.z, o4.w};
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    z[2 * j] += bf16_lo(ow[j]);
+                    z[2 * j + 1] += bf16_hi(ow[j]);
+                  }
+                }
+                *reinterpret_cast<uint4*>(box(b) + off) =
+                    make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
+                               pack_bf16x2(z[6], z[7]));
+              }
+            }
+          } else {
+            const int up_off = acc_cols / 2;  // accumulator column of u
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+              const uint32_t c = uint32_t(g * 64 + h * 16);
+              uint32_t gv[16], uv[16];
+              tmem_ld16x2_issue(tbase + c, tbase + uint32_t(up_off) + c, gv, uv);
+              tmem_wait_ld16(gv, uv);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t off = chunk_off(h * 2 + k);
+                uint32_t p[4], p2[4];
+                uint4 d4 = make_uint4(0, 0, 0, 0);
+                if (EPI == EPI_GATED_BWD) d4 = *reinterpret_cast<const uint4*>(box0 + off);
+                const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float g0 = __uint_as_float(gv[8 * k + 2 * j]), g1 = __uint_as_float(gv[8 * k + 2 * j + 1]);
+                  const float u0 = __uint_as_float(uv[8 * k + 2 * j]), u1 = __uint_as_float(uv[8 * k + 2 * j + 1]);
+                  if (EPI == EPI_GATED) {
+                    p[j] = pack_bf16x2(act_f32<ACT>(g0) * u0, act_f32<ACT>(g1) * u1);
+                  } else {
+                    float f0, df0, f1, df1;
+                    act_grad_f32<ACT>(g0, f0, df0);
+                    act_grad_f32<ACT>(g1, f1, df1);
+                    const float d0 = bf16_lo(dw[j]), d1 = bf16_hi(dw[j]);
+                    p[j] = pack_bf16x2(d0 * u0 * df0, d1 * u1 * df1);
+                    p2[j] = pack_bf16x2(d0 * f0, d1 * f1);
+                  }
+                }
+                *reinterpret_cast<uint4*>(box(b) + off) = make_uint4(p[0], p[1], p[2], p[3]);
+                if (EPI == EPI_GATED_BWD)
+                  *reinterpret_cast<uint4*>(box(1) + off) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            // rows beyond M and columns beyond N are clipped by the tensor maps
+            if (row0 < args.M && col0 < args.N) {
+              tma_store_2d(&tmO, smem_u32(box(b)), col0, row0);
+              if (paired) tma_store_2d(&tmZ, smem_u32(box(1)), col0, row0);
+            }
+            bulk_commit();
+            if (has_in && (paired || g + 1 == groups)) {
+              // the next load into box 0: of this tile (paired) or of the next unit
+              bulk_wait_read_0();
+              if (g + 1 < groups) load_in(u, g + 1, 0);
+              else if (un + num_pairs < args.num_units) load_in(unit_coords<EPI>(un + num_pairs, args), 0, 0);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(map_to_rank(tempty_bar(acc), 0));
+    }
+    // stores complete, and no load into shared memory is in flight, before exit
+    if (lane == 0) {
+      bulk_wait_all();
+      for (int b = 0; b < 2; ++b)
+        if ((ld_pending >> b) & 1u) mbar_wait(ld_bar(q, b), (ld_par >> b) & 1u, abort_flag, false, kDrainLimitNs);
+    }
+  }
+
+  // Both CTAs finish together: the leader's MMAs write the peer's TMEM and
+  // both CTAs signal barriers of the other.
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ joining the parts of K
+// Eight output columns per thread: the parts' fp32 sums added in order, then
+// the epilogue.  partial is [splits][m_pad][ld]; gated forms read columns c
+// and H + c.
+template <int EPI, int ACT>
+__global__ void __launch_bounds__(256) join_kernel(uint16_t* out, uint16_t* out2, const float* partial,
+                                                   const uint16_t* bias, const uint16_t* in, const float* a_scale,
+                                                   const float* w_scale, int splits, int64_t m_pad, int64_t ld,
+                                                   int64_t M, int64_t N) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t per_row = N >> 3;
+  const int64_t total = M * per_row;
+  const float scale = a_scale != nullptr ? a_scale[0] * w_scale[0] : 1.0f;
+  auto sum8 = [&](int64_t row, int64_t col, float (&f)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+    for (int s = 0; s < splits; ++s) {
+      const float4* p = reinterpret_cast<const float4*>(partial + (size_t(s) * size_t(m_pad) + size_t(row)) * size_t(ld) + size_t(col));
+      const float4 a = p[0], b = p[1];
+      f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+      f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+    }
+  };
+  auto pack = [](const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  };
+  auto unpack = [](uint4 v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = bf16_lo(w[j]);
+      f[2 * j + 1] = bf16_hi(w[j]);
+    }
+  };
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += int64_t(gridDim.x) * 256) {
+    const int64_t row = i / per_row, col = (i - row * per_row) * 8;
+    float z[8], t[8];
+    sum8(row, col, z);
+    if (EPI == EPI_LINEAR) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] *= scale;
+      if (bias != nullptr) {
+        unpack(ld16_ro(bias + col), t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] += t[j];
+      }
+      if (out2 != nullptr) stg16(out2 + row * N + col, pack(z));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = act_f32<ACT>(z[j]);
+      if (in != nullptr) {
+        unpack(ld16_once(in + row * N + col), t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] += t[j];
+      }
+      stg16(out + row * N + col, pack(z));
+    } else {
+      float up[8];
+      sum8(row, N + col, up);
+      if (EPI == EPI_GATED) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = act_f32<ACT>(z[j]) * up[j];
+        stg16(out + row * N + col, pack(z));
+      } else {
+        unpack(ld16_ro(in + row * N + col), t);
+        float du[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float f, df;
+          act_grad_f32<ACT>(z[j], f, df);
+          z[j] = t[j] * up[j] * df;
+          du[j] = t[j] * f;
+        }
+        stg16(out + row * 2 * N + col, pack(z));
+        stg16(out + row * 2 * N + N + col, pack(du));
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ dz = dout * act'(z) and its column sums
+// A block covers 256 columns (one warp's 32 lanes x 8 columns) and every
+// (8 * gridDim.y)-th group of rows; thread (warp w, lane l) owns columns
+// 8 l .. 8 l + 7 of rows w, w + 8, ...  The column sums are taken from the fp32
+// dz before its rounding; the block's eight warps are added in order and
+// column_sum_kernel adds the blocks'.  ACT_NONE (dz = dout) only sums.
+template <int ACT>
+__global__ void __launch_bounds__(256) act_backward_kernel(uint16_t* dz, float* partial, const uint16_t* dout,
+                                                           const uint16_t* z, int64_t M, int64_t N) {
+  __shared__ float comb[8][256 + 8];
+  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+  const int64_t col = int64_t(blockIdx.x) * 256 + l * 8;
+  const bool live = col < N;
+  float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (live) {
+    for (int64_t row = int64_t(blockIdx.y) * 8 + w; row < M; row += int64_t(gridDim.y) * 8) {
+      const size_t i = size_t(row) * size_t(N) + size_t(col);
+      const uint4 d4 = ld16_ro_stream(dout + i);
+      const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
+      float d[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d[2 * j] = bf16_lo(dw[j]);
+        d[2 * j + 1] = bf16_hi(dw[j]);
+      }
+      if (ACT != ACT_NONE) {
+        const uint4 z4 = ld16_ro_stream(z + i);
+        const uint32_t zw[4] = {z4.x, z4.y, z4.z, z4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float f, df;
+          act_grad_f32<ACT>(bf16_lo(zw[j]), f, df);
+          d[2 * j] *= df;
+          act_grad_f32<ACT>(bf16_hi(zw[j]), f, df);
+          d[2 * j + 1] *= df;
+        }
+        stg16(dz + i, make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[4], d[5]),
+                                 pack_bf16x2(d[6], d[7])));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += d[j];
+    }
+  }
+  if (partial == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) comb[w][l * 8 + j] = s[j];
+  __syncthreads();
+  const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (c < N) {
+    float v = comb[0][threadIdx.x];
+    for (int k = 1; k < 8; ++k) v += comb[k][threadIdx.x];
+    partial[size_t(blockIdx.y) * size_t(N) + size_t(c)] = v;
+  }
+}
+
+// ------------------------------------------------------------------ host side
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+// Tensor map of [rows, cols] (cols contiguous, rows `ld` elements apart) with
+// boxes of box_rows rows x 128 bytes, 128-byte swizzle; zeros outside.
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, int elem, const void* ptr, int64_t rows, int64_t cols,
+              int64_t ld, int box_rows, CUtensorMapL2promotion promo) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+  cuuint64_t strides[1] = {cuuint64_t(ld) * cuuint64_t(elem)};
+  cuuint32_t box[2] = {cuuint32_t(128 / elem), cuuint32_t(box_rows)};
+  cuuint32_t estr[2] = {1u, 1u};
+  return fn(map, type, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, promo, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// An MMA operand: [rows, k] K-major or, `mn`, [k, rows] as it lies in memory.
+template <int OP>
+bool operand_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t k, bool mn, int box_rows = 128) {
+  const CUtensorMapDataType t = OP == OP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  return mn ? make_map(map, t, OP == OP_BF16 ? 2 : 1, ptr, k, rows, rows, box_rows, CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
+            : make_map(map, t, OP == OP_BF16 ? 2 : 1, ptr, rows, k, k, box_rows, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+// A bf16 tensor the epilogue stores or loads in boxes of 32 rows x 64 columns.
+bool epi_map(CUtensorMap* map, const uint16_t* ptr, int64_t rows, int64_t cols, int64_t ld) {
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, rows, cols, ld, 32, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
+// 2-CTA clusters of a form that fit on the device at once (cached per device).
+template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
+cudaError_t max_pairs(int* pairs) {
+  static int cached[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && cached[dev] > 0) {
+    *pairs = cached[dev];
+    return cudaSuccess;
+  }
+  const auto fn = linear_kernel<OP, EPI, ACT, A_MN, B_MN>;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (num_sms() / 2));
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+  if (e != cudaSuccess) return e;
+  if (n < 1) return cudaErrorInvalidConfiguration;
+  if (dev >= 0 && dev < 64) cached[dev] = n;
+  *pairs = n;
+  return cudaSuccess;
+}
+
+struct Maps {
+  CUtensorMap a, b, bh, o, z, i;
+};
+
+template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
+cudaError_t launch(const Maps& m, const LinArgs& a, int pairs, bool pdl, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * unsigned(a.num_units < pairs ? a.num_units : pairs));
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, linear_kernel<OP, EPI, ACT, A_MN, B_MN>, m.a, m.b, m.bh, m.o, m.z, m.i, a);
+}
+
+// How a product [M, K] x [N, K]^T is cut: the tiles, and the parts of K where
+// the tiles alone would leave most SM pairs idle.
+struct Plan {
+  int tiles_m, tiles_n, tiles, num_kb, splits, kb_per_split;
+  int64_t m_pad;
+};
+constexpr int kPlanPairs = kNumSMsHint / 2;   // fixed, so a workspace size needs no device query
+Plan make_plan(int64_t M, int64_t N, int64_t K, int op) {
+  Plan p;
+  p.tiles_m = int((M + 2 * BM - 1) / (2 * BM));
+  p.tiles_n = int((N + BN - 1) / BN);
+  p.tiles = p.tiles_m * p.tiles_n;
+  p.num_kb = int((K + stage_k(op) - 1) / stage_k(op));
+  p.m_pad = (M + 31) / 32 * 32;
+  p.splits = 1;
+  if (p.tiles > 0 && 2 * p.tiles <= kPlanPairs) {
+    int s = kPlanPairs / p.tiles;
+    if (s > p.num_kb / 4) s = p.num_kb / 4;   // at least four stages of work per part
+    if (s > 16) s = 16;
+    if (s > 1) p.splits = s;
+  }
+  p.kb_per_split = (p.num_kb + p.splits - 1) / p.splits;
+  if (p.num_kb > 0) p.splits = (p.num_kb + p.kb_per_split - 1) / p.kb_per_split;
+  return p;
+}
+size_t plan_bytes(const Plan& p, int64_t N) {
+  return p.splits > 1 ? size_t(p.splits) * size_t(p.m_pad) * size_t(N) * sizeof(float) : 0;
+}
+
+// N-blocks per raster band: about 32 MB of weights, so that a band stays in L2
+// while the row groups cycle through it (measured for the FP8 gate|up GEMM,
+// gemm_fp8.cu); one band where the activations are the larger operand.
+int band_blocks(int tiles_n, int64_t M, int64_t N, int64_t k_bytes) {
+  if (N <= M) return tiles_n;
+  int64_t b = (int64_t(32) << 20) / (int64_t(BN) * (k_bytes > 0 ? k_bytes : 1));
+  if (b < 1) b = 1;
+  return b > tiles_n ? tiles_n : int(b);
+}
+
+template <int EPI, int ACT>
+cudaError_t launch_join(uint16_t* out, uint16_t* out2, const float* partial, const uint16_t* bias, const uint16_t* in,
+                        const float* a_scale, const float* w_scale, const Plan& p, int64_t ld, int64_t M, int64_t N,
+                        cudaStream_t s) {
+  const int64_t total = M * (N / 8);
+  int64_t blocks = (total + 255) / 256;
+  const int64_t cap = int64_t(num_sms()) * 8;
+  if (blocks > cap) blocks = cap;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(blocks));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<EPI, ACT>, out, out2, partial, bias, in, a_scale, w_scale, p.splits,
+                            p.m_pad, ld, M, N);
+}
+
+// One product with its epilogue.  EPI_LINEAR: N output columns; gated forms:
+// N = H and B = W1 [2H, K].  `partial` holds plan_bytes().
+template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
+cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_scale, const void* B,
+                    const float* w_scale, const uint16_t* bias, const uint16_t* in, int64_t M, int64_t N, int64_t K,
+                    float* partial, bool pdl, cudaStream_t s) {
+  constexpr bool GATED = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
+  const int64_t brows = GATED ? 2 * N : N;
+  const Plan p = make_plan(M, brows, K, OP);
+  Maps m;
+  if (!operand_map<OP>(&m.a, A, M, K, A_MN) || !operand_map<OP>(&m.b, B, brows, K, B_MN)) return cudaErrorInvalidValue;
+  m.bh = m.b;
+  LinArgs a{};
+  a.M = int(M);
+  a.tiles_m = p.tiles_m;
+  a.num_kb = p.num_kb;
+  a.up_row = int(N);
+  a.splits = 1;
+  int pairs = 0;
+  cudaError_t e;
+  if (p.splits > 1) {
+    if (!make_map(&m.o, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, partial, p.splits * p.m_pad, brows, brows, 32,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE))
+      return cudaErrorInvalidValue;
+    m.z = m.i = m.o;
+    a.N = int(brows);
+    a.tiles_n = p.tiles_n;
+    a.band_n = p.tiles_n;
+    a.splits = p.splits;
+    a.kb_per_split = p.kb_per_split;
+    a.m_pad = int(p.m_pad);
+    a.num_units = a.split_from = p.tiles * p.splits;
+    if ((e = max_pairs<OP, EPI_PARTIAL, ACT_NONE, A_MN, B_MN>(&pairs)) != cudaSuccess) return e;
+    if ((e = launch<OP, EPI_PARTIAL, ACT_NONE, A_MN, B_MN>(m, a, pairs, pdl, s)) != cudaSuccess) return e;
+    return launch_join<EPI, ACT>(out, z, partial, bias, in, a_scale, w_scale, p, brows, M, N, s);
+  }
+  a.N = int(N);
+  a.a_scale = a_scale;
+  a.w_scale = w_scale;
+  a.bias = bias;
+  a.has_in = in != nullptr;
+  a.save_z = z != nullptr;
+  a.tiles_n = GATED ? int((N + 127) / 128) : p.tiles_n;
+  a.band_n = band_blocks(a.tiles_n, M, brows, K * (OP == OP_BF16 ? 2 : 1));
+  a.num_units = a.split_from = a.tiles_m * a.tiles_n;
+  if (EPI == EPI_GATED_BWD) {
+    // the halves of d_gu [M, 2H] as two tensors, so that a box ending beyond H is clipped there
+    if (!epi_map(&m.o, out, M, N, 2 * N) || !epi_map(&m.z, out + N, M, N, 2 * N) || !epi_map(&m.i, in, M, N, N))
+      return cudaErrorInvalidValue;
+  } else {
+    if (!epi_map(&m.o, out, M, N, N)) return cudaErrorInvalidValue;
+    m.z = m.i = m.o;
+    if (z != nullptr && !epi_map(&m.z, z, M, N, N)) return cudaErrorInvalidValue;
+    if (in != nullptr && !epi_map(&m.i, in, M, N, N)) return cudaErrorInvalidValue;
+  }
+  if ((e = max_pairs<OP, EPI, ACT, A_MN, B_MN>(&pairs)) != cudaSuccess) return e;
+  // a last partial wave of R <= pairs / 2 tiles runs as 2 R half tiles in half the time
+  const int r = a.num_units % pairs;
+  if (EPI != EPI_GATED_BWD && a.num_units > pairs && r > 0 && 2 * r <= pairs) {
+    if (!B_MN && !operand_map<OP>(&m.bh, B, brows, K, false, 64)) return cudaErrorInvalidValue;
+    a.split_from = a.num_units - r;
+    a.num_units += r;
+  }
+  return launch<OP, EPI, ACT, A_MN, B_MN>(m, a, pairs, pdl, s);
+}
+
+int act_backward_blocks(int64_t M, int64_t N) {
+  const int64_t cols = (N + 255) / 256;
+  int64_t rows = (int64_t(kNumSMsHint) * 8 + cols - 1) / cols;   // about eight blocks per SM
+  const int64_t need = (M + 7) / 8;
+  if (rows > need) rows = need;
+  return int(rows < 1 ? 1 : (rows > 65535 ? 65535 : rows));
+}
+
+size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+
+// linear backward workspace: dz [M,N] bf16 | column partials | parts of K of the larger product
+void linear_bwd_offsets(int64_t M, int64_t N, int64_t K, size_t off[4]) {
+  off[0] = 0;
+  off[1] = round256(size_t(M) * size_t(N) * 2);
+  off[2] = off[1] + round256(size_t(act_backward_blocks(M, N)) * size_t(N) * sizeof(float));
+  const size_t a = plan_bytes(make_plan(M, K, N, OP_BF16), K), b = plan_bytes(make_plan(N, K, M, OP_BF16), K);
+  off[3] = off[2] + round256(a > b ? a : b);
+}
+
+// gated backward workspace: d_gu [M,2H] bf16 | parts of K of the largest product
+void gated_bwd_offsets(int64_t M, int64_t C, int64_t H, size_t off[3]) {
+  off[0] = 0;
+  off[1] = round256(size_t(M) * size_t(2 * H) * 2);
+  size_t a = plan_bytes(make_plan(M, 2 * H, C, OP_BF16), 2 * H);
+  const size_t b = plan_bytes(make_plan(M, C, 2 * H, OP_BF16), C), c = plan_bytes(make_plan(2 * H, C, M, OP_BF16), C);
+  a = a > b ? a : b;
+  off[2] = off[1] + round256(a > c ? a : c);
+}
+
+}  // namespace
+
+size_t linear_workspace(int64_t M, int64_t N, int64_t K, bool fp8) {
+  return plan_bytes(make_plan(M, N, K, fp8 ? OP_E4M3 : OP_BF16), N);
+}
+size_t gated_workspace(int64_t M, int64_t C, int64_t H) { return plan_bytes(make_plan(M, 2 * H, C, OP_BF16), 2 * H); }
+size_t linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
+  size_t off[4];
+  linear_bwd_offsets(M, N, K, off);
+  return off[3];
+}
+size_t gated_backward_workspace(int64_t M, int64_t C, int64_t H) {
+  size_t off[3];
+  gated_bwd_offsets(M, C, H, off);
+  return off[2];
+}
+
+#define QFFN_ACT_SWITCH(act, EXPR)                                 \
+  switch (act) {                                                   \
+    case ACT_RELU: { constexpr int ACT = ACT_RELU; return EXPR; }  \
+    case ACT_GELU: { constexpr int ACT = ACT_GELU; return EXPR; }  \
+    case ACT_GELU_TANH: { constexpr int ACT = ACT_GELU_TANH; return EXPR; } \
+    case ACT_SILU: { constexpr int ACT = ACT_SILU; return EXPR; }  \
+    default: { constexpr int ACT = ACT_NONE; return EXPR; }        \
+  }
+
+cudaError_t launch_linear(uint16_t* out, uint16_t* z, const uint16_t* x, const uint16_t* w, const uint16_t* bias,
+                          const uint16_t* res, int act, int64_t M, int64_t N, int64_t K, float* ws, cudaStream_t s) {
+  if (M == 0) return cudaSuccess;
+  QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_LINEAR, ACT, false, false>(out, z, x, nullptr, w, nullptr, bias, res, M, N,
+                                                                        K, ws, false, s)));
+}
+
+cudaError_t launch_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, const float* x_scale, const uint8_t* w,
+                              const float* w_scale, const uint16_t* bias, const uint16_t* res, int act, int64_t M,
+                              int64_t N, int64_t K, float* ws, cudaStream_t s) {
+  if (M == 0) return cudaSuccess;
+  QFFN_ACT_SWITCH(act, (product<OP_E4M3, EPI_LINEAR, ACT, false, false>(out, z, x, x_scale, w, w_scale, bias, res, M, N,
+                                                                        K, ws, false, s)));
+}
+
+cudaError_t launch_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int act, int64_t M, int64_t C, int64_t H,
+                         float* ws, cudaStream_t s) {
+  if (M == 0) return cudaSuccess;
+  QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_GATED, ACT, false, false>(h, nullptr, x, nullptr, w1, nullptr, nullptr,
+                                                                       nullptr, M, H, C, ws, false, s)));
+}
+
+namespace {
+template <int ACT>
+cudaError_t run_act_backward(uint16_t* dz, float* partial, const uint16_t* dout, const uint16_t* z, int64_t M,
+                             int64_t N, cudaStream_t s) {
+  const dim3 grid(unsigned((N + 255) / 256), unsigned(act_backward_blocks(M, N)));
+  act_backward_kernel<ACT><<<grid, 256, 0, s>>>(dz, partial, dout, z, M, N);
+  return cudaGetLastError();
+}
+cudaError_t act_backward(uint16_t* dz, float* partial, const uint16_t* dout, const uint16_t* z, int act, int64_t M,
+                         int64_t N, cudaStream_t s) {
+  QFFN_ACT_SWITCH(act, (run_act_backward<ACT>(dz, partial, dout, z, M, N, s)));
+}
+cudaError_t gated_bwd_product(uint16_t* dgu, const uint16_t* dh, const uint16_t* x, const uint16_t* w1, int act,
+                              int64_t M, int64_t C, int64_t H, float* part, cudaStream_t s) {
+  QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_GATED_BWD, ACT, false, false>(dgu, nullptr, x, nullptr, w1, nullptr,
+                                                                           nullptr, dh, M, H, C, part, false, s)));
+}
+// dx [M,K] = dz [M,N] . W [N,K];  dw [N,K] (+)= dz^T . x [M,K]: W, dz and x read where they lie
+cudaError_t grad_products(uint16_t* dx, uint16_t* dw, const uint16_t* dz, const uint16_t* x, const uint16_t* w,
+                          int64_t M, int64_t N, int64_t K, bool accumulate, float* part, bool pdl, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (dx != nullptr &&
+      (e = product<OP_BF16, EPI_LINEAR, ACT_NONE, false, true>(dx, nullptr, dz, nullptr, w, nullptr, nullptr, nullptr, M,
+                                                               K, N, part, pdl, s)) != cudaSuccess)
+    return e;
+  return product<OP_BF16, EPI_LINEAR, ACT_NONE, true, true>(dw, nullptr, dz, nullptr, x, nullptr, nullptr,
+                                                            accumulate ? dw : nullptr, N, K, M, part,
+                                                            pdl || dx != nullptr, s);
+}
+}  // namespace
+
+cudaError_t launch_linear_backward(uint16_t* dx, uint16_t* dw, float* dbias, const uint16_t* dout, const uint16_t* z,
+                                   const uint16_t* x, const uint16_t* w, int act, int64_t M, int64_t N, int64_t K,
+                                   bool accumulate, uint8_t* ws, cudaStream_t s) {
+  cudaError_t e;
+  if (M == 0) {
+    // sums over no rows: zero, or unchanged when accumulating
+    if (accumulate) return cudaSuccess;
+    if ((e = cudaMemsetAsync(dw, 0, size_t(N) * size_t(K) * 2, s)) != cudaSuccess) return e;
+    return dbias != nullptr ? cudaMemsetAsync(dbias, 0, size_t(N) * sizeof(float), s) : cudaSuccess;
+  }
+  size_t off[4];
+  linear_bwd_offsets(M, N, K, off);
+  uint16_t* dzb = reinterpret_cast<uint16_t*>(ws + off[0]);
+  float* cols = reinterpret_cast<float*>(ws + off[1]);
+  float* part = reinterpret_cast<float*>(ws + off[2]);
+  const uint16_t* dz = act == ACT_NONE ? dout : dzb;
+  bool chained = false;
+  if (act != ACT_NONE || dbias != nullptr) {
+    if ((e = act_backward(dzb, dbias != nullptr ? cols : nullptr, dout, z, act, M, N, s)) != cudaSuccess) return e;
+    if (dbias != nullptr) {
+      if ((e = launch_column_sum(dbias, nullptr, cols, act_backward_blocks(M, N), N, N, accumulate, s)) != cudaSuccess)
+        return e;
+    }
+    chained = true;
+  }
+  return grad_products(dx, dw, dz, x, w, M, N, K, accumulate, part, chained, s);
+}
+
+cudaError_t launch_gated_backward(uint16_t* dx, uint16_t* dw1, const uint16_t* dh, const uint16_t* x,
+                                  const uint16_t* w1, int act, int64_t M, int64_t C, int64_t H, bool accumulate,
+                                  uint8_t* ws, cudaStream_t s) {
+  if (M == 0) return accumulate ? cudaSuccess : cudaMemsetAsync(dw1, 0, size_t(2 * H) * size_t(C) * 2, s);
+  size_t off[3];
+  gated_bwd_offsets(M, C, H, off);
+  uint16_t* dgu = reinterpret_cast<uint16_t*>(ws + off[0]);
+  float* part = reinterpret_cast<float*>(ws + off[1]);
+  const cudaError_t e = gated_bwd_product(dgu, dh, x, w1, act, M, C, H, part, s);
+  if (e != cudaSuccess) return e;
+  return grad_products(dx, dw1, dgu, x, w1, M, 2 * H, C, accumulate, part, true, s);
+}
+
+cudaError_t linear_take_status(unsigned int* status) {
+  unsigned int v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_status, sizeof(v));
+  if (e != cudaSuccess) return e;
+  if (v != 0) e = cudaMemcpyToSymbol(g_status, &zero, sizeof(zero));
+  *status = v;
+  return e;
+}
+
+}  // namespace qffn
