@@ -147,9 +147,20 @@ def _buf(fn, device, name, t, size, n):
     return t.data_ptr()
 
 
-def _current_device():
+_torch = None                # imported on first use: the raw-address calls do not need it
+_has_gpu = False
+
+
+def _load_torch():
+    global _torch, _has_gpu
     import torch
-    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+    _torch, _has_gpu = torch, torch.cuda.is_available()
+
+
+def _current_device():
+    if _torch is None:
+        _load_torch()
+    return _torch._C._cuda_getDevice() if _has_gpu else -1
 
 
 def _workspace(fn, device, workspace, workspace_bytes):
@@ -161,10 +172,16 @@ def _workspace(fn, device, workspace, workspace_bytes):
     return _buf(fn, device, "workspace", workspace, workspace.element_size(), 1), nbytes
 
 
+def _current_stream():
+    if _torch is None:
+        _load_torch()
+    return _torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without the Stream object (2.8 us -> 0.1 us a call)
+        return _torch._C._cuda_getCurrentRawStream(_current_device()) if _has_gpu else _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

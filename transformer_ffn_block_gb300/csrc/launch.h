@@ -141,6 +141,13 @@ cudaError_t launch_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int
 cudaError_t launch_gated_backward(uint16_t* dx, uint16_t* dw1, const uint16_t* dh, const uint16_t* x,
                                   const uint16_t* w1, int act, int64_t M, int64_t C, int64_t H, bool accumulate,
                                   uint8_t* ws, cudaStream_t s);
+// The forms for few rows (skinny.cu), which launch_linear*, launch_gated take where skinny_rows(M).
+bool skinny_rows(int64_t M);
+cudaError_t launch_skinny(uint16_t* out, uint16_t* z, const void* x, const float* x_scale, const void* w,
+                          const float* w_scale, const uint16_t* bias, const uint16_t* res, int act, int64_t M,
+                          int64_t N, int64_t K, bool fp8, cudaStream_t s);
+cudaError_t launch_skinny_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int act, int64_t M, int64_t C,
+                                int64_t H, cudaStream_t s);
 // Reads and clears the linear kernels' device status word of the current device.
 cudaError_t linear_take_status(unsigned int* status);
 

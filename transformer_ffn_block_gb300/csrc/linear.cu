@@ -921,9 +921,11 @@ void gated_bwd_offsets(int64_t M, int64_t C, int64_t H, size_t off[3]) {
 }  // namespace
 
 size_t linear_workspace(int64_t M, int64_t N, int64_t K, bool fp8) {
-  return plan_bytes(make_plan(M, N, K, fp8 ? OP_E4M3 : OP_BF16), N);
+  return skinny_rows(M) ? 0 : plan_bytes(make_plan(M, N, K, fp8 ? OP_E4M3 : OP_BF16), N);
 }
-size_t gated_workspace(int64_t M, int64_t C, int64_t H) { return plan_bytes(make_plan(M, 2 * H, C, OP_BF16), 2 * H); }
+size_t gated_workspace(int64_t M, int64_t C, int64_t H) {
+  return skinny_rows(M) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16), 2 * H);
+}
 size_t linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
   size_t off[4];
   linear_bwd_offsets(M, N, K, off);
@@ -947,6 +949,7 @@ size_t gated_backward_workspace(int64_t M, int64_t C, int64_t H) {
 cudaError_t launch_linear(uint16_t* out, uint16_t* z, const uint16_t* x, const uint16_t* w, const uint16_t* bias,
                           const uint16_t* res, int act, int64_t M, int64_t N, int64_t K, float* ws, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
+  if (skinny_rows(M)) return launch_skinny(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, false, s);
   QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_LINEAR, ACT, false, false>(out, z, x, nullptr, w, nullptr, bias, res, M, N,
                                                                         K, ws, false, s)));
 }
@@ -955,6 +958,7 @@ cudaError_t launch_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, cons
                               const float* w_scale, const uint16_t* bias, const uint16_t* res, int act, int64_t M,
                               int64_t N, int64_t K, float* ws, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
+  if (skinny_rows(M)) return launch_skinny(out, z, x, x_scale, w, w_scale, bias, res, act, M, N, K, true, s);
   QFFN_ACT_SWITCH(act, (product<OP_E4M3, EPI_LINEAR, ACT, false, false>(out, z, x, x_scale, w, w_scale, bias, res, M, N,
                                                                         K, ws, false, s)));
 }
@@ -962,6 +966,7 @@ cudaError_t launch_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, cons
 cudaError_t launch_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int act, int64_t M, int64_t C, int64_t H,
                          float* ws, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
+  if (skinny_rows(M)) return launch_skinny_gated(h, x, w1, act, M, C, H, s);
   QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_GATED, ACT, false, false>(h, nullptr, x, nullptr, w1, nullptr, nullptr,
                                                                        nullptr, M, H, C, ws, false, s)));
 }
