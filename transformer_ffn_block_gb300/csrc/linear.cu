@@ -19,7 +19,7 @@
 // tcgen05.mma.cta_group::2 (M = 256, N = 256) chain per tile; CTA r of a pair
 // stages rows [128 r, 128 r + 128) of A and of the tile's 256 weight rows,
 // 256 bytes of K per stage and row, three stages.  One warp loads (TMA,
-// 128-byte swizzle), one thread of the leader issues the MMAs, four warps per
+// 128-byte swizzle), one thread of the leader issues the MMAs, eight warps per
 // CTA run the epilogue out of one of two TMEM accumulators while the next tile
 // accumulates in the other.  Per SM and byte of K this loads 16 + 16 KB per
 // 128 x 256 outputs; a bf16 MMA takes twice the cycles of an E4M3 one over the
@@ -48,11 +48,12 @@ constexpr int STAGES = 3;
 constexpr int OP_BYTES = KBOX * BOX_BYTES; // one operand's share of a stage
 constexpr int STAGE_BYTES = 2 * OP_BYTES;
 constexpr int STEPS = 8;                   // MMAs per stage (32 bytes of K each)
-constexpr int NUM_THREADS = 192;
+constexpr int EPI_WARPS = 8;
+constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 2 * BN;
-constexpr int NUM_BARS = 2 * STAGES + 5 + 8;
-constexpr int STAGE_BOX_BYTES = 32 * 128;  // epilogue staging box: 32 rows x 128 bytes
-constexpr int STAGING_BYTES = 4 * 2 * STAGE_BOX_BYTES;
+constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * EPI_WARPS;
+constexpr int STAGE_BOX_BYTES = 32 * 64;   // epilogue staging box: 32 rows x 64 bytes
+constexpr int STAGING_BYTES = EPI_WARPS * 2 * STAGE_BOX_BYTES;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 + NUM_BARS * 8 + 16;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
 constexpr int GROUP_M = 8;
@@ -184,13 +185,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // full[s] (leader): both CTAs' loads of stage s landed; empty[s]: the MMAs
   // reading stage s are done; tfull[a]: accumulator a is complete; tempty[a]
   // (leader): both CTAs' epilogue warps have read it; drain: all MMAs done;
-  // ld[q][b]: the TMA load into staging box b of epilogue warp q has landed
+  // ld[w][b]: the TMA load into staging box b of epilogue warp w has landed
   auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
   auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(STAGES + s); };
   auto tfull_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * STAGES + a); };
   auto tempty_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * STAGES + 2 + a); };
   const uint32_t drain_bar = bar0 + 8u * uint32_t(2 * STAGES + 4);
-  auto ld_bar = [&](int q, int b) { return bar0 + 8u * uint32_t(2 * STAGES + 5 + 2 * q + b); };
+  auto ld_bar = [&](int w, int b) { return bar0 + 8u * uint32_t(2 * STAGES + 5 + 2 * w + b); };
 
   constexpr bool GATED = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -204,12 +205,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
-      mbar_init(tempty_bar(a), 8);
+      mbar_init(tempty_bar(a), 2 * EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
-    for (int q = 0; q < 4; ++q) {
-      mbar_init(ld_bar(q, 0), 1);
-      mbar_init(ld_bar(q, 1), 1);
+    for (int w = 0; w < EPI_WARPS; ++w) {
+      mbar_init(ld_bar(w, 0), 1);
+      mbar_init(ld_bar(w, 1), 1);
     }
     *abort_flag = 0;
     mbar_init_fence();
@@ -320,17 +321,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
   } else {
     // -------------------------------------------------------------- epilogue
-    const int q = warp & 3;                  // TMEM lane quarter: rows 32 q .. 32 q + 31 of the CTA's 128
+    // Eight warps: two per TMEM lane quarter q (rows 32 q .. 32 q + 31 of the
+    // CTA's 128), which take the unit's groups of 32 output columns in turn.
+    const int q = warp & 3;
+    const int wg = (warp - 2) >> 2;          // 0: even groups, 1: odd groups
+    const int ew = q * 2 + wg;               // epilogue warp index of the staging boxes and barriers
     const float scale = args.a_scale != nullptr ? args.a_scale[0] * args.w_scale[0] : 1.0f;
-    uint8_t* const box0 = sStaging + (q * 2) * STAGE_BOX_BYTES;
+    uint8_t* const box0 = sStaging + ew * 2 * STAGE_BOX_BYTES;
     auto box = [&](int b) { return box0 + b * STAGE_BOX_BYTES; };
-    const uint32_t lane_off = uint32_t(lane) * 128u;
-    auto chunk_off = [&](int chunk) { return lane_off + (uint32_t(chunk ^ (lane & 7)) << 4); };
-    // Two ways to use the two staging boxes (32 rows x 64 bf16 columns):
+    // 16-byte chunk c of this lane's 64-byte row in a 64-byte-swizzled box
+    auto chunk_off = [&](int c) { return uint32_t(lane) * 64u + (uint32_t(c ^ ((lane >> 1) & 3)) << 4); };
+    // Two ways to use the warp's two staging boxes (32 rows x 32 bf16 columns):
     //  alternating: successive groups go out of the two boxes in turn; with an
-    //    input tensor (an even number of groups per unit, the first in box 0)
-    //    a box is filled by a TMA load first, the next group's load in flight
-    //    while a group is summed, and the result replaces it in place
+    //    input tensor (an even number of groups per warp and unit, the first in
+    //    box 0) a box is filled by a TMA load first, the next group's load in
+    //    flight while a group is summed, and the result replaces it in place
     //  paired (two outputs): box 0 holds the input and then the first output,
     //    box 1 the second output
     const bool paired = EPI == EPI_GATED_BWD || (EPI == EPI_LINEAR && args.save_z != 0);
@@ -338,16 +343,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t ld_par = 0u;                    // bit b: parity of the next load into box b
     uint32_t ld_pending = 0u;                // lane 0, bit b: a load has been issued and not waited for
     int flip = 0;
-    auto first_col = [&](const Unit& u) {    // output column of the unit's first group
+    auto first_col = [&](const Unit& u) {    // output column of the unit's group 0
       return GATED ? u.nb * 128 + (u.half < 0 ? 0 : u.half * 64) : u.nb * BN + (u.half < 0 ? 0 : u.half * 128);
     };
     auto first_row = [&](const Unit& u) { return u.mb * (2 * BM) + int(rank) * BM + q * 32; };
     auto load_in = [&](const Unit& u, int g, int b) {   // lane 0
-      mbar_expect_tx(ld_bar(q, b), STAGE_BOX_BYTES);
-      tma_load_2d(smem_u32(box(b)), &tmI, ld_bar(q, b), first_col(u) + g * 64, first_row(u));
+      mbar_expect_tx(ld_bar(ew, b), STAGE_BOX_BYTES);
+      tma_load_2d(smem_u32(box(b)), &tmI, ld_bar(ew, b), first_col(u) + g * 32, first_row(u));
       ld_pending |= 1u << b;
     };
-    if (has_in && lane == 0 && pair < args.num_units) load_in(unit_coords<EPI>(pair, args), 0, 0);
+    if (has_in && lane == 0 && pair < args.num_units) load_in(unit_coords<EPI>(pair, args), wg, 0);
     int local = 0;
     for (int un = pair; un < args.num_units; un += num_pairs, ++local) {
       const int acc = local & 1;
@@ -358,157 +363,145 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int row0 = first_row(u);
       const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * BN);
       const int acc_cols = u.half < 0 ? BN : BN / 2;
-      if (EPI == EPI_PARTIAL) {
-        // fp32 boxes of 32 rows x 32 columns, rows padded per part of K
-#pragma unroll 1
-        for (int c0 = 0; c0 < BN; c0 += 32) {
-          uint32_t v[32];
-          tmem_ld32(tbase + uint32_t(c0), v);
-          uint8_t* b = box((c0 >> 5) & 1);
-          if (lane == 0) bulk_wait_read_1();
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(b + chunk_off(k)) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          const int x = u.nb * BN + c0;
-          if (lane == 0) {
-            if (row0 < args.M && x < args.N) tma_store_2d(&tmO, smem_u32(b), x, u.sp * args.m_pad + row0);
-            bulk_commit();
-          }
-        }
-      } else {
-        const int groups = GATED ? acc_cols / 128 : acc_cols / 64;
-        bool ok = true;
-        for (int g = 0; g < groups; ++g) {
-          const int b = paired ? 0 : flip;
-          flip ^= 1;
-          if (has_in) {
-            if (!paired && g + 1 < groups) {
-              if (lane == 0) {
-                bulk_wait_read_0();          // the store that last read the other box is done
-                load_in(u, g + 1, b ^ 1);
-              }
-              __syncwarp();
-            }
-            if (!mbar_wait(ld_bar(q, b), (ld_par >> b) & 1u, abort_flag)) { ok = false; break; }
-            ld_par ^= 1u << b;
-            ld_pending &= ~(1u << b);
-          } else {
+      // groups of 32 output columns (partial sums: 32 fp32 columns, in both boxes)
+      const int groups = GATED ? acc_cols / 64 : acc_cols / 32;
+      bool ok = true;
+      for (int g = wg; g < groups; g += 2) {
+        const int b = paired || EPI == EPI_PARTIAL ? 0 : flip;
+        flip ^= 1;
+        if (has_in) {
+          if (!paired && g + 2 < groups) {
             if (lane == 0) {
-              if (paired) bulk_wait_read_0();
-              else bulk_wait_read_1();
+              bulk_wait_read_0();            // the store that last read the other box is done
+              load_in(u, g + 2, b ^ 1);
             }
             __syncwarp();
           }
-          const int col0 = first_col(u) + g * 64;
-          if (!GATED) {
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              const int col = col0 + h * 32;
-              uint4 bias[4];
-              if (args.bias != nullptr) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  bias[k] = col + 8 * k < args.N ? ld16_ro(args.bias + col + 8 * k) : make_uint4(0, 0, 0, 0);
-              }
-              uint32_t v[32];
-              tmem_ld32(tbase + uint32_t(g * 64 + h * 32), v);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t off = chunk_off(h * 4 + k);
-                float z[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = __uint_as_float(v[8 * k + j]);
-                if (OP == OP_E4M3) {
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) z[j] *= scale;
-                }
-                if (args.bias != nullptr) {
-                  const uint32_t bw[4] = {bias[k].x, bias[k].y, bias[k].z, bias[k].w};
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    z[2 * j] += bf16_lo(bw[j]);
-                    z[2 * j + 1] += bf16_hi(bw[j]);
-                  }
-                }
-                if (args.save_z)
-                  *reinterpret_cast<uint4*>(box(1) + off) =
-                      make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
-                                 pack_bf16x2(z[6], z[7]));
-#pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = act_f32<ACT>(z[j]);
-                if (args.has_in) {
-                  const uint4 o4 = *reinterpret_cast<const uint4*>(box(b) + off);
-                  const uint32_t ow[4] = {o4.x, o4.y, o4.z, o4.w};
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    z[2 * j] += bf16_lo(ow[j]);
-                    z[2 * j + 1] += bf16_hi(ow[j]);
-                  }
-                }
-                *reinterpret_cast<uint4*>(box(b) + off) =
-                    make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
-                               pack_bf16x2(z[6], z[7]));
-              }
-            }
-          } else {
-            const int up_off = acc_cols / 2;  // accumulator column of u
-#pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
-              const uint32_t c = uint32_t(g * 64 + h * 16);
-              uint32_t gv[16], uv[16];
-              tmem_ld16x2_issue(tbase + c, tbase + uint32_t(up_off) + c, gv, uv);
-              tmem_wait_ld16(gv, uv);
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint32_t off = chunk_off(h * 2 + k);
-                uint32_t p[4], p2[4];
-                uint4 d4 = make_uint4(0, 0, 0, 0);
-                if (EPI == EPI_GATED_BWD) d4 = *reinterpret_cast<const uint4*>(box0 + off);
-                const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float g0 = __uint_as_float(gv[8 * k + 2 * j]), g1 = __uint_as_float(gv[8 * k + 2 * j + 1]);
-                  const float u0 = __uint_as_float(uv[8 * k + 2 * j]), u1 = __uint_as_float(uv[8 * k + 2 * j + 1]);
-                  if (EPI == EPI_GATED) {
-                    p[j] = pack_bf16x2(act_f32<ACT>(g0) * u0, act_f32<ACT>(g1) * u1);
-                  } else {
-                    float f0, df0, f1, df1;
-                    act_grad_f32<ACT>(g0, f0, df0);
-                    act_grad_f32<ACT>(g1, f1, df1);
-                    const float d0 = bf16_lo(dw[j]), d1 = bf16_hi(dw[j]);
-                    p[j] = pack_bf16x2(d0 * u0 * df0, d1 * u1 * df1);
-                    p2[j] = pack_bf16x2(d0 * f0, d1 * f1);
-                  }
-                }
-                *reinterpret_cast<uint4*>(box(b) + off) = make_uint4(p[0], p[1], p[2], p[3]);
-                if (EPI == EPI_GATED_BWD)
-                  *reinterpret_cast<uint4*>(box(1) + off) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-              }
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
+          if (!mbar_wait(ld_bar(ew, b), (ld_par >> b) & 1u, abort_flag)) { ok = false; break; }
+          ld_par ^= 1u << b;
+          ld_pending &= ~(1u << b);
+        } else {
           if (lane == 0) {
-            // rows beyond M and columns beyond N are clipped by the tensor maps
-            if (row0 < args.M && col0 < args.N) {
-              tma_store_2d(&tmO, smem_u32(box(b)), col0, row0);
-              if (paired) tma_store_2d(&tmZ, smem_u32(box(1)), col0, row0);
-            }
-            bulk_commit();
-            if (has_in && (paired || g + 1 == groups)) {
-              // the next load into box 0: of this tile (paired) or of the next unit
-              bulk_wait_read_0();
-              if (g + 1 < groups) load_in(u, g + 1, 0);
-              else if (un + num_pairs < args.num_units) load_in(unit_coords<EPI>(un + num_pairs, args), 0, 0);
-            }
+            if (paired || EPI == EPI_PARTIAL) bulk_wait_read_0();
+            else bulk_wait_read_1();
           }
           __syncwarp();
         }
-        if (!ok) break;
+        const int col0 = first_col(u) + g * 32;
+        if (EPI == EPI_PARTIAL) {
+          uint32_t v[32];
+          tmem_ld32(tbase + uint32_t(g * 32), v);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(box(k >> 2) + chunk_off(k & 3)) =
+                make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        } else if (!GATED) {
+          uint4 bias[4];
+          if (args.bias != nullptr) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              bias[k] = col0 + 8 * k < args.N ? ld16_ro(args.bias + col0 + 8 * k) : make_uint4(0, 0, 0, 0);
+          }
+          uint32_t v[32];
+          tmem_ld32(tbase + uint32_t(g * 32), v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t off = chunk_off(k);
+            float z[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[j] = __uint_as_float(v[8 * k + j]);
+            if (OP == OP_E4M3) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) z[j] *= scale;
+            }
+            if (args.bias != nullptr) {
+              const uint32_t bw[4] = {bias[k].x, bias[k].y, bias[k].z, bias[k].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                z[2 * j] += bf16_lo(bw[j]);
+                z[2 * j + 1] += bf16_hi(bw[j]);
+              }
+            }
+            if (args.save_z)
+              *reinterpret_cast<uint4*>(box(1) + off) =
+                  make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
+                             pack_bf16x2(z[6], z[7]));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[j] = act_f32<ACT>(z[j]);
+            if (args.has_in) {
+              const uint4 o4 = *reinterpret_cast<const uint4*>(box(b) + off);
+              const uint32_t ow[4] = {o4.x, o4.y, o4.z, o4.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                z[2 * j] += bf16_lo(ow[j]);
+                z[2 * j + 1] += bf16_hi(ow[j]);
+              }
+            }
+            *reinterpret_cast<uint4*>(box(b) + off) =
+                make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
+                           pack_bf16x2(z[6], z[7]));
+          }
+        } else {
+          const int up_off = acc_cols / 2;   // accumulator column of u
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t c = uint32_t(g * 32 + h * 16);
+            uint32_t gv[16], uv[16];
+            tmem_ld16x2_issue(tbase + c, tbase + uint32_t(up_off) + c, gv, uv);
+            tmem_wait_ld16(gv, uv);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t off = chunk_off(h * 2 + k);
+              uint32_t p[4], p2[4];
+              uint4 d4 = make_uint4(0, 0, 0, 0);
+              if (EPI == EPI_GATED_BWD) d4 = *reinterpret_cast<const uint4*>(box0 + off);
+              const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float g0 = __uint_as_float(gv[8 * k + 2 * j]), g1 = __uint_as_float(gv[8 * k + 2 * j + 1]);
+                const float u0 = __uint_as_float(uv[8 * k + 2 * j]), u1 = __uint_as_float(uv[8 * k + 2 * j + 1]);
+                if (EPI == EPI_GATED) {
+                  p[j] = pack_bf16x2(act_f32<ACT>(g0) * u0, act_f32<ACT>(g1) * u1);
+                } else {
+                  float f0, df0, f1, df1;
+                  act_grad_f32<ACT>(g0, f0, df0);
+                  act_grad_f32<ACT>(g1, f1, df1);
+                  const float d0 = bf16_lo(dw[j]), d1 = bf16_hi(dw[j]);
+                  p[j] = pack_bf16x2(d0 * u0 * df0, d1 * u1 * df1);
+                  p2[j] = pack_bf16x2(d0 * f0, d1 * f1);
+                }
+              }
+              *reinterpret_cast<uint4*>(box(b) + off) = make_uint4(p[0], p[1], p[2], p[3]);
+              if (EPI == EPI_GATED_BWD)
+                *reinterpret_cast<uint4*>(box(1) + off) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          // rows beyond M and columns beyond N are clipped by the tensor maps
+          if (row0 < args.M && col0 < args.N) {
+            if (EPI == EPI_PARTIAL) {
+              // rows are padded per part of K to whole boxes
+              tma_store_2d(&tmO, smem_u32(box(0)), col0, u.sp * args.m_pad + row0);
+              if (col0 + 16 < args.N) tma_store_2d(&tmO, smem_u32(box(1)), col0 + 16, u.sp * args.m_pad + row0);
+            } else {
+              tma_store_2d(&tmO, smem_u32(box(b)), col0, row0);
+              if (paired) tma_store_2d(&tmZ, smem_u32(box(1)), col0, row0);
+            }
+          }
+          bulk_commit();
+          if (has_in && (paired || g + 2 >= groups)) {
+            // the next load into box 0: of this unit (paired) or of the next one
+            bulk_wait_read_0();
+            if (g + 2 < groups) load_in(u, g + 2, 0);
+            else if (un + num_pairs < args.num_units) load_in(unit_coords<EPI>(un + num_pairs, args), wg, 0);
+          }
+        }
+        __syncwarp();
       }
+      if (!ok) break;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(map_to_rank(tempty_bar(acc), 0));
@@ -517,7 +510,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (lane == 0) {
       bulk_wait_all();
       for (int b = 0; b < 2; ++b)
-        if ((ld_pending >> b) & 1u) mbar_wait(ld_bar(q, b), (ld_par >> b) & 1u, abort_flag, false, kDrainLimitNs);
+        if ((ld_pending >> b) & 1u) mbar_wait(ld_bar(ew, b), (ld_par >> b) & 1u, abort_flag, false, kDrainLimitNs);
     }
   }
 
@@ -682,28 +675,30 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // Tensor map of [rows, cols] (cols contiguous, rows `ld` elements apart) with
-// boxes of box_rows rows x 128 bytes, 128-byte swizzle; zeros outside.
+// boxes of box_rows rows x box_bytes (64 or 128) in the swizzle of that width;
+// zeros outside.
 bool make_map(CUtensorMap* map, CUtensorMapDataType type, int elem, const void* ptr, int64_t rows, int64_t cols,
-              int64_t ld, int box_rows, CUtensorMapL2promotion promo) {
+              int64_t ld, int box_rows, int box_bytes, CUtensorMapL2promotion promo) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
   cuuint64_t strides[1] = {cuuint64_t(ld) * cuuint64_t(elem)};
-  cuuint32_t box[2] = {cuuint32_t(128 / elem), cuuint32_t(box_rows)};
+  cuuint32_t box[2] = {cuuint32_t(box_bytes / elem), cuuint32_t(box_rows)};
   cuuint32_t estr[2] = {1u, 1u};
   return fn(map, type, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, promo, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, promo,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // An MMA operand: [rows, k] K-major or, `mn`, [k, rows] as it lies in memory.
 template <int OP>
 bool operand_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t k, bool mn, int box_rows = 128) {
   const CUtensorMapDataType t = OP == OP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  return mn ? make_map(map, t, OP == OP_BF16 ? 2 : 1, ptr, k, rows, rows, box_rows, CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
-            : make_map(map, t, OP == OP_BF16 ? 2 : 1, ptr, rows, k, k, box_rows, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  return mn ? make_map(map, t, OP == OP_BF16 ? 2 : 1, ptr, k, rows, rows, box_rows, 128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
+            : make_map(map, t, OP == OP_BF16 ? 2 : 1, ptr, rows, k, k, box_rows, 128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
-// A bf16 tensor the epilogue stores or loads in boxes of 32 rows x 64 columns.
+// A bf16 tensor the epilogue stores or loads in boxes of 32 rows x 32 columns.
 bool epi_map(CUtensorMap* map, const uint16_t* ptr, int64_t rows, int64_t cols, int64_t ld) {
-  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, rows, cols, ld, 32, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, rows, cols, ld, 32, 64, CU_TENSOR_MAP_L2_PROMOTION_NONE);
 }
 
 // 2-CTA clusters of a form that fit on the device at once (cached per device).
@@ -845,7 +840,7 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
   cudaError_t e;
   if (p.splits > 1) {
     if (!make_map(&m.o, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, partial, p.splits * p.m_pad, brows, brows, 32,
-                  CU_TENSOR_MAP_L2_PROMOTION_NONE))
+                  64, CU_TENSOR_MAP_L2_PROMOTION_NONE))
       return cudaErrorInvalidValue;
     m.z = m.i = m.o;
     a.N = int(brows);
