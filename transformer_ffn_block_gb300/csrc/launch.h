@@ -117,6 +117,8 @@ cudaError_t launch_norm_backward(uint16_t* dx, float* dgain, float* dshift, floa
                                  const uint16_t* dres, const uint16_t* r, const float* mean, const float* rstd,
                                  const uint16_t* gain, int64_t N, int C, bool centred, bool accumulate,
                                  float* partial, cudaStream_t s);
+// Reads and clears the norm kernels' device status word of the current device.
+cudaError_t norm_take_status(unsigned int* status);
 // out0 [cols0], out1 [cols - cols0] (+)= the sum of the rows of partial [parts, cols],
 // in a fixed order; either output may be NULL.  A programmatic dependent launch.
 cudaError_t launch_column_sum(float* out0, float* out1, const float* partial, int parts, int64_t cols0,
