@@ -16,6 +16,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "pipeline.cuh"
+#include "umma.cuh"
 
 namespace qffn {
 namespace {
@@ -39,100 +40,135 @@ QFFN_DEVI void team_sum2(float& a, float& b, float* red) {
   }
 }
 
-QFFN_DEVI void unpack8(uint4 v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    f[2 * j] = bf16_lo(w[j]);
-    f[2 * j + 1] = bf16_hi(w[j]);
-  }
+// Eight bf16 as four float pairs, and back.
+struct F8 {
+  uint64_t p[4];
+};
+QFFN_DEVI F8 unpack8(uint4 v) { return F8{{bf16x2_to_f2(v.x), bf16x2_to_f2(v.y), bf16x2_to_f2(v.z), bf16x2_to_f2(v.w)}}; }
+QFFN_DEVI uint32_t pack2(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return pack_bf16x2(lo, hi);
 }
-QFFN_DEVI uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+QFFN_DEVI uint4 pack8(const F8& f) { return make_uint4(pack2(f.p[0]), pack2(f.p[1]), pack2(f.p[2]), pack2(f.p[3])); }
+QFFN_DEVI uint64_t f2_dup(float v) { return f2_pack(v, v); }
+QFFN_DEVI float f2_sum(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return lo + hi;
 }
-QFFN_DEVI float absmax8(uint4 v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float m = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
-  return m;
+// Running max of |v| over the bf16 pairs of a chunk.
+QFFN_DEVI uint32_t absmax8(uint32_t m, uint4 v) {
+  return bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(m, v.x), v.y), v.z), v.w);
+}
+QFFN_DEVI void record_absmax(float* stats, uint32_t m) {
+  const float v = warp_max(fmaxf(bf16_lo(m), bf16_hi(m)));
+  if ((threadIdx.x & 31) == 0) atomic_max_nonneg(stats, v);
 }
 
+__device__ unsigned int g_status;
+constexpr unsigned long long kWaitLimitNs = 2000000000ull;
+constexpr unsigned long long kDrainLimitNs = 200000000ull;
+constexpr int kMaxStages = 8;
+
 // ------------------------------------------------------------------ layer norm forward
+struct LnFwd {
+  uint16_t* res_out;
+  uint16_t* y;
+  float* mean;
+  float* rstd;
+  float* stats;
+  const uint16_t* res_in;
+  const uint16_t* x;
+  const uint16_t* gain;
+  const uint16_t* shift;
+  float eps;
+  int64_t N;
+  int C;
+};
+
+// bf16 + bf16 in fp32, one rounding: the residual stream is kept in bf16.
+QFFN_DEVI uint4 add8(uint4 a, uint4 b) {
+  F8 x = unpack8(a);
+  const F8 z = unpack8(b);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x.p[j] = f2_add(x.p[j], z.p[j]);
+  return pack8(x);
+}
+QFFN_DEVI uint64_t sum8(const F8& f) { return f2_add(f2_add(f.p[0], f.p[1]), f2_add(f.p[2], f.p[3])); }
+// ss += (f - mean)^2 of a chunk
+QFFN_DEVI uint64_t squares8(const F8& f, uint64_t neg_mean, uint64_t ss) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t d = f2_add(f.p[j], neg_mean);
+    ss = f2_fma(d, d, ss);
+  }
+  return ss;
+}
+// (f - mean) * rstd * gain + shift
+QFFN_DEVI uint4 normed8(const F8& f, uint64_t neg_mean, uint64_t rstd, const F8& g, const F8& s) {
+  F8 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o.p[j] = f2_fma(f2_mul(f2_add(f.p[j], neg_mean), rstd), g.p[j], s.p[j]);
+  return pack8(o);
+}
+
 // One row per team of T threads; thread t owns the 16-byte chunks t, t+T, ...
+// Small teams with up to four chunks a thread for many rows: a dozen rows or
+// more of independent blocks per SM hide each other's loads and barriers
+// (16384 x 4096: see launch_layernorm for what that measured against
+// persistent blocks fed by bulk copies).  Larger teams for few rows, where a
+// call is a launch and one round of loads.
 template <int T, int V, int BLOCK>
-__global__ void __launch_bounds__(BLOCK) layernorm_kernel(uint16_t* res_out, uint16_t* y, float* mean_out,
-                                                          float* rstd_out, float* stats,
-                                                          const uint16_t* res_in, const uint16_t* x,
-                                                          const uint16_t* gain, const uint16_t* shift,
-                                                          float eps, int64_t N, int C) {
+__global__ void __launch_bounds__(BLOCK) layernorm_kernel(const LnFwd a) {
   __shared__ float red[2][64];
   const int t = threadIdx.x % T;
   const int64_t row = int64_t(blockIdx.x) * (BLOCK / T) + threadIdx.x / T;
-  const bool live = row < N;                 // a team of T > 32 is the block: always live
-  const int nchunk = C >> 3;
-  const size_t base = live ? size_t(row) * size_t(C) : 0;
+  const bool live = row < a.N;               // a team of T > 32 is the block: always live
+  const int nchunk = a.C >> 3;
+  const size_t base = live ? size_t(row) * size_t(a.C) : 0;
   uint4 rv[V];
-  float sum = 0.0f, unused = 0.0f;
+  uint64_t acc = 0ull;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = t + i * T;
     if (live && c < nchunk) {
-      uint4 r = ld16_once(x + base + size_t(c) * 8);
-      if (res_in != nullptr) {
-        const uint4 a = ld16_once(res_in + base + size_t(c) * 8);
-        // bf16 + bf16 in fp32, one rounding: the residual stream is kept in bf16
-        r.x = pack_bf16x2(bf16_lo(a.x) + bf16_lo(r.x), bf16_hi(a.x) + bf16_hi(r.x));
-        r.y = pack_bf16x2(bf16_lo(a.y) + bf16_lo(r.y), bf16_hi(a.y) + bf16_hi(r.y));
-        r.z = pack_bf16x2(bf16_lo(a.z) + bf16_lo(r.z), bf16_hi(a.z) + bf16_hi(r.z));
-        r.w = pack_bf16x2(bf16_lo(a.w) + bf16_lo(r.w), bf16_hi(a.w) + bf16_hi(r.w));
-        stg16(res_out + base + size_t(c) * 8, r);
+      rv[i] = ld16_once(a.x + base + size_t(c) * 8);
+      if (a.res_in != nullptr) {
+        rv[i] = add8(ld16_once(a.res_in + base + size_t(c) * 8), rv[i]);
+        stg16(a.res_out + base + size_t(c) * 8, rv[i]);
       }
-      rv[i] = r;
-      float f[8];
-      unpack8(r, f);
-      sum += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+      acc = f2_add(acc, sum8(unpack8(rv[i])));
     }
   }
+  float sum = f2_sum(acc), unused = 0.0f;
   team_sum2<T>(sum, unused, red[0]);
-  const float mean = sum / float(C);
-  float ss = 0.0f;
+  const float mean = sum / float(a.C);
+  const uint64_t neg_mean = f2_dup(-mean);
+  acc = 0ull;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (live && t + i * T < nchunk) {
-      float f[8];
-      unpack8(rv[i], f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(f[j] - mean, f[j] - mean, ss);
-    }
-  }
+  for (int i = 0; i < V; ++i)
+    if (live && t + i * T < nchunk) acc = squares8(unpack8(rv[i]), neg_mean, acc);
+  float ss = f2_sum(acc);
   team_sum2<T>(ss, unused, red[1]);
-  const float rstd = 1.0f / sqrtf(ss / float(C) + eps);
+  const float rstd = 1.0f / sqrtf(ss / float(a.C) + a.eps);
   if (live && t == 0) {
-    mean_out[row] = mean;
-    rstd_out[row] = rstd;
+    a.mean[row] = mean;
+    a.rstd[row] = rstd;
   }
-  float amax = 0.0f;
+  uint32_t amax = 0u;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = t + i * T;
     if (live && c < nchunk) {
-      float f[8], g[8], s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      unpack8(rv[i], f);
-      unpack8(ld16_ro(gain + size_t(c) * 8), g);
-      if (shift != nullptr) unpack8(ld16_ro(shift + size_t(c) * 8), s);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = fmaf((f[j] - mean) * rstd, g[j], s[j]);
-      const uint4 o = pack8(f);
-      stg16(y + base + size_t(c) * 8, o);
-      amax = fmaxf(amax, absmax8(o));
+      F8 s{{0ull, 0ull, 0ull, 0ull}};
+      if (a.shift != nullptr) s = unpack8(ld16_ro(a.shift + size_t(c) * 8));
+      const uint4 o = normed8(unpack8(rv[i]), neg_mean, f2_dup(rstd), unpack8(ld16_ro(a.gain + size_t(c) * 8)), s);
+      stg16(a.y + base + size_t(c) * 8, o);
+      if (a.stats != nullptr) amax = absmax8(amax, o);
     }
   }
-  if (stats != nullptr) {
-    amax = warp_max(amax);
-    if ((threadIdx.x & 31) == 0) atomic_max_nonneg(stats, amax);
-  }
+  if (a.stats != nullptr) record_absmax(a.stats, amax);
 }
 
 // ------------------------------------------------------------------ norm backward
@@ -142,39 +178,35 @@ __global__ void __launch_bounds__(BLOCK) layernorm_kernel(uint16_t* res_out, uin
 // its partial row of dgain (and dshift).  column_sum_kernel adds the blocks'
 // partial rows in a fixed order: no atomics, the same bits each run.
 
-// dx of one 16-byte chunk, from the row's c1 = mean(w xhat) and c2 = mean(w).
+// dx of one 16-byte chunk: e + rs w + k1 xhat + k2 with k1 = -rs c1, k2 = -rs c2.
 template <bool CENTRED>
-QFFN_DEVI uint4 norm_dx8(uint4 dv, uint4 rv, uint4 gv, uint4 ev, float mu, float rs, float c1, float c2) {
-  float d[8], x[8], g[8], e[8];
-  unpack8(dv, d);
-  unpack8(rv, x);
-  unpack8(gv, g);
-  unpack8(ev, e);
+QFFN_DEVI uint4 norm_dx8(uint4 dv, uint4 rv, uint4 gv, uint4 ev, uint64_t rs, uint64_t neg_mu_rs, uint64_t k1,
+                         uint64_t k2) {
+  const F8 d = unpack8(dv), x = unpack8(rv), g = unpack8(gv);
+  F8 e = unpack8(ev);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float xh = CENTRED ? (x[j] - mu) * rs : x[j] * rs;
-    float v = fmaf(-xh, c1, d[j] * g[j]);
-    if (CENTRED) v -= c2;
-    e[j] = fmaf(v, rs, e[j]);
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t xh = CENTRED ? f2_fma(x.p[j], rs, neg_mu_rs) : f2_mul(x.p[j], rs);
+    // the sum of the three gradient terms first, dres last
+    uint64_t v = CENTRED ? f2_fma(xh, k1, k2) : f2_mul(xh, k1);
+    v = f2_fma(f2_mul(d.p[j], g.p[j]), rs, v);
+    e.p[j] = f2_add(e.p[j], v);
   }
   return pack8(e);
 }
 // The chunk's terms of the row sums (s1 += w xhat, s2 += w) and column sums.
 template <bool CENTRED>
-QFFN_DEVI void norm_sums8(uint4 dv, uint4 rv, uint4 gv, float mu, float rs, float& s1, float& s2, float (&dg)[8],
-                          float (&ds)[8]) {
-  float d[8], x[8], g[8];
-  unpack8(dv, d);
-  unpack8(rv, x);
-  unpack8(gv, g);
+QFFN_DEVI void norm_sums8(uint4 dv, uint4 rv, uint4 gv, uint64_t rs, uint64_t neg_mu_rs, uint64_t& s1, uint64_t& s2,
+                          uint64_t (&dg)[4], uint64_t (&ds)[4]) {
+  const F8 d = unpack8(dv), x = unpack8(rv), g = unpack8(gv);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float xh = CENTRED ? (x[j] - mu) * rs : x[j] * rs;
-    const float w = d[j] * g[j];
-    s1 = fmaf(w, xh, s1);
-    if (CENTRED) s2 += w;
-    dg[j] = fmaf(d[j], xh, dg[j]);
-    if (CENTRED) ds[j] += d[j];
+  for (int j = 0; j < 4; ++j) {
+    const uint64_t xh = CENTRED ? f2_fma(x.p[j], rs, neg_mu_rs) : f2_mul(x.p[j], rs);
+    const uint64_t w = f2_mul(d.p[j], g.p[j]);
+    s1 = f2_fma(w, xh, s1);
+    if (CENTRED) s2 = f2_add(s2, w);
+    dg[j] = f2_fma(d.p[j], xh, dg[j]);
+    if (CENTRED) ds[j] = f2_add(ds[j], d.p[j]);
   }
 }
 
@@ -197,21 +229,21 @@ struct NormBwd {
 template <bool CENTRED, int V>
 __global__ void __launch_bounds__(256) norm_backward_warp_kernel(const NormBwd a) {
   constexpr int TEAMS = 8;
-  __shared__ float comb[TEAMS * 32 * V * 8];
+  __shared__ __align__(8) float comb[TEAMS * 32 * V * 8];
   const int t = threadIdx.x & 31, team = threadIdx.x >> 5;
   const int nchunk = a.C >> 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   uint4 gv[V];
-  float dg[V][8], ds[V][8];
+  uint64_t dg[V][4], ds[V][4];               // pairs of columns
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = t + i * 32;
     gv[i] = c < nchunk ? ld16_ro(a.gain + size_t(c) * 8) : zero;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dg[i][j] = ds[i][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) dg[i][j] = ds[i][j] = 0ull;
   }
   const float inv_c = 1.0f / float(a.C);
-  float amax = 0.0f;
+  uint32_t amax = 0u;
   for (int64_t row = int64_t(blockIdx.x) * TEAMS + team; row < a.N; row += int64_t(gridDim.x) * TEAMS) {
     const size_t base = size_t(row) * size_t(a.C);
     uint4 dv[V], rv[V], ev[V];
@@ -226,26 +258,24 @@ __global__ void __launch_bounds__(256) norm_backward_warp_kernel(const NormBwd a
       }
     }
     const float mu = CENTRED ? a.mean[row] : 0.0f, rs = a.rstd[row];
-    float s1 = 0.0f, s2 = 0.0f;
+    const uint64_t rs2 = f2_dup(rs), nm2 = f2_dup(-mu * rs);
+    uint64_t p1 = 0ull, p2 = 0ull;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (t + i * 32 < nchunk) norm_sums8<CENTRED>(dv[i], rv[i], gv[i], mu, rs, s1, s2, dg[i], ds[i]);
-    s1 = warp_sum(s1);
-    s2 = warp_sum(s2);
+      if (t + i * 32 < nchunk) norm_sums8<CENTRED>(dv[i], rv[i], gv[i], rs2, nm2, p1, p2, dg[i], ds[i]);
+    const uint64_t k1 = f2_dup(-rs * (warp_sum(f2_sum(p1)) * inv_c));
+    const uint64_t k2 = f2_dup(-rs * (warp_sum(f2_sum(p2)) * inv_c));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = t + i * 32;
       if (c < nchunk) {
-        const uint4 o = norm_dx8<CENTRED>(dv[i], rv[i], gv[i], ev[i], mu, rs, s1 * inv_c, s2 * inv_c);
+        const uint4 o = norm_dx8<CENTRED>(dv[i], rv[i], gv[i], ev[i], rs2, nm2, k1, k2);
         stg16(a.dx + base + size_t(c) * 8, o);
-        amax = fmaxf(amax, absmax8(o));
+        if (a.stats != nullptr) amax = absmax8(amax, o);
       }
     }
   }
-  if (a.stats != nullptr) {
-    amax = warp_max(amax);
-    if (t == 0) atomic_max_nonneg(a.stats, amax);
-  }
+  if (a.stats != nullptr) record_absmax(a.stats, amax);
   float* prow = a.partial + size_t(blockIdx.x) * size_t(CENTRED ? 2 : 1) * size_t(a.C);
 #pragma unroll
   for (int k = 0; k < (CENTRED ? 2 : 1); ++k) {
@@ -254,7 +284,8 @@ __global__ void __launch_bounds__(256) norm_backward_warp_kernel(const NormBwd a
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) comb[((team * 32 + t) * V + i) * 8 + j] = k == 0 ? dg[i][j] : ds[i][j];
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint64_t*>(&comb[((team * 32 + t) * V + i) * 8 + 2 * j]) = k == 0 ? dg[i][j] : ds[i][j];
     __syncthreads();
     for (int idx = threadIdx.x; idx < a.C; idx += 256) {
       const int chunk = idx >> 3, j = idx & 7;
@@ -264,11 +295,6 @@ __global__ void __launch_bounds__(256) norm_backward_warp_kernel(const NormBwd a
     }
   }
 }
-
-__device__ unsigned int g_status;
-constexpr unsigned long long kWaitLimitNs = 2000000000ull;
-constexpr unsigned long long kDrainLimitNs = 200000000ull;
-constexpr int kMaxStages = 8;
 
 // Longer rows: the block is the team.  A row's three inputs come by bulk copy
 // into one stage of a shared-memory ring, `stages` rows deep, so the loads of
@@ -309,16 +335,16 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const NormBwd a) {
   if (t == 0)
     for (; fill < a.stages && next_load < a.N; ++fill, next_load += gridDim.x) load_row(next_load, fill);
   uint4 gv[V];
-  float dg[V][8], ds[V][8];
+  uint64_t dg[V][4], ds[V][4];               // pairs of columns
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = t + i * T;
     gv[i] = c < nchunk ? ld16_ro(a.gain + size_t(c) * 8) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dg[i][j] = ds[i][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) dg[i][j] = ds[i][j] = 0ull;
   }
   const float inv_c = 1.0f / float(a.C);
-  float amax = 0.0f;
+  uint32_t amax = 0u;
   int buf = 0, s = 0, refill = -1;
   uint32_t parity = 0;
   bool ok = true;
@@ -336,15 +362,17 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const NormBwd a) {
     // a wait that runs out raises the abort flag, which all threads see after the barrier below
     mbar_wait_bounded(smem_u32(&bars[s]), parity, abort_flag, &g_status, true, kWaitLimitNs);
     const uint8_t* st = ring + size_t(s) * stage_bytes;
-    float s1 = 0.0f, s2 = 0.0f;
+    const uint64_t rs2 = f2_dup(rs), nm2 = f2_dup(-mu * rs);
+    uint64_t p1 = 0ull, p2 = 0ull;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = t + i * T;
       if (c < nchunk)
         norm_sums8<CENTRED>(*reinterpret_cast<const uint4*>(st + c * 16),
-                            *reinterpret_cast<const uint4*>(st + row_bytes + c * 16), gv[i], mu, rs, s1, s2, dg[i],
+                            *reinterpret_cast<const uint4*>(st + row_bytes + c * 16), gv[i], rs2, nm2, p1, p2, dg[i],
                             ds[i]);
     }
+    float s1 = f2_sum(p1), s2 = f2_sum(p2);
     team_sum2<T>(s1, s2, red[buf]);
     buf ^= 1;                                     // the next row's sums use the other buffer
     if (*abort_flag) { ok = false; break; }
@@ -353,6 +381,7 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const NormBwd a) {
       next_load += gridDim.x;
     }
     refill = s;
+    const uint64_t k1 = f2_dup(-rs * (s1 * inv_c)), k2 = f2_dup(-rs * (s2 * inv_c));
     const size_t base = size_t(row) * size_t(a.C);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -361,10 +390,10 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const NormBwd a) {
         const uint4 ev = inputs == 3 ? *reinterpret_cast<const uint4*>(st + 2 * row_bytes + c * 16)
                                      : make_uint4(0, 0, 0, 0);
         const uint4 o = norm_dx8<CENTRED>(*reinterpret_cast<const uint4*>(st + c * 16),
-                                          *reinterpret_cast<const uint4*>(st + row_bytes + c * 16), gv[i], ev, mu, rs,
-                                          s1 * inv_c, s2 * inv_c);
+                                          *reinterpret_cast<const uint4*>(st + row_bytes + c * 16), gv[i], ev, rs2, nm2,
+                                          k1, k2);
         stg16(a.dx + base + size_t(c) * 8, o);
-        amax = fmaxf(amax, absmax8(o));
+        if (a.stats != nullptr) amax = absmax8(amax, o);
       }
     }
     if (++s == a.stages) {
@@ -381,10 +410,7 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const NormBwd a) {
       }
     return;
   }
-  if (a.stats != nullptr) {
-    amax = warp_max(amax);
-    if ((t & 31) == 0) atomic_max_nonneg(a.stats, amax);
-  }
+  if (a.stats != nullptr) record_absmax(a.stats, amax);
   float* prow = a.partial + size_t(blockIdx.x) * size_t(CENTRED ? 2 : 1) * size_t(a.C);
 #pragma unroll
   for (int k = 0; k < (CENTRED ? 2 : 1); ++k)
@@ -392,29 +418,40 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const NormBwd a) {
     for (int i = 0; i < V; ++i) {
       const int c = t + i * T;
       if (c < nchunk) {
-        float4* dst = reinterpret_cast<float4*>(prow + size_t(k) * a.C + size_t(c) * 8);
-        const float(&v)[8] = k == 0 ? dg[i] : ds[i];
-        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        ulonglong2* dst = reinterpret_cast<ulonglong2*>(prow + size_t(k) * a.C + size_t(c) * 8);
+        const uint64_t(&v)[4] = k == 0 ? dg[i] : ds[i];
+        dst[0] = make_ulonglong2(v[0], v[1]);
+        dst[1] = make_ulonglong2(v[2], v[3]);
       }
     }
 }
 
-// out[c] (+)= sum over p of partial[p][c], p in order within each of 8 strided
-// groups, the groups added in order.  32 columns per block.
-__global__ void __launch_bounds__(256) column_sum_kernel(float* out0, float* out1, const float* partial, int parts,
-                                                         int64_t cols0, int64_t cols, int accumulate) {
+// out[c] (+)= sum over p of partial[p][c]: 32 groups of parts, p in order within
+// each and eight loads in flight, the groups added in order.  32 columns per
+// block.
+__global__ void __launch_bounds__(1024) column_sum_kernel(float* out0, float* out1, const float* partial, int parts,
+                                                          int64_t cols0, int64_t cols, int accumulate) {
   pdl_wait();
-  __shared__ float s[8][33];
-  const int64_t c = int64_t(blockIdx.x) * 32 + (threadIdx.x & 31);
-  const int g = threadIdx.x >> 5;
+  __shared__ float s[32][33];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int64_t c = int64_t(blockIdx.x) * 32 + lane;
   float v = 0.0f;
-  if (c < cols)
-    for (int p = g; p < parts; p += 8) v += partial[size_t(p) * size_t(cols) + size_t(c)];
-  s[g][threadIdx.x & 31] = v;
+  if (c < cols) {
+    const float* col = partial + c;
+    int p = g;
+    for (; p + 7 * 32 < parts; p += 8 * 32) {
+      float t[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) t[k] = col[size_t(p + k * 32) * size_t(cols)];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v += t[k];
+    }
+    for (; p < parts; p += 32) v += col[size_t(p) * size_t(cols)];
+  }
+  s[g][lane] = v;
   __syncthreads();
   if (g == 0 && c < cols) {
-    for (int k = 1; k < 8; ++k) v += s[k][threadIdx.x];
+    for (int k = 1; k < 32; ++k) v += s[k][lane];
     // columns [0, cols0) go to out0, the rest to out1; either may be absent
     float* dst = c < cols0 ? out0 : out1;
     const int64_t i = c < cols0 ? c : c - cols0;
@@ -423,36 +460,42 @@ __global__ void __launch_bounds__(256) column_sum_kernel(float* out0, float* out
 }
 
 template <int T, int V, int BLOCK>
-cudaError_t run_layernorm(uint16_t* res_out, uint16_t* y, float* mean, float* rstd, float* stats,
-                          const uint16_t* res_in, const uint16_t* x, const uint16_t* gain,
-                          const uint16_t* shift, float eps, int64_t N, int C, cudaStream_t s) {
+cudaError_t run_layernorm(const LnFwd& a, cudaStream_t s) {
   const int64_t rows = BLOCK / T;
-  layernorm_kernel<T, V, BLOCK><<<unsigned((N + rows - 1) / rows), BLOCK, 0, s>>>(
-      res_out, y, mean, rstd, stats, res_in, x, gain, shift, eps, N, C);
+  layernorm_kernel<T, V, BLOCK><<<unsigned((a.N + rows - 1) / rows), BLOCK, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-// Blocks per SM of the ring form, and the shared memory each may take.
-int ring_blocks_per_sm(int C) { return C <= 1024 ? 4 : C <= 4096 ? 2 : 1; }
+// Blocks per SM of the ring form: what their registers allow.  A row costs a
+// block a barrier and the latencies around it whatever its length, so short
+// rows need many blocks.
+int ring_blocks_backward(int C) { return C <= 1024 ? 6 : C <= 2048 ? 4 : C <= 4096 ? 2 : 1; }
 
-template <bool CENTRED, int T, int V>
-cudaError_t run_ring(NormBwd a, int blocks, cudaStream_t s) {
-  const int stage = a.C * 2 * (a.dres != nullptr ? 3 : 2);
-  const int budget = 208 * 1024 / ring_blocks_per_sm(a.C);
-  a.stages = budget / stage;
-  if (a.stages > kMaxStages) a.stages = kMaxStages;
-  const int bytes = a.stages * stage;
-  static bool set[64] = {false};
+constexpr int kRingBytes = 208 * 1024;            // shared memory of an SM that the rings take
+
+// Stages of a ring block with rows of `stage` bytes, and the kernel's permission to take that much.
+cudaError_t ring_stages(const void* kernel, int stage, int blocks_per_sm, int* stages, bool (&set)[64]) {
+  *stages = kRingBytes / blocks_per_sm / stage;
+  if (*stages > kMaxStages) *stages = kMaxStages;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    e = cudaFuncSetAttribute(norm_backward_kernel<CENTRED, T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             208 * 1024);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  norm_backward_kernel<CENTRED, T, V><<<blocks, T, bytes, s>>>(a);
+  return cudaSuccess;
+}
+
+template <bool CENTRED, int T, int V>
+cudaError_t run_ring(NormBwd a, int blocks, cudaStream_t s) {
+  static bool set[64] = {false};
+  const int stage = a.C * 2 * (a.dres != nullptr ? 3 : 2);
+  const cudaError_t e = ring_stages(reinterpret_cast<const void*>(norm_backward_kernel<CENTRED, T, V>), stage,
+                                    ring_blocks_backward(a.C), &a.stages, set);
+  if (e != cudaSuccess) return e;
+  norm_backward_kernel<CENTRED, T, V><<<blocks, T, a.stages * stage, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -474,7 +517,7 @@ cudaError_t norm_backward(const NormBwd& a, int blocks, cudaStream_t s) {
 
 int norm_backward_blocks(int64_t N, int C) {
   // fixed for the 152 SMs of the device, so that the workspace size needs no device query
-  const int64_t cap = int64_t(kNumSMsHint) * (C <= 512 ? 4 : ring_blocks_per_sm(C));
+  const int64_t cap = int64_t(kNumSMsHint) * (C <= 512 ? 4 : ring_blocks_backward(C));
   const int64_t need = C <= 512 ? (N + 7) / 8 : N;
   return int(need < cap ? (need > 0 ? need : 1) : cap);
 }
@@ -496,15 +539,21 @@ cudaError_t launch_layernorm(uint16_t* res_out, uint16_t* y, float* mean, float*
     if (e != cudaSuccess) return e;
   }
   if (N == 0) return cudaSuccess;
-#define QFFN_LN(T, V, B) run_layernorm<T, V, B>(res_out, y, mean, rstd, stats, res_in, x, gain, shift, eps, N, C, s)
-  if (C <= 256) return QFFN_LN(32, 1, 128);
-  if (C <= 512) return QFFN_LN(32, 2, 128);
-  if (C <= 1024) return QFFN_LN(32, 4, 128);
-  if (C <= 2048) return QFFN_LN(128, 2, 128);
-  if (C <= 4096) return QFFN_LN(128, 4, 128);
-  if (C <= 8192) return QFFN_LN(256, 4, 256);
-  return QFFN_LN(512, 4, 512);
-#undef QFFN_LN
+  const LnFwd a{res_out, y, mean, rstd, stats, res_in, x, gain, shift, eps, N, C};
+  if (C <= 256) return run_layernorm<32, 1, 128>(a, s);
+  if (C <= 512) return run_layernorm<32, 2, 128>(a, s);
+  if (N >= 8 * int64_t(num_sms())) {
+    if (C <= 1024) return run_layernorm<32, 4, 128>(a, s);
+    if (C <= 2048) return run_layernorm<128, 2, 128>(a, s);
+    if (C <= 4096) return run_layernorm<128, 4, 128>(a, s);
+    if (C <= 8192) return run_layernorm<256, 4, 256>(a, s);
+    return run_layernorm<512, 4, 512>(a, s);
+  }
+  if (C <= 1024) return run_layernorm<128, 1, 128>(a, s);
+  if (C <= 2048) return run_layernorm<256, 1, 256>(a, s);
+  if (C <= 4096) return run_layernorm<256, 2, 256>(a, s);
+  if (C <= 8192) return run_layernorm<512, 2, 512>(a, s);
+  return run_layernorm<1024, 2, 1024>(a, s);
 }
 
 cudaError_t launch_column_sum(float* out0, float* out1, const float* partial, int parts, int64_t cols0, int64_t cols,
@@ -512,7 +561,7 @@ cudaError_t launch_column_sum(float* out0, float* out1, const float* partial, in
   if (cols == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((cols + 31) / 32));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(1024);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
