@@ -71,7 +71,7 @@ QFFN_DEVI void act_grad_f32(float z, float& f, float& df) {
     df = fmaf(z * kInvSqrt2Pi, gauss, p);
   } else if (ACT == ACT_GELU_TANH) {
     const float z2 = z * z;
-    const float p = sigmoid_f32(kGeluTanhScale * fmaf(kGeluTanhCubic * z2, z, z));
+    const float p = sigmoid_f32(kGeluTanhScale * fmaf(kGeluTanhCubic * z * z, z, z));
     f = z * p;
     df = fmaf(f * (1.0f - p), kGeluTanhScale * fmaf(3.0f * kGeluTanhCubic, z2, 1.0f), p);
   } else if (ACT == ACT_SILU) {
@@ -81,6 +81,94 @@ QFFN_DEVI void act_grad_f32(float z, float& f, float& df) {
   } else {
     f = z;
     df = 1.0f;
+  }
+}
+
+// The same on pairs (f32x2): every lane's operations are those of the scalar
+// forms, so the results are the same bits; the fp32 pipe issues half as often.
+QFFN_DEVI uint64_t f2_dup(float v) { return f2_pack(v, v); }
+QFFN_DEVI uint64_t f2_abs(uint64_t v) { return v & 0x7FFFFFFF7FFFFFFFull; }
+
+QFFN_DEVI uint64_t sigmoid_f2(uint64_t v) {
+  float a, b, ea, eb, da, db;
+  f2_unpack(v, a, b);
+  ea = __expf(-fabsf(a));
+  eb = __expf(-fabsf(b));
+  const uint64_t e = f2_pack(ea, eb);
+  f2_unpack(f2_add(f2_dup(1.0f), e), da, db);
+  const float ra = __fdividef(1.0f, da), rb = __fdividef(1.0f, db);
+  float la, lb;
+  f2_unpack(f2_mul(e, f2_pack(ra, rb)), la, lb);
+  return f2_pack(a >= 0.0f ? ra : la, b >= 0.0f ? rb : lb);
+}
+
+QFFN_DEVI uint64_t normal_cdf_f2(uint64_t z, uint64_t& gauss) {
+  const uint64_t a = f2_abs(z);
+  float d0, d1, z0, z1;
+  f2_unpack(f2_fma(f2_dup(0.35f), a, f2_dup(1.0f)), d0, d1);
+  const uint64_t t = f2_pack(__fdividef(1.0f, d0), __fdividef(1.0f, d1));
+  uint64_t r = f2_dup(0.0489424504339695f);
+  r = f2_fma(r, t, f2_dup(-0.20211930572986603f));
+  r = f2_fma(r, t, f2_dup(0.24064083397388458f));
+  r = f2_fma(r, t, f2_dup(-0.01702345348894596f));
+  r = f2_fma(r, t, f2_dup(0.15596149861812592f));
+  r = f2_fma(r, t, f2_dup(0.13335509598255157f));
+  r = f2_fma(r, t, f2_dup(0.14027033746242523f));
+  r = f2_fma(r, t, f2_dup(-2.7315563784213737e-05f));
+  float q0, q1, t0, t1, c0, c1;
+  f2_unpack(f2_mul(f2_mul(f2_dup(-0.5f), a), a), q0, q1);
+  gauss = f2_pack(__expf(q0), __expf(q1));
+  const uint64_t tail = f2_mul(gauss, r);
+  f2_unpack(tail, t0, t1);
+  f2_unpack(f2_sub(f2_dup(1.0f), tail), c0, c1);
+  f2_unpack(z, z0, z1);
+  return f2_pack(z0 < 0.0f ? t0 : c0, z1 < 0.0f ? t1 : c1);
+}
+
+template <int ACT>
+QFFN_DEVI uint64_t act_f2(uint64_t z) {
+  if (ACT == ACT_RELU) {
+    float a, b;
+    f2_unpack(z, a, b);
+    return f2_pack(a < 0.0f ? 0.0f : a, b < 0.0f ? 0.0f : b);
+  }
+  if (ACT == ACT_GELU) {
+    uint64_t gauss;
+    return f2_mul(z, normal_cdf_f2(z, gauss));
+  }
+  if (ACT == ACT_GELU_TANH) {
+    const uint64_t s = f2_mul(f2_dup(kGeluTanhScale), f2_fma(f2_mul(f2_mul(f2_dup(kGeluTanhCubic), z), z), z, z));
+    return f2_mul(z, sigmoid_f2(s));
+  }
+  if (ACT == ACT_SILU) return f2_mul(z, sigmoid_f2(z));
+  return z;
+}
+
+template <int ACT>
+QFFN_DEVI void act_grad_f2(uint64_t z, uint64_t& f, uint64_t& df) {
+  if (ACT == ACT_GELU) {
+    uint64_t gauss;
+    const uint64_t p = normal_cdf_f2(z, gauss);
+    f = f2_mul(z, p);
+    df = f2_fma(f2_mul(z, f2_dup(kInvSqrt2Pi)), gauss, p);
+  } else if (ACT == ACT_GELU_TANH) {
+    const uint64_t z2 = f2_mul(z, z);
+    const uint64_t p =
+        sigmoid_f2(f2_mul(f2_dup(kGeluTanhScale), f2_fma(f2_mul(f2_mul(f2_dup(kGeluTanhCubic), z), z), z, z)));
+    f = f2_mul(z, p);
+    df = f2_fma(f2_mul(f, f2_sub(f2_dup(1.0f), p)),
+                f2_mul(f2_dup(kGeluTanhScale), f2_fma(f2_dup(3.0f * kGeluTanhCubic), z2, f2_dup(1.0f))), p);
+  } else if (ACT == ACT_SILU) {
+    const uint64_t p = sigmoid_f2(z);
+    f = f2_mul(z, p);
+    df = f2_mul(p, f2_fma(z, f2_sub(f2_dup(1.0f), p), f2_dup(1.0f)));
+  } else {
+    float a, b, fa, fb, da, db;
+    f2_unpack(z, a, b);
+    act_grad_f32<ACT>(a, fa, da);
+    act_grad_f32<ACT>(b, fb, db);
+    f = f2_pack(fa, fb);
+    df = f2_pack(da, db);
   }
 }
 

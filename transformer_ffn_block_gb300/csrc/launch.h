@@ -11,6 +11,24 @@ namespace qffn {
 // Number of SMs of the current device (cached per device).
 int num_sms();
 
+// Launches `kernel` as a programmatic dependent launch: its blocks may be
+// scheduled while the kernel before it on `s` drains.  Only for kernels that
+// call pdl_wait() in every thread before they touch global memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, int block, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(block));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // ---- elementwise / reduction kernels (elementwise.cu)
 cudaError_t launch_rmsnorm(uint16_t* res_out, uint16_t* y, float* rstd, float* stats,
                            const uint16_t* res_in, const uint16_t* x, const uint16_t* gain,

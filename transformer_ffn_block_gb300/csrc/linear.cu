@@ -9,6 +9,10 @@
 //                  recomputed g, u and dh [M,H] read in the epilogue
 //   EPI_PARTIAL    fp32 sums over one part of K, joined by join_kernel, which
 //                  then applies one of the epilogues above
+//   EPI_PARTIAL_T  the same with the weights as the 256-row operand and up to
+//                  256 activation rows as the other: for few rows, where the
+//                  weights' bytes bound the call and a 256-row tile of
+//                  activations would be mostly padding
 //
 // The matmul and the epilogues of a transformer block's feed-forward half
 // (llmq "llama_model.cpp", LLamaModel::_forward_block and _backward_block) in
@@ -67,7 +71,8 @@ constexpr int OP_BF16 = 0, OP_E4M3 = 1;
 constexpr int box_k(int op) { return op == OP_BF16 ? 64 : 128; }
 constexpr int stage_k(int op) { return KBOX * box_k(op); }
 
-constexpr int EPI_LINEAR = 0, EPI_GATED = 1, EPI_GATED_BWD = 2, EPI_PARTIAL = 3;
+constexpr int EPI_LINEAR = 0, EPI_GATED = 1, EPI_GATED_BWD = 2, EPI_PARTIAL = 3, EPI_PARTIAL_T = 4;
+constexpr bool is_partial(int epi) { return epi == EPI_PARTIAL || epi == EPI_PARTIAL_T; }
 
 // Instruction descriptor: D fp32 (bits 4-5 = 1); A and B formats at bits 7-9
 // and 10-12 (kind::f16: 1 = bf16; kind::f8f6f4: 0 = E4M3); bits 15 / 16: A / B
@@ -76,6 +81,13 @@ constexpr uint32_t idesc_for(int op, bool a_mn, bool b_mn, int n) {
   return (1u << 4) | (op == OP_BF16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
          (b_mn ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) | (uint32_t((2 * BM) >> 4) << 24);
 }
+
+QFFN_DEVI uint32_t pack2(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+QFFN_DEVI uint4 pack8(const uint64_t (&v)[4]) { return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3])); }
 
 __device__ unsigned int g_status;
 
@@ -90,7 +102,9 @@ struct LinArgs {
   int tiles_m, tiles_n, num_units, num_kb;
   int band_n;               // N-blocks per raster band
   int split_from;           // units from here on are 128-column halves of the last tiles
-  int splits, kb_per_split, m_pad;   // EPI_PARTIAL
+  int splits, kb_per_split, m_pad;   // EPI_PARTIAL*
+  float* partial;           // EPI_PARTIAL_T: [splits][m_pad][M], m_pad activation rows; N of them are stored
+  int bn;                   // EPI_PARTIAL_T: activation rows per tile (multiple of 32); else 256
 };
 
 // D(tmem, both CTAs) (+)= A(smem, both CTAs) . B(smem, both CTAs)^T
@@ -131,7 +145,7 @@ QFFN_DEVI bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag
 struct Unit {
   int mb, nb;      // pair M-block (256 rows), N-block
   int half;        // -1: whole tile; 0 / 1: first / second 128 accumulator columns of a split one
-  int sp;          // EPI_PARTIAL: part of K
+  int sp;          // EPI_PARTIAL*: part of K
 };
 
 template <int EPI>
@@ -140,7 +154,7 @@ QFFN_DEVI Unit unit_coords(int u, const LinArgs& a) {
   r.half = -1;
   r.sp = 0;
   int tile = u;
-  if (EPI == EPI_PARTIAL) {
+  if (is_partial(EPI)) {
     tile = u / a.splits;
     r.sp = u - tile * a.splits;
   } else if (u >= a.split_from) {
@@ -218,7 +232,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
-    tma_prefetch_desc(&tmO);
+    if (EPI != EPI_PARTIAL_T) tma_prefetch_desc(&tmO);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -234,9 +248,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   pdl_trigger();
 
   // K blocks of a unit
-  auto kb_begin = [&](const Unit& u) { return EPI == EPI_PARTIAL ? u.sp * args.kb_per_split : 0; };
+  auto kb_begin = [&](const Unit& u) { return is_partial(EPI) ? u.sp * args.kb_per_split : 0; };
   auto kb_end = [&](const Unit& u) {
-    return EPI == EPI_PARTIAL ? min(args.num_kb, (u.sp + 1) * args.kb_per_split) : args.num_kb;
+    return is_partial(EPI) ? min(args.num_kb, (u.sp + 1) * args.kb_per_split) : args.num_kb;
   };
 
   if (warp == 0) {
@@ -250,10 +264,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int rowA = u.mb * (2 * BM) + int(rank) * BM;
         // this CTA's weight rows: half of the tile's 256 (of a half tile's
         // 128); gated: CTA 0 the gate rows, CTA 1 the matching up rows
-        const int rowB = GATED ? (rank == 0 ? 0 : args.up_row) + u.nb * 128 + (u.half < 0 ? 0 : u.half * 64)
+        const int rowB = EPI == EPI_PARTIAL_T ? u.nb * args.bn + int(rank) * (args.bn / 2)
+                         : GATED ? (rank == 0 ? 0 : args.up_row) + u.nb * 128 + (u.half < 0 ? 0 : u.half * 64)
                          : u.half < 0 ? u.nb * BN + int(rank) * 128
                                       : u.nb * BN + u.half * 128 + int(rank) * 64;
-        const uint32_t stage_tx = u.half < 0 ? 2 * STAGE_BYTES : 2 * (OP_BYTES + OP_BYTES / 2);
+        const uint32_t stage_tx = EPI == EPI_PARTIAL_T ? 2u * uint32_t(OP_BYTES + args.bn / 2 * ROW_BYTES * KBOX)
+                                  : u.half < 0 ? 2 * STAGE_BYTES : 2 * (OP_BYTES + OP_BYTES / 2);
         const int kb1 = kb_end(u);
         for (int kb = kb_begin(u); kb < kb1; ++kb, ++it) {
           const int s = it % STAGES;
@@ -298,7 +314,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_after();
         const Unit u = unit_coords<EPI>(un, args);
         const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
-        const uint32_t idesc = u.half < 0 ? idesc_for(OP, A_MN, B_MN, BN) : idesc_for(OP, A_MN, B_MN, BN / 2);
+        const uint32_t idesc = EPI == EPI_PARTIAL_T ? idesc_for(OP, A_MN, B_MN, 32) + (uint32_t(args.bn - 32) << 14)
+                               : u.half < 0 ? idesc_for(OP, A_MN, B_MN, BN) : idesc_for(OP, A_MN, B_MN, BN / 2);
         const int kb0 = kb_begin(u), kb1 = kb_end(u);
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = it % STAGES;
@@ -362,11 +379,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const Unit u = unit_coords<EPI>(un, args);
       const int row0 = first_row(u);
       const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * BN);
-      const int acc_cols = u.half < 0 ? BN : BN / 2;
+      const int acc_cols = EPI == EPI_PARTIAL_T ? args.bn : u.half < 0 ? BN : BN / 2;
       // groups of 32 output columns (partial sums: 32 fp32 columns, in both boxes)
       const int groups = GATED ? acc_cols / 64 : acc_cols / 32;
       bool ok = true;
       for (int g = wg; g < groups; g += 2) {
+        if (EPI == EPI_PARTIAL_T) {
+          // lanes hold weight rows, columns are activation rows: a warp's store
+          // of one column is 128 contiguous bytes of that activation row
+          uint32_t v[32];
+          tmem_ld32(tbase + uint32_t(g * 32), v);
+          const int n = row0 + lane, m0 = u.nb * args.bn + g * 32;
+          if (n < args.M) {
+            float* dst = args.partial + (size_t(u.sp) * size_t(args.m_pad) + size_t(m0)) * size_t(args.M) + size_t(n);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (m0 + j < args.N) dst[size_t(j) * size_t(args.M)] = __uint_as_float(v[j]);
+          }
+          continue;
+        }
         const int b = paired || EPI == EPI_PARTIAL ? 0 : flip;
         flip ^= 1;
         if (has_in) {
@@ -407,39 +438,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t off = chunk_off(k);
-            float z[8];
+            uint64_t z[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) z[j] = __uint_as_float(v[8 * k + j]);
-            if (OP == OP_E4M3) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) z[j] *= scale;
+            for (int j = 0; j < 4; ++j) {
+              z[j] = f2_pack(__uint_as_float(v[8 * k + 2 * j]), __uint_as_float(v[8 * k + 2 * j + 1]));
+              if (OP == OP_E4M3) z[j] = f2_mul(z[j], f2_dup(scale));
             }
             if (args.bias != nullptr) {
               const uint32_t bw[4] = {bias[k].x, bias[k].y, bias[k].z, bias[k].w};
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                z[2 * j] += bf16_lo(bw[j]);
-                z[2 * j + 1] += bf16_hi(bw[j]);
-              }
+              for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bf16x2_to_f2(bw[j]));
             }
-            if (args.save_z)
-              *reinterpret_cast<uint4*>(box(1) + off) =
-                  make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
-                             pack_bf16x2(z[6], z[7]));
+            if (args.save_z) *reinterpret_cast<uint4*>(box(1) + off) = pack8(z);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) z[j] = act_f32<ACT>(z[j]);
+            for (int j = 0; j < 4; ++j) z[j] = act_f2<ACT>(z[j]);
             if (args.has_in) {
               const uint4 o4 = *reinterpret_cast<const uint4*>(box(b) + off);
               const uint32_t ow[4] = {o4.x, o4.y, o4.z, o4.w};
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                z[2 * j] += bf16_lo(ow[j]);
-                z[2 * j + 1] += bf16_hi(ow[j]);
-              }
+              for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bf16x2_to_f2(ow[j]));
             }
-            *reinterpret_cast<uint4*>(box(b) + off) =
-                make_uint4(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]), pack_bf16x2(z[4], z[5]),
-                           pack_bf16x2(z[6], z[7]));
+            *reinterpret_cast<uint4*>(box(b) + off) = pack8(z);
           }
         } else {
           const int up_off = acc_cols / 2;   // accumulator column of u
@@ -458,17 +477,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const float g0 = __uint_as_float(gv[8 * k + 2 * j]), g1 = __uint_as_float(gv[8 * k + 2 * j + 1]);
-                const float u0 = __uint_as_float(uv[8 * k + 2 * j]), u1 = __uint_as_float(uv[8 * k + 2 * j + 1]);
+                const uint64_t gp = f2_pack(__uint_as_float(gv[8 * k + 2 * j]), __uint_as_float(gv[8 * k + 2 * j + 1]));
+                const uint64_t up = f2_pack(__uint_as_float(uv[8 * k + 2 * j]), __uint_as_float(uv[8 * k + 2 * j + 1]));
                 if (EPI == EPI_GATED) {
-                  p[j] = pack_bf16x2(act_f32<ACT>(g0) * u0, act_f32<ACT>(g1) * u1);
+                  p[j] = pack2(f2_mul(act_f2<ACT>(gp), up));
                 } else {
-                  float f0, df0, f1, df1;
-                  act_grad_f32<ACT>(g0, f0, df0);
-                  act_grad_f32<ACT>(g1, f1, df1);
-                  const float d0 = bf16_lo(dw[j]), d1 = bf16_hi(dw[j]);
-                  p[j] = pack_bf16x2(d0 * u0 * df0, d1 * u1 * df1);
-                  p2[j] = pack_bf16x2(d0 * f0, d1 * f1);
+                  uint64_t f, df;
+                  act_grad_f2<ACT>(gp, f, df);
+                  const uint64_t d = bf16x2_to_f2(dw[j]);
+                  p[j] = pack2(f2_mul(f2_mul(d, up), df));
+                  p2[j] = pack2(f2_mul(d, f));
                 }
               }
               *reinterpret_cast<uint4*>(box(b) + off) = make_uint4(p[0], p[1], p[2], p[3]);
@@ -612,46 +630,54 @@ __global__ void __launch_bounds__(256) join_kernel(uint16_t* out, uint16_t* out2
 // 8 l .. 8 l + 7 of rows w, w + 8, ...  The column sums are taken from the fp32
 // dz before its rounding; the block's eight warps are added in order and
 // column_sum_kernel adds the blocks'.  ACT_NONE (dz = dout) only sums.
+constexpr int kRowsInFlight = 4;           // loads issued per thread before the first is used
 template <int ACT>
 __global__ void __launch_bounds__(256) act_backward_kernel(uint16_t* dz, float* partial, const uint16_t* dout,
                                                            const uint16_t* z, int64_t M, int64_t N) {
-  __shared__ float comb[8][256 + 8];
+  __shared__ __align__(8) float comb[8][256 + 8];
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
   const int64_t col = int64_t(blockIdx.x) * 256 + l * 8;
   const bool live = col < N;
-  float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  pdl_wait();
+  pdl_trigger();
+  uint64_t s[4] = {0ull, 0ull, 0ull, 0ull};
   if (live) {
-    for (int64_t row = int64_t(blockIdx.y) * 8 + w; row < M; row += int64_t(gridDim.y) * 8) {
-      const size_t i = size_t(row) * size_t(N) + size_t(col);
-      const uint4 d4 = ld16_ro_stream(dout + i);
-      const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
-      float d[8];
+    const int64_t step = int64_t(gridDim.y) * 8;
+    for (int64_t row0 = int64_t(blockIdx.y) * 8 + w; row0 < M; row0 += kRowsInFlight * step) {
+      uint4 d4[kRowsInFlight], z4[kRowsInFlight];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        d[2 * j] = bf16_lo(dw[j]);
-        d[2 * j + 1] = bf16_hi(dw[j]);
-      }
-      if (ACT != ACT_NONE) {
-        const uint4 z4 = ld16_ro_stream(z + i);
-        const uint32_t zw[4] = {z4.x, z4.y, z4.z, z4.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float f, df;
-          act_grad_f32<ACT>(bf16_lo(zw[j]), f, df);
-          d[2 * j] *= df;
-          act_grad_f32<ACT>(bf16_hi(zw[j]), f, df);
-          d[2 * j + 1] *= df;
+      for (int k = 0; k < kRowsInFlight; ++k) {
+        const int64_t row = row0 + k * step;
+        d4[k] = z4[k] = make_uint4(0, 0, 0, 0);
+        if (row < M) {
+          const size_t i = size_t(row) * size_t(N) + size_t(col);
+          d4[k] = ld16_once(dout + i);
+          if (ACT != ACT_NONE) z4[k] = ld16_once(z + i);
         }
-        stg16(dz + i, make_uint4(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]), pack_bf16x2(d[4], d[5]),
-                                 pack_bf16x2(d[6], d[7])));
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] += d[j];
+      for (int k = 0; k < kRowsInFlight; ++k) {
+        const int64_t row = row0 + k * step;
+        if (row >= M) break;
+        uint64_t d[4] = {bf16x2_to_f2(d4[k].x), bf16x2_to_f2(d4[k].y), bf16x2_to_f2(d4[k].z), bf16x2_to_f2(d4[k].w)};
+        if (ACT != ACT_NONE) {
+          const uint32_t zw[4] = {z4[k].x, z4[k].y, z4[k].z, z4[k].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint64_t f, df;
+            act_grad_f2<ACT>(bf16x2_to_f2(zw[j]), f, df);
+            d[j] = f2_mul(d[j], df);
+          }
+          stg16(dz + size_t(row) * size_t(N) + size_t(col), pack8(d));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = f2_add(s[j], d[j]);
+      }
     }
   }
   if (partial == nullptr) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) comb[w][l * 8 + j] = s[j];
+  for (int j = 0; j < 4; ++j) *reinterpret_cast<uint64_t*>(&comb[w][l * 8 + 2 * j]) = s[j];
   __syncthreads();
   const int64_t c = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (c < N) {
@@ -740,7 +766,7 @@ struct Maps {
 };
 
 template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
-cudaError_t launch(const Maps& m, const LinArgs& a, int pairs, bool pdl, cudaStream_t s) {
+cudaError_t launch(const Maps& m, const LinArgs& a, int pairs, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * unsigned(a.num_units < pairs ? a.num_units : pairs));
   cfg.blockDim = dim3(NUM_THREADS);
@@ -754,37 +780,52 @@ cudaError_t launch(const Maps& m, const LinArgs& a, int pairs, bool pdl, cudaStr
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, linear_kernel<OP, EPI, ACT, A_MN, B_MN>, m.a, m.b, m.bh, m.o, m.z, m.i, a);
 }
 
-// How a product [M, K] x [N, K]^T is cut: the tiles, and the parts of K where
-// the tiles alone would leave most SM pairs idle.
+// How a product [M, K] x [N, K]^T is cut: the tiles, their orientation, and the
+// parts of K where the tiles alone would leave SM pairs idle.
 struct Plan {
+  bool turned;               // the weights are the 256-row operand (EPI_PARTIAL_T)
+  int bn;                    // activation rows per tile when turned
   int tiles_m, tiles_n, tiles, num_kb, splits, kb_per_split;
   int64_t m_pad;
 };
 constexpr int kPlanPairs = kNumSMsHint / 2;   // fixed, so a workspace size needs no device query
-Plan make_plan(int64_t M, int64_t N, int64_t K, int op) {
+constexpr int kTurnedRows = 256;
+// can_turn: not for an MN-major activation operand (the weight gradients), whose
+// boxes are 64 values wide.
+Plan make_plan(int64_t M, int64_t N, int64_t K, int op, bool can_turn = true) {
   Plan p;
-  p.tiles_m = int((M + 2 * BM - 1) / (2 * BM));
-  p.tiles_n = int((N + BN - 1) / BN);
+  p.turned = can_turn && M <= kTurnedRows;
+  p.bn = p.turned ? int((M + 31) / 32 * 32) : BN;
+  const int64_t rows = p.turned ? N : M, cols = p.turned ? M : N;
+  p.tiles_m = int((rows + 2 * BM - 1) / (2 * BM));
+  p.tiles_n = p.turned ? 1 : int((cols + BN - 1) / BN);
   p.tiles = p.tiles_m * p.tiles_n;
   p.num_kb = int((K + stage_k(op) - 1) / stage_k(op));
   p.m_pad = (M + 31) / 32 * 32;
   p.splits = 1;
-  if (p.tiles > 0 && 2 * p.tiles <= kPlanPairs) {
-    int s = kPlanPairs / p.tiles;
-    if (s > p.num_kb / 4) s = p.num_kb / 4;   // at least four stages of work per part
-    if (s > 16) s = 16;
-    if (s > 1) p.splits = s;
+  if (p.tiles > 0 && (p.turned || 2 * p.tiles <= kPlanPairs)) {
+    // the number of parts with the shortest schedule, in stages: rounds of
+    // units over the pairs, each unit its part of K and about four stages'
+    // time of filling and draining; more parts only where they shorten it
+    int best = 0;
+    for (int s = 1; s <= 16 && s * 4 <= p.num_kb; ++s) {
+      const int cost = (p.tiles * s + kPlanPairs - 1) / kPlanPairs * ((p.num_kb + s - 1) / s + 4);
+      if (best == 0 || cost < best) {
+        best = cost;
+        p.splits = s;
+      }
+    }
   }
   p.kb_per_split = (p.num_kb + p.splits - 1) / p.splits;
   if (p.num_kb > 0) p.splits = (p.num_kb + p.kb_per_split - 1) / p.kb_per_split;
   return p;
 }
 size_t plan_bytes(const Plan& p, int64_t N) {
-  return p.splits > 1 ? size_t(p.splits) * size_t(p.m_pad) * size_t(N) * sizeof(float) : 0;
+  return p.turned || p.splits > 1 ? size_t(p.splits) * size_t(p.m_pad) * size_t(N) * sizeof(float) : 0;
 }
 
 // N-blocks per raster band: about 32 MB of weights, so that a band stays in L2
@@ -805,17 +846,8 @@ cudaError_t launch_join(uint16_t* out, uint16_t* out2, const float* partial, con
   int64_t blocks = (total + 255) / 256;
   const int64_t cap = int64_t(num_sms()) * 8;
   if (blocks > cap) blocks = cap;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(blocks));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<EPI, ACT>, out, out2, partial, bias, in, a_scale, w_scale, p.splits,
-                            p.m_pad, ld, M, N);
+  return launch_pdl(join_kernel<EPI, ACT>, dim3(unsigned(blocks)), 256, 0, s, out, out2, partial, bias, in, a_scale,
+                    w_scale, p.splits, p.m_pad, ld, M, N);
 }
 
 // One product with its epilogue.  EPI_LINEAR: N output columns; gated forms:
@@ -823,10 +855,10 @@ cudaError_t launch_join(uint16_t* out, uint16_t* out2, const float* partial, con
 template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
 cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_scale, const void* B,
                     const float* w_scale, const uint16_t* bias, const uint16_t* in, int64_t M, int64_t N, int64_t K,
-                    float* partial, bool pdl, cudaStream_t s) {
+                    float* partial, cudaStream_t s) {
   constexpr bool GATED = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
   const int64_t brows = GATED ? 2 * N : N;
-  const Plan p = make_plan(M, brows, K, OP);
+  const Plan p = make_plan(M, brows, K, OP, !A_MN);
   Maps m;
   if (!operand_map<OP>(&m.a, A, M, K, A_MN) || !operand_map<OP>(&m.b, B, brows, K, B_MN)) return cudaErrorInvalidValue;
   m.bh = m.b;
@@ -838,6 +870,27 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
   a.splits = 1;
   int pairs = 0;
   cudaError_t e;
+  a.bn = p.bn;
+  if constexpr (!A_MN) {
+    if (p.turned) {
+      // the weights are A, the activations B
+      Maps t;
+      if (!operand_map<OP>(&t.a, B, brows, K, B_MN) || !operand_map<OP>(&t.b, A, M, K, false, p.bn / 2))
+        return cudaErrorInvalidValue;
+      t.bh = t.o = t.z = t.i = t.b;
+      a.M = int(brows);
+      a.N = int(M);
+      a.tiles_n = a.band_n = p.tiles_n;
+      a.splits = p.splits;
+      a.kb_per_split = p.kb_per_split;
+      a.m_pad = int(p.m_pad);
+      a.partial = partial;
+      a.num_units = a.split_from = p.tiles * p.splits;
+      if ((e = max_pairs<OP, EPI_PARTIAL_T, ACT_NONE, B_MN, false>(&pairs)) != cudaSuccess) return e;
+      if ((e = launch<OP, EPI_PARTIAL_T, ACT_NONE, B_MN, false>(t, a, pairs, s)) != cudaSuccess) return e;
+      return launch_join<EPI, ACT>(out, z, partial, bias, in, a_scale, w_scale, p, brows, M, N, s);
+    }
+  }
   if (p.splits > 1) {
     if (!make_map(&m.o, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, partial, p.splits * p.m_pad, brows, brows, 32,
                   64, CU_TENSOR_MAP_L2_PROMOTION_NONE))
@@ -851,7 +904,7 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
     a.m_pad = int(p.m_pad);
     a.num_units = a.split_from = p.tiles * p.splits;
     if ((e = max_pairs<OP, EPI_PARTIAL, ACT_NONE, A_MN, B_MN>(&pairs)) != cudaSuccess) return e;
-    if ((e = launch<OP, EPI_PARTIAL, ACT_NONE, A_MN, B_MN>(m, a, pairs, pdl, s)) != cudaSuccess) return e;
+    if ((e = launch<OP, EPI_PARTIAL, ACT_NONE, A_MN, B_MN>(m, a, pairs, s)) != cudaSuccess) return e;
     return launch_join<EPI, ACT>(out, z, partial, bias, in, a_scale, w_scale, p, brows, M, N, s);
   }
   a.N = int(N);
@@ -881,7 +934,7 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
     a.split_from = a.num_units - r;
     a.num_units += r;
   }
-  return launch<OP, EPI, ACT, A_MN, B_MN>(m, a, pairs, pdl, s);
+  return launch<OP, EPI, ACT, A_MN, B_MN>(m, a, pairs, s);
 }
 
 int act_backward_blocks(int64_t M, int64_t N) {
@@ -899,7 +952,7 @@ void linear_bwd_offsets(int64_t M, int64_t N, int64_t K, size_t off[4]) {
   off[0] = 0;
   off[1] = round256(size_t(M) * size_t(N) * 2);
   off[2] = off[1] + round256(size_t(act_backward_blocks(M, N)) * size_t(N) * sizeof(float));
-  const size_t a = plan_bytes(make_plan(M, K, N, OP_BF16), K), b = plan_bytes(make_plan(N, K, M, OP_BF16), K);
+  const size_t a = plan_bytes(make_plan(M, K, N, OP_BF16), K), b = plan_bytes(make_plan(N, K, M, OP_BF16, false), K);
   off[3] = off[2] + round256(a > b ? a : b);
 }
 
@@ -908,7 +961,7 @@ void gated_bwd_offsets(int64_t M, int64_t C, int64_t H, size_t off[3]) {
   off[0] = 0;
   off[1] = round256(size_t(M) * size_t(2 * H) * 2);
   size_t a = plan_bytes(make_plan(M, 2 * H, C, OP_BF16), 2 * H);
-  const size_t b = plan_bytes(make_plan(M, C, 2 * H, OP_BF16), C), c = plan_bytes(make_plan(2 * H, C, M, OP_BF16), C);
+  const size_t b = plan_bytes(make_plan(M, C, 2 * H, OP_BF16), C), c = plan_bytes(make_plan(2 * H, C, M, OP_BF16, false), C);
   a = a > b ? a : b;
   off[2] = off[1] + round256(a > c ? a : c);
 }
@@ -946,7 +999,7 @@ cudaError_t launch_linear(uint16_t* out, uint16_t* z, const uint16_t* x, const u
   if (M == 0) return cudaSuccess;
   if (skinny_rows(M)) return launch_skinny(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, false, s);
   QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_LINEAR, ACT, false, false>(out, z, x, nullptr, w, nullptr, bias, res, M, N,
-                                                                        K, ws, false, s)));
+                                                                        K, ws, s)));
 }
 
 cudaError_t launch_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, const float* x_scale, const uint8_t* w,
@@ -955,7 +1008,7 @@ cudaError_t launch_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, cons
   if (M == 0) return cudaSuccess;
   if (skinny_rows(M)) return launch_skinny(out, z, x, x_scale, w, w_scale, bias, res, act, M, N, K, true, s);
   QFFN_ACT_SWITCH(act, (product<OP_E4M3, EPI_LINEAR, ACT, false, false>(out, z, x, x_scale, w, w_scale, bias, res, M, N,
-                                                                        K, ws, false, s)));
+                                                                        K, ws, s)));
 }
 
 cudaError_t launch_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int act, int64_t M, int64_t C, int64_t H,
@@ -963,7 +1016,7 @@ cudaError_t launch_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int
   if (M == 0) return cudaSuccess;
   if (skinny_rows(M)) return launch_skinny_gated(h, x, w1, act, M, C, H, s);
   QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_GATED, ACT, false, false>(h, nullptr, x, nullptr, w1, nullptr, nullptr,
-                                                                       nullptr, M, H, C, ws, false, s)));
+                                                                       nullptr, M, H, C, ws, s)));
 }
 
 namespace {
@@ -971,8 +1024,7 @@ template <int ACT>
 cudaError_t run_act_backward(uint16_t* dz, float* partial, const uint16_t* dout, const uint16_t* z, int64_t M,
                              int64_t N, cudaStream_t s) {
   const dim3 grid(unsigned((N + 255) / 256), unsigned(act_backward_blocks(M, N)));
-  act_backward_kernel<ACT><<<grid, 256, 0, s>>>(dz, partial, dout, z, M, N);
-  return cudaGetLastError();
+  return launch_pdl(act_backward_kernel<ACT>, grid, 256, 0, s, dz, partial, dout, z, M, N);
 }
 cudaError_t act_backward(uint16_t* dz, float* partial, const uint16_t* dout, const uint16_t* z, int act, int64_t M,
                          int64_t N, cudaStream_t s) {
@@ -981,19 +1033,18 @@ cudaError_t act_backward(uint16_t* dz, float* partial, const uint16_t* dout, con
 cudaError_t gated_bwd_product(uint16_t* dgu, const uint16_t* dh, const uint16_t* x, const uint16_t* w1, int act,
                               int64_t M, int64_t C, int64_t H, float* part, cudaStream_t s) {
   QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_GATED_BWD, ACT, false, false>(dgu, nullptr, x, nullptr, w1, nullptr,
-                                                                           nullptr, dh, M, H, C, part, false, s)));
+                                                                           nullptr, dh, M, H, C, part, s)));
 }
 // dx [M,K] = dz [M,N] . W [N,K];  dw [N,K] (+)= dz^T . x [M,K]: W, dz and x read where they lie
 cudaError_t grad_products(uint16_t* dx, uint16_t* dw, const uint16_t* dz, const uint16_t* x, const uint16_t* w,
-                          int64_t M, int64_t N, int64_t K, bool accumulate, float* part, bool pdl, cudaStream_t s) {
+                          int64_t M, int64_t N, int64_t K, bool accumulate, float* part, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (dx != nullptr &&
       (e = product<OP_BF16, EPI_LINEAR, ACT_NONE, false, true>(dx, nullptr, dz, nullptr, w, nullptr, nullptr, nullptr, M,
-                                                               K, N, part, pdl, s)) != cudaSuccess)
+                                                               K, N, part, s)) != cudaSuccess)
     return e;
   return product<OP_BF16, EPI_LINEAR, ACT_NONE, true, true>(dw, nullptr, dz, nullptr, x, nullptr, nullptr,
-                                                            accumulate ? dw : nullptr, N, K, M, part,
-                                                            pdl || dx != nullptr, s);
+                                                            accumulate ? dw : nullptr, N, K, M, part, s);
 }
 }  // namespace
 
@@ -1013,16 +1064,14 @@ cudaError_t launch_linear_backward(uint16_t* dx, uint16_t* dw, float* dbias, con
   float* cols = reinterpret_cast<float*>(ws + off[1]);
   float* part = reinterpret_cast<float*>(ws + off[2]);
   const uint16_t* dz = act == ACT_NONE ? dout : dzb;
-  bool chained = false;
   if (act != ACT_NONE || dbias != nullptr) {
     if ((e = act_backward(dzb, dbias != nullptr ? cols : nullptr, dout, z, act, M, N, s)) != cudaSuccess) return e;
     if (dbias != nullptr) {
       if ((e = launch_column_sum(dbias, nullptr, cols, act_backward_blocks(M, N), N, N, accumulate, s)) != cudaSuccess)
         return e;
     }
-    chained = true;
   }
-  return grad_products(dx, dw, dz, x, w, M, N, K, accumulate, part, chained, s);
+  return grad_products(dx, dw, dz, x, w, M, N, K, accumulate, part, s);
 }
 
 cudaError_t launch_gated_backward(uint16_t* dx, uint16_t* dw1, const uint16_t* dh, const uint16_t* x,
@@ -1035,7 +1084,7 @@ cudaError_t launch_gated_backward(uint16_t* dx, uint16_t* dw1, const uint16_t* d
   float* part = reinterpret_cast<float*>(ws + off[1]);
   const cudaError_t e = gated_bwd_product(dgu, dh, x, w1, act, M, C, H, part, s);
   if (e != cudaSuccess) return e;
-  return grad_products(dx, dw1, dgu, x, w1, M, 2 * H, C, accumulate, part, true, s);
+  return grad_products(dx, dw1, dgu, x, w1, M, 2 * H, C, accumulate, part, s);
 }
 
 cudaError_t linear_take_status(unsigned int* status) {

@@ -13,6 +13,7 @@
 // of squares about the mean; no cancellation when |mean| >> sqrt(var)) and the
 // two row sums of the backward cost no second read.  All sums are fp32; every
 // output is rounded once.
+#include "act.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "pipeline.cuh"
@@ -51,7 +52,6 @@ QFFN_DEVI uint32_t pack2(uint64_t v) {
   return pack_bf16x2(lo, hi);
 }
 QFFN_DEVI uint4 pack8(const F8& f) { return make_uint4(pack2(f.p[0]), pack2(f.p[1]), pack2(f.p[2]), pack2(f.p[3])); }
-QFFN_DEVI uint64_t f2_dup(float v) { return f2_pack(v, v); }
 QFFN_DEVI float f2_sum(uint64_t v) {
   float lo, hi;
   f2_unpack(v, lo, hi);
@@ -127,6 +127,8 @@ __global__ void __launch_bounds__(BLOCK) layernorm_kernel(const LnFwd a) {
   const bool live = row < a.N;               // a team of T > 32 is the block: always live
   const int nchunk = a.C >> 3;
   const size_t base = live ? size_t(row) * size_t(a.C) : 0;
+  pdl_wait();
+  pdl_trigger();
   uint4 rv[V];
   uint64_t acc = 0ull;
 #pragma unroll
@@ -233,6 +235,8 @@ __global__ void __launch_bounds__(256) norm_backward_warp_kernel(const NormBwd a
   const int t = threadIdx.x & 31, team = threadIdx.x >> 5;
   const int nchunk = a.C >> 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  pdl_wait();
+  pdl_trigger();
   uint4 gv[V];
   uint64_t dg[V][4], ds[V][4];               // pairs of columns
 #pragma unroll
@@ -322,6 +326,8 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const NormBwd a) {
     mbar_init_fence();
   }
   __syncthreads();
+  pdl_wait();
+  pdl_trigger();
   auto load_row = [&](int64_t row, int s) {       // thread 0
     const uint32_t bar = smem_u32(&bars[s]), dst = smem_u32(ring) + uint32_t(s) * stage_bytes;
     const size_t base = size_t(row) * size_t(a.C);
@@ -432,6 +438,7 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const NormBwd a) {
 __global__ void __launch_bounds__(1024) column_sum_kernel(float* out0, float* out1, const float* partial, int parts,
                                                           int64_t cols0, int64_t cols, int accumulate) {
   pdl_wait();
+  pdl_trigger();
   __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int64_t c = int64_t(blockIdx.x) * 32 + lane;
@@ -462,8 +469,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(float* out0, float* ou
 template <int T, int V, int BLOCK>
 cudaError_t run_layernorm(const LnFwd& a, cudaStream_t s) {
   const int64_t rows = BLOCK / T;
-  layernorm_kernel<T, V, BLOCK><<<unsigned((a.N + rows - 1) / rows), BLOCK, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(layernorm_kernel<T, V, BLOCK>, dim3(unsigned((a.N + rows - 1) / rows)), BLOCK, 0, s, a);
 }
 
 // Blocks per SM of the ring form: what their registers allow.  A row costs a
@@ -495,16 +501,14 @@ cudaError_t run_ring(NormBwd a, int blocks, cudaStream_t s) {
   const cudaError_t e = ring_stages(reinterpret_cast<const void*>(norm_backward_kernel<CENTRED, T, V>), stage,
                                     ring_blocks_backward(a.C), &a.stages, set);
   if (e != cudaSuccess) return e;
-  norm_backward_kernel<CENTRED, T, V><<<blocks, T, a.stages * stage, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(norm_backward_kernel<CENTRED, T, V>, dim3(unsigned(blocks)), T, size_t(a.stages) * size_t(stage), s, a);
 }
 
 template <bool CENTRED>
 cudaError_t norm_backward(const NormBwd& a, int blocks, cudaStream_t s) {
   if (a.C <= 512) {
-    if (a.C <= 256) norm_backward_warp_kernel<CENTRED, 1><<<blocks, 256, 0, s>>>(a);
-    else norm_backward_warp_kernel<CENTRED, 2><<<blocks, 256, 0, s>>>(a);
-    return cudaGetLastError();
+    if (a.C <= 256) return launch_pdl(norm_backward_warp_kernel<CENTRED, 1>, dim3(unsigned(blocks)), 256, 0, s, a);
+    return launch_pdl(norm_backward_warp_kernel<CENTRED, 2>, dim3(unsigned(blocks)), 256, 0, s, a);
   }
   if (a.C <= 1024) return run_ring<CENTRED, 128, 1>(a, blocks, s);
   if (a.C <= 2048) return run_ring<CENTRED, 256, 1>(a, blocks, s);
@@ -559,16 +563,8 @@ cudaError_t launch_layernorm(uint16_t* res_out, uint16_t* y, float* mean, float*
 cudaError_t launch_column_sum(float* out0, float* out1, const float* partial, int parts, int64_t cols0, int64_t cols,
                               bool accumulate, cudaStream_t s) {
   if (cols == 0) return cudaSuccess;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((cols + 31) / 32));
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, column_sum_kernel, out0, out1, partial, parts, cols0, cols, accumulate ? 1 : 0);
+  return launch_pdl(column_sum_kernel, dim3(unsigned((cols + 31) / 32)), 1024, 0, s, out0, out1, partial, parts, cols0,
+                    cols, accumulate ? 1 : 0);
 }
 
 cudaError_t launch_norm_backward(uint16_t* dx, float* dgain, float* dshift, float* stats, const uint16_t* dy,

@@ -146,8 +146,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 32 : 16) / WARPS) skinn
 
 template <bool FP8, bool GATED, int NT, int WARPS>
 cudaError_t launch(const SkinnyArgs& a, unsigned tiles, cudaStream_t s) {
-  skinny_kernel<FP8, GATED, NT, WARPS><<<tiles, WARPS * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(skinny_kernel<FP8, GATED, NT, WARPS>, dim3(tiles), WARPS * 32, 0, s, a);
 }
 
 template <bool FP8, bool GATED>
