@@ -12,9 +12,24 @@ namespace qffn {
 
 constexpr int ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4;
 
+// 2^v and 1/v, the hardware approximations (two and one units in the last
+// place) with denormals flushed: __expf and __fdividef wrap the same
+// instructions in range handling that these arguments do not need.
+QFFN_DEVI float exp2_f32(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+QFFN_DEVI float rcp_f32(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
 QFFN_DEVI float sigmoid_f32(float v) {
-  const float e = __expf(-fabsf(v));
-  const float r = __fdividef(1.0f, 1.0f + e);
+  const float e = exp2_f32(-kLog2e * fabsf(v));
+  const float r = rcp_f32(1.0f + e);
   return v >= 0.0f ? r : e * r;
 }
 
@@ -30,7 +45,7 @@ constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 // exp(-z^2 / 2) for the density.
 QFFN_DEVI float normal_cdf_f32(float z, float& gauss) {
   const float a = fabsf(z);
-  const float t = __fdividef(1.0f, fmaf(0.35f, a, 1.0f));
+  const float t = rcp_f32(fmaf(0.35f, a, 1.0f));
   float r = 0.0489424504339695f;
   r = fmaf(r, t, -0.20211930572986603f);
   r = fmaf(r, t, 0.24064083397388458f);
@@ -39,7 +54,7 @@ QFFN_DEVI float normal_cdf_f32(float z, float& gauss) {
   r = fmaf(r, t, 0.13335509598255157f);
   r = fmaf(r, t, 0.14027033746242523f);
   r = fmaf(r, t, -2.7315563784213737e-05f);
-  gauss = __expf(-0.5f * a * a);
+  gauss = exp2_f32(-0.5f * kLog2e * a * a);
   const float tail = gauss * r;
   return z < 0.0f ? tail : 1.0f - tail;
 }
@@ -90,13 +105,11 @@ QFFN_DEVI uint64_t f2_dup(float v) { return f2_pack(v, v); }
 QFFN_DEVI uint64_t f2_abs(uint64_t v) { return v & 0x7FFFFFFF7FFFFFFFull; }
 
 QFFN_DEVI uint64_t sigmoid_f2(uint64_t v) {
-  float a, b, ea, eb, da, db;
+  float a, b, da, db;
   f2_unpack(v, a, b);
-  ea = __expf(-fabsf(a));
-  eb = __expf(-fabsf(b));
-  const uint64_t e = f2_pack(ea, eb);
+  const uint64_t e = f2_pack(exp2_f32(-kLog2e * fabsf(a)), exp2_f32(-kLog2e * fabsf(b)));
   f2_unpack(f2_add(f2_dup(1.0f), e), da, db);
-  const float ra = __fdividef(1.0f, da), rb = __fdividef(1.0f, db);
+  const float ra = rcp_f32(da), rb = rcp_f32(db);
   float la, lb;
   f2_unpack(f2_mul(e, f2_pack(ra, rb)), la, lb);
   return f2_pack(a >= 0.0f ? ra : la, b >= 0.0f ? rb : lb);
@@ -106,7 +119,7 @@ QFFN_DEVI uint64_t normal_cdf_f2(uint64_t z, uint64_t& gauss) {
   const uint64_t a = f2_abs(z);
   float d0, d1, z0, z1;
   f2_unpack(f2_fma(f2_dup(0.35f), a, f2_dup(1.0f)), d0, d1);
-  const uint64_t t = f2_pack(__fdividef(1.0f, d0), __fdividef(1.0f, d1));
+  const uint64_t t = f2_pack(rcp_f32(d0), rcp_f32(d1));
   uint64_t r = f2_dup(0.0489424504339695f);
   r = f2_fma(r, t, f2_dup(-0.20211930572986603f));
   r = f2_fma(r, t, f2_dup(0.24064083397388458f));
@@ -116,8 +129,8 @@ QFFN_DEVI uint64_t normal_cdf_f2(uint64_t z, uint64_t& gauss) {
   r = f2_fma(r, t, f2_dup(0.14027033746242523f));
   r = f2_fma(r, t, f2_dup(-2.7315563784213737e-05f));
   float q0, q1, t0, t1, c0, c1;
-  f2_unpack(f2_mul(f2_mul(f2_dup(-0.5f), a), a), q0, q1);
-  gauss = f2_pack(__expf(q0), __expf(q1));
+  f2_unpack(f2_mul(f2_mul(f2_dup(-0.5f * kLog2e), a), a), q0, q1);
+  gauss = f2_pack(exp2_f32(q0), exp2_f32(q1));
   const uint64_t tail = f2_mul(gauss, r);
   f2_unpack(tail, t0, t1);
   f2_unpack(f2_sub(f2_dup(1.0f), tail), c0, c1);

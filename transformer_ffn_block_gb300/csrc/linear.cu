@@ -55,9 +55,9 @@ constexpr int STEPS = 8;                   // MMAs per stage (32 bytes of K each
 constexpr int EPI_WARPS = 8;
 constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 2 * BN;
-constexpr int NUM_BARS = 2 * STAGES + 5 + 2 * EPI_WARPS;
-constexpr int STAGE_BOX_BYTES = 32 * 64;   // epilogue staging box: 32 rows x 64 bytes
-constexpr int STAGING_BYTES = EPI_WARPS * 2 * STAGE_BOX_BYTES;
+constexpr int NUM_BARS = 2 * STAGES + 5;
+constexpr int STAGING_BOX = 32 * 128;      // a warp's transposing box: 32 rows x 32 fp32
+constexpr int STAGING_BYTES = EPI_WARPS * STAGING_BOX;
 constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 + NUM_BARS * 8 + 16;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
 constexpr int GROUP_M = 8;
@@ -94,16 +94,17 @@ __device__ unsigned int g_status;
 struct LinArgs {
   const float* a_scale;     // E4M3 operands: one float each; NULL: no scaling
   const float* w_scale;
+  uint16_t* out;            // [M, N] (GATED_BWD: [M, 2N])
+  uint16_t* z;              // EPI_LINEAR, optional
   const uint16_t* bias;     // EPI_LINEAR, optional
-  int has_in;               // EPI_LINEAR: add the bf16 tensor of the input map
-  int save_z;               // EPI_LINEAR: store z by the second output map
+  const uint16_t* in;       // [M, N]: EPI_LINEAR residual or previous output (optional), GATED_BWD dh
   int M, N;                 // output rows and columns (gated: columns = H)
   int up_row;               // gated: first up row of W1 (= H)
   int tiles_m, tiles_n, num_units, num_kb;
   int band_n;               // N-blocks per raster band
   int split_from;           // units from here on are 128-column halves of the last tiles
   int splits, kb_per_split, m_pad;   // EPI_PARTIAL*
-  float* partial;           // EPI_PARTIAL_T: [splits][m_pad][M], m_pad activation rows; N of them are stored
+  float* partial;           // EPI_PARTIAL: [splits][m_pad][N]; EPI_PARTIAL_T: [splits][m_pad][M], N rows stored
   int bn;                   // EPI_PARTIAL_T: activation rows per tile (multiple of 32); else 256
 };
 
@@ -178,15 +179,11 @@ QFFN_DEVI Unit unit_coords(int u, const LinArgs& a) {
   return r;
 }
 
-// tmO / tmZ: first and second output (EPI_LINEAR: out, z; GATED_BWD: dg, du);
-// tmI: tensor read in the epilogue (EPI_LINEAR: residual or previous output;
-// GATED_BWD: dh); tmBh: B with 64-row boxes for the half tiles.
+// tmBh: B with 64-row boxes for the half tiles.
 template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                  const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmO,
-                  const __grid_constant__ CUtensorMap tmZ, const __grid_constant__ CUtensorMap tmI,
-                  const LinArgs args) {
+                  const __grid_constant__ CUtensorMap tmBh, const LinArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -198,14 +195,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t bar0 = smem_u32(bars);
   // full[s] (leader): both CTAs' loads of stage s landed; empty[s]: the MMAs
   // reading stage s are done; tfull[a]: accumulator a is complete; tempty[a]
-  // (leader): both CTAs' epilogue warps have read it; drain: all MMAs done;
-  // ld[w][b]: the TMA load into staging box b of epilogue warp w has landed
+  // (leader): both CTAs' epilogue warps have read it; drain: all MMAs done
   auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
   auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(STAGES + s); };
   auto tfull_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * STAGES + a); };
   auto tempty_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * STAGES + 2 + a); };
   const uint32_t drain_bar = bar0 + 8u * uint32_t(2 * STAGES + 4);
-  auto ld_bar = [&](int w, int b) { return bar0 + 8u * uint32_t(2 * STAGES + 5 + 2 * w + b); };
 
   constexpr bool GATED = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -222,17 +217,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(tempty_bar(a), 2 * EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
-    for (int w = 0; w < EPI_WARPS; ++w) {
-      mbar_init(ld_bar(w, 0), 1);
-      mbar_init(ld_bar(w, 1), 1);
-    }
     *abort_flag = 0;
     mbar_init_fence();
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
-    if (EPI != EPI_PARTIAL_T) tma_prefetch_desc(&tmO);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -338,129 +328,142 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
   } else {
     // -------------------------------------------------------------- epilogue
-    // Eight warps: two per TMEM lane quarter q (rows 32 q .. 32 q + 31 of the
-    // CTA's 128), which take the unit's groups of 32 output columns in turn.
-    const int q = warp & 3;
-    const int wg = (warp - 2) >> 2;          // 0: even groups, 1: odd groups
-    const int ew = q * 2 + wg;               // epilogue warp index of the staging boxes and barriers
+    // EPI_WARPS / 4 warps per TMEM lane quarter q (rows 32 q .. 32 q + 31 of
+    // the CTA's 128), which take the unit's groups of 32 output columns in turn.
+    // A TMEM load gives a lane one row's 32 columns; a warp's box of shared
+    // memory turns that into the layout of the global accesses, lane l with 8
+    // columns (8 (l & 3) ..) of the rows (l >> 2) + 8 i, so that every load and
+    // store of 16 bytes per lane covers eight rows of 64 contiguous bytes
+    // (partial sums: 128).  Both directions use the box without bank conflicts.
+    constexpr int WG = EPI_WARPS / 4;
+    const int q = warp & 3, wg = (warp - 2) >> 2;
     const float scale = args.a_scale != nullptr ? args.a_scale[0] * args.w_scale[0] : 1.0f;
-    uint8_t* const box0 = sStaging + ew * 2 * STAGE_BOX_BYTES;
-    auto box = [&](int b) { return box0 + b * STAGE_BOX_BYTES; };
-    // 16-byte chunk c of this lane's 64-byte row in a 64-byte-swizzled box
-    auto chunk_off = [&](int c) { return uint32_t(lane) * 64u + (uint32_t(c ^ ((lane >> 1) & 3)) << 4); };
-    // Two ways to use the warp's two staging boxes (32 rows x 32 bf16 columns):
-    //  alternating: successive groups go out of the two boxes in turn; with an
-    //    input tensor (an even number of groups per warp and unit, the first in
-    //    box 0) a box is filled by a TMA load first, the next group's load in
-    //    flight while a group is summed, and the result replaces it in place
-    //  paired (two outputs): box 0 holds the input and then the first output,
-    //    box 1 the second output
-    const bool paired = EPI == EPI_GATED_BWD || (EPI == EPI_LINEAR && args.save_z != 0);
-    const bool has_in = EPI == EPI_GATED_BWD || (EPI == EPI_LINEAR && args.has_in != 0);
-    uint32_t ld_par = 0u;                    // bit b: parity of the next load into box b
-    uint32_t ld_pending = 0u;                // lane 0, bit b: a load has been issued and not waited for
-    int flip = 0;
-    auto first_col = [&](const Unit& u) {    // output column of the unit's group 0
-      return GATED ? u.nb * 128 + (u.half < 0 ? 0 : u.half * 64) : u.nb * BN + (u.half < 0 ? 0 : u.half * 128);
-    };
-    auto first_row = [&](const Unit& u) { return u.mb * (2 * BM) + int(rank) * BM + q * 32; };
-    auto load_in = [&](const Unit& u, int g, int b) {   // lane 0
-      mbar_expect_tx(ld_bar(ew, b), STAGE_BOX_BYTES);
-      tma_load_2d(smem_u32(box(b)), &tmI, ld_bar(ew, b), first_col(u) + g * 32, first_row(u));
-      ld_pending |= 1u << b;
-    };
-    if (has_in && lane == 0 && pair < args.num_units) load_in(unit_coords<EPI>(pair, args), wg, 0);
+    uint8_t* const box = sStaging + (q * WG + wg) * STAGING_BOX;
+    // 16-byte chunk c of a row of 32 fp32 (128 bytes) or of 32 bf16 (64 bytes)
+    auto off32 = [](int row, int c) { return uint32_t(row) * 128u + (uint32_t(c ^ (row & 7)) << 4); };
+    auto off16 = [](int row, int c) { return uint32_t(row) * 64u + (uint32_t(c ^ ((row >> 1) & 3)) << 4); };
+    const int sub = lane >> 2, ch = lane & 3;
     int local = 0;
     for (int un = pair; un < args.num_units; un += num_pairs, ++local) {
       const int acc = local & 1;
       const uint32_t aph = uint32_t(local >> 1) & 1u;
-      if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) break;
-      tc_fence_after();
       const Unit u = unit_coords<EPI>(un, args);
-      const int row0 = first_row(u);
+      const int row0 = u.mb * (2 * BM) + int(rank) * BM + q * 32;
+      // output column of the unit's group 0
+      const int first_col = GATED ? u.nb * 128 + (u.half < 0 ? 0 : u.half * 64)
+                                  : u.nb * BN + (u.half < 0 ? 0 : u.half * 128);
       const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * BN);
       const int acc_cols = EPI == EPI_PARTIAL_T ? args.bn : u.half < 0 ? BN : BN / 2;
-      // groups of 32 output columns (partial sums: 32 fp32 columns, in both boxes)
       const int groups = GATED ? acc_cols / 64 : acc_cols / 32;
-      bool ok = true;
-      for (int g = wg; g < groups; g += 2) {
+      // this lane's output rows and column of the group at hand
+      auto row_of = [&](int i) { return row0 + sub + 8 * i; };
+      if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) break;
+      tc_fence_after();
+      // after this warp's last load of the accumulator: hand it back
+      auto loaded = [&](int g) {
+        if (g + WG >= groups) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(map_to_rank(tempty_bar(acc), 0));
+        }
+      };
+      if (wg >= groups) loaded(wg);          // (a narrow tile has fewer groups than warps)
+      for (int g = wg; g < groups; g += WG) {
+        const int col0 = first_col + g * 32, col = col0 + ch * 8;
         if (EPI == EPI_PARTIAL_T) {
           // lanes hold weight rows, columns are activation rows: a warp's store
           // of one column is 128 contiguous bytes of that activation row
           uint32_t v[32];
           tmem_ld32(tbase + uint32_t(g * 32), v);
+          loaded(g);
           const int n = row0 + lane, m0 = u.nb * args.bn + g * 32;
+          const int rows = min(32, args.N - m0);
+          float* dst = args.partial + (size_t(u.sp) * size_t(args.m_pad) + size_t(m0)) * size_t(args.M) + size_t(n);
           if (n < args.M) {
-            float* dst = args.partial + (size_t(u.sp) * size_t(args.m_pad) + size_t(m0)) * size_t(args.M) + size_t(n);
+            if (rows == 32) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (m0 + j < args.N) dst[size_t(j) * size_t(args.M)] = __uint_as_float(v[j]);
-          }
-          continue;
-        }
-        const int b = paired || EPI == EPI_PARTIAL ? 0 : flip;
-        flip ^= 1;
-        if (has_in) {
-          if (!paired && g + 2 < groups) {
-            if (lane == 0) {
-              bulk_wait_read_0();            // the store that last read the other box is done
-              load_in(u, g + 2, b ^ 1);
+              for (int j = 0; j < 32; ++j) dst[size_t(j) * size_t(args.M)] = __uint_as_float(v[j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j < rows) dst[size_t(j) * size_t(args.M)] = __uint_as_float(v[j]);
             }
+          }
+        } else if (!GATED) {
+          uint4 bias4 = make_uint4(0, 0, 0, 0), in4[4];
+          const bool col_ok = col < args.N;
+          if (EPI == EPI_LINEAR) {
+            if (args.bias != nullptr && col_ok) bias4 = ld16_ro(args.bias + col);
+            if (args.in != nullptr) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                in4[i] = make_uint4(0, 0, 0, 0);
+                if (col_ok && row_of(i) < args.M)
+                  in4[i] = ld16_once(args.in + size_t(row_of(i)) * size_t(args.N) + size_t(col));
+              }
+            }
+          }
+          {
+            uint32_t v[32];
+            tmem_ld32(tbase + uint32_t(g * 32), v);
+            loaded(g);
+            __syncwarp();                    // the previous group has been read out of the box
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              *reinterpret_cast<uint4*>(box + off32(lane, c)) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
             __syncwarp();
           }
-          if (!mbar_wait(ld_bar(ew, b), (ld_par >> b) & 1u, abort_flag)) { ok = false; break; }
-          ld_par ^= 1u << b;
-          ld_pending &= ~(1u << b);
-        } else {
-          if (lane == 0) {
-            if (paired || EPI == EPI_PARTIAL) bulk_wait_read_0();
-            else bulk_wait_read_1();
-          }
-          __syncwarp();
-        }
-        const int col0 = first_col(u) + g * 32;
-        if (EPI == EPI_PARTIAL) {
-          uint32_t v[32];
-          tmem_ld32(tbase + uint32_t(g * 32), v);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(box(k >> 2) + chunk_off(k & 3)) =
-                make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        } else if (!GATED) {
-          uint4 bias[4];
-          if (args.bias != nullptr) {
+          for (int i = 0; i < 4; ++i) {
+            const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(box + off32(sub + 8 * i, 2 * ch));
+            const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(box + off32(sub + 8 * i, 2 * ch + 1));
+            const bool live = col_ok && row_of(i) < args.M;
+            if (EPI == EPI_PARTIAL) {
+              float* dst = args.partial + (size_t(u.sp) * size_t(args.m_pad) + size_t(row_of(i))) * size_t(args.N) + size_t(col);
+              if (live) {
+                reinterpret_cast<ulonglong2*>(dst)[0] = lo;
+                reinterpret_cast<ulonglong2*>(dst)[1] = hi;
+              }
+            } else {
+              uint64_t z[4] = {lo.x, lo.y, hi.x, hi.y};
+              const uint32_t bw[4] = {bias4.x, bias4.y, bias4.z, bias4.w};
+              const size_t o = size_t(row_of(i)) * size_t(args.N) + size_t(col);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              bias[k] = col0 + 8 * k < args.N ? ld16_ro(args.bias + col0 + 8 * k) : make_uint4(0, 0, 0, 0);
-          }
-          uint32_t v[32];
-          tmem_ld32(tbase + uint32_t(g * 32), v);
+              for (int j = 0; j < 4; ++j) {
+                if (OP == OP_E4M3) z[j] = f2_mul(z[j], f2_dup(scale));
+                z[j] = f2_add(z[j], bf16x2_to_f2(bw[j]));
+              }
+              if (args.z != nullptr && live) stg16(args.z + o, pack8(z));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t off = chunk_off(k);
-            uint64_t z[4];
+              for (int j = 0; j < 4; ++j) z[j] = act_f2<ACT>(z[j]);
+              if (args.in != nullptr) {
+                const uint32_t iw[4] = {in4[i].x, in4[i].y, in4[i].z, in4[i].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              z[j] = f2_pack(__uint_as_float(v[8 * k + 2 * j]), __uint_as_float(v[8 * k + 2 * j + 1]));
-              if (OP == OP_E4M3) z[j] = f2_mul(z[j], f2_dup(scale));
+                for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bf16x2_to_f2(iw[j]));
+              }
+              if (live) stg16(args.out + o, pack8(z));
             }
-            if (args.bias != nullptr) {
-              const uint32_t bw[4] = {bias[k].x, bias[k].y, bias[k].z, bias[k].w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bf16x2_to_f2(bw[j]));
-            }
-            if (args.save_z) *reinterpret_cast<uint4*>(box(1) + off) = pack8(z);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] = act_f2<ACT>(z[j]);
-            if (args.has_in) {
-              const uint4 o4 = *reinterpret_cast<const uint4*>(box(b) + off);
-              const uint32_t ow[4] = {o4.x, o4.y, o4.z, o4.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bf16x2_to_f2(ow[j]));
-            }
-            *reinterpret_cast<uint4*>(box(b) + off) = pack8(z);
           }
         } else {
+          const bool col_ok = col < args.N;
+          const size_t ld = EPI == EPI_GATED_BWD ? 2 * size_t(args.N) : size_t(args.N);
+          if (EPI == EPI_GATED_BWD) {
+            // dh into the box, read back row by row below
+            uint4 d4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              d4[i] = make_uint4(0, 0, 0, 0);
+              if (col_ok && row_of(i) < args.M) d4[i] = ld16_ro(args.in + size_t(row_of(i)) * size_t(args.N) + size_t(col));
+            }
+            __syncwarp();                    // the previous group has been read out of the box
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(box + off16(sub + 8 * i, ch)) = d4[i];
+            __syncwarp();
+          } else {
+            __syncwarp();
+          }
+          // second bf16 box (du) behind the first
+          uint8_t* const box2 = box + 32 * 64;
           const int up_off = acc_cols / 2;   // accumulator column of u
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
@@ -468,12 +471,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             uint32_t gv[16], uv[16];
             tmem_ld16x2_issue(tbase + c, tbase + uint32_t(up_off) + c, gv, uv);
             tmem_wait_ld16(gv, uv);
+            if (h == 1) loaded(g);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const uint32_t off = chunk_off(h * 2 + k);
               uint32_t p[4], p2[4];
               uint4 d4 = make_uint4(0, 0, 0, 0);
-              if (EPI == EPI_GATED_BWD) d4 = *reinterpret_cast<const uint4*>(box0 + off);
+              if (EPI == EPI_GATED_BWD) d4 = *reinterpret_cast<const uint4*>(box + off16(lane, h * 2 + k));
               const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
@@ -489,46 +492,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                   p2[j] = pack2(f2_mul(d, f));
                 }
               }
-              *reinterpret_cast<uint4*>(box(b) + off) = make_uint4(p[0], p[1], p[2], p[3]);
+              *reinterpret_cast<uint4*>(box + off16(lane, h * 2 + k)) = make_uint4(p[0], p[1], p[2], p[3]);
               if (EPI == EPI_GATED_BWD)
-                *reinterpret_cast<uint4*>(box(1) + off) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+                *reinterpret_cast<uint4*>(box2 + off16(lane, h * 2 + k)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
             }
           }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          // rows beyond M and columns beyond N are clipped by the tensor maps
-          if (row0 < args.M && col0 < args.N) {
-            if (EPI == EPI_PARTIAL) {
-              // rows are padded per part of K to whole boxes
-              tma_store_2d(&tmO, smem_u32(box(0)), col0, u.sp * args.m_pad + row0);
-              if (col0 + 16 < args.N) tma_store_2d(&tmO, smem_u32(box(1)), col0 + 16, u.sp * args.m_pad + row0);
-            } else {
-              tma_store_2d(&tmO, smem_u32(box(b)), col0, row0);
-              if (paired) tma_store_2d(&tmZ, smem_u32(box(1)), col0, row0);
-            }
-          }
-          bulk_commit();
-          if (has_in && (paired || g + 2 >= groups)) {
-            // the next load into box 0: of this unit (paired) or of the next one
-            bulk_wait_read_0();
-            if (g + 2 < groups) load_in(u, g + 2, 0);
-            else if (un + num_pairs < args.num_units) load_in(unit_coords<EPI>(un + num_pairs, args), wg, 0);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (!col_ok || row_of(i) >= args.M) continue;
+            uint16_t* dst = args.out + size_t(row_of(i)) * ld + size_t(col);
+            stg16(dst, *reinterpret_cast<const uint4*>(box + off16(sub + 8 * i, ch)));
+            if (EPI == EPI_GATED_BWD)
+              stg16(dst + args.N, *reinterpret_cast<const uint4*>(box2 + off16(sub + 8 * i, ch)));
           }
         }
-        __syncwarp();
       }
-      if (!ok) break;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(map_to_rank(tempty_bar(acc), 0));
-    }
-    // stores complete, and no load into shared memory is in flight, before exit
-    if (lane == 0) {
-      bulk_wait_all();
-      for (int b = 0; b < 2; ++b)
-        if ((ld_pending >> b) & 1u) mbar_wait(ld_bar(ew, b), (ld_par >> b) & 1u, abort_flag, false, kDrainLimitNs);
     }
   }
 
@@ -700,33 +679,27 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Tensor map of [rows, cols] (cols contiguous, rows `ld` elements apart) with
-// boxes of box_rows rows x box_bytes (64 or 128) in the swizzle of that width;
-// zeros outside.
+// Tensor map of the matrix [rows, cols] (cols contiguous) with
+// boxes of box_rows rows x 128 bytes, 128-byte swizzle; zeros outside.
 bool make_map(CUtensorMap* map, CUtensorMapDataType type, int elem, const void* ptr, int64_t rows, int64_t cols,
-              int64_t ld, int box_rows, int box_bytes, CUtensorMapL2promotion promo) {
+              int box_rows) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
-  cuuint64_t strides[1] = {cuuint64_t(ld) * cuuint64_t(elem)};
-  cuuint32_t box[2] = {cuuint32_t(box_bytes / elem), cuuint32_t(box_rows)};
+  cuuint64_t strides[1] = {cuuint64_t(cols) * cuuint64_t(elem)};
+  cuuint32_t box[2] = {cuuint32_t(ROW_BYTES / elem), cuuint32_t(box_rows)};
   cuuint32_t estr[2] = {1u, 1u};
   return fn(map, type, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, promo,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
 }
 // An MMA operand: [rows, k] K-major or, `mn`, [k, rows] as it lies in memory.
 template <int OP>
 bool operand_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t k, bool mn, int box_rows = 128) {
   const CUtensorMapDataType t = OP == OP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  return mn ? make_map(map, t, OP == OP_BF16 ? 2 : 1, ptr, k, rows, rows, box_rows, 128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B)
-            : make_map(map, t, OP == OP_BF16 ? 2 : 1, ptr, rows, k, k, box_rows, 128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+  return mn ? make_map(map, t, OP == OP_BF16 ? 2 : 1, ptr, k, rows, box_rows)
+            : make_map(map, t, OP == OP_BF16 ? 2 : 1, ptr, rows, k, box_rows);
 }
-// A bf16 tensor the epilogue stores or loads in boxes of 32 rows x 32 columns.
-bool epi_map(CUtensorMap* map, const uint16_t* ptr, int64_t rows, int64_t cols, int64_t ld) {
-  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, rows, cols, ld, 32, 64, CU_TENSOR_MAP_L2_PROMOTION_NONE);
-}
-
 // 2-CTA clusters of a form that fit on the device at once (cached per device).
 template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
 cudaError_t max_pairs(int* pairs) {
@@ -762,7 +735,7 @@ cudaError_t max_pairs(int* pairs) {
 }
 
 struct Maps {
-  CUtensorMap a, b, bh, o, z, i;
+  CUtensorMap a, b, bh;
 };
 
 template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
@@ -781,7 +754,7 @@ cudaError_t launch(const Maps& m, const LinArgs& a, int pairs, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<OP, EPI, ACT, A_MN, B_MN>, m.a, m.b, m.bh, m.o, m.z, m.i, a);
+  return cudaLaunchKernelEx(&cfg, linear_kernel<OP, EPI, ACT, A_MN, B_MN>, m.a, m.b, m.bh, a);
 }
 
 // How a product [M, K] x [N, K]^T is cut: the tiles, their orientation, and the
@@ -877,7 +850,7 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
       Maps t;
       if (!operand_map<OP>(&t.a, B, brows, K, B_MN) || !operand_map<OP>(&t.b, A, M, K, false, p.bn / 2))
         return cudaErrorInvalidValue;
-      t.bh = t.o = t.z = t.i = t.b;
+      t.bh = t.b;
       a.M = int(brows);
       a.N = int(M);
       a.tiles_n = a.band_n = p.tiles_n;
@@ -892,10 +865,7 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
     }
   }
   if (p.splits > 1) {
-    if (!make_map(&m.o, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, partial, p.splits * p.m_pad, brows, brows, 32,
-                  64, CU_TENSOR_MAP_L2_PROMOTION_NONE))
-      return cudaErrorInvalidValue;
-    m.z = m.i = m.o;
+    a.partial = partial;
     a.N = int(brows);
     a.tiles_n = p.tiles_n;
     a.band_n = p.tiles_n;
@@ -911,25 +881,16 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
   a.a_scale = a_scale;
   a.w_scale = w_scale;
   a.bias = bias;
-  a.has_in = in != nullptr;
-  a.save_z = z != nullptr;
+  a.out = out;
+  a.z = z;
+  a.in = in;
   a.tiles_n = GATED ? int((N + 127) / 128) : p.tiles_n;
   a.band_n = band_blocks(a.tiles_n, M, brows, K * (OP == OP_BF16 ? 2 : 1));
   a.num_units = a.split_from = a.tiles_m * a.tiles_n;
-  if (EPI == EPI_GATED_BWD) {
-    // the halves of d_gu [M, 2H] as two tensors, so that a box ending beyond H is clipped there
-    if (!epi_map(&m.o, out, M, N, 2 * N) || !epi_map(&m.z, out + N, M, N, 2 * N) || !epi_map(&m.i, in, M, N, N))
-      return cudaErrorInvalidValue;
-  } else {
-    if (!epi_map(&m.o, out, M, N, N)) return cudaErrorInvalidValue;
-    m.z = m.i = m.o;
-    if (z != nullptr && !epi_map(&m.z, z, M, N, N)) return cudaErrorInvalidValue;
-    if (in != nullptr && !epi_map(&m.i, in, M, N, N)) return cudaErrorInvalidValue;
-  }
   if ((e = max_pairs<OP, EPI, ACT, A_MN, B_MN>(&pairs)) != cudaSuccess) return e;
   // a last partial wave of R <= pairs / 2 tiles runs as 2 R half tiles in half the time
   const int r = a.num_units % pairs;
-  if (EPI != EPI_GATED_BWD && a.num_units > pairs && r > 0 && 2 * r <= pairs) {
+  if (a.num_units > pairs && r > 0 && 2 * r <= pairs) {
     if (!B_MN && !operand_map<OP>(&m.bh, B, brows, K, false, 64)) return cudaErrorInvalidValue;
     a.split_from = a.num_units - r;
     a.num_units += r;

@@ -34,7 +34,7 @@ struct SkinnyArgs {
   const float* w_scale;
   const uint16_t* bias;
   const uint16_t* res;
-  int act, M, N;             // N: output columns (gated: H)
+  int act, M, N;             // N: output columns (gated: H); block (i, j) takes rows 8 NT j .. of x
   int64_t row_bytes;         // of one row of w and of x
 };
 
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 32 : 16) / WARPS) skinn
   __shared__ float red[WARPS][16][TOK + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int r0 = blockIdx.x * (GATED ? 8 : 16);
+  const int r0 = blockIdx.x * (GATED ? 8 : 16), m0 = blockIdx.y * TOK;
   // this lane's two weight rows; a row beyond the last is read as the last and dropped
   const int64_t ra = GATED ? r0 + g : min(r0 + g, a.N - 1);
   const int64_t rb = GATED ? int64_t(a.N) + r0 + g : min(r0 + g + 8, a.N - 1);
@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 32 : 16) / WARPS) skinn
   bool xl[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    xl[n] = n * 8 + g < a.M;
-    xp[n] = a.x + int64_t(xl[n] ? n * 8 + g : 0) * a.row_bytes + t * 16;
+    xl[n] = m0 + n * 8 + g < a.M;
+    xp[n] = a.x + int64_t(xl[n] ? m0 + n * 8 + g : 0) * a.row_bytes + t * 16;
   }
   float c[NT][4];
 #pragma unroll
@@ -122,13 +122,13 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 32 : 16) / WARPS) skinn
   const float scale = FP8 ? a.x_scale[0] * a.w_scale[0] : 1.0f;
   constexpr int ROWS = GATED ? 8 : 16;
   for (int i = threadIdx.x; i < ROWS * TOK; i += WARPS * 32) {
-    const int r = i % ROWS, m = i / ROWS;
+    const int r = i % ROWS, mt = i / ROWS, m = m0 + mt;
     if (m >= a.M || r0 + r >= a.N) continue;
     float v = 0.0f, u = 0.0f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      v += red[w][r][m];
-      if (GATED) u += red[w][r + 8][m];
+      v += red[w][r][mt];
+      if (GATED) u += red[w][r + 8][mt];
     }
     const size_t o = size_t(m) * size_t(a.N) + size_t(r0 + r);
     if (GATED) {
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 32 : 16) / WARPS) skinn
 
 template <bool FP8, bool GATED, int NT, int WARPS>
 cudaError_t launch(const SkinnyArgs& a, unsigned tiles, cudaStream_t s) {
-  return launch_pdl(skinny_kernel<FP8, GATED, NT, WARPS>, dim3(tiles), WARPS * 32, 0, s, a);
+  return launch_pdl(skinny_kernel<FP8, GATED, NT, WARPS>, dim3(tiles, unsigned((a.M + 8 * NT - 1) / (8 * NT))), WARPS * 32, 0, s, a);
 }
 
 template <bool FP8, bool GATED>
