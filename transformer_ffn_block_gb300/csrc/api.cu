@@ -180,12 +180,13 @@ int qffn_abi_version(void) { return kAbiVersion; }
 
 qffn_status qffn_check_status(qffn_stream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return QFFN_ERR_CUDA;
-  unsigned int st = 0, sd = 0, sl = 0, sn = 0;
+  unsigned int st = 0, sd = 0, sl = 0, sf = 0, sn = 0;
   if (qffn::gemm_take_status(&st) != cudaSuccess) return QFFN_ERR_CUDA;
   if (qffn::decode_take_status(&sd) != cudaSuccess) return QFFN_ERR_CUDA;
   if (qffn::linear_take_status(&sl) != cudaSuccess) return QFFN_ERR_CUDA;
+  if (qffn::few_rows_take_status(&sf) != cudaSuccess) return QFFN_ERR_CUDA;
   if (qffn::norm_take_status(&sn) != cudaSuccess) return QFFN_ERR_CUDA;
-  return (st | sd | sl | sn) != 0 ? QFFN_ERR_TIMEOUT : QFFN_OK;
+  return (st | sd | sl | sf | sn) != 0 ? QFFN_ERR_TIMEOUT : QFFN_OK;
 }
 
 qffn_status qffn_gemm_clock_sample(uint64_t* out, qffn_stream_t stream) {

@@ -9,10 +9,6 @@
 //                  recomputed g, u and dh [M,H] read in the epilogue
 //   EPI_PARTIAL    fp32 sums over one part of K, joined by join_kernel, which
 //                  then applies one of the epilogues above
-//   EPI_PARTIAL_T  the same with the weights as the 256-row operand and up to
-//                  256 activation rows as the other: for few rows, where the
-//                  weights' bytes bound the call and a 256-row tile of
-//                  activations would be mostly padding
 //
 // The matmul and the epilogues of a transformer block's feed-forward half
 // (llmq "llama_model.cpp", LLamaModel::_forward_block and _backward_block) in
@@ -32,12 +28,12 @@
 // Every mbarrier wait is bounded; see gemm_fp8.cu for how a wait that runs out
 // ends the kernel (abort flag, status word, drained copies and MMAs).
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include "act.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "pipeline.cuh"
+#include "tensor_map.h"
 #include "umma.cuh"
 
 namespace qffn {
@@ -71,8 +67,7 @@ constexpr int OP_BF16 = 0, OP_E4M3 = 1;
 constexpr int box_k(int op) { return op == OP_BF16 ? 64 : 128; }
 constexpr int stage_k(int op) { return KBOX * box_k(op); }
 
-constexpr int EPI_LINEAR = 0, EPI_GATED = 1, EPI_GATED_BWD = 2, EPI_PARTIAL = 3, EPI_PARTIAL_T = 4;
-constexpr bool is_partial(int epi) { return epi == EPI_PARTIAL || epi == EPI_PARTIAL_T; }
+constexpr int EPI_LINEAR = 0, EPI_GATED = 1, EPI_GATED_BWD = 2, EPI_PARTIAL = 3;
 
 // Instruction descriptor: D fp32 (bits 4-5 = 1); A and B formats at bits 7-9
 // and 10-12 (kind::f16: 1 = bf16; kind::f8f6f4: 0 = E4M3); bits 15 / 16: A / B
@@ -103,9 +98,8 @@ struct LinArgs {
   int tiles_m, tiles_n, num_units, num_kb;
   int band_n;               // N-blocks per raster band
   int split_from;           // units from here on are 128-column halves of the last tiles
-  int splits, kb_per_split, m_pad;   // EPI_PARTIAL*
-  float* partial;           // EPI_PARTIAL: [splits][m_pad][N]; EPI_PARTIAL_T: [splits][m_pad][M], N rows stored
-  int bn;                   // EPI_PARTIAL_T: activation rows per tile (multiple of 32); else 256
+  int splits, kb_per_split, m_pad;   // EPI_PARTIAL
+  float* partial;           // EPI_PARTIAL: [splits][m_pad][N]
 };
 
 // D(tmem, both CTAs) (+)= A(smem, both CTAs) . B(smem, both CTAs)^T
@@ -146,7 +140,7 @@ QFFN_DEVI bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag
 struct Unit {
   int mb, nb;      // pair M-block (256 rows), N-block
   int half;        // -1: whole tile; 0 / 1: first / second 128 accumulator columns of a split one
-  int sp;          // EPI_PARTIAL*: part of K
+  int sp;          // EPI_PARTIAL: part of K
 };
 
 template <int EPI>
@@ -155,7 +149,7 @@ QFFN_DEVI Unit unit_coords(int u, const LinArgs& a) {
   r.half = -1;
   r.sp = 0;
   int tile = u;
-  if (is_partial(EPI)) {
+  if (EPI == EPI_PARTIAL) {
     tile = u / a.splits;
     r.sp = u - tile * a.splits;
   } else if (u >= a.split_from) {
@@ -238,9 +232,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   pdl_trigger();
 
   // K blocks of a unit
-  auto kb_begin = [&](const Unit& u) { return is_partial(EPI) ? u.sp * args.kb_per_split : 0; };
+  auto kb_begin = [&](const Unit& u) { return EPI == EPI_PARTIAL ? u.sp * args.kb_per_split : 0; };
   auto kb_end = [&](const Unit& u) {
-    return is_partial(EPI) ? min(args.num_kb, (u.sp + 1) * args.kb_per_split) : args.num_kb;
+    return EPI == EPI_PARTIAL ? min(args.num_kb, (u.sp + 1) * args.kb_per_split) : args.num_kb;
   };
 
   if (warp == 0) {
@@ -254,12 +248,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int rowA = u.mb * (2 * BM) + int(rank) * BM;
         // this CTA's weight rows: half of the tile's 256 (of a half tile's
         // 128); gated: CTA 0 the gate rows, CTA 1 the matching up rows
-        const int rowB = EPI == EPI_PARTIAL_T ? u.nb * args.bn + int(rank) * (args.bn / 2)
-                         : GATED ? (rank == 0 ? 0 : args.up_row) + u.nb * 128 + (u.half < 0 ? 0 : u.half * 64)
+        const int rowB = GATED ? (rank == 0 ? 0 : args.up_row) + u.nb * 128 + (u.half < 0 ? 0 : u.half * 64)
                          : u.half < 0 ? u.nb * BN + int(rank) * 128
                                       : u.nb * BN + u.half * 128 + int(rank) * 64;
-        const uint32_t stage_tx = EPI == EPI_PARTIAL_T ? 2u * uint32_t(OP_BYTES + args.bn / 2 * ROW_BYTES * KBOX)
-                                  : u.half < 0 ? 2 * STAGE_BYTES : 2 * (OP_BYTES + OP_BYTES / 2);
+        const uint32_t stage_tx = u.half < 0 ? 2 * STAGE_BYTES : 2 * (OP_BYTES + OP_BYTES / 2);
         const int kb1 = kb_end(u);
         for (int kb = kb_begin(u); kb < kb1; ++kb, ++it) {
           const int s = it % STAGES;
@@ -304,8 +296,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_after();
         const Unit u = unit_coords<EPI>(un, args);
         const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
-        const uint32_t idesc = EPI == EPI_PARTIAL_T ? idesc_for(OP, A_MN, B_MN, 32) + (uint32_t(args.bn - 32) << 14)
-                               : u.half < 0 ? idesc_for(OP, A_MN, B_MN, BN) : idesc_for(OP, A_MN, B_MN, BN / 2);
+        const uint32_t idesc = u.half < 0 ? idesc_for(OP, A_MN, B_MN, BN) : idesc_for(OP, A_MN, B_MN, BN / 2);
         const int kb0 = kb_begin(u), kb1 = kb_end(u);
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = it % STAGES;
@@ -353,7 +344,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int first_col = GATED ? u.nb * 128 + (u.half < 0 ? 0 : u.half * 64)
                                   : u.nb * BN + (u.half < 0 ? 0 : u.half * 128);
       const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * BN);
-      const int acc_cols = EPI == EPI_PARTIAL_T ? args.bn : u.half < 0 ? BN : BN / 2;
+      const int acc_cols = u.half < 0 ? BN : BN / 2;
       const int groups = GATED ? acc_cols / 64 : acc_cols / 32;
       // this lane's output rows and column of the group at hand
       auto row_of = [&](int i) { return row0 + sub + 8 * i; };
@@ -367,29 +358,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (lane == 0) mbar_arrive_remote(map_to_rank(tempty_bar(acc), 0));
         }
       };
-      if (wg >= groups) loaded(wg);          // (a narrow tile has fewer groups than warps)
+      if (wg >= groups) loaded(wg);          // (a unit with fewer groups than warps)
       for (int g = wg; g < groups; g += WG) {
         const int col0 = first_col + g * 32, col = col0 + ch * 8;
-        if (EPI == EPI_PARTIAL_T) {
-          // lanes hold weight rows, columns are activation rows: a warp's store
-          // of one column is 128 contiguous bytes of that activation row
-          uint32_t v[32];
-          tmem_ld32(tbase + uint32_t(g * 32), v);
-          loaded(g);
-          const int n = row0 + lane, m0 = u.nb * args.bn + g * 32;
-          const int rows = min(32, args.N - m0);
-          float* dst = args.partial + (size_t(u.sp) * size_t(args.m_pad) + size_t(m0)) * size_t(args.M) + size_t(n);
-          if (n < args.M) {
-            if (rows == 32) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) dst[size_t(j) * size_t(args.M)] = __uint_as_float(v[j]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (j < rows) dst[size_t(j) * size_t(args.M)] = __uint_as_float(v[j]);
-            }
-          }
-        } else if (!GATED) {
+        if (!GATED) {
           uint4 bias4 = make_uint4(0, 0, 0, 0), in4[4];
           const bool col_ok = col < args.N;
           if (EPI == EPI_LINEAR) {
@@ -667,39 +639,13 @@ __global__ void __launch_bounds__(256) act_backward_kernel(uint16_t* dz, float* 
 }
 
 // ------------------------------------------------------------------ host side
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
-
-// Tensor map of the matrix [rows, cols] (cols contiguous) with
-// boxes of box_rows rows x 128 bytes, 128-byte swizzle; zeros outside.
-bool make_map(CUtensorMap* map, CUtensorMapDataType type, int elem, const void* ptr, int64_t rows, int64_t cols,
-              int box_rows) {
-  const PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (fn == nullptr) return false;
-  cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
-  cuuint64_t strides[1] = {cuuint64_t(cols) * cuuint64_t(elem)};
-  cuuint32_t box[2] = {cuuint32_t(ROW_BYTES / elem), cuuint32_t(box_rows)};
-  cuuint32_t estr[2] = {1u, 1u};
-  return fn(map, type, 2, const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
-}
 // An MMA operand: [rows, k] K-major or, `mn`, [k, rows] as it lies in memory.
 template <int OP>
 bool operand_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t k, bool mn, int box_rows = 128) {
-  const CUtensorMapDataType t = OP == OP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  return mn ? make_map(map, t, OP == OP_BF16 ? 2 : 1, ptr, k, rows, box_rows)
-            : make_map(map, t, OP == OP_BF16 ? 2 : 1, ptr, rows, k, box_rows);
+  return mn ? make_operand_map(map, ptr, OP == OP_BF16, k, rows, box_rows)
+            : make_operand_map(map, ptr, OP == OP_BF16, rows, k, box_rows);
 }
+
 // 2-CTA clusters of a form that fit on the device at once (cached per device).
 template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
 cudaError_t max_pairs(int* pairs) {
@@ -757,48 +703,33 @@ cudaError_t launch(const Maps& m, const LinArgs& a, int pairs, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, linear_kernel<OP, EPI, ACT, A_MN, B_MN>, m.a, m.b, m.bh, a);
 }
 
-// How a product [M, K] x [N, K]^T is cut: the tiles, their orientation, and the
-// parts of K where the tiles alone would leave SM pairs idle.
+// How a product [M, K] x [N, K]^T is cut: the tiles, and the parts of K where
+// the tiles alone would leave half of the SM pairs idle or more.
 struct Plan {
-  bool turned;               // the weights are the 256-row operand (EPI_PARTIAL_T)
-  int bn;                    // activation rows per tile when turned
   int tiles_m, tiles_n, tiles, num_kb, splits, kb_per_split;
   int64_t m_pad;
 };
 constexpr int kPlanPairs = kNumSMsHint / 2;   // fixed, so a workspace size needs no device query
-constexpr int kTurnedRows = 256;
-// can_turn: not for an MN-major activation operand (the weight gradients), whose
-// boxes are 64 values wide.
-Plan make_plan(int64_t M, int64_t N, int64_t K, int op, bool can_turn = true) {
+Plan make_plan(int64_t M, int64_t N, int64_t K, int op) {
   Plan p;
-  p.turned = can_turn && M <= kTurnedRows;
-  p.bn = p.turned ? int((M + 31) / 32 * 32) : BN;
-  const int64_t rows = p.turned ? N : M, cols = p.turned ? M : N;
-  p.tiles_m = int((rows + 2 * BM - 1) / (2 * BM));
-  p.tiles_n = p.turned ? 1 : int((cols + BN - 1) / BN);
+  p.tiles_m = int((M + 2 * BM - 1) / (2 * BM));
+  p.tiles_n = int((N + BN - 1) / BN);
   p.tiles = p.tiles_m * p.tiles_n;
   p.num_kb = int((K + stage_k(op) - 1) / stage_k(op));
   p.m_pad = (M + 31) / 32 * 32;
   p.splits = 1;
-  if (p.tiles > 0 && (p.turned || 2 * p.tiles <= kPlanPairs)) {
-    // the number of parts with the shortest schedule, in stages: rounds of
-    // units over the pairs, each unit its part of K and about four stages'
-    // time of filling and draining; more parts only where they shorten it
-    int best = 0;
-    for (int s = 1; s <= 16 && s * 4 <= p.num_kb; ++s) {
-      const int cost = (p.tiles * s + kPlanPairs - 1) / kPlanPairs * ((p.num_kb + s - 1) / s + 4);
-      if (best == 0 || cost < best) {
-        best = cost;
-        p.splits = s;
-      }
-    }
+  if (p.tiles > 0 && 2 * p.tiles <= kPlanPairs) {
+    int s = kPlanPairs / p.tiles;
+    if (s > p.num_kb / 4) s = p.num_kb / 4;   // at least four stages of work per part
+    if (s > 16) s = 16;
+    if (s > 1) p.splits = s;
   }
   p.kb_per_split = (p.num_kb + p.splits - 1) / p.splits;
   if (p.num_kb > 0) p.splits = (p.num_kb + p.kb_per_split - 1) / p.kb_per_split;
   return p;
 }
 size_t plan_bytes(const Plan& p, int64_t N) {
-  return p.turned || p.splits > 1 ? size_t(p.splits) * size_t(p.m_pad) * size_t(N) * sizeof(float) : 0;
+  return p.splits > 1 ? size_t(p.splits) * size_t(p.m_pad) * size_t(N) * sizeof(float) : 0;
 }
 
 // N-blocks per raster band: about 32 MB of weights, so that a band stays in L2
@@ -831,7 +762,7 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
                     float* partial, cudaStream_t s) {
   constexpr bool GATED = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
   const int64_t brows = GATED ? 2 * N : N;
-  const Plan p = make_plan(M, brows, K, OP, !A_MN);
+  const Plan p = make_plan(M, brows, K, OP);
   Maps m;
   if (!operand_map<OP>(&m.a, A, M, K, A_MN) || !operand_map<OP>(&m.b, B, brows, K, B_MN)) return cudaErrorInvalidValue;
   m.bh = m.b;
@@ -843,27 +774,6 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
   a.splits = 1;
   int pairs = 0;
   cudaError_t e;
-  a.bn = p.bn;
-  if constexpr (!A_MN) {
-    if (p.turned) {
-      // the weights are A, the activations B
-      Maps t;
-      if (!operand_map<OP>(&t.a, B, brows, K, B_MN) || !operand_map<OP>(&t.b, A, M, K, false, p.bn / 2))
-        return cudaErrorInvalidValue;
-      t.bh = t.b;
-      a.M = int(brows);
-      a.N = int(M);
-      a.tiles_n = a.band_n = p.tiles_n;
-      a.splits = p.splits;
-      a.kb_per_split = p.kb_per_split;
-      a.m_pad = int(p.m_pad);
-      a.partial = partial;
-      a.num_units = a.split_from = p.tiles * p.splits;
-      if ((e = max_pairs<OP, EPI_PARTIAL_T, ACT_NONE, B_MN, false>(&pairs)) != cudaSuccess) return e;
-      if ((e = launch<OP, EPI_PARTIAL_T, ACT_NONE, B_MN, false>(t, a, pairs, s)) != cudaSuccess) return e;
-      return launch_join<EPI, ACT>(out, z, partial, bias, in, a_scale, w_scale, p, brows, M, N, s);
-    }
-  }
   if (p.splits > 1) {
     a.partial = partial;
     a.N = int(brows);
@@ -913,7 +823,8 @@ void linear_bwd_offsets(int64_t M, int64_t N, int64_t K, size_t off[4]) {
   off[0] = 0;
   off[1] = round256(size_t(M) * size_t(N) * 2);
   off[2] = off[1] + round256(size_t(act_backward_blocks(M, N)) * size_t(N) * sizeof(float));
-  const size_t a = plan_bytes(make_plan(M, K, N, OP_BF16), K), b = plan_bytes(make_plan(N, K, M, OP_BF16, false), K);
+  const size_t a = few_rows(M) ? 0 : plan_bytes(make_plan(M, K, N, OP_BF16), K);
+  const size_t b = plan_bytes(make_plan(N, K, M, OP_BF16), K);
   off[3] = off[2] + round256(a > b ? a : b);
 }
 
@@ -921,8 +832,9 @@ void linear_bwd_offsets(int64_t M, int64_t N, int64_t K, size_t off[4]) {
 void gated_bwd_offsets(int64_t M, int64_t C, int64_t H, size_t off[3]) {
   off[0] = 0;
   off[1] = round256(size_t(M) * size_t(2 * H) * 2);
-  size_t a = plan_bytes(make_plan(M, 2 * H, C, OP_BF16), 2 * H);
-  const size_t b = plan_bytes(make_plan(M, C, 2 * H, OP_BF16), C), c = plan_bytes(make_plan(2 * H, C, M, OP_BF16, false), C);
+  size_t a = few_rows(M) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16), 2 * H);
+  const size_t b = few_rows(M) ? 0 : plan_bytes(make_plan(M, C, 2 * H, OP_BF16), C);
+  const size_t c = plan_bytes(make_plan(2 * H, C, M, OP_BF16), C);
   a = a > b ? a : b;
   off[2] = off[1] + round256(a > c ? a : c);
 }
@@ -930,10 +842,10 @@ void gated_bwd_offsets(int64_t M, int64_t C, int64_t H, size_t off[3]) {
 }  // namespace
 
 size_t linear_workspace(int64_t M, int64_t N, int64_t K, bool fp8) {
-  return skinny_rows(M) ? 0 : plan_bytes(make_plan(M, N, K, fp8 ? OP_E4M3 : OP_BF16), N);
+  return few_rows(M) ? 0 : plan_bytes(make_plan(M, N, K, fp8 ? OP_E4M3 : OP_BF16), N);
 }
 size_t gated_workspace(int64_t M, int64_t C, int64_t H) {
-  return skinny_rows(M) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16), 2 * H);
+  return few_rows(M) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16), 2 * H);
 }
 size_t linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
   size_t off[4];
@@ -959,6 +871,7 @@ cudaError_t launch_linear(uint16_t* out, uint16_t* z, const uint16_t* x, const u
                           const uint16_t* res, int act, int64_t M, int64_t N, int64_t K, float* ws, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
   if (skinny_rows(M)) return launch_skinny(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, false, s);
+  if (few_rows(M)) return launch_few_rows(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, false, false, s);
   QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_LINEAR, ACT, false, false>(out, z, x, nullptr, w, nullptr, bias, res, M, N,
                                                                         K, ws, s)));
 }
@@ -968,6 +881,7 @@ cudaError_t launch_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, cons
                               int64_t N, int64_t K, float* ws, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
   if (skinny_rows(M)) return launch_skinny(out, z, x, x_scale, w, w_scale, bias, res, act, M, N, K, true, s);
+  if (few_rows(M)) return launch_few_rows(out, z, x, x_scale, w, w_scale, bias, res, act, M, N, K, true, false, s);
   QFFN_ACT_SWITCH(act, (product<OP_E4M3, EPI_LINEAR, ACT, false, false>(out, z, x, x_scale, w, w_scale, bias, res, M, N,
                                                                         K, ws, s)));
 }
@@ -976,6 +890,7 @@ cudaError_t launch_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int
                          float* ws, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
   if (skinny_rows(M)) return launch_skinny_gated(h, x, w1, act, M, C, H, s);
+  if (few_rows(M)) return launch_few_rows_gated(h, x, w1, nullptr, act, M, C, H, s);
   QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_GATED, ACT, false, false>(h, nullptr, x, nullptr, w1, nullptr, nullptr,
                                                                        nullptr, M, H, C, ws, s)));
 }
@@ -993,6 +908,7 @@ cudaError_t act_backward(uint16_t* dz, float* partial, const uint16_t* dout, con
 }
 cudaError_t gated_bwd_product(uint16_t* dgu, const uint16_t* dh, const uint16_t* x, const uint16_t* w1, int act,
                               int64_t M, int64_t C, int64_t H, float* part, cudaStream_t s) {
+  if (few_rows(M)) return launch_few_rows_gated(dgu, x, w1, dh, act, M, C, H, s);
   QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_GATED_BWD, ACT, false, false>(dgu, nullptr, x, nullptr, w1, nullptr,
                                                                            nullptr, dh, M, H, C, part, s)));
 }
@@ -1000,10 +916,13 @@ cudaError_t gated_bwd_product(uint16_t* dgu, const uint16_t* dh, const uint16_t*
 cudaError_t grad_products(uint16_t* dx, uint16_t* dw, const uint16_t* dz, const uint16_t* x, const uint16_t* w,
                           int64_t M, int64_t N, int64_t K, bool accumulate, float* part, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
-  if (dx != nullptr &&
-      (e = product<OP_BF16, EPI_LINEAR, ACT_NONE, false, true>(dx, nullptr, dz, nullptr, w, nullptr, nullptr, nullptr, M,
-                                                               K, N, part, s)) != cudaSuccess)
-    return e;
+  if (dx != nullptr) {
+    e = few_rows(M) ? launch_few_rows(dx, nullptr, dz, nullptr, w, nullptr, nullptr, nullptr, ACT_NONE, M, K, N, false,
+                                      true, s)
+                    : product<OP_BF16, EPI_LINEAR, ACT_NONE, false, true>(dx, nullptr, dz, nullptr, w, nullptr, nullptr,
+                                                                          nullptr, M, K, N, part, s);
+    if (e != cudaSuccess) return e;
+  }
   return product<OP_BF16, EPI_LINEAR, ACT_NONE, true, true>(dw, nullptr, dz, nullptr, x, nullptr, nullptr,
                                                             accumulate ? dw : nullptr, N, K, M, part, s);
 }
