@@ -423,6 +423,38 @@ cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, FewArgs a, int cl
   return cudaLaunchKernelEx(&cfg, fn, w, x, a);
 }
 
+// Clusters of `size` CTAs that fit on the current device at once with one CTA per
+// SM (cached per device; the same for every form, whose shared memory is that
+// of one CTA per SM).
+cudaError_t max_clusters(int size, int* n) {
+  static int cached[64][4] = {};
+  const int i = size == 2 ? 1 : size == 4 ? 2 : 3;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && cached[dev][i] > 0) {
+    *n = cached[dev][i];
+    return cudaSuccess;
+  }
+  const auto fn = few_rows_kernel<OP_BF16, false, EPI_LINEAR>;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne + 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(num_sms() / size * size));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemOne + 1024;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(size);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(n, fn, &cfg);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) cached[dev][i] = *n;
+  return e;
+}
+
 }  // namespace
 
 bool few_rows(int64_t M) { return M <= 128; }
@@ -448,9 +480,17 @@ cudaError_t few_rows_product(uint16_t* out, uint16_t* z, const void* x, const fl
   a.bn = int(((M + mtiles - 1) / mtiles + 31) / 32 * 32);
   a.tiles_n = int(GATED ? (N + 63) / 64 : (N + 127) / 128);
   const int clusters = a.tiles_n * mtiles;
-  // parts of K: as many as the SMs have room for, each with at least four stages
+  // parts of K: as many as leave every cluster on the GPU at once, each with at
+  // least four stages (clusters of 8 do not fill it: 16 of them, which would
+  // take 128 of 152 SMs, run in two rounds)
   a.splits = 1;
-  while (a.splits < kMaxSplits && clusters * a.splits * 2 <= kNumSMsHint && a.num_kb >= 8 * a.splits) a.splits *= 2;
+  for (int s = 2; s <= kMaxSplits && a.num_kb >= 4 * s; s *= 2) {
+    int fit = 0;
+    const cudaError_t e = max_clusters(s, &fit);
+    if (e != cudaSuccess) return e;
+    if (clusters > fit) break;
+    a.splits = s;
+  }
   while (a.splits > 1 && (a.splits - 1) * ((a.num_kb + a.splits - 1) / a.splits) >= a.num_kb) a.splits /= 2;
   a.stage_bytes = BOX_BYTES + a.bn * ROW_BYTES;
   const bool two = clusters * a.splits > kNumSMsHint && a.bn <= 128;

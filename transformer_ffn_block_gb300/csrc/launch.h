@@ -161,15 +161,16 @@ cudaError_t launch_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int
 cudaError_t launch_gated_backward(uint16_t* dx, uint16_t* dw1, const uint16_t* dh, const uint16_t* x,
                                   const uint16_t* w1, int act, int64_t M, int64_t C, int64_t H, bool accumulate,
                                   uint8_t* ws, cudaStream_t s);
-// The forms for few rows (skinny.cu), which launch_linear*, launch_gated take where skinny_rows(M).
-bool skinny_rows(int64_t M);
+// The forms for few rows or small weights (skinny.cu), which launch_linear* and
+// launch_gated take where skinny_rows(); wrows: rows of the weight matrix.
+bool skinny_rows(int64_t M, int64_t wrows, int64_t K, bool fp8);
 cudaError_t launch_skinny(uint16_t* out, uint16_t* z, const void* x, const float* x_scale, const void* w,
                           const float* w_scale, const uint16_t* bias, const uint16_t* res, int act, int64_t M,
                           int64_t N, int64_t K, bool fp8, cudaStream_t s);
 cudaError_t launch_skinny_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int act, int64_t M, int64_t C,
                                 int64_t H, cudaStream_t s);
 // The forms for few rows on the tensor cores (few_rows.cu), taken where few_rows(M)
-// and, forward, not skinny_rows(M).  No workspace.  w_mn: w given as [K, N]
+// and, forward, not skinny_rows().  No workspace.  w_mn: w given as [K, N]
 // (bf16).  Gated: h from w1 = [2H, C], or, with dh, d_gu [M, 2H].
 bool few_rows(int64_t M);
 cudaError_t launch_few_rows(uint16_t* out, uint16_t* z, const void* x, const float* x_scale, const void* w,

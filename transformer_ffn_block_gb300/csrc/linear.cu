@@ -719,10 +719,17 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int op) {
   p.m_pad = (M + 31) / 32 * 32;
   p.splits = 1;
   if (p.tiles > 0 && 2 * p.tiles <= kPlanPairs) {
-    int s = kPlanPairs / p.tiles;
-    if (s > p.num_kb / 4) s = p.num_kb / 4;   // at least four stages of work per part
-    if (s > 16) s = 16;
-    if (s > 1) p.splits = s;
+    // In stages (about 0.55 us each): a part's share of K, and for more than one
+    // part the second kernel, about eight stages' time and half a stage for
+    // each part it reads (1024 x 1024 x 1024: one part 8.5 us, two 12.3).
+    int best = 2 * p.num_kb;
+    for (int s = 2; s <= 16 && s * p.tiles <= kPlanPairs && s * 4 <= p.num_kb; ++s) {
+      const int cost = 2 * ((p.num_kb + s - 1) / s) + 16 + s;
+      if (cost < best) {
+        best = cost;
+        p.splits = s;
+      }
+    }
   }
   p.kb_per_split = (p.num_kb + p.splits - 1) / p.splits;
   if (p.num_kb > 0) p.splits = (p.num_kb + p.kb_per_split - 1) / p.kb_per_split;
@@ -842,10 +849,10 @@ void gated_bwd_offsets(int64_t M, int64_t C, int64_t H, size_t off[3]) {
 }  // namespace
 
 size_t linear_workspace(int64_t M, int64_t N, int64_t K, bool fp8) {
-  return few_rows(M) ? 0 : plan_bytes(make_plan(M, N, K, fp8 ? OP_E4M3 : OP_BF16), N);
+  return few_rows(M) || skinny_rows(M, N, K, fp8) ? 0 : plan_bytes(make_plan(M, N, K, fp8 ? OP_E4M3 : OP_BF16), N);
 }
 size_t gated_workspace(int64_t M, int64_t C, int64_t H) {
-  return few_rows(M) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16), 2 * H);
+  return few_rows(M) || skinny_rows(M, 2 * H, C, false) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16), 2 * H);
 }
 size_t linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
   size_t off[4];
@@ -870,7 +877,7 @@ size_t gated_backward_workspace(int64_t M, int64_t C, int64_t H) {
 cudaError_t launch_linear(uint16_t* out, uint16_t* z, const uint16_t* x, const uint16_t* w, const uint16_t* bias,
                           const uint16_t* res, int act, int64_t M, int64_t N, int64_t K, float* ws, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
-  if (skinny_rows(M)) return launch_skinny(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, false, s);
+  if (skinny_rows(M, N, K, false)) return launch_skinny(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, false, s);
   if (few_rows(M)) return launch_few_rows(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, false, false, s);
   QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_LINEAR, ACT, false, false>(out, z, x, nullptr, w, nullptr, bias, res, M, N,
                                                                         K, ws, s)));
@@ -880,7 +887,7 @@ cudaError_t launch_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, cons
                               const float* w_scale, const uint16_t* bias, const uint16_t* res, int act, int64_t M,
                               int64_t N, int64_t K, float* ws, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
-  if (skinny_rows(M)) return launch_skinny(out, z, x, x_scale, w, w_scale, bias, res, act, M, N, K, true, s);
+  if (skinny_rows(M, N, K, true)) return launch_skinny(out, z, x, x_scale, w, w_scale, bias, res, act, M, N, K, true, s);
   if (few_rows(M)) return launch_few_rows(out, z, x, x_scale, w, w_scale, bias, res, act, M, N, K, true, false, s);
   QFFN_ACT_SWITCH(act, (product<OP_E4M3, EPI_LINEAR, ACT, false, false>(out, z, x, x_scale, w, w_scale, bias, res, M, N,
                                                                         K, ws, s)));
@@ -889,7 +896,7 @@ cudaError_t launch_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, cons
 cudaError_t launch_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int act, int64_t M, int64_t C, int64_t H,
                          float* ws, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
-  if (skinny_rows(M)) return launch_skinny_gated(h, x, w1, act, M, C, H, s);
+  if (skinny_rows(M, 2 * H, C, false)) return launch_skinny_gated(h, x, w1, act, M, C, H, s);
   if (few_rows(M)) return launch_few_rows_gated(h, x, w1, nullptr, act, M, C, H, s);
   QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_GATED, ACT, false, false>(h, nullptr, x, nullptr, w1, nullptr, nullptr,
                                                                        nullptr, M, H, C, ws, s)));

@@ -171,7 +171,21 @@ cudaError_t run(const SkinnyArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-bool skinny_rows(int64_t M) { return M <= 32; }
+// Up to 16 rows the weights' stream bounds the call and this form is the
+// fastest at every size (measured: 16 rows, 4096 x 14336: 21.6 us against 24.4 by
+// few_rows.cu; 28672 x 4096: 41.8 against 41.3).  Beyond, each block of 32 rows
+// reads the weights again, through L2: about 4 ns per CTA and 7.3 ns per CTA
+// and 1024 elements of K over the whole grid, against 4.5 us and more that a
+// tcgen05 kernel takes to set up, fill and drain.  It is taken while that
+// sum is below 5 us (E4M3, whose products cost the same and whose loads cost the
+// other form half: 3 us).  Measured in us, this form against the other: 256 rows
+// of 768 x 256 4.2 / 7.0, of 1024 x 1024 7.3 / 8.5, 64 rows of 4096 x 1024 7.7 /
+// 7.8, 32 rows of 28672 x 4096 58 / 41, E4M3 64 rows of 4096 x 256 6.5 / 4.9.
+bool skinny_rows(int64_t M, int64_t wrows, int64_t K, bool fp8) {
+  if (M <= 16) return true;
+  const int64_t ctas = (wrows + 15) / 16 * ((M + 31) / 32);
+  return ctas * (K + 550) <= (fp8 ? 400000 : 700000);
+}
 
 cudaError_t launch_skinny(uint16_t* out, uint16_t* z, const void* x, const float* x_scale, const void* w,
                           const float* w_scale, const uint16_t* bias, const uint16_t* res, int act, int64_t M,
