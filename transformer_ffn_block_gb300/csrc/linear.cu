@@ -72,7 +72,7 @@ constexpr int EPI_LINEAR = 0, EPI_GATED = 1, EPI_GATED_BWD = 2, EPI_PARTIAL = 3;
 // Instruction descriptor: D fp32 (bits 4-5 = 1); A and B formats at bits 7-9
 // and 10-12 (kind::f16: 1 = bf16; kind::f8f6f4: 0 = E4M3); bits 15 / 16: A / B
 // MN-major; N >> 3 at bits 17-22, M >> 4 at bits 24-28 (M = 256 over the pair).
-constexpr uint32_t idesc_for(int op, bool a_mn, bool b_mn, int n) {
+QFFN_DEVI constexpr uint32_t idesc_for(int op, bool a_mn, bool b_mn, int n) {
   return (1u << 4) | (op == OP_BF16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
          (b_mn ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) | (uint32_t((2 * BM) >> 4) << 24);
 }
@@ -94,6 +94,7 @@ struct LinArgs {
   const uint16_t* bias;     // EPI_LINEAR, optional
   const uint16_t* in;       // [M, N]: EPI_LINEAR residual or previous output (optional), GATED_BWD dh
   int M, N;                 // output rows and columns (gated: columns = H)
+  int narrow;               // every unit is BN >> narrow accumulator columns wide
   int up_row;               // gated: first up row of W1 (= H)
   int tiles_m, tiles_n, num_units, num_kb;
   int band_n;               // N-blocks per raster band
@@ -139,7 +140,7 @@ QFFN_DEVI bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag
 
 struct Unit {
   int mb, nb;      // pair M-block (256 rows), N-block
-  int half;        // -1: whole tile; 0 / 1: first / second 128 accumulator columns of a split one
+  int half;        // -1: whole tile; 0 / 1: first / second half of a split one (narrow = 0 only)
   int sp;          // EPI_PARTIAL: part of K
 };
 
@@ -173,7 +174,7 @@ QFFN_DEVI Unit unit_coords(int u, const LinArgs& a) {
   return r;
 }
 
-// tmBh: B with 64-row boxes for the half tiles.
+// tmB: B with boxes of 128 >> narrow rows; tmBh: of 64 rows, for the half tiles.
 template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -231,6 +232,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   pdl_wait();              // nothing in global memory is touched before the preceding kernel is done
   pdl_trigger();
 
+  const int bn = BN >> args.narrow;        // accumulator columns of a whole unit
   // K blocks of a unit
   auto kb_begin = [&](const Unit& u) { return EPI == EPI_PARTIAL ? u.sp * args.kb_per_split : 0; };
   auto kb_end = [&](const Unit& u) {
@@ -248,10 +250,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int rowA = u.mb * (2 * BM) + int(rank) * BM;
         // this CTA's weight rows: half of the tile's 256 (of a half tile's
         // 128); gated: CTA 0 the gate rows, CTA 1 the matching up rows
-        const int rowB = GATED ? (rank == 0 ? 0 : args.up_row) + u.nb * 128 + (u.half < 0 ? 0 : u.half * 64)
-                         : u.half < 0 ? u.nb * BN + int(rank) * 128
+        const int rowB = GATED ? (rank == 0 ? 0 : args.up_row) + u.nb * (bn / 2) + (u.half < 0 ? 0 : u.half * 64)
+                         : u.half < 0 ? u.nb * bn + int(rank) * (bn / 2)
                                       : u.nb * BN + u.half * 128 + int(rank) * 64;
-        const uint32_t stage_tx = u.half < 0 ? 2 * STAGE_BYTES : 2 * (OP_BYTES + OP_BYTES / 2);
+        const uint32_t stage_tx = 2u * uint32_t(OP_BYTES + (u.half < 0 ? OP_BYTES >> args.narrow : OP_BYTES / 2));
         const int kb1 = kb_end(u);
         for (int kb = kb_begin(u); kb < kb1; ++kb, ++it) {
           const int s = it % STAGES;
@@ -267,8 +269,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (A_MN) tma_load_2d_pair(da, &tmA, fb, rowA + bx * 64, k0);
             else tma_load_2d_pair(da, &tmA, fb, k0 + bx * box_k(OP), rowA);
             if (B_MN) {
-              // a half tile's 64 rows are one box
-              if (u.half < 0 || bx == 0) tma_load_2d_pair(db, &tmB, fb, rowB + bx * 64, k0);
+              // 64 rows (a half tile's or a narrow unit's) are one box
+              if ((u.half < 0 && args.narrow == 0) || bx == 0) tma_load_2d_pair(db, &tmB, fb, rowB + bx * 64, k0);
             } else {
               tma_load_2d_pair(db, u.half < 0 ? &tmB : &tmBh, fb, k0 + bx * box_k(OP), rowB);
             }
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_after();
         const Unit u = unit_coords<EPI>(un, args);
         const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
-        const uint32_t idesc = u.half < 0 ? idesc_for(OP, A_MN, B_MN, BN) : idesc_for(OP, A_MN, B_MN, BN / 2);
+        const uint32_t idesc = idesc_for(OP, A_MN, B_MN, u.half < 0 ? bn : BN / 2);
         const int kb0 = kb_begin(u), kb1 = kb_end(u);
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = it % STAGES;
@@ -341,10 +343,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const Unit u = unit_coords<EPI>(un, args);
       const int row0 = u.mb * (2 * BM) + int(rank) * BM + q * 32;
       // output column of the unit's group 0
-      const int first_col = GATED ? u.nb * 128 + (u.half < 0 ? 0 : u.half * 64)
-                                  : u.nb * BN + (u.half < 0 ? 0 : u.half * 128);
+      const int first_col = GATED ? u.nb * (bn / 2) + (u.half < 0 ? 0 : u.half * 64)
+                                  : u.nb * bn + (u.half < 0 ? 0 : u.half * 128);
       const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * BN);
-      const int acc_cols = u.half < 0 ? BN : BN / 2;
+      const int acc_cols = u.half < 0 ? bn : BN / 2;
       const int groups = GATED ? acc_cols / 64 : acc_cols / 32;
       // this lane's output rows and column of the group at hand
       auto row_of = [&](int i) { return row0 + sub + 8 * i; };
@@ -703,34 +705,47 @@ cudaError_t launch(const Maps& m, const LinArgs& a, int pairs, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, linear_kernel<OP, EPI, ACT, A_MN, B_MN>, m.a, m.b, m.bh, a);
 }
 
-// How a product [M, K] x [N, K]^T is cut: the tiles, and the parts of K where
-// the tiles alone would leave half of the SM pairs idle or more.
+// How a product [M, K] x [N, K]^T is cut: into units of 256 rows by 256 >> narrow
+// columns, and the parts of K where even narrow units would leave SM pairs idle.
 struct Plan {
-  int tiles_m, tiles_n, tiles, num_kb, splits, kb_per_split;
+  int tiles_m, tiles_n, tiles, num_kb, narrow, splits, kb_per_split;
   int64_t m_pad;
 };
 constexpr int kPlanPairs = kNumSMsHint / 2;   // fixed, so a workspace size needs no device query
-Plan make_plan(int64_t M, int64_t N, int64_t K, int op) {
+// max_narrow: 2, or 1 where B is MN-major (its boxes are 64 columns wide).
+Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
   Plan p;
   p.tiles_m = int((M + 2 * BM - 1) / (2 * BM));
-  p.tiles_n = int((N + BN - 1) / BN);
-  p.tiles = p.tiles_m * p.tiles_n;
   p.num_kb = int((K + stage_k(op) - 1) / stage_k(op));
   p.m_pad = (M + 31) / 32 * 32;
+  p.narrow = 0;
   p.splits = 1;
-  if (p.tiles > 0 && 2 * p.tiles <= kPlanPairs) {
-    // In stages (about 0.55 us each): a part's share of K, and for more than one
-    // part the second kernel, about eight stages' time and half a stage for
-    // each part it reads (1024 x 1024 x 1024: one part 8.5 us, two 12.3).
-    int best = 2 * p.num_kb;
-    for (int s = 2; s <= 16 && s * p.tiles <= kPlanPairs && s * 4 <= p.num_kb; ++s) {
-      const int cost = 2 * ((p.num_kb + s - 1) / s) + 16 + s;
-      if (cost < best) {
-        best = cost;
-        p.splits = s;
+  const int64_t whole = int64_t(p.tiles_m) * ((N + BN - 1) / BN);
+  if (2 * whole <= kPlanPairs) {
+    // Less than half a round of whole tiles: the cheapest of narrower units and
+    // parts of K, in SM cycles.  A stage of a unit takes the cycles of its MMAs
+    // (1024 >> narrow) or of its loads (32 KB of A and 32 KB >> narrow of B per
+    // SM at 64 bytes a cycle), the last unit's epilogue 4500 >> narrow, joining
+    // parts about 8200 and 500 for each.  Measured against whole tiles, the
+    // parts alone: 512 x 4096 x 4096 24.5 us, 256 x 1024 x 1024 10.5 us; see
+    // launch_linear for what the units measured.
+    int64_t best = -1;
+    for (int n = 0; n <= max_narrow; ++n) {
+      const int64_t units = int64_t(p.tiles_m) * ((N + (BN >> n) - 1) / (BN >> n));
+      const int stage = n == 0 ? 1024 : n == 1 ? 768 : 640;
+      for (int s = 1; s <= 16 && (s == 1 || (s * 4 <= p.num_kb && units * s <= kPlanPairs)); ++s) {
+        const int64_t rounds = (units * s + kPlanPairs - 1) / kPlanPairs;
+        const int64_t cost = rounds * ((p.num_kb + s - 1) / s) * stage + (4500 >> n) + (s > 1 ? 8200 + 500 * s : 0);
+        if (best < 0 || cost < best) {
+          best = cost;
+          p.narrow = n;
+          p.splits = s;
+        }
       }
     }
   }
+  p.tiles_n = int((N + (BN >> p.narrow) - 1) / (BN >> p.narrow));
+  p.tiles = p.tiles_m * p.tiles_n;
   p.kb_per_split = (p.num_kb + p.splits - 1) / p.splits;
   if (p.num_kb > 0) p.splits = (p.num_kb + p.kb_per_split - 1) / p.kb_per_split;
   return p;
@@ -769,15 +784,16 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
                     float* partial, cudaStream_t s) {
   constexpr bool GATED = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
   const int64_t brows = GATED ? 2 * N : N;
-  const Plan p = make_plan(M, brows, K, OP);
+  const Plan p = make_plan(M, brows, K, OP, B_MN ? 1 : 2);
   Maps m;
-  if (!operand_map<OP>(&m.a, A, M, K, A_MN) || !operand_map<OP>(&m.b, B, brows, K, B_MN)) return cudaErrorInvalidValue;
+  if (!operand_map<OP>(&m.a, A, M, K, A_MN) || !operand_map<OP>(&m.b, B, brows, K, B_MN, B_MN ? 128 : 128 >> p.narrow)) return cudaErrorInvalidValue;
   m.bh = m.b;
   LinArgs a{};
   a.M = int(M);
   a.tiles_m = p.tiles_m;
   a.num_kb = p.num_kb;
   a.up_row = int(N);
+  a.narrow = p.narrow;
   a.splits = 1;
   int pairs = 0;
   cudaError_t e;
@@ -801,13 +817,13 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
   a.out = out;
   a.z = z;
   a.in = in;
-  a.tiles_n = GATED ? int((N + 127) / 128) : p.tiles_n;
+  a.tiles_n = GATED ? int((N + (128 >> p.narrow) - 1) / (128 >> p.narrow)) : p.tiles_n;
   a.band_n = band_blocks(a.tiles_n, M, brows, K * (OP == OP_BF16 ? 2 : 1));
   a.num_units = a.split_from = a.tiles_m * a.tiles_n;
   if ((e = max_pairs<OP, EPI, ACT, A_MN, B_MN>(&pairs)) != cudaSuccess) return e;
   // a last partial wave of R <= pairs / 2 tiles runs as 2 R half tiles in half the time
   const int r = a.num_units % pairs;
-  if (a.num_units > pairs && r > 0 && 2 * r <= pairs) {
+  if (p.narrow == 0 && a.num_units > pairs && r > 0 && 2 * r <= pairs) {
     if (!B_MN && !operand_map<OP>(&m.bh, B, brows, K, false, 64)) return cudaErrorInvalidValue;
     a.split_from = a.num_units - r;
     a.num_units += r;
@@ -830,8 +846,8 @@ void linear_bwd_offsets(int64_t M, int64_t N, int64_t K, size_t off[4]) {
   off[0] = 0;
   off[1] = round256(size_t(M) * size_t(N) * 2);
   off[2] = off[1] + round256(size_t(act_backward_blocks(M, N)) * size_t(N) * sizeof(float));
-  const size_t a = few_rows(M) ? 0 : plan_bytes(make_plan(M, K, N, OP_BF16), K);
-  const size_t b = plan_bytes(make_plan(N, K, M, OP_BF16), K);
+  const size_t a = few_rows(M) ? 0 : plan_bytes(make_plan(M, K, N, OP_BF16, 1), K);
+  const size_t b = plan_bytes(make_plan(N, K, M, OP_BF16, 1), K);
   off[3] = off[2] + round256(a > b ? a : b);
 }
 
@@ -839,9 +855,9 @@ void linear_bwd_offsets(int64_t M, int64_t N, int64_t K, size_t off[4]) {
 void gated_bwd_offsets(int64_t M, int64_t C, int64_t H, size_t off[3]) {
   off[0] = 0;
   off[1] = round256(size_t(M) * size_t(2 * H) * 2);
-  size_t a = few_rows(M) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16), 2 * H);
-  const size_t b = few_rows(M) ? 0 : plan_bytes(make_plan(M, C, 2 * H, OP_BF16), C);
-  const size_t c = plan_bytes(make_plan(2 * H, C, M, OP_BF16), C);
+  size_t a = few_rows(M) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16, 2), 2 * H);
+  const size_t b = few_rows(M) ? 0 : plan_bytes(make_plan(M, C, 2 * H, OP_BF16, 1), C);
+  const size_t c = plan_bytes(make_plan(2 * H, C, M, OP_BF16, 1), C);
   a = a > b ? a : b;
   off[2] = off[1] + round256(a > c ? a : c);
 }
@@ -849,10 +865,10 @@ void gated_bwd_offsets(int64_t M, int64_t C, int64_t H, size_t off[3]) {
 }  // namespace
 
 size_t linear_workspace(int64_t M, int64_t N, int64_t K, bool fp8) {
-  return few_rows(M) || skinny_rows(M, N, K, fp8) ? 0 : plan_bytes(make_plan(M, N, K, fp8 ? OP_E4M3 : OP_BF16), N);
+  return few_rows(M) || skinny_rows(M, N, K, fp8) ? 0 : plan_bytes(make_plan(M, N, K, fp8 ? OP_E4M3 : OP_BF16, 2), N);
 }
 size_t gated_workspace(int64_t M, int64_t C, int64_t H) {
-  return few_rows(M) || skinny_rows(M, 2 * H, C, false) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16), 2 * H);
+  return few_rows(M) || skinny_rows(M, 2 * H, C, false) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16, 2), 2 * H);
 }
 size_t linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
   size_t off[4];
