@@ -2,19 +2,21 @@
 // tensor cores (tcgen05, sm_103a): the weights are the 128-row operand.
 //
 //   D[n, m] = sum_k W[n, k] x[m, k]   n: 128 weight rows per CTA,
-//                                     m: bn <= 256 activation rows
+//                                     m: bn <= 128 activation rows
 //
 // With so few rows the bytes of the weights bound the call.  A tile of 256
 // activation rows would be mostly padding, and there are too few tiles for the
 // SMs; here the MMA's N is the number of activation rows (a multiple of 32), and
 // K is split over the CTAs of a cluster (1, 2, 4 or 8).  Each CTA sums its part
-// of K in TMEM; the parts are then exchanged through distributed shared memory,
-// every CTA adding its share of the activation rows in a fixed order, and the
-// epilogue is applied where the sum is formed.  One launch, no partial sums in
-// global memory, no workspace, the same bits each run.  (Measured at 64 x 4096
-// x 4096: partial sums in a workspace with a second kernel to join them 13.8 us,
-// 3 us of it from the first kernel's end to the second's; SM pairs in clusters
-// of 8, of which 16 do not fit on the GPU at once, 20.6 us.)
+// of K in TMEM, sends each other CTA of the cluster that one's share of the
+// activation rows (bulk copies between their shared memories), adds its own
+// share in a fixed order and applies the epilogue to it.  One launch, no partial
+// sums in global memory, no workspace, the same bits each run.  (Measured at 64
+// x 4096 x 4096: partial sums in a workspace with a second kernel to join them
+// 13.8 us, 3 us of it from the first kernel's end to the second's; SM pairs in
+// clusters of 8, of which 16 do not fit on the GPU at once, 20.6 us; the shares
+// fetched by loads from the other CTAs' shared memory, 16 bytes a lane, 12.1 us,
+// 2 us of it for 32 KB per CTA.)
 //
 // Per CTA: one warp's lane loads (TMA, 128-byte swizzle) 128 weight rows and
 // the tile's activation rows, 128 bytes of K per stage; one thread issues the
@@ -58,8 +60,9 @@ struct FewArgs {
   int act;
   int M, N;                 // activation rows; output columns (gated: H)
   int num_kb, splits;       // K blocks of a stage each; parts of K (CTAs per cluster)
-  int bn, tiles_n;          // activation rows per tile; tiles of weight rows
+  int bn, tiles_m;          // activation rows per tile; tiles of activation rows
   int stages, stage_bytes;
+  int recv_bytes;           // shared memory for the other CTAs' sums, behind the stages
   int tmem_cols;
 };
 
@@ -100,11 +103,16 @@ QFFN_DEVI bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag
   return mbar_wait_bounded(bar, parity, abort_flag, &g_status, honour_abort, limit);
 }
 
-QFFN_DEVI ulonglong2 ld_dsmem16(uint32_t addr) {
-  ulonglong2 v;
-  asm volatile("ld.shared::cluster.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(addr));
-  return v;
+// Bulk copy from this CTA's shared memory into another's (shared::cluster
+// addresses), completing on a barrier of that CTA.
+QFFN_DEVI void send_bulk(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "r"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
+QFFN_DEVI void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+QFFN_DEVI void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 QFFN_DEVI uint32_t pack2(uint64_t v) {
   float lo, hi;
@@ -149,16 +157,17 @@ QFFN_DEVI void act_grad8(int act, const uint64_t (&v)[4], uint64_t (&f)[4], uint
   }
 }
 
-// Eight sums of activation row m, from weight row n on: the parts in order, all
-// loads issued before the first is added.
+// Eight sums of row m of this CTA's share, from weight row n on, the parts in
+// order: slot j < SPLITS - 1 of `recv` holds part j (j < part) or j + 1.
 template <int SPLITS>
-QFFN_DEVI void sum8(const uint32_t (&peer)[SPLITS], int m, int n, uint64_t (&v)[4]) {
-  const uint32_t o = uint32_t(m * 128 + n) * 4u;
+QFFN_DEVI void sum8(const float* own, const float* recv, int share, int part, int m, int n, uint64_t (&v)[4]) {
   ulonglong2 a[SPLITS], b[SPLITS];
 #pragma unroll
   for (int j = 0; j < SPLITS; ++j) {
-    a[j] = ld_dsmem16(peer[j] + o);
-    b[j] = ld_dsmem16(peer[j] + o + 16u);
+    const float* src = j == part ? own : recv + (j < part ? j : j - 1) * share * 128;
+    const ulonglong2* p = reinterpret_cast<const ulonglong2*>(src + m * 128 + n);
+    a[j] = p[0];
+    b[j] = p[1];
   }
   v[0] = a[0].x;
   v[1] = a[0].y;
@@ -173,29 +182,29 @@ QFFN_DEVI void sum8(const uint32_t (&peer)[SPLITS], int m, int n, uint64_t (&v)[
   }
 }
 
-// The parts added and the epilogue: this CTA's share are the activation rows
-// part, part + SPLITS, ... of the tile, for the tile's weight rows.
+// The parts added and the epilogue for this CTA's share, the activation rows
+// part * share .. of the tile (share = bn / SPLITS), for the tile's weight rows.
 template <int OP, int EPI, int SPLITS>
-QFFN_DEVI void finish(const FewArgs& args, uint32_t base, int part, int n0, int mt) {
+QFFN_DEVI void finish(const FewArgs& args, const float* sums, const float* recv, int part, int n0, int mt) {
   constexpr bool GATED = EPI != EPI_LINEAR;
   constexpr int TPM = GATED ? 8 : 16;        // threads per activation row, eight outputs each
-  uint32_t peer[SPLITS];
-#pragma unroll
-  for (int j = 0; j < SPLITS; ++j) peer[j] = map_to_rank(base, uint32_t(j));
+  const int share = args.bn / SPLITS;
+  const float* own = sums + part * share * 128;
   const int nl = int(threadIdx.x) % TPM * 8, n = n0 + nl;
   if (n >= args.N) return;
   const float scale = OP == OP_E4M3 ? args.a_scale[0] * args.w_scale[0] : 1.0f;
   uint64_t bias[4] = {0ull, 0ull, 0ull, 0ull};
   if (EPI == EPI_LINEAR && args.bias != nullptr) unpack8(ld16_ro(args.bias + n), bias);
-  const int rows = min(args.bn, args.M - mt * args.bn);
+  const int m0 = mt * args.bn + part * share;
+  const int rows = min(share, args.M - m0);
 #pragma unroll 2
-  for (int ml = int(threadIdx.x) / TPM * SPLITS + part; ml < rows; ml += kThreads / TPM * SPLITS) {
-    const size_t m = size_t(mt) * size_t(args.bn) + size_t(ml);
+  for (int ml = int(threadIdx.x) / TPM; ml < rows; ml += kThreads / TPM) {
+    const size_t m = size_t(m0) + size_t(ml);
     const size_t o = m * size_t(args.N) + size_t(n);
     uint4 in4 = make_uint4(0, 0, 0, 0);
     if (args.in != nullptr) in4 = ld16_once(args.in + o);
     uint64_t v[4], t[4];
-    sum8<SPLITS>(peer, ml, nl, v);
+    sum8<SPLITS>(own, recv, share, part, ml, nl, v);
     unpack8(in4, t);
     if (EPI == EPI_LINEAR) {
 #pragma unroll
@@ -212,7 +221,7 @@ QFFN_DEVI void finish(const FewArgs& args, uint32_t base, int part, int n0, int 
       stg16(args.out + o, pack8(v));
     } else {
       uint64_t up[4];
-      sum8<SPLITS>(peer, ml, 64 + nl, up);
+      sum8<SPLITS>(own, recv, share, part, ml, 64 + nl, up);
       if (EPI == EPI_GATED) {
         act8(args.act, v);
 #pragma unroll
@@ -242,22 +251,25 @@ __global__ void __launch_bounds__(kThreads)
                     const FewArgs args) {
   constexpr bool GATED = EPI != EPI_LINEAR;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 3];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t bar0 = smem_u32(bars);
   // full[s]: the loads of stage s landed; empty[s]: the MMAs reading it are done;
-  // done: this CTA's sums are complete; drain: all MMAs issued have completed
+  // done: this CTA's sums are complete; drain: all MMAs issued have completed;
+  // recv: the other CTAs' sums for this one's share have arrived
   auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
   auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(kMaxStages + s); };
   const uint32_t done_bar = bar0 + 8u * uint32_t(2 * kMaxStages);
   const uint32_t drain_bar = bar0 + 8u * uint32_t(2 * kMaxStages + 1);
+  const uint32_t recv_bar = bar0 + 8u * uint32_t(2 * kMaxStages + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = int(cluster_ctarank());
-  const int tile = int(cluster_id_x()) % args.tiles_n, mt = int(cluster_id_x()) / args.tiles_n;
+  // (clusters next to each other read the same weights)
+  const int tile = int(cluster_id_x()) / args.tiles_m, mt = int(cluster_id_x()) % args.tiles_m;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < args.stages; ++s) {
@@ -266,8 +278,10 @@ __global__ void __launch_bounds__(kThreads)
     }
     mbar_init(done_bar, 1);
     mbar_init(drain_bar, 1);
+    mbar_init(recv_bar, 1);
     *abort_flag = 0;
     mbar_init_fence();
+    if (args.splits > 1) mbar_expect_tx(recv_bar, uint32_t(args.recv_bytes));
     tma_prefetch_desc(&tmW);
     tma_prefetch_desc(&tmX);
   }
@@ -280,6 +294,7 @@ __global__ void __launch_bounds__(kThreads)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  cluster_arrive();        // this CTA can receive (waited for before any CTA sends)
   const uint32_t tmem_base = tmem_slot;
   pdl_wait();
   pdl_trigger();
@@ -366,21 +381,37 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   tc_fence_before();
-  __syncwarp();
-  cluster_sync_all();
+  fence_proxy_async_smem();
+  __syncthreads();
+  cluster_wait();
+  const float* recv = reinterpret_cast<const float*>(smem + args.stages * args.stage_bytes);
+  bool have = ok;
+  if (args.splits > 1) {
+    if (ok && warp == 0) {
+      // lane j sends part j its share; the slots of the receiver skip its own part
+      const uint32_t bytes = uint32_t(args.bn / args.splits) * 512u;
+      if (lane < args.splits && lane != part) {
+        const uint32_t slot = uint32_t(part < lane ? part : part - 1);
+        send_bulk(map_to_rank(smem_u32(recv) + slot * bytes, uint32_t(lane)), smem_u32(sums) + uint32_t(lane) * bytes,
+                  bytes, map_to_rank(recv_bar, uint32_t(lane)));
+      }
+      __syncwarp();
+    }
+    have = mbar_wait(recv_bar, 0, abort_flag) && ok;
+    __syncwarp();
+  }
+  cluster_arrive();        // this CTA has received all; its own sends are done when all have arrived
   // ---------------------------------------------------------------- the parts added, epilogue
-  if (ok) {
-    const uint32_t base = smem_u32(sums);
+  if (have) {
     switch (args.splits) {
-      case 1: finish<OP, EPI, 1>(args, base, part, n0, mt); break;
-      case 2: finish<OP, EPI, 2>(args, base, part, n0, mt); break;
-      case 4: finish<OP, EPI, 4>(args, base, part, n0, mt); break;
-      default: finish<OP, EPI, 8>(args, base, part, n0, mt); break;
+      case 1: finish<OP, EPI, 1>(args, sums, recv, part, n0, mt); break;
+      case 2: finish<OP, EPI, 2>(args, sums, recv, part, n0, mt); break;
+      case 4: finish<OP, EPI, 4>(args, sums, recv, part, n0, mt); break;
+      default: finish<OP, EPI, 8>(args, sums, recv, part, n0, mt); break;
     }
   }
-  // no CTA leaves while another may read its sums
   __syncwarp();
-  cluster_sync_all();
+  cluster_wait();
   if (warp == 2) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(args.tmem_cols)
@@ -396,7 +427,7 @@ constexpr int kSmemOne = 200 * 1024, kSmemTwo = 100 * 1024;
 template <int OP, bool W_MN, int EPI>
 cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, FewArgs a, int clusters, cudaStream_t s) {
   const auto fn = few_rows_kernel<OP, W_MN, EPI>;
-  const int bytes = a.stages * a.stage_bytes + 1024;
+  const int bytes = a.stages * a.stage_bytes + a.recv_bytes + 1024;
   static bool set[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -457,7 +488,7 @@ cudaError_t max_clusters(int size, int* n) {
 
 }  // namespace
 
-bool few_rows(int64_t M) { return M <= 128; }
+bool few_rows(int64_t M) { return M <= 256; }
 
 // One product: x [M, K] (K-major), W [wrows, K] or, w_mn, [K, wrows].
 template <int OP, bool W_MN, int EPI>
@@ -476,10 +507,9 @@ cudaError_t few_rows_product(uint16_t* out, uint16_t* z, const void* x, const fl
   a.M = int(M);
   a.N = int(N);
   a.num_kb = int((K + stage_k(OP) - 1) / stage_k(OP));
-  const int mtiles = int((M + 255) / 256);
-  a.bn = int(((M + mtiles - 1) / mtiles + 31) / 32 * 32);
-  a.tiles_n = int(GATED ? (N + 63) / 64 : (N + 127) / 128);
-  const int clusters = a.tiles_n * mtiles;
+  a.tiles_m = int((M + 127) / 128);
+  a.bn = int(((M + a.tiles_m - 1) / a.tiles_m + 31) / 32 * 32);
+  const int clusters = int(GATED ? (N + 63) / 64 : (N + 127) / 128) * a.tiles_m;
   // parts of K: as many as leave every cluster on the GPU at once, each with at
   // least four stages (clusters of 8 do not fill it: 16 of them, which would
   // take 128 of 152 SMs, run in two rounds)
@@ -494,8 +524,10 @@ cudaError_t few_rows_product(uint16_t* out, uint16_t* z, const void* x, const fl
   while (a.splits > 1 && (a.splits - 1) * ((a.num_kb + a.splits - 1) / a.splits) >= a.num_kb) a.splits /= 2;
   a.stage_bytes = BOX_BYTES + a.bn * ROW_BYTES;
   const bool two = clusters * a.splits > kNumSMsHint && a.bn <= 128;
-  a.stages = (two ? kSmemTwo : kSmemOne) / a.stage_bytes;
-  if (a.stages > kMaxStages) a.stages = kMaxStages;        // (128 to 200 KB: room for the sums, bn x 512 bytes)
+  a.recv_bytes = (a.splits - 1) * (a.bn / a.splits) * 512;
+  // (the sums, bn x 512 bytes, take at most 64 KB of the stages' 96 to 200 KB)
+  a.stages = ((two ? kSmemTwo : kSmemOne) - a.recv_bytes) / a.stage_bytes;
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
   a.tmem_cols = 32;
   while (a.tmem_cols < a.bn) a.tmem_cols *= 2;
   CUtensorMap mw, mx;
