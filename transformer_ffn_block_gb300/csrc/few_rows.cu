@@ -488,7 +488,43 @@ cudaError_t max_clusters(int size, int* n) {
 
 }  // namespace
 
-bool few_rows(int64_t M) { return M <= 256; }
+namespace {
+// Clusters and parts of K of a product with N outputs (gated: N = H).  Parts: as
+// many as leave every cluster on the GPU at once, each with at least four
+// stages (clusters of 8 do not fill it: 16 of them, which would take 128 of 152
+// SMs, run in two rounds).
+cudaError_t few_rows_split(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, int* clusters, int* splits,
+                           int* num_kb) {
+  *num_kb = int((K + stage_k(fp8 ? OP_E4M3 : OP_BF16) - 1) / stage_k(fp8 ? OP_E4M3 : OP_BF16));
+  *clusters = int((gated ? (N + 63) / 64 : (N + 127) / 128) * ((M + 127) / 128));
+  *splits = 1;
+  for (int s = 2; s <= kMaxSplits && *num_kb >= 4 * s; s *= 2) {
+    int fit = 0;
+    const cudaError_t e = max_clusters(s, &fit);
+    if (e != cudaSuccess) return e;
+    if (*clusters > fit) break;
+    *splits = s;
+  }
+  // every part has at least one stage
+  while (*splits > 1 && (*splits - 1) * ((*num_kb + *splits - 1) / *splits) >= *num_kb) *splits /= 2;
+  return cudaSuccess;
+}
+}  // namespace
+
+// Up to 128 rows the 256-row tiles of linear.cu are mostly padding.  Up to 512
+// rows it goes by an estimate of both in SM cycles: here about 640 cycles per
+// stage and round of clusters and 5500 to set up, exchange and store; there 1.4
+// times the plan's cycles.  Measured in us, here against there: 256 rows of 4096
+// x 4096 17.1 / 20.0, of 2048 x 2048 9.9 / 11.9, of 8192 x 2048 16.5 / 14.3, of
+// 4096 x 14336 42 / 36, of 28672 x 4096 68 / 51.
+bool few_rows(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, int64_t other_cycles) {
+  if (M <= 128) return true;
+  if (M > 512) return false;
+  int clusters, splits, num_kb;
+  if (few_rows_split(M, N, K, gated, fp8, &clusters, &splits, &num_kb) != cudaSuccess) return false;
+  const int64_t rounds = (int64_t(clusters) * splits + kNumSMsHint - 1) / kNumSMsHint;
+  return 10 * (rounds * ((num_kb + splits - 1) / splits) * 640 + 5500) < 14 * other_cycles;
+}
 
 // One product: x [M, K] (K-major), W [wrows, K] or, w_mn, [K, wrows].
 template <int OP, bool W_MN, int EPI>
@@ -506,22 +542,11 @@ cudaError_t few_rows_product(uint16_t* out, uint16_t* z, const void* x, const fl
   a.act = act;
   a.M = int(M);
   a.N = int(N);
-  a.num_kb = int((K + stage_k(OP) - 1) / stage_k(OP));
   a.tiles_m = int((M + 127) / 128);
   a.bn = int(((M + a.tiles_m - 1) / a.tiles_m + 31) / 32 * 32);
-  const int clusters = int(GATED ? (N + 63) / 64 : (N + 127) / 128) * a.tiles_m;
-  // parts of K: as many as leave every cluster on the GPU at once, each with at
-  // least four stages (clusters of 8 do not fill it: 16 of them, which would
-  // take 128 of 152 SMs, run in two rounds)
-  a.splits = 1;
-  for (int s = 2; s <= kMaxSplits && a.num_kb >= 4 * s; s *= 2) {
-    int fit = 0;
-    const cudaError_t e = max_clusters(s, &fit);
-    if (e != cudaSuccess) return e;
-    if (clusters > fit) break;
-    a.splits = s;
-  }
-  while (a.splits > 1 && (a.splits - 1) * ((a.num_kb + a.splits - 1) / a.splits) >= a.num_kb) a.splits /= 2;
+  int clusters = 0;
+  const cudaError_t e = few_rows_split(M, N, K, GATED, OP == OP_E4M3, &clusters, &a.splits, &a.num_kb);
+  if (e != cudaSuccess) return e;
   a.stage_bytes = BOX_BYTES + a.bn * ROW_BYTES;
   const bool two = clusters * a.splits > kNumSMsHint && a.bn <= 128;
   a.recv_bytes = (a.splits - 1) * (a.bn / a.splits) * 512;

@@ -710,6 +710,7 @@ cudaError_t launch(const Maps& m, const LinArgs& a, int pairs, cudaStream_t s) {
 struct Plan {
   int tiles_m, tiles_n, tiles, num_kb, narrow, splits, kb_per_split;
   int64_t m_pad;
+  int64_t cycles;            // estimate
 };
 constexpr int kPlanPairs = kNumSMsHint / 2;   // fixed, so a workspace size needs no device query
 // max_narrow: 2, or 1 where B is MN-major (its boxes are 64 columns wide).
@@ -721,6 +722,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
   p.narrow = 0;
   p.splits = 1;
   const int64_t whole = int64_t(p.tiles_m) * ((N + BN - 1) / BN);
+  p.cycles = (whole + kPlanPairs - 1) / kPlanPairs * p.num_kb * 1024 + 4500;
   if (2 * whole <= kPlanPairs) {
     // Less than half a round of whole tiles: the cheapest of narrower units and
     // parts of K, in SM cycles.  A stage of a unit takes the cycles of its MMAs
@@ -743,6 +745,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
         }
       }
     }
+    p.cycles = best;
   }
   p.tiles_n = int((N + (BN >> p.narrow) - 1) / (BN >> p.narrow));
   p.tiles = p.tiles_m * p.tiles_n;
@@ -750,6 +753,13 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
   if (p.num_kb > 0) p.splits = (p.num_kb + p.kb_per_split - 1) / p.kb_per_split;
   return p;
 }
+// Whether few_rows.cu takes a product (N: output columns, gated H).
+bool takes_few_rows(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, bool b_mn) {
+  return few_rows(M, N, K, gated, fp8,
+                  make_plan(M, gated ? 2 * N : N, K, fp8 ? OP_E4M3 : OP_BF16, b_mn ? 1 : 2).cycles);
+}
+// (A workspace size must not depend on the device: above 128 rows it covers the
+// plan whether or not few_rows.cu is taken.)
 size_t plan_bytes(const Plan& p, int64_t N) {
   return p.splits > 1 ? size_t(p.splits) * size_t(p.m_pad) * size_t(N) * sizeof(float) : 0;
 }
@@ -846,7 +856,7 @@ void linear_bwd_offsets(int64_t M, int64_t N, int64_t K, size_t off[4]) {
   off[0] = 0;
   off[1] = round256(size_t(M) * size_t(N) * 2);
   off[2] = off[1] + round256(size_t(act_backward_blocks(M, N)) * size_t(N) * sizeof(float));
-  const size_t a = few_rows(M) ? 0 : plan_bytes(make_plan(M, K, N, OP_BF16, 1), K);
+  const size_t a = M <= 128 ? 0 : plan_bytes(make_plan(M, K, N, OP_BF16, 1), K);
   const size_t b = plan_bytes(make_plan(N, K, M, OP_BF16, 1), K);
   off[3] = off[2] + round256(a > b ? a : b);
 }
@@ -855,8 +865,8 @@ void linear_bwd_offsets(int64_t M, int64_t N, int64_t K, size_t off[4]) {
 void gated_bwd_offsets(int64_t M, int64_t C, int64_t H, size_t off[3]) {
   off[0] = 0;
   off[1] = round256(size_t(M) * size_t(2 * H) * 2);
-  size_t a = few_rows(M) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16, 2), 2 * H);
-  const size_t b = few_rows(M) ? 0 : plan_bytes(make_plan(M, C, 2 * H, OP_BF16, 1), C);
+  size_t a = M <= 128 ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16, 2), 2 * H);
+  const size_t b = M <= 128 ? 0 : plan_bytes(make_plan(M, C, 2 * H, OP_BF16, 1), C);
   const size_t c = plan_bytes(make_plan(2 * H, C, M, OP_BF16, 1), C);
   a = a > b ? a : b;
   off[2] = off[1] + round256(a > c ? a : c);
@@ -865,10 +875,10 @@ void gated_bwd_offsets(int64_t M, int64_t C, int64_t H, size_t off[3]) {
 }  // namespace
 
 size_t linear_workspace(int64_t M, int64_t N, int64_t K, bool fp8) {
-  return few_rows(M) || skinny_rows(M, N, K, fp8) ? 0 : plan_bytes(make_plan(M, N, K, fp8 ? OP_E4M3 : OP_BF16, 2), N);
+  return M <= 128 || skinny_rows(M, N, K, fp8) ? 0 : plan_bytes(make_plan(M, N, K, fp8 ? OP_E4M3 : OP_BF16, 2), N);
 }
 size_t gated_workspace(int64_t M, int64_t C, int64_t H) {
-  return few_rows(M) || skinny_rows(M, 2 * H, C, false) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16, 2), 2 * H);
+  return M <= 128 || skinny_rows(M, 2 * H, C, false) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16, 2), 2 * H);
 }
 size_t linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
   size_t off[4];
@@ -894,7 +904,8 @@ cudaError_t launch_linear(uint16_t* out, uint16_t* z, const uint16_t* x, const u
                           const uint16_t* res, int act, int64_t M, int64_t N, int64_t K, float* ws, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
   if (skinny_rows(M, N, K, false)) return launch_skinny(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, false, s);
-  if (few_rows(M)) return launch_few_rows(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, false, false, s);
+  if (takes_few_rows(M, N, K, false, false, false))
+    return launch_few_rows(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, false, false, s);
   QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_LINEAR, ACT, false, false>(out, z, x, nullptr, w, nullptr, bias, res, M, N,
                                                                         K, ws, s)));
 }
@@ -904,7 +915,8 @@ cudaError_t launch_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, cons
                               int64_t N, int64_t K, float* ws, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
   if (skinny_rows(M, N, K, true)) return launch_skinny(out, z, x, x_scale, w, w_scale, bias, res, act, M, N, K, true, s);
-  if (few_rows(M)) return launch_few_rows(out, z, x, x_scale, w, w_scale, bias, res, act, M, N, K, true, false, s);
+  if (takes_few_rows(M, N, K, false, true, false))
+    return launch_few_rows(out, z, x, x_scale, w, w_scale, bias, res, act, M, N, K, true, false, s);
   QFFN_ACT_SWITCH(act, (product<OP_E4M3, EPI_LINEAR, ACT, false, false>(out, z, x, x_scale, w, w_scale, bias, res, M, N,
                                                                         K, ws, s)));
 }
@@ -913,7 +925,7 @@ cudaError_t launch_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int
                          float* ws, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
   if (skinny_rows(M, 2 * H, C, false)) return launch_skinny_gated(h, x, w1, act, M, C, H, s);
-  if (few_rows(M)) return launch_few_rows_gated(h, x, w1, nullptr, act, M, C, H, s);
+  if (takes_few_rows(M, H, C, true, false, false)) return launch_few_rows_gated(h, x, w1, nullptr, act, M, C, H, s);
   QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_GATED, ACT, false, false>(h, nullptr, x, nullptr, w1, nullptr, nullptr,
                                                                        nullptr, M, H, C, ws, s)));
 }
@@ -931,7 +943,7 @@ cudaError_t act_backward(uint16_t* dz, float* partial, const uint16_t* dout, con
 }
 cudaError_t gated_bwd_product(uint16_t* dgu, const uint16_t* dh, const uint16_t* x, const uint16_t* w1, int act,
                               int64_t M, int64_t C, int64_t H, float* part, cudaStream_t s) {
-  if (few_rows(M)) return launch_few_rows_gated(dgu, x, w1, dh, act, M, C, H, s);
+  if (takes_few_rows(M, H, C, true, false, false)) return launch_few_rows_gated(dgu, x, w1, dh, act, M, C, H, s);
   QFFN_ACT_SWITCH(act, (product<OP_BF16, EPI_GATED_BWD, ACT, false, false>(dgu, nullptr, x, nullptr, w1, nullptr,
                                                                            nullptr, dh, M, H, C, part, s)));
 }
@@ -940,7 +952,8 @@ cudaError_t grad_products(uint16_t* dx, uint16_t* dw, const uint16_t* dz, const 
                           int64_t M, int64_t N, int64_t K, bool accumulate, float* part, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (dx != nullptr) {
-    e = few_rows(M) ? launch_few_rows(dx, nullptr, dz, nullptr, w, nullptr, nullptr, nullptr, ACT_NONE, M, K, N, false,
+    e = takes_few_rows(M, K, N, false, false, true)
+            ? launch_few_rows(dx, nullptr, dz, nullptr, w, nullptr, nullptr, nullptr, ACT_NONE, M, K, N, false,
                                       true, s)
                     : product<OP_BF16, EPI_LINEAR, ACT_NONE, false, true>(dx, nullptr, dz, nullptr, w, nullptr, nullptr,
                                                                           nullptr, M, K, N, part, s);
