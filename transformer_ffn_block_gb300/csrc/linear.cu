@@ -350,6 +350,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int groups = GATED ? acc_cols / 64 : acc_cols / 32;
       // this lane's output rows and column of the group at hand
       auto row_of = [&](int i) { return row0 + sub + 8 * i; };
+      // what a group reads from global memory, requested a group ahead (the
+      // first group's before the accumulator is awaited)
+      uint4 next_bias = make_uint4(0, 0, 0, 0), next_in[4];
+      auto request = [&](int g) {
+        const int col = first_col + g * 32 + ch * 8;
+        const bool col_ok = g < groups && col < args.N;
+        if (EPI == EPI_LINEAR && args.bias != nullptr) next_bias = col_ok ? ld16_ro(args.bias + col) : make_uint4(0, 0, 0, 0);
+        if ((EPI == EPI_LINEAR && args.in != nullptr) || EPI == EPI_GATED_BWD) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            next_in[i] = make_uint4(0, 0, 0, 0);
+            if (col_ok && row_of(i) < args.M)
+              next_in[i] = ld16_once(args.in + size_t(row_of(i)) * size_t(args.N) + size_t(col));
+          }
+        }
+      };
+      request(wg);
       if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) break;
       tc_fence_after();
       // after this warp's last load of the accumulator: hand it back
@@ -357,25 +374,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (g + WG >= groups) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote(map_to_rank(tempty_bar(acc), 0));
+          if (lane == 0) mbar_arrive_remote_relaxed(map_to_rank(tempty_bar(acc), 0));
         }
       };
       if (wg >= groups) loaded(wg);          // (a unit with fewer groups than warps)
       for (int g = wg; g < groups; g += WG) {
         const int col0 = first_col + g * 32, col = col0 + ch * 8;
         if (!GATED) {
-          uint4 bias4 = make_uint4(0, 0, 0, 0), in4[4];
           const bool col_ok = col < args.N;
-          if (EPI == EPI_LINEAR) {
-            if (args.bias != nullptr && col_ok) bias4 = ld16_ro(args.bias + col);
-            if (args.in != nullptr) {
+          uint4 in4[4];
+          const uint4 bias4 = next_bias;
+          if (EPI == EPI_LINEAR && args.in != nullptr) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                in4[i] = make_uint4(0, 0, 0, 0);
-                if (col_ok && row_of(i) < args.M)
-                  in4[i] = ld16_once(args.in + size_t(row_of(i)) * size_t(args.N) + size_t(col));
-              }
-            }
+            for (int i = 0; i < 4; ++i) in4[i] = next_in[i];
           }
           {
             uint32_t v[32];
@@ -387,6 +398,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               *reinterpret_cast<uint4*>(box + off32(lane, c)) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
             __syncwarp();
           }
+          request(g + WG);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(box + off32(sub + 8 * i, 2 * ch));
@@ -423,16 +435,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const size_t ld = EPI == EPI_GATED_BWD ? 2 * size_t(args.N) : size_t(args.N);
           if (EPI == EPI_GATED_BWD) {
             // dh into the box, read back row by row below
-            uint4 d4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              d4[i] = make_uint4(0, 0, 0, 0);
-              if (col_ok && row_of(i) < args.M) d4[i] = ld16_ro(args.in + size_t(row_of(i)) * size_t(args.N) + size_t(col));
-            }
             __syncwarp();                    // the previous group has been read out of the box
 #pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(box + off16(sub + 8 * i, ch)) = d4[i];
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(box + off16(sub + 8 * i, ch)) = next_in[i];
             __syncwarp();
+            request(g + WG);
           } else {
             __syncwarp();
           }

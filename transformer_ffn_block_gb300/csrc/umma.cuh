@@ -68,6 +68,13 @@ QFFN_DEVI void mbar_arrive_remote(uint32_t cluster_addr) {
                : "memory");
 }
 
+// The same without release: for handing back what this thread has only read
+// (TMEM columns whose loads have completed); the release form would wait for
+// the thread's outstanding global stores.
+QFFN_DEVI void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // 2-D tile load whose completion is signalled on a barrier of either CTA of
 // the pair (`bar` is a shared::cluster address).
 QFFN_DEVI void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
