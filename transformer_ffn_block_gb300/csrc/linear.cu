@@ -158,19 +158,22 @@ QFFN_DEVI Unit unit_coords(int u, const LinArgs& a) {
     r.half = (u - a.split_from) & 1;
   }
   // bands of band_n N-blocks; within a band, groups of GROUP_M M-blocks sweep
-  // the band's N-blocks, M fastest, odd groups backwards
+  // the band's N-blocks, M fastest, odd groups backwards.  (Every warp of the
+  // epilogue computes this for every unit, in the open: a division is some 40
+  // instructions, so those that have a known answer are left out.)
   const int band_tiles = a.tiles_m * a.band_n;
-  const int band = tile / band_tiles;
+  const int band = tile < band_tiles ? 0 : tile / band_tiles;
   const int n0 = band * a.band_n;
   const int wb = min(a.band_n, a.tiles_n - n0);
   const int t = tile - band * band_tiles;
   const int per_group = GROUP_M * wb;
-  const int group = t / per_group;
+  const int group = t < per_group ? 0 : t / per_group;
   const int first_m = group * GROUP_M;
   const int gsize = min(a.tiles_m - first_m, GROUP_M);
   const int k = t - group * per_group;
-  r.mb = first_m + k % gsize;
-  r.nb = n0 + ((group & 1) ? wb - 1 - k / gsize : k / gsize);
+  const int col = gsize == GROUP_M ? k / GROUP_M : gsize == 1 ? k : k / gsize;
+  r.mb = first_m + k - col * gsize;
+  r.nb = n0 + ((group & 1) ? wb - 1 - col : col);
   return r;
 }
 
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else {
     // -------------------------------------------------------------- epilogue
     // EPI_WARPS / 4 warps per TMEM lane quarter q (rows 32 q .. 32 q + 31 of
-    // the CTA's 128), which take the unit's groups of 32 output columns in turn.
+    // the CTA's 128), which share the unit's groups of 32 output columns.
     // A TMEM load gives a lane one row's 32 columns; a warp's box of shared
     // memory turns that into the layout of the global accesses, lane l with 8
     // columns (8 (l & 3) ..) of the rows (l >> 2) + 8 i, so that every load and
@@ -331,11 +334,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr int WG = EPI_WARPS / 4;
     const int q = warp & 3, wg = (warp - 2) >> 2;
     const float scale = args.a_scale != nullptr ? args.a_scale[0] * args.w_scale[0] : 1.0f;
-    uint8_t* const box = sStaging + (q * WG + wg) * STAGING_BOX;
-    // 16-byte chunk c of a row of 32 fp32 (128 bytes) or of 32 bf16 (64 bytes)
-    auto off32 = [](int row, int c) { return uint32_t(row) * 128u + (uint32_t(c ^ (row & 7)) << 4); };
-    auto off16 = [](int row, int c) { return uint32_t(row) * 64u + (uint32_t(c ^ ((row >> 1) & 3)) << 4); };
     const int sub = lane >> 2, ch = lane & 3;
+    const uint32_t box = smem_u32(sStaging + (q * WG + wg) * STAGING_BOX);
+    // 32 fp32 columns (rows of 128 bytes, 16-byte chunk c of row r at c ^ (r & 7)):
+    // this lane's row is written at row32 ^ 16 c, its turned share read at
+    // turn32 and turn32 ^ 16, plus 1024 i
+    const uint32_t row32 = box + uint32_t(lane) * 128u + (uint32_t(lane & 7) << 4);
+    const uint32_t turn32 = box + uint32_t(sub) * 128u + (uint32_t((2 * ch) ^ sub) << 4);
+    // 32 bf16 columns (rows of 64 bytes, chunk c of row r at c ^ (r / 2 & 3)): row
+    // at row16 ^ 16 c, turned share at turn16 plus 512 i; a second such box behind
+    const uint32_t row16 = box + uint32_t(lane) * 64u + (uint32_t((lane >> 1) & 3) << 4);
+    const uint32_t turn16 = box + uint32_t(sub) * 64u + (uint32_t(ch ^ ((sub >> 1) & 3)) << 4);
+    constexpr uint32_t kBox2 = 32 * 64;
+    constexpr bool kRead = EPI == EPI_LINEAR || EPI == EPI_GATED_BWD;   // may read a bf16 tensor
     int local = 0;
     for (int un = pair; un < args.num_units; un += num_pairs, ++local) {
       const int acc = local & 1;
@@ -348,42 +359,51 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * BN);
       const int acc_cols = u.half < 0 ? bn : BN / 2;
       const int groups = GATED ? acc_cols / 64 : acc_cols / 32;
-      // this lane's output rows and column of the group at hand
-      auto row_of = [&](int i) { return row0 + sub + 8 * i; };
+      // this warp's groups, next to each other: whole 128-byte lines from one
+      // warp (interleaved groups: 8192 x 8192 x 64 with a residual 80 us, so 73)
+      const int share = (groups + WG - 1) / WG, g0 = wg * share, g1 = min(groups, g0 + share);
+      // this lane's part of the global accesses: rows row0 + sub + 8 i (bit i of
+      // `rows`: there is one), element offset of the first at the group's column
+      uint32_t rows = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rows |= (row0 + sub + 8 * i < args.M ? 1u : 0u) << i;
+      const size_t at = size_t(row0 + sub) * size_t(args.N) + size_t(first_col + ch * 8);
+      const size_t step = size_t(8) * size_t(args.N);
       // what a group reads from global memory, requested a group ahead (the
       // first group's before the accumulator is awaited)
       uint4 next_bias = make_uint4(0, 0, 0, 0), next_in[4];
       auto request = [&](int g) {
-        const int col = first_col + g * 32 + ch * 8;
-        const bool col_ok = g < groups && col < args.N;
-        if (EPI == EPI_LINEAR && args.bias != nullptr) next_bias = col_ok ? ld16_ro(args.bias + col) : make_uint4(0, 0, 0, 0);
-        if ((EPI == EPI_LINEAR && args.in != nullptr) || EPI == EPI_GATED_BWD) {
+        const uint32_t live = g < g1 && first_col + g * 32 + ch * 8 < args.N ? rows : 0u;
+        if (EPI == EPI_LINEAR && args.bias != nullptr)
+          next_bias = live != 0u ? ld16_ro(args.bias + first_col + g * 32 + ch * 8) : make_uint4(0, 0, 0, 0);
+        if (kRead && args.in != nullptr) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             next_in[i] = make_uint4(0, 0, 0, 0);
-            if (col_ok && row_of(i) < args.M)
-              next_in[i] = ld16_once(args.in + size_t(row_of(i)) * size_t(args.N) + size_t(col));
+            if ((live >> i) & 1u) next_in[i] = ld16_once(args.in + (at + size_t(g * 32) + size_t(i) * step));
           }
         }
       };
-      request(wg);
+      if (kRead) request(g0);
       if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) break;
       tc_fence_after();
       // after this warp's last load of the accumulator: hand it back
       auto loaded = [&](int g) {
-        if (g + WG >= groups) {
+        if (g + 1 >= g1) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_remote_relaxed(map_to_rank(tempty_bar(acc), 0));
         }
       };
-      if (wg >= groups) loaded(wg);          // (a unit with fewer groups than warps)
-      for (int g = wg; g < groups; g += WG) {
-        const int col0 = first_col + g * 32, col = col0 + ch * 8;
+      if (g0 >= g1) loaded(g0);              // (a unit with fewer groups than warps)
+      for (int g = g0; g < g1; ++g) {
+        const uint32_t live = first_col + g * 32 + ch * 8 < args.N ? rows : 0u;
         if (!GATED) {
-          const bool col_ok = col < args.N;
           uint4 in4[4];
-          const uint4 bias4 = next_bias;
+          uint64_t bias[4];
+          const uint32_t bw[4] = {next_bias.x, next_bias.y, next_bias.z, next_bias.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) bias[j] = bf16x2_to_f2(bw[j]);
           if (EPI == EPI_LINEAR && args.in != nullptr) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) in4[i] = next_in[i];
@@ -395,56 +415,78 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             __syncwarp();                    // the previous group has been read out of the box
 #pragma unroll
             for (int c = 0; c < 8; ++c)
-              *reinterpret_cast<uint4*>(box + off32(lane, c)) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+              sts16(row32 ^ uint32_t(16 * c), make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
             __syncwarp();
           }
-          request(g + WG);
+          if (kRead) request(g + 1);
+          const size_t o = EPI == EPI_PARTIAL
+                               ? (size_t(u.sp) * size_t(args.m_pad)) * size_t(args.N) + at + size_t(g * 32)
+                               : at + size_t(g * 32);
+          uint4 los[4], his[4];              // all reads issued before the first is used
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const ulonglong2 lo = *reinterpret_cast<const ulonglong2*>(box + off32(sub + 8 * i, 2 * ch));
-            const ulonglong2 hi = *reinterpret_cast<const ulonglong2*>(box + off32(sub + 8 * i, 2 * ch + 1));
-            const bool live = col_ok && row_of(i) < args.M;
-            if (EPI == EPI_PARTIAL) {
-              float* dst = args.partial + (size_t(u.sp) * size_t(args.m_pad) + size_t(row_of(i))) * size_t(args.N) + size_t(col);
-              if (live) {
-                reinterpret_cast<ulonglong2*>(dst)[0] = lo;
-                reinterpret_cast<ulonglong2*>(dst)[1] = hi;
-              }
-            } else {
-              uint64_t z[4] = {lo.x, lo.y, hi.x, hi.y};
-              const uint32_t bw[4] = {bias4.x, bias4.y, bias4.z, bias4.w};
-              const size_t o = size_t(row_of(i)) * size_t(args.N) + size_t(col);
+            los[i] = lds16(turn32 + 1024u * i);
+            his[i] = lds16((turn32 ^ 16u) + 1024u * i);
+          }
+          if (EPI == EPI_PARTIAL) {
+            float* const dst = args.partial + o;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                if (OP == OP_E4M3) z[j] = f2_mul(z[j], f2_dup(scale));
-                z[j] = f2_add(z[j], bf16x2_to_f2(bw[j]));
+            for (int i = 0; i < 4; ++i)
+              if ((live >> i) & 1u) {
+                stg16(dst + size_t(i) * step, los[i]);
+                stg16(dst + size_t(i) * step + 4, his[i]);
               }
-              if (args.z != nullptr && live) stg16(args.z + o, pack8(z));
+          } else {
+            // each step over all four rows: sixteen independent pairs, so that the
+            // two warps of a scheduler cover the latencies of the activation
+            uint64_t z[4][4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) z[j] = act_f2<ACT>(z[j]);
-              if (args.in != nullptr) {
+            for (int i = 0; i < 4; ++i) {
+              z[i][0] = f2_pack(__uint_as_float(los[i].x), __uint_as_float(los[i].y));
+              z[i][1] = f2_pack(__uint_as_float(los[i].z), __uint_as_float(los[i].w));
+              z[i][2] = f2_pack(__uint_as_float(his[i].x), __uint_as_float(his[i].y));
+              z[i][3] = f2_pack(__uint_as_float(his[i].z), __uint_as_float(his[i].w));
+              if (OP == OP_E4M3) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[i][j] = f2_mul(z[i][j], f2_dup(scale));
+              }
+            }
+            if (args.bias != nullptr) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[i][j] = f2_add(z[i][j], bias[j]);
+            }
+            if (args.z != nullptr) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if ((live >> i) & 1u) stg16(args.z + (o + size_t(i) * step), pack8(z[i]));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) z[i][j] = act_f2<ACT>(z[i][j]);
+            if (args.in != nullptr) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
                 const uint32_t iw[4] = {in4[i].x, in4[i].y, in4[i].z, in4[i].w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bf16x2_to_f2(iw[j]));
+                for (int j = 0; j < 4; ++j) z[i][j] = f2_add(z[i][j], bf16x2_to_f2(iw[j]));
               }
-              if (live) stg16(args.out + o, pack8(z));
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((live >> i) & 1u) stg16(args.out + (o + size_t(i) * step), pack8(z[i]));
           }
         } else {
-          const bool col_ok = col < args.N;
-          const size_t ld = EPI == EPI_GATED_BWD ? 2 * size_t(args.N) : size_t(args.N);
+          __syncwarp();                      // the previous group has been read out of the boxes
           if (EPI == EPI_GATED_BWD) {
             // dh into the box, read back row by row below
-            __syncwarp();                    // the previous group has been read out of the box
 #pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(box + off16(sub + 8 * i, ch)) = next_in[i];
+            for (int i = 0; i < 4; ++i) sts16(turn16 + 512u * i, next_in[i]);
             __syncwarp();
-            request(g + WG);
-          } else {
-            __syncwarp();
+            request(g + 1);
           }
-          // second bf16 box (du) behind the first
-          uint8_t* const box2 = box + 32 * 64;
           const int up_off = acc_cols / 2;   // accumulator column of u
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
@@ -455,9 +497,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (h == 1) loaded(g);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+              const uint32_t off = row16 ^ uint32_t(16 * (h * 2 + k));
               uint32_t p[4], p2[4];
               uint4 d4 = make_uint4(0, 0, 0, 0);
-              if (EPI == EPI_GATED_BWD) d4 = *reinterpret_cast<const uint4*>(box + off16(lane, h * 2 + k));
+              if (EPI == EPI_GATED_BWD) d4 = lds16(off);
               const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
@@ -473,19 +516,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                   p2[j] = pack2(f2_mul(d, f));
                 }
               }
-              *reinterpret_cast<uint4*>(box + off16(lane, h * 2 + k)) = make_uint4(p[0], p[1], p[2], p[3]);
-              if (EPI == EPI_GATED_BWD)
-                *reinterpret_cast<uint4*>(box2 + off16(lane, h * 2 + k)) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+              sts16(off, make_uint4(p[0], p[1], p[2], p[3]));
+              if (EPI == EPI_GATED_BWD) sts16(off + kBox2, make_uint4(p2[0], p2[1], p2[2], p2[3]));
             }
           }
           __syncwarp();
+          // d_gu has rows of 2 N
+          uint16_t* const dst = EPI == EPI_GATED_BWD
+                                    ? args.out + (at + size_t(row0 + sub) * size_t(args.N) + size_t(g * 32))
+                                    : args.out + (at + size_t(g * 32));
+          const size_t dstep = EPI == EPI_GATED_BWD ? 2 * step : step;
+          uint4 first[4], second[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if (!col_ok || row_of(i) >= args.M) continue;
-            uint16_t* dst = args.out + size_t(row_of(i)) * ld + size_t(col);
-            stg16(dst, *reinterpret_cast<const uint4*>(box + off16(sub + 8 * i, ch)));
-            if (EPI == EPI_GATED_BWD)
-              stg16(dst + args.N, *reinterpret_cast<const uint4*>(box2 + off16(sub + 8 * i, ch)));
+            first[i] = lds16(turn16 + 512u * i);
+            if (EPI == EPI_GATED_BWD) second[i] = lds16(turn16 + 512u * i + kBox2);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (((live >> i) & 1u) == 0u) continue;
+            stg16(dst + size_t(i) * dstep, first[i]);
+            if (EPI == EPI_GATED_BWD) stg16(dst + size_t(i) * dstep + args.N, second[i]);
           }
         }
       }
