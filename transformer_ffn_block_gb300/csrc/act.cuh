@@ -1,8 +1,8 @@
 // Activations of the linear and gated forms, in fp32, and their derivatives.
 //
-// ACT values are those of QFFN_ACT_* (include/qffn.h).  The sigmoid is formed
-// from e = exp(-|v|) in (0, 1], so neither branch overflows and the small
-// values of the negative branch keep their relative accuracy.  NaN propagates;
+// ACT values are those of QFFN_ACT_* (include/qffn.h).  The sigmoid is 1 / (1 +
+// exp(-v)): for negative v the sum is dominated by the exponential, so the small
+// values keep their relative accuracy, and below -87 it is 0.  NaN propagates;
 // relu'(0) = 0.
 #pragma once
 
@@ -28,9 +28,7 @@ QFFN_DEVI float rcp_f32(float v) {
 constexpr float kLog2e = 1.4426950408889634f;
 
 QFFN_DEVI float sigmoid_f32(float v) {
-  const float e = exp2_f32(-kLog2e * fabsf(v));
-  const float r = rcp_f32(1.0f + e);
-  return v >= 0.0f ? r : e * r;
+  return rcp_f32(1.0f + exp2_f32(-kLog2e * v));
 }
 
 constexpr float kGeluTanhScale = 1.5957691216057308f;   // 2 sqrt(2 / pi)
@@ -106,13 +104,9 @@ QFFN_DEVI uint64_t f2_abs(uint64_t v) { return v & 0x7FFFFFFF7FFFFFFFull; }
 
 QFFN_DEVI uint64_t sigmoid_f2(uint64_t v) {
   float a, b, da, db;
-  f2_unpack(v, a, b);
-  const uint64_t e = f2_pack(exp2_f32(-kLog2e * fabsf(a)), exp2_f32(-kLog2e * fabsf(b)));
-  f2_unpack(f2_add(f2_dup(1.0f), e), da, db);
-  const float ra = rcp_f32(da), rb = rcp_f32(db);
-  float la, lb;
-  f2_unpack(f2_mul(e, f2_pack(ra, rb)), la, lb);
-  return f2_pack(a >= 0.0f ? ra : la, b >= 0.0f ? rb : lb);
+  f2_unpack(f2_mul(f2_dup(-kLog2e), v), a, b);
+  f2_unpack(f2_add(f2_dup(1.0f), f2_pack(exp2_f32(a), exp2_f32(b))), da, db);
+  return f2_pack(rcp_f32(da), rcp_f32(db));
 }
 
 QFFN_DEVI uint64_t normal_cdf_f2(uint64_t z, uint64_t& gauss) {

@@ -509,21 +509,27 @@ cudaError_t few_rows_split(int64_t M, int64_t N, int64_t K, bool gated, bool fp8
   while (*splits > 1 && (*splits - 1) * ((*num_kb + *splits - 1) / *splits) >= *num_kb) *splits /= 2;
   return cudaSuccess;
 }
+
+// Rows per tile: the rows spread evenly over tiles of at most 128, in steps of 32.
+int few_rows_bn(int64_t M) {
+  const int64_t tiles = (M + 127) / 128;
+  return int(((M + tiles - 1) / tiles + 31) / 32 * 32);
+}
 }  // namespace
 
-// Up to 128 rows the 256-row tiles of linear.cu are mostly padding.  Up to 512
-// rows it goes by an estimate of both in SM cycles: here about 640 cycles per
-// stage and round of clusters and 5500 to set up, exchange and store; there 1.4
-// times the plan's cycles.  Measured in us, here against there: 256 rows of 4096
-// x 4096 17.1 / 20.0, of 2048 x 2048 9.9 / 11.9, of 8192 x 2048 16.5 / 14.3, of
-// 4096 x 14336 42 / 36, of 28672 x 4096 68 / 51.
+// Up to 512 rows, by an estimate of both forms in SM cycles: here about 640 per
+// stage and round of clusters, 48 per row of a tile for its sums and stores, and
+// 4000 for an exchange; there 1.4 times the plan's cycles.  Measured in us, here
+// against there: 64 rows of 4096 x 1024 7.0 / 7.8, 128 rows 9.1 / 7.8, of 4096 x
+// 4096 13.4 / 20, 256 rows 17.1 / 20, of 2048 x 2048 9.9 / 11.7, of 8192 x 2048
+// 16.5 / 13.5, of 4096 x 14336 42 / 36, of 28672 x 4096 68 / 49.
 bool few_rows(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, int64_t other_cycles) {
-  if (M <= 128) return true;
   if (M > 512) return false;
   int clusters, splits, num_kb;
   if (few_rows_split(M, N, K, gated, fp8, &clusters, &splits, &num_kb) != cudaSuccess) return false;
   const int64_t rounds = (int64_t(clusters) * splits + kNumSMsHint - 1) / kNumSMsHint;
-  return 10 * (rounds * ((num_kb + splits - 1) / splits) * 640 + 5500) < 14 * other_cycles;
+  const int64_t here = rounds * ((num_kb + splits - 1) / splits) * 640 + 48 * few_rows_bn(M) - 700 + (splits > 1 ? 4000 : 0);
+  return 10 * here < 14 * other_cycles + 6000;
 }
 
 // One product: x [M, K] (K-major), W [wrows, K] or, w_mn, [K, wrows].
@@ -543,7 +549,7 @@ cudaError_t few_rows_product(uint16_t* out, uint16_t* z, const void* x, const fl
   a.M = int(M);
   a.N = int(N);
   a.tiles_m = int((M + 127) / 128);
-  a.bn = int(((M + a.tiles_m - 1) / a.tiles_m + 31) / 32 * 32);
+  a.bn = few_rows_bn(M);
   int clusters = 0;
   const cudaError_t e = few_rows_split(M, N, K, GATED, OP == OP_E4M3, &clusters, &a.splits, &a.num_kb);
   if (e != cudaSuccess) return e;

@@ -171,7 +171,7 @@ cudaError_t launch_skinny_gated(uint16_t* h, const uint16_t* x, const uint16_t* 
                                 int64_t H, cudaStream_t s);
 // The forms for few rows on the tensor cores (few_rows.cu), taken where few_rows()
 // and, forward, not skinny_rows(); other_cycles: linear.cu's estimate for the
-// same product (used above 128 rows).  No workspace.  w_mn: w given as [K, N]
+// same product.  No workspace.  w_mn: w given as [K, N]
 // (bf16).  Gated: h from w1 = [2H, C], or, with dh, d_gu [M, 2H].
 bool few_rows(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, int64_t other_cycles);
 cudaError_t launch_few_rows(uint16_t* out, uint16_t* z, const void* x, const float* x_scale, const void* w,

@@ -816,8 +816,8 @@ bool takes_few_rows(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, bool 
   return few_rows(M, N, K, gated, fp8,
                   make_plan(M, gated ? 2 * N : N, K, fp8 ? OP_E4M3 : OP_BF16, b_mn ? 1 : 2).cycles);
 }
-// (A workspace size must not depend on the device: above 128 rows it covers the
-// plan whether or not few_rows.cu is taken.)
+// (A workspace size must not depend on the device: it covers the plan whether or
+// not few_rows.cu is taken.)
 size_t plan_bytes(const Plan& p, int64_t N) {
   return p.splits > 1 ? size_t(p.splits) * size_t(p.m_pad) * size_t(N) * sizeof(float) : 0;
 }
@@ -914,7 +914,7 @@ void linear_bwd_offsets(int64_t M, int64_t N, int64_t K, size_t off[4]) {
   off[0] = 0;
   off[1] = round256(size_t(M) * size_t(N) * 2);
   off[2] = off[1] + round256(size_t(act_backward_blocks(M, N)) * size_t(N) * sizeof(float));
-  const size_t a = M <= 128 ? 0 : plan_bytes(make_plan(M, K, N, OP_BF16, 1), K);
+  const size_t a = plan_bytes(make_plan(M, K, N, OP_BF16, 1), K);
   const size_t b = plan_bytes(make_plan(N, K, M, OP_BF16, 1), K);
   off[3] = off[2] + round256(a > b ? a : b);
 }
@@ -923,8 +923,8 @@ void linear_bwd_offsets(int64_t M, int64_t N, int64_t K, size_t off[4]) {
 void gated_bwd_offsets(int64_t M, int64_t C, int64_t H, size_t off[3]) {
   off[0] = 0;
   off[1] = round256(size_t(M) * size_t(2 * H) * 2);
-  size_t a = M <= 128 ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16, 2), 2 * H);
-  const size_t b = M <= 128 ? 0 : plan_bytes(make_plan(M, C, 2 * H, OP_BF16, 1), C);
+  size_t a = plan_bytes(make_plan(M, 2 * H, C, OP_BF16, 2), 2 * H);
+  const size_t b = plan_bytes(make_plan(M, C, 2 * H, OP_BF16, 1), C);
   const size_t c = plan_bytes(make_plan(2 * H, C, M, OP_BF16, 1), C);
   a = a > b ? a : b;
   off[2] = off[1] + round256(a > c ? a : c);
@@ -933,10 +933,10 @@ void gated_bwd_offsets(int64_t M, int64_t C, int64_t H, size_t off[3]) {
 }  // namespace
 
 size_t linear_workspace(int64_t M, int64_t N, int64_t K, bool fp8) {
-  return M <= 128 || skinny_rows(M, N, K, fp8) ? 0 : plan_bytes(make_plan(M, N, K, fp8 ? OP_E4M3 : OP_BF16, 2), N);
+  return skinny_rows(M, N, K, fp8) ? 0 : plan_bytes(make_plan(M, N, K, fp8 ? OP_E4M3 : OP_BF16, 2), N);
 }
 size_t gated_workspace(int64_t M, int64_t C, int64_t H) {
-  return M <= 128 || skinny_rows(M, 2 * H, C, false) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16, 2), 2 * H);
+  return skinny_rows(M, 2 * H, C, false) ? 0 : plan_bytes(make_plan(M, 2 * H, C, OP_BF16, 2), 2 * H);
 }
 size_t linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
   size_t off[4];

@@ -184,7 +184,7 @@ cudaError_t run(const SkinnyArgs& a, cudaStream_t s) {
 bool skinny_rows(int64_t M, int64_t wrows, int64_t K, bool fp8) {
   if (M <= 16) return true;
   const int64_t ctas = (wrows + 15) / 16 * ((M + 31) / 32);
-  return ctas * (K + 550) <= (fp8 ? 400000 : 700000);
+  return ctas * (K + 550) <= (fp8 ? 400000 : 600000);
 }
 
 cudaError_t launch_skinny(uint16_t* out, uint16_t* z, const void* x, const float* x_scale, const void* w,
