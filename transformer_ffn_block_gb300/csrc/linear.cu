@@ -640,11 +640,13 @@ __global__ void __launch_bounds__(256) join_kernel(uint16_t* out, uint16_t* out2
 // (8 * gridDim.y)-th group of rows; thread (warp w, lane l) owns columns
 // 8 l .. 8 l + 7 of rows w, w + 8, ...  The column sums are taken from the fp32
 // dz before its rounding; the block's eight warps are added in order and
-// column_sum_kernel adds the blocks'.  ACT_NONE (dz = dout) only sums.
+// column_sum_kernel adds the blocks' (few rows take one block per 256 columns,
+// which writes dbias itself).  ACT_NONE (dz = dout) only sums.
 constexpr int kRowsInFlight = 4;           // loads issued per thread before the first is used
 template <int ACT>
-__global__ void __launch_bounds__(256) act_backward_kernel(uint16_t* dz, float* partial, const uint16_t* dout,
-                                                           const uint16_t* z, int64_t M, int64_t N) {
+__global__ void __launch_bounds__(256) act_backward_kernel(uint16_t* dz, float* partial, float* dbias,
+                                                           const uint16_t* dout, const uint16_t* z, int64_t M,
+                                                           int64_t N, int accumulate) {
   __shared__ __align__(8) float comb[8][256 + 8];
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
   const int64_t col = int64_t(blockIdx.x) * 256 + l * 8;
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(256) act_backward_kernel(uint16_t* dz, float* 
       }
     }
   }
-  if (partial == nullptr) return;
+  if (dbias == nullptr) return;
 #pragma unroll
   for (int j = 0; j < 4; ++j) *reinterpret_cast<uint64_t*>(&comb[w][l * 8 + 2 * j]) = s[j];
   __syncthreads();
@@ -694,7 +696,8 @@ __global__ void __launch_bounds__(256) act_backward_kernel(uint16_t* dz, float* 
   if (c < N) {
     float v = comb[0][threadIdx.x];
     for (int k = 1; k < 8; ++k) v += comb[k][threadIdx.x];
-    partial[size_t(blockIdx.y) * size_t(N) + size_t(c)] = v;
+    if (gridDim.y > 1) partial[size_t(blockIdx.y) * size_t(N) + size_t(c)] = v;
+    else dbias[c] = accumulate ? dbias[c] + v : v;
   }
 }
 
@@ -900,6 +903,7 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
 }
 
 int act_backward_blocks(int64_t M, int64_t N) {
+  if (M <= 64) return 1;
   const int64_t cols = (N + 255) / 256;
   int64_t rows = (int64_t(kNumSMsHint) * 8 + cols - 1) / cols;   // about eight blocks per SM
   const int64_t need = (M + 7) / 8;
@@ -990,14 +994,14 @@ cudaError_t launch_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int
 
 namespace {
 template <int ACT>
-cudaError_t run_act_backward(uint16_t* dz, float* partial, const uint16_t* dout, const uint16_t* z, int64_t M,
-                             int64_t N, cudaStream_t s) {
+cudaError_t run_act_backward(uint16_t* dz, float* partial, float* dbias, const uint16_t* dout, const uint16_t* z,
+                             int64_t M, int64_t N, bool accumulate, cudaStream_t s) {
   const dim3 grid(unsigned((N + 255) / 256), unsigned(act_backward_blocks(M, N)));
-  return launch_pdl(act_backward_kernel<ACT>, grid, 256, 0, s, dz, partial, dout, z, M, N);
+  return launch_pdl(act_backward_kernel<ACT>, grid, 256, 0, s, dz, partial, dbias, dout, z, M, N, accumulate ? 1 : 0);
 }
-cudaError_t act_backward(uint16_t* dz, float* partial, const uint16_t* dout, const uint16_t* z, int act, int64_t M,
-                         int64_t N, cudaStream_t s) {
-  QFFN_ACT_SWITCH(act, (run_act_backward<ACT>(dz, partial, dout, z, M, N, s)));
+cudaError_t act_backward(uint16_t* dz, float* partial, float* dbias, const uint16_t* dout, const uint16_t* z, int act,
+                         int64_t M, int64_t N, bool accumulate, cudaStream_t s) {
+  QFFN_ACT_SWITCH(act, (run_act_backward<ACT>(dz, partial, dbias, dout, z, M, N, accumulate, s)));
 }
 cudaError_t gated_bwd_product(uint16_t* dgu, const uint16_t* dh, const uint16_t* x, const uint16_t* w1, int act,
                               int64_t M, int64_t C, int64_t H, float* part, cudaStream_t s) {
@@ -1039,8 +1043,8 @@ cudaError_t launch_linear_backward(uint16_t* dx, uint16_t* dw, float* dbias, con
   float* part = reinterpret_cast<float*>(ws + off[2]);
   const uint16_t* dz = act == ACT_NONE ? dout : dzb;
   if (act != ACT_NONE || dbias != nullptr) {
-    if ((e = act_backward(dzb, dbias != nullptr ? cols : nullptr, dout, z, act, M, N, s)) != cudaSuccess) return e;
-    if (dbias != nullptr) {
+    if ((e = act_backward(dzb, cols, dbias, dout, z, act, M, N, accumulate, s)) != cudaSuccess) return e;
+    if (dbias != nullptr && act_backward_blocks(M, N) > 1) {
       if ((e = launch_column_sum(dbias, nullptr, cols, act_backward_blocks(M, N), N, N, accumulate, s)) != cudaSuccess)
         return e;
     }

@@ -432,6 +432,111 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const NormBwd a) {
     }
 }
 
+// Few rows: one launch.  Block b < N does row b; the blocks behind do 64 columns
+// each of dgain and dshift, which need the given statistics only and read dy and
+// r again (from L2).  Eight threads cover a row's 64 columns, T / 8 rows at a
+// time, four loads in flight each; the partial sums are added in a fixed order.
+template <bool CENTRED, int T>
+__global__ void __launch_bounds__(T) norm_backward_short_kernel(const NormBwd a, float* dgain, float* dshift,
+                                                                int accumulate) {
+  __shared__ float red[64];
+  __shared__ float comb[2][T / 32][64];
+  const int t = threadIdx.x;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  pdl_wait();
+  pdl_trigger();
+  if (int64_t(blockIdx.x) < a.N) {
+    constexpr int V = 2;
+    const int64_t row = blockIdx.x;
+    const size_t base = size_t(row) * size_t(a.C);
+    const int nchunk = a.C >> 3;
+    const float mu = CENTRED ? a.mean[row] : 0.0f, rs = a.rstd[row];
+    uint4 dv[V], rv[V], ev[V], gv[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * T;
+      dv[i] = rv[i] = ev[i] = gv[i] = zero;
+      if (c < nchunk) {
+        dv[i] = ld16_once(a.dy + base + size_t(c) * 8);
+        rv[i] = ld16_once(a.r + base + size_t(c) * 8);
+        gv[i] = ld16_ro(a.gain + size_t(c) * 8);
+        if (a.dres != nullptr) ev[i] = ld16_once(a.dres + base + size_t(c) * 8);
+      }
+    }
+    const uint64_t rs2 = f2_dup(rs), nm2 = f2_dup(-mu * rs);
+    uint64_t p1 = 0ull, p2 = 0ull, dg[4] = {0ull, 0ull, 0ull, 0ull}, ds[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+    for (int i = 0; i < V; ++i) norm_sums8<CENTRED>(dv[i], rv[i], gv[i], rs2, nm2, p1, p2, dg, ds);
+    float s1 = f2_sum(p1), s2 = f2_sum(p2);
+    team_sum2<T>(s1, s2, red);
+    const float inv_c = 1.0f / float(a.C);
+    const uint64_t k1 = f2_dup(-rs * (s1 * inv_c)), k2 = f2_dup(-rs * (s2 * inv_c));
+    uint32_t amax = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * T;
+      if (c < nchunk) {
+        const uint4 o = norm_dx8<CENTRED>(dv[i], rv[i], gv[i], ev[i], rs2, nm2, k1, k2);
+        stg16(a.dx + base + size_t(c) * 8, o);
+        if (a.stats != nullptr) amax = absmax8(amax, o);
+      }
+    }
+    if (a.stats != nullptr) record_absmax(a.stats, amax);
+    return;
+  }
+  constexpr int kRows = T / 8, kFlight = 4;
+  const int64_t col = (int64_t(blockIdx.x) - a.N) * 64 + (t & 7) * 8;
+  uint64_t dg[4] = {0ull, 0ull, 0ull, 0ull}, ds[4] = {0ull, 0ull, 0ull, 0ull}, unused1 = 0ull, unused2 = 0ull;
+  if (col < a.C) {
+    for (int64_t row0 = t >> 3; row0 < a.N; row0 += kRows * kFlight) {
+      uint4 dv[kFlight], rv[kFlight];
+      float mu[kFlight], rs[kFlight];
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) {
+        const int64_t row = row0 + k * kRows;
+        const bool live = row < a.N;
+        const size_t i = size_t(live ? row : 0) * size_t(a.C) + size_t(col);
+        dv[k] = live ? ld16_once(a.dy + i) : zero;
+        rv[k] = live ? ld16_once(a.r + i) : zero;
+        mu[k] = CENTRED && live ? a.mean[row] : 0.0f;
+        rs[k] = live ? a.rstd[row] : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k)
+        if (row0 + k * kRows < a.N)
+          norm_sums8<CENTRED>(dv[k], rv[k], zero, f2_dup(rs[k]), f2_dup(-mu[k] * rs[k]), unused1, unused2, dg, ds);
+    }
+  }
+  // the four rows of a warp, then the warps in order
+  const int warp = t >> 5, lane = t & 31;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float v[4];
+    f2_unpack(dg[j], v[0], v[1]);
+    f2_unpack(ds[j], v[2], v[3]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] += __shfl_xor_sync(0xffffffffu, v[k], 8);
+      v[k] += __shfl_xor_sync(0xffffffffu, v[k], 16);
+    }
+    if (lane < 8) {
+      comb[0][warp][lane * 8 + 2 * j] = v[0];
+      comb[0][warp][lane * 8 + 2 * j + 1] = v[1];
+      comb[1][warp][lane * 8 + 2 * j] = v[2];
+      comb[1][warp][lane * 8 + 2 * j + 1] = v[3];
+    }
+  }
+  __syncthreads();
+  const int which = t >> 6, c = t & 63;      // threads 0 .. 63 dgain, 64 .. 127 dshift
+  const int64_t out = (int64_t(blockIdx.x) - a.N) * 64 + c;
+  float* const dst = which == 0 ? dgain : which == 1 ? dshift : nullptr;
+  if (dst != nullptr && out < a.C) {
+    float v = comb[which][0][c];
+    for (int w = 1; w < T / 32; ++w) v += comb[which][w][c];
+    dst[out] = accumulate ? dst[out] + v : v;
+  }
+}
+
 // out[c] (+)= sum over p of partial[p][c]: 32 groups of parts, p in order within
 // each and eight loads in flight, the groups added in order.  32 columns per
 // block.
@@ -517,6 +622,21 @@ cudaError_t norm_backward(const NormBwd& a, int blocks, cudaStream_t s) {
   return run_ring<CENTRED, 512, 4>(a, blocks, s);
 }
 
+// Up to this many rows one launch that reads dy and r twice beats two (layer norm,
+// us, one launch against two: 77 x 2048 2.1 / 5.2, about 512 x 4096 7.8 / 10.5,
+// 512 x 1024 7.0 / 6.7, 512 x 256 4.9 / 3.9).
+int64_t short_rows(int C) { return C <= 512 ? 256 : 512; }
+
+template <bool CENTRED>
+cudaError_t norm_backward_short(const NormBwd& a, float* dgain, float* dshift, bool accumulate, cudaStream_t s) {
+  const dim3 grid(unsigned(a.N + (a.C + 63) / 64));
+  const int acc = accumulate ? 1 : 0;
+  if (a.C <= 2048) return launch_pdl(norm_backward_short_kernel<CENTRED, 128>, grid, 128, 0, s, a, dgain, dshift, acc);
+  if (a.C <= 4096) return launch_pdl(norm_backward_short_kernel<CENTRED, 256>, grid, 256, 0, s, a, dgain, dshift, acc);
+  if (a.C <= 8192) return launch_pdl(norm_backward_short_kernel<CENTRED, 512>, grid, 512, 0, s, a, dgain, dshift, acc);
+  return launch_pdl(norm_backward_short_kernel<CENTRED, 1024>, grid, 1024, 0, s, a, dgain, dshift, acc);
+}
+
 }  // namespace
 
 int norm_backward_blocks(int64_t N, int C) {
@@ -578,6 +698,11 @@ cudaError_t launch_norm_backward(uint16_t* dx, float* dgain, float* dshift, floa
     if (accumulate) return cudaSuccess;
     if ((e = cudaMemsetAsync(dgain, 0, size_t(C) * sizeof(float), s)) != cudaSuccess) return e;
     return dshift != nullptr ? cudaMemsetAsync(dshift, 0, size_t(C) * sizeof(float), s) : cudaSuccess;
+  }
+  if (N <= short_rows(C) && dx != dy) {         // (its column sums read dy while rows of dx are written)
+    const NormBwd b{dx, nullptr, stats, dy, dres, r, mean, rstd, gain, N, C, 0};
+    return centred ? norm_backward_short<true>(b, dgain, dshift, accumulate, s)
+                   : norm_backward_short<false>(b, dgain, nullptr, accumulate, s);
   }
   const int blocks = norm_backward_blocks(N, C);
   const NormBwd a{dx, partial, stats, dy, dres, r, mean, rstd, gain, N, C, 0};
