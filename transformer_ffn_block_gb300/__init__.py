@@ -160,7 +160,7 @@ def _load_torch():
 def _current_device():
     if _torch is None:
         _load_torch()
-    return _torch._C._cuda_getDevice() if _has_gpu else -1
+    return _torch._C._cuda_getDevice() if _has_gpu else -2        # (-1 is a CPU tensor's)
 
 
 def _workspace(fn, device, workspace, workspace_bytes):
