@@ -138,50 +138,53 @@ def _ptr(t):
 def _buf(fn, device, name, t, size, n):
     """_ptr of a tensor after the checks that a bare address cannot have: ``n`` elements of
     ``size`` bytes at least, contiguous, on the current device."""
-    if t is None or isinstance(t, int):
+    if t is None:
+        return None
+    if t.__class__ is int:
         return t
-    if t.element_size() != size or t.numel() < n or not t.is_contiguous() or (n and t.get_device() != device):
-        raise QffnError(fn, 1, f"{name}: expected {n} contiguous elements of {size} bytes on cuda:{device}, got "
-                               f"{tuple(t.shape)} {t.dtype} on {t.device}"
-                               f"{'' if t.is_contiguous() else ', not contiguous'}")
-    return t.data_ptr()
+    if t.is_contiguous() and t.element_size() == size and t.numel() >= n and (t.get_device() == device or n <= 0):
+        return t.data_ptr()
+    raise QffnError(fn, 1, f"{name}: expected {n} contiguous elements of {size} bytes on cuda:{device}, got "
+                           f"{tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
 _torch = None                # imported on first use: the raw-address calls do not need it
-_has_gpu = False
+_get_device = _get_stream = None
 
 
 def _load_torch():
-    global _torch, _has_gpu
+    global _torch, _get_device, _get_stream
     import torch
-    _torch, _has_gpu = torch, torch.cuda.is_available()
+    _torch = torch
+    if torch.cuda.is_available():
+        torch.cuda.init()
+        _get_device, _get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _current_device():
+    if _get_device is not None:
+        return _get_device()
     if _torch is None:
         _load_torch()
-    return _torch._C._cuda_getDevice() if _has_gpu else -2        # (-1 is a CPU tensor's)
+        return _current_device()
+    return -2                # (-1 is a CPU tensor's)
 
 
 def _workspace(fn, device, workspace, workspace_bytes):
-    if isinstance(workspace, int) or workspace is None:
+    if workspace is None or workspace.__class__ is int:
         return workspace, int(workspace_bytes or 0)
-    nbytes = workspace.numel() * workspace.element_size()
+    size = workspace.element_size()
+    nbytes = workspace.numel() * size
     if workspace_bytes is not None:
         nbytes = min(nbytes, int(workspace_bytes))
-    return _buf(fn, device, "workspace", workspace, workspace.element_size(), 1), nbytes
-
-
-def _current_stream():
-    if _torch is None:
-        _load_torch()
-    return _torch.cuda.current_stream().cuda_stream
+    return _buf(fn, device, "workspace", workspace, size, 1), nbytes
 
 
 def _stream(stream):
     if stream is None:
         # torch.cuda.current_stream().cuda_stream without the Stream object (2.8 us -> 0.1 us a call)
-        return _torch._C._cuda_getCurrentRawStream(_current_device()) if _has_gpu else _current_stream()
+        device = _current_device()
+        return _get_stream(device) if _get_stream is not None else _torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
