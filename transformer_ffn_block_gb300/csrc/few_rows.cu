@@ -64,6 +64,7 @@ struct FewArgs {
   int stages, stage_bytes;
   int recv_bytes;           // shared memory for the other CTAs' sums, behind the stages
   int tmem_cols;
+  int late_wait;            // does not read the preceding kernel's results (see launch.h)
 };
 
 // D(tmem) (+)= A(smem) . B(smem)^T
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreads)
   tc_fence_after();
   cluster_arrive();        // this CTA can receive (waited for before any CTA sends)
   const uint32_t tmem_base = tmem_slot;
-  pdl_wait();
+  if (!args.late_wait) pdl_wait();
   pdl_trigger();
 
   const int per = (args.num_kb + args.splits - 1) / args.splits;
@@ -412,6 +413,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncwarp();
   cluster_wait();
+  if (args.late_wait) pdl_wait();    // this kernel is not complete before the preceding one
   if (warp == 2) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(args.tmem_cols)
@@ -518,8 +520,9 @@ int few_rows_bn(int64_t M) {
 }  // namespace
 
 // Up to 512 rows, by an estimate of both forms in SM cycles: here about 640 per
-// stage and round of clusters, 48 per row of a tile for its sums and stores, and
-// 4000 for an exchange; there 1.4 times the plan's cycles.  Measured in us, here
+// stage and round of clusters, 48 per row of a tile for its sums and stores, 700
+// for each further tile of rows and 4000 for an exchange; there 1.4 times the
+// plan's cycles.  Measured in us, here
 // against there: 64 rows of 4096 x 1024 7.0 / 7.8, 128 rows 9.1 / 7.8, of 4096 x
 // 4096 13.4 / 20, 256 rows 17.1 / 20, of 2048 x 2048 9.9 / 11.7, of 8192 x 2048
 // 16.5 / 13.5, of 4096 x 14336 42 / 36, of 28672 x 4096 68 / 49.
@@ -528,7 +531,8 @@ bool few_rows(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, int64_t oth
   int clusters, splits, num_kb;
   if (few_rows_split(M, N, K, gated, fp8, &clusters, &splits, &num_kb) != cudaSuccess) return false;
   const int64_t rounds = (int64_t(clusters) * splits + kNumSMsHint - 1) / kNumSMsHint;
-  const int64_t here = rounds * ((num_kb + splits - 1) / splits) * 640 + 48 * few_rows_bn(M) - 700 + (splits > 1 ? 4000 : 0);
+  const int64_t here = rounds * ((num_kb + splits - 1) / splits) * 640 + 48 * few_rows_bn(M) +
+                       700 * ((M + 127) / 128 - 2) + (splits > 1 ? 4000 : 0);
   return 10 * here < 14 * other_cycles + 6000;
 }
 
@@ -536,9 +540,10 @@ bool few_rows(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, int64_t oth
 template <int OP, bool W_MN, int EPI>
 cudaError_t few_rows_product(uint16_t* out, uint16_t* z, const void* x, const float* x_scale, const void* w,
                              const float* w_scale, const uint16_t* bias, const uint16_t* in, int act, int64_t M,
-                             int64_t N, int64_t K, cudaStream_t s) {
+                             int64_t N, int64_t K, cudaStream_t s, bool late_wait = false) {
   constexpr bool GATED = EPI != EPI_LINEAR;
   FewArgs a{};
+  a.late_wait = late_wait ? 1 : 0;
   a.out = out;
   a.z = z;
   a.bias = bias;
@@ -572,9 +577,10 @@ cudaError_t few_rows_product(uint16_t* out, uint16_t* z, const void* x, const fl
 
 cudaError_t launch_few_rows(uint16_t* out, uint16_t* z, const void* x, const float* x_scale, const void* w,
                             const float* w_scale, const uint16_t* bias, const uint16_t* res, int act, int64_t M,
-                            int64_t N, int64_t K, bool fp8, bool w_mn, cudaStream_t s) {
+                            int64_t N, int64_t K, bool fp8, bool w_mn, cudaStream_t s, bool late_wait) {
   if (fp8) return few_rows_product<OP_E4M3, false, EPI_LINEAR>(out, z, x, x_scale, w, w_scale, bias, res, act, M, N, K, s);
-  if (w_mn) return few_rows_product<OP_BF16, true, EPI_LINEAR>(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, s);
+  if (w_mn)
+    return few_rows_product<OP_BF16, true, EPI_LINEAR>(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, s, late_wait);
   return few_rows_product<OP_BF16, false, EPI_LINEAR>(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, s);
 }
 

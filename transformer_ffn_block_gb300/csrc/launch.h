@@ -14,6 +14,13 @@ int num_sms();
 // Launches `kernel` as a programmatic dependent launch: its blocks may be
 // scheduled while the kernel before it on `s` drains.  Only for kernels that
 // call pdl_wait() in every thread before they touch global memory.
+//
+// A kernel whose inputs were complete before the kernel launched just before it
+// could start (that one having waited for them itself, in every thread, before
+// its pdl_trigger()) may put its pdl_wait() at its end instead ("late wait"):
+// it then runs beside the preceding kernel, on the SMs that one leaves free, and
+// still counts as complete only after it, which is what the kernel behind
+// relies on.  Neither may write what the other reads or writes.
 template <typename... Params, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, int block, size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
@@ -176,7 +183,7 @@ cudaError_t launch_skinny_gated(uint16_t* h, const uint16_t* x, const uint16_t* 
 bool few_rows(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, int64_t other_cycles);
 cudaError_t launch_few_rows(uint16_t* out, uint16_t* z, const void* x, const float* x_scale, const void* w,
                             const float* w_scale, const uint16_t* bias, const uint16_t* res, int act, int64_t M,
-                            int64_t N, int64_t K, bool fp8, bool w_mn, cudaStream_t s);
+                            int64_t N, int64_t K, bool fp8, bool w_mn, cudaStream_t s, bool late_wait = false);
 cudaError_t launch_few_rows_gated(uint16_t* out, const uint16_t* x, const uint16_t* w1, const uint16_t* dh, int act,
                                   int64_t M, int64_t C, int64_t H, cudaStream_t s);
 cudaError_t few_rows_take_status(unsigned int* status);
