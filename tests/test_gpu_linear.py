@@ -191,6 +191,27 @@ def test_linear_backward_activations(q, name):
     assert torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("name", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_linear_backward_far_preactivations(q, name):
+    """Where z is huge or infinite the slope is 0 or 1, and a NaN stays in its column."""
+    M, N, K = 5, 16, 8
+    z = torch.zeros(M, N)
+    for c, v in enumerate((1e30, -1e30, 3e38, -3e38, float("inf"), -float("inf"), 90.0, -90.0, 200.0, -200.0, float("nan"))):
+        z[:, c] = v
+    dout, x, w = _t(1, M, N), _t(2, M, K), _t(3, N, K)
+    dx, dw, db = (torch.empty(*s, dtype=t, device="cuda") for s, t in (((M, K), bf16), ((N, K), bf16), ((N,), f32)))
+    ws = torch.empty(q.qffn_linear_backward_workspace_size(M, N, K), dtype=torch.uint8, device="cuda")
+    q.qffn_linear_backward(dx, dw, db, dout.cuda(), z.to(bf16).cuda(), x.cuda(), w.cuda(), _act(q, name), M, N, K, False, ws)
+    q.qffn_check_status()
+    db, want = db.cpu().double(), dout.double().sum(0)
+    tol = 2.0 ** -20 * dout.double().abs().sum(0)
+    for c in range(10):
+        assert abs(db[c] - (want[c] if c % 2 == 0 else 0.0)) <= tol[c] + 1e-30, c
+    assert db[10].isnan() and dw[10].isnan().all() and torch.isfinite(dw[:10].float()).all()
+    at_zero = P.act_grad(torch.zeros(1, dtype=torch.float64), name).item()
+    assert bool(((db[11:] - at_zero * want[11:]).abs() <= tol[11:]).all())
+
+
 @pytest.mark.parametrize("M,C,H", [(1, 8, 8), (1, 1024, 2048), (3, 72, 136), (16, 520, 264), (17, 2048, 72), (40, 136, 1000),
                                    (130, 264, 128), (300, 1024, 776), (700, 264, 3000), (2304, 136, 1280)])
 @pytest.mark.parametrize("name", ["silu", "gelu"])

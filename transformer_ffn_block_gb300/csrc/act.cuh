@@ -71,6 +71,14 @@ QFFN_DEVI float act_f32(float z) {
   return z;
 }
 
+// z within +-100, NaN as it is: there every derivative here has reached 0 or 1 in
+// fp32, and beyond its terms would be 0 times infinity.
+QFFN_DEVI float slope_range(float z) {
+  float r;
+  asm("{\n .reg .f32 t;\n max.NaN.f32 t, %1, 0fC2C80000;\n min.NaN.f32 %0, t, 0f42C80000;\n}" : "=f"(r) : "f"(z));
+  return r;
+}
+
 // Value and derivative.
 template <int ACT>
 QFFN_DEVI void act_grad_f32(float z, float& f, float& df) {
@@ -79,57 +87,34 @@ QFFN_DEVI void act_grad_f32(float z, float& f, float& df) {
     df = z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
   } else if (ACT == ACT_GELU) {
     float gauss;
-    const float p = normal_cdf_f32(z, gauss);
+    const float c = slope_range(z);
+    const float p = normal_cdf_f32(c, gauss);
     f = z * p;
-    df = fmaf(z * kInvSqrt2Pi, gauss, p);
+    df = fmaf(c * kInvSqrt2Pi, gauss, p);
   } else if (ACT == ACT_GELU_TANH) {
-    const float z2 = z * z;
-    const float p = sigmoid_f32(kGeluTanhScale * fmaf(kGeluTanhCubic * z * z, z, z));
+    const float c = slope_range(z), c2 = c * c;
+    const float p = sigmoid_f32(kGeluTanhScale * fmaf(kGeluTanhCubic * c2, c, c));
     f = z * p;
-    df = fmaf(f * (1.0f - p), kGeluTanhScale * fmaf(3.0f * kGeluTanhCubic, z2, 1.0f), p);
+    df = fmaf(c * p * (1.0f - p), kGeluTanhScale * fmaf(3.0f * kGeluTanhCubic, c2, 1.0f), p);
   } else if (ACT == ACT_SILU) {
-    const float p = sigmoid_f32(z);
+    const float c = slope_range(z);
+    const float p = sigmoid_f32(c);
     f = z * p;
-    df = p * fmaf(z, 1.0f - p, 1.0f);
+    df = p * fmaf(c, 1.0f - p, 1.0f);
   } else {
     f = z;
     df = 1.0f;
   }
 }
 
-// The same on pairs (f32x2): every lane's operations are those of the scalar
-// forms, so the results are the same bits; the fp32 pipe issues half as often.
+// The same on pairs (f32x2).
 QFFN_DEVI uint64_t f2_dup(float v) { return f2_pack(v, v); }
-QFFN_DEVI uint64_t f2_abs(uint64_t v) { return v & 0x7FFFFFFF7FFFFFFFull; }
 
 QFFN_DEVI uint64_t sigmoid_f2(uint64_t v) {
   float a, b, da, db;
   f2_unpack(f2_mul(f2_dup(-kLog2e), v), a, b);
   f2_unpack(f2_add(f2_dup(1.0f), f2_pack(exp2_f32(a), exp2_f32(b))), da, db);
   return f2_pack(rcp_f32(da), rcp_f32(db));
-}
-
-QFFN_DEVI uint64_t normal_cdf_f2(uint64_t z, uint64_t& gauss) {
-  const uint64_t a = f2_abs(z);
-  float d0, d1, z0, z1;
-  f2_unpack(f2_fma(f2_dup(0.35f), a, f2_dup(1.0f)), d0, d1);
-  const uint64_t t = f2_pack(rcp_f32(d0), rcp_f32(d1));
-  uint64_t r = f2_dup(0.0489424504339695f);
-  r = f2_fma(r, t, f2_dup(-0.20211930572986603f));
-  r = f2_fma(r, t, f2_dup(0.24064083397388458f));
-  r = f2_fma(r, t, f2_dup(-0.01702345348894596f));
-  r = f2_fma(r, t, f2_dup(0.15596149861812592f));
-  r = f2_fma(r, t, f2_dup(0.13335509598255157f));
-  r = f2_fma(r, t, f2_dup(0.14027033746242523f));
-  r = f2_fma(r, t, f2_dup(-2.7315563784213737e-05f));
-  float q0, q1, t0, t1, c0, c1;
-  f2_unpack(f2_mul(f2_mul(f2_dup(-0.5f * kLog2e), a), a), q0, q1);
-  gauss = f2_pack(exp2_f32(q0), exp2_f32(q1));
-  const uint64_t tail = f2_mul(gauss, r);
-  f2_unpack(tail, t0, t1);
-  f2_unpack(f2_sub(f2_dup(1.0f), tail), c0, c1);
-  f2_unpack(z, z0, z1);
-  return f2_pack(z0 < 0.0f ? t0 : c0, z1 < 0.0f ? t1 : c1);
 }
 
 template <int ACT>
@@ -140,8 +125,11 @@ QFFN_DEVI uint64_t act_f2(uint64_t z) {
     return f2_pack(a < 0.0f ? 0.0f : a, b < 0.0f ? 0.0f : b);
   }
   if (ACT == ACT_GELU) {
-    uint64_t gauss;
-    return f2_mul(z, normal_cdf_f2(z, gauss));
+    // (its polynomial runs faster on single values than on pairs, whose constants
+    // take register pairs: 8192 x 8192 x 64 with GELU 79 us on pairs, 73 so)
+    float a, b;
+    f2_unpack(z, a, b);
+    return f2_pack(act_f32<ACT_GELU>(a), act_f32<ACT_GELU>(b));
   }
   if (ACT == ACT_GELU_TANH) {
     const uint64_t s = f2_mul(f2_dup(kGeluTanhScale), f2_fma(f2_mul(f2_mul(f2_dup(kGeluTanhCubic), z), z), z, z));
@@ -153,25 +141,21 @@ QFFN_DEVI uint64_t act_f2(uint64_t z) {
 
 template <int ACT>
 QFFN_DEVI void act_grad_f2(uint64_t z, uint64_t& f, uint64_t& df) {
-  if (ACT == ACT_GELU) {
-    uint64_t gauss;
-    const uint64_t p = normal_cdf_f2(z, gauss);
+  float a, b;
+  f2_unpack(z, a, b);
+  if (ACT == ACT_GELU_TANH) {
+    const uint64_t c = f2_pack(slope_range(a), slope_range(b)), c2 = f2_mul(c, c);
+    const uint64_t p = sigmoid_f2(f2_mul(f2_dup(kGeluTanhScale), f2_fma(f2_mul(f2_dup(kGeluTanhCubic), c2), c, c)));
     f = f2_mul(z, p);
-    df = f2_fma(f2_mul(z, f2_dup(kInvSqrt2Pi)), gauss, p);
-  } else if (ACT == ACT_GELU_TANH) {
-    const uint64_t z2 = f2_mul(z, z);
-    const uint64_t p =
-        sigmoid_f2(f2_mul(f2_dup(kGeluTanhScale), f2_fma(f2_mul(f2_mul(f2_dup(kGeluTanhCubic), z), z), z, z)));
-    f = f2_mul(z, p);
-    df = f2_fma(f2_mul(f, f2_sub(f2_dup(1.0f), p)),
-                f2_mul(f2_dup(kGeluTanhScale), f2_fma(f2_dup(3.0f * kGeluTanhCubic), z2, f2_dup(1.0f))), p);
+    df = f2_fma(f2_mul(f2_mul(c, p), f2_sub(f2_dup(1.0f), p)),
+                f2_mul(f2_dup(kGeluTanhScale), f2_fma(f2_dup(3.0f * kGeluTanhCubic), c2, f2_dup(1.0f))), p);
   } else if (ACT == ACT_SILU) {
-    const uint64_t p = sigmoid_f2(z);
+    const uint64_t c = f2_pack(slope_range(a), slope_range(b));
+    const uint64_t p = sigmoid_f2(c);
     f = f2_mul(z, p);
-    df = f2_mul(p, f2_fma(z, f2_sub(f2_dup(1.0f), p), f2_dup(1.0f)));
+    df = f2_mul(p, f2_fma(c, f2_sub(f2_dup(1.0f), p), f2_dup(1.0f)));
   } else {
-    float a, b, fa, fb, da, db;
-    f2_unpack(z, a, b);
+    float fa, fb, da, db;
     act_grad_f32<ACT>(a, fa, da);
     act_grad_f32<ACT>(b, fb, db);
     f = f2_pack(fa, fb);
