@@ -18,7 +18,7 @@
 // Pipeline: SM pairs (2-CTA clusters), persistent over 256 x 256 tiles, one
 // tcgen05.mma.cta_group::2 (M = 256, N = 256) chain per tile; CTA r of a pair
 // stages rows [128 r, 128 r + 128) of A and of the tile's 256 weight rows,
-// 256 bytes of K per stage and row, three stages.  One warp loads (TMA,
+// 256 bytes of K per stage and row, three stages (four of narrow units).  One warp loads (TMA,
 // 128-byte swizzle), one thread of the leader issues the MMAs, eight warps per
 // CTA run the epilogue out of one of two TMEM accumulators while the next tile
 // accumulates in the other.  Per SM and byte of K this loads 16 + 16 KB per
@@ -44,17 +44,17 @@ constexpr int BN = 256;                    // accumulator columns
 constexpr int ROW_BYTES = 128;             // one swizzle atom row
 constexpr int BOX_BYTES = 128 * ROW_BYTES; // one TMA box: 128 rows
 constexpr int KBOX = 2;                    // boxes per operand and stage
-constexpr int STAGES = 3;
+constexpr int MAX_STAGES = 4;
 constexpr int OP_BYTES = KBOX * BOX_BYTES; // one operand's share of a stage
-constexpr int STAGE_BYTES = 2 * OP_BYTES;
+constexpr int RING_BYTES = 3 * 2 * OP_BYTES;   // the stages: three of whole units, four of narrow ones
 constexpr int STEPS = 8;                   // MMAs per stage (32 bytes of K each)
 constexpr int EPI_WARPS = 8;
 constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 2 * BN;
-constexpr int NUM_BARS = 2 * STAGES + 5;
+constexpr int NUM_BARS = 2 * MAX_STAGES + 5;
 constexpr int STAGING_BOX = 32 * 128;      // a warp's transposing box: 32 rows x 32 fp32
 constexpr int STAGING_BYTES = EPI_WARPS * STAGING_BOX;
-constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 + NUM_BARS * 8 + 16;
+constexpr int SMEM_BYTES = RING_BYTES + STAGING_BYTES + 1024 + NUM_BARS * 8 + 16;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
 constexpr int GROUP_M = 8;
 constexpr uint16_t kBothCtas = 0x3;
@@ -128,8 +128,8 @@ QFFN_DEVI void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_
 // groups 1024 bytes apart) in both boxes, whose distance is the leading byte
 // offset.
 template <bool MN>
-QFFN_DEVI uint64_t step_desc(uint32_t base, int i) {
-  if (!MN) return sdesc_sw128(base + uint32_t(i >> 2) * BOX_BYTES + uint32_t(i & 3) * 32u);
+QFFN_DEVI uint64_t step_desc(uint32_t base, int i, uint32_t box_bytes) {
+  if (!MN) return sdesc_sw128(base + uint32_t(i >> 2) * box_bytes + uint32_t(i & 3) * 32u);
   const uint64_t d = sdesc_sw128(base + uint32_t(i) * 16u * ROW_BYTES);
   return (d & ~(uint64_t(0x3FFF) << 16)) | (uint64_t(BOX_BYTES >> 4) << 16);
 }
@@ -185,9 +185,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                   const __grid_constant__ CUtensorMap tmBh, const LinArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sA = smem;
-  uint8_t* sB = smem + STAGES * OP_BYTES;
-  uint8_t* sStaging = smem + STAGES * STAGE_BYTES;
+  uint8_t* sStaging = smem + RING_BYTES;
+  // a stage: this CTA's A rows, then its B rows
+  const uint32_t ring = smem_u32(smem), stage_bytes = uint32_t(OP_BYTES + (OP_BYTES >> args.narrow));
+  const int stages = args.narrow == 0 ? 3 : 4;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sStaging + STAGING_BYTES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -196,10 +197,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // reading stage s are done; tfull[a]: accumulator a is complete; tempty[a]
   // (leader): both CTAs' epilogue warps have read it; drain: all MMAs done
   auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
-  auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(STAGES + s); };
-  auto tfull_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * STAGES + a); };
-  auto tempty_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * STAGES + 2 + a); };
-  const uint32_t drain_bar = bar0 + 8u * uint32_t(2 * STAGES + 4);
+  auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(MAX_STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * MAX_STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * MAX_STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * uint32_t(2 * MAX_STAGES + 4);
 
   constexpr bool GATED = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int pair = int(cluster_id_x()), num_pairs = int(num_clusters_x());
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
@@ -237,6 +238,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   pdl_trigger();
 
   const int bn = BN >> args.narrow;        // accumulator columns of a whole unit
+  const uint32_t b_box = uint32_t(BOX_BYTES >> args.narrow);   // bytes of a box of this CTA's bn / 2 B rows
   // K blocks of a unit
   auto kb_begin = [&](const Unit& u) { return EPI == EPI_PARTIAL ? u.sp * args.kb_per_split : 0; };
   auto kb_end = [&](const Unit& u) {
@@ -246,8 +248,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ producer
-      uint32_t issued = 0, issued_parity = 0;
-      int it = 0;
+      uint32_t issued = 0, issued_parity = 0, ph = 0;
+      int s = 0;
       bool ok = true;
       for (int un = pair; ok && un < args.num_units; un += num_pairs) {
         const Unit u = unit_coords<EPI>(un, args);
@@ -259,17 +261,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                       : u.nb * BN + u.half * 128 + int(rank) * 64;
         const uint32_t stage_tx = 2u * uint32_t(OP_BYTES + (u.half < 0 ? OP_BYTES >> args.narrow : OP_BYTES / 2));
         const int kb1 = kb_end(u);
-        for (int kb = kb_begin(u); kb < kb1; ++kb, ++it) {
-          const int s = it % STAGES;
-          const uint32_t ph = uint32_t(it / STAGES) & 1u;
+        for (int kb = kb_begin(u); kb < kb1; ++kb) {
           if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) { ok = false; break; }
           if (rank == 0) mbar_expect_tx(full_bar(s), stage_tx);
           const uint32_t fb = map_to_rank(full_bar(s), 0);
           const int k0 = kb * stage_k(OP);
 #pragma unroll
           for (int bx = 0; bx < KBOX; ++bx) {
-            const uint32_t da = smem_u32(sA + s * OP_BYTES + bx * BOX_BYTES);
-            const uint32_t db = smem_u32(sB + s * OP_BYTES + bx * BOX_BYTES);
+            const uint32_t da = ring + uint32_t(s) * stage_bytes + uint32_t(bx * BOX_BYTES);
+            const uint32_t db = ring + uint32_t(s) * stage_bytes + uint32_t(OP_BYTES) + uint32_t(bx) * b_box;
             if (A_MN) tma_load_2d_pair(da, &tmA, fb, rowA + bx * 64, k0);
             else tma_load_2d_pair(da, &tmA, fb, k0 + bx * box_k(OP), rowA);
             if (B_MN) {
@@ -281,19 +281,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           issued |= 1u << s;
           issued_parity = (issued_parity & ~(1u << s)) | (ph << s);
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
       }
       // every phase the leader armed completes before shared memory is released
       if (rank == 0)
-        for (int s = 0; s < STAGES; ++s)
-          if (issued & (1u << s))
-            mbar_wait(full_bar(s), (issued_parity >> s) & 1u, abort_flag, false, kDrainLimitNs);
+        for (int k = 0; k < stages; ++k)
+          if (issued & (1u << k))
+            mbar_wait(full_bar(k), (issued_parity >> k) & 1u, abort_flag, false, kDrainLimitNs);
     }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       // ------------------------------------------------------------ MMA issuer (leader)
-      int it = 0, local = 0;
+      int s = 0, local = 0;
+      uint32_t ph = 0;
       bool ok = true;
       for (int un = pair; ok && un < args.num_units; un += num_pairs, ++local) {
         const int acc = local & 1;
@@ -304,17 +309,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
         const uint32_t idesc = idesc_for(OP, A_MN, B_MN, u.half < 0 ? bn : BN / 2);
         const int kb0 = kb_begin(u), kb1 = kb_end(u);
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % STAGES;
-          const uint32_t ph = uint32_t(it / STAGES) & 1u;
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + s * OP_BYTES);
-          const uint32_t b0 = smem_u32(sB + s * OP_BYTES);
+          const uint32_t a0 = ring + uint32_t(s) * stage_bytes, b0 = a0 + uint32_t(OP_BYTES);
 #pragma unroll
           for (int i = 0; i < STEPS; ++i)
-            mma_pair<OP>(d_tmem, step_desc<A_MN>(a0, i), step_desc<B_MN>(b0, i), idesc, uint32_t((kb - kb0) | i));
+            mma_pair<OP>(d_tmem, step_desc<A_MN>(a0, i, BOX_BYTES), step_desc<B_MN>(b0, i, b_box), idesc,
+                         uint32_t((kb - kb0) | i));
           mma_commit_mc(empty_bar(s), kBothCtas);
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
         if (!ok) break;
         mma_commit_mc(tfull_bar(acc), kBothCtas);
