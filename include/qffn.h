@@ -367,8 +367,8 @@ qffn_status qffn_layernorm_absmax(uint16_t* res_out, uint16_t* y, float* mean, f
  * dx is the gradient of both inputs of the residual sum.  dx may alias dy or
  * dres.  The column sums are added in a fixed order (no atomics): the same
  * bits in every run.  workspace: >= qffn_norm_backward_workspace_size() bytes,
- * 256-byte aligned, any content.  Two launches.  Shape rules of
- * qffn_layernorm_absmax. */
+ * 256-byte aligned, any content.  One or two launches (and a 4-byte memset with
+ * stats).  Shape rules of qffn_layernorm_absmax. */
 size_t qffn_norm_backward_workspace_size(int64_t N, int64_t C);
 qffn_status qffn_layernorm_backward(uint16_t* dx, float* dgain, float* dshift, float* stats,
                                     const uint16_t* dy, const uint16_t* dres, const uint16_t* r,

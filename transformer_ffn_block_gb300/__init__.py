@@ -213,7 +213,7 @@ def qffn_selftest_bounded_wait(out, arrive, limit_ns, stream=None):
 
 
 def qffn_gemm_clock_sample(stream=None):
-    """(SM clock cycles, nanoseconds) of the first CTA of the most recent GEMM launch."""
+    """(SM clock cycles, nanoseconds) of the first CTA of the most recent FP8 GEMM launch."""
     out = (ctypes.c_uint64 * 2)()
     _check("qffn_gemm_clock_sample", lib.qffn_gemm_clock_sample(
         ctypes.cast(out, ctypes.c_void_p), _stream(stream)))

@@ -115,10 +115,10 @@ QFFN_DEVI uint4 normed8(const F8& f, uint64_t neg_mean, uint64_t rstd, const F8&
 
 // One row per team of T threads; thread t owns the 16-byte chunks t, t+T, ...
 // Small teams with up to four chunks a thread for many rows: a dozen rows or
-// more of independent blocks per SM hide each other's loads and barriers
-// (16384 x 4096: see launch_layernorm for what that measured against
-// persistent blocks fed by bulk copies).  Larger teams for few rows, where a
-// call is a launch and one round of loads.
+// more of independent blocks per SM hide each other's loads and barriers (16384
+// x 4096 with a residual 81 us, 6.6 TB/s; persistent blocks fed by bulk copies
+// 85 to 98).  Larger teams for few rows, where a call is a launch and one round
+// of loads (one row of 4096: 3.1 us against 4.1).
 template <int T, int V, int BLOCK>
 __global__ void __launch_bounds__(BLOCK) layernorm_kernel(const LnFwd a) {
   __shared__ float red[2][64];
@@ -305,9 +305,10 @@ __global__ void __launch_bounds__(256) norm_backward_warp_kernel(const NormBwd a
 // the next rows are in flight while a row is reduced and written; threads need
 // registers for the column sums only.  A stage is refilled by thread 0 one row
 // later, after that row's barrier (inside team_sum2), which every thread
-// reaches only when it has read the stage.  Measured at 16384 x 4096 (layer
-// norm, with dres): loads into registers 148 us, two to three rows in flight
-// per SM; see the launch for the ring's figures.
+// reaches only when it has read the stage.  Measured at 16384 x 4096 with dres
+// (floor 79 us): loads into registers, two to three rows in flight per SM, 148
+// us (layer norm) and 96 (RMS norm); this ring 96 and 82; with the arithmetic
+// in pairs 82.5 and 80.5 (6.5 TB/s).
 template <bool CENTRED, int T, int V>
 __global__ void __launch_bounds__(T) norm_backward_kernel(const NormBwd a) {
   extern __shared__ __align__(16) uint8_t ring[];
