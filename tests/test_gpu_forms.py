@@ -25,11 +25,13 @@ FORWARD_FP8 = [(1, 8, 4112), (1, 8, 8272), (9, 8, 4128), (35, 5672, 16), (135, 9
 GATED = [(1, 2056, 8), (1, 4112, 8), (10, 2104, 8), (33, 8, 4552), (134, 8, 5272), (17, 784, 3744), (138, 3272, 1456),
          (130, 1928, 392), (266, 2528, 176), (549, 8, 3424), (24, 7600, 2312), (34, 504, 2488), (787, 4304, 144),
          (937, 3488, 40)]
-# input gradient few rows over parts of K, whole, narrow and split units; weight gradient whole, narrow and split
+# input gradient few rows over parts of K, whole, narrow and split units; weight gradient whole, narrow and split,
+# and begun on the SMs that the input gradient leaves free
 BACKWARD = [(135, 1432, 3112), (273, 1592, 1808), (419, 2296, 1264), (130, 968, 8), (392, 2024, 8), (137, 8, 9776),
-            (524, 8, 6664), (2, 4008, 4624), (517, 2328, 8), (8, 264, 10696), (3240, 8, 3384), (2336, 8, 8)]
+            (524, 8, 6664), (2, 4008, 4624), (517, 2328, 8), (8, 264, 10696), (3240, 8, 3384), (2336, 8, 8),
+            (700, 5000, 2056), (1111, 4104, 2056)]
 GATED_BACKWARD = [(135, 8, 5192), (139, 3312, 1248), (414, 1992, 8), (534, 8, 3384), (2, 4008, 2344), (533, 3744, 264),
-                  (524, 2800, 8), (35, 520, 2520)]
+                  (524, 2800, 8), (35, 520, 2520), (700, 2056, 2504)]
 
 
 @pytest.mark.parametrize("M,N,K", FORWARD)

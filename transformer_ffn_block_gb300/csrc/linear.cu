@@ -99,6 +99,7 @@ struct LinArgs {
   int tiles_m, tiles_n, num_units, num_kb;
   int band_n;               // N-blocks per raster band
   int split_from;           // units from here on are 128-column halves of the last tiles
+  int early, early_units;   // the first `early` pairs share the first early_units units, all pairs the rest
   int splits, kb_per_split, m_pad;   // EPI_PARTIAL
   float* partial;           // EPI_PARTIAL: [splits][m_pad][N]
   int late_wait;            // does not read the preceding kernel's results (see launch.h)
@@ -178,6 +179,13 @@ QFFN_DEVI Unit unit_coords(int u, const LinArgs& a) {
   return r;
 }
 
+// The units of a pair, in order: first_unit, then next_unit of it.
+QFFN_DEVI int first_unit(int pair, const LinArgs& a) { return pair < a.early ? pair : a.early_units + pair; }
+QFFN_DEVI int next_unit(int un, int pair, int num_pairs, const LinArgs& a) {
+  if (un >= a.early_units) return un + num_pairs;
+  return un + a.early < a.early_units ? un + a.early : a.early_units + pair;
+}
+
 // tmB: B with boxes of 128 >> narrow rows; tmBh: of 64 rows, for the half tiles.
 template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -251,7 +259,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t issued = 0, issued_parity = 0, ph = 0;
       int s = 0;
       bool ok = true;
-      for (int un = pair; ok && un < args.num_units; un += num_pairs) {
+      for (int un = first_unit(pair, args); ok && un < args.num_units; un = next_unit(un, pair, num_pairs, args)) {
         const Unit u = unit_coords<EPI>(un, args);
         const int rowA = u.mb * (2 * BM) + int(rank) * BM;
         // this CTA's weight rows: half of the tile's 256 (of a half tile's
@@ -300,7 +308,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int s = 0, local = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int un = pair; ok && un < args.num_units; un += num_pairs, ++local) {
+      for (int un = first_unit(pair, args); ok && un < args.num_units;
+           un = next_unit(un, pair, num_pairs, args), ++local) {
         const int acc = local & 1;
         const uint32_t aph = uint32_t(local >> 1) & 1u;
         if (!mbar_wait_cluster_bounded(tempty_bar(acc), aph ^ 1u, abort_flag, &g_status, kWaitLimitNs)) break;
@@ -356,7 +365,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr uint32_t kBox2 = 32 * 64;
     constexpr bool kRead = EPI == EPI_LINEAR || EPI == EPI_GATED_BWD;   // may read a bf16 tensor
     int local = 0;
-    for (int un = pair; un < args.num_units; un += num_pairs, ++local) {
+    for (int un = first_unit(pair, args); un < args.num_units; un = next_unit(un, pair, num_pairs, args), ++local) {
       const int acc = local & 1;
       const uint32_t aph = uint32_t(local >> 1) & 1u;
       const Unit u = unit_coords<EPI>(un, args);
@@ -783,6 +792,14 @@ struct Plan {
   int64_t cycles;            // estimate
 };
 constexpr int kPlanPairs = kNumSMsHint / 2;   // fixed, so a workspace size needs no device query
+constexpr int64_t kNextKernelCycles = 6000;   // from a kernel's start to the next one's
+constexpr int stage_cycles(int narrow) { return narrow == 0 ? 1024 : narrow == 1 ? 768 : 640; }
+
+// What a product leaves idle at its end: this many SM pairs for so many cycles.
+struct Idle {
+  int pairs;
+  int64_t cycles;
+};
 // max_narrow: 2, or 1 where B is MN-major (its boxes are 64 columns wide).
 Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
   Plan p;
@@ -798,13 +815,13 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
     // parts of K, in SM cycles.  A stage of a unit takes the cycles of its MMAs
     // (1024 >> narrow) or of its loads (32 KB of A and 32 KB >> narrow of B per
     // SM at 64 bytes a cycle), the last unit's epilogue 4500 >> narrow, joining
-    // parts about 8200 and 500 for each.  Measured against whole tiles, the
-    // parts alone: 512 x 4096 x 4096 24.5 us, 256 x 1024 x 1024 10.5 us; see
-    // launch_linear for what the units measured.
+    // parts about 8200 and 500 for each.  Measured, parts of K alone against
+    // this choice: 512 x 4096 x 4096 24.5 / 19.3 us, 256 x 8192 x 2048 20.2 /
+    // 12.6, 256 x 1024 x 1024 10.5 / 6.8.
     int64_t best = -1;
     for (int n = 0; n <= max_narrow; ++n) {
       const int64_t units = int64_t(p.tiles_m) * ((N + (BN >> n) - 1) / (BN >> n));
-      const int stage = n == 0 ? 1024 : n == 1 ? 768 : 640;
+      const int stage = stage_cycles(n);
       for (int s = 1; s <= 16 && (s == 1 || (s * 4 <= p.num_kb && units * s <= kPlanPairs)); ++s) {
         const int64_t rounds = (units * s + kPlanPairs - 1) / kPlanPairs;
         const int64_t cost = rounds * ((p.num_kb + s - 1) / s) * stage + (4500 >> n) + (s > 1 ? 8200 + 500 * s : 0);
@@ -857,11 +874,14 @@ cudaError_t launch_join(uint16_t* out, uint16_t* out2, const float* partial, con
 }
 
 // One product with its epilogue.  EPI_LINEAR: N output columns; gated forms:
-// N = H and B = W1 [2H, K].  `partial` holds plan_bytes().
+// N = H and B = W1 [2H, K].  `partial` holds plan_bytes().  `before`: what the
+// kernel launched last leaves idle, if this one may start beside it (late_wait);
+// `after` receives what this one does.
 template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
 cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_scale, const void* B,
                     const float* w_scale, const uint16_t* bias, const uint16_t* in, int64_t M, int64_t N, int64_t K,
-                    float* partial, cudaStream_t s, bool late_wait = false) {
+                    float* partial, cudaStream_t s, bool late_wait = false, Idle before = {0, 0},
+                    Idle* after = nullptr) {
   constexpr bool GATED = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
   const int64_t brows = GATED ? 2 * N : N;
   const Plan p = make_plan(M, brows, K, OP, B_MN ? 1 : 2);
@@ -903,8 +923,37 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
   a.num_units = a.split_from = a.tiles_m * a.tiles_n;
   if ((e = max_pairs<OP, EPI, ACT, A_MN, B_MN>(&pairs)) != cudaSuccess) return e;
   // a last partial wave of R <= pairs / 2 tiles runs as 2 R half tiles in half the time
-  const int r = a.num_units % pairs;
-  if (p.narrow == 0 && a.num_units > pairs && r > 0 && 2 * r <= pairs) {
+  const int64_t unit = int64_t(p.num_kb) * stage_cycles(p.narrow);
+  auto last_wave = [&](int units) { return units > pairs ? units % pairs : 0; };
+  auto halves = [&](int r) { return p.narrow == 0 && r > 0 && 2 * r <= pairs; };
+  if (before.pairs > 0 && before.pairs < pairs && a.num_units > pairs) {
+    // The first before.pairs pairs start early (clusters start in the order of
+    // their numbers) and take `extra` units more than the others: as many as end
+    // while the rest of the SMs is still busy, and with the fewest rounds of
+    // units.  (Input and weight gradient, us, without and with: M = 4096, N = 8192,
+    // K = 2048 165 / 152, 700, 5000, 2056 46 / 40.5, 1111, 4104, 2056 50 / 43.7.)
+    const int64_t fit = before.cycles / unit;
+    int64_t best = -1;
+    for (int extra = 0; extra <= fit && a.num_units - extra * before.pairs > pairs; ++extra) {
+      const int rest = a.num_units - extra * before.pairs;
+      const int r = last_wave(rest);
+      const int64_t half_rounds = 2 * (rest / pairs) + (r == 0 ? 0 : halves(r) ? 1 : 2);
+      if (best < 0 || half_rounds < best) {
+        best = half_rounds;
+        a.early = before.pairs;
+        a.early_units = extra * before.pairs;
+      }
+    }
+    if (a.early_units == 0) a.early = 0;
+  }
+  const int r = last_wave(a.num_units - a.early_units);
+  if (after != nullptr)
+    // (a kernel of one round leaves them from its start, but the next is launched later)
+    *after = a.num_units < pairs ? Idle{pairs - a.num_units, unit - kNextKernelCycles}
+             : r == 0            ? Idle{0, 0}
+             : halves(r)         ? Idle{pairs - 2 * r, unit / 2}
+                                 : Idle{pairs - r, unit};
+  if (halves(r)) {
     if (!B_MN && !operand_map<OP>(&m.bh, B, brows, K, false, 64)) return cudaErrorInvalidValue;
     a.split_from = a.num_units - r;
     a.num_units += r;
@@ -1021,22 +1070,24 @@ cudaError_t gated_bwd_product(uint16_t* dgu, const uint16_t* dh, const uint16_t*
 // where they lie.  `ready`: dz was complete before the kernel launched last may
 // have started, so dx need not wait for that one either; dw never reads what
 // the kernel before it writes and starts on the SMs that dx leaves free
-// (512 x 1024 x 1024, both: 19.9 us one after the other).
+// (512 x 1024 x 1024, both: 18 us, one after the other 19.9).
 cudaError_t grad_products(uint16_t* dx, uint16_t* dw, const uint16_t* dz, const uint16_t* x, const uint16_t* w,
                           int64_t M, int64_t N, int64_t K, bool accumulate, float* part_dx, float* part_dw, bool ready,
                           cudaStream_t s) {
   cudaError_t e = cudaSuccess;
+  Idle idle{0, 0};
   if (dx != nullptr) {
     e = takes_few_rows(M, K, N, false, false, true)
             ? launch_few_rows(dx, nullptr, dz, nullptr, w, nullptr, nullptr, nullptr, ACT_NONE, M, K, N, false, true, s,
                               ready)
             : product<OP_BF16, EPI_LINEAR, ACT_NONE, false, true>(dx, nullptr, dz, nullptr, w, nullptr, nullptr,
-                                                                  nullptr, M, K, N, part_dx, s, ready);
+                                                                  nullptr, M, K, N, part_dx, s, ready, Idle{0, 0}, &idle);
     if (e != cudaSuccess) return e;
     ready = true;
   }
   return product<OP_BF16, EPI_LINEAR, ACT_NONE, true, true>(dw, nullptr, dz, nullptr, x, nullptr, nullptr,
-                                                            accumulate ? dw : nullptr, N, K, M, part_dw, s, ready);
+                                                            accumulate ? dw : nullptr, N, K, M, part_dw, s, ready,
+                                                            idle);
 }
 }  // namespace
 
