@@ -95,6 +95,7 @@ struct LinArgs {
   const uint16_t* in;       // [M, N]: EPI_LINEAR residual or previous output (optional), GATED_BWD dh
   int M, N;                 // output rows and columns (gated: columns = H)
   int narrow;               // every unit is BN >> narrow accumulator columns wide
+  int bn, stages;           // SWAP: accumulator columns of a unit, stages of the ring
   int up_row;               // gated: first up row of W1 (= H)
   int tiles_m, tiles_n, num_units, num_kb;
   int band_n;               // N-blocks per raster band
@@ -187,7 +188,9 @@ QFFN_DEVI int next_unit(int un, int pair, int num_pairs, const LinArgs& a) {
 }
 
 // tmB: B with boxes of 128 >> narrow rows; tmBh: of 64 rows, for the half tiles.
-template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
+// SWAP: A is W and B is x with boxes of bn / 2 rows, so a unit is 256 output
+// columns (the TMEM lanes) by bn output rows.
+template <int OP, int EPI, int ACT, bool A_MN, bool B_MN, bool SWAP>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmBh, const LinArgs args) {
@@ -195,8 +198,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sStaging = smem + RING_BYTES;
   // a stage: this CTA's A rows, then its B rows
-  const uint32_t ring = smem_u32(smem), stage_bytes = uint32_t(OP_BYTES + (OP_BYTES >> args.narrow));
-  const int stages = args.narrow == 0 ? 3 : 4;
+  const int bn = SWAP ? args.bn : BN >> args.narrow;           // accumulator columns of a whole unit
+  const uint32_t b_box = uint32_t(bn / 2 * ROW_BYTES);         // bytes of a box of this CTA's bn / 2 B rows
+  const uint32_t ring = smem_u32(smem), stage_bytes = uint32_t(OP_BYTES) + KBOX * b_box;
+  const int stages = SWAP ? args.stages : args.narrow == 0 ? 3 : MAX_STAGES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sStaging + STAGING_BYTES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -245,8 +250,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (!args.late_wait) pdl_wait();   // nothing in global memory is touched before the preceding kernel is done
   pdl_trigger();
 
-  const int bn = BN >> args.narrow;        // accumulator columns of a whole unit
-  const uint32_t b_box = uint32_t(BOX_BYTES >> args.narrow);   // bytes of a box of this CTA's bn / 2 B rows
   // K blocks of a unit
   auto kb_begin = [&](const Unit& u) { return EPI == EPI_PARTIAL ? u.sp * args.kb_per_split : 0; };
   auto kb_end = [&](const Unit& u) {
@@ -261,13 +264,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool ok = true;
       for (int un = first_unit(pair, args); ok && un < args.num_units; un = next_unit(un, pair, num_pairs, args)) {
         const Unit u = unit_coords<EPI>(un, args);
-        const int rowA = u.mb * (2 * BM) + int(rank) * BM;
+        const int rowA = (SWAP ? u.nb : u.mb) * (2 * BM) + int(rank) * BM;
         // this CTA's weight rows: half of the tile's 256 (of a half tile's
         // 128); gated: CTA 0 the gate rows, CTA 1 the matching up rows
-        const int rowB = GATED ? (rank == 0 ? 0 : args.up_row) + u.nb * (bn / 2) + (u.half < 0 ? 0 : u.half * 64)
+        const int rowB = SWAP    ? u.mb * bn + int(rank) * (bn / 2)
+                         : GATED ? (rank == 0 ? 0 : args.up_row) + u.nb * (bn / 2) + (u.half < 0 ? 0 : u.half * 64)
                          : u.half < 0 ? u.nb * bn + int(rank) * (bn / 2)
                                       : u.nb * BN + u.half * 128 + int(rank) * 64;
-        const uint32_t stage_tx = 2u * uint32_t(OP_BYTES + (u.half < 0 ? OP_BYTES >> args.narrow : OP_BYTES / 2));
+        const uint32_t stage_tx = 2u * (u.half < 0 ? stage_bytes : uint32_t(OP_BYTES + OP_BYTES / 2));
         const int kb1 = kb_end(u);
         for (int kb = kb_begin(u); kb < kb1; ++kb) {
           if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) { ok = false; break; }
@@ -358,6 +362,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // turn32 and turn32 ^ 16, plus 1024 i
     const uint32_t row32 = box + uint32_t(lane) * 128u + (uint32_t(lane & 7) << 4);
     const uint32_t turn32 = box + uint32_t(sub) * 128u + (uint32_t((2 * ch) ^ sub) << 4);
+    // (a lane's column: at col32 ^ 16 (r & 7), plus 128 r)
+    const uint32_t col32 = box + uint32_t(lane) * 4u;
     // 32 bf16 columns (rows of 64 bytes, chunk c of row r at c ^ (r / 2 & 3)): row
     // at row16 ^ 16 c, turned share at turn16 plus 512 i; a second such box behind
     const uint32_t row16 = box + uint32_t(lane) * 64u + (uint32_t((lane >> 1) & 3) << 4);
@@ -369,35 +375,48 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int acc = local & 1;
       const uint32_t aph = uint32_t(local >> 1) & 1u;
       const Unit u = unit_coords<EPI>(un, args);
-      const int row0 = u.mb * (2 * BM) + int(rank) * BM + q * 32;
-      // output column of the unit's group 0
-      const int first_col = GATED ? u.nb * (bn / 2) + (u.half < 0 ? 0 : u.half * 64)
-                                  : u.nb * bn + (u.half < 0 ? 0 : u.half * 128);
+      // output row and column of the unit's group 0 for this warp; SWAP: the
+      // groups are of 32 rows and the warp's quarter of the lanes is 32 columns
+      const int row0 = SWAP ? u.mb * bn : u.mb * (2 * BM) + int(rank) * BM + q * 32;
+      const int row_end = SWAP ? min(args.M, row0 + bn) : args.M;
+      const int first_col = SWAP    ? u.nb * (2 * BM) + int(rank) * BM + q * 32
+                            : GATED ? u.nb * (bn / 2) + (u.half < 0 ? 0 : u.half * 64)
+                                    : u.nb * bn + (u.half < 0 ? 0 : u.half * 128);
       const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * BN);
       const int acc_cols = u.half < 0 ? bn : BN / 2;
-      const int groups = GATED ? acc_cols / 64 : acc_cols / 32;
+      const int groups = GATED ? acc_cols / 64 : (acc_cols + 31) / 32;
       // this warp's groups, next to each other: whole 128-byte lines from one
       // warp (interleaved groups: 8192 x 8192 x 64 with a residual 80 us, so 73)
       const int share = (groups + WG - 1) / WG, g0 = wg * share, g1 = min(groups, g0 + share);
-      // this lane's part of the global accesses: rows row0 + sub + 8 i (bit i of
-      // `rows`: there is one), element offset of the first at the group's column
+      // this lane's part of the global accesses of group g: rows sub + 8 i behind
+      // the group's first (bit i of live_rows: there is one), element offset of the first
       uint32_t rows = 0u;
 #pragma unroll
       for (int i = 0; i < 4; ++i) rows |= (row0 + sub + 8 * i < args.M ? 1u : 0u) << i;
       const size_t at = size_t(row0 + sub) * size_t(args.N) + size_t(first_col + ch * 8);
       const size_t step = size_t(8) * size_t(args.N);
+      auto col = [&](int g) { return first_col + (SWAP ? 0 : g * 32) + ch * 8; };
+      auto live_rows = [&](int g) {
+        if (col(g) >= args.N) return 0u;
+        if (!SWAP) return rows;
+        uint32_t v = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v |= (row0 + g * 32 + sub + 8 * i < row_end ? 1u : 0u) << i;
+        return v;
+      };
+      auto offset = [&](int g) { return SWAP ? at + size_t(4 * g) * step : at + size_t(g * 32); };
       // what a group reads from global memory, requested a group ahead (the
       // first group's before the accumulator is awaited)
       uint4 next_bias = make_uint4(0, 0, 0, 0), next_in[4];
       auto request = [&](int g) {
-        const uint32_t live = g < g1 && first_col + g * 32 + ch * 8 < args.N ? rows : 0u;
+        const uint32_t live = g < g1 ? live_rows(g) : 0u;
         if (EPI == EPI_LINEAR && args.bias != nullptr)
-          next_bias = live != 0u ? ld16_ro(args.bias + first_col + g * 32 + ch * 8) : make_uint4(0, 0, 0, 0);
+          next_bias = live != 0u ? ld16_ro(args.bias + col(g)) : make_uint4(0, 0, 0, 0);
         if (kRead && args.in != nullptr) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             next_in[i] = make_uint4(0, 0, 0, 0);
-            if ((live >> i) & 1u) next_in[i] = ld16_once(args.in + (at + size_t(g * 32) + size_t(i) * step));
+            if ((live >> i) & 1u) next_in[i] = ld16_once(args.in + (offset(g) + size_t(i) * step));
           }
         }
       };
@@ -414,7 +433,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       };
       if (g0 >= g1) loaded(g0);              // (a unit with fewer groups than warps)
       for (int g = g0; g < g1; ++g) {
-        const uint32_t live = first_col + g * 32 + ch * 8 < args.N ? rows : 0u;
+        const uint32_t live = live_rows(g);
         if (!GATED) {
           uint4 in4[4];
           uint64_t bias[4];
@@ -430,15 +449,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tmem_ld32(tbase + uint32_t(g * 32), v);
             loaded(g);
             __syncwarp();                    // the previous group has been read out of the box
+            if (SWAP) {                      // the lane is a column of the box
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              sts16(row32 ^ uint32_t(16 * c), make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
+              for (int c = 0; c < 32; ++c) sts4((col32 ^ uint32_t(16 * (c & 7))) + uint32_t(128 * c), v[c]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                sts16(row32 ^ uint32_t(16 * c), make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]));
+            }
             __syncwarp();
           }
           if (kRead) request(g + 1);
           const size_t o = EPI == EPI_PARTIAL
-                               ? (size_t(u.sp) * size_t(args.m_pad)) * size_t(args.N) + at + size_t(g * 32)
-                               : at + size_t(g * 32);
+                               ? (size_t(u.sp) * size_t(args.m_pad)) * size_t(args.N) + offset(g)
+                               : offset(g);
           uint4 los[4], his[4];              // all reads issued before the first is used
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -728,7 +752,7 @@ bool operand_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t k, boo
 }
 
 // 2-CTA clusters of a form that fit on the device at once (cached per device).
-template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
+template <int OP, int EPI, int ACT, bool A_MN, bool B_MN, bool SWAP = false>
 cudaError_t max_pairs(int* pairs) {
   static int cached[64] = {0};
   int dev = 0;
@@ -738,7 +762,7 @@ cudaError_t max_pairs(int* pairs) {
     *pairs = cached[dev];
     return cudaSuccess;
   }
-  const auto fn = linear_kernel<OP, EPI, ACT, A_MN, B_MN>;
+  const auto fn = linear_kernel<OP, EPI, ACT, A_MN, B_MN, SWAP>;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -765,7 +789,7 @@ struct Maps {
   CUtensorMap a, b, bh;
 };
 
-template <int OP, int EPI, int ACT, bool A_MN, bool B_MN>
+template <int OP, int EPI, int ACT, bool A_MN, bool B_MN, bool SWAP = false>
 cudaError_t launch(const Maps& m, const LinArgs& a, int pairs, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * unsigned(a.num_units < pairs ? a.num_units : pairs));
@@ -781,7 +805,7 @@ cudaError_t launch(const Maps& m, const LinArgs& a, int pairs, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<OP, EPI, ACT, A_MN, B_MN>, m.a, m.b, m.bh, a);
+  return cudaLaunchKernelEx(&cfg, linear_kernel<OP, EPI, ACT, A_MN, B_MN, SWAP>, m.a, m.b, m.bh, a);
 }
 
 // How a product [M, K] x [N, K]^T is cut: into units of 256 rows by 256 >> narrow
@@ -840,6 +864,32 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
   if (p.num_kb > 0) p.splits = (p.num_kb + p.kb_per_split - 1) / p.kb_per_split;
   return p;
 }
+// The same product with the operands exchanged: units of 256 output columns by
+// bn rows, a multiple of 32, so that the rows divide evenly into tiles.  A stage
+// takes the cycles of its MMAs, 4 bn, or of its loads, 32 KB of W and 128 bn bytes
+// of x per SM.  Taken where that estimate is the lower (us, without and with: 333
+// x 8192 x 2048 with GELU 19.8 / 17.6, 260 x 8192 x 4096 25.8 / 22.4, 700 x 4096 x
+// 4096 24.9 / 22.0, 1111 x 4096 x 4096 37.8 / 35.7).
+struct SwapPlan {
+  int tiles_m, tiles_n, bn;
+  int64_t unit, cycles;
+};
+SwapPlan make_swap_plan(int64_t M, int64_t N, int64_t K, int op) {
+  SwapPlan best{0, 0, 0, 0, -1};
+  const int64_t num_kb = (K + stage_k(op) - 1) / stage_k(op);
+  const int64_t first = (M + BN - 1) / BN;
+  for (int64_t t = first; t < first + 4; ++t) {
+    SwapPlan p;
+    p.bn = int(((M + t - 1) / t + 31) / 32 * 32);
+    p.tiles_m = int((M + p.bn - 1) / p.bn);
+    p.tiles_n = int((N + 2 * BM - 1) / (2 * BM));
+    const int64_t mma = 4 * p.bn, loads = 512 + 2 * p.bn;
+    p.unit = num_kb * (mma > loads ? mma : loads);
+    p.cycles = (int64_t(p.tiles_m) * p.tiles_n + kPlanPairs - 1) / kPlanPairs * p.unit + 4500 * p.bn / BN;
+    if (best.cycles < 0 || p.cycles < best.cycles) best = p;
+  }
+  return best;
+}
 // Whether few_rows.cu takes a product (N: output columns, gated H).
 bool takes_few_rows(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, bool b_mn) {
   return few_rows(M, N, K, gated, fp8,
@@ -873,6 +923,44 @@ cudaError_t launch_join(uint16_t* out, uint16_t* out2, const float* partial, con
                     w_scale, p.splits, p.m_pad, ld, M, N);
 }
 
+// One product in the exchanged form (B K-major or, `B_MN`, [K, N] as it lies).
+template <int OP, int ACT, bool B_MN>
+cudaError_t product_swapped(const SwapPlan& p, uint16_t* out, uint16_t* z, const void* A, const float* a_scale,
+                            const void* B, const float* w_scale, const uint16_t* bias, const uint16_t* in, int64_t M,
+                            int64_t N, int64_t K, cudaStream_t s, bool late_wait, Idle* after) {
+  Maps m;
+  if (!operand_map<OP>(&m.a, B, N, K, B_MN) || !operand_map<OP>(&m.b, A, M, K, false, p.bn / 2)) return cudaErrorInvalidValue;
+  m.bh = m.b;
+  LinArgs a{};
+  a.M = int(M);
+  a.N = int(N);
+  a.bn = p.bn;
+  a.stages = RING_BYTES / (OP_BYTES + p.bn * ROW_BYTES);
+  if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
+  a.tiles_m = p.tiles_m;
+  a.tiles_n = a.band_n = p.tiles_n;
+  a.num_kb = int((K + stage_k(OP) - 1) / stage_k(OP));
+  a.num_units = a.split_from = p.tiles_m * p.tiles_n;
+  a.splits = 1;
+  a.late_wait = late_wait ? 1 : 0;
+  a.a_scale = a_scale;
+  a.w_scale = w_scale;
+  a.bias = bias;
+  a.out = out;
+  a.z = z;
+  a.in = in;
+  int pairs = 0;
+  const cudaError_t e = max_pairs<OP, EPI_LINEAR, ACT, B_MN, false, true>(&pairs);
+  if (e != cudaSuccess) return e;
+  if (after != nullptr) {
+    const int r = a.num_units % pairs;
+    *after = a.num_units < pairs ? Idle{pairs - a.num_units, p.unit - kNextKernelCycles}
+             : r == 0            ? Idle{0, 0}
+                                 : Idle{pairs - r, p.unit};
+  }
+  return launch<OP, EPI_LINEAR, ACT, B_MN, false, true>(m, a, pairs, s);
+}
+
 // One product with its epilogue.  EPI_LINEAR: N output columns; gated forms:
 // N = H and B = W1 [2H, K].  `partial` holds plan_bytes().  `before`: what the
 // kernel launched last leaves idle, if this one may start beside it (late_wait);
@@ -885,6 +973,11 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
   constexpr bool GATED = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
   const int64_t brows = GATED ? 2 * N : N;
   const Plan p = make_plan(M, brows, K, OP, B_MN ? 1 : 2);
+  if constexpr (EPI == EPI_LINEAR && !A_MN) {
+    const SwapPlan sp = make_swap_plan(M, N, K, OP);
+    if (sp.cycles < p.cycles)
+      return product_swapped<OP, ACT, B_MN>(sp, out, z, A, a_scale, B, w_scale, bias, in, M, N, K, s, late_wait, after);
+  }
   Maps m;
   if (!operand_map<OP>(&m.a, A, M, K, A_MN) || !operand_map<OP>(&m.b, B, brows, K, B_MN, B_MN ? 128 : 128 >> p.narrow)) return cudaErrorInvalidValue;
   m.bh = m.b;
