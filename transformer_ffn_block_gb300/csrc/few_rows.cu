@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t drain_bar = bar0 + 8u * uint32_t(2 * kMaxStages + 1);
   const uint32_t recv_bar = bar0 + 8u * uint32_t(2 * kMaxStages + 2);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int part = int(cluster_ctarank());
   // (clusters next to each other read the same weights)
   const int tile = int(cluster_id_x()) / args.tiles_m, mt = int(cluster_id_x()) % args.tiles_m;
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads)
   // first output of this CTA (gated: 64 outputs, 128 otherwise)
   const int n0 = tile * (GATED ? 64 : 128);
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ------------------------------------------------------------ producer
       uint32_t issued = 0, issued_parity = 0;
       int s = 0;
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ------------------------------------------------------------ MMA issuer
       // D fp32, operand formats, W MN-major, N = bn, M = 128 (see linear.cu)
       const uint32_t idesc = (1u << 4) | (OP == OP_BF16 ? (1u << 7) | (1u << 10) : 0u) | (W_MN ? 1u << 15 : 0u) |

@@ -17,13 +17,17 @@
 //
 // Pipeline: SM pairs (2-CTA clusters), persistent over 256 x 256 tiles, one
 // tcgen05.mma.cta_group::2 (M = 256, N = 256) chain per tile; CTA r of a pair
-// stages rows [128 r, 128 r + 128) of A and of the tile's 256 weight rows,
-// 256 bytes of K per stage and row, three stages (four of narrow units).  One warp loads (TMA,
-// 128-byte swizzle), one thread of the leader issues the MMAs, eight warps per
-// CTA run the epilogue out of one of two TMEM accumulators while the next tile
-// accumulates in the other.  Per SM and byte of K this loads 16 + 16 KB per
+// stages rows [128 r, 128 r + 128) of A and of the tile's 256 weight rows, 128
+// bytes of K per stage and row, six stages (eight of narrow units).  One warp loads
+// (TMA, 128-byte swizzle), one thread of the leader issues the MMAs, eight warps
+// per CTA run the epilogue out of one of two TMEM accumulators while the next
+// tile accumulates in the other.  Per SM and byte of K this loads 16 + 16 KB per
 // 128 x 256 outputs; a bf16 MMA takes twice the cycles of an E4M3 one over the
-// same bytes of shared memory, so the operand feed has room to spare.
+// same bytes of shared memory, so the operand feed has room to spare.  What binds
+// narrow units is the issue of the MMAs: with the issuing thread chosen by its lane's number
+// 70 cycles each, by elect.sync 24; that and stages of one swizzle row instead
+// of two took 512 x 4096 x 4096 from 19.4 to 16.0 us and 8192 x 4096 x 28672 (gated)
+// from 1066 to 1054.
 //
 // Every mbarrier wait is bounded; see gemm_fp8.cu for how a wait that runs out
 // ends the kernel (abort flag, status word, drained copies and MMAs).
@@ -42,12 +46,11 @@ namespace {
 constexpr int BM = 128;                    // rows of A per CTA (256 per pair)
 constexpr int BN = 256;                    // accumulator columns
 constexpr int ROW_BYTES = 128;             // one swizzle atom row
-constexpr int BOX_BYTES = 128 * ROW_BYTES; // one TMA box: 128 rows
-constexpr int KBOX = 2;                    // boxes per operand and stage
-constexpr int MAX_STAGES = 4;
-constexpr int OP_BYTES = KBOX * BOX_BYTES; // one operand's share of a stage
-constexpr int RING_BYTES = 3 * 2 * OP_BYTES;   // the stages: three of whole units, four of narrow ones
-constexpr int STEPS = 8;                   // MMAs per stage (32 bytes of K each)
+constexpr int OP_BYTES = 128 * ROW_BYTES;  // an operand's share of a stage: 128 rows of one swizzle row
+constexpr int MN_BOX_BYTES = 64 * ROW_BYTES;   // MN-major: 64 values by 64 of K, two boxes to the share
+constexpr int MAX_STAGES = 8;
+constexpr int RING_BYTES = 6 * 2 * OP_BYTES;   // the stages: six of whole units, eight of narrow ones
+constexpr int STEPS = 4;                   // MMAs per stage (32 bytes of K each)
 constexpr int EPI_WARPS = 8;
 constexpr int NUM_THREADS = 64 + 32 * EPI_WARPS;
 constexpr int TMEM_COLS = 2 * BN;
@@ -63,9 +66,7 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 constexpr unsigned long long kDrainLimitNs = 200000000ull;
 
 constexpr int OP_BF16 = 0, OP_E4M3 = 1;
-// elements of K per box row, and per stage
-constexpr int box_k(int op) { return op == OP_BF16 ? 64 : 128; }
-constexpr int stage_k(int op) { return KBOX * box_k(op); }
+constexpr int stage_k(int op) { return op == OP_BF16 ? 64 : 128; }   // elements of K per stage
 
 constexpr int EPI_LINEAR = 0, EPI_GATED = 1, EPI_GATED_BWD = 2, EPI_PARTIAL = 3;
 
@@ -124,16 +125,15 @@ QFFN_DEVI void mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_
 }
 
 // Shared-memory descriptor of MMA step i of a stage's operand.
-// K-major: box i/4 (64 or 128 elements of K), 32 bytes along its 128-byte rows
-// per step.  MN-major (16-bit types): the operand's 128 M (N) values lie in two
-// boxes of 64 values x 128 K rows; a step is 16 K rows of 128 bytes (8-row
-// groups 1024 bytes apart) in both boxes, whose distance is the leading byte
-// offset.
+// K-major: 32 bytes along its 128-byte rows per step.  MN-major (16-bit types):
+// the operand's 128 M (N) values lie in two boxes of 64 values x 64 K rows; a step
+// is 16 K rows of 128 bytes (8-row groups 1024 bytes apart) in both boxes, whose
+// distance is the leading byte offset.
 template <bool MN>
-QFFN_DEVI uint64_t step_desc(uint32_t base, int i, uint32_t box_bytes) {
-  if (!MN) return sdesc_sw128(base + uint32_t(i >> 2) * box_bytes + uint32_t(i & 3) * 32u);
+QFFN_DEVI uint64_t step_desc(uint32_t base, int i) {
+  if (!MN) return sdesc_sw128(base + uint32_t(i) * 32u);
   const uint64_t d = sdesc_sw128(base + uint32_t(i) * 16u * ROW_BYTES);
-  return (d & ~(uint64_t(0x3FFF) << 16)) | (uint64_t(BOX_BYTES >> 4) << 16);
+  return (d & ~(uint64_t(0x3FFF) << 16)) | (uint64_t(MN_BOX_BYTES >> 4) << 16);
 }
 
 QFFN_DEVI bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, bool honour_abort = true,
@@ -199,9 +199,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* sStaging = smem + RING_BYTES;
   // a stage: this CTA's A rows, then its B rows
   const int bn = SWAP ? args.bn : BN >> args.narrow;           // accumulator columns of a whole unit
-  const uint32_t b_box = uint32_t(bn / 2 * ROW_BYTES);         // bytes of a box of this CTA's bn / 2 B rows
-  const uint32_t ring = smem_u32(smem), stage_bytes = uint32_t(OP_BYTES) + KBOX * b_box;
-  const int stages = SWAP ? args.stages : args.narrow == 0 ? 3 : MAX_STAGES;
+  const uint32_t ring = smem_u32(smem), stage_bytes = uint32_t(OP_BYTES + bn / 2 * ROW_BYTES);
+  const int stages = SWAP ? args.stages : args.narrow == 0 ? 6 : MAX_STAGES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sStaging + STAGING_BYTES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -216,7 +215,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t drain_bar = bar0 + 8u * uint32_t(2 * MAX_STAGES + 4);
 
   constexpr bool GATED = EPI == EPI_GATED || EPI == EPI_GATED_BWD;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = int(cluster_id_x()), num_pairs = int(num_clusters_x());
 
@@ -257,7 +256,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // ------------------------------------------------------------ producer
       uint32_t issued = 0, issued_parity = 0, ph = 0;
       int s = 0;
@@ -278,18 +277,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (rank == 0) mbar_expect_tx(full_bar(s), stage_tx);
           const uint32_t fb = map_to_rank(full_bar(s), 0);
           const int k0 = kb * stage_k(OP);
-#pragma unroll
-          for (int bx = 0; bx < KBOX; ++bx) {
-            const uint32_t da = ring + uint32_t(s) * stage_bytes + uint32_t(bx * BOX_BYTES);
-            const uint32_t db = ring + uint32_t(s) * stage_bytes + uint32_t(OP_BYTES) + uint32_t(bx) * b_box;
-            if (A_MN) tma_load_2d_pair(da, &tmA, fb, rowA + bx * 64, k0);
-            else tma_load_2d_pair(da, &tmA, fb, k0 + bx * box_k(OP), rowA);
-            if (B_MN) {
-              // 64 rows (a half tile's or a narrow unit's) are one box
-              if ((u.half < 0 && args.narrow == 0) || bx == 0) tma_load_2d_pair(db, &tmB, fb, rowB + bx * 64, k0);
-            } else {
-              tma_load_2d_pair(db, u.half < 0 ? &tmB : &tmBh, fb, k0 + bx * box_k(OP), rowB);
-            }
+          const uint32_t da = ring + uint32_t(s) * stage_bytes, db = da + uint32_t(OP_BYTES);
+          if (A_MN) {
+            tma_load_2d_pair(da, &tmA, fb, rowA, k0);
+            tma_load_2d_pair(da + MN_BOX_BYTES, &tmA, fb, rowA + 64, k0);
+          } else {
+            tma_load_2d_pair(da, &tmA, fb, k0, rowA);
+          }
+          if (B_MN) {
+            tma_load_2d_pair(db, &tmB, fb, rowB, k0);
+            // (the 64 rows of a half tile or a narrow unit are one box)
+            if (u.half < 0 && args.narrow == 0) tma_load_2d_pair(db + MN_BOX_BYTES, &tmB, fb, rowB + 64, k0);
+          } else {
+            tma_load_2d_pair(db, u.half < 0 ? &tmB : &tmBh, fb, k0, rowB);
           }
           issued |= 1u << s;
           issued_parity = (issued_parity & ~(1u << s)) | (ph << s);
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       // ------------------------------------------------------------ MMA issuer (leader)
       int s = 0, local = 0;
       uint32_t ph = 0;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const uint32_t a0 = ring + uint32_t(s) * stage_bytes, b0 = a0 + uint32_t(OP_BYTES);
 #pragma unroll
           for (int i = 0; i < STEPS; ++i)
-            mma_pair<OP>(d_tmem, step_desc<A_MN>(a0, i, BOX_BYTES), step_desc<B_MN>(b0, i, b_box), idesc,
+            mma_pair<OP>(d_tmem, step_desc<A_MN>(a0, i), step_desc<B_MN>(b0, i), idesc,
                          uint32_t((kb - kb0) | i));
           mma_commit_mc(empty_bar(s), kBothCtas);
           if (++s == stages) {
@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(256) act_backward_kernel(uint16_t* dz, float* 
 // An MMA operand: [rows, k] K-major or, `mn`, [k, rows] as it lies in memory.
 template <int OP>
 bool operand_map(CUtensorMap* map, const void* ptr, int64_t rows, int64_t k, bool mn, int box_rows = 128) {
-  return mn ? make_operand_map(map, ptr, OP == OP_BF16, k, rows, box_rows)
+  return mn ? make_operand_map(map, ptr, OP == OP_BF16, k, rows, 64)
             : make_operand_map(map, ptr, OP == OP_BF16, rows, k, box_rows);
 }
 
@@ -817,7 +817,7 @@ struct Plan {
 };
 constexpr int kPlanPairs = kNumSMsHint / 2;   // fixed, so a workspace size needs no device query
 constexpr int64_t kNextKernelCycles = 6000;   // from a kernel's start to the next one's
-constexpr int stage_cycles(int narrow) { return narrow == 0 ? 1024 : narrow == 1 ? 768 : 640; }
+constexpr int stage_cycles(int narrow) { return narrow == 0 ? 512 : narrow == 1 ? 384 : 320; }
 
 // What a product leaves idle at its end: this many SM pairs for so many cycles.
 struct Idle {
@@ -833,11 +833,11 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
   p.narrow = 0;
   p.splits = 1;
   const int64_t whole = int64_t(p.tiles_m) * ((N + BN - 1) / BN);
-  p.cycles = (whole + kPlanPairs - 1) / kPlanPairs * p.num_kb * 1024 + 4500;
+  p.cycles = (whole + kPlanPairs - 1) / kPlanPairs * p.num_kb * 512 + 4500;
   if (2 * whole <= kPlanPairs) {
     // Less than half a round of whole tiles: the cheapest of narrower units and
     // parts of K, in SM cycles.  A stage of a unit takes the cycles of its MMAs
-    // (1024 >> narrow) or of its loads (32 KB of A and 32 KB >> narrow of B per
+    // (512 >> narrow) or of its loads (16 KB of A and 16 KB >> narrow of B per
     // SM at 64 bytes a cycle), the last unit's epilogue 4500 >> narrow, joining
     // parts about 8200 and 500 for each.  Measured, parts of K alone against
     // this choice: 512 x 4096 x 4096 24.5 / 19.3 us, 256 x 8192 x 2048 20.2 /
@@ -846,7 +846,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
     for (int n = 0; n <= max_narrow; ++n) {
       const int64_t units = int64_t(p.tiles_m) * ((N + (BN >> n) - 1) / (BN >> n));
       const int stage = stage_cycles(n);
-      for (int s = 1; s <= 16 && (s == 1 || (s * 4 <= p.num_kb && units * s <= kPlanPairs)); ++s) {
+      for (int s = 1; s <= 16 && (s == 1 || (s * 8 <= p.num_kb && units * s <= kPlanPairs)); ++s) {
         const int64_t rounds = (units * s + kPlanPairs - 1) / kPlanPairs;
         const int64_t cost = rounds * ((p.num_kb + s - 1) / s) * stage + (4500 >> n) + (s > 1 ? 8200 + 500 * s : 0);
         if (best < 0 || cost < best) {
@@ -866,7 +866,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
 }
 // The same product with the operands exchanged: units of 256 output columns by
 // bn rows, a multiple of 32, so that the rows divide evenly into tiles.  A stage
-// takes the cycles of its MMAs, 4 bn, or of its loads, 32 KB of W and 128 bn bytes
+// takes the cycles of its MMAs, 2 bn, or of its loads, 16 KB of W and 64 bn bytes
 // of x per SM.  Taken where that estimate is the lower (us, without and with: 333
 // x 8192 x 2048 with GELU 19.8 / 17.6, 260 x 8192 x 4096 25.8 / 22.4, 700 x 4096 x
 // 4096 24.9 / 22.0, 1111 x 4096 x 4096 37.8 / 35.7).
@@ -883,7 +883,7 @@ SwapPlan make_swap_plan(int64_t M, int64_t N, int64_t K, int op) {
     p.bn = int(((M + t - 1) / t + 31) / 32 * 32);
     p.tiles_m = int((M + p.bn - 1) / p.bn);
     p.tiles_n = int((N + 2 * BM - 1) / (2 * BM));
-    const int64_t mma = 4 * p.bn, loads = 512 + 2 * p.bn;
+    const int64_t mma = 2 * p.bn, loads = 256 + p.bn;
     p.unit = num_kb * (mma > loads ? mma : loads);
     p.cycles = (int64_t(p.tiles_m) * p.tiles_n + kPlanPairs - 1) / kPlanPairs * p.unit + 4500 * p.bn / BN;
     if (best.cycles < 0 || p.cycles < best.cycles) best = p;
@@ -935,7 +935,7 @@ cudaError_t product_swapped(const SwapPlan& p, uint16_t* out, uint16_t* z, const
   a.M = int(M);
   a.N = int(N);
   a.bn = p.bn;
-  a.stages = RING_BYTES / (OP_BYTES + p.bn * ROW_BYTES);
+  a.stages = RING_BYTES / (OP_BYTES + p.bn / 2 * ROW_BYTES);
   if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
   a.tiles_m = p.tiles_m;
   a.tiles_n = a.band_n = p.tiles_n;
@@ -979,7 +979,7 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
       return product_swapped<OP, ACT, B_MN>(sp, out, z, A, a_scale, B, w_scale, bias, in, M, N, K, s, late_wait, after);
   }
   Maps m;
-  if (!operand_map<OP>(&m.a, A, M, K, A_MN) || !operand_map<OP>(&m.b, B, brows, K, B_MN, B_MN ? 128 : 128 >> p.narrow)) return cudaErrorInvalidValue;
+  if (!operand_map<OP>(&m.a, A, M, K, A_MN) || !operand_map<OP>(&m.b, B, brows, K, B_MN, 128 >> p.narrow)) return cudaErrorInvalidValue;
   m.bh = m.b;
   LinArgs a{};
   a.M = int(M);
