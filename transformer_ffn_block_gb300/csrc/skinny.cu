@@ -1,5 +1,5 @@
-// Linear and gated layers for few rows of activations (decode, M <= 32):
-// HBM-bound on the weights.
+// Linear and gated layers for few rows of activations (decode) or few weights:
+// bound by the weights' way from HBM.
 //
 //   out[m, r] = bf16(res + act(s * sum_k W[r,k] x[m,k] + bias[r]))   (and z)
 //   h[m, r]   = bf16(act(g) * u),  g / u from rows r and H + r of W1
@@ -52,6 +52,8 @@ QFFN_DEVI void mma_16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+QFFN_DEVI void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 QFFN_DEVI float act_any(int act, float z) {
   switch (act) {
     case ACT_RELU: return act_f32<ACT_RELU>(z);
@@ -85,6 +87,20 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 32 : 16) / WARPS) skinn
 #pragma unroll
   for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  // The first group's weights on their way into L2 while the preceding kernel ends:
+  // a hint, so it may run before that kernel's results are there (bf16, one row:
+  // 4096 x 14336 20.3 -> 18.5 us, 28672 x 4096 36.3 -> 34.4; two groups lose on
+  // the latter, 39.2, and E4M3, with half the bytes, loses: 12.9 -> 13.2).
+  if (!FP8) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int64_t k = int64_t(warp) * (kU * 64) + u * 64;
+      if (k + t * 16 < a.row_bytes) {
+        prefetch_l2(wa + k);
+        prefetch_l2(wb + k);
+      }
+    }
+  }
   pdl_wait();
   pdl_trigger();
   for (int64_t k0 = int64_t(warp) * (kU * 64); k0 < a.row_bytes; k0 += int64_t(WARPS) * (kU * 64)) {
@@ -177,8 +193,8 @@ cudaError_t run(const SkinnyArgs& a, cudaStream_t s) {
 // reads the weights again, through L2: about 4 ns per CTA and 7.3 ns per CTA
 // and 1024 elements of K over the whole grid, against 4.5 us and more that a
 // tcgen05 kernel takes to set up, fill and drain.  It is taken while that
-// sum is below 5 us (E4M3, whose products cost the same and whose loads cost the
-// other form half: 3 us).  Measured in us, this form against the other: 256 rows
+// sum is below 4.4 us (E4M3, whose products cost the same and whose loads cost the
+// other form half: 2.9 us).  Measured in us, this form against the other: 256 rows
 // of 768 x 256 4.2 / 7.0, of 1024 x 1024 7.3 / 8.5, 64 rows of 4096 x 1024 7.7 /
 // 7.8, 32 rows of 28672 x 4096 58 / 41, E4M3 64 rows of 4096 x 256 6.5 / 4.9.
 bool skinny_rows(int64_t M, int64_t wrows, int64_t K, bool fp8) {
