@@ -519,21 +519,18 @@ int few_rows_bn(int64_t M) {
 }
 }  // namespace
 
-// Up to 512 rows, by an estimate of both forms in SM cycles: here about 640 per
-// stage and round of clusters, 48 per row of a tile for its sums and stores, 700
-// for each further tile of rows and 4000 for an exchange; there 1.4 times the
-// plan's cycles.  Measured in us, here
-// against there: 64 rows of 4096 x 1024 7.0 / 7.8, 128 rows 9.1 / 7.8, of 4096 x
-// 4096 13.4 / 20, 256 rows 17.1 / 20, of 2048 x 2048 9.9 / 11.7, of 8192 x 2048
-// 16.5 / 13.5, of 4096 x 14336 42 / 36, of 28672 x 4096 68 / 49.
-bool few_rows(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, int64_t other_cycles) {
-  if (M > 512) return false;
+// Up to 512 rows: an estimate in SM cycles, fitted to measurements of 64 to 512
+// rows: 5700 for the call, per round of clusters 500 for each stage and 39 for
+// each row of a tile, 3900 for an exchange (beyond: -1).  Measured in us, here against
+// linear.cu's forms: 64 rows of 2048 x 2048 6.9 / 8.2, of 4096 x 4096 10.6 / 12.9, of 4096 x
+// 14336 23.3 / 28.4, of 4096 x 1024 6.7 / 6.2, of 14336 x 4096 23.1 / 22.3, 128 rows of
+// 4096 x 4096 13.4 / 13.8, of 2048 x 2048 9.1 / 8.2, 256 rows of 14336 x 4096 33 / 27.5.
+int64_t few_rows_cycles(int64_t M, int64_t N, int64_t K, bool gated, bool fp8) {
+  if (M > 512) return -1;
   int clusters, splits, num_kb;
-  if (few_rows_split(M, N, K, gated, fp8, &clusters, &splits, &num_kb) != cudaSuccess) return false;
+  if (few_rows_split(M, N, K, gated, fp8, &clusters, &splits, &num_kb) != cudaSuccess) return -1;
   const int64_t rounds = (int64_t(clusters) * splits + kNumSMsHint - 1) / kNumSMsHint;
-  const int64_t here = rounds * ((num_kb + splits - 1) / splits) * 640 + 48 * few_rows_bn(M) +
-                       700 * ((M + 127) / 128 - 2) + (splits > 1 ? 4000 : 0);
-  return 10 * here < 14 * other_cycles + 6000;
+  return 5700 + rounds * (((num_kb + splits - 1) / splits) * 500 + 39 * few_rows_bn(M)) + (splits > 1 ? 3900 : 0);
 }
 
 // One product: x [M, K] (K-major), W [wrows, K] or, w_mn, [K, wrows].
@@ -559,7 +556,7 @@ cudaError_t few_rows_product(uint16_t* out, uint16_t* z, const void* x, const fl
   const cudaError_t e = few_rows_split(M, N, K, GATED, OP == OP_E4M3, &clusters, &a.splits, &a.num_kb);
   if (e != cudaSuccess) return e;
   a.stage_bytes = BOX_BYTES + a.bn * ROW_BYTES;
-  const bool two = clusters * a.splits > kNumSMsHint && a.bn <= 128;
+  const bool two = clusters * a.splits > kNumSMsHint;
   a.recv_bytes = (a.splits - 1) * (a.bn / a.splits) * 512;
   // (the sums, bn x 512 bytes, take at most 64 KB of the stages' 96 to 200 KB)
   a.stages = ((two ? kSmemTwo : kSmemOne) - a.recv_bytes) / a.stage_bytes;

@@ -176,11 +176,10 @@ cudaError_t launch_skinny(uint16_t* out, uint16_t* z, const void* x, const float
                           int64_t N, int64_t K, bool fp8, cudaStream_t s);
 cudaError_t launch_skinny_gated(uint16_t* h, const uint16_t* x, const uint16_t* w1, int act, int64_t M, int64_t C,
                                 int64_t H, cudaStream_t s);
-// The forms for few rows on the tensor cores (few_rows.cu), taken where few_rows()
-// and, forward, not skinny_rows(); other_cycles: linear.cu's estimate for the
-// same product.  No workspace.  w_mn: w given as [K, N]
-// (bf16).  Gated: h from w1 = [2H, C], or, with dh, d_gu [M, 2H].
-bool few_rows(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, int64_t other_cycles);
+// The forms for few rows on the tensor cores (few_rows.cu) and the estimate of
+// their time in SM cycles, -1 where they do not apply.  No workspace.  w_mn: w given
+// as [K, N] (bf16).  Gated: h from w1 = [2H, C], or, with dh, d_gu [M, 2H].
+int64_t few_rows_cycles(int64_t M, int64_t N, int64_t K, bool gated, bool fp8);
 cudaError_t launch_few_rows(uint16_t* out, uint16_t* z, const void* x, const float* x_scale, const void* w,
                             const float* w_scale, const uint16_t* bias, const uint16_t* res, int act, int64_t M,
                             int64_t N, int64_t K, bool fp8, bool w_mn, cudaStream_t s, bool late_wait = false);

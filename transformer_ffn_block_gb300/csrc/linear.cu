@@ -824,8 +824,9 @@ struct Plan {
   int64_t cycles;            // estimate
 };
 constexpr int kPlanPairs = kNumSMsHint / 2;   // fixed, so a workspace size needs no device query
+constexpr int kFixedCycles = 7800;            // of a call: launch, first loads, end
 constexpr int64_t kNextKernelCycles = 6000;   // from a kernel's start to the next one's
-constexpr int stage_cycles(int narrow) { return narrow == 0 ? 512 : narrow == 1 ? 384 : 320; }
+constexpr int stage_cycles(int narrow) { return narrow == 0 ? 512 : narrow == 1 ? 308 : 288; }
 
 // What a product leaves idle at its end: this many SM pairs for so many cycles.
 struct Idle {
@@ -841,22 +842,24 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
   p.narrow = 0;
   p.splits = 1;
   const int64_t whole = int64_t(p.tiles_m) * ((N + BN - 1) / BN);
-  p.cycles = (whole + kPlanPairs - 1) / kPlanPairs * p.num_kb * 512 + 4500;
+  const int64_t rest = whole % kPlanPairs;       // (a last round of up to half the pairs' number: half tiles)
+  const int64_t half_rounds = 2 * (whole / kPlanPairs) + (rest == 0 ? 0 : whole > kPlanPairs && 2 * rest <= kPlanPairs ? 1 : 2);
+  p.cycles = half_rounds * p.num_kb * 256 + kFixedCycles + 2560;
   if (2 * whole <= kPlanPairs) {
     // Less than half a round of whole tiles: the cheapest of narrower units and
-    // parts of K, in SM cycles.  A stage of a unit takes the cycles of its MMAs
-    // (512 >> narrow) or of its loads (16 KB of A and 16 KB >> narrow of B per
-    // SM at 64 bytes a cycle), the last unit's epilogue 4500 >> narrow, joining
-    // parts about 8200 and 500 for each.  Measured, parts of K alone against
-    // this choice: 512 x 4096 x 4096 24.5 / 19.3 us, 256 x 8192 x 2048 20.2 /
-    // 12.6, 256 x 1024 x 1024 10.5 / 6.8.
+    // parts of K, in SM cycles, fitted to measurements of 64 to 1000 rows: a stage
+    // takes its MMAs' cycles or what the loads and the issue of the MMAs take,
+    // the last unit's epilogue 2560 >> narrow, joining parts 5700 and for each 450
+    // and one for 700 outputs.  (us, parts of K alone / this choice: 512 x 4096 x
+    // 4096 21 / 15.6, 200 x 1024 x 4096 13.2 / 9.9, 256 x 1024 x 1024 9.5 / 5.7.)
     int64_t best = -1;
     for (int n = 0; n <= max_narrow; ++n) {
       const int64_t units = int64_t(p.tiles_m) * ((N + (BN >> n) - 1) / (BN >> n));
       const int stage = stage_cycles(n);
       for (int s = 1; s <= 16 && (s == 1 || (s * 8 <= p.num_kb && units * s <= kPlanPairs)); ++s) {
         const int64_t rounds = (units * s + kPlanPairs - 1) / kPlanPairs;
-        const int64_t cost = rounds * ((p.num_kb + s - 1) / s) * stage + (4500 >> n) + (s > 1 ? 8200 + 500 * s : 0);
+        const int64_t join = s == 1 ? 0 : 5700 + (450 + M * N / 700) * s;
+        const int64_t cost = rounds * ((p.num_kb + s - 1) / s) * stage + kFixedCycles + (2560 >> n) + join;
         if (best < 0 || cost < best) {
           best = cost;
           p.narrow = n;
@@ -874,10 +877,10 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
 }
 // The same product with the operands exchanged: units of 256 output columns by
 // bn rows, a multiple of 32, so that the rows divide evenly into tiles.  A stage
-// takes the cycles of its MMAs, 2 bn, or of its loads, 16 KB of W and 64 bn bytes
-// of x per SM.  Taken where that estimate is the lower (us, without and with: 333
-// x 8192 x 2048 with GELU 19.8 / 17.6, 260 x 8192 x 4096 25.8 / 22.4, 700 x 4096 x
-// 4096 24.9 / 22.0, 1111 x 4096 x 4096 37.8 / 35.7).
+// takes 113 + 1.55 bn cycles, 288 at least (fitted, as above).  Taken where that
+// estimate is the lower (us, without and with: 333 x 8192 x 2048 with GELU 18.3 /
+// 16.3, 260 x 8192 x 4096 25.8 / 18.9, 700 x 4096 x 4096 23.4 / 19.9, 333 x 4096 x
+// 14336 41.6 / 39.7).
 struct SwapPlan {
   int tiles_m, tiles_n, bn;
   int64_t unit, cycles;
@@ -891,17 +894,27 @@ SwapPlan make_swap_plan(int64_t M, int64_t N, int64_t K, int op) {
     p.bn = int(((M + t - 1) / t + 31) / 32 * 32);
     p.tiles_m = int((M + p.bn - 1) / p.bn);
     p.tiles_n = int((N + 2 * BM - 1) / (2 * BM));
-    const int64_t mma = 2 * p.bn, loads = 256 + p.bn;
-    p.unit = num_kb * (mma > loads ? mma : loads);
-    p.cycles = (int64_t(p.tiles_m) * p.tiles_n + kPlanPairs - 1) / kPlanPairs * p.unit + 4500 * p.bn / BN;
+    const int64_t stage = 113 + 31 * p.bn / 20;
+    p.unit = num_kb * (stage > 288 ? stage : 288);
+    p.cycles = (int64_t(p.tiles_m) * p.tiles_n + kPlanPairs - 1) / kPlanPairs * p.unit + kFixedCycles + 12 * p.bn;
     if (best.cycles < 0 || p.cycles < best.cycles) best = p;
   }
   return best;
 }
-// Whether few_rows.cu takes a product (N: output columns, gated H).
+// Whether few_rows.cu takes a product (N: output columns, gated H): where its
+// estimate is the lower.  No form beats the weights' way from HBM, about 2900
+// bytes a cycle; where that bounds both, the exchanged form is the faster (64 rows
+// of 28672 x 4096 40.2 us, few_rows.cu 41.6, this one unexchanged 44.3).
 bool takes_few_rows(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, bool b_mn) {
-  return few_rows(M, N, K, gated, fp8,
-                  make_plan(M, gated ? 2 * N : N, K, fp8 ? OP_E4M3 : OP_BF16, b_mn ? 1 : 2).cycles);
+  const int op = fp8 ? OP_E4M3 : OP_BF16;
+  const int64_t wrows = gated ? 2 * N : N;
+  const int64_t few = few_rows_cycles(M, N, K, gated, fp8);
+  if (few < 0) return false;
+  const int64_t hbm = kFixedCycles + wrows * K * (fp8 ? 1 : 2) / 2900;
+  const int64_t here = make_plan(M, wrows, K, op, b_mn ? 1 : 2).cycles;
+  if (gated) return few < (here > hbm ? here : hbm + 1);
+  const int64_t swapped = make_swap_plan(M, N, K, op).cycles;
+  return few < here && few < swapped && swapped > hbm;
 }
 // (A workspace size must not depend on the device: it covers the plan whether or
 // not few_rows.cu is taken.)
@@ -1024,7 +1037,9 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
   a.num_units = a.split_from = a.tiles_m * a.tiles_n;
   if ((e = max_pairs<OP, EPI, ACT, A_MN, B_MN>(&pairs)) != cudaSuccess) return e;
   // a last partial wave of R <= pairs / 2 tiles runs as 2 R half tiles in half the time
-  const int64_t unit = int64_t(p.num_kb) * stage_cycles(p.narrow);
+  // (a unit's epilogue, beside the next one's products, takes some 4000 cycles)
+  int64_t unit = int64_t(p.num_kb) * stage_cycles(p.narrow);
+  if (unit < 4000 >> p.narrow) unit = 4000 >> p.narrow;
   auto last_wave = [&](int units) { return units > pairs ? units % pairs : 0; };
   auto halves = [&](int r) { return p.narrow == 0 && r > 0 && 2 * r <= pairs; };
   if (before.pairs > 0 && before.pairs < pairs && a.num_units > pairs) {
