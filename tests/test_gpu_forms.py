@@ -34,6 +34,24 @@ GATED_BACKWARD = [(135, 8, 5192), (139, 3312, 1248), (414, 1992, 8), (534, 8, 33
                   (524, 2800, 8), (35, 520, 2520), (700, 2056, 2504)]
 
 
+# the same with the operands exchanged (columns and rows of several tiles), and every split of few rows in each number
+# of tiles
+FORWARD += [(776, 2312, 8), (653, 3104, 8), (66, 6640, 136), (33, 9928, 8), (19, 5008, 4696), (270, 3144, 8176),
+            (165, 584, 2192), (257, 488, 2104), (410, 432, 2576), (372, 312, 1992), (1486, 2848, 8), (1472, 10032, 8),
+            (1145, 7352, 80), (803, 1256, 136), (338, 2504, 8), (104, 792, 2632)]
+FORWARD_FP8 += [(771, 2392, 16), (772, 2648, 16), (68, 6472, 144), (18, 11336, 16), (154, 264, 4400), (279, 176, 4208),
+                (421, 416, 4896), (18, 1440, 4064), (133, 232, 4880), (322, 104, 4768), (1488, 2424, 16),
+                (1467, 7656, 16), (1160, 7344, 144), (816, 1248, 272), (516, 1632, 16), (9, 8, 16)]
+GATED += [(17, 8, 10232), (267, 8, 2448), (17, 2520, 2440), (281, 5160, 1464), (33, 1760, 1072), (258, 2072, 232),
+          (421, 2480, 264), (34, 4680, 464), (234, 1992, 248), (499, 2416, 104), (260, 8, 8056), (70, 8, 2928),
+          (99, 2600, 392)]
+BACKWARD += [(3384, 8, 3400), (1, 4912, 4904), (131, 1952, 8), (272, 1960, 8), (503, 2064, 16), (259, 2360, 8),
+             (1463, 8, 2456), (1454, 72, 5968), (1, 5256, 5080), (588, 8, 3080), (796, 8, 2592), (68, 136, 6728)]
+GATED_BACKWARD += [(1, 8, 9840), (257, 8, 2480), (1, 1992, 2448), (279, 4728, 1480), (1, 976, 8), (147, 1928, 8),
+                   (275, 2144, 8), (393, 2464, 216), (1, 2000, 8), (131, 2280, 8), (259, 2008, 8), (267, 8, 7376),
+                   (1, 5136, 2800), (65, 8, 2616), (71, 3088, 8)]
+
+
 @pytest.mark.parametrize("M,N,K", FORWARD)
 @pytest.mark.parametrize("name,bias,res,save_z", [("none", False, False, False), ("gelu", True, True, True)])
 def test_linear_forms(q, M, N, K, name, bias, res, save_z):  # noqa: F811
@@ -47,7 +65,7 @@ def test_linear_fp8_forms(q, M, N, K, name, bias, res, save_z):  # noqa: F811
 
 
 @pytest.mark.parametrize("M,N,K", [(16, 520, 264), (133, 2008, 8), (33, 1072, 4392), (101, 4312, 8), (533, 408, 4568),
-                                   (1100, 5000, 200)])
+                                   (700, 3104, 264), (1100, 5000, 200)])
 def test_linear_residual_in_place_in_each_form(q, M, N, K):  # noqa: F811
     x, w, r, b = _t(1, M, K).cuda(), _t(2, N, K, std=K ** -0.5).cuda(), _t(3, M, N).cuda(), _t(4, N).cuda()
     ws = torch.empty(q.qffn_linear_workspace_size(M, N, K), dtype=torch.uint8, device="cuda")
