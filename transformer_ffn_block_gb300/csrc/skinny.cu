@@ -87,11 +87,13 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 32 : 16) / WARPS) skinn
 #pragma unroll
   for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  // The first group's weights on their way into L2 while the preceding kernel ends:
-  // a hint, so it may run before that kernel's results are there (bf16, one row:
-  // 4096 x 14336 20.3 -> 18.5 us, 28672 x 4096 36.3 -> 34.4; two groups lose on
-  // the latter, 39.2, and E4M3, with half the bytes, loses: 12.9 -> 13.2).
-  if (!FP8) {
+  // With few CTAs, all resident at once, the first group's weights set out for L2
+  // while the preceding kernel ends: a hint, so it may run before that kernel's
+  // results are there.  Measured, us without and with, one row: 4096 x 14336 in part
+  // in L2 17.45 / 15.9, from HBM 20.1 / 20.3, 4096 x 4096 7.0 / 6.9.  More CTAs than
+  // that only disturb each other's order in HBM: 28672 x 4096 35.6 / 37.6, gated 4096
+  // x 14336 35.4 / 36.6; and so does E4M3.
+  if (!FP8 && NT == 1 && WARPS >= 16) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int64_t k = int64_t(warp) * (kU * 64) + u * 64;
