@@ -347,19 +347,21 @@ __global__ void __launch_bounds__(kThreads)
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
+      bool ready = false;                    // the next stage was there before this one's MMAs were issued
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
+        if (!ready && !mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t a0 = smem_u32(smem) + uint32_t(s * args.stage_bytes), b0 = a0 + BOX_BYTES;
-#pragma unroll
-        for (int i = 0; i < STEPS; ++i)
-          mma_one<OP>(tmem_base, w_desc<W_MN>(a0, i), sdesc_sw128(b0 + uint32_t(i) * 32u), idesc,
-                      uint32_t((kb - kb0) | i));
-        mma_commit(empty_bar(s));
+        const uint32_t a0 = smem_u32(smem) + uint32_t(s * args.stage_bytes), b0 = a0 + BOX_BYTES, empty = empty_bar(s);
         if (++s == args.stages) {
           s = 0;
           ph ^= 1u;
         }
+        ready = kb + 1 < kb1 && mbar_test_wait(full_bar(s), ph);
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+          mma_one<OP>(tmem_base, w_desc<W_MN>(a0, i), sdesc_sw128(b0 + uint32_t(i) * 32u), idesc,
+                      uint32_t((kb - kb0) | i));
+        mma_commit(empty);
       }
       if (ok) mma_commit(done_bar);
       mma_commit(drain_bar);

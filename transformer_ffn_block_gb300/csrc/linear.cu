@@ -324,19 +324,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
         const uint32_t idesc = idesc_for(OP, A_MN, B_MN, u.half < 0 ? bn : BN / 2);
         const int kb0 = kb_begin(u), kb1 = kb_end(u);
+        bool ready = false;                  // the next stage was there before this one's MMAs were issued
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
+          if (!ready && !mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a0 = ring + uint32_t(s) * stage_bytes, b0 = a0 + uint32_t(OP_BYTES);
-#pragma unroll
-          for (int i = 0; i < STEPS; ++i)
-            mma_pair<OP>(d_tmem, step_desc<A_MN>(a0, i), step_desc<B_MN>(b0, i), idesc,
-                         uint32_t((kb - kb0) | i));
-          mma_commit_mc(empty_bar(s), kBothCtas);
+          const uint32_t a0 = ring + uint32_t(s) * stage_bytes, b0 = a0 + uint32_t(OP_BYTES), empty = empty_bar(s);
           if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
+          ready = kb + 1 < kb1 && mbar_test_wait(full_bar(s), ph);
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i)
+            mma_pair<OP>(d_tmem, step_desc<A_MN>(a0, i), step_desc<B_MN>(b0, i), idesc,
+                         uint32_t((kb - kb0) | i));
+          mma_commit_mc(empty, kBothCtas);
         }
         if (!ok) break;
         mma_commit_mc(tfull_bar(acc), kBothCtas);
