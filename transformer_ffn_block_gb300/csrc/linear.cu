@@ -879,7 +879,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
 }
 // The same product with the operands exchanged: units of 256 output columns by
 // bn rows, a multiple of 32, so that the rows divide evenly into tiles.  A stage
-// takes 113 + 1.55 bn cycles, 288 at least (fitted, as above).  Taken where that
+// takes 117 + 1.55 bn cycles, 288 at least (fitted, as above).  Taken where that
 // estimate is the lower (us, without and with: 333 x 8192 x 2048 with GELU 18.3 /
 // 16.3, 260 x 8192 x 4096 25.8 / 18.9, 700 x 4096 x 4096 23.4 / 19.9, 333 x 4096 x
 // 14336 41.6 / 39.7).
@@ -896,7 +896,7 @@ SwapPlan make_swap_plan(int64_t M, int64_t N, int64_t K, int op) {
     p.bn = int(((M + t - 1) / t + 31) / 32 * 32);
     p.tiles_m = int((M + p.bn - 1) / p.bn);
     p.tiles_n = int((N + 2 * BM - 1) / (2 * BM));
-    const int64_t stage = 113 + 31 * p.bn / 20;
+    const int64_t stage = 117 + 31 * p.bn / 20;
     p.unit = num_kb * (stage > 288 ? stage : 288);
     p.cycles = (int64_t(p.tiles_m) * p.tiles_n + kPlanPairs - 1) / kPlanPairs * p.unit + kFixedCycles + 12 * p.bn;
     if (best.cycles < 0 || p.cycles < best.cycles) best = p;
@@ -961,7 +961,8 @@ cudaError_t product_swapped(const SwapPlan& p, uint16_t* out, uint16_t* z, const
   a.stages = RING_BYTES / (OP_BYTES + p.bn / 2 * ROW_BYTES);
   if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
   a.tiles_m = p.tiles_m;
-  a.tiles_n = a.band_n = p.tiles_n;
+  a.tiles_n = p.tiles_n;
+  a.band_n = band_blocks(p.tiles_n, M, N, K * (OP == OP_BF16 ? 2 : 1));
   a.num_kb = int((K + stage_k(OP) - 1) / stage_k(OP));
   a.num_units = a.split_from = p.tiles_m * p.tiles_n;
   a.splits = 1;
