@@ -272,6 +272,8 @@ def _own(s):
         return b
     if s["dw"] is not None:
         b["dw"].copy_(s["dw"])                                      # what the micro-batches before this one left
+        if b.get("db") is not None:
+            b["db"].zero_()                                         # (they left no bias gradient)
     if op == "linear_backward":
         q.qffn_linear_backward(b["dx"], b["dw"], b["db"], s["dout"], s["z"], s["x"], s["w"], act, rows, cols, inner,
                                s["dw"] is not None, s["ws"])
