@@ -23,11 +23,11 @@
 // per CTA run the epilogue out of one of two TMEM accumulators while the next
 // tile accumulates in the other.  Per SM and byte of K this loads 16 + 16 KB per
 // 128 x 256 outputs; a bf16 MMA takes twice the cycles of an E4M3 one over the
-// same bytes of shared memory, so the operand feed has room to spare.  What binds
-// narrow units is the issue of the MMAs: with the issuing thread chosen by its lane's number
-// 70 cycles each, by elect.sync 24; that and stages of one swizzle row instead
-// of two took 512 x 4096 x 4096 from 19.4 to 16.0 us and 8192 x 4096 x 28672 (gated)
-// from 1066 to 1054.
+// same bytes of shared memory, so the operand feed has room to spare.  Units of
+// fewer columns were bound by the issue of their MMAs, 70 cycles each with the
+// issuing thread chosen by its lane's number, 24 by elect.sync; that and stages of
+// one swizzle row instead of two took 512 x 4096 x 4096 from 19.4 to 16.0 us and
+// the gated 8192 x 4096 x 14336 from 1066 to 1054.
 //
 // Every mbarrier wait is bounded; see gemm_fp8.cu for how a wait that runs out
 // ends the kernel (abort flag, status word, drained copies and MMAs).
@@ -845,7 +845,8 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int op, int max_narrow) {
   p.splits = 1;
   const int64_t whole = int64_t(p.tiles_m) * ((N + BN - 1) / BN);
   const int64_t rest = whole % kPlanPairs;       // (a last round of up to half the pairs' number: half tiles)
-  const int64_t half_rounds = 2 * (whole / kPlanPairs) + (rest == 0 ? 0 : whole > kPlanPairs && 2 * rest <= kPlanPairs ? 1 : 2);
+  const int64_t last = rest == 0 ? 0 : whole > kPlanPairs && 2 * rest <= kPlanPairs ? 1 : 2;
+  const int64_t half_rounds = 2 * (whole / kPlanPairs) + last;
   p.cycles = half_rounds * p.num_kb * 256 + kFixedCycles + 2560;
   if (2 * whole <= kPlanPairs) {
     // Less than half a round of whole tiles: the cheapest of narrower units and
@@ -952,7 +953,8 @@ cudaError_t product_swapped(const SwapPlan& p, uint16_t* out, uint16_t* z, const
                             const void* B, const float* w_scale, const uint16_t* bias, const uint16_t* in, int64_t M,
                             int64_t N, int64_t K, cudaStream_t s, bool late_wait, Idle* after) {
   Maps m;
-  if (!operand_map<OP>(&m.a, B, N, K, B_MN) || !operand_map<OP>(&m.b, A, M, K, false, p.bn / 2)) return cudaErrorInvalidValue;
+  if (!operand_map<OP>(&m.a, B, N, K, B_MN) || !operand_map<OP>(&m.b, A, M, K, false, p.bn / 2))
+    return cudaErrorInvalidValue;
   m.bh = m.b;
   LinArgs a{};
   a.M = int(M);
@@ -1003,7 +1005,8 @@ cudaError_t product(uint16_t* out, uint16_t* z, const void* A, const float* a_sc
       return product_swapped<OP, ACT, B_MN>(sp, out, z, A, a_scale, B, w_scale, bias, in, M, N, K, s, late_wait, after);
   }
   Maps m;
-  if (!operand_map<OP>(&m.a, A, M, K, A_MN) || !operand_map<OP>(&m.b, B, brows, K, B_MN, 128 >> p.narrow)) return cudaErrorInvalidValue;
+  if (!operand_map<OP>(&m.a, A, M, K, A_MN) || !operand_map<OP>(&m.b, B, brows, K, B_MN, 128 >> p.narrow))
+    return cudaErrorInvalidValue;
   m.bh = m.b;
   LinArgs a{};
   a.M = int(M);
