@@ -375,7 +375,114 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr uint32_t kBox2 = 32 * 64;
     constexpr bool kRead = EPI == EPI_LINEAR || EPI == EPI_GATED_BWD;   // may read a bf16 tensor
     int local = 0;
-    for (int un = first_unit(pair, args); un < args.num_units; un = next_unit(un, pair, num_pairs, args), ++local) {
+    constexpr bool kPlain = EPI == EPI_LINEAR && ACT == ACT_NONE && !SWAP;
+    const bool plain = kPlain && args.bias == nullptr && args.z == nullptr;
+    if (plain) {
+      // out = bf16(s * sum (+ in)) alone, the gradients': with few K blocks per unit
+      // the epilogue bounds the kernel, so it takes 64 columns at a time (whole
+      // 128-byte lines), turns them as bf16, and requests what it adds one group
+      // ahead across units.  A lane's accumulator row: chunk c of row r of the box
+      // at c ^ (r & 7); its turned share: chunk ch8 of the rows sub8 + 4 i.
+      const int sub8 = lane >> 3, ch8 = lane & 7;
+      const uint32_t turn8 = box + uint32_t(sub8) * 128u + (uint32_t(ch8 ^ sub8) << 4);
+      const size_t step4 = size_t(4) * size_t(args.N);
+      struct Part {
+        int g0, g1, col;                     // groups of this warp, column of this lane's share of group 0
+        uint32_t rows;                       // bit i: row sub8 + 4 i exists
+        size_t at;                           // element offset of that share's first row
+      };
+      auto part_of = [&](const Unit& u) {
+        Part p;
+        const int row0 = u.mb * (2 * BM) + int(rank) * BM + q * 32;
+        const int groups = (u.half < 0 ? bn : BN / 2) / 64, share = (groups + WG - 1) / WG;
+        p.g0 = wg * share;
+        p.g1 = min(groups, p.g0 + share);
+        p.col = u.nb * bn + (u.half < 0 ? 0 : u.half * 128) + ch8 * 8;
+        p.rows = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p.rows |= (row0 + sub8 + 4 * i < args.M ? 1u : 0u) << i;
+        p.at = size_t(row0 + sub8) * size_t(args.N) + size_t(p.col);
+        return p;
+      };
+      uint4 in8[8];
+      auto request = [&](const Part& p, int g) {
+        const uint32_t live = g < p.g1 && p.col + g * 64 < args.N ? p.rows : 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          in8[i] = make_uint4(0, 0, 0, 0);
+          if ((live >> i) & 1u) in8[i] = ld16_once(args.in + (p.at + size_t(g * 64) + size_t(i) * step4));
+        }
+      };
+      int un = first_unit(pair, args);
+      Part p = part_of(unit_coords<EPI>(un, args));
+      if (args.in != nullptr && un < args.num_units) request(p, p.g0);
+      for (; un < args.num_units; ++local) {
+        const int acc = local & 1;
+        const uint32_t aph = uint32_t(local >> 1) & 1u;
+        const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * BN);
+        const int next = next_unit(un, pair, num_pairs, args);
+        const bool awaited = next < args.num_units && next_unit(next, pair, num_pairs, args) < args.num_units;
+        const Part p_next = part_of(unit_coords<EPI>(next < args.num_units ? next : un, args));
+        if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) break;
+        tc_fence_after();
+        auto loaded = [&](int g) {
+          if (g + 1 >= p.g1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && awaited) mbar_arrive_remote_relaxed(map_to_rank(tempty_bar(acc), 0));
+          }
+        };
+        if (p.g0 >= p.g1) {                  // (a unit with fewer groups than warps)
+          loaded(p.g0);
+          if (args.in != nullptr && next < args.num_units) request(p_next, p_next.g0);
+        }
+        for (int g = p.g0; g < p.g1; ++g) {
+          __syncwarp();                      // the previous group has been read out of the box
+          if (args.in != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sts16((turn8 ^ uint32_t((i & 1) << 6)) + 512u * i, in8[i]);
+            __syncwarp();
+            if (g + 1 < p.g1) request(p, g + 1);
+            else if (next < args.num_units) request(p_next, p_next.g0);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[32];
+            tmem_ld32(tbase + uint32_t(g * 64 + h * 32), v);
+            if (h == 1) loaded(g);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t addr = row32 ^ uint32_t(16 * (4 * h + c));
+              uint64_t z[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                z[j] = f2_pack(__uint_as_float(v[8 * c + 2 * j]), __uint_as_float(v[8 * c + 2 * j + 1]));
+                if (OP == OP_E4M3) z[j] = f2_mul(z[j], f2_dup(scale));
+              }
+              if (args.in != nullptr) {
+                const uint4 d = lds16(addr);
+                const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bf16x2_to_f2(dw[j]));
+              }
+              sts16(addr, pack8(z));
+            }
+          }
+          __syncwarp();
+          const uint32_t live = p.col + g * 64 < args.N ? p.rows : 0u;
+          uint16_t* const dst = args.out + (p.at + size_t(g * 64));
+          uint4 o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = lds16((turn8 ^ uint32_t((i & 1) << 6)) + 512u * i);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if ((live >> i) & 1u) stg16(dst + size_t(i) * step4, o[i]);
+        }
+        un = next;
+        p = p_next;
+      }
+    }
+    for (int un = plain ? args.num_units : first_unit(pair, args); un < args.num_units; un = next_unit(un, pair, num_pairs, args), ++local) {
       const int acc = local & 1;
       const uint32_t aph = uint32_t(local >> 1) & 1u;
       const Unit u = unit_coords<EPI>(un, args);
