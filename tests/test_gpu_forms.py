@@ -76,6 +76,13 @@ def test_linear_residual_in_place_in_each_form(q, M, N, K):  # noqa: F811
     assert torch.equal(out, r) and torch.equal(z, z2)
 
 
+@pytest.mark.parametrize("M,N,K", [(1100, 5008, 208), (803, 1256, 144), (101, 4312, 16), (1472, 10032, 16), (300, 2048, 272),
+                                   (257, 264, 8848)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_linear_residual_alone(q, M, N, K, fp8):  # noqa: F811
+    _check_linear(q, M, N, K, "none", False, True, False, fp8=fp8)
+
+
 @pytest.mark.parametrize("M,C,H", GATED)
 def test_gated_linear_forms(q, M, C, H):  # noqa: F811
     _gated(q, M, C, H, "silu")

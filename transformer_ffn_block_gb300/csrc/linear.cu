@@ -83,6 +83,15 @@ QFFN_DEVI uint32_t pack2(uint64_t v) {
   f2_unpack(v, lo, hi);
   return pack_bf16x2(lo, hi);
 }
+// An epilogue's addend, past the 30 KB that shared memory leaves of L1.
+QFFN_DEVI uint4 ld16_past_l1(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
 QFFN_DEVI uint4 pack8(const uint64_t (&v)[4]) { return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3])); }
 
 __device__ unsigned int g_status;
@@ -380,9 +389,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (plain) {
       // out = bf16(s * sum (+ in)) alone, the gradients': with few K blocks per unit
       // the epilogue bounds the kernel, so it takes 64 columns at a time (whole
-      // 128-byte lines), turns them as bf16, and requests what it adds one group
-      // ahead across units.  A lane's accumulator row: chunk c of row r of the box
-      // at c ^ (r & 7); its turned share: chunk ch8 of the rows sub8 + 4 i.
+      // 128-byte lines), turns them as bf16, and requests what it adds a unit ahead
+      // (weight gradient of one row, 8192 x 4096, us: 32 columns through fp32 22.1, so
+      // 14.7; added to the previous one 41.2 and 32.3).  The box holds 32 rows of 128
+      // bytes, chunk c of row r at c ^ (r & 7); a lane writes its accumulator row and
+      // takes chunk ch8 of the rows sub8 + 4 i.
       const int sub8 = lane >> 3, ch8 = lane & 7;
       const uint32_t turn8 = box + uint32_t(sub8) * 128u + (uint32_t(ch8 ^ sub8) << 4);
       const size_t step4 = size_t(4) * size_t(args.N);
@@ -394,9 +405,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto part_of = [&](const Unit& u) {
         Part p;
         const int row0 = u.mb * (2 * BM) + int(rank) * BM + q * 32;
-        const int groups = (u.half < 0 ? bn : BN / 2) / 64, share = (groups + WG - 1) / WG;
-        p.g0 = wg * share;
-        p.g1 = min(groups, p.g0 + share);
+        p.g0 = wg;
+        p.g1 = (u.half < 0 ? bn : BN / 2) / 64;
         p.col = u.nb * bn + (u.half < 0 ? 0 : u.half * 128) + ch8 * 8;
         p.rows = 0u;
 #pragma unroll
@@ -404,18 +414,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         p.at = size_t(row0 + sub8) * size_t(args.N) + size_t(p.col);
         return p;
       };
-      uint4 in8[8];
-      auto request = [&](const Part& p, int g) {
+      uint4 in8[2][8];
+      auto request = [&](const Part& p, int k, uint4 (&d)[8]) {
+        const int g = p.g0 + k * WG;
         const uint32_t live = g < p.g1 && p.col + g * 64 < args.N ? p.rows : 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          in8[i] = make_uint4(0, 0, 0, 0);
-          if ((live >> i) & 1u) in8[i] = ld16_once(args.in + (p.at + size_t(g * 64) + size_t(i) * step4));
+          d[i] = make_uint4(0, 0, 0, 0);
+          if ((live >> i) & 1u) d[i] = ld16_past_l1(args.in + (p.at + size_t(g * 64) + size_t(i) * step4));
         }
       };
       int un = first_unit(pair, args);
       Part p = part_of(unit_coords<EPI>(un, args));
-      if (args.in != nullptr && un < args.num_units) request(p, p.g0);
+      if (args.in != nullptr) {
+        request(p, 0, in8[0]);
+        request(p, 1, in8[1]);
+      }
       for (; un < args.num_units; ++local) {
         const int acc = local & 1;
         const uint32_t aph = uint32_t(local >> 1) & 1u;
@@ -426,25 +440,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) break;
         tc_fence_after();
         auto loaded = [&](int g) {
-          if (g + 1 >= p.g1) {
+          if (g + WG >= p.g1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0 && awaited) mbar_arrive_remote_relaxed(map_to_rank(tempty_bar(acc), 0));
           }
         };
-        if (p.g0 >= p.g1) {                  // (a unit with fewer groups than warps)
-          loaded(p.g0);
-          if (args.in != nullptr && next < args.num_units) request(p_next, p_next.g0);
-        }
-        for (int g = p.g0; g < p.g1; ++g) {
+        if (p.g0 >= p.g1) loaded(p.g0);      // (a unit with fewer groups than warps)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {        // a warp has two groups at most
+          const int g = p.g0 + k * WG;
           __syncwarp();                      // the previous group has been read out of the box
           if (args.in != nullptr) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sts16((turn8 ^ uint32_t((i & 1) << 6)) + 512u * i, in8[i]);
+            for (int i = 0; i < 8; ++i) sts16((turn8 ^ uint32_t((i & 1) << 6)) + 512u * i, in8[k][i]);
             __syncwarp();
-            if (g + 1 < p.g1) request(p, g + 1);
-            else if (next < args.num_units) request(p_next, p_next.g0);
+            if (next < args.num_units) request(p_next, k, in8[k]);
           }
+          if (g >= p.g1) continue;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t v[32];
@@ -527,7 +540,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             next_in[i] = make_uint4(0, 0, 0, 0);
-            if ((live >> i) & 1u) next_in[i] = ld16_once(args.in + (offset(g) + size_t(i) * step));
+            if ((live >> i) & 1u) next_in[i] = ld16_past_l1(args.in + (offset(g) + size_t(i) * step));
           }
         }
       };
