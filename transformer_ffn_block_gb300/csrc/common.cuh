@@ -185,14 +185,36 @@ QFFN_DEVI float warp_sum(float v) {
 }
 
 // 16-byte global loads / stores.
-// ld16_ro: data that no thread writes during the kernel (weights, gain).
-// ld16_once: plain coherent load (activations that a call may overwrite in
-// place afterwards; a plain load keeps the compiler's aliasing order).
+// ld16_once, ld16_stream (past L1): coherent loads, which stay behind the
+// pdl_wait() in front of them.
+// ld16_settled: a coherent load that the compiler may move past stores and
+// barriers, of data that the kernel does not write; it stays behind pdl_wait()
+// because its pointer comes from behind_wait().
+// ld16_ro, ld16_ro_stream: non-coherent loads, of data that nothing writes while
+// the kernel lives.  Not in a kernel that is launched as a programmatic dependent
+// launch: its life begins while the kernel before it still writes, be it
+// activations, weights or a gain, and the compiler may move ld16_ro up across
+// pdl_wait().
 QFFN_DEVI uint4 ld16_ro(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 QFFN_DEVI uint4 ld16_ro_stream(const void* p) {
   uint4 r;
-  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+QFFN_DEVI uint4 ld16_stream(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+QFFN_DEVI uint4 ld16_settled(const void* p) {
+  uint4 r;
+  asm("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
   return r;
 }
 QFFN_DEVI uint4 ld16_once(const void* p) { return *reinterpret_cast<const uint4*>(p); }
@@ -202,6 +224,12 @@ QFFN_DEVI void stg16(void* p, uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
 // let the next kernel start launching.  Both are no-ops without the launch
 // attribute.
 QFFN_DEVI void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// `p`, known to the compiler only after the pdl_wait() that this follows.
+template <typename T>
+QFFN_DEVI T* behind_wait(T* p) {
+  asm volatile("" : "+l"(p) : : "memory");
+  return p;
+}
 QFFN_DEVI void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 }  // namespace qffn

@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(kThreads, 4) gemv_kernel(const Gemv G, const b
       for (int u = 0; u < kU; ++u) {
         const int cc = t + TPR * u;
         if (cc < nchunk) {
-          a[u] = ld16_ro_stream(r0 + size_t(cc) * 16);
-          if (DUAL) b[u] = ld16_ro_stream(r1 + size_t(cc) * 16);
+          a[u] = ld16_stream(r0 + size_t(cc) * 16);
+          if (DUAL) b[u] = ld16_stream(r1 + size_t(cc) * 16);
         }
       }
       have = true;
@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(kThreads, 4) gemv_kernel(const Gemv G, const b
           for (int u = 0; u < kU; ++u) {
             const int cc = c + TPR * u;
             if (cc < nchunk) {
-              a[u] = ld16_ro_stream(r0 + size_t(cc) * 16);
-              if (DUAL) b[u] = ld16_ro_stream(r1 + size_t(cc) * 16);
+              a[u] = ld16_stream(r0 + size_t(cc) * 16);
+              if (DUAL) b[u] = ld16_stream(r1 + size_t(cc) * 16);
             }
           }
         }

@@ -195,7 +195,7 @@ QFFN_DEVI void finish(const FewArgs& args, const float* sums, const float* recv,
   if (n >= args.N) return;
   const float scale = OP == OP_E4M3 ? args.a_scale[0] * args.w_scale[0] : 1.0f;
   uint64_t bias[4] = {0ull, 0ull, 0ull, 0ull};
-  if (EPI == EPI_LINEAR && args.bias != nullptr) unpack8(ld16_ro(args.bias + n), bias);
+  if (EPI == EPI_LINEAR && args.bias != nullptr) unpack8(ld16_once(args.bias + n), bias);
   const int m0 = mt * args.bn + part * share;
   const int rows = min(share, args.M - m0);
 #pragma unroll 2

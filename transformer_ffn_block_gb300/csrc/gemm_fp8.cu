@@ -481,9 +481,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // columns per load, about 1 us off every launch of this form.
 #pragma unroll 1
         for (int c0 = 0; c0 < ncols; c0 += 32) {
+          const int col = cbase + c0;
+          uint4 bias[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            bias[k] = args.bias != nullptr && col + 8 * k < args.N ? ld16_once(args.bias + col + 8 * k)
+                                                                  : make_uint4(0, 0, 0, 0);
           uint32_t v[32];
           tmem_ld32(tbase + uint32_t(c0), v);
-          const int col = cbase + c0;
           uint8_t* sbox = sStaging + (q * 2 + sbuf) * STAGE_BOX_BYTES;
           if ((c0 & 63) == 0) {
             if (lane == 0) bulk_wait_read_1();   // the store that last read this box is done
@@ -494,8 +499,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int chunk = ((c0 & 63) >> 3) + k;
             uint32_t p[4];
             if (args.bias != nullptr) {
-              const uint4 b4 = col + 8 * k < args.N ? ld16_ro(args.bias + col + 8 * k) : make_uint4(0, 0, 0, 0);
-              const uint32_t bw[4] = {b4.x, b4.y, b4.z, b4.w};
+              const uint32_t bw[4] = {bias[k].x, bias[k].y, bias[k].z, bias[k].w};
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 p[j] = pack_bf16x2(__uint_as_float(v[8 * k + 2 * j]) * scale + bf16_lo(bw[j]),
@@ -543,12 +547,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int c8 = 0; c8 < 8; ++c8) {
             const int c0 = g * 64 + c8 * 8;
             const int col = nb * BN + c0;
+            const uint4 b4 = (args.bias != nullptr && col < args.N) ? ld16_once(args.bias + col)
+                                                                     : make_uint4(0, 0, 0, 0);
             uint32_t v[8];
             tmem_ld8(tbase + uint32_t(c0), v);
             const uint32_t off = uint32_t(lane) * 128u + (uint32_t(c8 ^ (lane & 7)) << 4);
             const uint4 o4 = *reinterpret_cast<const uint4*>(box + off);
-            const uint4 b4 = (args.bias != nullptr && col < args.N) ? ld16_ro(args.bias + col)
-                                                                     : make_uint4(0, 0, 0, 0);
             const uint32_t bw[4] = {b4.x, b4.y, b4.z, b4.w}, ow[4] = {o4.x, o4.y, o4.z, o4.w};
             uint32_t p[4];
 #pragma unroll

@@ -83,15 +83,6 @@ QFFN_DEVI uint32_t pack2(uint64_t v) {
   f2_unpack(v, lo, hi);
   return pack_bf16x2(lo, hi);
 }
-// An epilogue's addend, past the 30 KB that shared memory leaves of L1.
-QFFN_DEVI uint4 ld16_past_l1(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p)
-               : "memory");
-  return r;
-}
 QFFN_DEVI uint4 pack8(const uint64_t (&v)[4]) { return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3])); }
 
 __device__ unsigned int g_status;
@@ -256,6 +247,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   if (!args.late_wait) pdl_wait();   // nothing in global memory is touched before the preceding kernel is done
+  const uint16_t* const bias_row = behind_wait(args.bias);
   pdl_trigger();
 
   // K blocks of a unit
@@ -421,7 +413,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           d[i] = make_uint4(0, 0, 0, 0);
-          if ((live >> i) & 1u) d[i] = ld16_past_l1(args.in + (p.at + size_t(g * 64) + size_t(i) * step4));
+          if ((live >> i) & 1u) d[i] = ld16_stream(args.in + (p.at + size_t(g * 64) + size_t(i) * step4));
         }
       };
       int un = first_unit(pair, args);
@@ -535,12 +527,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto request = [&](int g) {
         const uint32_t live = g < g1 ? live_rows(g) : 0u;
         if (EPI == EPI_LINEAR && args.bias != nullptr)
-          next_bias = live != 0u ? ld16_ro(args.bias + col(g)) : make_uint4(0, 0, 0, 0);
+          next_bias = live != 0u ? ld16_settled(bias_row + col(g)) : make_uint4(0, 0, 0, 0);
         if (kRead && args.in != nullptr) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             next_in[i] = make_uint4(0, 0, 0, 0);
-            if ((live >> i) & 1u) next_in[i] = ld16_past_l1(args.in + (offset(g) + size_t(i) * step));
+            if ((live >> i) & 1u) next_in[i] = ld16_stream(args.in + (offset(g) + size_t(i) * step));
           }
         }
       };
@@ -770,7 +762,7 @@ __global__ void __launch_bounds__(256) join_kernel(uint16_t* out, uint16_t* out2
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[j] *= scale;
       if (bias != nullptr) {
-        unpack(ld16_ro(bias + col), t);
+        unpack(ld16_once(bias + col), t);
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[j] += t[j];
       }
@@ -791,7 +783,7 @@ __global__ void __launch_bounds__(256) join_kernel(uint16_t* out, uint16_t* out2
         for (int j = 0; j < 8; ++j) z[j] = act_f32<ACT>(z[j]) * up[j];
         stg16(out + row * N + col, pack(z));
       } else {
-        unpack(ld16_ro(in + row * N + col), t);
+        unpack(ld16_once(in + row * N + col), t);
         float du[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(BLOCK) layernorm_kernel(const LnFwd a) {
   const int nchunk = a.C >> 3;
   const size_t base = live ? size_t(row) * size_t(a.C) : 0;
   pdl_wait();
+  const uint16_t *gain = behind_wait(a.gain), *shift = behind_wait(a.shift);
   pdl_trigger();
   uint4 rv[V];
   uint64_t acc = 0ull;
@@ -164,8 +165,8 @@ __global__ void __launch_bounds__(BLOCK) layernorm_kernel(const LnFwd a) {
     const int c = t + i * T;
     if (live && c < nchunk) {
       F8 s{{0ull, 0ull, 0ull, 0ull}};
-      if (a.shift != nullptr) s = unpack8(ld16_ro(a.shift + size_t(c) * 8));
-      const uint4 o = normed8(unpack8(rv[i]), neg_mean, f2_dup(rstd), unpack8(ld16_ro(a.gain + size_t(c) * 8)), s);
+      if (shift != nullptr) s = unpack8(ld16_settled(shift + size_t(c) * 8));
+      const uint4 o = normed8(unpack8(rv[i]), neg_mean, f2_dup(rstd), unpack8(ld16_settled(gain + size_t(c) * 8)), s);
       stg16(a.y + base + size_t(c) * 8, o);
       if (a.stats != nullptr) amax = absmax8(amax, o);
     }
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(256) norm_backward_warp_kernel(const NormBwd a
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = t + i * 32;
-    gv[i] = c < nchunk ? ld16_ro(a.gain + size_t(c) * 8) : zero;
+    gv[i] = c < nchunk ? ld16_once(a.gain + size_t(c) * 8) : zero;
 #pragma unroll
     for (int j = 0; j < 4; ++j) dg[i][j] = ds[i][j] = 0ull;
   }
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const NormBwd a) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = t + i * T;
-    gv[i] = c < nchunk ? ld16_ro(a.gain + size_t(c) * 8) : make_uint4(0, 0, 0, 0);
+    gv[i] = c < nchunk ? ld16_once(a.gain + size_t(c) * 8) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) dg[i][j] = ds[i][j] = 0ull;
   }
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(T) norm_backward_short_kernel(const NormBwd a,
       if (c < nchunk) {
         dv[i] = ld16_once(a.dy + base + size_t(c) * 8);
         rv[i] = ld16_once(a.r + base + size_t(c) * 8);
-        gv[i] = ld16_ro(a.gain + size_t(c) * 8);
+        gv[i] = ld16_once(a.gain + size_t(c) * 8);
         if (a.dres != nullptr) ev[i] = ld16_once(a.dres + base + size_t(c) * 8);
       }
     }

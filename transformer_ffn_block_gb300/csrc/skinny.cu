@@ -111,15 +111,15 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 ? 32 : 16) / WARPS) skinn
     for (int u = 0; u < kU; ++u) {
       const int64_t k = k0 + u * 64;
       const bool in = k + t * 16 < a.row_bytes;      // the row's length is a multiple of 16 bytes
-      va[u] = in ? ld16_ro_stream(wa + k) : zero;
-      vb[u] = in ? ld16_ro_stream(wb + k) : zero;
+      va[u] = in ? ld16_stream(wa + k) : zero;
+      vb[u] = in ? ld16_stream(wb + k) : zero;
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int64_t k = k0 + u * 64;
       const bool in = k + t * 16 < a.row_bytes;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) vx[n][u] = in && xl[n] ? ld16_ro(xp[n] + k) : zero;
+      for (int n = 0; n < NT; ++n) vx[n][u] = in && xl[n] ? ld16_once(xp[n] + k) : zero;
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u)
