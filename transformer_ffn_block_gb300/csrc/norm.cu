@@ -181,15 +181,23 @@ __global__ void __launch_bounds__(BLOCK) layernorm_kernel(const LnFwd a) {
 // its partial row of dgain (and dshift).  column_sum_kernel adds the blocks'
 // partial rows in a fixed order: no atomics, the same bits each run.
 
+// xhat of a pair.  The mean is subtracted first: the difference is exact or nearly
+// so where the row lies far from zero, while rs x - rs mean would keep the rounding
+// of rs mean, the same in every element of the row, in the sums.
+template <bool CENTRED>
+QFFN_DEVI uint64_t norm_hat(uint64_t x, uint64_t rs, uint64_t neg_mu) {
+  return f2_mul(CENTRED ? f2_add(x, neg_mu) : x, rs);
+}
+
 // dx of one 16-byte chunk: e + rs w + k1 xhat + k2 with k1 = -rs c1, k2 = -rs c2.
 template <bool CENTRED>
-QFFN_DEVI uint4 norm_dx8(uint4 dv, uint4 rv, uint4 gv, uint4 ev, uint64_t rs, uint64_t neg_mu_rs, uint64_t k1,
+QFFN_DEVI uint4 norm_dx8(uint4 dv, uint4 rv, uint4 gv, uint4 ev, uint64_t rs, uint64_t neg_mu, uint64_t k1,
                          uint64_t k2) {
   const F8 d = unpack8(dv), x = unpack8(rv), g = unpack8(gv);
   F8 e = unpack8(ev);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint64_t xh = CENTRED ? f2_fma(x.p[j], rs, neg_mu_rs) : f2_mul(x.p[j], rs);
+    const uint64_t xh = norm_hat<CENTRED>(x.p[j], rs, neg_mu);
     // the sum of the three gradient terms first, dres last
     uint64_t v = CENTRED ? f2_fma(xh, k1, k2) : f2_mul(xh, k1);
     v = f2_fma(f2_mul(d.p[j], g.p[j]), rs, v);
@@ -199,12 +207,12 @@ QFFN_DEVI uint4 norm_dx8(uint4 dv, uint4 rv, uint4 gv, uint4 ev, uint64_t rs, ui
 }
 // The chunk's terms of the row sums (s1 += w xhat, s2 += w) and column sums.
 template <bool CENTRED>
-QFFN_DEVI void norm_sums8(uint4 dv, uint4 rv, uint4 gv, uint64_t rs, uint64_t neg_mu_rs, uint64_t& s1, uint64_t& s2,
+QFFN_DEVI void norm_sums8(uint4 dv, uint4 rv, uint4 gv, uint64_t rs, uint64_t neg_mu, uint64_t& s1, uint64_t& s2,
                           uint64_t (&dg)[4], uint64_t (&ds)[4]) {
   const F8 d = unpack8(dv), x = unpack8(rv), g = unpack8(gv);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint64_t xh = CENTRED ? f2_fma(x.p[j], rs, neg_mu_rs) : f2_mul(x.p[j], rs);
+    const uint64_t xh = norm_hat<CENTRED>(x.p[j], rs, neg_mu);
     const uint64_t w = f2_mul(d.p[j], g.p[j]);
     s1 = f2_fma(w, xh, s1);
     if (CENTRED) s2 = f2_add(s2, w);
@@ -263,7 +271,7 @@ __global__ void __launch_bounds__(256) norm_backward_warp_kernel(const NormBwd a
       }
     }
     const float mu = CENTRED ? a.mean[row] : 0.0f, rs = a.rstd[row];
-    const uint64_t rs2 = f2_dup(rs), nm2 = f2_dup(-mu * rs);
+    const uint64_t rs2 = f2_dup(rs), nm2 = f2_dup(-mu);
     uint64_t p1 = 0ull, p2 = 0ull;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -370,7 +378,7 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const NormBwd a) {
     // a wait that runs out raises the abort flag, which all threads see after the barrier below
     mbar_wait_bounded(smem_u32(&bars[s]), parity, abort_flag, &g_status, true, kWaitLimitNs);
     const uint8_t* st = ring + size_t(s) * stage_bytes;
-    const uint64_t rs2 = f2_dup(rs), nm2 = f2_dup(-mu * rs);
+    const uint64_t rs2 = f2_dup(rs), nm2 = f2_dup(-mu);
     uint64_t p1 = 0ull, p2 = 0ull;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -465,7 +473,7 @@ __global__ void __launch_bounds__(T) norm_backward_short_kernel(const NormBwd a,
         if (a.dres != nullptr) ev[i] = ld16_once(a.dres + base + size_t(c) * 8);
       }
     }
-    const uint64_t rs2 = f2_dup(rs), nm2 = f2_dup(-mu * rs);
+    const uint64_t rs2 = f2_dup(rs), nm2 = f2_dup(-mu);
     uint64_t p1 = 0ull, p2 = 0ull, dg[4] = {0ull, 0ull, 0ull, 0ull}, ds[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
     for (int i = 0; i < V; ++i) norm_sums8<CENTRED>(dv[i], rv[i], gv[i], rs2, nm2, p1, p2, dg, ds);
@@ -506,7 +514,7 @@ __global__ void __launch_bounds__(T) norm_backward_short_kernel(const NormBwd a,
 #pragma unroll
       for (int k = 0; k < kFlight; ++k)
         if (row0 + k * kRows < a.N)
-          norm_sums8<CENTRED>(dv[k], rv[k], zero, f2_dup(rs[k]), f2_dup(-mu[k] * rs[k]), unused1, unused2, dg, ds);
+          norm_sums8<CENTRED>(dv[k], rv[k], zero, f2_dup(rs[k]), f2_dup(-mu[k]), unused1, unused2, dg, ds);
     }
   }
   // the four rows of a warp, then the warps in order
@@ -625,7 +633,7 @@ cudaError_t norm_backward(const NormBwd& a, int blocks, cudaStream_t s) {
 }
 
 // Up to this many rows one launch that reads dy and r twice beats two (layer norm,
-// us, one launch against two: 77 x 2048 2.1 / 5.2, about 512 x 4096 7.8 / 10.5,
+// us, one launch against two: 77 x 2048 2.1 / 5.2, about 512 x 4096 8.0 / 10.5,
 // 512 x 1024 7.0 / 6.7, 512 x 256 4.9 / 3.9).
 int64_t short_rows(int C) { return C <= 512 ? 256 : 512; }
 
