@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 
 from ._build import LIB as LIB_PATH
 from ._build import build
@@ -150,24 +151,25 @@ def _buf(fn, device, name, t, size, n):
 
 _torch = None                # imported on first use: the raw-address calls do not need it
 _get_device = _get_stream = None
+_load_lock = threading.Lock()
 
 
 def _load_torch():
     global _torch, _get_device, _get_stream
     import torch
-    _torch = torch
-    if torch.cuda.is_available():
-        torch.cuda.init()
-        _get_device, _get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    with _load_lock:         # first calls from several threads: the others wait
+        if _torch is not None:
+            return
+        if torch.cuda.is_available():
+            torch.cuda.init()
+            _get_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        _torch = torch       # last: with it set, the two above are what they stay
 
 
 def _current_device():
-    if _get_device is not None:
-        return _get_device()
     if _torch is None:
         _load_torch()
-        return _current_device()
-    return -2                # (-1 is a CPU tensor's)
+    return _get_device() if _get_device is not None else -2      # (-1 is a CPU tensor's)
 
 
 def _workspace(fn, device, workspace, workspace_bytes):
