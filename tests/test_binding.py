@@ -1,9 +1,13 @@
 """The Python binding's own host code: what needs no GPU."""
+import subprocess
+import sys
 import threading
 import time
 
 import pytest
 import torch
+
+from conftest import ROOT
 
 from test_abi import A, lib  # noqa: F401  (lib: the module's build-and-load fixture)
 
@@ -39,3 +43,27 @@ def test_first_calls_from_many_threads(fresh, monkeypatch):
     for t in threads:
         t.join()
     assert seen == [3] * 8
+
+
+RAW = """
+import sys
+import transformer_ffn_block_gb300 as q
+A = 4096
+for call in (lambda: q.qffn_linear(A, None, A, A, None, None, 9, 4, 32, 64, A, 4096, stream=0),
+             lambda: q.qffn_gated_linear(A, A, A, 9, 4, 32, 64, A, 4096, stream=0),
+             lambda: q.qffn_layernorm_absmax(None, A, A, A, None, None, A, A, None, -1.0, 4, 64, stream=0),
+             lambda: q.qffn_rmsnorm_backward(A, A, None, A, None, A, A, A, -4, 64, False, A, 4096, stream=0)):
+    try:
+        call()
+    except q.QffnError as e:
+        assert e.status == 1
+    else:
+        raise SystemExit("not refused")
+assert "torch" not in sys.modules, "torch was imported"
+"""
+
+
+def test_raw_addresses_need_no_torch(lib):  # noqa: F811
+    """Calls with bare addresses and a stream reach the library without importing torch."""
+    r = subprocess.run([sys.executable, "-c", RAW], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr

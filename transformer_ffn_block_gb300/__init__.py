@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 import threading
 
 from ._build import LIB as LIB_PATH
@@ -149,7 +150,7 @@ def _buf(fn, device, name, t, size, n):
                            f"{tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-_torch = None                # imported on first use: the raw-address calls do not need it
+_torch = None                # imported on first use: calls with bare addresses and a stream do not need it
 _get_device = _get_stream = None
 _load_lock = threading.Lock()
 
@@ -168,6 +169,8 @@ def _load_torch():
 
 def _current_device():
     if _torch is None:
+        if "torch" not in sys.modules:       # then no argument is a tensor
+            return -2
         _load_torch()
     return _get_device() if _get_device is not None else -2      # (-1 is a CPU tensor's)
 
@@ -185,8 +188,9 @@ def _workspace(fn, device, workspace, workspace_bytes):
 def _stream(stream):
     if stream is None:
         # torch.cuda.current_stream().cuda_stream without the Stream object (2.8 us -> 0.1 us a call)
-        device = _current_device()
-        return _get_stream(device) if _get_stream is not None else _torch.cuda.current_stream().cuda_stream
+        if _torch is None:
+            _load_torch()
+        return _get_stream(_get_device()) if _get_device is not None else _torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
