@@ -4,8 +4,8 @@ Argument marshalling only: each function here has the name of a C entry
 point of ``include/qffn.h``, turns torch tensors (or raw integer device
 addresses) into pointers, passes the current torch CUDA stream unless one is
 given, and raises ``QffnError`` on a non-zero status.  The norm, linear and
-gated-linear functions also refuse tensors that are too small, not contiguous
-or not on the current device.  Every step of the
+gated-linear functions also refuse tensors that are too small, of another
+type, not contiguous or not on the current device.  Every step of the
 block runs in the CUDA kernels of ``libqffn.so``; there is no fallback.  If
 the library is missing the import fails (run ``build()`` first).
 """
@@ -137,16 +137,21 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _buf(fn, device, name, t, size, n):
-    """_ptr of a tensor after the checks that a bare address cannot have: ``n`` elements of
-    ``size`` bytes at least, contiguous, on the current device."""
+_BF16, _F32, _E4M3 = set(), set(), set()      # the tensor types that hold each (filled with torch)
+
+
+def _buf(fn, device, name, t, types, n):
+    """_ptr of a tensor after the checks that a bare address cannot have: ``n`` elements at least of one
+    of ``types``, contiguous, on the current device.  bf16 may come as int16 or uint16 bits and E4M3
+    as uint8 codes, as in the other functions."""
     if t is None:
         return None
     if t.__class__ is int:
         return t
-    if t.is_contiguous() and t.element_size() == size and t.numel() >= n and (t.get_device() == device or n <= 0):
+    if t.is_contiguous() and t.dtype in types and t.numel() >= n and (t.get_device() == device or n <= 0):
         return t.data_ptr()
-    raise QffnError(fn, 1, f"{name}: expected {n} contiguous elements of {size} bytes on cuda:{device}, got "
+    kind = "bf16" if types is _BF16 else "fp32" if types is _F32 else "E4M3"
+    raise QffnError(fn, 1, f"{name}: expected {n} contiguous {kind} elements on cuda:{device}, got "
                            f"{tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
@@ -161,6 +166,9 @@ def _load_torch():
     with _load_lock:         # first calls from several threads: the others wait
         if _torch is not None:
             return
+        _BF16.update((torch.bfloat16, torch.int16, torch.uint16))
+        _F32.add(torch.float32)
+        _E4M3.update((torch.float8_e4m3fn, torch.uint8))
         if torch.cuda.is_available():
             torch.cuda.init()
             _get_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
@@ -168,6 +176,8 @@ def _load_torch():
 
 
 def _current_device():
+    if _get_device is not None:
+        return _get_device()
     if _torch is None:
         if "torch" not in sys.modules:       # then no argument is a tensor
             return -2
@@ -178,17 +188,19 @@ def _current_device():
 def _workspace(fn, device, workspace, workspace_bytes):
     if workspace is None or workspace.__class__ is int:
         return workspace, int(workspace_bytes or 0)
-    size = workspace.element_size()
-    nbytes = workspace.numel() * size
+    nbytes = workspace.numel() * workspace.element_size()
+    if not (workspace.is_contiguous() and nbytes > 0 and workspace.get_device() == device):
+        raise QffnError(fn, 1, f"workspace: expected contiguous memory on cuda:{device}, got "
+                               f"{tuple(workspace.shape)} {workspace.dtype} on {workspace.device}")
     if workspace_bytes is not None:
         nbytes = min(nbytes, int(workspace_bytes))
-    return _buf(fn, device, "workspace", workspace, size, 1), nbytes
+    return workspace.data_ptr(), nbytes
 
 
 def _stream(stream):
     if stream is None:
         # torch.cuda.current_stream().cuda_stream without the Stream object (2.8 us -> 0.1 us a call)
-        if _torch is None:
+        if _get_device is None:
             _load_torch()
         return _get_stream(_get_device()) if _get_device is not None else _torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
@@ -368,10 +380,10 @@ def qffn_ffn_backward(d_ln2, dw1, dw2, stats_dout, stats_dgu, dout, yq, y_scale,
 def qffn_layernorm_absmax(res_out, y, mean, rstd, stats, res_in, x, gain, shift, eps, N, C, stream=None):
     fn, d, n = "qffn_layernorm_absmax", _current_device(), N * C
     _check(fn, lib.qffn_layernorm_absmax(
-        _buf(fn, d, "res_out", res_out, 2, n), _buf(fn, d, "y", y, 2, n), _buf(fn, d, "mean", mean, 4, N),
-        _buf(fn, d, "rstd", rstd, 4, N), _buf(fn, d, "stats", stats, 4, 1), _buf(fn, d, "res_in", res_in, 2, n),
-        _buf(fn, d, "x", x, 2, n), _buf(fn, d, "gain", gain, 2, C), _buf(fn, d, "shift", shift, 2, C),
-        eps, N, C, _stream(stream)))
+        _buf(fn, d, "res_out", res_out, _BF16, n), _buf(fn, d, "y", y, _BF16, n), _buf(fn, d, "mean", mean, _F32, N),
+        _buf(fn, d, "rstd", rstd, _F32, N), _buf(fn, d, "stats", stats, _F32, 1),
+        _buf(fn, d, "res_in", res_in, _BF16, n), _buf(fn, d, "x", x, _BF16, n),
+        _buf(fn, d, "gain", gain, _BF16, C), _buf(fn, d, "shift", shift, _BF16, C), eps, N, C, _stream(stream)))
 
 
 def qffn_norm_backward_workspace_size(N, C) -> int:
@@ -383,10 +395,10 @@ def qffn_layernorm_backward(dx, dgain, dshift, stats, dy, dres, r, mean, rstd, g
     fn, d, n = "qffn_layernorm_backward", _current_device(), N * C
     ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
     _check(fn, lib.qffn_layernorm_backward(
-        _buf(fn, d, "dx", dx, 2, n), _buf(fn, d, "dgain", dgain, 4, C), _buf(fn, d, "dshift", dshift, 4, C),
-        _buf(fn, d, "stats", stats, 4, 1), _buf(fn, d, "dy", dy, 2, n), _buf(fn, d, "dres", dres, 2, n),
-        _buf(fn, d, "r", r, 2, n), _buf(fn, d, "mean", mean, 4, N), _buf(fn, d, "rstd", rstd, 4, N),
-        _buf(fn, d, "gain", gain, 2, C), N, C, bool(accumulate), ws, nbytes, _stream(stream)))
+        _buf(fn, d, "dx", dx, _BF16, n), _buf(fn, d, "dgain", dgain, _F32, C), _buf(fn, d, "dshift", dshift, _F32, C),
+        _buf(fn, d, "stats", stats, _F32, 1), _buf(fn, d, "dy", dy, _BF16, n), _buf(fn, d, "dres", dres, _BF16, n),
+        _buf(fn, d, "r", r, _BF16, n), _buf(fn, d, "mean", mean, _F32, N), _buf(fn, d, "rstd", rstd, _F32, N),
+        _buf(fn, d, "gain", gain, _BF16, C), N, C, bool(accumulate), ws, nbytes, _stream(stream)))
 
 
 def qffn_rmsnorm_backward(dx, dgain, stats, dy, dres, r, rstd, gain, N, C, accumulate, workspace,
@@ -394,9 +406,9 @@ def qffn_rmsnorm_backward(dx, dgain, stats, dy, dres, r, rstd, gain, N, C, accum
     fn, d, n = "qffn_rmsnorm_backward", _current_device(), N * C
     ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
     _check(fn, lib.qffn_rmsnorm_backward(
-        _buf(fn, d, "dx", dx, 2, n), _buf(fn, d, "dgain", dgain, 4, C), _buf(fn, d, "stats", stats, 4, 1),
-        _buf(fn, d, "dy", dy, 2, n), _buf(fn, d, "dres", dres, 2, n), _buf(fn, d, "r", r, 2, n),
-        _buf(fn, d, "rstd", rstd, 4, N), _buf(fn, d, "gain", gain, 2, C), N, C, bool(accumulate), ws, nbytes,
+        _buf(fn, d, "dx", dx, _BF16, n), _buf(fn, d, "dgain", dgain, _F32, C), _buf(fn, d, "stats", stats, _F32, 1),
+        _buf(fn, d, "dy", dy, _BF16, n), _buf(fn, d, "dres", dres, _BF16, n), _buf(fn, d, "r", r, _BF16, n),
+        _buf(fn, d, "rstd", rstd, _F32, N), _buf(fn, d, "gain", gain, _BF16, C), N, C, bool(accumulate), ws, nbytes,
         _stream(stream)))
 
 
@@ -408,9 +420,9 @@ def qffn_linear(out, z, x, w, bias, residual, act, M, N, K, workspace, workspace
     fn, d = "qffn_linear", _current_device()
     ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
     _check(fn, lib.qffn_linear(
-        _buf(fn, d, "out", out, 2, M * N), _buf(fn, d, "z", z, 2, M * N), _buf(fn, d, "x", x, 2, M * K),
-        _buf(fn, d, "w", w, 2, N * K), _buf(fn, d, "bias", bias, 2, N), _buf(fn, d, "residual", residual, 2, M * N),
-        act, M, N, K, ws, nbytes, _stream(stream)))
+        _buf(fn, d, "out", out, _BF16, M * N), _buf(fn, d, "z", z, _BF16, M * N), _buf(fn, d, "x", x, _BF16, M * K),
+        _buf(fn, d, "w", w, _BF16, N * K), _buf(fn, d, "bias", bias, _BF16, N),
+        _buf(fn, d, "residual", residual, _BF16, M * N), act, M, N, K, ws, nbytes, _stream(stream)))
 
 
 def qffn_linear_fp8_workspace_size(M, N, K) -> int:
@@ -422,10 +434,10 @@ def qffn_linear_fp8(out, z, x, x_scale, w, w_scale, bias, residual, act, M, N, K
     fn, d = "qffn_linear_fp8", _current_device()
     ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
     _check(fn, lib.qffn_linear_fp8(
-        _buf(fn, d, "out", out, 2, M * N), _buf(fn, d, "z", z, 2, M * N), _buf(fn, d, "x", x, 1, M * K),
-        _buf(fn, d, "x_scale", x_scale, 4, 1), _buf(fn, d, "w", w, 1, N * K), _buf(fn, d, "w_scale", w_scale, 4, 1),
-        _buf(fn, d, "bias", bias, 2, N), _buf(fn, d, "residual", residual, 2, M * N), act, M, N, K, ws, nbytes,
-        _stream(stream)))
+        _buf(fn, d, "out", out, _BF16, M * N), _buf(fn, d, "z", z, _BF16, M * N), _buf(fn, d, "x", x, _E4M3, M * K),
+        _buf(fn, d, "x_scale", x_scale, _F32, 1), _buf(fn, d, "w", w, _E4M3, N * K),
+        _buf(fn, d, "w_scale", w_scale, _F32, 1), _buf(fn, d, "bias", bias, _BF16, N),
+        _buf(fn, d, "residual", residual, _BF16, M * N), act, M, N, K, ws, nbytes, _stream(stream)))
 
 
 def qffn_linear_backward_workspace_size(M, N, K) -> int:
@@ -437,9 +449,9 @@ def qffn_linear_backward(dx, dw, dbias, dout, z, x, w, act, M, N, K, accumulate,
     fn, d = "qffn_linear_backward", _current_device()
     ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
     _check(fn, lib.qffn_linear_backward(
-        _buf(fn, d, "dx", dx, 2, M * K), _buf(fn, d, "dw", dw, 2, N * K), _buf(fn, d, "dbias", dbias, 4, N),
-        _buf(fn, d, "dout", dout, 2, M * N), _buf(fn, d, "z", z, 2, M * N), _buf(fn, d, "x", x, 2, M * K),
-        _buf(fn, d, "w", w, 2, N * K), act, M, N, K, bool(accumulate), ws, nbytes, _stream(stream)))
+        _buf(fn, d, "dx", dx, _BF16, M * K), _buf(fn, d, "dw", dw, _BF16, N * K), _buf(fn, d, "dbias", dbias, _F32, N),
+        _buf(fn, d, "dout", dout, _BF16, M * N), _buf(fn, d, "z", z, _BF16, M * N), _buf(fn, d, "x", x, _BF16, M * K),
+        _buf(fn, d, "w", w, _BF16, N * K), act, M, N, K, bool(accumulate), ws, nbytes, _stream(stream)))
 
 
 def qffn_gated_linear_workspace_size(N, C, H) -> int:
@@ -450,8 +462,8 @@ def qffn_gated_linear(h, x, w1, act, N, C, H, workspace, workspace_bytes=None, s
     fn, d = "qffn_gated_linear", _current_device()
     ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
     _check(fn, lib.qffn_gated_linear(
-        _buf(fn, d, "h", h, 2, N * H), _buf(fn, d, "x", x, 2, N * C), _buf(fn, d, "w1", w1, 2, 2 * H * C), act, N, C, H,
-        ws, nbytes, _stream(stream)))
+        _buf(fn, d, "h", h, _BF16, N * H), _buf(fn, d, "x", x, _BF16, N * C), _buf(fn, d, "w1", w1, _BF16, 2 * H * C),
+        act, N, C, H, ws, nbytes, _stream(stream)))
 
 
 def qffn_gated_linear_backward_workspace_size(N, C, H) -> int:
@@ -463,9 +475,9 @@ def qffn_gated_linear_backward(dx, dw1, dh, x, w1, act, N, C, H, accumulate, wor
     fn, d = "qffn_gated_linear_backward", _current_device()
     ws, nbytes = _workspace(fn, d, workspace, workspace_bytes)
     _check(fn, lib.qffn_gated_linear_backward(
-        _buf(fn, d, "dx", dx, 2, N * C), _buf(fn, d, "dw1", dw1, 2, 2 * H * C), _buf(fn, d, "dh", dh, 2, N * H),
-        _buf(fn, d, "x", x, 2, N * C), _buf(fn, d, "w1", w1, 2, 2 * H * C), act, N, C, H, bool(accumulate), ws, nbytes,
-        _stream(stream)))
+        _buf(fn, d, "dx", dx, _BF16, N * C), _buf(fn, d, "dw1", dw1, _BF16, 2 * H * C),
+        _buf(fn, d, "dh", dh, _BF16, N * H), _buf(fn, d, "x", x, _BF16, N * C), _buf(fn, d, "w1", w1, _BF16, 2 * H * C),
+        act, N, C, H, bool(accumulate), ws, nbytes, _stream(stream)))
 
 
 def qffn_gemv_dual(g, u, x, w_gate, s_gate, w_up, s_up, H, C, stream=None):
