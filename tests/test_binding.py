@@ -137,3 +137,18 @@ def test_types_of_the_right_width_are_refused(on_cpu):
                     f(*args[:i], torch.zeros(a.shape, dtype=torch.uint8).to(d) if d.itemsize == 1 else a.view(d),
                       *args[i + 1:], stream=0)
                 assert e.value.status == 1 and on_cpu.lib.calls == n and str(d) in str(e.value), (f.__name__, i, d)
+
+
+def test_workspace_bytes_limit_the_workspace(on_cpu, monkeypatch):
+    """workspace_bytes counts where it is less than the tensor holds, never as more; a negative one is refused."""
+    seen = []
+    monkeypatch.setattr(on_cpu.lib, "qffn_gated_linear", lambda *a: seen.append(a[8]) or 0)
+    f, args = next(c for c in _calls(on_cpu) if c[0].__name__ == "qffn_gated_linear")
+    size = args[-1].numel()
+    for given, counted in ((None, size), (0, 0), (100, 100), (size, size), (size + 1, size)):
+        f(*args, workspace_bytes=given, stream=0)
+        assert seen[-1] == counted
+    for ws in (args[-1], A):
+        with pytest.raises(on_cpu.QffnError) as e:
+            f(*args[:-1], ws, workspace_bytes=-1, stream=0)
+        assert e.value.status == 1 and len(seen) == 5

@@ -186,6 +186,8 @@ def _current_device():
 
 
 def _workspace(fn, device, workspace, workspace_bytes):
+    if workspace_bytes is not None and workspace_bytes < 0:      # (as a size_t it would be enough for anything)
+        raise QffnError(fn, 1, f"workspace_bytes: {workspace_bytes}")
     if workspace is None or workspace.__class__ is int:
         return workspace, int(workspace_bytes or 0)
     nbytes = workspace.numel() * workspace.element_size()
