@@ -341,7 +341,9 @@ qffn_status qffn_ffn_backward(uint16_t* d_ln2, uint16_t* dw1, uint16_t* dw2, flo
 /* ---- Layer norm and the norms' backward -------------------------------------
  * The layer norm beside qffn_rmsnorm_absmax, and the step of [llmq-model]
  * _backward_block that follows the gradients of the projections: the fused
- * residual norm's backward (rmsnorm_backward there).  All sums are fp32. */
+ * residual norm's backward (rmsnorm_backward there).  All sums are fp32.
+ * Here and in the linear and gated layers below, the buffers that have a row per
+ * row of activations may be NULL in a call without rows (N == 0, M == 0). */
 
 /* Fused residual add + layer norm + abs-max, with r = bf16(res_in + x) (or x
  * when res_in == NULL):

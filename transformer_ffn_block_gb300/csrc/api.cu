@@ -37,6 +37,8 @@ struct NvtxRange {
     if (!(cond)) return (err);  \
   } while (0)
 #define QFFN_PTR(p) QFFN_REQUIRE((p) != nullptr, QFFN_ERR_INVALID_ARG)
+// a buffer of `rows` rows: without any it may be NULL, the address of an empty tensor
+#define QFFN_PTR_ROWS(rows, p) QFFN_REQUIRE((rows) == 0 || (p) != nullptr, QFFN_ERR_INVALID_ARG)
 #define QFFN_ALIGNED(p) QFFN_REQUIRE((p) == nullptr || aligned16(p), QFFN_ERR_MISALIGNED)
 // fp32 scalars and vectors (stats pairs, scales, rstd, row scales): natural alignment
 #define QFFN_ALIGNED4(p) QFFN_REQUIRE((reinterpret_cast<uintptr_t>(p) & 3u) == 0, QFFN_ERR_MISALIGNED)
@@ -574,8 +576,8 @@ qffn_status qffn_layernorm_absmax(uint16_t* res_out, uint16_t* y, float* mean, f
                                   const uint16_t* gain, const uint16_t* shift, float eps, int64_t N,
                                   int64_t C, qffn_stream_t stream) {
   QFFN_RANGE();
-  QFFN_PTR(y); QFFN_PTR(mean); QFFN_PTR(rstd); QFFN_PTR(x); QFFN_PTR(gain);
-  if (res_in != nullptr) QFFN_PTR(res_out);
+  QFFN_PTR_ROWS(N, y); QFFN_PTR_ROWS(N, mean); QFFN_PTR_ROWS(N, rstd); QFFN_PTR_ROWS(N, x); QFFN_PTR(gain);
+  if (res_in != nullptr) QFFN_PTR_ROWS(N, res_out);
   QFFN_REQUIRE(isfinite(eps) && eps >= 0.0f, QFFN_ERR_INVALID_ARG);
   const qffn_status st = check_norm_shape(N, C);
   if (st != QFFN_OK) return st;
@@ -598,8 +600,8 @@ qffn_status qffn_layernorm_backward(uint16_t* dx, float* dgain, float* dshift, f
                                     int64_t N, int64_t C, int accumulate, void* workspace,
                                     size_t workspace_bytes, qffn_stream_t stream) {
   QFFN_RANGE();
-  QFFN_PTR(dx); QFFN_PTR(dgain); QFFN_PTR(dy); QFFN_PTR(r); QFFN_PTR(mean); QFFN_PTR(rstd); QFFN_PTR(gain);
-  QFFN_PTR(workspace);
+  QFFN_PTR_ROWS(N, dx); QFFN_PTR_ROWS(N, dy); QFFN_PTR_ROWS(N, r); QFFN_PTR_ROWS(N, mean); QFFN_PTR_ROWS(N, rstd);
+  QFFN_PTR(dgain); QFFN_PTR(gain); QFFN_PTR(workspace);
   const qffn_status st = check_norm_shape(N, C);
   if (st != QFFN_OK) return st;
   QFFN_REQUIRE(workspace_bytes >= qffn_norm_backward_workspace_size(N, C), QFFN_ERR_INVALID_ARG);
@@ -615,8 +617,8 @@ qffn_status qffn_rmsnorm_backward(uint16_t* dx, float* dgain, float* stats, cons
                                   const uint16_t* gain, int64_t N, int64_t C, int accumulate,
                                   void* workspace, size_t workspace_bytes, qffn_stream_t stream) {
   QFFN_RANGE();
-  QFFN_PTR(dx); QFFN_PTR(dgain); QFFN_PTR(dy); QFFN_PTR(r); QFFN_PTR(rstd); QFFN_PTR(gain);
-  QFFN_PTR(workspace);
+  QFFN_PTR_ROWS(N, dx); QFFN_PTR_ROWS(N, dy); QFFN_PTR_ROWS(N, r); QFFN_PTR_ROWS(N, rstd);
+  QFFN_PTR(dgain); QFFN_PTR(gain); QFFN_PTR(workspace);
   const qffn_status st = check_norm_shape(N, C);
   if (st != QFFN_OK) return st;
   QFFN_REQUIRE(workspace_bytes >= qffn_norm_backward_workspace_size(N, C), QFFN_ERR_INVALID_ARG);
@@ -637,7 +639,7 @@ qffn_status qffn_linear(uint16_t* out, uint16_t* z, const uint16_t* x, const uin
                         const uint16_t* bias, const uint16_t* residual, int act, int64_t M, int64_t N,
                         int64_t K, void* workspace, size_t workspace_bytes, qffn_stream_t stream) {
   QFFN_RANGE();
-  QFFN_PTR(out); QFFN_PTR(x); QFFN_PTR(w); QFFN_PTR(workspace);
+  QFFN_PTR_ROWS(M, out); QFFN_PTR_ROWS(M, x); QFFN_PTR(w); QFFN_PTR(workspace);
   QFFN_REQUIRE(valid_act(act), QFFN_ERR_INVALID_ARG);
   const qffn_status st = check_linear_shape(M, N, K, 8);
   if (st != QFFN_OK) return st;
@@ -658,7 +660,8 @@ qffn_status qffn_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, const 
                             const uint16_t* residual, int act, int64_t M, int64_t N, int64_t K,
                             void* workspace, size_t workspace_bytes, qffn_stream_t stream) {
   QFFN_RANGE();
-  QFFN_PTR(out); QFFN_PTR(x); QFFN_PTR(x_scale); QFFN_PTR(w); QFFN_PTR(w_scale); QFFN_PTR(workspace);
+  QFFN_PTR_ROWS(M, out); QFFN_PTR_ROWS(M, x);
+  QFFN_PTR(x_scale); QFFN_PTR(w); QFFN_PTR(w_scale); QFFN_PTR(workspace);
   QFFN_REQUIRE(valid_act(act), QFFN_ERR_INVALID_ARG);
   const qffn_status st = check_linear_shape(M, N, K, 16);
   if (st != QFFN_OK) return st;
@@ -680,9 +683,9 @@ qffn_status qffn_linear_backward(uint16_t* dx, uint16_t* dw, float* dbias, const
                                  int64_t M, int64_t N, int64_t K, int accumulate, void* workspace,
                                  size_t workspace_bytes, qffn_stream_t stream) {
   QFFN_RANGE();
-  QFFN_PTR(dw); QFFN_PTR(dout); QFFN_PTR(x); QFFN_PTR(w); QFFN_PTR(workspace);
+  QFFN_PTR(dw); QFFN_PTR_ROWS(M, dout); QFFN_PTR_ROWS(M, x); QFFN_PTR(w); QFFN_PTR(workspace);
   QFFN_REQUIRE(valid_act(act), QFFN_ERR_INVALID_ARG);
-  if (act != QFFN_ACT_NONE) QFFN_PTR(z);
+  if (act != QFFN_ACT_NONE) QFFN_PTR_ROWS(M, z);
   const qffn_status st = check_linear_backward_shape(M, N, K);
   if (st != QFFN_OK) return st;
   QFFN_REQUIRE(workspace_bytes >= qffn_linear_backward_workspace_size(M, N, K), QFFN_ERR_INVALID_ARG);
@@ -702,7 +705,7 @@ qffn_status qffn_gated_linear(uint16_t* h, const uint16_t* x, const uint16_t* w1
                               int64_t C, int64_t H, void* workspace, size_t workspace_bytes,
                               qffn_stream_t stream) {
   QFFN_RANGE();
-  QFFN_PTR(h); QFFN_PTR(x); QFFN_PTR(w1); QFFN_PTR(workspace);
+  QFFN_PTR_ROWS(N, h); QFFN_PTR_ROWS(N, x); QFFN_PTR(w1); QFFN_PTR(workspace);
   QFFN_REQUIRE(valid_act(act), QFFN_ERR_INVALID_ARG);
   const qffn_status st = check_gated_shape(N, C, H, false);
   if (st != QFFN_OK) return st;
@@ -722,7 +725,7 @@ qffn_status qffn_gated_linear_backward(uint16_t* dx, uint16_t* dw1, const uint16
                                        int64_t C, int64_t H, int accumulate, void* workspace,
                                        size_t workspace_bytes, qffn_stream_t stream) {
   QFFN_RANGE();
-  QFFN_PTR(dw1); QFFN_PTR(dh); QFFN_PTR(x); QFFN_PTR(w1); QFFN_PTR(workspace);
+  QFFN_PTR(dw1); QFFN_PTR_ROWS(N, dh); QFFN_PTR_ROWS(N, x); QFFN_PTR(w1); QFFN_PTR(workspace);
   QFFN_REQUIRE(valid_act(act), QFFN_ERR_INVALID_ARG);
   const qffn_status st = check_gated_shape(N, C, H, true);
   if (st != QFFN_OK) return st;
