@@ -368,7 +368,9 @@ qffn_status qffn_layernorm_absmax(uint16_t* res_out, uint16_t* y, float* mean, f
  *               that qffn_backward_qmm of the layer before quantises dx with
  * dx is the gradient of both inputs of the residual sum.  dx may alias dy or
  * dres.  The column sums are added in a fixed order (no atomics): the same
- * bits in every run.  workspace: >= qffn_norm_backward_workspace_size() bytes,
+ * bits in every run.  (Up to 512 rows, dx in the place of dy takes the order of
+ * more rows: equal to the call out of place within the rounding of the sums, not
+ * bit for bit.)  workspace: >= qffn_norm_backward_workspace_size() bytes,
  * 256-byte aligned, any content.  One or two launches (and a 4-byte memset with
  * stats).  Shape rules of qffn_layernorm_absmax. */
 size_t qffn_norm_backward_workspace_size(int64_t N, int64_t C);
@@ -416,7 +418,9 @@ qffn_status qffn_linear(uint16_t* out, uint16_t* z, const uint16_t* x, const uin
  *   z = x_scale * w_scale * (x . w^T) + bias
  * K % 16 == 0, K >= 16; the other rules as above.  With bias, residual and z
  * NULL and QFFN_ACT_NONE it computes qffn_fp8_gemm_scaled (the fp32 sums may
- * be split over K in another way). */
+ * be split over K in another way).  Its z serves qffn_linear_backward, which takes
+ * x and w in bf16; the gradient with E4M3 operands (qffn_backward_qmm) has no
+ * activation of its own. */
 size_t qffn_linear_fp8_workspace_size(int64_t M, int64_t N, int64_t K);
 qffn_status qffn_linear_fp8(uint16_t* out, uint16_t* z, const uint8_t* x, const float* x_scale,
                             const uint8_t* w, const float* w_scale, const uint16_t* bias,

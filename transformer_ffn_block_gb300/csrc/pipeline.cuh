@@ -9,7 +9,6 @@ namespace qffn {
 
 QFFN_DEVI uint32_t smem_u32(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
 
-// 16-byte shared-memory accesses by 32-bit shared address.
 // Whether the phase is complete, without waiting.
 QFFN_DEVI bool mbar_test_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -21,6 +20,7 @@ QFFN_DEVI bool mbar_test_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// Shared-memory accesses of 16 and 4 bytes by 32-bit shared address.
 QFFN_DEVI void sts16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }

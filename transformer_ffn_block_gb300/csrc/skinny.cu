@@ -5,7 +5,7 @@
 //   h[m, r]   = bf16(act(g) * u),  g / u from rows r and H + r of W1
 //
 // A CTA owns 16 weight rows (gated: 8 gate rows and the 8 up rows of the same
-// outputs); its eight warps take the row's 256-byte groups in turn.  The
+// outputs); its 8, 16 or 32 warps take the row's 256-byte groups in turn.  The
 // products run on the tensor cores with the weights as the 16-row operand and
 // up to 8 NT activation rows as the other (mma.sync m16n8k16 bf16 / m16n8k32
 // E4M3): the weights are used once, so what counts is that every lane loads 16
