@@ -474,6 +474,79 @@ qffn_status qffn_gated_linear_backward(uint16_t* dx, uint16_t* dw1, const uint16
                                        int64_t C, int64_t H, int accumulate, void* workspace,
                                        size_t workspace_bytes, qffn_stream_t stream);
 
+/* ---- E4M3 with a scale for each block of 128 ------------------------------------
+ * The finer form of the per-tensor records above: a block is 128 consecutive
+ * values of a row (the last of a row may be shorter), of weights 128 rows by 128
+ * columns of one matrix.  A scale is a power of two, stored as its E8M0 code c (one
+ * byte, value 2^(c - 127); 255 is NaN), the form that the tensor cores multiply with:
+ *   amax = max |v| over the block;  2^(c - 127) = the smallest power of two (2^-127
+ *   at least) with amax <= 448 * 2^(c - 127);  amax == 0: c = 127
+ *   q = e4m3(v * 2^(127 - c)), nearest even;  v = q * 2^(c - 127)
+ * A block with an infinity or a NaN gets c = 255 and NaN codes.  Scales have no
+ * alignment rule.  Rows are multiples of 16 values. */
+
+/* q[rows,cols], scale[rows, ceil(cols/128)] of a bf16 tensor.  rows >= 0,
+ * cols % 16 == 0, 16 <= cols <= 2^20. */
+qffn_status qffn_quantize_blocks(uint8_t* q, uint8_t* scale, const uint16_t* in, int64_t rows, int64_t cols,
+                                 qffn_stream_t stream);
+
+/* Weights: q[count,rows,cols], scale[count, ceil(rows/128), ceil(cols/128)] of
+ * `count` bf16 matrices (one per expert; 1 for a single layer), a scale for each
+ * 128 x 128.  0 <= count <= 4096, the other rules as above. */
+qffn_status qffn_quantize_weight_blocks(uint8_t* q, uint8_t* scale, const uint16_t* w, int64_t count, int64_t rows,
+                                        int64_t cols, qffn_stream_t stream);
+
+/* qffn_rmsnorm_absmax with a block-scaled E4M3 output in the same pass:
+ *   r = bf16(res_in + x) -> res_out (or x; res_out skipped if res_in == NULL)
+ *   rstd[N] = 1 / sqrt(mean_C(r^2) + eps)
+ *   q[N,C], scale[N, ceil(C/128)] = blocks of r * rstd * gain, which stays in fp32
+ *   y[N,C]  = bf16(r * rstd * gain)   (y == NULL: not written)
+ * qffn_rmsnorm_backward takes its r and rstd.  res_out may alias res_in or x.
+ * N >= 0, C % 16 == 0, 16 <= C <= 16384; eps >= 0 and finite. */
+qffn_status qffn_rmsnorm_quantize_blocks(uint16_t* res_out, uint16_t* y, uint8_t* q, uint8_t* scale, float* rstd,
+                                         const uint16_t* res_in, const uint16_t* x, const uint16_t* gain, float eps,
+                                         int64_t N, int64_t C, qffn_stream_t stream);
+
+/* qffn_swiglu_quant with block scales, in one pass (no abs-max to wait for):
+ * q[N,H], scale[N, ceil(H/128)] = blocks of silu(g) * u, which stays in fp32, for
+ * gate_up [N, 2H] bf16 (gate = cols [0,H));  h[N,H] = bf16 of it (NULL: not
+ * written).  N >= 0, H % 16 == 0, 16 <= H <= 2^20. */
+qffn_status qffn_swiglu_quantize_blocks(uint16_t* h, uint8_t* q, uint8_t* scale, const uint16_t* gate_up, int64_t N,
+                                        int64_t H, qffn_stream_t stream);
+
+/* qffn_linear_fp8 with block scales: x [M,K] with x_scale [M, ceil(K/128)], w [N,K]
+ * with w_scale [ceil(N/128), ceil(K/128)], as the calls above make them:
+ *   out[M,N] = bf16(sum over blocks b of K of
+ *                   2^(cx[m,b] - 127) 2^(cw[n/128,b] - 127) sum_{k in b} x[m,k] w[n,k]
+ *                   + bias[n] + residual[m,n])
+ * with fp32 sums; bias and residual (bf16) may be NULL; out may alias residual.
+ * Its gradient is that of the bf16 layer (qffn_linear_backward).  No workspace.
+ * M >= 0, N % 8 == 0, N >= 8, K % 16 == 0, K >= 16; the limits of qffn_linear. */
+qffn_status qffn_linear_fp8_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
+                                   const uint8_t* w_scale, const uint16_t* bias, const uint16_t* residual, int64_t M,
+                                   int64_t N, int64_t K, qffn_stream_t stream);
+
+/* ---- Products grouped by expert ---------------------------------------------------
+ * G matrices w [G,N,K]; rows offsets[g] .. offsets[g+1] - 1 of x and out belong to
+ * matrix g.  offsets: G + 1 device int32, not decreasing, 0 <= offsets <= M, read on
+ * the stream (the host does not see the sizes, so a call can be captured once and
+ * replayed with others).  Groups may be empty.  Rows before offsets[0] and from
+ * offsets[G] on are left as they were.  (An offset outside 0 .. M counts as 0 or
+ * M and a group whose end is before its start is empty: no access leaves the
+ * buffers; decreasing offsets leave rows undefined that two groups claim.)
+ * 1 <= G <= 4096; M, N, K as in qffn_linear.  No workspace. */
+
+/*   out[m] = bf16(x[m] . w[g]^T) for the rows m of group g, bf16 with fp32 sums.
+ * N % 8 == 0, K % 8 == 0. */
+qffn_status qffn_grouped_linear(uint16_t* out, const uint16_t* x, const uint16_t* w, const int32_t* offsets, int64_t G,
+                                int64_t M, int64_t N, int64_t K, qffn_stream_t stream);
+
+/* The same with block-scaled E4M3: x_scale [M, ceil(K/128)], w_scale [G, ceil(N/128),
+ * ceil(K/128)], the sum of qffn_linear_fp8_blocks.  K % 16 == 0. */
+qffn_status qffn_grouped_linear_fp8_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
+                                           const uint8_t* w_scale, const int32_t* offsets, int64_t G, int64_t M,
+                                           int64_t N, int64_t K, qffn_stream_t stream);
+
 /* ---- Step A6: dual row-scaled FP8 GEMV ------------------------------------
  * [metrale] w8a16_gemv_dual: one pass over x for two weight matrices.
  *   g[r] = bf16(s_gate[r] * sum_k Wg[r,k] * x[k]),  u likewise with Wu, s_up.

@@ -36,6 +36,8 @@ __all__ = [
     "qffn_gated_linear_workspace_size", "qffn_gated_linear", "qffn_gated_linear_backward_workspace_size",
     "qffn_gated_linear_backward", "QFFN_ACT_NONE", "QFFN_ACT_RELU", "QFFN_ACT_GELU", "QFFN_ACT_GELU_TANH",
     "QFFN_ACT_SILU",
+    "qffn_quantize_blocks", "qffn_quantize_weight_blocks", "qffn_rmsnorm_quantize_blocks",
+    "qffn_swiglu_quantize_blocks", "qffn_linear_fp8_blocks", "qffn_grouped_linear", "qffn_grouped_linear_fp8_blocks",
     "qffn_gemv_dual", "qffn_gemv", "qffn_gemv_silu_input", "qffn_silu_mul", "qffn_decode_workspace_size",
     "qffn_decode_workspace_offsets", "qffn_decode_forward", "qffn_decode_forward_ex", "qffn_decode_forward_gu",
     "qffn_decode_forward_noalloc", "QFFN_DECODE_WEIGHTS_STABLE",
@@ -105,6 +107,13 @@ _SIGS = {
     "qffn_gated_linear": ([_P] * 3 + [_S, _I64, _I64, _I64, _P, _SZ, _P], _S),
     "qffn_gated_linear_backward_workspace_size": ([_I64] * 3, _SZ),
     "qffn_gated_linear_backward": ([_P] * 5 + [_S, _I64, _I64, _I64, _S, _P, _SZ, _P], _S),
+    "qffn_quantize_blocks": ([_P] * 3 + [_I64] * 2 + [_P], _S),
+    "qffn_quantize_weight_blocks": ([_P] * 3 + [_I64] * 3 + [_P], _S),
+    "qffn_rmsnorm_quantize_blocks": ([_P] * 8 + [_F, _I64, _I64, _P], _S),
+    "qffn_swiglu_quantize_blocks": ([_P] * 4 + [_I64] * 2 + [_P], _S),
+    "qffn_linear_fp8_blocks": ([_P] * 7 + [_I64] * 3 + [_P], _S),
+    "qffn_grouped_linear": ([_P] * 4 + [_I64] * 4 + [_P], _S),
+    "qffn_grouped_linear_fp8_blocks": ([_P] * 6 + [_I64] * 4 + [_P], _S),
     "qffn_gemv_dual": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _P], _S),
     "qffn_gemv": ([_P, _P, _P, _P, _I64, _I64, _P], _S),
     "qffn_gemv_silu_input": ([_P, _P, _P, _P, _P, _I64, _I64, _P], _S),
@@ -137,20 +146,22 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_BF16, _F32, _E4M3 = set(), set(), set()      # the tensor types that hold each (filled with torch)
+# the tensor types that hold each (filled with torch)
+_BF16, _F32, _E4M3, _E8M0, _I32 = set(), set(), set(), set(), set()
+_KINDS = ((_BF16, "bf16"), (_F32, "fp32"), (_E4M3, "E4M3"), (_E8M0, "E8M0"), (_I32, "int32"))
 
 
 def _buf(fn, device, name, t, types, n):
     """_ptr of a tensor after the checks that a bare address cannot have: ``n`` elements at least of one
     of ``types``, contiguous, on the current device.  bf16 may come as int16 or uint16 bits and E4M3
-    as uint8 codes, as in the other functions."""
+    and E8M0 as uint8 codes, as in the other functions."""
     if t is None:
         return None
     if t.__class__ is int:
         return t
     if t.is_contiguous() and t.dtype in types and t.numel() >= n and (t.get_device() == device or n <= 0):
         return t.data_ptr()
-    kind = "bf16" if types is _BF16 else "fp32" if types is _F32 else "E4M3"
+    kind = next(name for held, name in _KINDS if held is types)
     raise QffnError(fn, 1, f"{name}: expected {n} contiguous {kind} elements on cuda:{device}, got "
                            f"{tuple(t.shape)} {t.dtype} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
 
@@ -169,6 +180,8 @@ def _load_torch():
         _BF16.update((torch.bfloat16, torch.int16, torch.uint16))
         _F32.add(torch.float32)
         _E4M3.update((torch.float8_e4m3fn, torch.uint8))
+        _E8M0.update((torch.float8_e8m0fnu, torch.uint8))
+        _I32.add(torch.int32)
         if torch.cuda.is_available():
             torch.cuda.init()
             _get_stream, _get_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
@@ -480,6 +493,65 @@ def qffn_gated_linear_backward(dx, dw1, dh, x, w1, act, N, C, H, accumulate, wor
         _buf(fn, d, "dx", dx, _BF16, N * C), _buf(fn, d, "dw1", dw1, _BF16, 2 * H * C),
         _buf(fn, d, "dh", dh, _BF16, N * H), _buf(fn, d, "x", x, _BF16, N * C), _buf(fn, d, "w1", w1, _BF16, 2 * H * C),
         act, N, C, H, bool(accumulate), ws, nbytes, _stream(stream)))
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def qffn_quantize_blocks(q, scale, inp, rows, cols, stream=None):
+    fn, d, n = "qffn_quantize_blocks", _current_device(), rows * cols
+    _check(fn, lib.qffn_quantize_blocks(
+        _buf(fn, d, "q", q, _E4M3, n), _buf(fn, d, "scale", scale, _E8M0, rows * _blocks(cols)),
+        _buf(fn, d, "inp", inp, _BF16, n), rows, cols, _stream(stream)))
+
+
+def qffn_quantize_weight_blocks(q, scale, w, count, rows, cols, stream=None):
+    fn, d, n = "qffn_quantize_weight_blocks", _current_device(), count * rows * cols
+    _check(fn, lib.qffn_quantize_weight_blocks(
+        _buf(fn, d, "q", q, _E4M3, n), _buf(fn, d, "scale", scale, _E8M0, count * _blocks(rows) * _blocks(cols)),
+        _buf(fn, d, "w", w, _BF16, n), count, rows, cols, _stream(stream)))
+
+
+def qffn_rmsnorm_quantize_blocks(res_out, y, q, scale, rstd, res_in, x, gain, eps, N, C, stream=None):
+    fn, d, n = "qffn_rmsnorm_quantize_blocks", _current_device(), N * C
+    _check(fn, lib.qffn_rmsnorm_quantize_blocks(
+        _buf(fn, d, "res_out", res_out, _BF16, n), _buf(fn, d, "y", y, _BF16, n), _buf(fn, d, "q", q, _E4M3, n),
+        _buf(fn, d, "scale", scale, _E8M0, N * _blocks(C)), _buf(fn, d, "rstd", rstd, _F32, N),
+        _buf(fn, d, "res_in", res_in, _BF16, n), _buf(fn, d, "x", x, _BF16, n), _buf(fn, d, "gain", gain, _BF16, C),
+        eps, N, C, _stream(stream)))
+
+
+def qffn_swiglu_quantize_blocks(h, q, scale, gate_up, N, H, stream=None):
+    fn, d, n = "qffn_swiglu_quantize_blocks", _current_device(), N * H
+    _check(fn, lib.qffn_swiglu_quantize_blocks(
+        _buf(fn, d, "h", h, _BF16, n), _buf(fn, d, "q", q, _E4M3, n), _buf(fn, d, "scale", scale, _E8M0, N * _blocks(H)),
+        _buf(fn, d, "gate_up", gate_up, _BF16, 2 * n), N, H, _stream(stream)))
+
+
+def qffn_linear_fp8_blocks(out, x, x_scale, w, w_scale, bias, residual, M, N, K, stream=None):
+    fn, d = "qffn_linear_fp8_blocks", _current_device()
+    _check(fn, lib.qffn_linear_fp8_blocks(
+        _buf(fn, d, "out", out, _BF16, M * N), _buf(fn, d, "x", x, _E4M3, M * K),
+        _buf(fn, d, "x_scale", x_scale, _E8M0, M * _blocks(K)), _buf(fn, d, "w", w, _E4M3, N * K),
+        _buf(fn, d, "w_scale", w_scale, _E8M0, _blocks(N) * _blocks(K)), _buf(fn, d, "bias", bias, _BF16, N),
+        _buf(fn, d, "residual", residual, _BF16, M * N), M, N, K, _stream(stream)))
+
+
+def qffn_grouped_linear(out, x, w, offsets, G, M, N, K, stream=None):
+    fn, d = "qffn_grouped_linear", _current_device()
+    _check(fn, lib.qffn_grouped_linear(
+        _buf(fn, d, "out", out, _BF16, M * N), _buf(fn, d, "x", x, _BF16, M * K), _buf(fn, d, "w", w, _BF16, G * N * K),
+        _buf(fn, d, "offsets", offsets, _I32, G + 1), G, M, N, K, _stream(stream)))
+
+
+def qffn_grouped_linear_fp8_blocks(out, x, x_scale, w, w_scale, offsets, G, M, N, K, stream=None):
+    fn, d = "qffn_grouped_linear_fp8_blocks", _current_device()
+    _check(fn, lib.qffn_grouped_linear_fp8_blocks(
+        _buf(fn, d, "out", out, _BF16, M * N), _buf(fn, d, "x", x, _E4M3, M * K),
+        _buf(fn, d, "x_scale", x_scale, _E8M0, M * _blocks(K)), _buf(fn, d, "w", w, _E4M3, G * N * K),
+        _buf(fn, d, "w_scale", w_scale, _E8M0, G * _blocks(N) * _blocks(K)),
+        _buf(fn, d, "offsets", offsets, _I32, G + 1), G, M, N, K, _stream(stream)))
 
 
 def qffn_gemv_dual(g, u, x, w_gate, s_gate, w_up, s_up, H, C, stream=None):

@@ -155,6 +155,21 @@ qffn_status check_gated_shape(int64_t N, int64_t C, int64_t H, bool backward) {
 bool valid_act(int act) { return act >= QFFN_ACT_NONE && act <= QFFN_ACT_SILU; }
 size_t at_least_256(size_t v) { return v < 256 ? 256 : v; }
 
+// products grouped by expert: at most kMaxGroups, and the products' sizes in all
+constexpr int64_t kMaxGroups = 4096;
+qffn_status check_grouped_shape(int64_t G, int64_t M, int64_t N, int64_t K, int64_t k_step) {
+  QFFN_REQUIRE(G >= 1, QFFN_ERR_INVALID_ARG);
+  QFFN_REQUIRE(G <= kMaxGroups, QFFN_ERR_UNSUPPORTED_SHAPE);
+  return check_linear_shape(M, N, K, k_step);
+}
+// rows of E4M3 with a scale per block of 128: a row is a whole number of 16-byte loads
+qffn_status check_block_rows(int64_t rows, int64_t cols, int64_t max_cols) {
+  QFFN_REQUIRE(rows >= 0 && cols >= 0, QFFN_ERR_INVALID_ARG);
+  QFFN_REQUIRE(rows <= kMaxRows, QFFN_ERR_UNSUPPORTED_SHAPE);
+  QFFN_REQUIRE(cols % 16 == 0 && cols >= 16 && cols <= max_cols, QFFN_ERR_UNSUPPORTED_SHAPE);
+  return QFFN_OK;
+}
+
 qffn_status check_norm_shape(int64_t N, int64_t C) {
   QFFN_REQUIRE(N >= 0 && C >= 0, QFFN_ERR_INVALID_ARG);
   QFFN_REQUIRE(N <= kMaxRows, QFFN_ERR_UNSUPPORTED_SHAPE);
@@ -734,6 +749,86 @@ qffn_status qffn_gated_linear_backward(uint16_t* dx, uint16_t* dw1, const uint16
   QFFN_ALIGNED(dx); QFFN_ALIGNED(dw1); QFFN_ALIGNED(dh); QFFN_ALIGNED(x); QFFN_ALIGNED(w1);
   return from_cuda(qffn::launch_gated_backward(dx, dw1, dh, x, w1, act, N, C, H, accumulate != 0,
                                                static_cast<uint8_t*>(workspace), stream));
+}
+
+qffn_status qffn_quantize_blocks(uint8_t* q, uint8_t* scale, const uint16_t* in, int64_t rows, int64_t cols,
+                                 qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR_ROWS(rows, q); QFFN_PTR_ROWS(rows, scale); QFFN_PTR_ROWS(rows, in);
+  const qffn_status st = check_block_rows(rows, cols, kMaxDim);
+  if (st != QFFN_OK) return st;
+  QFFN_ALIGNED(q); QFFN_ALIGNED(in);
+  return from_cuda(qffn::launch_quantize_blocks(q, scale, in, rows, cols, stream));
+}
+
+qffn_status qffn_quantize_weight_blocks(uint8_t* q, uint8_t* scale, const uint16_t* w, int64_t count, int64_t rows,
+                                        int64_t cols, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_REQUIRE(count >= 0, QFFN_ERR_INVALID_ARG);
+  QFFN_REQUIRE(count <= kMaxGroups, QFFN_ERR_UNSUPPORTED_SHAPE);
+  const bool any = count > 0 && rows > 0;
+  QFFN_PTR_ROWS(any, q); QFFN_PTR_ROWS(any, scale); QFFN_PTR_ROWS(any, w);
+  const qffn_status st = check_block_rows(rows, cols, kMaxDim);
+  if (st != QFFN_OK) return st;
+  QFFN_ALIGNED(q); QFFN_ALIGNED(w);
+  return from_cuda(qffn::launch_quantize_weight_blocks(q, scale, w, count, rows, cols, stream));
+}
+
+qffn_status qffn_rmsnorm_quantize_blocks(uint16_t* res_out, uint16_t* y, uint8_t* q, uint8_t* scale, float* rstd,
+                                         const uint16_t* res_in, const uint16_t* x, const uint16_t* gain, float eps,
+                                         int64_t N, int64_t C, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR_ROWS(N, q); QFFN_PTR_ROWS(N, scale); QFFN_PTR_ROWS(N, rstd); QFFN_PTR_ROWS(N, x); QFFN_PTR(gain);
+  if (res_in != nullptr) QFFN_PTR_ROWS(N, res_out);
+  QFFN_REQUIRE(isfinite(eps) && eps >= 0.0f, QFFN_ERR_INVALID_ARG);
+  const qffn_status st = check_block_rows(N, C, 16384);
+  if (st != QFFN_OK) return st;
+  QFFN_ALIGNED(y); QFFN_ALIGNED(q); QFFN_ALIGNED4(rstd); QFFN_ALIGNED(x); QFFN_ALIGNED(gain);
+  if (res_in != nullptr) { QFFN_ALIGNED(res_in); QFFN_ALIGNED(res_out); }
+  return from_cuda(qffn::launch_rmsnorm_quantize_blocks(res_out, y, q, scale, rstd, res_in, x, gain, eps, N, int(C),
+                                                        stream));
+}
+
+qffn_status qffn_swiglu_quantize_blocks(uint16_t* h, uint8_t* q, uint8_t* scale, const uint16_t* gate_up, int64_t N,
+                                        int64_t H, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR_ROWS(N, q); QFFN_PTR_ROWS(N, scale); QFFN_PTR_ROWS(N, gate_up);
+  const qffn_status st = check_block_rows(N, H, kMaxDim);
+  if (st != QFFN_OK) return st;
+  QFFN_ALIGNED(h); QFFN_ALIGNED(q); QFFN_ALIGNED(gate_up);
+  return from_cuda(qffn::launch_swiglu_quantize_blocks(h, q, scale, gate_up, N, H, stream));
+}
+
+qffn_status qffn_linear_fp8_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
+                                   const uint8_t* w_scale, const uint16_t* bias, const uint16_t* residual, int64_t M,
+                                   int64_t N, int64_t K, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR_ROWS(M, out); QFFN_PTR_ROWS(M, x); QFFN_PTR_ROWS(M, x_scale); QFFN_PTR(w); QFFN_PTR(w_scale);
+  const qffn_status st = check_linear_shape(M, N, K, 16);
+  if (st != QFFN_OK) return st;
+  QFFN_ALIGNED(out); QFFN_ALIGNED(x); QFFN_ALIGNED(w); QFFN_ALIGNED(bias); QFFN_ALIGNED(residual);
+  return from_cuda(M == 0 ? cudaSuccess : qffn::launch_few_groups(out, x, x_scale, w, w_scale, bias, residual, nullptr, 1, M, N, K, stream));
+}
+
+qffn_status qffn_grouped_linear(uint16_t* out, const uint16_t* x, const uint16_t* w, const int32_t* offsets, int64_t G,
+                                int64_t M, int64_t N, int64_t K, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR_ROWS(M, out); QFFN_PTR_ROWS(M, x); QFFN_PTR(w); QFFN_PTR(offsets);
+  const qffn_status st = check_grouped_shape(G, M, N, K, 8);
+  if (st != QFFN_OK) return st;
+  QFFN_ALIGNED(out); QFFN_ALIGNED(x); QFFN_ALIGNED(w); QFFN_ALIGNED4(offsets);
+  return from_cuda(M == 0 ? cudaSuccess : qffn::launch_few_groups(out, x, nullptr, w, nullptr, nullptr, nullptr, offsets, G, M, N, K, stream));
+}
+
+qffn_status qffn_grouped_linear_fp8_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
+                                           const uint8_t* w_scale, const int32_t* offsets, int64_t G, int64_t M,
+                                           int64_t N, int64_t K, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR_ROWS(M, out); QFFN_PTR_ROWS(M, x); QFFN_PTR_ROWS(M, x_scale); QFFN_PTR(w); QFFN_PTR(w_scale); QFFN_PTR(offsets);
+  const qffn_status st = check_grouped_shape(G, M, N, K, 16);
+  if (st != QFFN_OK) return st;
+  QFFN_ALIGNED(out); QFFN_ALIGNED(x); QFFN_ALIGNED(w); QFFN_ALIGNED4(offsets);
+  return from_cuda(M == 0 ? cudaSuccess : qffn::launch_few_groups(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, stream));
 }
 
 qffn_status qffn_gemv_dual(uint16_t* g, uint16_t* u, const uint16_t* x, const uint8_t* w_gate,

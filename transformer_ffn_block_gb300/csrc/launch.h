@@ -189,6 +189,24 @@ cudaError_t few_rows_take_status(unsigned int* status);
 // Reads and clears the linear kernels' device status word of the current device.
 cudaError_t linear_take_status(unsigned int* status);
 
+// ---- E4M3 with a scale per block of 128 (blocks.cu); scales are E8M0 codes
+cudaError_t launch_quantize_blocks(uint8_t* q, uint8_t* scale, const uint16_t* in, int64_t rows, int64_t cols,
+                                   cudaStream_t s);
+cudaError_t launch_quantize_weight_blocks(uint8_t* q, uint8_t* scale, const uint16_t* w, int64_t count, int64_t rows,
+                                          int64_t cols, cudaStream_t s);
+cudaError_t launch_swiglu_quantize_blocks(uint16_t* h, uint8_t* q, uint8_t* scale, const uint16_t* gate_up, int64_t N,
+                                          int64_t H, cudaStream_t s);
+cudaError_t launch_rmsnorm_quantize_blocks(uint16_t* res_out, uint16_t* y, uint8_t* q, uint8_t* scale, float* rstd,
+                                           const uint16_t* res_in, const uint16_t* x, const uint16_t* gain, float eps,
+                                           int64_t N, int C, cudaStream_t s);
+
+// ---- products of groups of rows with a matrix each, and block-scaled products.
+// x, w: bf16, or E4M3 with x_scale and w_scale; offsets NULL: one group of all M rows.
+// Few rows (grouped_few.cu):
+cudaError_t launch_few_groups(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w,
+                              const uint8_t* w_scale, const uint16_t* bias, const uint16_t* res, const int* offsets,
+                              int64_t G, int64_t M, int64_t N, int64_t K, cudaStream_t s);
+
 // Reads and clears the decode kernels' device status word of the current device.
 cudaError_t decode_take_status(unsigned int* status);
 
