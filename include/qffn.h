@@ -541,7 +541,19 @@ qffn_status qffn_linear_fp8_blocks(uint16_t* out, const uint8_t* x, const uint8_
 qffn_status qffn_grouped_linear(uint16_t* out, const uint16_t* x, const uint16_t* w, const int32_t* offsets, int64_t G,
                                 int64_t M, int64_t N, int64_t K, qffn_stream_t stream);
 
-/* The same with block-scaled E4M3: x_scale [M, ceil(K/128)], w_scale [G, ceil(N/128),
+/* Backward of qffn_grouped_linear for the gradient dout [M,N] of its out:
+ *   dx[m,K]    = bf16(dout[m] . w[g]) for the rows m of group g   (dx may be NULL)
+ *   dw[g,N,K]  = bf16(sum over the rows m of group g of dout[m]^T x[m] (+ dw[g]))
+ * with fp32 sums; the previous dw is added when accumulate != 0.  A group without
+ * rows has dw = 0 (or keeps it).  Rows of dx of no group are left as they were, and
+ * such rows of dout and x reach nothing.  The same bits in every run.  dx and dw
+ * must not overlap any input or each other.  N % 8 == 0, K % 8 == 0, and at most
+ * 2^28 tiles of 256 x 256 in dw. */
+qffn_status qffn_grouped_linear_backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uint16_t* x,
+                                         const uint16_t* w, const int32_t* offsets, int64_t G, int64_t M, int64_t N,
+                                         int64_t K, int accumulate, qffn_stream_t stream);
+
+/* qffn_grouped_linear with block-scaled E4M3: x_scale [M, ceil(K/128)], w_scale [G, ceil(N/128),
  * ceil(K/128)], the sum of qffn_linear_fp8_blocks.  K % 16 == 0. */
 qffn_status qffn_grouped_linear_fp8_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
                                            const uint8_t* w_scale, const int32_t* offsets, int64_t G, int64_t M,

@@ -41,6 +41,14 @@ def test_product_refusals(lib):  # noqa: F811
     _refuses(lib.lib.qffn_grouped_linear, good,
              [(i, NULL, 1) for i in range(4)] + [(4, 0, 1), (4, -1, 1), (4, 4097, 2), (5, -1, 1), (6, 12, 2), (7, 12, 2), (7, 0, 2)]
              + [(i, MIS, 3) for i in range(3)] + [(3, ODD4, 3)])
+    # dx, dw, dout, x, w, offsets, G, M, N, K, accumulate, stream
+    good = [A] * 6 + [8, 4, 256, 512, 0, None]
+    _refuses(lib.lib.qffn_grouped_linear_backward, good,
+             [(i, NULL, 1) for i in (1, 2, 3, 4, 5)] + [(6, 0, 1), (6, 4097, 2), (7, -1, 1), (8, 12, 2), (9, 12, 2), (8, 0, 2)]
+             + [(i, MIS, 3) for i in range(5)] + [(5, ODD4, 3)])
+    big = list(good)
+    big[6], big[8], big[9] = 4096, 1 << 17, 1 << 17                 # dw of 2^30 tiles
+    assert lib.lib.qffn_grouped_linear_backward(*big) == 2
     # out, x, x_scale, w, w_scale, offsets, G, M, N, K, stream
     good = [A, A, A + 1, A, A + 1, A, 8, 4, 256, 512, None]
     _refuses(lib.lib.qffn_grouped_linear_fp8_blocks, good,
@@ -59,6 +67,7 @@ def test_calls_without_rows(lib):  # noqa: F811
     assert f.qffn_linear_fp8_blocks(NULL, NULL, NULL, A, A, NULL, NULL, 0, 256, 512, None) == 0
     assert f.qffn_grouped_linear(NULL, NULL, A, A, 4, 0, 256, 512, None) == 0
     assert f.qffn_grouped_linear_fp8_blocks(NULL, NULL, NULL, A, A, A, 4, 0, 256, 512, None) == 0
+    assert f.qffn_grouped_linear_backward(NULL, A, NULL, NULL, A, A, 4, 0, 256, 512, 1, None) == 0
 
 
 def test_binding_refuses_tensors(lib):  # noqa: F811

@@ -173,3 +173,49 @@ def test_offsets_outside_the_rows_are_clamped(q, M, fp8):
     want, bound, _ = B.grouped(xv, wv, [0, M // 3, M // 3, M // 2, M])
     sure = [i for i in range(M) if not M // 3 - 2 <= i < M // 3]    # (rows that two groups claim are undefined)
     P.check(out[sure], want[sure], bound[sure], "out")
+
+
+@pytest.mark.parametrize("G,M,N,K", GROUPED)
+@pytest.mark.parametrize("kind", ["ragged", "one", "gaps"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_grouped_backward(q, G, M, N, K, kind, accumulate):
+    off = _sizes(kind, G, M)
+    dout, x, w = _t(1, M, N, std=0.1), _t(2, M, K), _t(3, G, N, K, std=0.1)
+    old = _t(4, G, N, K) if accumulate else None
+    dx, dw = _new(M, K), old.cuda() if accumulate else _new(G, N, K)
+    q.qffn_grouped_linear_backward(dx, dw, dout.cuda(), x.cuda(), w.cuda(), off.cuda(), G, M, N, K, accumulate)
+    q.qffn_check_status()
+    want_dx, want_dw, b_dx, b_dw, live = B.grouped_backward(dout.double(), x.double(), w.double(), off,
+                                                            old.double() if accumulate else None)
+    P.check(dx[live.cuda()], want_dx[live], b_dx[live], "dx")
+    P.check(dw, want_dw, b_dw, "dw")
+    assert bool(torch.isnan(dx[~live.cuda()]).all())                # left as they were
+    again = old.cuda() if accumulate else _new(G, N, K)             # the weight gradient alone, the same bits
+    q.qffn_grouped_linear_backward(None, again, dout.cuda(), x.cuda(), w.cuda(), off.cuda(), G, M, N, K, accumulate)
+    assert torch.equal(again, dw)
+
+
+@pytest.mark.parametrize("M", [6, 40, 700])
+def test_grouped_backward_neighbours_do_not_mix(q, M):
+    """A group that ends anywhere: what the next one, or no group, holds does not reach its gradients."""
+    G, N, K = 4, 200, 208
+    off = torch.tensor([1, M // 4 + 1, M // 2, M // 2, M - 1], dtype=torch.int32)
+    dout, x, w = _t(1, M, N), _t(2, M, K), _t(3, G, N, K)
+    bad = slice(int(off[1]), int(off[2]))
+
+    def run():
+        dx, dw = _new(M, K), _new(G, N, K)
+        q.qffn_grouped_linear_backward(dx, dw, dout.cuda(), x.cuda(), w.cuda(), off.cuda(), G, M, N, K, False)
+        q.qffn_check_status()
+        return dx, dw
+
+    base_dx, base_dw = run()
+    dout[bad], w[1] = float("nan"), float("inf")
+    for t in (x, dout):
+        t[0], t[-1] = float("inf"), float("nan")
+    x[bad], w[2] = float("-inf"), float("nan")
+    dx, dw = run()
+    base_dx[bad], base_dw[1] = float("nan"), float("nan")
+    for got, want in ((dx, base_dx), (dw, base_dw)):
+        assert torch.equal(torch.nan_to_num(got, nan=7.0), torch.nan_to_num(want, nan=7.0))
+    assert not dw[2].any()

@@ -37,7 +37,8 @@ __all__ = [
     "qffn_gated_linear_backward", "QFFN_ACT_NONE", "QFFN_ACT_RELU", "QFFN_ACT_GELU", "QFFN_ACT_GELU_TANH",
     "QFFN_ACT_SILU",
     "qffn_quantize_blocks", "qffn_quantize_weight_blocks", "qffn_rmsnorm_quantize_blocks",
-    "qffn_swiglu_quantize_blocks", "qffn_linear_fp8_blocks", "qffn_grouped_linear", "qffn_grouped_linear_fp8_blocks",
+    "qffn_swiglu_quantize_blocks", "qffn_linear_fp8_blocks", "qffn_grouped_linear", "qffn_grouped_linear_backward",
+    "qffn_grouped_linear_fp8_blocks",
     "qffn_gemv_dual", "qffn_gemv", "qffn_gemv_silu_input", "qffn_silu_mul", "qffn_decode_workspace_size",
     "qffn_decode_workspace_offsets", "qffn_decode_forward", "qffn_decode_forward_ex", "qffn_decode_forward_gu",
     "qffn_decode_forward_noalloc", "QFFN_DECODE_WEIGHTS_STABLE",
@@ -113,6 +114,7 @@ _SIGS = {
     "qffn_swiglu_quantize_blocks": ([_P] * 4 + [_I64] * 2 + [_P], _S),
     "qffn_linear_fp8_blocks": ([_P] * 7 + [_I64] * 3 + [_P], _S),
     "qffn_grouped_linear": ([_P] * 4 + [_I64] * 4 + [_P], _S),
+    "qffn_grouped_linear_backward": ([_P] * 6 + [_I64] * 4 + [_S, _P], _S),
     "qffn_grouped_linear_fp8_blocks": ([_P] * 6 + [_I64] * 4 + [_P], _S),
     "qffn_gemv_dual": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _P], _S),
     "qffn_gemv": ([_P, _P, _P, _P, _I64, _I64, _P], _S),
@@ -543,6 +545,14 @@ def qffn_grouped_linear(out, x, w, offsets, G, M, N, K, stream=None):
     _check(fn, lib.qffn_grouped_linear(
         _buf(fn, d, "out", out, _BF16, M * N), _buf(fn, d, "x", x, _BF16, M * K), _buf(fn, d, "w", w, _BF16, G * N * K),
         _buf(fn, d, "offsets", offsets, _I32, G + 1), G, M, N, K, _stream(stream)))
+
+
+def qffn_grouped_linear_backward(dx, dw, dout, x, w, offsets, G, M, N, K, accumulate, stream=None):
+    fn, d = "qffn_grouped_linear_backward", _current_device()
+    _check(fn, lib.qffn_grouped_linear_backward(
+        _buf(fn, d, "dx", dx, _BF16, M * K), _buf(fn, d, "dw", dw, _BF16, G * N * K), _buf(fn, d, "dout", dout, _BF16, M * N),
+        _buf(fn, d, "x", x, _BF16, M * K), _buf(fn, d, "w", w, _BF16, G * N * K),
+        _buf(fn, d, "offsets", offsets, _I32, G + 1), G, M, N, K, bool(accumulate), _stream(stream)))
 
 
 def qffn_grouped_linear_fp8_blocks(out, x, x_scale, w, w_scale, offsets, G, M, N, K, stream=None):

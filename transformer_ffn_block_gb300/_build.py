@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqffn.so")
 
 SOURCES = ["api.cu", "elementwise.cu", "gemm_fp8.cu", "decode.cu", "decode_noalloc.cu", "backward.cu", "norm.cu",
-           "linear.cu", "few_rows.cu", "skinny.cu", "blocks.cu", "grouped_few.cu"]
+           "linear.cu", "few_rows.cu", "skinny.cu", "blocks.cu", "grouped.cu", "grouped_few.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("act.cuh", "common.cuh", "launch.h", "pipeline.cuh", "tensor_map.h",
                                              "umma.cuh")] + [os.path.join(INCLUDE, "qffn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -197,13 +197,14 @@ int qffn_abi_version(void) { return kAbiVersion; }
 
 qffn_status qffn_check_status(qffn_stream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return QFFN_ERR_CUDA;
-  unsigned int st = 0, sd = 0, sl = 0, sf = 0, sn = 0;
+  unsigned int st = 0, sd = 0, sl = 0, sf = 0, sn = 0, sg = 0;
   if (qffn::gemm_take_status(&st) != cudaSuccess) return QFFN_ERR_CUDA;
   if (qffn::decode_take_status(&sd) != cudaSuccess) return QFFN_ERR_CUDA;
   if (qffn::linear_take_status(&sl) != cudaSuccess) return QFFN_ERR_CUDA;
   if (qffn::few_rows_take_status(&sf) != cudaSuccess) return QFFN_ERR_CUDA;
   if (qffn::norm_take_status(&sn) != cudaSuccess) return QFFN_ERR_CUDA;
-  return (st | sd | sl | sf | sn) != 0 ? QFFN_ERR_TIMEOUT : QFFN_OK;
+  if (qffn::grouped_take_status(&sg) != cudaSuccess) return QFFN_ERR_CUDA;
+  return (st | sd | sl | sf | sn | sg) != 0 ? QFFN_ERR_TIMEOUT : QFFN_OK;
 }
 
 qffn_status qffn_gemm_clock_sample(uint64_t* out, qffn_stream_t stream) {
@@ -807,7 +808,7 @@ qffn_status qffn_linear_fp8_blocks(uint16_t* out, const uint8_t* x, const uint8_
   const qffn_status st = check_linear_shape(M, N, K, 16);
   if (st != QFFN_OK) return st;
   QFFN_ALIGNED(out); QFFN_ALIGNED(x); QFFN_ALIGNED(w); QFFN_ALIGNED(bias); QFFN_ALIGNED(residual);
-  return from_cuda(M == 0 ? cudaSuccess : qffn::launch_few_groups(out, x, x_scale, w, w_scale, bias, residual, nullptr, 1, M, N, K, stream));
+  return from_cuda(qffn::launch_linear_blocks(out, x, x_scale, w, w_scale, bias, residual, M, N, K, stream));
 }
 
 qffn_status qffn_grouped_linear(uint16_t* out, const uint16_t* x, const uint16_t* w, const int32_t* offsets, int64_t G,
@@ -817,7 +818,7 @@ qffn_status qffn_grouped_linear(uint16_t* out, const uint16_t* x, const uint16_t
   const qffn_status st = check_grouped_shape(G, M, N, K, 8);
   if (st != QFFN_OK) return st;
   QFFN_ALIGNED(out); QFFN_ALIGNED(x); QFFN_ALIGNED(w); QFFN_ALIGNED4(offsets);
-  return from_cuda(M == 0 ? cudaSuccess : qffn::launch_few_groups(out, x, nullptr, w, nullptr, nullptr, nullptr, offsets, G, M, N, K, stream));
+  return from_cuda(qffn::launch_grouped(out, x, nullptr, w, nullptr, offsets, G, M, N, K, stream));
 }
 
 qffn_status qffn_grouped_linear_fp8_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
@@ -828,7 +829,20 @@ qffn_status qffn_grouped_linear_fp8_blocks(uint16_t* out, const uint8_t* x, cons
   const qffn_status st = check_grouped_shape(G, M, N, K, 16);
   if (st != QFFN_OK) return st;
   QFFN_ALIGNED(out); QFFN_ALIGNED(x); QFFN_ALIGNED(w); QFFN_ALIGNED4(offsets);
-  return from_cuda(M == 0 ? cudaSuccess : qffn::launch_few_groups(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, stream));
+  return from_cuda(qffn::launch_grouped(out, x, x_scale, w, w_scale, offsets, G, M, N, K, stream));
+}
+
+qffn_status qffn_grouped_linear_backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uint16_t* x,
+                                         const uint16_t* w, const int32_t* offsets, int64_t G, int64_t M, int64_t N,
+                                         int64_t K, int accumulate, qffn_stream_t stream) {
+  QFFN_RANGE();
+  QFFN_PTR(dw); QFFN_PTR_ROWS(M, dout); QFFN_PTR_ROWS(M, x); QFFN_PTR(w); QFFN_PTR(offsets);
+  qffn_status st = check_grouped_shape(G, M, N, K, 8);
+  if (st == QFFN_OK) st = check_linear_backward_shape(M, N, K);
+  if (st != QFFN_OK) return st;
+  QFFN_REQUIRE(product_fits(G * ((N + 255) / 256 * 256), K), QFFN_ERR_UNSUPPORTED_SHAPE);
+  QFFN_ALIGNED(dx); QFFN_ALIGNED(dw); QFFN_ALIGNED(dout); QFFN_ALIGNED(x); QFFN_ALIGNED(w); QFFN_ALIGNED4(offsets);
+  return from_cuda(qffn::launch_grouped_backward(dx, dw, dout, x, w, offsets, G, M, N, K, accumulate != 0, stream));
 }
 
 qffn_status qffn_gemv_dual(uint16_t* g, uint16_t* u, const uint16_t* x, const uint8_t* w_gate,

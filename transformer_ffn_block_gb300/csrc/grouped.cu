@@ -1,0 +1,952 @@
+// Products grouped by expert and block-scaled products on the 5th-generation tensor
+// cores (tcgen05, sm_103a), groups of rows with a matrix each:
+//
+//   KIND_ROWS     out[m,n]   = bf16(sum_k x[m,k] w_g[n,k] (+ bias[n]) (+ in[m,n])),  m in group g;
+//                 bf16, or E4M3 with a power-of-two scale per block of 128
+//   KIND_ROWS_MN  dx[m,k]    = bf16(sum_n dout[m,n] w_g[n,k]): w read where it lies
+//   KIND_WEIGHT   dw_g[n,k]  = bf16(sum_{m in g} dout[m,n] x[m,k] (+ dw_g[n,k]))
+//
+// The pipeline is that of linear.cu: SM pairs, persistent over units of work, one
+// warp loads by TMA into a ring of stages (128 bytes of K each), one thread issues
+// tcgen05.mma.cta_group::2, eight warps per CTA run the epilogue out of one of two
+// accumulators while the other fills.  What is new:
+//
+// - The sizes of the groups are on the device.  Every CTA reads the offsets once
+//   into a table of units in shared memory; the roles look their units up there.
+// - The weights are the 256-row operand and the rows of x the other (as in linear.cu's
+//   exchanged form), so that the width of a unit, 32 to 256 rows of x, follows the
+//   group: its rows are spread evenly over its tiles, and a group of a few rows costs
+//   its weights' bytes and no more.  The rows of x come in boxes of 128, 64, 32 and 16
+//   rows.
+// - The weight gradient's contraction runs over a group's rows, which end anywhere. The
+//   last stage of a unit may hold rows of the next group; a warp overwrites them with
+//   zeros in shared memory before the MMAs read the stage, in both operands, so that
+//   neither finite values nor NaN of a neighbour meet a group.
+// - E4M3: tcgen05.mma.kind::mxf8f6f4.block_scale takes E8M0 scales for every 32
+//   values of K from TMEM; a scale per 128 is the same byte in four MMAs.  Two warps
+//   read the scales of 512 of K at a time (one byte per row of x and block, one per
+//   128 weight rows and block), lay them out in shared memory, and the issuing thread
+//   copies them to TMEM (tcgen05.cp) in front of the MMAs that use them.  The tensor
+//   cores then scale for nothing; sums never leave TMEM.  TMEM holds two
+//   accumulators of 224 columns and the scales.
+//
+// Every mbarrier wait is bounded; see gemm_fp8.cu for how a wait that runs out
+// ends the kernel (abort flag, status word, drained copies and MMAs).
+#include <cuda.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "pipeline.cuh"
+#include "tensor_map.h"
+#include "umma.cuh"
+
+namespace qffn {
+namespace {
+
+constexpr int OP_BF16 = 0, OP_BLOCKS = 1;
+constexpr int KIND_ROWS = 0, KIND_ROWS_MN = 1, KIND_WEIGHT = 2;
+
+constexpr int BM = 128;                    // weight rows per CTA (256 per pair)
+constexpr int ROW_BYTES = 128;             // one swizzle atom row
+constexpr int OP_BYTES = 128 * ROW_BYTES;  // an operand's share of a stage: 128 rows of one swizzle row
+constexpr int MN_BOX_BYTES = 64 * ROW_BYTES;   // MN-major: 64 values by 64 of K, two boxes to the share
+constexpr int STEPS = 4;                   // MMAs per stage (32 bytes of K each)
+constexpr int EPI_WARPS = 8;
+constexpr int SCALE_WARPS = 2;
+constexpr int MAX_STAGES = 6;
+constexpr int SF_STAGES = 4;               // stages of scales, 512 of K each
+constexpr int SF_BYTES = 3 * 512;          // 128 weight rows, 256 rows of x: 4 bytes each
+constexpr int STAGING_BOX = 32 * 128;      // a warp's transposing box: 32 rows x 32 fp32
+constexpr int STAGING_BYTES = EPI_WARPS * STAGING_BOX;
+constexpr int NUM_BARS = 4 * MAX_STAGES + 5 + 2 * SF_STAGES;
+constexpr int SMEM_LIMIT = 227 * 1024 - 1024;  // (behind the alignment to 1024 bytes)
+constexpr int TMEM_COLS = 512;
+constexpr int GROUP_M = 8;
+constexpr uint16_t kBothCtas = 0x3;
+constexpr uint16_t kLeaderOnly = 0x1;
+constexpr unsigned long long kWaitLimitNs = 2000000000ull;
+constexpr unsigned long long kDrainLimitNs = 200000000ull;
+
+constexpr int stage_k(int op) { return op == OP_BF16 ? 64 : 128; }   // elements of K per stage
+constexpr int max_bn(int op) { return op == OP_BF16 ? 256 : 224; }   // columns of an accumulator
+constexpr int stage_bytes(int op) { return OP_BYTES + max_bn(op) / 2 * ROW_BYTES; }
+constexpr int num_threads(int op, int kind) {
+  return 32 * (2 + EPI_WARPS + (op == OP_BLOCKS ? SCALE_WARPS : kind == KIND_WEIGHT ? 1 : 0));
+}
+constexpr int fixed_bytes(int op) {
+  return STAGING_BYTES + (op == OP_BLOCKS ? SF_STAGES * SF_BYTES : 0) + NUM_BARS * 8 + 16;
+}
+constexpr int SF_TMEM = 448;               // first column of the scales: two slots of 16
+
+// Instruction descriptors.  kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 (bits 7-9,
+// 10-12 = 1); kind::mxf8f6f4: bits 4-5 / 29-30 which byte of the scales' words B / A
+// takes, A and B E4M3 (0), scales E8M0 (bit 23).  Both: bits 15 / 16 A / B MN-major,
+// N >> 3 at bits 17-22, M >> 4 at bits 24-28 (M = 256 over the pair).
+QFFN_DEVI uint32_t idesc_for(int op, bool a_mn, bool b_mn, int n) {
+  return (op == OP_BF16 ? (1u << 4) | (1u << 7) | (1u << 10) : 1u << 23) | (a_mn ? 1u << 15 : 0u) |
+         (b_mn ? 1u << 16 : 0u) | (uint32_t(n >> 3) << 17) | (uint32_t((2 * BM) >> 4) << 24);
+}
+
+__device__ unsigned int g_status;
+
+struct GroupArgs {
+  uint16_t* out;
+  const uint16_t* bias;     // ROWS, optional
+  const uint16_t* in;       // what is added: [M, N], or the previous dw; optional
+  const uint8_t* x_scale;   // E4M3: [M, blocks] and [G, n_blocks, blocks]
+  const uint8_t* w_scale;
+  int blocks, n_blocks;
+  const int* offsets;       // NULL: one group of all rows
+  int G, M;
+  int N;                    // values in a row of the output
+  int rows;                 // WEIGHT: rows of one matrix
+  int tiles_n;              // units of 256 across the output's row (WEIGHT: 256 across a matrix's rows times across its columns)
+  int tiles_k;              // WEIGHT: units of 256 across the columns
+  int bn_cap;               // ROWS: most rows of a unit, a multiple of 32
+  int band_n;               // ROWS: units across N that are swept together
+  int num_kb;               // ROWS: stages of K
+  int stages;
+};
+
+// D(tmem, both CTAs) (+)= A(smem, both CTAs) . B(smem, both CTAs)^T
+QFFN_DEVI void mma_pair_f16(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The same with E4M3 operands and the scales at TMEM columns sfa and sfb.
+QFFN_DEVI void mma_pair_blocks(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                               uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+// 32 rows of 16 bytes of each CTA's shared memory to four columns of its TMEM, for
+// all four lane quarters: the scales of 128 rows, row r in lane r % 32 and word r / 32.
+QFFN_DEVI void copy_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+// Descriptor of such rows: no swizzle, groups of eight rows 128 bytes apart.
+QFFN_DEVI uint64_t sdesc_scales(uint32_t saddr) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(16 >> 4) << 16) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
+}
+
+// Shared-memory descriptor of MMA step i of a stage's operand (see linear.cu).
+template <bool MN>
+QFFN_DEVI uint64_t step_desc(uint32_t base, int i) {
+  if (!MN) return sdesc_sw128(base + uint32_t(i) * 32u);
+  const uint64_t d = sdesc_sw128(base + uint32_t(i) * 16u * ROW_BYTES);
+  return (d & ~(uint64_t(0x3FFF) << 16)) | (uint64_t(MN_BOX_BYTES >> 4) << 16);
+}
+
+QFFN_DEVI bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, bool honour_abort = true,
+                         unsigned long long limit = kWaitLimitNs) {
+  return mbar_wait_bounded(bar, parity, abort_flag, &g_status, honour_abort, limit);
+}
+
+QFFN_DEVI uint32_t pack2(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+QFFN_DEVI uint4 pack8(const uint64_t (&v)[4]) { return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3])); }
+
+// The table of units in shared memory: off[0 .. G] the offsets within 0 .. M, first[0
+// .. G] the number of the first unit of each group (ROWS).
+struct Table {
+  const int* off;
+  const int* first;
+};
+struct Unit {
+  int group;
+  int begin, rows;    // the group's rows
+  int row0, bn;       // ROWS: first row of the unit, its width
+  int nb, kb;         // 256-wide unit of the output's row (WEIGHT: of the matrix's rows, columns)
+};
+
+QFFN_DEVI int group_rows(const Table& t, int g) { return max(t.off[g + 1] - t.off[g], 0); }
+
+// Unit u of KIND_ROWS; `g`: the group of the last unit that this thread looked up.
+QFFN_DEVI Unit rows_unit(int u, int& g, const Table& t, const GroupArgs& a) {
+  if (u >= t.first[g + 1]) {
+    int lo = g + 1, hi = a.G - 1;            // the last group whose first unit is u or before
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (t.first[mid] <= u) lo = mid;
+      else hi = mid - 1;
+    }
+    g = lo;
+  }
+  Unit r;
+  r.group = g;
+  r.begin = t.off[g];
+  r.rows = group_rows(t, g);
+  const int tm = r.rows <= a.bn_cap ? 1 : (r.rows + a.bn_cap - 1) / a.bn_cap;
+  r.bn = ((tm == 1 ? r.rows : (r.rows + tm - 1) / tm) + 31) & ~31;
+  // bands of band_n; within a band, groups of GROUP_M tiles of rows sweep its columns, odd
+  // groups backwards (see linear.cu)
+  int k = u - t.first[g], mt = 0;
+  if (tm == 1) {
+    r.nb = k;
+  } else {
+    const int band_tiles = tm * a.band_n;
+    const int band = k < band_tiles ? 0 : k / band_tiles;
+    const int n0 = band * a.band_n, wb = min(a.band_n, a.tiles_n - n0);
+    k -= band * band_tiles;
+    const int per_group = GROUP_M * wb;
+    const int sweep = k < per_group ? 0 : k / per_group;
+    const int size = min(tm - sweep * GROUP_M, GROUP_M);
+    k -= sweep * per_group;
+    const int col = k / size;
+    mt = sweep * GROUP_M + k - col * size;
+    r.nb = n0 + ((sweep & 1) ? wb - 1 - col : col);
+  }
+  r.row0 = r.begin + mt * r.bn;
+  r.kb = 0;
+  return r;
+}
+QFFN_DEVI Unit weight_unit(int u, const Table& t, const GroupArgs& a) {
+  Unit r;
+  r.group = u / a.tiles_n;
+  r.begin = t.off[r.group];
+  r.rows = group_rows(t, r.group);
+  const int k = u - r.group * a.tiles_n;
+  r.nb = k / a.tiles_k;
+  r.kb = k - r.nb * a.tiles_k;
+  r.row0 = 0;
+  r.bn = 256;
+  return r;
+}
+
+struct Maps {
+  CUtensorMap w;        // ROWS: the weights [G, rows, cols]; WEIGHT: dout
+  CUtensorMap x[4];     // ROWS: rows of x in boxes of 128, 64, 32, 16; WEIGHT: [0]: x
+};
+
+template <int OP, int KIND>
+__global__ void __launch_bounds__(num_threads(OP, KIND), 1)
+    grouped_kernel(const __grid_constant__ Maps maps, const GroupArgs args) {
+  constexpr bool WEIGHT = KIND == KIND_WEIGHT;
+  constexpr bool A_MN = KIND != KIND_ROWS, B_MN = WEIGHT;
+  constexpr int STAGE = stage_bytes(OP);
+  constexpr int ACC_COLS = max_bn(OP);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t ring = smem_u32(smem);
+  uint8_t* sStaging = smem + args.stages * STAGE;
+  uint8_t* sScales = sStaging + STAGING_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sScales + (OP == OP_BLOCKS ? SF_STAGES * SF_BYTES : 0));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* table_off = reinterpret_cast<int*>(tmem_slot + 4);
+  int* table_first = table_off + args.G + 1;
+  const Table table{table_off, table_first};
+  const uint32_t bar0 = smem_u32(bars);
+  // full[s] (leader): both CTAs' loads of stage s landed; empty[s]: the MMAs
+  // reading stage s are done; tfull[a]: accumulator a is complete; tempty[a]
+  // (leader): both CTAs' epilogue warps have read it; drain: all MMAs done;
+  // sfull[s] (leader): both CTAs' scales of stage s are written; sempty[s]: copied;
+  // WEIGHT, a stage with rows behind its group: tail[s]: this CTA's loads landed,
+  // cleared[s] (leader): both CTAs have cleared those rows
+  auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
+  auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(MAX_STAGES + s); };
+  auto tfull_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * MAX_STAGES + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * MAX_STAGES + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * uint32_t(2 * MAX_STAGES + 4);
+  auto sfull_bar = [&](int s) { return bar0 + 8u * uint32_t(2 * MAX_STAGES + 5 + s); };
+  auto tail_bar = [&](int s) { return bar0 + 8u * uint32_t(2 * MAX_STAGES + 5 + 2 * SF_STAGES + s); };
+  auto cleared_bar = [&](int s) { return bar0 + 8u * uint32_t(3 * MAX_STAGES + 5 + 2 * SF_STAGES + s); };
+  auto sempty_bar = [&](int s) { return bar0 + 8u * uint32_t(2 * MAX_STAGES + 5 + SF_STAGES + s); };
+
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = int(cluster_id_x()), num_pairs = int(num_clusters_x());
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < args.stages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull_bar(a), 1);
+      mbar_init(tempty_bar(a), 2 * EPI_WARPS);
+    }
+    mbar_init(drain_bar, 1);
+    if (OP == OP_BLOCKS)
+      for (int s = 0; s < SF_STAGES; ++s) {
+        mbar_init(sfull_bar(s), 2);
+        mbar_init(sempty_bar(s), 1);
+      }
+    if (WEIGHT)
+      for (int s = 0; s < args.stages; ++s) {
+        mbar_init(tail_bar(s), 1);
+        mbar_init(cleared_bar(s), 2);
+      }
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&maps.w);
+    tma_prefetch_desc(&maps.x[0]);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();              // nothing in global memory is touched before the preceding kernel is done
+  const uint16_t* const bias_row = behind_wait(args.bias);
+  pdl_trigger();
+  for (int i = threadIdx.x; i <= args.G; i += num_threads(OP, KIND))
+    table_off[i] = args.offsets != nullptr ? min(max(args.offsets[i], 0), args.M) : i == 0 ? 0 : args.M;
+  __syncthreads();
+  if (!WEIGHT && warp == 0) {
+    int total = 0;
+    for (int base = 0; base < args.G; base += 32) {
+      const int i = base + lane;
+      int n = i < args.G ? (group_rows(table, i) + args.bn_cap - 1) / args.bn_cap * args.tiles_n : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int below = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o) n += below;
+      }
+      if (i < args.G) table_first[i + 1] = total + n;
+      total += __shfl_sync(0xffffffffu, n, 31);
+    }
+    if (lane == 0) table_first[0] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();      // both CTAs' barriers exist before either signals the other's
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const int num_units = WEIGHT ? args.G * args.tiles_n : table_first[args.G];
+  int group_cursor = 0;
+  auto unit_at = [&](int u) { return WEIGHT ? weight_unit(u, table, args) : rows_unit(u, group_cursor, table, args); };
+  // the units of this pair in order; empty groups have none here (their dw is cleared at the end)
+  auto next_unit = [&](int u) {
+    u += num_pairs;
+    if (WEIGHT)
+      while (u < num_units && group_rows(table, u / args.tiles_n) == 0) u += num_pairs;
+    return u;
+  };
+  auto first_unit = [&]() { return next_unit(pair - num_pairs); };
+  // stages of K of a unit
+  auto stages_of = [&](const Unit& u) { return WEIGHT ? (u.rows + 63) / 64 : args.num_kb; };
+
+  if (warp == 0) {
+    if (elect_one()) {
+      // ------------------------------------------------------------ producer
+      uint32_t issued = 0, issued_parity = 0, ph = 0;
+      uint32_t tails = 0, tail_parity = 0;   // WEIGHT: stages whose tail barrier was armed, and its phase now
+      int s = 0;
+      bool ok = true;
+      for (int un = first_unit(); ok && un < num_units; un = next_unit(un)) {
+        const Unit u = unit_at(un);
+        const int row_w = u.nb * (2 * BM) + int(rank) * BM;      // of the 256-row operand
+        const int half = u.bn / 2;
+        const int row_x = WEIGHT ? u.kb * 256 + int(rank) * 128 : u.row0 + int(rank) * half;
+        const uint32_t stage_tx = 2u * uint32_t(OP_BYTES + half * ROW_BYTES);
+        const int num = stages_of(u);
+        for (int kb = 0; kb < num; ++kb) {
+          if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) { ok = false; break; }
+          const int k0 = kb * stage_k(OP);
+          // a stage with rows behind the group completes on this CTA's own barrier, for the
+          // warp that clears them
+          const bool tail = WEIGHT && k0 + 64 > u.rows;
+          if (rank == 0) {
+            if (tail) mbar_arrive(full_bar(s));
+            else mbar_expect_tx(full_bar(s), stage_tx);
+          }
+          if (tail) {
+            mbar_expect_tx(tail_bar(s), uint32_t(2 * OP_BYTES));
+            tails |= 1u << s;
+            tail_parity ^= 1u << s;
+          }
+          const uint32_t fb = tail ? map_to_rank(tail_bar(s), rank) : map_to_rank(full_bar(s), 0);
+          const uint32_t da = ring + uint32_t(s) * uint32_t(STAGE);
+          uint32_t db = da + uint32_t(OP_BYTES);
+          if (WEIGHT) {
+            const int row = u.begin + k0;
+            tma_load_2d_pair(da, &maps.w, fb, row_w, row);
+            tma_load_2d_pair(da + MN_BOX_BYTES, &maps.w, fb, row_w + 64, row);
+            tma_load_2d_pair(db, &maps.x[0], fb, row_x, row);
+            tma_load_2d_pair(db + MN_BOX_BYTES, &maps.x[0], fb, row_x + 64, row);
+          } else {
+            if (A_MN) {
+              tma_load_3d_pair(da, &maps.w, fb, row_w, k0, u.group);
+              tma_load_3d_pair(da + MN_BOX_BYTES, &maps.w, fb, row_w + 64, k0, u.group);
+            } else {
+              tma_load_3d_pair(da, &maps.w, fb, k0, row_w, u.group);
+            }
+            int row = row_x;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              if (half & (128 >> b)) {
+                tma_load_2d_pair(db, &maps.x[b], fb, k0, row);
+                db += uint32_t((128 >> b) * ROW_BYTES);
+                row += 128 >> b;
+              }
+            }
+          }
+          issued |= 1u << s;
+          issued_parity = (issued_parity & ~(1u << s)) | (ph << s);
+          if (++s == args.stages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // before shared memory is released every phase the leader armed completes, and
+      // the MMAs' last arrivals reach this CTA
+      for (int k = 0; k < args.stages; ++k)
+        if (issued & (1u << k)) {
+          if (WEIGHT && (tails & (1u << k)))
+            mbar_wait(tail_bar(k), ((tail_parity >> k) & 1u) ^ 1u, abort_flag, false, kDrainLimitNs);
+          if (rank == 0) mbar_wait(full_bar(k), (issued_parity >> k) & 1u, abort_flag, false, kDrainLimitNs);
+          mbar_wait(empty_bar(k), (issued_parity >> k) & 1u, abort_flag, false, kDrainLimitNs);
+        }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one()) {
+      // ------------------------------------------------------------ MMA issuer (leader)
+      int s = 0, local = 0, chunk = 0;
+      uint32_t ph = 0, cleared_parity = 0;
+      bool ok = true;
+      for (int un = first_unit(); ok && un < num_units; un = next_unit(un), ++local) {
+        const int acc = local & 1;
+        const uint32_t aph = uint32_t(local >> 1) & 1u;
+        if (!mbar_wait_cluster_bounded(tempty_bar(acc), aph ^ 1u, abort_flag, &g_status, kWaitLimitNs)) break;
+        tc_fence_after();
+        const Unit u = unit_at(un);
+        const uint32_t d_tmem = tmem_base + uint32_t(acc * ACC_COLS);
+        const uint32_t idesc = idesc_for(OP, A_MN, B_MN, u.bn);
+        const int num = stages_of(u);
+        uint32_t sf = 0;                     // TMEM columns of the current scales
+        bool ready = false;                  // the next stage was there before this one's MMAs were issued
+        for (int kb = 0; kb < num; ++kb) {
+          if (OP == OP_BLOCKS && (kb & 3) == 0) {
+            const int ss = chunk % SF_STAGES;
+            if (!mbar_wait_cluster_bounded(sfull_bar(ss), uint32_t(chunk / SF_STAGES) & 1u, abort_flag, &g_status, kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            sf = tmem_base + uint32_t(SF_TMEM + 16 * (chunk & 1));
+            const uint32_t src = smem_u32(sScales) + uint32_t(ss * SF_BYTES);
+            copy_scales(sf, sdesc_scales(src));
+            copy_scales(sf + 4, sdesc_scales(src + 512));
+            copy_scales(sf + 8, sdesc_scales(src + 1024));
+            mma_commit_mc(sempty_bar(ss), kBothCtas);
+            ++chunk;
+          }
+          if (!ready && !mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
+          if (WEIGHT && kb * 64 + 64 > u.rows) {
+            if (!mbar_wait_cluster_bounded(cleared_bar(s), (cleared_parity >> s) & 1u, abort_flag, &g_status, kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
+            cleared_parity ^= 1u << s;
+          }
+          tc_fence_after();
+          const uint32_t a0 = ring + uint32_t(s) * uint32_t(STAGE), b0 = a0 + uint32_t(OP_BYTES), empty = empty_bar(s);
+          if (++s == args.stages) {
+            s = 0;
+            ph ^= 1u;
+          }
+          ready = kb + 1 < num && mbar_test_wait(full_bar(s), ph);
+          if (OP == OP_BLOCKS) {
+            const uint32_t which = uint32_t(kb & 3);
+            const uint32_t id = idesc | (which << 4) | (which << 29);
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i)
+              mma_pair_blocks(d_tmem, step_desc<A_MN>(a0, i), step_desc<B_MN>(b0, i), id, sf, sf + 4, uint32_t(kb | i));
+          } else {
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i)
+              mma_pair_f16(d_tmem, step_desc<A_MN>(a0, i), step_desc<B_MN>(b0, i), idesc, uint32_t(kb | i));
+          }
+          mma_commit_mc(empty, kBothCtas);
+        }
+        if (!ok) break;
+        mma_commit_mc(tfull_bar(acc), kBothCtas);
+      }
+      mma_commit_mc(drain_bar, kLeaderOnly);
+      mbar_wait(drain_bar, 0, abort_flag, false, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else if (OP == OP_BLOCKS && warp >= 2 + EPI_WARPS) {
+    // -------------------------------------------------------------- scales
+    // Warp `mine` of the two takes every second chunk of 512 of K.  Lane l holds the
+    // words (four blocks' bytes) of rows l, l + 32, ... of x; this CTA's 128 weight rows
+    // have one word.  Blocks behind the last are never multiplied with.
+    const int mine = warp - (2 + EPI_WARPS);
+    const bool whole = (args.blocks & 3) == 0 && (reinterpret_cast<uintptr_t>(args.x_scale) & 3u) == 0;
+    int chunk = 0, waited = 0;
+    bool ok = true;
+    for (int un = first_unit(); ok && un < num_units; un = next_unit(un)) {
+      const Unit u = unit_at(un);
+      const int num = (args.num_kb + 3) / 4;
+      const int block_w = u.nb * 2 + int(rank);
+      const uint8_t* const ws = args.w_scale + (size_t(u.group) * size_t(args.n_blocks) + size_t(min(block_w, args.n_blocks - 1))) * size_t(args.blocks);
+      const int per_lane = u.bn / 32;
+      for (int c = 0; c < num; ++c, ++chunk) {
+        if ((chunk & 1) != mine) continue;
+        const int left = args.blocks - 4 * c;
+        uint32_t word_w = 0u, word_x[8];
+        for (int j = 0; j < 4; ++j)
+          if (j < left) word_w |= uint32_t(ws[4 * c + j]) << (8 * j);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          word_x[i] = 0u;
+          if (i < per_lane) {
+            const int row = min(u.row0 + 32 * i + lane, args.M - 1);
+            const uint8_t* const p = args.x_scale + size_t(row) * size_t(args.blocks) + size_t(4 * c);
+            if (whole) {
+              word_x[i] = *reinterpret_cast<const uint32_t*>(p);
+            } else {
+              for (int j = 0; j < 4; ++j)
+                if (j < left) word_x[i] |= uint32_t(p[j]) << (8 * j);
+            }
+          }
+        }
+        const int ss = chunk % SF_STAGES;
+        ok = __all_sync(0xffffffffu, mbar_wait(sempty_bar(ss), (uint32_t(chunk / SF_STAGES) & 1u) ^ 1u, abort_flag));
+        if (!ok) break;
+        const uint32_t dst = smem_u32(sScales) + uint32_t(ss * SF_BYTES + lane * 16);
+        sts16(dst, make_uint4(word_w, word_w, word_w, word_w));
+        sts16(dst + 512, make_uint4(word_x[0], word_x[1], word_x[2], word_x[3]));
+        sts16(dst + 1024, make_uint4(word_x[4], word_x[5], word_x[6], word_x[7]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(map_to_rank(sfull_bar(ss), 0));
+        waited = chunk + 1;
+      }
+    }
+    // the issuer's last arrivals on the stages that this warp filled reach this CTA
+    for (int c = max(0, waited - SF_STAGES); ok && c < waited; ++c)
+      if ((c & 1) == mine)
+        mbar_wait(sempty_bar(c % SF_STAGES), uint32_t(c / SF_STAGES) & 1u, abort_flag, false, kDrainLimitNs);
+    __syncwarp();
+  } else if (WEIGHT && warp >= 2 + EPI_WARPS) {
+    // -------------------------------------------------------------- rows behind a group
+    // The last stage of a unit: rows behind the group's end are overwritten with zeros in
+    // the four boxes of this CTA's operands (row r of a box is its bytes 128 r ..).
+    uint32_t parity = 0;
+    int s = 0;
+    for (int un = first_unit(); un < num_units; un = next_unit(un)) {
+      const Unit u = unit_at(un);
+      const int num = stages_of(u), live = u.rows - (num - 1) * 64;
+      s = (s + num - 1) % args.stages;
+      if (live < 64) {
+        if (!__all_sync(0xffffffffu, mbar_wait(tail_bar(s), (parity >> s) & 1u, abort_flag))) break;
+        parity ^= 1u << s;
+        const uint32_t at = ring + uint32_t(s) * uint32_t(STAGE);
+        for (int b = 0; b < 4; ++b)
+          for (int i = live * ROW_BYTES + lane * 16; i < MN_BOX_BYTES; i += 512)
+            sts16(at + uint32_t(b * MN_BOX_BYTES + i), make_uint4(0, 0, 0, 0));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(map_to_rank(cleared_bar(s), 0));
+      }
+      s = s + 1 == args.stages ? 0 : s + 1;
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- epilogue
+    // Two warps per TMEM lane quarter q (32 rows of the 256-row operand), which share
+    // the unit's columns.  A box of shared memory turns the accumulator's layout into
+    // that of the global accesses, 16 bytes per lane (see linear.cu).
+    constexpr int WG = EPI_WARPS / 4;
+    const int q = warp & 3, wg = (warp - 2) >> 2;
+    const uint32_t box = smem_u32(sStaging + (q * WG + wg) * STAGING_BOX);
+    int local = 0;
+    int un = first_unit(), next = un < num_units ? next_unit(un) : un;
+    if (!WEIGHT) {
+      // the lane is a column of the output, the accumulator's columns its rows, 32 at a time
+      const int sub = lane >> 2, ch = lane & 3;
+      const uint32_t col32 = box + uint32_t(lane) * 4u;
+      const uint32_t turn32 = box + uint32_t(sub) * 128u + (uint32_t((2 * ch) ^ sub) << 4);
+      const size_t step = size_t(8) * size_t(args.N);
+      for (; un < num_units; ++local) {
+        const int acc = local & 1;
+        const uint32_t aph = uint32_t(local >> 1) & 1u;
+        const Unit u = unit_at(un);
+        const int row_end = min(u.begin + u.rows, u.row0 + u.bn);
+        const int col = u.nb * (2 * BM) + int(rank) * BM + q * 32 + ch * 8;
+        const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * ACC_COLS);
+        const int groups = u.bn / 32;
+        const int share = (groups + WG - 1) / WG, g0 = wg * share, g1 = min(groups, g0 + share);
+        const size_t at = size_t(u.row0 + sub) * size_t(args.N) + size_t(col);
+        auto live_rows = [&](int g) {
+          uint32_t v = 0u;
+          if (col < args.N) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v |= (u.row0 + g * 32 + sub + 8 * i < row_end ? 1u : 0u) << i;
+          }
+          return v;
+        };
+        uint64_t bias[4] = {0ull, 0ull, 0ull, 0ull};
+        if (args.bias != nullptr && col < args.N) {
+          const uint4 b = ld16_settled(bias_row + col);
+          bias[0] = bf16x2_to_f2(b.x);
+          bias[1] = bf16x2_to_f2(b.y);
+          bias[2] = bf16x2_to_f2(b.z);
+          bias[3] = bf16x2_to_f2(b.w);
+        }
+        uint4 next_in[4];                    // what is added, requested a group ahead
+        auto request = [&](int g) {
+          const uint32_t live = g < g1 ? live_rows(g) : 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            next_in[i] = make_uint4(0, 0, 0, 0);
+            if ((live >> i) & 1u) next_in[i] = ld16_stream(args.in + (at + size_t(4 * g + i) * step));
+          }
+        };
+        if (args.in != nullptr) request(g0);
+        if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) break;
+        tc_fence_after();
+        const int next2 = next < num_units ? next_unit(next) : next;
+        const bool awaited = next < num_units && next2 < num_units;   // another unit takes this accumulator
+        auto loaded = [&](int g) {
+          if (g + 1 >= g1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && awaited) mbar_arrive_remote_relaxed(map_to_rank(tempty_bar(acc), 0));
+          }
+        };
+        if (g0 >= g1) loaded(g0);            // (a unit with fewer groups than warps)
+        for (int g = g0; g < g1; ++g) {
+          const uint32_t live = live_rows(g);
+          uint32_t v[32];
+          tmem_ld32(tbase + uint32_t(g * 32), v);
+          loaded(g);
+          uint4 in4[4];
+          if (args.in != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) in4[i] = next_in[i];
+            request(g + 1);
+          }
+          __syncwarp();                      // the previous group has been read out of the box
+#pragma unroll
+          for (int c = 0; c < 32; ++c) sts4((col32 ^ uint32_t(16 * (c & 7))) + uint32_t(128 * c), v[c]);
+          __syncwarp();
+          uint4 los[4], his[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            los[i] = lds16(turn32 + 1024u * i);
+            his[i] = lds16((turn32 ^ 16u) + 1024u * i);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint64_t z[4] = {f2_pack(__uint_as_float(los[i].x), __uint_as_float(los[i].y)),
+                             f2_pack(__uint_as_float(los[i].z), __uint_as_float(los[i].w)),
+                             f2_pack(__uint_as_float(his[i].x), __uint_as_float(his[i].y)),
+                             f2_pack(__uint_as_float(his[i].z), __uint_as_float(his[i].w))};
+            if (args.bias != nullptr) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bias[j]);
+            }
+            if (args.in != nullptr) {
+              const uint32_t iw[4] = {in4[i].x, in4[i].y, in4[i].z, in4[i].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bf16x2_to_f2(iw[j]));
+            }
+            if ((live >> i) & 1u) stg16(args.out + (at + size_t(4 * g + i) * step), pack8(z));
+          }
+        }
+        un = next;
+        next = next2;
+      }
+    } else {
+      // dw (+)= the sums: the lane is a row of the matrix; 64 columns at a time through a box
+      // of 32 rows x 128 bytes (chunk c of row r at c ^ (r & 7)), whole 128-byte lines
+      const int sub8 = lane >> 3, ch8 = lane & 7;
+      const uint32_t row32 = box + uint32_t(lane) * 128u + (uint32_t(lane & 7) << 4);
+      const uint32_t turn8 = box + uint32_t(sub8) * 128u + (uint32_t(ch8 ^ sub8) << 4);
+      const size_t step4 = size_t(4) * size_t(args.N);
+      struct Part {
+        int col;                             // column of this lane's share of the first 64
+        uint32_t rows;                       // bit i: row sub8 + 4 i exists
+        size_t at;
+      };
+      auto part_of = [&](const Unit& u) {
+        Part p;
+        const int row0 = u.nb * (2 * BM) + int(rank) * BM + q * 32;
+        p.col = u.kb * 256 + ch8 * 8;
+        p.rows = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p.rows |= (row0 + sub8 + 4 * i < args.rows ? 1u : 0u) << i;
+        p.at = (size_t(u.group) * size_t(args.rows) + size_t(row0 + sub8)) * size_t(args.N) + size_t(p.col);
+        return p;
+      };
+      uint4 in8[2][8];
+      auto request = [&](const Part& p, int k, uint4 (&d)[8]) {
+        const int g = wg + k * WG;
+        const uint32_t live = p.col + g * 64 < args.N ? p.rows : 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          d[i] = make_uint4(0, 0, 0, 0);
+          if ((live >> i) & 1u) d[i] = ld16_stream(args.in + (p.at + size_t(g * 64) + size_t(i) * step4));
+        }
+      };
+      Part p = part_of(weight_unit(min(un, num_units - 1), table, args));
+      if (args.in != nullptr && un < num_units) {
+        request(p, 0, in8[0]);
+        request(p, 1, in8[1]);
+      }
+      for (; un < num_units; ++local) {
+        const int acc = local & 1;
+        const uint32_t aph = uint32_t(local >> 1) & 1u;
+        const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * ACC_COLS);
+        const int next2 = next < num_units ? next_unit(next) : next;
+        const bool awaited = next < num_units && next2 < num_units;
+        const Part p_next = part_of(weight_unit(next < num_units ? next : un, table, args));
+        if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {        // four groups of 64 columns, two of them this warp's
+          const int g = wg + k * WG;
+          __syncwarp();                      // the previous group has been read out of the box
+          if (args.in != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sts16((turn8 ^ uint32_t((i & 1) << 6)) + 512u * i, in8[k][i]);
+            __syncwarp();
+            if (next < num_units) request(p_next, k, in8[k]);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t v[32];
+            tmem_ld32(tbase + uint32_t(g * 64 + h * 32), v);
+            if (h == 1 && k == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0 && awaited) mbar_arrive_remote_relaxed(map_to_rank(tempty_bar(acc), 0));
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t addr = row32 ^ uint32_t(16 * (4 * h + c));
+              uint64_t z[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                z[j] = f2_pack(__uint_as_float(v[8 * c + 2 * j]), __uint_as_float(v[8 * c + 2 * j + 1]));
+              if (args.in != nullptr) {
+                const uint4 d = lds16(addr);
+                const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bf16x2_to_f2(dw[j]));
+              }
+              sts16(addr, pack8(z));
+            }
+          }
+          __syncwarp();
+          const uint32_t live = p.col + g * 64 < args.N ? p.rows : 0u;
+          uint16_t* const dst = args.out + (p.at + size_t(g * 64));
+          uint4 o[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = lds16((turn8 ^ uint32_t((i & 1) << 6)) + 512u * i);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if ((live >> i) & 1u) stg16(dst + size_t(i) * step4, o[i]);
+        }
+        un = next;
+        next = next2;
+        p = p_next;
+      }
+      // the gradient of a matrix without rows is zero, or what it was when adding
+      if (args.in == nullptr)
+        for (int e = pair; e < num_units; e += num_pairs) {
+          if (group_rows(table, e / args.tiles_n) != 0) continue;
+          const Part z = part_of(weight_unit(e, table, args));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int g = wg + k * WG;
+            const uint32_t live = z.col + g * 64 < args.N ? z.rows : 0u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if ((live >> i) & 1u) stg16(args.out + (z.at + size_t(g * 64) + size_t(i) * step4), make_uint4(0, 0, 0, 0));
+          }
+        }
+    }
+  }
+
+  // Both CTAs finish together: the leader's MMAs write the peer's TMEM and
+  // both CTAs signal barriers of the other.  (Every arrival and copy that the other
+  // CTA makes here has been waited for, so the barrier orders no memory.)
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_relaxed();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TMEM_COLS)
+                 : "memory");
+  }
+}
+
+// ------------------------------------------------------------------ host side
+// 2-CTA clusters of a form that fit on the device at once (cached per device).
+template <int OP, int KIND>
+cudaError_t max_pairs(int* pairs) {
+  static int cached[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && cached[dev] > 0) {
+    *pairs = cached[dev];
+    return cudaSuccess;
+  }
+  const auto fn = grouped_kernel<OP, KIND>;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT + 1024);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (num_sms() / 2));
+  cfg.blockDim = dim3(num_threads(OP, KIND));
+  cfg.dynamicSmemBytes = SMEM_LIMIT + 1024;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+  if (e != cudaSuccess) return e;
+  if (n < 1) return cudaErrorInvalidConfiguration;
+  if (dev >= 0 && dev < 64) cached[dev] = n;
+  *pairs = n;
+  return cudaSuccess;
+}
+
+// `units`: no fewer than the kernel will find
+template <int OP, int KIND>
+cudaError_t launch(const Maps& m, GroupArgs a, int64_t units, cudaStream_t s) {
+  const int table = 8 * (a.G + 1);
+  a.stages = (SMEM_LIMIT - fixed_bytes(OP) - table) / stage_bytes(OP);
+  if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
+  int pairs = 0;
+  const cudaError_t e = max_pairs<OP, KIND>(&pairs);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * unsigned(units < pairs ? units : pairs));
+  cfg.blockDim = dim3(num_threads(OP, KIND));
+  cfg.dynamicSmemBytes = size_t(a.stages * stage_bytes(OP) + fixed_bytes(OP) + table + 1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, grouped_kernel<OP, KIND>, m, a);
+}
+
+int ceil_div(int64_t a, int64_t b) { return int((a + b - 1) / b); }
+
+// out [M, N] from x [M, K] and w [G, N, K] (KIND_ROWS) or [G, K, N] (KIND_ROWS_MN).
+template <int OP, int KIND>
+cudaError_t rows_product(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w, const uint8_t* w_scale,
+                         const uint16_t* bias, const uint16_t* in, const int* offsets, int64_t G, int64_t M, int64_t N,
+                         int64_t K, cudaStream_t s) {
+  constexpr bool BF16 = OP == OP_BF16;
+  const int64_t bytes = BF16 ? 2 : 1;
+  Maps m;
+  const bool ok_w = KIND == KIND_ROWS_MN ? make_operand_map_3d(&m.w, w, BF16, G, K, N, N * bytes, K * N * bytes, 64)
+                                         : make_operand_map_3d(&m.w, w, BF16, G, N, K, K * bytes, K * N * bytes, 128);
+  if (!ok_w) return cudaErrorInvalidValue;
+  for (int b = 0; b < 4; ++b)
+    if (!make_operand_map(&m.x[b], x, BF16, M, K, 128 >> b)) return cudaErrorInvalidValue;
+  GroupArgs a{};
+  a.out = out;
+  a.bias = bias;
+  a.in = in;
+  a.x_scale = x_scale;
+  a.w_scale = w_scale;
+  a.blocks = ceil_div(K, 128);
+  a.n_blocks = ceil_div(N, 128);
+  a.offsets = offsets;
+  a.G = int(G);
+  a.M = int(M);
+  a.N = int(N);
+  a.tiles_n = ceil_div(N, 2 * BM);
+  a.bn_cap = max_bn(OP);
+  a.num_kb = ceil_div(K, stage_k(OP));
+  // bands of about 32 MB of weights where they are the larger operand (see linear.cu)
+  const int64_t band = (int64_t(32) << 20) / (2 * BM * K * bytes);
+  a.band_n = N <= M / G || band >= a.tiles_n ? a.tiles_n : band < 1 ? 1 : int(band);
+  const int64_t units = (M / a.bn_cap + (G < M ? G : M)) * a.tiles_n;
+  return launch<OP, KIND>(m, a, units, s);
+}
+
+// dw [G, N, K] (+)= dout [M, N]^T . x [M, K] by group.
+cudaError_t weight_product(uint16_t* dw, const uint16_t* dout, const uint16_t* x, const int* offsets, int64_t G,
+                           int64_t M, int64_t N, int64_t K, bool accumulate, cudaStream_t s) {
+  Maps m;
+  if (!make_operand_map(&m.w, dout, true, M, N, 64) || !make_operand_map(&m.x[0], x, true, M, K, 64))
+    return cudaErrorInvalidValue;
+  m.x[1] = m.x[2] = m.x[3] = m.x[0];
+  GroupArgs a{};
+  a.out = dw;
+  a.in = accumulate ? dw : nullptr;
+  a.offsets = offsets;
+  a.G = int(G);
+  a.M = int(M);
+  a.N = int(K);
+  a.rows = int(N);
+  a.tiles_k = ceil_div(K, 256);
+  a.tiles_n = ceil_div(N, 256) * a.tiles_k;
+  a.bn_cap = 256;
+  return launch<OP_BF16, KIND_WEIGHT>(m, a, int64_t(a.tiles_n) * G, s);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
+                                 const uint8_t* w_scale, const uint16_t* bias, const uint16_t* res, int64_t M, int64_t N,
+                                 int64_t K, cudaStream_t s) {
+  if (M == 0) return cudaSuccess;
+  if (M <= 32) return launch_few_groups(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
+  return rows_product<OP_BLOCKS, KIND_ROWS>(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
+}
+
+cudaError_t launch_grouped(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w, const uint8_t* w_scale,
+                           const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K, cudaStream_t s) {
+  if (M == 0) return cudaSuccess;
+  if (M <= 32) return launch_few_groups(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, s);
+  if (x_scale != nullptr)
+    return rows_product<OP_BLOCKS, KIND_ROWS>(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, s);
+  return rows_product<OP_BF16, KIND_ROWS>(out, x, nullptr, w, nullptr, nullptr, nullptr, offsets, G, M, N, K, s);
+}
+
+cudaError_t launch_grouped_backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uint16_t* x,
+                                    const uint16_t* w, const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K,
+                                    bool accumulate, cudaStream_t s) {
+  if (M == 0) return accumulate ? cudaSuccess : cudaMemsetAsync(dw, 0, size_t(G) * size_t(N) * size_t(K) * 2, s);
+  if (dx != nullptr) {
+    const cudaError_t e =
+        rows_product<OP_BF16, KIND_ROWS_MN>(dx, dout, nullptr, w, nullptr, nullptr, nullptr, offsets, G, M, K, N, s);
+    if (e != cudaSuccess) return e;
+  }
+  return weight_product(dw, dout, x, offsets, G, M, N, K, accumulate, s);
+}
+
+cudaError_t grouped_take_status(unsigned int* status) {
+  unsigned int v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_status, sizeof(v));
+  if (e != cudaSuccess) return e;
+  if (v != 0) e = cudaMemcpyToSymbol(g_status, &zero, sizeof(zero));
+  *status = v;
+  return e;
+}
+
+}  // namespace qffn

@@ -207,6 +207,18 @@ cudaError_t launch_few_groups(uint16_t* out, const void* x, const uint8_t* x_sca
                               const uint8_t* w_scale, const uint16_t* bias, const uint16_t* res, const int* offsets,
                               int64_t G, int64_t M, int64_t N, int64_t K, cudaStream_t s);
 
+// Any number of rows (grouped.cu), which takes the form above where that is the faster:
+cudaError_t launch_linear_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
+                                 const uint8_t* w_scale, const uint16_t* bias, const uint16_t* res, int64_t M, int64_t N,
+                                 int64_t K, cudaStream_t s);
+cudaError_t launch_grouped(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w, const uint8_t* w_scale,
+                           const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K, cudaStream_t s);
+cudaError_t launch_grouped_backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uint16_t* x,
+                                    const uint16_t* w, const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K,
+                                    bool accumulate, cudaStream_t s);
+// Reads and clears the grouped kernels' device status word of the current device.
+cudaError_t grouped_take_status(unsigned int* status);
+
 // Reads and clears the decode kernels' device status word of the current device.
 cudaError_t decode_take_status(unsigned int* status);
 

@@ -36,4 +36,20 @@ inline bool make_operand_map(CUtensorMap* map, const void* ptr, bool bf16, int64
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same for a stack of matrices [count, rows, cols] or any two outer dimensions
+// with strides of their own (bytes): boxes of box_rows rows x 128 bytes of one
+// matrix, zeros outside its rows.
+inline bool make_operand_map_3d(CUtensorMap* map, const void* ptr, bool bf16, int64_t count, int64_t rows, int64_t cols,
+                                int64_t row_stride, int64_t matrix_stride, int box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(count)};
+  cuuint64_t strides[2] = {cuuint64_t(row_stride), cuuint64_t(matrix_stride)};
+  cuuint32_t box[3] = {cuuint32_t(bf16 ? 64 : 128), cuuint32_t(box_rows), 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace qffn
