@@ -14,6 +14,7 @@
 //
 // All are bound by HBM.  A lane holds 8 values (16-byte loads, 8-byte stores of
 // codes), so 16 lanes hold a block and four shuffles give its abs-max.
+#include "act.cuh"
 #include "common.cuh"
 #include "launch.h"
 
@@ -39,87 +40,95 @@ QFFN_DEVI uint32_t scale_code(uint32_t amax) {
 // 2^(127 - c); NaN for 255 (whose codes are all NaN)
 QFFN_DEVI float code_inverse(uint32_t c) { return __uint_as_float(c == 255u ? 0x7FC00000u : (254u - c) << 23); }
 
-QFFN_DEVI uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-QFFN_DEVI uint32_t amax8(const float (&v)[8]) {
-  uint32_t m = abs_bits(v[0]);
-#pragma unroll
-  for (int j = 1; j < 8; ++j) m = max(m, abs_bits(v[j]));
-  return m;
+// Eight values as four pairs.
+using Eight = uint64_t[4];
+
+// max(m, |a|, |b|), NaN if one is
+QFFN_DEVI float max_abs(float m, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
 }
-QFFN_DEVI uint2 codes8(const float (&v)[8], float inv) {
-  uint32_t p[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) p[j] = f32x2_to_e4m3x2(v[2 * j] * inv, v[2 * j + 1] * inv);
-  return make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
-}
-QFFN_DEVI void unpack8(uint4 w, float (&v)[8]) {
-  const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+// Abs-max of the eight, as bits.
+QFFN_DEVI uint32_t amax8(const Eight& v) {
+  float m = 0.0f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    v[2 * j] = bf16_lo(a[j]);
-    v[2 * j + 1] = bf16_hi(a[j]);
+    float a, b;
+    f2_unpack(v[j], a, b);
+    m = max_abs(m, a, b);
   }
+  return __float_as_uint(m);
 }
-QFFN_DEVI uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+QFFN_DEVI uint2 codes8(const Eight& v, float inv) {
+  uint32_t p[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a, b;
+    f2_unpack(f2_mul(v[j], f2_dup(inv)), a, b);
+    p[j] = f32x2_to_e4m3x2(a, b);
+  }
+  return make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
 }
+QFFN_DEVI void unpack8(uint4 w, Eight& v) {
+  v[0] = bf16x2_to_f2(w.x);
+  v[1] = bf16x2_to_f2(w.y);
+  v[2] = bf16x2_to_f2(w.z);
+  v[3] = bf16x2_to_f2(w.w);
+}
+QFFN_DEVI uint32_t pack2(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return pack_bf16x2(a, b);
+}
+QFFN_DEVI uint4 pack8(const Eight& v) { return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3])); }
 QFFN_DEVI void stg8(void* p, uint2 v) { *reinterpret_cast<uint2*>(p) = v; }
 
 // ------------------------------------------------------------------ rows, and SwiGLU
 // Chunks of 8 values, a row padded to whole blocks of 16 chunks, so that the 16
-// lanes of a block are in one half warp; each thread strides over all of them,
-// kFlight at a time.  Row and column advance by addition: one division per thread.
+// lanes of a block are in one half warp; a thread takes kFlight of them, all loads in
+// flight at once.  The row of a chunk is a product with `magic` = floor(2^64 / chunks per
+// row) + 1: exact for fewer than 2^44 chunks, as the divisor is at most 2^17.
 constexpr int kFlight = 4;
 template <bool SWIGLU>
-__global__ void __launch_bounds__(kThreads) rows_kernel(uint16_t* h, uint8_t* q, uint8_t* scale, const uint16_t* in,
-                                                        int64_t rows, int64_t cols) {
-  const int64_t blocks = (cols + 127) >> 7, per_row = blocks * 16, chunks = cols >> 3;
-  const int64_t stride = int64_t(gridDim.x) * kThreads;
-  const int64_t at = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  int64_t row = at / per_row, c = at - row * per_row;
-  const int64_t drow = stride / per_row, dc = stride - drow * per_row;
+__global__ void __launch_bounds__(kThreads, SWIGLU ? 4 : 6) rows_kernel(uint16_t* h, uint8_t* q, uint8_t* scale,
+                                                                        const uint16_t* in, int64_t rows, int64_t cols,
+                                                                        uint64_t magic) {
+  const int64_t blocks = (cols + 127) >> 7;
+  const int per_row = int(blocks) * 16, chunks = int(cols >> 3);
+  const uint64_t at = uint64_t(blockIdx.x) * (kThreads * kFlight) + threadIdx.x;
   pdl_wait();
   pdl_trigger();
-  // (the two halves of a warp may be at different rows, but leave together: a row
-  // beyond the last is computed as zeros and not stored)
-  while (__any_sync(0xffffffffu, row < rows)) {
-    uint4 a[kFlight], b[kFlight];
-    int64_t rr[kFlight], cc[kFlight];
+  uint4 a[kFlight], b[kFlight];
 #pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
-      rr[k] = row;
-      cc[k] = c;
-      a[k] = b[k] = make_uint4(0, 0, 0, 0);
-      if (row < rows && c < chunks) {
-        const uint16_t* p = in + (SWIGLU ? 2 * row : row) * cols + c * 8;
-        a[k] = ld16_stream(p);
-        if (SWIGLU) b[k] = ld16_stream(p + cols);
-      }
-      row += drow;
-      c += dc;
-      if (c >= per_row) {
-        c -= per_row;
-        ++row;
-      }
+  for (int k = 0; k < kFlight; ++k) {
+    const int64_t row = int64_t(__umul64hi(at + k * kThreads, magic));
+    const int c = int(at + k * kThreads - uint64_t(row) * uint64_t(per_row));
+    a[k] = b[k] = make_uint4(0, 0, 0, 0);
+    if (row < rows && c < chunks) {
+      const uint16_t* p = in + (SWIGLU ? 2 * row : row) * cols + c * 8;
+      a[k] = ld16_stream(p);
+      if (SWIGLU) b[k] = ld16_stream(p + cols);
     }
+  }
 #pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
-      float v[8];
-      unpack8(a[k], v);
-      if (SWIGLU) {
-        float u[8];
-        unpack8(b[k], u);
+  for (int k = 0; k < kFlight; ++k) {
+    Eight v;
+    unpack8(a[k], v);
+    if (SWIGLU) {
+      Eight u;
+      unpack8(b[k], u);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = silu_mul_f32(v[j], u[j]);
-      }
-      const uint32_t code = scale_code(max16(amax8(v)));
-      if (rr[k] >= rows) continue;
-      if (cc[k] < chunks) {
-        const int64_t o = rr[k] * cols + cc[k] * 8;
-        stg8(q + o, codes8(v, code_inverse(code)));
-        if (SWIGLU && h != nullptr) stg16(h + o, pack8(v));
-      }
-      if ((threadIdx.x & 15) == 0) scale[rr[k] * blocks + (cc[k] >> 4)] = uint8_t(code);
+      for (int j = 0; j < 4; ++j) v[j] = f2_mul(act_f2<ACT_SILU>(v[j]), u[j]);
+    }
+    const uint32_t code = scale_code(max16(amax8(v)));
+    const int64_t row = int64_t(__umul64hi(at + k * kThreads, magic));
+    const int c = int(at + k * kThreads - uint64_t(row) * uint64_t(per_row));
+    if (row < rows && c < chunks) {
+      const int64_t o = row * cols + c * 8;
+      stg8(q + o, codes8(v, code_inverse(code)));
+      if (SWIGLU && h != nullptr) stg16(h + o, pack8(v));
+      if ((c & 15) == 0) scale[row * blocks + (c >> 4)] = uint8_t(code);
     }
   }
 }
@@ -127,85 +136,116 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(uint16_t* h, uint8_t* q,
 // ------------------------------------------------------------------ RMS norm
 // TPR threads per row, which keep the row's V chunks of 8 values in registers
 // between the sum of squares and the quantisation; rows of up to 1024 values take a
-// warp each and no barrier.
-template <int TPR, int V>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) rmsnorm_blocks_kernel(
+// warp each and no barrier.  Short rows go R at a time, so that a thread has about
+// four loads in flight.
+// FEW: the gain is requested with the row, for calls of few rows, which wait once; else
+// after the sums, from L1, which leaves registers for more rows at a time.
+template <int V, bool FEW>
+constexpr int rows_at_once() { return FEW || V > 2 ? 1 : V == 2 ? 2 : 4; }
+
+template <int TPR, int V, bool FEW>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (FEW || V <= 2 ? 1024 : 1280) / (TPR < 128 ? 128 : TPR)) rmsnorm_blocks_kernel(
     uint16_t* res_out, uint16_t* y, uint8_t* q, uint8_t* scale, float* rstd, const uint16_t* res_in,
-    const uint16_t* x, const uint16_t* gain, float eps, int64_t N, int C) {
-  constexpr int ROWS = TPR < 128 ? 128 / TPR : 1;
-  __shared__ float red[TPR / 32];
+    const uint16_t* x, const uint16_t* gain, float eps, int64_t N, int C, float inv_c) {
+  constexpr int TEAMS = TPR < 128 ? 128 / TPR : 1, R = rows_at_once<V, FEW>();
+  __shared__ float red[R][TPR / 32];
   const int tid = threadIdx.x % TPR;
-  const int64_t row = int64_t(blockIdx.x) * ROWS + threadIdx.x / TPR;
+  const int64_t row0 = (int64_t(blockIdx.x) * TEAMS + threadIdx.x / TPR) * R;
   const int chunks = C >> 3, blocks = (C + 127) >> 7;
-  const bool live = row < N;
-  const size_t base = size_t(row) * size_t(C);
   pdl_wait();
   const uint16_t* const gains = behind_wait(gain);
   pdl_trigger();
-  uint4 r[V], g[V];
-  float ss = 0.0f;
+  uint4 r[R][V], g[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = tid + i * TPR;
-    r[i] = g[i] = make_uint4(0, 0, 0, 0);
-    if (live && c < chunks) {
-      r[i] = ld16_stream(x + base + size_t(c) * 8);
-      g[i] = ld16_settled(gains + size_t(c) * 8);
+  for (int k = 0; k < R; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = tid + i * TPR;
+      r[k][i] = make_uint4(0, 0, 0, 0);
+      if (row0 + k < N && c < chunks) r[k][i] = ld16_stream(x + size_t(row0 + k) * size_t(C) + size_t(c) * 8);
+      if (k == 0) {
+        g[i] = make_uint4(0, 0, 0, 0);
+        if (FEW && c < chunks) g[i] = ld16_settled(gains + size_t(c) * 8);
+      }
     }
-  }
   if (res_in != nullptr) {
-    uint4 a[V];
+    uint4 a[R][V];
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = tid + i * TPR;
+        a[k][i] = make_uint4(0, 0, 0, 0);
+        if (row0 + k < N && c < chunks) a[k][i] = ld16_stream(res_in + size_t(row0 + k) * size_t(C) + size_t(c) * 8);
+      }
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = tid + i * TPR;
+        Eight s, t;
+        unpack8(a[k][i], s);
+        unpack8(r[k][i], t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[j] = f2_add(s[j], t[j]);
+        r[k][i] = pack8(s);
+        if (row0 + k < N && c < chunks) stg16(res_out + size_t(row0 + k) * size_t(C) + size_t(c) * 8, r[k][i]);
+      }
+  }
+  float ss[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    uint64_t squares[2] = {0ull, 0ull};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = tid + i * TPR;
-      a[i] = make_uint4(0, 0, 0, 0);
-      if (live && c < chunks) a[i] = ld16_stream(res_in + base + size_t(c) * 8);
+      Eight v;
+      unpack8(r[k][i], v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) squares[j & 1] = f2_fma(v[j], v[j], squares[j & 1]);
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = tid + i * TPR;
-      float s[8], t[8];
-      unpack8(a[i], s);
-      unpack8(r[i], t);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] += t[j];
-      r[i] = pack8(s);
-      if (live && c < chunks) stg16(res_out + base + size_t(c) * 8, r[i]);
-    }
+    float odd;
+    f2_unpack(f2_add(squares[0], squares[1]), ss[k], odd);
+    ss[k] = warp_sum(ss[k] + odd);
   }
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float v[8];
-    unpack8(r[i], v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-  }
-  ss = warp_sum(ss);
   if (TPR > 32) {
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ss;
-    __syncthreads();
-    ss = red[0];
 #pragma unroll
-    for (int w = 1; w < TPR / 32; ++w) ss += red[w];
+    for (int k = 0; k < R; ++k)
+      if ((threadIdx.x & 31) == 0) red[k][threadIdx.x >> 5] = ss[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      ss[k] = red[k][0];
+#pragma unroll
+      for (int w = 1; w < TPR / 32; ++w) ss[k] += red[k][w];
+    }
   }
-  const float rs = 1.0f / sqrtf(ss / float(C) + eps);
-  if (live && tid == 0) rstd[row] = rs;
+  float rs[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    rs[k] = rsqrtf(fmaf(ss[k], inv_c, eps));
+    if (row0 + k < N && tid == 0) rstd[row0 + k] = rs[k];
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = tid + i * TPR;
-    float v[8], w[8];
-    unpack8(r[i], v);
+    if (!FEW && c < chunks) g[i] = ld16_once(gains + size_t(c) * 8);
+    Eight w;
     unpack8(g[i], w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = v[j] * rs * w[j];
-    const bool in = live && c < chunks;
-    // (lanes without a chunk have zeros, also where rs is not finite)
-    const uint32_t code = scale_code(max16(in ? amax8(v) : 0u));
-    if (in) {
-      const size_t o = base + size_t(c) * 8;
-      stg8(q + o, codes8(v, code_inverse(code)));
-      if (y != nullptr) stg16(y + o, pack8(v));
-      if ((tid & 15) == 0) scale[size_t(row) * size_t(blocks) + size_t(c >> 4)] = uint8_t(code);
+    for (int k = 0; k < R; ++k) {
+      const bool in = row0 + k < N && c < chunks;
+      Eight v;
+      unpack8(r[k][i], v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = f2_mul(f2_mul(v[j], f2_dup(rs[k])), w[j]);
+      // (lanes without a chunk have zeros, also where rs is not finite)
+      const uint32_t code = scale_code(max16(in ? amax8(v) : 0u));
+      if (in) {
+        const size_t o = size_t(row0 + k) * size_t(C) + size_t(c) * 8;
+        stg8(q + o, codes8(v, code_inverse(code)));
+        if (y != nullptr) stg16(y + o, pack8(v));
+        if ((tid & 15) == 0) scale[size_t(row0 + k) * size_t(blocks) + size_t(c >> 4)] = uint8_t(code);
+      }
     }
   }
 }
@@ -232,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) weight_blocks_kernel(uint8_t* q, uin
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float f[8];
+      Eight f;
       unpack8(v[i], f);
       top = max(top, amax8(f));
     }
@@ -247,7 +287,7 @@ __global__ void __launch_bounds__(kThreads) weight_blocks_kernel(uint8_t* q, uin
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t row = row0 + 16 * i;
-      float f[8];
+      Eight f;
       unpack8(v[i], f);
       if (row < rows && col < cols) stg8(q + (m * rows + row) * cols + col, codes8(f, inv));
     }
@@ -255,29 +295,36 @@ __global__ void __launch_bounds__(kThreads) weight_blocks_kernel(uint8_t* q, uin
   }
 }
 
-template <int TPR>
-cudaError_t run_rmsnorm(uint16_t* res_out, uint16_t* y, uint8_t* q, uint8_t* scale, float* rstd,
-                        const uint16_t* res_in, const uint16_t* x, const uint16_t* gain, float eps, int64_t N, int C,
-                        cudaStream_t s) {
-  constexpr int ROWS = TPR < 128 ? 128 / TPR : 1, BLOCK = TPR < 128 ? 128 : TPR;
-  const dim3 grid(unsigned((N + ROWS - 1) / ROWS));
+template <int TPR, bool FEW, typename... Args>
+cudaError_t run_rmsnorm(int64_t N, int C, cudaStream_t s, Args... args) {
+  constexpr int TEAMS = TPR < 128 ? 128 / TPR : 1, BLOCK = TPR < 128 ? 128 : TPR;
+  const float inv_c = 1.0f / float(C);
+  auto grid = [&](int at_once) { return dim3(unsigned((N + TEAMS * at_once - 1) / (TEAMS * at_once))); };
   switch ((C / 8 + TPR - 1) / TPR) {
-    case 1: return launch_pdl(rmsnorm_blocks_kernel<TPR, 1>, grid, BLOCK, 0, s, res_out, y, q, scale, rstd, res_in, x, gain, eps, N, C);
-    case 2: return launch_pdl(rmsnorm_blocks_kernel<TPR, 2>, grid, BLOCK, 0, s, res_out, y, q, scale, rstd, res_in, x, gain, eps, N, C);
-    case 3: return launch_pdl(rmsnorm_blocks_kernel<TPR, 3>, grid, BLOCK, 0, s, res_out, y, q, scale, rstd, res_in, x, gain, eps, N, C);
-    default: return launch_pdl(rmsnorm_blocks_kernel<TPR, 4>, grid, BLOCK, 0, s, res_out, y, q, scale, rstd, res_in, x, gain, eps, N, C);
+    case 1: return launch_pdl(rmsnorm_blocks_kernel<TPR, 1, FEW>, grid(rows_at_once<1, FEW>()), BLOCK, 0, s, args..., N, C, inv_c);
+    case 2: return launch_pdl(rmsnorm_blocks_kernel<TPR, 2, FEW>, grid(rows_at_once<2, FEW>()), BLOCK, 0, s, args..., N, C, inv_c);
+    case 3: return launch_pdl(rmsnorm_blocks_kernel<TPR, 3, FEW>, grid(rows_at_once<3, FEW>()), BLOCK, 0, s, args..., N, C, inv_c);
+    default: return launch_pdl(rmsnorm_blocks_kernel<TPR, 4, FEW>, grid(rows_at_once<4, FEW>()), BLOCK, 0, s, args..., N, C, inv_c);
   }
+}
+template <bool FEW, typename... Args>
+cudaError_t choose_rmsnorm(int64_t N, int C, cudaStream_t s, Args... args) {
+  if (C <= 1024) return run_rmsnorm<32, FEW>(N, C, s, args...);
+  if (C <= 4096) return run_rmsnorm<128, FEW>(N, C, s, args...);
+  if (C <= 8192) return run_rmsnorm<256, FEW>(N, C, s, args...);
+  return run_rmsnorm<512, FEW>(N, C, s, args...);
 }
 
 template <bool SWIGLU>
 cudaError_t run_rows(uint16_t* h, uint8_t* q, uint8_t* scale, const uint16_t* in, int64_t rows, int64_t cols,
                      cudaStream_t s) {
   if (rows == 0) return cudaSuccess;
-  const int64_t slots = rows * ((cols + 127) / 128) * 16;
-  int64_t grid = (slots + kThreads - 1) / kThreads;
-  const int64_t cap = int64_t(num_sms()) * 8;
-  if (grid > cap) grid = cap;
-  return launch_pdl(rows_kernel<SWIGLU>, dim3(unsigned(grid)), kThreads, 0, s, h, q, scale, in, rows, cols);
+  const int64_t per_row = (cols + 127) / 128 * 16;
+  const int64_t grid = (rows * per_row + kThreads * kFlight - 1) / (kThreads * kFlight);
+  if (grid > (int64_t(1) << 31) - 1) return cudaErrorInvalidValue;
+  // (per_row >= 16 divides 2^64 at most evenly: then this is the quotient + 1 too)
+  const uint64_t magic = ~uint64_t(0) / uint64_t(per_row) + 1 + ((per_row & (per_row - 1)) == 0 ? 1 : 0);
+  return launch_pdl(rows_kernel<SWIGLU>, dim3(unsigned(grid)), kThreads, 0, s, h, q, scale, in, rows, cols, magic);
 }
 
 }  // namespace
@@ -304,10 +351,9 @@ cudaError_t launch_rmsnorm_quantize_blocks(uint16_t* res_out, uint16_t* y, uint8
                                            const uint16_t* res_in, const uint16_t* x, const uint16_t* gain, float eps,
                                            int64_t N, int C, cudaStream_t s) {
   if (N == 0) return cudaSuccess;
-  if (C <= 1024) return run_rmsnorm<32>(res_out, y, q, scale, rstd, res_in, x, gain, eps, N, C, s);
-  if (C <= 4096) return run_rmsnorm<128>(res_out, y, q, scale, rstd, res_in, x, gain, eps, N, C, s);
-  if (C <= 8192) return run_rmsnorm<256>(res_out, y, q, scale, rstd, res_in, x, gain, eps, N, C, s);
-  return run_rmsnorm<512>(res_out, y, q, scale, rstd, res_in, x, gain, eps, N, C, s);
+  if (N * C <= int64_t(num_sms()) * 32768)
+    return choose_rmsnorm<true>(N, C, s, res_out, y, q, scale, rstd, res_in, x, gain, eps);
+  return choose_rmsnorm<false>(N, C, s, res_out, y, q, scale, rstd, res_in, x, gain, eps);
 }
 
 }  // namespace qffn

@@ -185,8 +185,9 @@ QFFN_DEVI Unit rows_unit(int u, int& g, const Table& t, const GroupArgs& a) {
   r.group = g;
   r.begin = t.off[g];
   r.rows = group_rows(t, g);
-  const int tm = r.rows <= a.bn_cap ? 1 : (r.rows + a.bn_cap - 1) / a.bn_cap;
-  r.bn = ((tm == 1 ? r.rows : (r.rows + tm - 1) / tm) + 31) & ~31;
+  // its rows in 32s, spread over tm tiles whose widths differ by 32 at most
+  const int parts = (r.rows + 31) >> 5, cap = a.bn_cap >> 5;
+  const int tm = parts <= cap ? 1 : (parts + cap - 1) / cap;
   // bands of band_n; within a band, groups of GROUP_M tiles of rows sweep its columns, odd
   // groups backwards (see linear.cu)
   int k = u - t.first[g], mt = 0;
@@ -205,7 +206,9 @@ QFFN_DEVI Unit rows_unit(int u, int& g, const Table& t, const GroupArgs& a) {
     mt = sweep * GROUP_M + k - col * size;
     r.nb = n0 + ((sweep & 1) ? wb - 1 - col : col);
   }
-  r.row0 = r.begin + mt * r.bn;
+  const int least = tm == 1 ? parts : parts / tm, wider = parts - least * tm;
+  r.bn = 32 * (least + (mt < wider ? 1 : 0));
+  r.row0 = r.begin + 32 * (mt * least + min(mt, wider));
   r.kb = 0;
   return r;
 }
