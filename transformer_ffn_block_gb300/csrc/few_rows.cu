@@ -23,6 +23,10 @@
 // MMAs; then all eight warps read TMEM.  Gated forms: the 128 rows are 64 gate
 // rows and the 64 up rows of the same outputs.  Every mbarrier wait is bounded,
 // as in linear.cu.
+//
+// OP_BLOCKS: E4M3 with a power-of-two scale per block of 128, which the tensor cores
+// multiply (grouped.cu says how): two warps write the scales of 512 of K at a time to
+// shared memory, the issuing thread copies them to TMEM in front of their MMAs.
 #include <cuda.h>
 
 #include "act.cuh"
@@ -44,7 +48,8 @@ constexpr int kMaxSplits = 8;
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 constexpr unsigned long long kDrainLimitNs = 200000000ull;
 
-constexpr int OP_BF16 = 0, OP_E4M3 = 1;
+constexpr int OP_BF16 = 0, OP_E4M3 = 1, OP_BLOCKS = 2;
+constexpr int kScaleStages = 4, kScaleBytes = 2 * 512;   // 128 weight rows, 128 rows of x: 4 bytes each
 constexpr int EPI_LINEAR = 0, EPI_GATED = 1, EPI_GATED_BWD = 2;
 constexpr int stage_k(int op) { return op == OP_BF16 ? 64 : 128; }   // elements of K per stage
 
@@ -57,6 +62,9 @@ struct FewArgs {
   const uint16_t* in;       // EPI_LINEAR: residual (optional); GATED_BWD: dh
   const float* a_scale;     // E4M3 operands; else NULL
   const float* w_scale;
+  const uint8_t* x_blocks;  // OP_BLOCKS: E8M0 scales [M, blocks] and [ceil(N / 128), blocks]
+  const uint8_t* w_blocks;
+  int blocks;
   int act;
   int M, N;                 // activation rows; output columns (gated: H)
   int num_kb, splits;       // K blocks of a stage each; parts of K (CTAs per cluster)
@@ -82,6 +90,19 @@ QFFN_DEVI void mma_one(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t
         " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+// The same with block scales at TMEM columns sfa and sfb.
+QFFN_DEVI void mma_one_blocks(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                              uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+// The scales of 128 rows, 512 bytes of shared memory, to four TMEM columns (see grouped.cu).
+QFFN_DEVI void copy_scales(uint32_t taddr, uint32_t saddr) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc_scales(saddr)) : "memory");
 }
 // Arrive once on `bar` when all previously issued MMAs of this thread have completed.
 QFFN_DEVI void mma_commit(uint32_t bar) {
@@ -252,7 +273,8 @@ __global__ void __launch_bounds__(kThreads)
                     const FewArgs args) {
   constexpr bool GATED = EPI != EPI_LINEAR;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 3];
+  constexpr bool BLOCKS = OP == OP_BLOCKS;
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 3 + (BLOCKS ? 2 * kScaleStages : 0)];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
@@ -266,6 +288,10 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t done_bar = bar0 + 8u * uint32_t(2 * kMaxStages);
   const uint32_t drain_bar = bar0 + 8u * uint32_t(2 * kMaxStages + 1);
   const uint32_t recv_bar = bar0 + 8u * uint32_t(2 * kMaxStages + 2);
+  // sfull[s]: the scales of stage s are written; sempty[s]: copied
+  auto sfull_bar = [&](int s) { return bar0 + 8u * uint32_t(2 * kMaxStages + 3 + s); };
+  auto sempty_bar = [&](int s) { return bar0 + 8u * uint32_t(2 * kMaxStages + 3 + kScaleStages + s); };
+  const uint32_t scales = smem_u32(smem) + uint32_t(args.stages * args.stage_bytes + args.recv_bytes);
 
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int part = int(cluster_ctarank());
@@ -280,6 +306,11 @@ __global__ void __launch_bounds__(kThreads)
     mbar_init(done_bar, 1);
     mbar_init(drain_bar, 1);
     mbar_init(recv_bar, 1);
+    if (BLOCKS)
+      for (int s = 0; s < kScaleStages; ++s) {
+        mbar_init(sfull_bar(s), 1);
+        mbar_init(sempty_bar(s), 1);
+      }
     *abort_flag = 0;
     mbar_init_fence();
     if (args.splits > 1) mbar_expect_tx(recv_bar, uint32_t(args.recv_bytes));
@@ -342,13 +373,24 @@ __global__ void __launch_bounds__(kThreads)
     if (elect_one()) {
       // ------------------------------------------------------------ MMA issuer
       // D fp32, operand formats, W MN-major, N = bn, M = 128 (see linear.cu)
-      const uint32_t idesc = (1u << 4) | (OP == OP_BF16 ? (1u << 7) | (1u << 10) : 0u) | (W_MN ? 1u << 15 : 0u) |
-                             (uint32_t(args.bn >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+      // (OP_BLOCKS: E8M0 scales, bit 23; see grouped.cu)
+      const uint32_t idesc = (BLOCKS ? 1u << 23 : 1u << 4) | (OP == OP_BF16 ? (1u << 7) | (1u << 10) : 0u) |
+                             (W_MN ? 1u << 15 : 0u) | (uint32_t(args.bn >> 3) << 17) | (uint32_t(128 >> 4) << 24);
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
+      uint32_t sf = 0;                       // TMEM columns of the current scales
       bool ready = false;                    // the next stage was there before this one's MMAs were issued
       for (int kb = kb0; kb < kb1; ++kb) {
+        if (BLOCKS && ((kb - kb0) & 3) == 0) {
+          const int chunk = (kb - kb0) >> 2, ss = chunk % kScaleStages;
+          if (!mbar_wait(sfull_bar(ss), uint32_t(chunk / kScaleStages) & 1u, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          sf = tmem_base + uint32_t(args.bn + 8 * (chunk & 1));
+          copy_scales(sf, scales + uint32_t(ss * kScaleBytes));
+          copy_scales(sf + 4, scales + uint32_t(ss * kScaleBytes + 512));
+          mma_commit(sempty_bar(ss));
+        }
         if (!ready && !mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t a0 = smem_u32(smem) + uint32_t(s * args.stage_bytes), b0 = a0 + BOX_BYTES, empty = empty_bar(s);
@@ -357,6 +399,13 @@ __global__ void __launch_bounds__(kThreads)
           ph ^= 1u;
         }
         ready = kb + 1 < kb1 && mbar_test_wait(full_bar(s), ph);
+        if (BLOCKS) {
+          const uint32_t which = uint32_t((kb - kb0) & 3);
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i)
+            mma_one_blocks(tmem_base, w_desc<W_MN>(a0, i), sdesc_sw128(b0 + uint32_t(i) * 32u),
+                           idesc | (which << 4) | (which << 29), sf, sf + 4, uint32_t((kb - kb0) | i));
+        } else
 #pragma unroll
         for (int i = 0; i < STEPS; ++i)
           mma_one<OP>(tmem_base, w_desc<W_MN>(a0, i), sdesc_sw128(b0 + uint32_t(i) * 32u), idesc,
@@ -366,6 +415,37 @@ __global__ void __launch_bounds__(kThreads)
       if (ok) mma_commit(done_bar);
       mma_commit(drain_bar);
       mbar_wait(drain_bar, 0, abort_flag, false, kDrainLimitNs);
+    }
+    __syncwarp();
+  } else if (BLOCKS && (warp == 3 || warp == 4)) {
+    // -------------------------------------------------------------- scales
+    // Each warp every second chunk of four blocks.  Lane l: the words of rows l, l + 32, l +
+    // 64, l + 96 of x; the 128 weight rows have one word.
+    const int chunks = (kb1 - kb0 + 3) / 4;
+    const uint8_t* const wb = args.w_blocks + size_t(tile) * size_t(args.blocks);
+    bool going = true;
+    for (int c = warp - 3; going && c < chunks; c += 2) {
+      const int first = kb0 + 4 * c, n = min(4, kb1 - first);
+      uint32_t word_w = 0u, word_x[4];
+      for (int j = 0; j < n; ++j) word_w |= uint32_t(wb[first + j]) << (8 * j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        word_x[i] = 0u;
+        if (32 * i < args.bn) {
+          const size_t row = size_t(min(mt * args.bn + 32 * i + lane, args.M - 1));
+          const uint8_t* const p = args.x_blocks + row * size_t(args.blocks) + size_t(first);
+          for (int j = 0; j < n; ++j) word_x[i] |= uint32_t(p[j]) << (8 * j);
+        }
+      }
+      const int ss = c % kScaleStages;
+      going = __all_sync(0xffffffffu, mbar_wait(sempty_bar(ss), (uint32_t(c / kScaleStages) & 1u) ^ 1u, abort_flag));
+      if (!going) break;
+      const uint32_t dst = scales + uint32_t(ss * kScaleBytes + lane * 16);
+      sts16(dst, make_uint4(word_w, word_w, word_w, word_w));
+      sts16(dst + 512, make_uint4(word_x[0], word_x[1], word_x[2], word_x[3]));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sfull_bar(ss));
     }
     __syncwarp();
   }
@@ -431,7 +511,7 @@ constexpr int kSmemOne = 200 * 1024, kSmemTwo = 100 * 1024;
 template <int OP, bool W_MN, int EPI>
 cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, FewArgs a, int clusters, cudaStream_t s) {
   const auto fn = few_rows_kernel<OP, W_MN, EPI>;
-  const int bytes = a.stages * a.stage_bytes + a.recv_bytes + 1024;
+  const int bytes = a.stages * a.stage_bytes + a.recv_bytes + (OP == OP_BLOCKS ? kScaleStages * kScaleBytes : 0) + 1024;
   static bool set[64] = {false};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -539,7 +619,8 @@ int64_t few_rows_cycles(int64_t M, int64_t N, int64_t K, bool gated, bool fp8) {
 template <int OP, bool W_MN, int EPI>
 cudaError_t few_rows_product(uint16_t* out, uint16_t* z, const void* x, const float* x_scale, const void* w,
                              const float* w_scale, const uint16_t* bias, const uint16_t* in, int act, int64_t M,
-                             int64_t N, int64_t K, cudaStream_t s, bool late_wait = false) {
+                             int64_t N, int64_t K, cudaStream_t s, bool late_wait = false,
+                             const uint8_t* x_blocks = nullptr, const uint8_t* w_blocks = nullptr) {
   constexpr bool GATED = EPI != EPI_LINEAR;
   FewArgs a{};
   a.late_wait = late_wait ? 1 : 0;
@@ -549,22 +630,26 @@ cudaError_t few_rows_product(uint16_t* out, uint16_t* z, const void* x, const fl
   a.in = in;
   a.a_scale = x_scale;
   a.w_scale = w_scale;
+  a.x_blocks = x_blocks;
+  a.w_blocks = w_blocks;
+  a.blocks = int((K + 127) / 128);
   a.act = act;
   a.M = int(M);
   a.N = int(N);
   a.tiles_m = int((M + 127) / 128);
   a.bn = few_rows_bn(M);
   int clusters = 0;
-  const cudaError_t e = few_rows_split(M, N, K, GATED, OP == OP_E4M3, &clusters, &a.splits, &a.num_kb);
+  const cudaError_t e = few_rows_split(M, N, K, GATED, OP != OP_BF16, &clusters, &a.splits, &a.num_kb);
   if (e != cudaSuccess) return e;
   a.stage_bytes = BOX_BYTES + a.bn * ROW_BYTES;
   const bool two = clusters * a.splits > kNumSMsHint;
   a.recv_bytes = (a.splits - 1) * (a.bn / a.splits) * 512;
   // (the sums, bn x 512 bytes, take at most 64 KB of the stages' 96 to 200 KB)
-  a.stages = ((two ? kSmemTwo : kSmemOne) - a.recv_bytes) / a.stage_bytes;
+  const int extra = a.recv_bytes + (OP == OP_BLOCKS ? kScaleStages * kScaleBytes : 0);
+  a.stages = ((two ? kSmemTwo : kSmemOne) - extra) / a.stage_bytes;
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   a.tmem_cols = 32;
-  while (a.tmem_cols < a.bn) a.tmem_cols *= 2;
+  while (a.tmem_cols < a.bn + (OP == OP_BLOCKS ? 16 : 0)) a.tmem_cols *= 2;   // (two slots of scales)
   CUtensorMap mw, mx;
   const bool bf16 = OP == OP_BF16;
   const bool ok = (W_MN ? make_operand_map(&mw, w, bf16, K, N, 64)
@@ -581,6 +666,13 @@ cudaError_t launch_few_rows(uint16_t* out, uint16_t* z, const void* x, const flo
   if (w_mn)
     return few_rows_product<OP_BF16, true, EPI_LINEAR>(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, s, late_wait);
   return few_rows_product<OP_BF16, false, EPI_LINEAR>(out, z, x, nullptr, w, nullptr, bias, res, act, M, N, K, s);
+}
+
+cudaError_t launch_few_rows_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
+                                   const uint8_t* w_scale, const uint16_t* bias, const uint16_t* res, int64_t M,
+                                   int64_t N, int64_t K, cudaStream_t s) {
+  return few_rows_product<OP_BLOCKS, false, EPI_LINEAR>(out, nullptr, x, nullptr, w, nullptr, bias, res, ACT_NONE, M, N,
+                                                        K, s, false, x_scale, w_scale);
 }
 
 cudaError_t launch_few_rows_gated(uint16_t* out, const uint16_t* x, const uint16_t* w1, const uint16_t* dh, int act,

@@ -23,7 +23,7 @@
 //   zeros in shared memory before the MMAs read the stage, in both operands, so that
 //   neither finite values nor NaN of a neighbour meet a group.
 // - E4M3: tcgen05.mma.kind::mxf8f6f4.block_scale takes E8M0 scales for every 32
-//   values of K from TMEM; a scale per 128 is the same byte in four MMAs.  Two warps
+//   values of K from TMEM; a scale per 128 is the same byte in four MMAs.  Four warps
 //   read the scales of 512 of K at a time (one byte per row of x and block, one per
 //   128 weight rows and block), lay them out in shared memory, and the issuing thread
 //   copies them to TMEM (tcgen05.cp) in front of the MMAs that use them.  The tensor
@@ -52,9 +52,9 @@ constexpr int OP_BYTES = 128 * ROW_BYTES;  // an operand's share of a stage: 128
 constexpr int MN_BOX_BYTES = 64 * ROW_BYTES;   // MN-major: 64 values by 64 of K, two boxes to the share
 constexpr int STEPS = 4;                   // MMAs per stage (32 bytes of K each)
 constexpr int EPI_WARPS = 8;
-constexpr int SCALE_WARPS = 2;
-constexpr int MAX_STAGES = 6;
-constexpr int SF_STAGES = 4;               // stages of scales, 512 of K each
+constexpr int SCALE_WARPS = 4;
+constexpr int MAX_STAGES = 10;
+constexpr int SF_STAGES = SCALE_WARPS;     // stages of scales, 512 of K each, one for each warp that fills them
 constexpr int SF_BYTES = 3 * 512;          // 128 weight rows, 256 rows of x: 4 bytes each
 constexpr int STAGING_BOX = 32 * 128;      // a warp's transposing box: 32 rows x 32 fp32
 constexpr int STAGING_BYTES = EPI_WARPS * STAGING_BOX;
@@ -69,7 +69,6 @@ constexpr unsigned long long kDrainLimitNs = 200000000ull;
 
 constexpr int stage_k(int op) { return op == OP_BF16 ? 64 : 128; }   // elements of K per stage
 constexpr int max_bn(int op) { return op == OP_BF16 ? 256 : 224; }   // columns of an accumulator
-constexpr int stage_bytes(int op) { return OP_BYTES + max_bn(op) / 2 * ROW_BYTES; }
 constexpr int num_threads(int op, int kind) {
   return 32 * (2 + EPI_WARPS + (op == OP_BLOCKS ? SCALE_WARPS : kind == KIND_WEIGHT ? 1 : 0));
 }
@@ -105,7 +104,8 @@ struct GroupArgs {
   int bn_cap;               // ROWS: most rows of a unit, a multiple of 32
   int band_n;               // ROWS: units across N that are swept together
   int num_kb;               // ROWS: stages of K
-  int stages;
+  int accs;                 // accumulators: 2, or 1 where a unit is wider than half of TMEM allows
+  int stages, stage_bytes;  // stage_bytes: with room for bn_cap / 2 rows of x
 };
 
 // D(tmem, both CTAs) (+)= A(smem, both CTAs) . B(smem, both CTAs)^T
@@ -130,11 +130,6 @@ QFFN_DEVI void mma_pair_blocks(uint32_t d, uint64_t adesc, uint64_t bdesc, uint3
 QFFN_DEVI void copy_scales(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
-// Descriptor of such rows: no swizzle, groups of eight rows 128 bytes apart.
-QFFN_DEVI uint64_t sdesc_scales(uint32_t saddr) {
-  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(16 >> 4) << 16) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
-}
-
 // Shared-memory descriptor of MMA step i of a stage's operand (see linear.cu).
 template <bool MN>
 QFFN_DEVI uint64_t step_desc(uint32_t base, int i) {
@@ -235,12 +230,12 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     grouped_kernel(const __grid_constant__ Maps maps, const GroupArgs args) {
   constexpr bool WEIGHT = KIND == KIND_WEIGHT;
   constexpr bool A_MN = KIND != KIND_ROWS, B_MN = WEIGHT;
-  constexpr int STAGE = stage_bytes(OP);
+  const uint32_t stage = uint32_t(args.stage_bytes);
   constexpr int ACC_COLS = max_bn(OP);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t ring = smem_u32(smem);
-  uint8_t* sStaging = smem + args.stages * STAGE;
+  uint8_t* sStaging = smem + args.stages * args.stage_bytes;
   uint8_t* sScales = sStaging + STAGING_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sScales + (OP == OP_BLOCKS ? SF_STAGES * SF_BYTES : 0));
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
@@ -302,6 +297,10 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
+  tc_fence_before();
+  cluster_sync_all();      // both CTAs' barriers exist before either signals the other's
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
   pdl_wait();              // nothing in global memory is touched before the preceding kernel is done
   const uint16_t* const bias_row = behind_wait(args.bias);
   pdl_trigger();
@@ -323,11 +322,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     }
     if (lane == 0) table_first[0] = 0;
   }
-  tc_fence_before();
   __syncthreads();
-  cluster_sync_all();      // both CTAs' barriers exist before either signals the other's
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
 
   const int num_units = WEIGHT ? args.G * args.tiles_n : table_first[args.G];
   int group_cursor = 0;
@@ -373,7 +368,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
             tail_parity ^= 1u << s;
           }
           const uint32_t fb = tail ? map_to_rank(tail_bar(s), rank) : map_to_rank(full_bar(s), 0);
-          const uint32_t da = ring + uint32_t(s) * uint32_t(STAGE);
+          const uint32_t da = ring + uint32_t(s) * stage;
           uint32_t db = da + uint32_t(OP_BYTES);
           if (WEIGHT) {
             const int row = u.begin + k0;
@@ -424,8 +419,8 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       uint32_t ph = 0, cleared_parity = 0;
       bool ok = true;
       for (int un = first_unit(); ok && un < num_units; un = next_unit(un), ++local) {
-        const int acc = local & 1;
-        const uint32_t aph = uint32_t(local >> 1) & 1u;
+        const int acc = local & (args.accs - 1);
+        const uint32_t aph = uint32_t(local >> (args.accs - 1)) & 1u;
         if (!mbar_wait_cluster_bounded(tempty_bar(acc), aph ^ 1u, abort_flag, &g_status, kWaitLimitNs)) break;
         tc_fence_after();
         const Unit u = unit_at(un);
@@ -459,7 +454,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
             cleared_parity ^= 1u << s;
           }
           tc_fence_after();
-          const uint32_t a0 = ring + uint32_t(s) * uint32_t(STAGE), b0 = a0 + uint32_t(OP_BYTES), empty = empty_bar(s);
+          const uint32_t a0 = ring + uint32_t(s) * stage, b0 = a0 + uint32_t(OP_BYTES), empty = empty_bar(s);
           if (++s == args.stages) {
             s = 0;
             ph ^= 1u;
@@ -487,56 +482,55 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     __syncwarp();
   } else if (OP == OP_BLOCKS && warp >= 2 + EPI_WARPS) {
     // -------------------------------------------------------------- scales
-    // Warp `mine` of the two takes every second chunk of 512 of K.  Lane l holds the
-    // words (four blocks' bytes) of rows l, l + 32, ... of x; this CTA's 128 weight rows
-    // have one word.  Blocks behind the last are never multiplied with.
+    // Four blocks (512 of K, a chunk) at a time, the warps in turn: reading a few bytes of many
+    // rows and publishing them takes a warp 1 to 2 us (with two warps instead of four 128 x
+    // 4096 x 14336 took 30.0 us instead of SCALE_TIME).  Warp and stage of a chunk are its number modulo
+    // four, so a stage is one warp's, as waits by parity need.  Lane l holds the words (four
+    // blocks' bytes) of rows l, l + 32, ... of x; this CTA's 128 weight rows have one word.
+    // Blocks behind the last are never multiplied with.
     const int mine = warp - (2 + EPI_WARPS);
-    const bool whole = (args.blocks & 3) == 0 && (reinterpret_cast<uintptr_t>(args.x_scale) & 3u) == 0;
-    int chunk = 0, waited = 0;
+    const bool whole = ((reinterpret_cast<uintptr_t>(args.x_scale) | reinterpret_cast<uintptr_t>(args.w_scale) | uintptr_t(args.blocks)) & 3u) == 0;
+    const int chunks = (args.num_kb + 3) / 4;          // of a unit
+    auto word = [&](const uint8_t* p, int left) {
+      if (whole) return *reinterpret_cast<const uint32_t*>(p);
+      uint32_t v = p[0];
+      if (left > 1) v |= uint32_t(p[1]) << 8;
+      if (left > 2) v |= uint32_t(p[2]) << 16;
+      if (left > 3) v |= uint32_t(p[3]) << 24;
+      return v;
+    };
+    const uint32_t dst = smem_u32(sScales) + uint32_t(mine * SF_BYTES + lane * 16);
+    int c = mine;
+    uint32_t fills = 0;
     bool ok = true;
-    for (int un = first_unit(); ok && un < num_units; un = next_unit(un)) {
+    for (int un = first_unit(); ok && un < num_units; un = next_unit(un), c -= chunks) {
+      if (c >= chunks) continue;
       const Unit u = unit_at(un);
-      const int num = (args.num_kb + 3) / 4;
-      const int block_w = u.nb * 2 + int(rank);
-      const uint8_t* const ws = args.w_scale + (size_t(u.group) * size_t(args.n_blocks) + size_t(min(block_w, args.n_blocks - 1))) * size_t(args.blocks);
-      const int per_lane = u.bn / 32;
-      for (int c = 0; c < num; ++c, ++chunk) {
-        if ((chunk & 1) != mine) continue;
+      const int block_w = min(u.nb * 2 + int(rank), args.n_blocks - 1);
+      const uint8_t* const ws = args.w_scale + (size_t(u.group) * size_t(args.n_blocks) + size_t(block_w)) * size_t(args.blocks);
+      for (; c < chunks; c += SCALE_WARPS) {
         const int left = args.blocks - 4 * c;
-        uint32_t word_w = 0u, word_x[8];
-        for (int j = 0; j < 4; ++j)
-          if (j < left) word_w |= uint32_t(ws[4 * c + j]) << (8 * j);
+        const uint32_t w = word(ws + size_t(4 * c), left);
+        uint32_t x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          word_x[i] = 0u;
-          if (i < per_lane) {
-            const int row = min(u.row0 + 32 * i + lane, args.M - 1);
-            const uint8_t* const p = args.x_scale + size_t(row) * size_t(args.blocks) + size_t(4 * c);
-            if (whole) {
-              word_x[i] = *reinterpret_cast<const uint32_t*>(p);
-            } else {
-              for (int j = 0; j < 4; ++j)
-                if (j < left) word_x[i] |= uint32_t(p[j]) << (8 * j);
-            }
-          }
+          x[i] = 0u;
+          if (32 * i < u.bn)
+            x[i] = word(args.x_scale + size_t(min(u.row0 + 32 * i + lane, args.M - 1)) * size_t(args.blocks) + size_t(4 * c), left);
         }
-        const int ss = chunk % SF_STAGES;
-        ok = __all_sync(0xffffffffu, mbar_wait(sempty_bar(ss), (uint32_t(chunk / SF_STAGES) & 1u) ^ 1u, abort_flag));
+        ok = __all_sync(0xffffffffu, mbar_wait(sempty_bar(mine), (fills & 1u) ^ 1u, abort_flag));
         if (!ok) break;
-        const uint32_t dst = smem_u32(sScales) + uint32_t(ss * SF_BYTES + lane * 16);
-        sts16(dst, make_uint4(word_w, word_w, word_w, word_w));
-        sts16(dst + 512, make_uint4(word_x[0], word_x[1], word_x[2], word_x[3]));
-        sts16(dst + 1024, make_uint4(word_x[4], word_x[5], word_x[6], word_x[7]));
+        sts16(dst, make_uint4(w, w, w, w));
+        sts16(dst + 512, make_uint4(x[0], x[1], x[2], x[3]));
+        sts16(dst + 1024, make_uint4(x[4], x[5], x[6], x[7]));
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(map_to_rank(sfull_bar(ss), 0));
-        waited = chunk + 1;
+        if (lane == 0) mbar_arrive_remote(map_to_rank(sfull_bar(mine), 0));
+        ++fills;
       }
     }
-    // the issuer's last arrivals on the stages that this warp filled reach this CTA
-    for (int c = max(0, waited - SF_STAGES); ok && c < waited; ++c)
-      if ((c & 1) == mine)
-        mbar_wait(sempty_bar(c % SF_STAGES), uint32_t(c / SF_STAGES) & 1u, abort_flag, false, kDrainLimitNs);
+    // the issuer's last arrival on this stage reaches this CTA
+    if (ok && fills > 0) mbar_wait(sempty_bar(mine), (fills & 1u) ^ 1u, abort_flag, false, kDrainLimitNs);
     __syncwarp();
   } else if (WEIGHT && warp >= 2 + EPI_WARPS) {
     // -------------------------------------------------------------- rows behind a group
@@ -551,7 +545,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       if (live < 64) {
         if (!__all_sync(0xffffffffu, mbar_wait(tail_bar(s), (parity >> s) & 1u, abort_flag))) break;
         parity ^= 1u << s;
-        const uint32_t at = ring + uint32_t(s) * uint32_t(STAGE);
+        const uint32_t at = ring + uint32_t(s) * stage;
         for (int b = 0; b < 4; ++b)
           for (int i = live * ROW_BYTES + lane * 16; i < MN_BOX_BYTES; i += 512)
             sts16(at + uint32_t(b * MN_BOX_BYTES + i), make_uint4(0, 0, 0, 0));
@@ -579,8 +573,8 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       const uint32_t turn32 = box + uint32_t(sub) * 128u + (uint32_t((2 * ch) ^ sub) << 4);
       const size_t step = size_t(8) * size_t(args.N);
       for (; un < num_units; ++local) {
-        const int acc = local & 1;
-        const uint32_t aph = uint32_t(local >> 1) & 1u;
+        const int acc = local & (args.accs - 1);
+        const uint32_t aph = uint32_t(local >> (args.accs - 1)) & 1u;
         const Unit u = unit_at(un);
         const int row_end = min(u.begin + u.rows, u.row0 + u.bn);
         const int col = u.nb * (2 * BM) + int(rank) * BM + q * 32 + ch * 8;
@@ -617,7 +611,8 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) break;
         tc_fence_after();
         const int next2 = next < num_units ? next_unit(next) : next;
-        const bool awaited = next < num_units && next2 < num_units;   // another unit takes this accumulator
+        // another unit takes this accumulator
+        const bool awaited = next < num_units && (args.accs == 1 || next2 < num_units);
         auto loaded = [&](int g) {
           if (g + 1 >= g1) {
             tc_fence_before();
@@ -706,8 +701,8 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         request(p, 1, in8[1]);
       }
       for (; un < num_units; ++local) {
-        const int acc = local & 1;
-        const uint32_t aph = uint32_t(local >> 1) & 1u;
+        const int acc = local & (args.accs - 1);
+        const uint32_t aph = uint32_t(local >> (args.accs - 1)) & 1u;
         const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * ACC_COLS);
         const int next2 = next < num_units ? next_unit(next) : next;
         const bool awaited = next < num_units && next2 < num_units;
@@ -828,19 +823,21 @@ cudaError_t max_pairs(int* pairs) {
   return cudaSuccess;
 }
 
-// `units`: no fewer than the kernel will find
+// `units`: no fewer than the kernel will find (if the offsets do not decrease)
 template <int OP, int KIND>
-cudaError_t launch(const Maps& m, GroupArgs a, int64_t units, cudaStream_t s) {
+cudaError_t launch(const Maps& m, GroupArgs a, int64_t units, int pairs, cudaStream_t s) {
   const int table = 8 * (a.G + 1);
-  a.stages = (SMEM_LIMIT - fixed_bytes(OP) - table) / stage_bytes(OP);
+  const bool wide = a.bn_cap > max_bn(OP);
+  a.accs = wide ? 1 : 2;
+  // (narrow units: more stages, whose loads' latency is what bounds them; 512 x 4096 x 2048
+  // with six stages STAGE6 us, with eight STAGE8)
+  a.stage_bytes = OP_BYTES + a.bn_cap / 2 * ROW_BYTES;
+  a.stages = (SMEM_LIMIT - fixed_bytes(OP) - table) / a.stage_bytes;
   if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
-  int pairs = 0;
-  const cudaError_t e = max_pairs<OP, KIND>(&pairs);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * unsigned(units < pairs ? units : pairs));
   cfg.blockDim = dim3(num_threads(OP, KIND));
-  cfg.dynamicSmemBytes = size_t(a.stages * stage_bytes(OP) + fixed_bytes(OP) + table + 1024);
+  cfg.dynamicSmemBytes = size_t(a.stages * a.stage_bytes + fixed_bytes(OP) + table + 1024);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -855,6 +852,33 @@ cudaError_t launch(const Maps& m, GroupArgs a, int64_t units, cudaStream_t s) {
 }
 
 int ceil_div(int64_t a, int64_t b) { return int((a + b - 1) / b); }
+
+// Most rows of a unit.  The widest, where the host does not know the groups' sizes or
+// they make many units; one group's rows are cut so that its units fill the SM pairs in
+// the fewest and narrowest rounds, a stage taking 117 + 1.55 bn cycles and 288 at least
+// (see linear.cu).  With one unit per pair at most, E4M3 needs no second accumulator and
+// takes 256 rows too.
+int choose_cap(int op, int64_t G, int64_t M, int tiles_n, int pairs) {
+  const int cap = max_bn(op);
+  const bool one_round = (M / 256 + (G < M ? G : M)) * tiles_n <= pairs;
+  // (groups of few rows: 128, for the sake of more stages)
+  if (G > 1) return M / G < 96 ? 128 : one_round ? 256 : cap;
+  const int64_t parts = (M + 31) / 32;
+  int64_t best = -1;
+  int best_cap = cap;
+  for (int64_t tm = (parts + 7) / 8; tm < (parts + 7) / 8 + 8 && tm <= parts; ++tm) {
+    const int bn = 32 * int((parts + tm - 1) / tm);
+    const int64_t units = tm * tiles_n;
+    if (bn > cap && units > pairs) continue;
+    const int64_t stage = 117 + 31 * bn / 20;
+    const int64_t cost = (units + pairs - 1) / pairs * (stage > 288 ? stage : 288);
+    if (best < 0 || cost < best) {
+      best = cost;
+      best_cap = bn;
+    }
+  }
+  return best_cap;
+}
 
 // out [M, N] from x [M, K] and w [G, N, K] (KIND_ROWS) or [G, K, N] (KIND_ROWS_MN).
 template <int OP, int KIND>
@@ -882,13 +906,16 @@ cudaError_t rows_product(uint16_t* out, const void* x, const uint8_t* x_scale, c
   a.M = int(M);
   a.N = int(N);
   a.tiles_n = ceil_div(N, 2 * BM);
-  a.bn_cap = max_bn(OP);
+  int pairs = 0;
+  const cudaError_t e = max_pairs<OP, KIND>(&pairs);
+  if (e != cudaSuccess) return e;
+  a.bn_cap = choose_cap(OP, G, M, a.tiles_n, pairs);
   a.num_kb = ceil_div(K, stage_k(OP));
   // bands of about 32 MB of weights where they are the larger operand (see linear.cu)
   const int64_t band = (int64_t(32) << 20) / (2 * BM * K * bytes);
   a.band_n = N <= M / G || band >= a.tiles_n ? a.tiles_n : band < 1 ? 1 : int(band);
   const int64_t units = (M / a.bn_cap + (G < M ? G : M)) * a.tiles_n;
-  return launch<OP, KIND>(m, a, units, s);
+  return launch<OP, KIND>(m, a, units, pairs, s);
 }
 
 // dw [G, N, K] (+)= dout [M, N]^T . x [M, K] by group.
@@ -909,7 +936,10 @@ cudaError_t weight_product(uint16_t* dw, const uint16_t* dout, const uint16_t* x
   a.tiles_k = ceil_div(K, 256);
   a.tiles_n = ceil_div(N, 256) * a.tiles_k;
   a.bn_cap = 256;
-  return launch<OP_BF16, KIND_WEIGHT>(m, a, int64_t(a.tiles_n) * G, s);
+  int pairs = 0;
+  const cudaError_t e = max_pairs<OP_BF16, KIND_WEIGHT>(&pairs);
+  if (e != cudaSuccess) return e;
+  return launch<OP_BF16, KIND_WEIGHT>(m, a, int64_t(a.tiles_n) * G, pairs, s);
 }
 
 }  // namespace

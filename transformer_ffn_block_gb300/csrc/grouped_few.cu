@@ -4,22 +4,25 @@
 //   out[m, r] = bf16(sum_k W_g[r,k] x[m,k] (+ bias[r]) (+ res[m,r])),  m in group g
 //
 // A CTA owns 16 weight rows of one group; its warps take the rows' 256-byte groups
-// in turn and their sums are added in order through shared memory (the operand
-// layout and the reasons for it are those of skinny.cu).  The CTA goes over the
+// (E4M3: 128-byte groups) in turn and their sums are added in order through shared
+// memory (the operand layout and the reasons for it are those of skinny.cu).  The CTA goes over the
 // group's rows 8 NT at a time; beyond the first pass its weights come from L2.
 // blockIdx.y counts the groups that have rows, found from the offsets by a
 // warp-wide search, so that empty groups cost nothing.
 //
-// Block scales (E4M3): 256 bytes of a row are two blocks of 128.  Each block's
-// products are summed by the tensor cores from zero, and the fp32 sum joins the
-// total multiplied by 2^(cx + cw - 254), exactly.
+// Block scales (E4M3): a group of 128 bytes is one block.  Its products are summed by
+// the tensor cores from zero, and the fp32 sum joins the total multiplied by
+// 2^(cx + cw - 254), exactly.
 #include "common.cuh"
 #include "launch.h"
 
 namespace qffn {
 namespace {
 
-constexpr int kU = 4;                      // 64-byte chunks per step: 256 bytes of a row
+// 64-byte chunks of a row per group
+constexpr int chunks_of(bool fp8) { return fp8 ? 2 : 4; }
+// Warps per SM that the registers are to leave room for
+constexpr int warps_of(bool fp8, int nt) { return nt == 1 ? 32 : fp8 && nt == 2 ? 24 : 16; }
 
 struct FewGroupArgs {
   uint16_t* out;
@@ -59,8 +62,8 @@ QFFN_DEVI float scaled(float v, uint32_t a, uint32_t b) {
 }
 
 template <bool FP8, int NT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, (NT == 1 && !FP8 ? 32 : NT <= 2 || !FP8 ? 16 : 8) / WARPS) few_groups_kernel(const FewGroupArgs a) {
-  constexpr int TOK = 8 * NT;
+__global__ void __launch_bounds__(WARPS * 32, warps_of(FP8, NT) / WARPS) few_groups_kernel(const FewGroupArgs a) {
+  constexpr int TOK = 8 * NT, kU = chunks_of(FP8);
   __shared__ float red[WARPS][16][TOK + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -117,7 +120,7 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 && !FP8 ? 32 : NT <= 2 ||
     for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.0f;
     for (int64_t k0 = int64_t(warp) * (kU * 64); k0 < a.row_bytes; k0 += int64_t(WARPS) * (kU * 64)) {
       uint4 va[kU], vb[kU], vx[NT][kU];
-      uint32_t sw[2] = {0u, 0u}, sx[2][NT][2];
+      uint32_t sw = 0u, sx[NT][2];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int64_t k = k0 + u * 64;
@@ -126,15 +129,11 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 && !FP8 ? 32 : NT <= 2 ||
         vb[u] = in ? ld16_stream(wb + k) : zero;
       }
       if (FP8) {
+        sw = ws[k0 >> 7];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int64_t kb = min((k0 >> 7) + b, a.blocks - 1);
-          sw[b] = ws[kb];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) sx[b][n][j] = xs[n][j][kb];
-        }
+          for (int j = 0; j < 2; ++j) sx[n][j] = xs[n][j][k0 >> 7];
       }
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
@@ -153,19 +152,15 @@ __global__ void __launch_bounds__(WARPS * 32, (NT == 1 && !FP8 ? 32 : NT <= 2 ||
           }
       } else {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (k0 + b * 128 >= a.row_bytes) break;      // (a block that is not there has no scale either)
+        for (int n = 0; n < NT; ++n) {
+          float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int u = 2 * b; u < 2 * b + 2; ++u) {
-              mma_16x8<FP8>(p, va[u].x, vb[u].x, va[u].y, vb[u].y, vx[n][u].x, vx[n][u].y);
-              mma_16x8<FP8>(p, va[u].z, vb[u].z, va[u].w, vb[u].w, vx[n][u].z, vx[n][u].w);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[n][j] += scaled(p[j], sw[b], sx[b][n][j & 1]);
+          for (int u = 0; u < kU; ++u) {
+            mma_16x8<FP8>(p, va[u].x, vb[u].x, va[u].y, vb[u].y, vx[n][u].x, vx[n][u].y);
+            mma_16x8<FP8>(p, va[u].z, vb[u].z, va[u].w, vb[u].w, vx[n][u].z, vx[n][u].w);
           }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) c[n][j] += scaled(p[j], sw, sx[n][j & 1]);
         }
       }
     }
@@ -201,10 +196,10 @@ template <bool FP8>
 cudaError_t run(const FewGroupArgs& a, cudaStream_t s) {
   const unsigned tiles = unsigned((a.N + 15) / 16), slots = unsigned(a.G < a.M ? a.G : a.M);
   // warps per CTA as in skinny.cu
-  const int64_t steps = a.row_bytes / (kU * 64), ctas = int64_t(tiles) * slots, sms = num_sms();
+  const int64_t steps = a.row_bytes / (chunks_of(FP8) * 64), ctas = int64_t(tiles) * slots, sms = num_sms();
   const int rows = a.offsets == nullptr ? a.M : (a.M + a.G - 1) / a.G;
   if (rows <= 8) {
-    if (!FP8 && ctas <= sms && steps >= 32) return launch<FP8, 1, 32>(a, tiles, slots, s);
+    if (ctas <= sms && steps >= 32) return launch<FP8, 1, 32>(a, tiles, slots, s);
     if (ctas <= 2 * sms && steps >= 16) return launch<FP8, 1, 16>(a, tiles, slots, s);
     return launch<FP8, 1, 8>(a, tiles, slots, s);
   }

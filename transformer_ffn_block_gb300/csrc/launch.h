@@ -185,6 +185,10 @@ cudaError_t launch_few_rows(uint16_t* out, uint16_t* z, const void* x, const flo
                             int64_t N, int64_t K, bool fp8, bool w_mn, cudaStream_t s, bool late_wait = false);
 cudaError_t launch_few_rows_gated(uint16_t* out, const uint16_t* x, const uint16_t* w1, const uint16_t* dh, int act,
                                   int64_t M, int64_t C, int64_t H, cudaStream_t s);
+// E4M3 with block scales (E8M0):
+cudaError_t launch_few_rows_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
+                                   const uint8_t* w_scale, const uint16_t* bias, const uint16_t* res, int64_t M,
+                                   int64_t N, int64_t K, cudaStream_t s);
 cudaError_t few_rows_take_status(unsigned int* status);
 // Reads and clears the linear kernels' device status word of the current device.
 cudaError_t linear_take_status(unsigned int* status);

@@ -153,6 +153,12 @@ QFFN_DEVI uint64_t sdesc_sw128(uint32_t saddr) {
   return d;
 }
 
+// Descriptor of block scales to be copied to TMEM, 32 rows of 16 bytes: no swizzle,
+// groups of eight rows 128 bytes apart.
+QFFN_DEVI uint64_t sdesc_scales(uint32_t saddr) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | (uint64_t(16 >> 4) << 16) | (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
+}
+
 // Arrive once on the barrier at offset `bar` of every CTA in `mask` when all
 // previously issued MMAs of this thread have completed.
 QFFN_DEVI void mma_commit_mc(uint32_t bar, uint16_t mask) {
