@@ -1,10 +1,11 @@
 // Products grouped by expert and block-scaled products on the 5th-generation tensor
 // cores (tcgen05, sm_103a), groups of rows with a matrix each:
 //
-//   KIND_ROWS     out[m,n]   = bf16(sum_k x[m,k] w_g[n,k] (+ bias[n]) (+ in[m,n])),  m in group g;
-//                 bf16, or E4M3 with a power-of-two scale per block of 128
-//   KIND_ROWS_MN  dx[m,k]    = bf16(sum_n dout[m,n] w_g[n,k]): w read where it lies
-//   KIND_WEIGHT   dw_g[n,k]  = bf16(sum_{m in g} dout[m,n] x[m,k] (+ dw_g[n,k]))
+//   KIND_FORWARD   out[m,n]  = bf16(sum_k x[m,k] w_g[n,k] (+ bias[n]) (+ in[m,n])),  m in group g;
+//                  bf16, or E4M3 with a power-of-two scale per block of 128
+//   KIND_BACKWARD  dx[m,k]   = bf16(sum_n dout[m,n] w_g[n,k])  and
+//                  dw_g[n,k] = bf16(sum_{m in g} dout[m,n] x[m,k] (+ dw_g[n,k])), in one
+//                  launch; w, dout and x are read where they lie
 //
 // The pipeline is that of linear.cu: SM pairs, persistent over units of work, one
 // warp loads by TMA into a ring of stages (128 bytes of K each), one thread issues
@@ -12,7 +13,12 @@
 // accumulators while the other fills.  What is new:
 //
 // - The sizes of the groups are on the device.  Every CTA reads the offsets once
-//   into a table of units in shared memory; the roles look their units up there.
+//   into a table of units in shared memory; the roles look their units up there.  The
+//   widest unit is chosen there too, so that the units fill the pairs' rounds.
+// - The units of the weight gradients follow those of dx in one launch, the longest
+//   groups' first: one tail at the end, of the smallest units, instead of two (16384 rows
+//   unevenly in eight groups of 4096 x 2048 371 -> 360 us, 800 in 16 of 2048 x 1032, added,
+//   94 -> 86).
 // - The weights are the 256-row operand and the rows of x the other (as in linear.cu's
 //   exchanged form), so that the width of a unit, 32 to 256 rows of x, follows the
 //   group: its rows are spread evenly over its tiles, and a group of a few rows costs
@@ -44,7 +50,7 @@ namespace qffn {
 namespace {
 
 constexpr int OP_BF16 = 0, OP_BLOCKS = 1;
-constexpr int KIND_ROWS = 0, KIND_ROWS_MN = 1, KIND_WEIGHT = 2;
+constexpr int KIND_FORWARD = 0, KIND_BACKWARD = 1;
 
 constexpr int BM = 128;                    // weight rows per CTA (256 per pair)
 constexpr int ROW_BYTES = 128;             // one swizzle atom row
@@ -70,7 +76,7 @@ constexpr unsigned long long kDrainLimitNs = 200000000ull;
 constexpr int stage_k(int op) { return op == OP_BF16 ? 64 : 128; }   // elements of K per stage
 constexpr int max_bn(int op) { return op == OP_BF16 ? 256 : 224; }   // columns of an accumulator
 constexpr int num_threads(int op, int kind) {
-  return 32 * (2 + EPI_WARPS + (op == OP_BLOCKS ? SCALE_WARPS : kind == KIND_WEIGHT ? 1 : 0));
+  return 32 * (2 + EPI_WARPS + (op == OP_BLOCKS ? SCALE_WARPS : kind == KIND_BACKWARD ? 1 : 0));
 }
 constexpr int fixed_bytes(int op) {
   return STAGING_BYTES + (op == OP_BLOCKS ? SF_STAGES * SF_BYTES : 0) + NUM_BARS * 8 + 16;
@@ -89,21 +95,22 @@ QFFN_DEVI uint32_t idesc_for(int op, bool a_mn, bool b_mn, int n) {
 __device__ unsigned int g_status;
 
 struct GroupArgs {
-  uint16_t* out;
-  const uint16_t* bias;     // ROWS, optional
-  const uint16_t* in;       // what is added: [M, N], or the previous dw; optional
+  uint16_t* out;            // [M, N]; backward: dx (NULL: none)
+  uint16_t* dw;             // backward: [G, rows, N]
+  const uint16_t* bias;     // forward, optional
+  const uint16_t* in;       // what is added: [M, N], backward the previous dw; optional
   const uint8_t* x_scale;   // E4M3: [M, blocks] and [G, n_blocks, blocks]
   const uint8_t* w_scale;
   int blocks, n_blocks;
   const int* offsets;       // NULL: one group of all rows
-  int G, M;
-  int N;                    // values in a row of the output
-  int rows;                 // WEIGHT: rows of one matrix
-  int tiles_n;              // units of 256 across the output's row (WEIGHT: 256 across a matrix's rows times across its columns)
-  int tiles_k;              // WEIGHT: units of 256 across the columns
-  int bn_cap;               // ROWS: most rows of a unit, a multiple of 32
-  int band_n;               // ROWS: units across N that are swept together
-  int num_kb;               // ROWS: stages of K
+  int G, M, N;
+  int rows;                 // backward: rows of a matrix
+  int tiles_n;              // units of 256 across a row of N
+  int tiles_r;              // backward: units of 256 across a matrix's rows
+  int bn_cap;               // most rows of a unit, a multiple of 32
+  int choose;               // a narrower cap may be chosen from the groups' sizes
+  int band_n;               // units across N that are swept together
+  int num_kb;               // stages of K of out
   int accs;                 // accumulators: 2, or 1 where a unit is wider than half of TMEM allows
   int stages, stage_bytes;  // stage_bytes: with room for bn_cap / 2 rows of x
 };
@@ -151,21 +158,25 @@ QFFN_DEVI uint32_t pack2(uint64_t v) {
 QFFN_DEVI uint4 pack8(const uint64_t (&v)[4]) { return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3])); }
 
 // The table of units in shared memory: off[0 .. G] the offsets within 0 .. M, first[0
-// .. G] the number of the first unit of each group (ROWS).
+// .. G] the number of the first unit of out of each group; backward: order[0 .. G - 1] the
+// groups, those with rows (`busy` of them) first.
 struct Table {
   const int* off;
   const int* first;
+  const int* order;
+  int cap;            // most rows of a unit
+  int busy;
 };
 struct Unit {
   int group;
   int begin, rows;    // the group's rows
-  int row0, bn;       // ROWS: first row of the unit, its width
-  int nb, kb;         // 256-wide unit of the output's row (WEIGHT: of the matrix's rows, columns)
+  int row0, bn;       // of out: first row of the unit, its width
+  int nb, kb;         // 256-wide unit of the row of N (of dw: of the matrix's rows, and of the row)
 };
 
-QFFN_DEVI int group_rows(const Table& t, int g) { return max(t.off[g + 1] - t.off[g], 0); }
+QFFN_DEVI int group_rows(const int* off, int g) { return max(off[g + 1] - off[g], 0); }
 
-// Unit u of KIND_ROWS; `g`: the group of the last unit that this thread looked up.
+// Unit u of out; `g`: the group of the last unit that this thread looked up.
 QFFN_DEVI Unit rows_unit(int u, int& g, const Table& t, const GroupArgs& a) {
   if (u >= t.first[g + 1]) {
     int lo = g + 1, hi = a.G - 1;            // the last group whose first unit is u or before
@@ -179,9 +190,9 @@ QFFN_DEVI Unit rows_unit(int u, int& g, const Table& t, const GroupArgs& a) {
   Unit r;
   r.group = g;
   r.begin = t.off[g];
-  r.rows = group_rows(t, g);
+  r.rows = group_rows(t.off, g);
   // its rows in 32s, spread over tm tiles whose widths differ by 32 at most
-  const int parts = (r.rows + 31) >> 5, cap = a.bn_cap >> 5;
+  const int parts = (r.rows + 31) >> 5, cap = t.cap >> 5;
   const int tm = parts <= cap ? 1 : (parts + cap - 1) / cap;
   // bands of band_n; within a band, groups of GROUP_M tiles of rows sweep its columns, odd
   // groups backwards (see linear.cu)
@@ -207,29 +218,32 @@ QFFN_DEVI Unit rows_unit(int u, int& g, const Table& t, const GroupArgs& a) {
   r.kb = 0;
   return r;
 }
+// Unit u of the weight gradients of the groups with rows.
 QFFN_DEVI Unit weight_unit(int u, const Table& t, const GroupArgs& a) {
+  const int per_group = a.tiles_r * a.tiles_n;
   Unit r;
-  r.group = u / a.tiles_n;
+  const int at = u / per_group;
+  r.group = t.order[at];
   r.begin = t.off[r.group];
-  r.rows = group_rows(t, r.group);
-  const int k = u - r.group * a.tiles_n;
-  r.nb = k / a.tiles_k;
-  r.kb = k - r.nb * a.tiles_k;
+  r.rows = group_rows(t.off, r.group);
+  const int k = u - at * per_group;
+  r.nb = k / a.tiles_n;
+  r.kb = k - r.nb * a.tiles_n;
   r.row0 = 0;
   r.bn = 256;
   return r;
 }
 
 struct Maps {
-  CUtensorMap w;        // ROWS: the weights [G, rows, cols]; WEIGHT: dout
-  CUtensorMap x[4];     // ROWS: rows of x in boxes of 128, 64, 32, 16; WEIGHT: [0]: x
+  CUtensorMap w;        // the weights [G, rows, cols]
+  CUtensorMap x[4];     // rows of x (backward: of dout) in boxes of 128, 64, 32, 16
+  CUtensorMap dout_mn, x_mn;   // backward: boxes of 64 rows by 64 values
 };
 
 template <int OP, int KIND>
 __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     grouped_kernel(const __grid_constant__ Maps maps, const GroupArgs args) {
-  constexpr bool WEIGHT = KIND == KIND_WEIGHT;
-  constexpr bool A_MN = KIND != KIND_ROWS, B_MN = WEIGHT;
+  constexpr bool BACKWARD = KIND == KIND_BACKWARD;
   const uint32_t stage = uint32_t(args.stage_bytes);
   constexpr int ACC_COLS = max_bn(OP);
   extern __shared__ uint8_t smem_raw[];
@@ -242,13 +256,14 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* table_off = reinterpret_cast<int*>(tmem_slot + 4);
   int* table_first = table_off + args.G + 1;
-  const Table table{table_off, table_first};
+  int* table_order = table_first + args.G + 1;         // backward
+  int* found = table_order + (BACKWARD ? args.G : 0);  // the cap's costs, groups with rows
   const uint32_t bar0 = smem_u32(bars);
   // full[s] (leader): both CTAs' loads of stage s landed; empty[s]: the MMAs
   // reading stage s are done; tfull[a]: accumulator a is complete; tempty[a]
   // (leader): both CTAs' epilogue warps have read it; drain: all MMAs done;
   // sfull[s] (leader): both CTAs' scales of stage s are written; sempty[s]: copied;
-  // WEIGHT, a stage with rows behind its group: tail[s]: this CTA's loads landed,
+  // backward, a stage of dw with rows behind its group: tail[s]: this CTA's loads landed,
   // cleared[s] (leader): both CTAs have cleared those rows
   auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
   auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(MAX_STAGES + s); };
@@ -279,7 +294,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         mbar_init(sfull_bar(s), 2);
         mbar_init(sempty_bar(s), 1);
       }
-    if (WEIGHT)
+    if (BACKWARD)
       for (int s = 0; s < args.stages; ++s) {
         mbar_init(tail_bar(s), 1);
         mbar_init(cleared_bar(s), 2);
@@ -307,11 +322,31 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   for (int i = threadIdx.x; i <= args.G; i += num_threads(OP, KIND))
     table_off[i] = args.offsets != nullptr ? min(max(args.offsets[i], 0), args.M) : i == 0 ? 0 : args.M;
   __syncthreads();
-  if (!WEIGHT && warp == 0) {
+  Table table{table_off, table_first, table_order, args.bn_cap, 0};
+  if (!BACKWARD && args.choose != 0) {
+    // Where the widest units make few rounds: the width whose units take the least time, their
+    // rounds by a stage's cycles, 117 + 1.55 bn and 288 at least (see linear.cu); one width per
+    // warp.  (Not for more: narrower units keep less in flight.)
+    const int parts = (args.bn_cap >> 5) - warp;
+    if (warp < 8) {
+      int n = 0;
+      for (int i = lane; i < args.G && parts > 0; i += 32) n += (((group_rows(table_off, i) + 31) >> 5) + parts - 1) / parts;
+      n = int(__reduce_add_sync(0xffffffffu, unsigned(n)));
+      const int64_t rounds = (int64_t(n) * args.tiles_n + num_pairs - 1) / num_pairs;
+      const int64_t cost = rounds * max(288, 117 + 31 * (32 * parts) / 20);
+      if (lane == 0) found[warp] = parts > 0 && (warp > 0 || rounds <= 3) ? int(min(cost, int64_t(0x7FFFFFFE))) : warp > 0 ? 0x7FFFFFFF : -1;
+    }
+    __syncthreads();
+    int best = 0;
+    for (int i = 1; i < 8; ++i)
+      if (found[i] < found[best]) best = i;
+    table.cap -= 32 * best;
+  }
+  if (warp == 0) {
     int total = 0;
     for (int base = 0; base < args.G; base += 32) {
       const int i = base + lane;
-      int n = i < args.G ? (group_rows(table, i) + args.bn_cap - 1) / args.bn_cap * args.tiles_n : 0;
+      int n = i < args.G ? (group_rows(table_off, i) + table.cap - 1) / table.cap * args.tiles_n : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int below = __shfl_up_sync(0xffffffffu, n, o);
@@ -322,42 +357,72 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     }
     if (lane == 0) table_first[0] = 0;
   }
+  if (BACKWARD) {
+    // the groups in the order of their weight gradients: the longest first, up to 256 of them
+    // (each counts those before it); more as they come, those without rows last
+    if (args.G <= 256) {
+      const int i = int(threadIdx.x), n = i < args.G ? group_rows(table_off, i) : 0;
+      if (i < args.G) {
+        int at = 0;
+#pragma unroll 4
+        for (int j = 0; j < args.G; ++j) {
+          const int m = group_rows(table_off, j);
+          at += m > n || (m == n && j < i) ? 1 : 0;
+        }
+        table_order[at] = i;
+      }
+      table.busy = __syncthreads_count(n > 0);
+    } else {
+      if (warp == 1) {
+        int busy = 0;
+        for (int base = 0; base < args.G; base += 32) {
+          const int i = base + lane;
+          const bool rows = i < args.G && group_rows(table_off, i) > 0;
+          const uint32_t some = __ballot_sync(0xffffffffu, rows);
+          const int before = busy + __popc(some & ((1u << lane) - 1u));
+          if (i < args.G) table_order[rows ? before : args.G - 1 - (i - before)] = i;
+          busy += __popc(some);
+        }
+        if (lane == 0) found[8] = busy;
+      }
+      __syncthreads();
+      table.busy = found[8];
+    }
+  }
   __syncthreads();
 
-  const int num_units = WEIGHT ? args.G * args.tiles_n : table_first[args.G];
+  // Units: of out (rows_units of them), then of dw.  This pair's in round r:
+  const int rows_units = BACKWARD && args.out == nullptr ? 0 : table_first[args.G];
+  const int num_units = rows_units + (BACKWARD ? table.busy * args.tiles_r * args.tiles_n : 0);
+  auto number = [&](int r) { return r * num_pairs + pair; };
   int group_cursor = 0;
-  auto unit_at = [&](int u) { return WEIGHT ? weight_unit(u, table, args) : rows_unit(u, group_cursor, table, args); };
-  // the units of this pair in order; empty groups have none here (their dw is cleared at the end)
-  auto next_unit = [&](int u) {
-    u += num_pairs;
-    if (WEIGHT)
-      while (u < num_units && group_rows(table, u / args.tiles_n) == 0) u += num_pairs;
-    return u;
+  auto unit_at = [&](int u) {
+    return BACKWARD && u >= rows_units ? weight_unit(u - rows_units, table, args) : rows_unit(u, group_cursor, table, args);
   };
-  auto first_unit = [&]() { return next_unit(pair - num_pairs); };
   // stages of K of a unit
-  auto stages_of = [&](const Unit& u) { return WEIGHT ? (u.rows + 63) / 64 : args.num_kb; };
+  auto stages_of = [&](const Unit& u, bool weight) { return weight ? (u.rows + 63) / 64 : args.num_kb; };
 
   if (warp == 0) {
     if (elect_one()) {
       // ------------------------------------------------------------ producer
       uint32_t issued = 0, issued_parity = 0, ph = 0;
-      uint32_t tails = 0, tail_parity = 0;   // WEIGHT: stages whose tail barrier was armed, and its phase now
+      uint32_t tails = 0, tail_parity = 0;   // stages whose tail barrier was armed, and its phase now
       int s = 0;
       bool ok = true;
-      for (int un = first_unit(); ok && un < num_units; un = next_unit(un)) {
+      for (int r = 0, un = number(0); ok && un < num_units; un = number(++r)) {
         const Unit u = unit_at(un);
+        const bool weight = BACKWARD && un >= rows_units;
         const int row_w = u.nb * (2 * BM) + int(rank) * BM;      // of the 256-row operand
         const int half = u.bn / 2;
-        const int row_x = WEIGHT ? u.kb * 256 + int(rank) * 128 : u.row0 + int(rank) * half;
+        const int row_x = weight ? u.kb * 256 + int(rank) * 128 : u.row0 + int(rank) * half;
         const uint32_t stage_tx = 2u * uint32_t(OP_BYTES + half * ROW_BYTES);
-        const int num = stages_of(u);
+        const int num = stages_of(u, weight);
         for (int kb = 0; kb < num; ++kb) {
           if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) { ok = false; break; }
           const int k0 = kb * stage_k(OP);
           // a stage with rows behind the group completes on this CTA's own barrier, for the
           // warp that clears them
-          const bool tail = WEIGHT && k0 + 64 > u.rows;
+          const bool tail = weight && k0 + 64 > u.rows;
           if (rank == 0) {
             if (tail) mbar_arrive(full_bar(s));
             else mbar_expect_tx(full_bar(s), stage_tx);
@@ -370,14 +435,14 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
           const uint32_t fb = tail ? map_to_rank(tail_bar(s), rank) : map_to_rank(full_bar(s), 0);
           const uint32_t da = ring + uint32_t(s) * stage;
           uint32_t db = da + uint32_t(OP_BYTES);
-          if (WEIGHT) {
+          if (weight) {
             const int row = u.begin + k0;
-            tma_load_2d_pair(da, &maps.w, fb, row_w, row);
-            tma_load_2d_pair(da + MN_BOX_BYTES, &maps.w, fb, row_w + 64, row);
-            tma_load_2d_pair(db, &maps.x[0], fb, row_x, row);
-            tma_load_2d_pair(db + MN_BOX_BYTES, &maps.x[0], fb, row_x + 64, row);
+            tma_load_2d_pair(da, &maps.dout_mn, fb, row_w, row);
+            tma_load_2d_pair(da + MN_BOX_BYTES, &maps.dout_mn, fb, row_w + 64, row);
+            tma_load_2d_pair(db, &maps.x_mn, fb, row_x, row);
+            tma_load_2d_pair(db + MN_BOX_BYTES, &maps.x_mn, fb, row_x + 64, row);
           } else {
-            if (A_MN) {
+            if (BACKWARD) {
               tma_load_3d_pair(da, &maps.w, fb, row_w, k0, u.group);
               tma_load_3d_pair(da + MN_BOX_BYTES, &maps.w, fb, row_w + 64, k0, u.group);
             } else {
@@ -405,7 +470,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       // the MMAs' last arrivals reach this CTA
       for (int k = 0; k < args.stages; ++k)
         if (issued & (1u << k)) {
-          if (WEIGHT && (tails & (1u << k)))
+          if (BACKWARD && (tails & (1u << k)))
             mbar_wait(tail_bar(k), ((tail_parity >> k) & 1u) ^ 1u, abort_flag, false, kDrainLimitNs);
           if (rank == 0) mbar_wait(full_bar(k), (issued_parity >> k) & 1u, abort_flag, false, kDrainLimitNs);
           mbar_wait(empty_bar(k), (issued_parity >> k) & 1u, abort_flag, false, kDrainLimitNs);
@@ -418,15 +483,16 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       int s = 0, local = 0, chunk = 0;
       uint32_t ph = 0, cleared_parity = 0;
       bool ok = true;
-      for (int un = first_unit(); ok && un < num_units; un = next_unit(un), ++local) {
+      for (int un = number(0); ok && un < num_units; un = number(++local)) {
         const int acc = local & (args.accs - 1);
         const uint32_t aph = uint32_t(local >> (args.accs - 1)) & 1u;
         if (!mbar_wait_cluster_bounded(tempty_bar(acc), aph ^ 1u, abort_flag, &g_status, kWaitLimitNs)) break;
         tc_fence_after();
         const Unit u = unit_at(un);
+        const bool weight = BACKWARD && un >= rows_units;
         const uint32_t d_tmem = tmem_base + uint32_t(acc * ACC_COLS);
-        const uint32_t idesc = idesc_for(OP, A_MN, B_MN, u.bn);
-        const int num = stages_of(u);
+        const uint32_t idesc = idesc_for(OP, BACKWARD, weight, u.bn);
+        const int num = stages_of(u, weight);
         uint32_t sf = 0;                     // TMEM columns of the current scales
         bool ready = false;                  // the next stage was there before this one's MMAs were issued
         for (int kb = 0; kb < num; ++kb) {
@@ -446,7 +512,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
             ++chunk;
           }
           if (!ready && !mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
-          if (WEIGHT && kb * 64 + 64 > u.rows) {
+          if (weight && kb * 64 + 64 > u.rows) {
             if (!mbar_wait_cluster_bounded(cleared_bar(s), (cleared_parity >> s) & 1u, abort_flag, &g_status, kWaitLimitNs)) {
               ok = false;
               break;
@@ -465,11 +531,15 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
             const uint32_t id = idesc | (which << 4) | (which << 29);
 #pragma unroll
             for (int i = 0; i < STEPS; ++i)
-              mma_pair_blocks(d_tmem, step_desc<A_MN>(a0, i), step_desc<B_MN>(b0, i), id, sf, sf + 4, uint32_t(kb | i));
+              mma_pair_blocks(d_tmem, step_desc<false>(a0, i), step_desc<false>(b0, i), id, sf, sf + 4, uint32_t(kb | i));
+          } else if (weight) {
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i)
+              mma_pair_f16(d_tmem, step_desc<true>(a0, i), step_desc<true>(b0, i), idesc, uint32_t(kb | i));
           } else {
 #pragma unroll
             for (int i = 0; i < STEPS; ++i)
-              mma_pair_f16(d_tmem, step_desc<A_MN>(a0, i), step_desc<B_MN>(b0, i), idesc, uint32_t(kb | i));
+              mma_pair_f16(d_tmem, step_desc<BACKWARD>(a0, i), step_desc<false>(b0, i), idesc, uint32_t(kb | i));
           }
           mma_commit_mc(empty, kBothCtas);
         }
@@ -503,7 +573,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     int c = mine;
     uint32_t fills = 0;
     bool ok = true;
-    for (int un = first_unit(); ok && un < num_units; un = next_unit(un), c -= chunks) {
+    for (int r = 0, un = number(0); ok && un < num_units; un = number(++r), c -= chunks) {
       if (c >= chunks) continue;
       const Unit u = unit_at(un);
       const int block_w = min(u.nb * 2 + int(rank), args.n_blocks - 1);
@@ -532,15 +602,16 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     // the issuer's last arrival on this stage reaches this CTA
     if (ok && fills > 0) mbar_wait(sempty_bar(mine), (fills & 1u) ^ 1u, abort_flag, false, kDrainLimitNs);
     __syncwarp();
-  } else if (WEIGHT && warp >= 2 + EPI_WARPS) {
+  } else if (BACKWARD && warp >= 2 + EPI_WARPS) {
     // -------------------------------------------------------------- rows behind a group
-    // The last stage of a unit: rows behind the group's end are overwritten with zeros in
-    // the four boxes of this CTA's operands (row r of a box is its bytes 128 r ..).
+    // The last stage of a unit of dw: rows behind the group's end are overwritten with zeros
+    // in the four boxes of this CTA's operands (row r of a box is its bytes 128 r ..).
     uint32_t parity = 0;
     int s = 0;
-    for (int un = first_unit(); un < num_units; un = next_unit(un)) {
-      const Unit u = unit_at(un);
-      const int num = stages_of(u), live = u.rows - (num - 1) * 64;
+    for (int r = 0, un = number(0); un < num_units; un = number(++r)) {
+      const bool weight = un >= rows_units;
+      const Unit u = weight ? unit_at(un) : Unit{};
+      const int num = stages_of(u, weight), live = weight ? u.rows - (num - 1) * 64 : 64;
       s = (s + num - 1) % args.stages;
       if (live < 64) {
         if (!__all_sync(0xffffffffu, mbar_wait(tail_bar(s), (parity >> s) & 1u, abort_flag))) break;
@@ -564,15 +635,14 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     constexpr int WG = EPI_WARPS / 4;
     const int q = warp & 3, wg = (warp - 2) >> 2;
     const uint32_t box = smem_u32(sStaging + (q * WG + wg) * STAGING_BOX);
-    int local = 0;
-    int un = first_unit(), next = un < num_units ? next_unit(un) : un;
-    if (!WEIGHT) {
-      // the lane is a column of the output, the accumulator's columns its rows, 32 at a time
+    int local = 0, un = number(0);
+    {
+      // out: the lane is a column of the output, the accumulator's columns its rows, 32 at a time
       const int sub = lane >> 2, ch = lane & 3;
       const uint32_t col32 = box + uint32_t(lane) * 4u;
       const uint32_t turn32 = box + uint32_t(sub) * 128u + (uint32_t((2 * ch) ^ sub) << 4);
       const size_t step = size_t(8) * size_t(args.N);
-      for (; un < num_units; ++local) {
+      for (; un < rows_units; un = number(++local)) {
         const int acc = local & (args.accs - 1);
         const uint32_t aph = uint32_t(local >> (args.accs - 1)) & 1u;
         const Unit u = unit_at(un);
@@ -591,7 +661,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
           return v;
         };
         uint64_t bias[4] = {0ull, 0ull, 0ull, 0ull};
-        if (args.bias != nullptr && col < args.N) {
+        if (!BACKWARD && args.bias != nullptr && col < args.N) {
           const uint4 b = ld16_settled(bias_row + col);
           bias[0] = bf16x2_to_f2(b.x);
           bias[1] = bf16x2_to_f2(b.y);
@@ -607,12 +677,10 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
             if ((live >> i) & 1u) next_in[i] = ld16_stream(args.in + (at + size_t(4 * g + i) * step));
           }
         };
-        if (args.in != nullptr) request(g0);
-        if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) break;
+        if (!BACKWARD && args.in != nullptr) request(g0);
+        if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) { un = num_units; break; }
         tc_fence_after();
-        const int next2 = next < num_units ? next_unit(next) : next;
-        // another unit takes this accumulator
-        const bool awaited = next < num_units && (args.accs == 1 || next2 < num_units);
+        const bool awaited = number(local + args.accs) < num_units;   // another unit takes this accumulator
         auto loaded = [&](int g) {
           if (g + 1 >= g1) {
             tc_fence_before();
@@ -627,7 +695,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
           tmem_ld32(tbase + uint32_t(g * 32), v);
           loaded(g);
           uint4 in4[4];
-          if (args.in != nullptr) {
+          if (!BACKWARD && args.in != nullptr) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) in4[i] = next_in[i];
             request(g + 1);
@@ -648,11 +716,11 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
                              f2_pack(__uint_as_float(los[i].z), __uint_as_float(los[i].w)),
                              f2_pack(__uint_as_float(his[i].x), __uint_as_float(his[i].y)),
                              f2_pack(__uint_as_float(his[i].z), __uint_as_float(his[i].w))};
-            if (args.bias != nullptr) {
+            if (!BACKWARD && args.bias != nullptr) {
 #pragma unroll
               for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bias[j]);
             }
-            if (args.in != nullptr) {
+            if (!BACKWARD && args.in != nullptr) {
               const uint32_t iw[4] = {in4[i].x, in4[i].y, in4[i].z, in4[i].w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bf16x2_to_f2(iw[j]));
@@ -660,10 +728,9 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
             if ((live >> i) & 1u) stg16(args.out + (at + size_t(4 * g + i) * step), pack8(z));
           }
         }
-        un = next;
-        next = next2;
       }
-    } else {
+    }
+    if constexpr (BACKWARD) {
       // dw (+)= the sums: the lane is a row of the matrix; 64 columns at a time through a box
       // of 32 rows x 128 bytes (chunk c of row r at c ^ (r & 7)), whole 128-byte lines
       const int sub8 = lane >> 3, ch8 = lane & 7;
@@ -695,18 +762,21 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
           if ((live >> i) & 1u) d[i] = ld16_stream(args.in + (p.at + size_t(g * 64) + size_t(i) * step4));
         }
       };
-      Part p = part_of(weight_unit(min(un, num_units - 1), table, args));
-      if (args.in != nullptr && un < num_units) {
-        request(p, 0, in8[0]);
-        request(p, 1, in8[1]);
+      Part p{};
+      if (un < num_units) {
+        p = part_of(unit_at(un));
+        if (args.in != nullptr) {
+          request(p, 0, in8[0]);
+          request(p, 1, in8[1]);
+        }
       }
-      for (; un < num_units; ++local) {
+      for (; un < num_units; un = number(++local)) {
         const int acc = local & (args.accs - 1);
         const uint32_t aph = uint32_t(local >> (args.accs - 1)) & 1u;
         const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * ACC_COLS);
-        const int next2 = next < num_units ? next_unit(next) : next;
-        const bool awaited = next < num_units && next2 < num_units;
-        const Part p_next = part_of(weight_unit(next < num_units ? next : un, table, args));
+        const int next = number(local + 1);
+        const bool awaited = number(local + 2) < num_units;
+        const Part p_next = part_of(unit_at(next < num_units ? next : un));
         if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) break;
         tc_fence_after();
 #pragma unroll
@@ -746,7 +816,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
           }
           __syncwarp();
           const uint32_t live = p.col + g * 64 < args.N ? p.rows : 0u;
-          uint16_t* const dst = args.out + (p.at + size_t(g * 64));
+          uint16_t* const dst = args.dw + (p.at + size_t(g * 64));
           uint4 o[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = lds16((turn8 ^ uint32_t((i & 1) << 6)) + 512u * i);
@@ -754,14 +824,12 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
           for (int i = 0; i < 8; ++i)
             if ((live >> i) & 1u) stg16(dst + size_t(i) * step4, o[i]);
         }
-        un = next;
-        next = next2;
         p = p_next;
       }
       // the gradient of a matrix without rows is zero, or what it was when adding
-      if (args.in == nullptr)
-        for (int e = pair; e < num_units; e += num_pairs) {
-          if (group_rows(table, e / args.tiles_n) != 0) continue;
+      if (args.in == nullptr && *abort_flag == 0) {
+        const int per_group = args.tiles_r * args.tiles_n;
+        for (int e = table.busy * per_group + pair; e < args.G * per_group; e += num_pairs) {
           const Part z = part_of(weight_unit(e, table, args));
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -769,9 +837,10 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
             const uint32_t live = z.col + g * 64 < args.N ? z.rows : 0u;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if ((live >> i) & 1u) stg16(args.out + (z.at + size_t(g * 64) + size_t(i) * step4), make_uint4(0, 0, 0, 0));
+              if ((live >> i) & 1u) stg16(args.dw + (z.at + size_t(g * 64) + size_t(i) * step4), make_uint4(0, 0, 0, 0));
           }
         }
+      }
     }
   }
 
@@ -826,7 +895,7 @@ cudaError_t max_pairs(int* pairs) {
 // `units`: no fewer than the kernel will find (if the offsets do not decrease)
 template <int OP, int KIND>
 cudaError_t launch(const Maps& m, GroupArgs a, int64_t units, int pairs, cudaStream_t s) {
-  const int table = 8 * (a.G + 1);
+  const int table = (KIND == KIND_BACKWARD ? 12 : 8) * (a.G + 1) + 48;
   const bool wide = a.bn_cap > max_bn(OP);
   a.accs = wide ? 1 : 2;
   // (narrow units: more stages, whose loads' latency is what bounds them; 512 x 4096 x 2048
@@ -880,19 +949,17 @@ int choose_cap(int op, int64_t G, int64_t M, int tiles_n, int pairs) {
   return best_cap;
 }
 
-// out [M, N] from x [M, K] and w [G, N, K] (KIND_ROWS) or [G, K, N] (KIND_ROWS_MN).
-template <int OP, int KIND>
-cudaError_t rows_product(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w, const uint8_t* w_scale,
-                         const uint16_t* bias, const uint16_t* in, const int* offsets, int64_t G, int64_t M, int64_t N,
-                         int64_t K, cudaStream_t s) {
+// out [M, N] from x [M, K] and w [G, N, K].
+template <int OP>
+cudaError_t forward(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w, const uint8_t* w_scale,
+                    const uint16_t* bias, const uint16_t* in, const int* offsets, int64_t G, int64_t M, int64_t N,
+                    int64_t K, cudaStream_t s) {
   constexpr bool BF16 = OP == OP_BF16;
   const int64_t bytes = BF16 ? 2 : 1;
-  Maps m;
-  const bool ok_w = KIND == KIND_ROWS_MN ? make_operand_map_3d(&m.w, w, BF16, G, K, N, N * bytes, K * N * bytes, 64)
-                                         : make_operand_map_3d(&m.w, w, BF16, G, N, K, K * bytes, K * N * bytes, 128);
-  if (!ok_w) return cudaErrorInvalidValue;
-  for (int b = 0; b < 4; ++b)
-    if (!make_operand_map(&m.x[b], x, BF16, M, K, 128 >> b)) return cudaErrorInvalidValue;
+  Maps m{};
+  bool ok = make_operand_map_3d(&m.w, w, BF16, G, N, K, K * bytes, K * N * bytes, 128);
+  for (int b = 0; ok && b < 4; ++b) ok = make_operand_map(&m.x[b], x, BF16, M, K, 128 >> b);
+  if (!ok) return cudaErrorInvalidValue;
   GroupArgs a{};
   a.out = out;
   a.bias = bias;
@@ -907,39 +974,47 @@ cudaError_t rows_product(uint16_t* out, const void* x, const uint8_t* x_scale, c
   a.N = int(N);
   a.tiles_n = ceil_div(N, 2 * BM);
   int pairs = 0;
-  const cudaError_t e = max_pairs<OP, KIND>(&pairs);
+  const cudaError_t e = max_pairs<OP, KIND_FORWARD>(&pairs);
   if (e != cudaSuccess) return e;
   a.bn_cap = choose_cap(OP, G, M, a.tiles_n, pairs);
+  a.choose = G > 1 && a.bn_cap <= max_bn(OP);
   a.num_kb = ceil_div(K, stage_k(OP));
   // bands of about 32 MB of weights where they are the larger operand (see linear.cu)
   const int64_t band = (int64_t(32) << 20) / (2 * BM * K * bytes);
   a.band_n = N <= M / G || band >= a.tiles_n ? a.tiles_n : band < 1 ? 1 : int(band);
-  const int64_t units = (M / a.bn_cap + (G < M ? G : M)) * a.tiles_n;
-  return launch<OP, KIND>(m, a, units, pairs, s);
+  // (a cap chosen on the device is 32 at least)
+  const int64_t units = (M / (a.choose ? 32 : a.bn_cap) + (G < M ? G : M)) * a.tiles_n;
+  return launch<OP, KIND_FORWARD>(m, a, units, pairs, s);
 }
 
-// dw [G, N, K] (+)= dout [M, N]^T . x [M, K] by group.
-cudaError_t weight_product(uint16_t* dw, const uint16_t* dout, const uint16_t* x, const int* offsets, int64_t G,
-                           int64_t M, int64_t N, int64_t K, bool accumulate, cudaStream_t s) {
-  Maps m;
-  if (!make_operand_map(&m.w, dout, true, M, N, 64) || !make_operand_map(&m.x[0], x, true, M, K, 64))
-    return cudaErrorInvalidValue;
-  m.x[1] = m.x[2] = m.x[3] = m.x[0];
+// dx [M, K] (NULL: none) and dw [G, N, K] (+)= from dout [M, N], x [M, K] and w [G, N, K].
+cudaError_t backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uint16_t* x, const uint16_t* w,
+                     const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K, bool accumulate, cudaStream_t s) {
+  Maps m{};
+  bool ok = make_operand_map_3d(&m.w, w, true, G, N, K, K * 2, K * N * 2, 64) &&
+            make_operand_map(&m.dout_mn, dout, true, M, N, 64) && make_operand_map(&m.x_mn, x, true, M, K, 64);
+  for (int b = 0; ok && b < 4; ++b) ok = make_operand_map(&m.x[b], dout, true, M, N, 128 >> b);
+  if (!ok) return cudaErrorInvalidValue;
   GroupArgs a{};
-  a.out = dw;
+  a.out = dx;
+  a.dw = dw;
   a.in = accumulate ? dw : nullptr;
   a.offsets = offsets;
   a.G = int(G);
   a.M = int(M);
   a.N = int(K);
   a.rows = int(N);
-  a.tiles_k = ceil_div(K, 256);
-  a.tiles_n = ceil_div(N, 256) * a.tiles_k;
-  a.bn_cap = 256;
+  a.tiles_n = ceil_div(K, 256);
+  a.tiles_r = ceil_div(N, 256);
+  a.bn_cap = max_bn(OP_BF16);
+  a.num_kb = ceil_div(N, 64);
+  const int64_t band = (int64_t(32) << 20) / (2 * BM * N * 2);
+  a.band_n = K <= M / G || band >= a.tiles_n ? a.tiles_n : band < 1 ? 1 : int(band);
   int pairs = 0;
-  const cudaError_t e = max_pairs<OP_BF16, KIND_WEIGHT>(&pairs);
+  const cudaError_t e = max_pairs<OP_BF16, KIND_BACKWARD>(&pairs);
   if (e != cudaSuccess) return e;
-  return launch<OP_BF16, KIND_WEIGHT>(m, a, int64_t(a.tiles_n) * G, pairs, s);
+  const int64_t units = int64_t(a.tiles_r) * a.tiles_n * G + (dx != nullptr ? (M / a.bn_cap + (G < M ? G : M)) * a.tiles_n : 0);
+  return launch<OP_BF16, KIND_BACKWARD>(m, a, units, pairs, s);
 }
 
 }  // namespace
@@ -949,7 +1024,7 @@ cudaError_t launch_linear_blocks(uint16_t* out, const uint8_t* x, const uint8_t*
                                  int64_t K, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
   if (M <= 32) return launch_few_groups(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
-  return rows_product<OP_BLOCKS, KIND_ROWS>(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
+  return forward<OP_BLOCKS>(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
 }
 
 cudaError_t launch_grouped(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w, const uint8_t* w_scale,
@@ -957,20 +1032,15 @@ cudaError_t launch_grouped(uint16_t* out, const void* x, const uint8_t* x_scale,
   if (M == 0) return cudaSuccess;
   if (M <= 32) return launch_few_groups(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, s);
   if (x_scale != nullptr)
-    return rows_product<OP_BLOCKS, KIND_ROWS>(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, s);
-  return rows_product<OP_BF16, KIND_ROWS>(out, x, nullptr, w, nullptr, nullptr, nullptr, offsets, G, M, N, K, s);
+    return forward<OP_BLOCKS>(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, s);
+  return forward<OP_BF16>(out, x, nullptr, w, nullptr, nullptr, nullptr, offsets, G, M, N, K, s);
 }
 
 cudaError_t launch_grouped_backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uint16_t* x,
                                     const uint16_t* w, const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K,
                                     bool accumulate, cudaStream_t s) {
   if (M == 0) return accumulate ? cudaSuccess : cudaMemsetAsync(dw, 0, size_t(G) * size_t(N) * size_t(K) * 2, s);
-  if (dx != nullptr) {
-    const cudaError_t e =
-        rows_product<OP_BF16, KIND_ROWS_MN>(dx, dout, nullptr, w, nullptr, nullptr, nullptr, offsets, G, M, K, N, s);
-    if (e != cudaSuccess) return e;
-  }
-  return weight_product(dw, dout, x, offsets, G, M, N, K, accumulate, s);
+  return backward(dx, dw, dout, x, w, offsets, G, M, N, K, accumulate, s);
 }
 
 cudaError_t grouped_take_status(unsigned int* status) {
