@@ -423,18 +423,26 @@ __global__ void __launch_bounds__(kThreads)
     // 64, l + 96 of x; the 128 weight rows have one word.
     const int chunks = (kb1 - kb0 + 3) / 4;
     const uint8_t* const wb = args.w_blocks + size_t(tile) * size_t(args.blocks);
+    const bool whole = ((reinterpret_cast<uintptr_t>(args.x_blocks) | reinterpret_cast<uintptr_t>(args.w_blocks) | uintptr_t(args.blocks | kb0)) & 3u) == 0;
+    auto word = [&](const uint8_t* p, int n) {
+      if (whole) return *reinterpret_cast<const uint32_t*>(p);
+      uint32_t v = p[0];
+      if (n > 1) v |= uint32_t(p[1]) << 8;
+      if (n > 2) v |= uint32_t(p[2]) << 16;
+      if (n > 3) v |= uint32_t(p[3]) << 24;
+      return v;
+    };
     bool going = true;
     for (int c = warp - 3; going && c < chunks; c += 2) {
       const int first = kb0 + 4 * c, n = min(4, kb1 - first);
-      uint32_t word_w = 0u, word_x[4];
-      for (int j = 0; j < n; ++j) word_w |= uint32_t(wb[first + j]) << (8 * j);
+      const uint32_t word_w = word(wb + first, n);
+      uint32_t word_x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         word_x[i] = 0u;
         if (32 * i < args.bn) {
           const size_t row = size_t(min(mt * args.bn + 32 * i + lane, args.M - 1));
-          const uint8_t* const p = args.x_blocks + row * size_t(args.blocks) + size_t(first);
-          for (int j = 0; j < n; ++j) word_x[i] |= uint32_t(p[j]) << (8 * j);
+          word_x[i] = word(args.x_blocks + row * size_t(args.blocks) + size_t(first), n);
         }
       }
       const int ss = c % kScaleStages;

@@ -25,9 +25,10 @@
 //   its weights' bytes and no more.  The rows of x come in boxes of 128, 64, 32 and 16
 //   rows.
 // - The weight gradient's contraction runs over a group's rows, which end anywhere. The
-//   last stage of a unit may hold rows of the next group; a warp overwrites them with
-//   zeros in shared memory before the MMAs read the stage, in both operands, so that
-//   neither finite values nor NaN of a neighbour meet a group.
+//   last stage of a unit may hold rows of the next group: only the MMAs (of 16 rows) that
+//   the group reaches are issued, and a warp overwrites the rows behind it in the last of
+//   them with zeros in shared memory, in both operands, so that neither finite values nor
+//   NaN of a neighbour meet a group.
 // - E4M3: tcgen05.mma.kind::mxf8f6f4.block_scale takes E8M0 scales for every 32
 //   values of K from TMEM; a scale per 128 is the same byte in four MMAs.  Four warps
 //   read the scales of 512 of K at a time (one byte per row of x and block, one per
@@ -57,13 +58,14 @@ constexpr int ROW_BYTES = 128;             // one swizzle atom row
 constexpr int OP_BYTES = 128 * ROW_BYTES;  // an operand's share of a stage: 128 rows of one swizzle row
 constexpr int MN_BOX_BYTES = 64 * ROW_BYTES;   // MN-major: 64 values by 64 of K, two boxes to the share
 constexpr int STEPS = 4;                   // MMAs per stage (32 bytes of K each)
+// (Sixteen warps in the backward's epilogue, us against eight: 1 row in each of 64 groups of
+// 2048 x 1024 55 / 60, 1000 in each of eight of 4096 x 2048 179 / 166.)
 constexpr int EPI_WARPS = 8;
 constexpr int SCALE_WARPS = 4;
 constexpr int MAX_STAGES = 10;
 constexpr int SF_STAGES = SCALE_WARPS;     // stages of scales, 512 of K each, one for each warp that fills them
 constexpr int SF_BYTES = 3 * 512;          // 128 weight rows, 256 rows of x: 4 bytes each
 constexpr int STAGING_BOX = 32 * 128;      // a warp's transposing box: 32 rows x 32 fp32
-constexpr int STAGING_BYTES = EPI_WARPS * STAGING_BOX;
 constexpr int NUM_BARS = 4 * MAX_STAGES + 5 + 2 * SF_STAGES;
 constexpr int SMEM_LIMIT = 227 * 1024 - 1024;  // (behind the alignment to 1024 bytes)
 constexpr int TMEM_COLS = 512;
@@ -79,7 +81,7 @@ constexpr int num_threads(int op, int kind) {
   return 32 * (2 + EPI_WARPS + (op == OP_BLOCKS ? SCALE_WARPS : kind == KIND_BACKWARD ? 1 : 0));
 }
 constexpr int fixed_bytes(int op) {
-  return STAGING_BYTES + (op == OP_BLOCKS ? SF_STAGES * SF_BYTES : 0) + NUM_BARS * 8 + 16;
+  return EPI_WARPS * STAGING_BOX + (op == OP_BLOCKS ? SF_STAGES * SF_BYTES : 0) + NUM_BARS * 8 + 16;
 }
 constexpr int SF_TMEM = 448;               // first column of the scales: two slots of 16
 
@@ -230,9 +232,12 @@ QFFN_DEVI Unit weight_unit(int u, const Table& t, const GroupArgs& a) {
   r.nb = k / a.tiles_n;
   r.kb = k - r.nb * a.tiles_n;
   r.row0 = 0;
-  r.bn = 256;
+  r.bn = a.N - r.kb * 256 <= 128 ? 128 : 256;
   return r;
 }
+
+// Whether a stage of dw whose group has `left` more rows holds rows behind it in an MMA's 16.
+QFFN_DEVI bool rows_to_clear(int left) { return left < 64 && (left & 15) != 0; }
 
 struct Maps {
   CUtensorMap w;        // the weights [G, rows, cols]
@@ -250,7 +255,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t ring = smem_u32(smem);
   uint8_t* sStaging = smem + args.stages * args.stage_bytes;
-  uint8_t* sScales = sStaging + STAGING_BYTES;
+  uint8_t* sScales = sStaging + EPI_WARPS * STAGING_BOX;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sScales + (OP == OP_BLOCKS ? SF_STAGES * SF_BYTES : 0));
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -414,21 +419,21 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         const bool weight = BACKWARD && un >= rows_units;
         const int row_w = u.nb * (2 * BM) + int(rank) * BM;      // of the 256-row operand
         const int half = u.bn / 2;
-        const int row_x = weight ? u.kb * 256 + int(rank) * 128 : u.row0 + int(rank) * half;
+        const int row_x = (weight ? u.kb * 256 : u.row0) + int(rank) * half;
         const uint32_t stage_tx = 2u * uint32_t(OP_BYTES + half * ROW_BYTES);
         const int num = stages_of(u, weight);
         for (int kb = 0; kb < num; ++kb) {
           if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) { ok = false; break; }
           const int k0 = kb * stage_k(OP);
-          // a stage with rows behind the group completes on this CTA's own barrier, for the
-          // warp that clears them
-          const bool tail = weight && k0 + 64 > u.rows;
+          // a stage with rows to be cleared completes on this CTA's own barrier, for the warp
+          // that does
+          const bool tail = weight && rows_to_clear(u.rows - k0);
           if (rank == 0) {
             if (tail) mbar_arrive(full_bar(s));
             else mbar_expect_tx(full_bar(s), stage_tx);
           }
           if (tail) {
-            mbar_expect_tx(tail_bar(s), uint32_t(2 * OP_BYTES));
+            mbar_expect_tx(tail_bar(s), stage_tx / 2u);
             tails |= 1u << s;
             tail_parity ^= 1u << s;
           }
@@ -440,7 +445,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
             tma_load_2d_pair(da, &maps.dout_mn, fb, row_w, row);
             tma_load_2d_pair(da + MN_BOX_BYTES, &maps.dout_mn, fb, row_w + 64, row);
             tma_load_2d_pair(db, &maps.x_mn, fb, row_x, row);
-            tma_load_2d_pair(db + MN_BOX_BYTES, &maps.x_mn, fb, row_x + 64, row);
+            if (half > 64) tma_load_2d_pair(db + MN_BOX_BYTES, &maps.x_mn, fb, row_x + 64, row);
           } else {
             if (BACKWARD) {
               tma_load_3d_pair(da, &maps.w, fb, row_w, k0, u.group);
@@ -512,7 +517,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
             ++chunk;
           }
           if (!ready && !mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
-          if (weight && kb * 64 + 64 > u.rows) {
+          if (weight && rows_to_clear(u.rows - kb * 64)) {
             if (!mbar_wait_cluster_bounded(cleared_bar(s), (cleared_parity >> s) & 1u, abort_flag, &g_status, kWaitLimitNs)) {
               ok = false;
               break;
@@ -535,7 +540,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
           } else if (weight) {
 #pragma unroll
             for (int i = 0; i < STEPS; ++i)
-              mma_pair_f16(d_tmem, step_desc<true>(a0, i), step_desc<true>(b0, i), idesc, uint32_t(kb | i));
+              if (kb * 64 + 16 * i < u.rows) mma_pair_f16(d_tmem, step_desc<true>(a0, i), step_desc<true>(b0, i), idesc, uint32_t(kb | i));
           } else {
 #pragma unroll
             for (int i = 0; i < STEPS; ++i)
@@ -554,7 +559,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     // -------------------------------------------------------------- scales
     // Four blocks (512 of K, a chunk) at a time, the warps in turn: reading a few bytes of many
     // rows and publishing them takes a warp 1 to 2 us (with two warps instead of four 128 x
-    // 4096 x 14336 took 30.0 us instead of SCALE_TIME).  Warp and stage of a chunk are its number modulo
+    // 4096 x 14336 took 30.0 us instead of 27.3).  Warp and stage of a chunk are its number modulo
     // four, so a stage is one warp's, as waits by parity need.  Lane l holds the words (four
     // blocks' bytes) of rows l, l + 32, ... of x; this CTA's 128 weight rows have one word.
     // Blocks behind the last are never multiplied with.
@@ -604,22 +609,24 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     __syncwarp();
   } else if (BACKWARD && warp >= 2 + EPI_WARPS) {
     // -------------------------------------------------------------- rows behind a group
-    // The last stage of a unit of dw: rows behind the group's end are overwritten with zeros
-    // in the four boxes of this CTA's operands (row r of a box is its bytes 128 r ..).
+    // The last stage of a unit of dw: rows behind the group's end, up to the next multiple of
+    // 16, are overwritten with zeros in the four boxes of this CTA's operands (row r of a box
+    // is its bytes 128 r ..).
     uint32_t parity = 0;
     int s = 0;
     for (int r = 0, un = number(0); un < num_units; un = number(++r)) {
       const bool weight = un >= rows_units;
       const Unit u = weight ? unit_at(un) : Unit{};
-      const int num = stages_of(u, weight), live = weight ? u.rows - (num - 1) * 64 : 64;
+      const int num = stages_of(u, weight), live = u.rows - (num - 1) * 64;
       s = (s + num - 1) % args.stages;
-      if (live < 64) {
+      if (weight && rows_to_clear(live)) {
         if (!__all_sync(0xffffffffu, mbar_wait(tail_bar(s), (parity >> s) & 1u, abort_flag))) break;
         parity ^= 1u << s;
-        const uint32_t at = ring + uint32_t(s) * stage;
-        for (int b = 0; b < 4; ++b)
-          for (int i = live * ROW_BYTES + lane * 16; i < MN_BOX_BYTES; i += 512)
-            sts16(at + uint32_t(b * MN_BOX_BYTES + i), make_uint4(0, 0, 0, 0));
+        const uint32_t at = ring + uint32_t(s) * stage + uint32_t(live * ROW_BYTES);
+        for (int i = lane * 16; i < (-live & 15) * ROW_BYTES; i += 512) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) sts16(at + uint32_t(b * MN_BOX_BYTES + i), make_uint4(0, 0, 0, 0));
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(map_to_rank(cleared_bar(s), 0));
@@ -629,7 +636,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     __syncwarp();
   } else {
     // -------------------------------------------------------------- epilogue
-    // Two warps per TMEM lane quarter q (32 rows of the 256-row operand), which share
+    // WG warps per TMEM lane quarter q (32 rows of the 256-row operand), which share
     // the unit's columns.  A box of shared memory turns the accumulator's layout into
     // that of the global accesses, 16 bytes per lane (see linear.cu).
     constexpr int WG = EPI_WARPS / 4;
@@ -650,7 +657,9 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         const int col = u.nb * (2 * BM) + int(rank) * BM + q * 32 + ch * 8;
         const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * ACC_COLS);
         const int groups = u.bn / 32;
-        const int share = (groups + WG - 1) / WG, g0 = wg * share, g1 = min(groups, g0 + share);
+        // (a quarter of the lanes past the last column has none)
+        const bool columns = col - ch * 8 < args.N;
+        const int share = (groups + WG - 1) / WG, g0 = wg * share, g1 = columns ? min(groups, g0 + share) : 0;
         const size_t at = size_t(u.row0 + sub) * size_t(args.N) + size_t(col);
         auto live_rows = [&](int g) {
           uint32_t v = 0u;
@@ -752,7 +761,8 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         p.at = (size_t(u.group) * size_t(args.rows) + size_t(row0 + sub8)) * size_t(args.N) + size_t(p.col);
         return p;
       };
-      uint4 in8[2][8];
+      constexpr int GROUPS = 4 / WG;         // groups of 64 columns of a warp
+      uint4 in8[GROUPS][8];
       auto request = [&](const Part& p, int k, uint4 (&d)[8]) {
         const int g = wg + k * WG;
         const uint32_t live = p.col + g * 64 < args.N ? p.rows : 0u;
@@ -766,8 +776,8 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       if (un < num_units) {
         p = part_of(unit_at(un));
         if (args.in != nullptr) {
-          request(p, 0, in8[0]);
-          request(p, 1, in8[1]);
+#pragma unroll
+          for (int k = 0; k < GROUPS; ++k) request(p, k, in8[k]);
         }
       }
       for (; un < num_units; un = number(++local)) {
@@ -780,7 +790,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) break;
         tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {        // four groups of 64 columns, two of them this warp's
+        for (int k = 0; k < GROUPS; ++k) {
           const int g = wg + k * WG;
           __syncwarp();                      // the previous group has been read out of the box
           if (args.in != nullptr) {
@@ -793,7 +803,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
           for (int h = 0; h < 2; ++h) {
             uint32_t v[32];
             tmem_ld32(tbase + uint32_t(g * 64 + h * 32), v);
-            if (h == 1 && k == 1) {
+            if (h == 1 && k == GROUPS - 1) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0 && awaited) mbar_arrive_remote_relaxed(map_to_rank(tempty_bar(acc), 0));
@@ -832,7 +842,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         for (int e = table.busy * per_group + pair; e < args.G * per_group; e += num_pairs) {
           const Part z = part_of(weight_unit(e, table, args));
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < GROUPS; ++k) {
             const int g = wg + k * WG;
             const uint32_t live = z.col + g * 64 < args.N ? z.rows : 0u;
 #pragma unroll
@@ -899,7 +909,7 @@ cudaError_t launch(const Maps& m, GroupArgs a, int64_t units, int pairs, cudaStr
   const bool wide = a.bn_cap > max_bn(OP);
   a.accs = wide ? 1 : 2;
   // (narrow units: more stages, whose loads' latency is what bounds them; 512 x 4096 x 2048
-  // with six stages STAGE6 us, with eight STAGE8)
+  // with six stages 11.3 us, with eight 10.7)
   a.stage_bytes = OP_BYTES + a.bn_cap / 2 * ROW_BYTES;
   a.stages = (SMEM_LIMIT - fixed_bytes(OP) - table) / a.stage_bytes;
   if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
@@ -922,31 +932,35 @@ cudaError_t launch(const Maps& m, GroupArgs a, int64_t units, int pairs, cudaStr
 
 int ceil_div(int64_t a, int64_t b) { return int((a + b - 1) / b); }
 
-// Most rows of a unit.  The widest, where the host does not know the groups' sizes or
-// they make many units; one group's rows are cut so that its units fill the SM pairs in
-// the fewest and narrowest rounds, a stage taking 117 + 1.55 bn cycles and 288 at least
-// (see linear.cu).  With one unit per pair at most, E4M3 needs no second accumulator and
-// takes 256 rows too.
-int choose_cap(int op, int64_t G, int64_t M, int tiles_n, int pairs) {
+// One group's rows are cut so that its units fill the SM pairs in the fewest and
+// narrowest rounds, a stage taking 117 + 1.55 bn cycles and 288 at least (see linear.cu).
+// With one unit per pair at most, E4M3 needs no second accumulator and takes 256 rows
+// too.  `cycles`: of a stage of K in all rounds.
+struct Cut {
+  int bn;
+  int64_t cycles;
+};
+Cut cut_rows(int op, int64_t M, int tiles_n, int pairs) {
   const int cap = max_bn(op);
-  const bool one_round = (M / 256 + (G < M ? G : M)) * tiles_n <= pairs;
-  // (groups of few rows: 128, for the sake of more stages)
-  if (G > 1) return M / G < 96 ? 128 : one_round ? 256 : cap;
   const int64_t parts = (M + 31) / 32;
-  int64_t best = -1;
-  int best_cap = cap;
+  Cut best{cap, -1};
   for (int64_t tm = (parts + 7) / 8; tm < (parts + 7) / 8 + 8 && tm <= parts; ++tm) {
     const int bn = 32 * int((parts + tm - 1) / tm);
     const int64_t units = tm * tiles_n;
     if (bn > cap && units > pairs) continue;
     const int64_t stage = 117 + 31 * bn / 20;
     const int64_t cost = (units + pairs - 1) / pairs * (stage > 288 ? stage : 288);
-    if (best < 0 || cost < best) {
-      best = cost;
-      best_cap = bn;
-    }
+    if (best.cycles < 0 || cost < best.cycles) best = Cut{bn, cost};
   }
-  return best_cap;
+  return best;
+}
+// Most rows of a unit.  Several groups, whose sizes the host does not know: the widest
+// (256 in E4M3 where a pair has one unit at most), or 128 where they have few rows, for the
+// sake of more stages.
+int choose_cap(int op, int64_t G, int64_t M, int tiles_n, int pairs) {
+  if (G == 1) return cut_rows(op, M, tiles_n, pairs).bn;
+  const bool one_round = (M / 256 + (G < M ? G : M)) * tiles_n <= pairs;
+  return M / G < 96 ? 128 : one_round ? 256 : max_bn(op);
 }
 
 // out [M, N] from x [M, K] and w [G, N, K].
@@ -1019,20 +1033,41 @@ cudaError_t backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uin
 
 }  // namespace
 
+// Which form a block-scaled layer takes.  grouped_few.cu up to 8 rows, and up to 16 and 32
+// while the weights are small: us, it against few_rows.cu: 1 row of 4096 x 14336 13.0 / 13.1, 16
+// of 1024 x 1024 2.2 / 4.4, of 4096 x 4096 6.9 / 7.1, of 8192 x 2048 7.4 / 7.0, 32 of 4096 x 1024
+// 4.3 / 4.4, of 4096 x 4096 11.2 / 7.3.  few_rows.cu up to 512 rows where its estimate is not
+// 1.15 times this file's, 8000 cycles for the call, 36 for each row of a unit and the stages
+// (its few stages of long K overlap better than both formulas say): few_rows.cu against it, 64
+// rows of 4096 x 14336 14.7 / 26, of 4096 x 4096 8.0 / 10.5, 512 of 4096 x 4096 13.4 / 12.5, of 14336 x
+// 4096 39 / 30, of 2048 x 14336 20 / 26.
 cudaError_t launch_linear_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
                                  const uint8_t* w_scale, const uint16_t* bias, const uint16_t* res, int64_t M, int64_t N,
                                  int64_t K, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
-  if (M <= 32) return launch_few_groups(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
+  if (M <= 8 || (M <= 16 && N * K <= (int64_t(1) << 23)) || (M <= 32 && K <= 1024 && N * K <= (int64_t(1) << 22)))
+    return launch_few_groups(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
+  const int64_t few = few_rows_cycles(M, N, K, false, true);
+  if (few >= 0) {
+    const Cut c = cut_rows(OP_BLOCKS, M, ceil_div(N, 2 * BM), kNumSMsHint / 2);
+    const int64_t here = 8000 + 36 * c.bn + c.cycles * ceil_div(K, 128);
+    if (20 * few < 23 * here) return launch_few_rows_blocks(out, x, x_scale, w, w_scale, bias, res, M, N, K, s);
+  }
   return forward<OP_BLOCKS>(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
 }
 
+// grouped_few.cu: up to 32 rows and 8 per group on average, while it has a few thousand CTAs
+// (each costs 1.6 ns in E4M3).  Measured, us, it against this file: bf16 2 rows, 2 groups with
+// rows of 4096 x 2048 7.5 / 10.6, of 14336 x 4096 36 / 39, 16 rows of one of four of 2048 x 2048 8.0
+// / 9.7, 32 of one 13.6 / 9.7; E4M3 2 rows of 4096 x 2048 5.9 / 9.1, 3 rows in each of 64 of 4096
+// x 2048 109 / 82.
 cudaError_t launch_grouped(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w, const uint8_t* w_scale,
                            const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
-  if (M <= 32) return launch_few_groups(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, s);
-  if (x_scale != nullptr)
-    return forward<OP_BLOCKS>(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, s);
+  const bool fp8 = x_scale != nullptr;
+  if (M <= 32 && M <= 8 * G && (G < M ? G : M) * ((N + 15) / 16) <= (fp8 ? 2048 : 4096))
+    return launch_few_groups(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, s);
+  if (fp8) return forward<OP_BLOCKS>(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, s);
   return forward<OP_BF16>(out, x, nullptr, w, nullptr, nullptr, nullptr, offsets, G, M, N, K, s);
 }
 

@@ -22,7 +22,7 @@ namespace {
 // 64-byte chunks of a row per group
 constexpr int chunks_of(bool fp8) { return fp8 ? 2 : 4; }
 // Warps per SM that the registers are to leave room for
-constexpr int warps_of(bool fp8, int nt) { return nt == 1 ? 32 : fp8 && nt == 2 ? 24 : 16; }
+constexpr int warps_of(int nt) { return nt == 1 ? 32 : 16; }
 
 struct FewGroupArgs {
   uint16_t* out;
@@ -62,7 +62,7 @@ QFFN_DEVI float scaled(float v, uint32_t a, uint32_t b) {
 }
 
 template <bool FP8, int NT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, warps_of(FP8, NT) / WARPS) few_groups_kernel(const FewGroupArgs a) {
+__global__ void __launch_bounds__(WARPS * 32, warps_of(NT) / WARPS) few_groups_kernel(const FewGroupArgs a) {
   constexpr int TOK = 8 * NT, kU = chunks_of(FP8);
   __shared__ float red[WARPS][16][TOK + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
