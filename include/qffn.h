@@ -532,8 +532,8 @@ qffn_status qffn_linear_fp8_blocks(uint16_t* out, const uint8_t* x, const uint8_
  * the stream (the host does not see the sizes, so a call can be captured once and
  * replayed with others).  Groups may be empty.  Rows before offsets[0] and from
  * offsets[G] on are left as they were.  (An offset outside 0 .. M counts as 0 or
- * M and a group whose end is before its start is empty: no access leaves the
- * buffers; decreasing offsets leave rows undefined that two groups claim.)
+ * M, and one below an offset before it as that one: no access leaves the buffers and
+ * no row belongs to two groups.)
  * 1 <= G <= 4096; M, N, K as in qffn_linear.  No workspace. */
 
 /*   out[m] = bf16(x[m] . w[g]^T) for the rows m of group g, bf16 with fp32 sums.

@@ -88,8 +88,10 @@ def linear(x, w, bias=None, residual=None):
 
 def groups(offsets, M):
     """(first row, end) of each group, as the calls read the offsets."""
-    o = [min(max(int(v), 0), M) for v in offsets]
-    return [(a, max(a, b)) for a, b in zip(o[:-1], o[1:])]
+    o = [0]
+    for v in offsets:
+        o.append(max(o[-1], min(max(int(v), 0), M)))
+    return list(zip(o[1:-1], o[2:]))
 
 
 def grouped(x, w, offsets):

@@ -159,7 +159,8 @@ QFFN_DEVI uint32_t pack2(uint64_t v) {
 }
 QFFN_DEVI uint4 pack8(const uint64_t (&v)[4]) { return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3])); }
 
-// The table of units in shared memory: off[0 .. G] the offsets within 0 .. M, first[0
+// The table of units in shared memory: off[0 .. G] the offsets (within 0 .. M, none below
+// the one before it), first[0
 // .. G] the number of the first unit of out of each group; backward: order[0 .. G - 1] the
 // groups, those with rows (`busy` of them) first.
 struct Table {
@@ -176,7 +177,7 @@ struct Unit {
   int nb, kb;         // 256-wide unit of the row of N (of dw: of the matrix's rows, and of the row)
 };
 
-QFFN_DEVI int group_rows(const int* off, int g) { return max(off[g + 1] - off[g], 0); }
+QFFN_DEVI int group_rows(const int* off, int g) { return off[g + 1] - off[g]; }
 
 // Unit u of out; `g`: the group of the last unit that this thread looked up.
 QFFN_DEVI Unit rows_unit(int u, int& g, const Table& t, const GroupArgs& a) {
@@ -327,6 +328,24 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   for (int i = threadIdx.x; i <= args.G; i += num_threads(OP, KIND))
     table_off[i] = args.offsets != nullptr ? min(max(args.offsets[i], 0), args.M) : i == 0 ? 0 : args.M;
   __syncthreads();
+  if (args.offsets != nullptr) {
+    // an offset below one before it counts as that one, so that no two groups claim a row
+    if (warp == 0) {
+      int top = 0;
+      for (int base = 0; base <= args.G; base += 32) {
+        const int i = base + lane;
+        int v = i <= args.G ? max(table_off[i], top) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int below = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v = max(v, below);
+        }
+        if (i <= args.G) table_off[i] = v;
+        top = __shfl_sync(0xffffffffu, v, 31);
+      }
+    }
+    __syncthreads();
+  }
   Table table{table_off, table_first, table_order, args.bn_cap, 0};
   if (!BACKWARD && args.choose != 0) {
     // Where the widest units make few rounds: the width whose units take the least time, their
@@ -902,7 +921,7 @@ cudaError_t max_pairs(int* pairs) {
   return cudaSuccess;
 }
 
-// `units`: no fewer than the kernel will find (if the offsets do not decrease)
+// `units`: no fewer than the kernel will find
 template <int OP, int KIND>
 cudaError_t launch(const Maps& m, GroupArgs a, int64_t units, int pairs, cudaStream_t s) {
   const int table = (KIND == KIND_BACKWARD ? 12 : 8) * (a.G + 1) + 48;

@@ -73,15 +73,23 @@ __global__ void __launch_bounds__(WARPS * 32, warps_of(NT) / WARPS) few_groups_k
   // the group of this CTA: the blockIdx.y-th of those with rows
   int group = 0, begin = 0, end = a.M;
   if (a.offsets != nullptr) {
-    int skip = int(blockIdx.y);
+    // (an offset counts as one within 0 .. M and not below any before it)
+    int skip = int(blockIdx.y), top = 0;
     group = -1;
     for (int base = 0; base < a.G; base += 32) {
       const int i = base + lane;
       int lo = 0, hi = 0;
       if (i < a.G) {
-        lo = min(max(a.offsets[i], 0), a.M);
-        hi = min(max(a.offsets[i + 1], 0), a.M);
+        lo = min(max(a.offsets[i], top), a.M);
+        hi = min(max(a.offsets[i + 1], top), a.M);
       }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int below = __shfl_up_sync(0xffffffffu, lo, o);
+        if (lane >= o) lo = max(lo, below);
+      }
+      hi = max(hi, lo);
+      top = __reduce_max_sync(0xffffffffu, hi);
       const uint32_t some = __ballot_sync(0xffffffffu, hi > lo);
       const int n = __popc(some);
       if (skip < n) {
