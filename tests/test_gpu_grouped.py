@@ -110,7 +110,9 @@ def _sizes(kind, G, M):
 
 GROUPED = [(1, 1, 8, 16), (1, 300, 264, 272), (3, 1, 1000, 144), (8, 2, 512, 4096), (5, 7, 136, 1040), (8, 16, 1032, 512), (16, 33, 264, 256),
            (4, 100, 2048, 1024), (64, 200, 264, 528), (3, 500, 520, 1152), (8, 900, 1032, 784), (2, 1500, 256, 2064), (130, 700, 136, 144),
-           (300, 40, 264, 272), (1000, 3000, 72, 80)]
+           (300, 40, 264, 272), (1000, 3000, 72, 80),
+           # few units of long K: parts of it over clusters of 8, 4 and 2; wide matrices
+           (1, 9, 248, 10288), (2, 554, 144, 3840), (2, 84, 1008, 3584), (4, 800, 1024, 4096), (2, 200, 6000, 1040)]
 
 
 @pytest.mark.parametrize("G,M,N,K", GROUPED)

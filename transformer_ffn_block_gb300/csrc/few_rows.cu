@@ -24,6 +24,10 @@
 // rows and the 64 up rows of the same outputs.  Every mbarrier wait is bounded,
 // as in linear.cu.
 //
+// GROUPED: rows in groups with a matrix each (see grouped.cu), a cluster per (tile of
+// 128 weight rows, tile of rows of one group).  The host launches as many tiles of rows as
+// there can be; a cluster finds its group from the offsets, and one beyond the last ends.
+//
 // OP_BLOCKS: E4M3 with a power-of-two scale per block of 128, which the tensor cores
 // multiply (grouped.cu says how): two warps write the scales of 512 of K at a time to
 // shared memory, the issuing thread copies them to TMEM in front of their MMAs.
@@ -65,6 +69,8 @@ struct FewArgs {
   const uint8_t* x_blocks;  // OP_BLOCKS: E8M0 scales [M, blocks] and [ceil(N / 128), blocks]
   const uint8_t* w_blocks;
   int blocks;
+  const int* offsets;       // GROUPED
+  int G;
   int act;
   int M, N;                 // activation rows; output columns (gated: H)
   int num_kb, splits;       // K blocks of a stage each; parts of K (CTAs per cluster)
@@ -206,8 +212,9 @@ QFFN_DEVI void sum8(const float* own, const float* recv, int share, int part, in
 
 // The parts added and the epilogue for this CTA's share, the activation rows
 // part * share .. of the tile (share = bn / SPLITS), for the tile's weight rows.
+// `row0`: the tile's first row; rows from `row_end` on are not the tile's.
 template <int OP, int EPI, int SPLITS>
-QFFN_DEVI void finish(const FewArgs& args, const float* sums, const float* recv, int part, int n0, int mt) {
+QFFN_DEVI void finish(const FewArgs& args, const float* sums, const float* recv, int part, int n0, int row0, int row_end) {
   constexpr bool GATED = EPI != EPI_LINEAR;
   constexpr int TPM = GATED ? 8 : 16;        // threads per activation row, eight outputs each
   const int share = args.bn / SPLITS;
@@ -217,8 +224,8 @@ QFFN_DEVI void finish(const FewArgs& args, const float* sums, const float* recv,
   const float scale = OP == OP_E4M3 ? args.a_scale[0] * args.w_scale[0] : 1.0f;
   uint64_t bias[4] = {0ull, 0ull, 0ull, 0ull};
   if (EPI == EPI_LINEAR && args.bias != nullptr) unpack8(ld16_once(args.bias + n), bias);
-  const int m0 = mt * args.bn + part * share;
-  const int rows = min(share, args.M - m0);
+  const int m0 = row0 + part * share;
+  const int rows = min(share, row_end - m0);
 #pragma unroll 2
   for (int ml = int(threadIdx.x) / TPM; ml < rows; ml += kThreads / TPM) {
     const size_t m = size_t(m0) + size_t(ml);
@@ -267,7 +274,7 @@ QFFN_DEVI void finish(const FewArgs& args, const float* sums, const float* recv,
 
 // Grid: one cluster of `splits` CTAs per (tile of 128 weight rows, tile of bn
 // activation rows).
-template <int OP, bool W_MN, int EPI>
+template <int OP, bool W_MN, int EPI, bool GROUPED = false>
 __global__ void __launch_bounds__(kThreads)
     few_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     const FewArgs args) {
@@ -330,6 +337,51 @@ __global__ void __launch_bounds__(kThreads)
   const uint32_t tmem_base = tmem_slot;
   if (!args.late_wait) pdl_wait();
   pdl_trigger();
+  int row0 = mt * args.bn, row_end = args.M, group = 0;
+  if constexpr (GROUPED) {
+    // the group and the rows of the mt-th tile (an offset counts as one within 0 .. M and not
+    // below any before it)
+    int skip = mt, top = 0;
+    group = -1;
+    for (int base = 0; base < args.G; base += 32) {
+      const int i = base + lane;
+      int lo = 0, hi = 0;
+      if (i < args.G) {
+        lo = min(max(args.offsets[i], top), args.M);
+        hi = min(max(args.offsets[i + 1], top), args.M);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int below = __shfl_up_sync(0xffffffffu, lo, o);
+        if (lane >= o) lo = max(lo, below);
+      }
+      hi = max(hi, lo);
+      const int own = (hi - lo + args.bn - 1) / args.bn;
+      int tiles = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int below = __shfl_up_sync(0xffffffffu, tiles, o);
+        if (lane >= o) tiles += below;
+      }
+      const uint32_t reach = __ballot_sync(0xffffffffu, tiles > skip);
+      if (reach != 0u) {
+        const int l = __ffs(int(reach)) - 1;
+        group = base + l;
+        row0 = __shfl_sync(0xffffffffu, lo, l) + (skip - __shfl_sync(0xffffffffu, tiles - own, l)) * args.bn;
+        row_end = __shfl_sync(0xffffffffu, hi, l);
+        break;
+      }
+      skip -= __shfl_sync(0xffffffffu, tiles, 31);
+      top = __reduce_max_sync(0xffffffffu, hi);
+    }
+    if (group < 0) {                         // (the same in the whole cluster)
+      cluster_wait();
+      if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(args.tmem_cols)
+                     : "memory");
+      return;
+    }
+  }
 
   const int per = (args.num_kb + args.splits - 1) / args.splits;
   const int kb0 = part * per, kb1 = min(args.num_kb, kb0 + per);   // every part has at least one
@@ -350,13 +402,15 @@ __global__ void __launch_bounds__(kThreads)
         if (GATED) {
           tma_load_2d(dw, &tmW, fb, k0, n0);
           tma_load_2d(dw + BOX_BYTES / 2, &tmW, fb, k0, args.N + n0);
+        } else if (GROUPED) {
+          tma_load_3d(dw, &tmW, fb, k0, n0, group);
         } else if (W_MN) {
           tma_load_2d(dw, &tmW, fb, n0, k0);
           tma_load_2d(dw + BOX_BYTES / 2, &tmW, fb, n0 + 64, k0);
         } else {
           tma_load_2d(dw, &tmW, fb, k0, n0);
         }
-        tma_load_2d(dx, &tmX, fb, k0, mt * args.bn);
+        tma_load_2d(dx, &tmX, fb, k0, row0);
         issued |= 1u << s;
         issued_parity = (issued_parity & ~(1u << s)) | (ph << s);
         if (++s == args.stages) {
@@ -422,7 +476,7 @@ __global__ void __launch_bounds__(kThreads)
     // Each warp every second chunk of four blocks.  Lane l: the words of rows l, l + 32, l +
     // 64, l + 96 of x; the 128 weight rows have one word.
     const int chunks = (kb1 - kb0 + 3) / 4;
-    const uint8_t* const wb = args.w_blocks + size_t(tile) * size_t(args.blocks);
+    const uint8_t* const wb = args.w_blocks + size_t(group * ((args.N + 127) / 128) + tile) * size_t(args.blocks);
     const bool whole = ((reinterpret_cast<uintptr_t>(args.x_blocks) | reinterpret_cast<uintptr_t>(args.w_blocks) | uintptr_t(args.blocks | kb0)) & 3u) == 0;
     auto word = [&](const uint8_t* p, int n) {
       if (whole) return *reinterpret_cast<const uint32_t*>(p);
@@ -441,7 +495,7 @@ __global__ void __launch_bounds__(kThreads)
       for (int i = 0; i < 4; ++i) {
         word_x[i] = 0u;
         if (32 * i < args.bn) {
-          const size_t row = size_t(min(mt * args.bn + 32 * i + lane, args.M - 1));
+          const size_t row = size_t(min(row0 + 32 * i + lane, args.M - 1));
           word_x[i] = word(args.x_blocks + row * size_t(args.blocks) + size_t(first), n);
         }
       }
@@ -495,10 +549,10 @@ __global__ void __launch_bounds__(kThreads)
   // ---------------------------------------------------------------- the parts added, epilogue
   if (have) {
     switch (args.splits) {
-      case 1: finish<OP, EPI, 1>(args, sums, recv, part, n0, mt); break;
-      case 2: finish<OP, EPI, 2>(args, sums, recv, part, n0, mt); break;
-      case 4: finish<OP, EPI, 4>(args, sums, recv, part, n0, mt); break;
-      default: finish<OP, EPI, 8>(args, sums, recv, part, n0, mt); break;
+      case 1: finish<OP, EPI, 1>(args, sums, recv, part, n0, row0, row_end); break;
+      case 2: finish<OP, EPI, 2>(args, sums, recv, part, n0, row0, row_end); break;
+      case 4: finish<OP, EPI, 4>(args, sums, recv, part, n0, row0, row_end); break;
+      default: finish<OP, EPI, 8>(args, sums, recv, part, n0, row0, row_end); break;
     }
   }
   __syncwarp();
@@ -516,9 +570,9 @@ __global__ void __launch_bounds__(kThreads)
 // tiles fit twice, so that one's set-up and exchange overlap the other's loads.
 constexpr int kSmemOne = 200 * 1024, kSmemTwo = 100 * 1024;
 
-template <int OP, bool W_MN, int EPI>
+template <int OP, bool W_MN, int EPI, bool GROUPED = false>
 cudaError_t launch(const CUtensorMap& w, const CUtensorMap& x, FewArgs a, int clusters, cudaStream_t s) {
-  const auto fn = few_rows_kernel<OP, W_MN, EPI>;
+  const auto fn = few_rows_kernel<OP, W_MN, EPI, GROUPED>;
   const int bytes = a.stages * a.stage_bytes + a.recv_bytes + (OP == OP_BLOCKS ? kScaleStages * kScaleBytes : 0) + 1024;
   static bool set[64] = {false};
   int dev = 0;
@@ -585,21 +639,24 @@ namespace {
 // many as leave every cluster on the GPU at once, each with at least four
 // stages (clusters of 8 do not fill it: 16 of them, which would take 128 of 152
 // SMs, run in two rounds).
+cudaError_t split_k(int clusters, int num_kb, int* splits) {
+  *splits = 1;
+  for (int s = 2; s <= kMaxSplits && num_kb >= 4 * s; s *= 2) {
+    int fit = 0;
+    const cudaError_t e = max_clusters(s, &fit);
+    if (e != cudaSuccess) return e;
+    if (clusters > fit) break;
+    *splits = s;
+  }
+  // every part has at least one stage
+  while (*splits > 1 && (*splits - 1) * ((num_kb + *splits - 1) / *splits) >= num_kb) *splits /= 2;
+  return cudaSuccess;
+}
 cudaError_t few_rows_split(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, int* clusters, int* splits,
                            int* num_kb) {
   *num_kb = int((K + stage_k(fp8 ? OP_E4M3 : OP_BF16) - 1) / stage_k(fp8 ? OP_E4M3 : OP_BF16));
   *clusters = int((gated ? (N + 63) / 64 : (N + 127) / 128) * ((M + 127) / 128));
-  *splits = 1;
-  for (int s = 2; s <= kMaxSplits && *num_kb >= 4 * s; s *= 2) {
-    int fit = 0;
-    const cudaError_t e = max_clusters(s, &fit);
-    if (e != cudaSuccess) return e;
-    if (*clusters > fit) break;
-    *splits = s;
-  }
-  // every part has at least one stage
-  while (*splits > 1 && (*splits - 1) * ((*num_kb + *splits - 1) / *splits) >= *num_kb) *splits /= 2;
-  return cudaSuccess;
+  return split_k(*clusters, *num_kb, splits);
 }
 
 // Rows per tile: the rows spread evenly over tiles of at most 128, in steps of 32.
@@ -615,12 +672,25 @@ int few_rows_bn(int64_t M) {
 // linear.cu's forms: 64 rows of 2048 x 2048 6.9 / 8.2, of 4096 x 4096 10.6 / 12.9, of 4096 x
 // 14336 23.3 / 28.4, of 4096 x 1024 6.7 / 6.2, of 14336 x 4096 23.1 / 22.3, 128 rows of
 // 4096 x 4096 13.4 / 13.8, of 2048 x 2048 9.1 / 8.2, 256 rows of 14336 x 4096 33 / 27.5.
-int64_t few_rows_cycles(int64_t M, int64_t N, int64_t K, bool gated, bool fp8) {
-  if (M > 512) return -1;
+int64_t few_rows_cycles(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, int64_t max_rows) {
+  if (M > max_rows) return -1;
   int clusters, splits, num_kb;
   if (few_rows_split(M, N, K, gated, fp8, &clusters, &splits, &num_kb) != cudaSuccess) return -1;
   const int64_t rounds = (int64_t(clusters) * splits + kNumSMsHint - 1) / kNumSMsHint;
   return 5700 + rounds * (((num_kb + splits - 1) / splits) * 500 + 39 * few_rows_bn(M)) + (splits > 1 ? 3900 : 0);
+}
+
+// Stages, shared memory and TMEM of a CTA.
+void size_cta(FewArgs& a, int clusters, int op) {
+  a.stage_bytes = BOX_BYTES + a.bn * ROW_BYTES;
+  const bool two = clusters * a.splits > kNumSMsHint;
+  a.recv_bytes = (a.splits - 1) * (a.bn / a.splits) * 512;
+  // (the sums, bn x 512 bytes, take at most 64 KB of the stages' 96 to 200 KB)
+  const int extra = a.recv_bytes + (op == OP_BLOCKS ? kScaleStages * kScaleBytes : 0);
+  a.stages = ((two ? kSmemTwo : kSmemOne) - extra) / a.stage_bytes;
+  if (a.stages > kMaxStages) a.stages = kMaxStages;
+  a.tmem_cols = 32;
+  while (a.tmem_cols < a.bn + (op == OP_BLOCKS ? 16 : 0)) a.tmem_cols *= 2;   // (two slots of scales)
 }
 
 // One product: x [M, K] (K-major), W [wrows, K] or, w_mn, [K, wrows].
@@ -649,15 +719,7 @@ cudaError_t few_rows_product(uint16_t* out, uint16_t* z, const void* x, const fl
   int clusters = 0;
   const cudaError_t e = few_rows_split(M, N, K, GATED, OP != OP_BF16, &clusters, &a.splits, &a.num_kb);
   if (e != cudaSuccess) return e;
-  a.stage_bytes = BOX_BYTES + a.bn * ROW_BYTES;
-  const bool two = clusters * a.splits > kNumSMsHint;
-  a.recv_bytes = (a.splits - 1) * (a.bn / a.splits) * 512;
-  // (the sums, bn x 512 bytes, take at most 64 KB of the stages' 96 to 200 KB)
-  const int extra = a.recv_bytes + (OP == OP_BLOCKS ? kScaleStages * kScaleBytes : 0);
-  a.stages = ((two ? kSmemTwo : kSmemOne) - extra) / a.stage_bytes;
-  if (a.stages > kMaxStages) a.stages = kMaxStages;
-  a.tmem_cols = 32;
-  while (a.tmem_cols < a.bn + (OP == OP_BLOCKS ? 16 : 0)) a.tmem_cols *= 2;   // (two slots of scales)
+  size_cta(a, clusters, OP);
   CUtensorMap mw, mx;
   const bool bf16 = OP == OP_BF16;
   const bool ok = (W_MN ? make_operand_map(&mw, w, bf16, K, N, 64)
@@ -666,7 +728,6 @@ cudaError_t few_rows_product(uint16_t* out, uint16_t* z, const void* x, const fl
   if (!ok) return cudaErrorInvalidValue;
   return launch<OP, W_MN, EPI>(mw, mx, a, clusters, s);
 }
-
 cudaError_t launch_few_rows(uint16_t* out, uint16_t* z, const void* x, const float* x_scale, const void* w,
                             const float* w_scale, const uint16_t* bias, const uint16_t* res, int act, int64_t M,
                             int64_t N, int64_t K, bool fp8, bool w_mn, cudaStream_t s, bool late_wait) {
@@ -681,6 +742,63 @@ cudaError_t launch_few_rows_blocks(uint16_t* out, const uint8_t* x, const uint8_
                                    int64_t N, int64_t K, cudaStream_t s) {
   return few_rows_product<OP_BLOCKS, false, EPI_LINEAR>(out, nullptr, x, nullptr, w, nullptr, bias, res, ACT_NONE, M, N,
                                                         K, s, false, x_scale, w_scale);
+}
+
+// Groups of rows: rows per tile, a quarter above the average group's, in steps of 32; tiles
+// of rows, as many as there can be.
+namespace {
+int grouped_bn(int64_t G, int64_t M) {
+  const int64_t rows = M / (G < M ? G : M) * 5 / 4;
+  return rows >= 128 ? 128 : int((rows + 31) / 32 * 32);
+}
+int64_t grouped_clusters(int64_t G, int64_t M, int64_t N) {
+  return (N + 127) / 128 * (M / grouped_bn(G, M) + (G < M ? G : M));
+}
+template <int OP>
+cudaError_t grouped_product(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w, const uint8_t* w_scale,
+                            const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K, cudaStream_t s) {
+  FewArgs a{};
+  a.out = out;
+  a.x_blocks = x_scale;
+  a.w_blocks = w_scale;
+  a.blocks = int((K + 127) / 128);
+  a.offsets = offsets;
+  a.G = int(G);
+  a.M = int(M);
+  a.N = int(N);
+  a.act = ACT_NONE;
+  a.bn = grouped_bn(G, M);
+  a.tiles_m = int(M / a.bn + (G < M ? G : M));
+  a.num_kb = int((K + stage_k(OP) - 1) / stage_k(OP));
+  const int clusters = int(grouped_clusters(G, M, N));
+  const cudaError_t e = split_k(clusters, a.num_kb, &a.splits);
+  if (e != cudaSuccess) return e;
+  size_cta(a, clusters, OP);
+  CUtensorMap mw, mx;
+  const bool bf16 = OP == OP_BF16;
+  const int64_t pitch = K * (bf16 ? 2 : 1);
+  if (!make_operand_map_3d(&mw, w, bf16, G, N, K, pitch, N * pitch, 128) || !make_operand_map(&mx, x, bf16, M, K, a.bn))
+    return cudaErrorInvalidValue;
+  return launch<OP, false, EPI_LINEAR, true>(mw, mx, a, clusters, s);
+}
+}  // namespace
+
+// The estimate of few_rows_cycles for groups of rows; 1500 cycles more for the search.
+int64_t few_rows_grouped_cycles(int64_t G, int64_t M, int64_t N, int64_t K, bool fp8) {
+  const int64_t clusters = grouped_clusters(G, M, N);
+  if (clusters > 4 * kNumSMsHint) return -1;
+  const int num_kb = int((K + stage_k(fp8 ? OP_E4M3 : OP_BF16) - 1) / stage_k(fp8 ? OP_E4M3 : OP_BF16));
+  int splits = 1;
+  if (split_k(int(clusters), num_kb, &splits) != cudaSuccess) return -1;
+  const int64_t rounds = (clusters * splits + kNumSMsHint - 1) / kNumSMsHint;
+  return 7200 + rounds * (((num_kb + splits - 1) / splits) * 500 + 39 * grouped_bn(G, M)) + (splits > 1 ? 3900 : 0);
+}
+
+cudaError_t launch_few_rows_grouped(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w,
+                                    const uint8_t* w_scale, const int* offsets, int64_t G, int64_t M, int64_t N,
+                                    int64_t K, cudaStream_t s) {
+  return x_scale != nullptr ? grouped_product<OP_BLOCKS>(out, x, x_scale, w, w_scale, offsets, G, M, N, K, s)
+                            : grouped_product<OP_BF16>(out, x, nullptr, w, nullptr, offsets, G, M, N, K, s);
 }
 
 cudaError_t launch_few_rows_gated(uint16_t* out, const uint16_t* x, const uint16_t* w1, const uint16_t* dh, int act,

@@ -152,6 +152,33 @@ QFFN_DEVI bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag
   return mbar_wait_bounded(bar, parity, abort_flag, &g_status, honour_abort, limit);
 }
 
+QFFN_DEVI void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// Sixteen lanes by 32 columns of TMEM at each of two addresses, without waiting
+// (tmem_wait_ld16 makes them usable): registers 4 c .. 4 c + 3 of a thread hold columns
+// 8 c + 2 (lane % 4) and the next, of lane lane / 4 and of lane lane / 4 + 8.
+QFFN_DEVI void tmem_ld_blocks_issue(uint32_t ta, uint32_t tb, uint32_t (&a)[16], uint32_t (&b)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
+      : "r"(ta), "r"(tb)
+      : "memory");
+}
+// Four 8 x 8 blocks of 16-bit values between shared memory and the threads' fragments,
+// transposed; lane l gives the address of row l % 8 of block l / 8.
+QFFN_DEVI void stmatrix_trans(uint32_t addr, const uint32_t (&p)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(p[0]), "r"(p[1]),
+               "r"(p[2]), "r"(p[3])
+               : "memory");
+}
+QFFN_DEVI void ldmatrix_trans(uint32_t addr, uint32_t (&p)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3])
+               : "r"(addr)
+               : "memory");
+}
+
 QFFN_DEVI uint32_t pack2(uint64_t v) {
   float lo, hi;
   f2_unpack(v, lo, hi);
@@ -179,45 +206,68 @@ struct Unit {
 
 QFFN_DEVI int group_rows(const int* off, int g) { return off[g + 1] - off[g]; }
 
-// Unit u of out; `g`: the group of the last unit that this thread looked up.
-QFFN_DEVI Unit rows_unit(int u, int& g, const Table& t, const GroupArgs& a) {
-  if (u >= t.first[g + 1]) {
-    int lo = g + 1, hi = a.G - 1;            // the last group whose first unit is u or before
+// n / d for n >= 0, d > 0: by the reciprocal where floats hold both, which an integer
+// division takes five times as long for.
+QFFN_DEVI int quick_div(int n, int d) {
+  if (n >= 1 << 22) return n / d;
+  int q = int(__fdividef(float(n), float(d)));
+  const int r = n - q * d;
+  q += r >= d ? 1 : r < 0 ? -1 : 0;
+  return q;
+}
+
+// The group of the last unit that a thread looked up: its first unit and the next group's, its
+// rows in 32s spread over tm tiles, `wider` of `least` + 1 and the others of `least`.
+struct Cursor {
+  int group = -1, first = 0, next = 0, begin, rows, tm, least, wider;
+};
+// Unit u of out.  (Every role looks up every unit: with divisions in the open 900 cycles, in
+// which the issuing thread left the tensor cores without work.)
+QFFN_DEVI Unit rows_unit(int u, Cursor& c, const Table& t, const GroupArgs& a) {
+  if (u >= c.next) {
+    int lo = c.group + 1, hi = a.G - 1;      // the last group whose first unit is u or before
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (t.first[mid] <= u) lo = mid;
       else hi = mid - 1;
     }
-    g = lo;
+    c.group = lo;
+    c.first = t.first[lo];
+    c.next = t.first[lo + 1];
+    c.begin = t.off[lo];
+    c.rows = group_rows(t.off, lo);
+    const int parts = (c.rows + 31) >> 5, cap = t.cap >> 5;
+    c.tm = parts <= cap ? 1 : quick_div(parts + cap - 1, cap);
+    c.least = c.tm == 1 ? parts : quick_div(parts, c.tm);
+    c.wider = parts - c.least * c.tm;
   }
   Unit r;
-  r.group = g;
-  r.begin = t.off[g];
-  r.rows = group_rows(t.off, g);
-  // its rows in 32s, spread over tm tiles whose widths differ by 32 at most
-  const int parts = (r.rows + 31) >> 5, cap = t.cap >> 5;
-  const int tm = parts <= cap ? 1 : (parts + cap - 1) / cap;
+  r.group = c.group;
+  r.begin = c.begin;
+  r.rows = c.rows;
   // bands of band_n; within a band, groups of GROUP_M tiles of rows sweep its columns, odd
   // groups backwards (see linear.cu)
-  int k = u - t.first[g], mt = 0;
-  if (tm == 1) {
-    r.nb = k;
-  } else {
-    const int band_tiles = tm * a.band_n;
-    const int band = k < band_tiles ? 0 : k / band_tiles;
-    const int n0 = band * a.band_n, wb = min(a.band_n, a.tiles_n - n0);
-    k -= band * band_tiles;
-    const int per_group = GROUP_M * wb;
-    const int sweep = k < per_group ? 0 : k / per_group;
-    const int size = min(tm - sweep * GROUP_M, GROUP_M);
-    k -= sweep * per_group;
-    const int col = k / size;
+  int k = u - c.first, mt = 0;
+  r.nb = k;
+  if (c.tm > 1) {
+    int n0 = 0, wb = a.tiles_n, sweep = 0;
+    if (a.band_n < a.tiles_n) {
+      const int band = quick_div(k, c.tm * a.band_n);
+      n0 = band * a.band_n;
+      wb = min(a.band_n, a.tiles_n - n0);
+      k -= n0 * c.tm;
+    }
+    if (c.tm > GROUP_M) {
+      sweep = quick_div(k, GROUP_M * wb);
+      k -= sweep * GROUP_M * wb;
+    }
+    const int size = min(c.tm - sweep * GROUP_M, GROUP_M);
+    const int col = size == GROUP_M ? k / GROUP_M : quick_div(k, size);
     mt = sweep * GROUP_M + k - col * size;
     r.nb = n0 + ((sweep & 1) ? wb - 1 - col : col);
   }
-  const int least = tm == 1 ? parts : parts / tm, wider = parts - least * tm;
-  r.bn = 32 * (least + (mt < wider ? 1 : 0));
-  r.row0 = r.begin + 32 * (mt * least + min(mt, wider));
+  r.bn = 32 * (c.least + (mt < c.wider ? 1 : 0));
+  r.row0 = r.begin + 32 * (mt * c.least + min(mt, c.wider));
   r.kb = 0;
   return r;
 }
@@ -225,12 +275,12 @@ QFFN_DEVI Unit rows_unit(int u, int& g, const Table& t, const GroupArgs& a) {
 QFFN_DEVI Unit weight_unit(int u, const Table& t, const GroupArgs& a) {
   const int per_group = a.tiles_r * a.tiles_n;
   Unit r;
-  const int at = u / per_group;
+  const int at = quick_div(u, per_group);
   r.group = t.order[at];
   r.begin = t.off[r.group];
   r.rows = group_rows(t.off, r.group);
   const int k = u - at * per_group;
-  r.nb = k / a.tiles_n;
+  r.nb = quick_div(k, a.tiles_n);
   r.kb = k - r.nb * a.tiles_n;
   r.row0 = 0;
   r.bn = a.N - r.kb * 256 <= 128 ? 128 : 256;
@@ -239,6 +289,11 @@ QFFN_DEVI Unit weight_unit(int u, const Table& t, const GroupArgs& a) {
 
 // Whether a stage of dw whose group has `left` more rows holds rows behind it in an MMA's 16.
 QFFN_DEVI bool rows_to_clear(int left) { return left < 64 && (left & 15) != 0; }
+
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
+};
 
 struct Maps {
   CUtensorMap w;        // the weights [G, rows, cols]
@@ -419,9 +474,9 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   const int rows_units = BACKWARD && args.out == nullptr ? 0 : table_first[args.G];
   const int num_units = rows_units + (BACKWARD ? table.busy * args.tiles_r * args.tiles_n : 0);
   auto number = [&](int r) { return r * num_pairs + pair; };
-  int group_cursor = 0;
+  Cursor cursor;
   auto unit_at = [&](int u) {
-    return BACKWARD && u >= rows_units ? weight_unit(u - rows_units, table, args) : rows_unit(u, group_cursor, table, args);
+    return BACKWARD && u >= rows_units ? weight_unit(u - rows_units, table, args) : rows_unit(u, cursor, table, args);
   };
   // stages of K of a unit
   auto stages_of = [&](const Unit& u, bool weight) { return weight ? (u.rows + 63) / 64 : args.num_kb; };
@@ -510,10 +565,10 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       for (int un = number(0); ok && un < num_units; un = number(++local)) {
         const int acc = local & (args.accs - 1);
         const uint32_t aph = uint32_t(local >> (args.accs - 1)) & 1u;
+        const Unit u = unit_at(un);          // (while the MMAs before run)
+        const bool weight = BACKWARD && un >= rows_units;
         if (!mbar_wait_cluster_bounded(tempty_bar(acc), aph ^ 1u, abort_flag, &g_status, kWaitLimitNs)) break;
         tc_fence_after();
-        const Unit u = unit_at(un);
-        const bool weight = BACKWARD && un >= rows_units;
         const uint32_t d_tmem = tmem_base + uint32_t(acc * ACC_COLS);
         const uint32_t idesc = idesc_for(OP, BACKWARD, weight, u.bn);
         const int num = stages_of(u, weight);
@@ -655,7 +710,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     __syncwarp();
   } else {
     // -------------------------------------------------------------- epilogue
-    // WG warps per TMEM lane quarter q (32 rows of the 256-row operand), which share
+    // Two warps per TMEM lane quarter q (32 rows of the 256-row operand), which share
     // the unit's columns.  A box of shared memory turns the accumulator's layout into
     // that of the global accesses, 16 bytes per lane (see linear.cu).
     constexpr int WG = EPI_WARPS / 4;
@@ -663,49 +718,55 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     const uint32_t box = smem_u32(sStaging + (q * WG + wg) * STAGING_BOX);
     int local = 0, un = number(0);
     {
-      // out: the lane is a column of the output, the accumulator's columns its rows, 32 at a time
+      // out: the lanes are columns of the output, the accumulator's columns its rows, 32 at a
+      // time.  TMEM loads of 16 lanes by 8 columns give each thread two neighbouring rows of
+      // the output for one column, the fragment of an 8 x 8 block: rounded to bf16, blocks
+      // are stored transposed (stmatrix) to a box of 32 rows x 64 bytes (chunk c of row r at
+      // c ^ (r / 2 & 3)), from which rows of the output leave 16 bytes a lane.  What is added
+      // takes the same way back (ldmatrix).  (The accumulator turned through the box in
+      // fp32, a word at a time: 8192 x 4096 x 1024 33.8 us, so 29.1.)
       const int sub = lane >> 2, ch = lane & 3;
-      const uint32_t col32 = box + uint32_t(lane) * 4u;
-      const uint32_t turn32 = box + uint32_t(sub) * 128u + (uint32_t((2 * ch) ^ sub) << 4);
+      const uint32_t turn16 = box + uint32_t(sub) * 64u + (uint32_t(ch ^ ((sub >> 1) & 3)) << 4);
+      // this lane's row of the four blocks of eight rows: block of columns lane / 8, row lane % 8
+      const uint32_t block8 = box + uint32_t(lane & 7) * 64u + (uint32_t((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
       const size_t step = size_t(8) * size_t(args.N);
       for (; un < rows_units; un = number(++local)) {
         const int acc = local & (args.accs - 1);
         const uint32_t aph = uint32_t(local >> (args.accs - 1)) & 1u;
         const Unit u = unit_at(un);
         const int row_end = min(u.begin + u.rows, u.row0 + u.bn);
-        const int col = u.nb * (2 * BM) + int(rank) * BM + q * 32 + ch * 8;
+        const int col0 = u.nb * (2 * BM) + int(rank) * BM + q * 32, col = col0 + ch * 8;
         const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * ACC_COLS);
         const int groups = u.bn / 32;
         // (a quarter of the lanes past the last column has none)
-        const bool columns = col - ch * 8 < args.N;
-        const int share = (groups + WG - 1) / WG, g0 = wg * share, g1 = columns ? min(groups, g0 + share) : 0;
+        const int share = (groups + WG - 1) / WG, g0 = wg * share, g1 = col0 < args.N ? min(groups, g0 + share) : 0;
         const size_t at = size_t(u.row0 + sub) * size_t(args.N) + size_t(col);
-        auto live_rows = [&](int g) {
-          uint32_t v = 0u;
-          if (col < args.N) {
+        const int rows_here = col < args.N ? row_end - u.row0 - sub : 0;   // group g: rows 8 i < rows_here - 32 g
+        float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};      // of columns sub, 8 + sub, ..
+        if (!BACKWARD && args.bias != nullptr) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v |= (u.row0 + g * 32 + sub + 8 * i < row_end ? 1u : 0u) << i;
-          }
-          return v;
-        };
-        uint64_t bias[4] = {0ull, 0ull, 0ull, 0ull};
-        if (!BACKWARD && args.bias != nullptr && col < args.N) {
-          const uint4 b = ld16_settled(bias_row + col);
-          bias[0] = bf16x2_to_f2(b.x);
-          bias[1] = bf16x2_to_f2(b.y);
-          bias[2] = bf16x2_to_f2(b.z);
-          bias[3] = bf16x2_to_f2(b.w);
+          for (int j = 0; j < 4; ++j)
+            if (col0 + 8 * j < args.N) bias[j] = bf16_to_f32(bias_row[col0 + 8 * j + sub]);
         }
         uint4 next_in[4];                    // what is added, requested a group ahead
         auto request = [&](int g) {
-          const uint32_t live = g < g1 ? live_rows(g) : 0u;
+          const int left = g < g1 ? rows_here - 32 * g : 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             next_in[i] = make_uint4(0, 0, 0, 0);
-            if ((live >> i) & 1u) next_in[i] = ld16_stream(args.in + (at + size_t(4 * g + i) * step));
+            if (8 * i < left) next_in[i] = ld16_stream(args.in + (at + size_t(4 * g + i) * step));
           }
         };
-        if (!BACKWARD && args.in != nullptr) request(g0);
+        if (!BACKWARD && args.in != nullptr) {
+          // the first group's are requested here, the others' set out for L2
+          if ((ch & 1) == 0)
+            for (int g = g0 + 1; g < g1; ++g) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (8 * i < rows_here - 32 * g) prefetch_l2(args.in + (at + size_t(4 * g + i) * step));
+            }
+          request(g0);
+        }
         if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) { un = num_units; break; }
         tc_fence_after();
         const bool awaited = number(local + args.accs) < num_units;   // another unit takes this accumulator
@@ -716,46 +777,67 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
             if (lane == 0 && awaited) mbar_arrive_remote_relaxed(map_to_rank(tempty_bar(acc), 0));
           }
         };
-        if (g0 >= g1) loaded(g0);            // (a unit with fewer groups than warps)
-        for (int g = g0; g < g1; ++g) {
-          const uint32_t live = live_rows(g);
-          uint32_t v[32];
-          tmem_ld32(tbase + uint32_t(g * 32), v);
-          loaded(g);
-          uint4 in4[4];
-          if (!BACKWARD && args.in != nullptr) {
+        auto issue = [&](int g, uint32_t (&lo)[16], uint32_t (&hi)[16]) {   // lanes 0 .. 15 and 16 .. 31 of the quarter
+          tmem_ld_blocks_issue(tbase + uint32_t(g * 32), tbase + (16u << 16) + uint32_t(g * 32), lo, hi);
+        };
+        uint16_t* const dst = args.out + at;
+        auto leave = [&](int g) {            // the box's rows to the output
+          __syncwarp();
+          uint4 o[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) in4[i] = next_in[i];
+          for (int i = 0; i < 4; ++i) o[i] = lds16(turn16 + 512u * i);
+          uint16_t* row = dst + size_t(4 * g) * step;
+          const int left = rows_here - 32 * g;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (8 * i < left) stg16(row, o[i]);
+            row += step;
+          }
+        };
+        // (two loops, so that the common one is free of branches)
+        auto process = [&](auto extras, int g, const uint32_t (&lo)[16], const uint32_t (&hi)[16]) {
+          __syncwarp();                      // the previous group has been read out of the box
+          if (decltype(extras)::value && args.in != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sts16(turn16 + 512u * i, next_in[i]);
+            __syncwarp();
             request(g + 1);
           }
-          __syncwarp();                      // the previous group has been read out of the box
 #pragma unroll
-          for (int c = 0; c < 32; ++c) sts4((col32 ^ uint32_t(16 * (c & 7))) + uint32_t(128 * c), v[c]);
-          __syncwarp();
-          uint4 los[4], his[4];
+          for (int c = 0; c < 4; ++c) {      // rows 8 c .. of the group, four blocks of columns
+            uint32_t p[4];
+            if (decltype(extras)::value) {
+              uint64_t z[4] = {f2_pack(__uint_as_float(lo[4 * c]), __uint_as_float(lo[4 * c + 1])),
+                               f2_pack(__uint_as_float(lo[4 * c + 2]), __uint_as_float(lo[4 * c + 3])),
+                               f2_pack(__uint_as_float(hi[4 * c]), __uint_as_float(hi[4 * c + 1])),
+                               f2_pack(__uint_as_float(hi[4 * c + 2]), __uint_as_float(hi[4 * c + 3]))};
+              uint32_t d[4] = {0u, 0u, 0u, 0u};
+              if (args.in != nullptr) ldmatrix_trans(block8 + 512u * c, d);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            los[i] = lds16(turn32 + 1024u * i);
-            his[i] = lds16((turn32 ^ 16u) + 1024u * i);
-          }
+              for (int j = 0; j < 4; ++j) p[j] = pack2(f2_add(f2_add(z[j], f2_pack(bias[j], bias[j])), bf16x2_to_f2(d[j])));
+            } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint64_t z[4] = {f2_pack(__uint_as_float(los[i].x), __uint_as_float(los[i].y)),
-                             f2_pack(__uint_as_float(los[i].z), __uint_as_float(los[i].w)),
-                             f2_pack(__uint_as_float(his[i].x), __uint_as_float(his[i].y)),
-                             f2_pack(__uint_as_float(his[i].z), __uint_as_float(his[i].w))};
-            if (!BACKWARD && args.bias != nullptr) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bias[j]);
+              for (int j = 0; j < 2; ++j) {
+                p[j] = pack_bf16x2(__uint_as_float(lo[4 * c + 2 * j]), __uint_as_float(lo[4 * c + 2 * j + 1]));
+                p[2 + j] = pack_bf16x2(__uint_as_float(hi[4 * c + 2 * j]), __uint_as_float(hi[4 * c + 2 * j + 1]));
+              }
             }
-            if (!BACKWARD && args.in != nullptr) {
-              const uint32_t iw[4] = {in4[i].x, in4[i].y, in4[i].z, in4[i].w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) z[j] = f2_add(z[j], bf16x2_to_f2(iw[j]));
-            }
-            if ((live >> i) & 1u) stg16(args.out + (at + size_t(4 * g + i) * step), pack8(z));
+            stmatrix_trans(block8 + 512u * c, p);
           }
-        }
+          leave(g);
+        };
+        auto unit = [&](auto extras) {
+          for (int g = g0; g < g1; ++g) {
+            uint32_t lo[16], hi[16];
+            issue(g, lo, hi);
+            tmem_wait_ld16(lo, hi);
+            loaded(g);
+            process(extras, g, lo, hi);
+          }
+        };
+        if (g0 >= g1) loaded(g0);            // (a unit with fewer groups than warps)
+        else if (!BACKWARD && (args.in != nullptr || args.bias != nullptr)) unit(Flag<!BACKWARD>{});
+        else unit(Flag<false>{});
       }
     }
     if constexpr (BACKWARD) {
@@ -1066,7 +1148,7 @@ cudaError_t launch_linear_blocks(uint16_t* out, const uint8_t* x, const uint8_t*
   if (M == 0) return cudaSuccess;
   if (M <= 8 || (M <= 16 && N * K <= (int64_t(1) << 23)) || (M <= 32 && K <= 1024 && N * K <= (int64_t(1) << 22)))
     return launch_few_groups(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
-  const int64_t few = few_rows_cycles(M, N, K, false, true);
+  const int64_t few = few_rows_cycles(M, N, K, false, true, 2048);
   if (few >= 0) {
     const Cut c = cut_rows(OP_BLOCKS, M, ceil_div(N, 2 * BM), kNumSMsHint / 2);
     const int64_t here = 8000 + 36 * c.bn + c.cycles * ceil_div(K, 128);
@@ -1075,17 +1157,37 @@ cudaError_t launch_linear_blocks(uint16_t* out, const uint8_t* x, const uint8_t*
   return forward<OP_BLOCKS>(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
 }
 
+// What forward() takes for groups of the average size, in SM cycles: 10500 for the call, 36 for
+// each row of a unit, and the stages.
+int64_t grouped_cycles(int op, int64_t G, int64_t M, int64_t N, int64_t K) {
+  const int64_t groups = G < M ? G : M, rows = (M + groups - 1) / groups;
+  const int cap = (M / G < 96 ? 128 : max_bn(op)) / 32;
+  const int64_t parts = (rows + 31) / 32, tiles = (parts + cap - 1) / cap, bn = 32 * ((parts + tiles - 1) / tiles);
+  const int64_t units = groups * tiles * ceil_div(N, 2 * BM), pairs = kNumSMsHint / 2;
+  const int64_t stage = 117 + 31 * bn / 20;
+  return 10500 + 36 * bn + (units + pairs - 1) / pairs * ceil_div(K, stage_k(op)) * (stage > 288 ? stage : 288);
+}
+
 // grouped_few.cu: up to 32 rows and 8 per group on average, while it has a few thousand CTAs
 // (each costs 1.6 ns in E4M3).  Measured, us, it against this file: bf16 2 rows, 2 groups with
 // rows of 4096 x 2048 7.5 / 10.6, of 14336 x 4096 36 / 39, 16 rows of one of four of 2048 x 2048 8.0
 // / 9.7, 32 of one 13.6 / 9.7; E4M3 2 rows of 4096 x 2048 5.9 / 9.1, 3 rows in each of 64 of 4096
 // x 2048 109 / 82.
+// few_rows.cu where its estimate is the lower, in E4M3 (whose start costs this file more) below
+// 1.4 times: it against this file: bf16 277 rows in each of two of 144 x 3840 9.4 / 16.1, 500 in
+// each of two of 256 x 2048 8.4 / 10.9, 60 in each of four of 4096 x 2048 19 / 14.6; E4M3 9 rows of
+// 248 x 10288 6.8 / 21, 4 in each of ten of 2728 x 2048 12.1 / 15.2, 2 in each of 64 of 512 x 1024 9.1
+// / 12.3, 300 in each of two of 4096 x 4096 19.7 / 15.3.
 cudaError_t launch_grouped(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w, const uint8_t* w_scale,
                            const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
   const bool fp8 = x_scale != nullptr;
   if (M <= 32 && M <= 8 * G && (G < M ? G : M) * ((N + 15) / 16) <= (fp8 ? 2048 : 4096))
     return launch_few_groups(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, s);
+  const int64_t few = few_rows_grouped_cycles(G, M, N, K, fp8);
+  const int64_t here = grouped_cycles(fp8 ? OP_BLOCKS : OP_BF16, G, M, N, K);
+  if (few >= 0 && 5 * few < (fp8 ? 7 : 5) * here)
+    return launch_few_rows_grouped(out, x, x_scale, w, w_scale, offsets, G, M, N, K, s);
   if (fp8) return forward<OP_BLOCKS>(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, s);
   return forward<OP_BF16>(out, x, nullptr, w, nullptr, nullptr, nullptr, offsets, G, M, N, K, s);
 }

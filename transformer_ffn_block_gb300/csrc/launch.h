@@ -179,7 +179,7 @@ cudaError_t launch_skinny_gated(uint16_t* h, const uint16_t* x, const uint16_t* 
 // The forms for few rows on the tensor cores (few_rows.cu) and the estimate of
 // their time in SM cycles, -1 where they do not apply.  No workspace.  w_mn: w given
 // as [K, N] (bf16).  Gated: h from w1 = [2H, C], or, with dh, d_gu [M, 2H].
-int64_t few_rows_cycles(int64_t M, int64_t N, int64_t K, bool gated, bool fp8);
+int64_t few_rows_cycles(int64_t M, int64_t N, int64_t K, bool gated, bool fp8, int64_t max_rows = 512);
 cudaError_t launch_few_rows(uint16_t* out, uint16_t* z, const void* x, const float* x_scale, const void* w,
                             const float* w_scale, const uint16_t* bias, const uint16_t* res, int act, int64_t M,
                             int64_t N, int64_t K, bool fp8, bool w_mn, cudaStream_t s, bool late_wait = false);
@@ -189,6 +189,11 @@ cudaError_t launch_few_rows_gated(uint16_t* out, const uint16_t* x, const uint16
 cudaError_t launch_few_rows_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
                                    const uint8_t* w_scale, const uint16_t* bias, const uint16_t* res, int64_t M,
                                    int64_t N, int64_t K, cudaStream_t s);
+// Groups of rows with a matrix each (offsets on the device; x_scale NULL: bf16), and its estimate.
+int64_t few_rows_grouped_cycles(int64_t G, int64_t M, int64_t N, int64_t K, bool fp8);
+cudaError_t launch_few_rows_grouped(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w,
+                                    const uint8_t* w_scale, const int* offsets, int64_t G, int64_t M, int64_t N,
+                                    int64_t K, cudaStream_t s);
 cudaError_t few_rows_take_status(unsigned int* status);
 // Reads and clears the linear kernels' device status word of the current device.
 cudaError_t linear_take_status(unsigned int* status);
