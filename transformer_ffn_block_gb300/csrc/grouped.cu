@@ -65,8 +65,10 @@ constexpr int SCALE_WARPS = 4;
 constexpr int MAX_STAGES = 10;
 constexpr int SF_STAGES = SCALE_WARPS;     // stages of scales, 512 of K each, one for each warp that fills them
 constexpr int SF_BYTES = 3 * 512;          // 128 weight rows, 256 rows of x: 4 bytes each
-constexpr int STAGING_BOX = 32 * 128;      // a warp's transposing box: 32 rows x 32 fp32
-constexpr int NUM_BARS = 4 * MAX_STAGES + 5 + 2 * SF_STAGES;
+constexpr int NUM_BARS = 4 * MAX_STAGES + 6 + 2 * SF_STAGES;
+constexpr int WIDE_KB = 16;                // E4M3 groups: stages of K from which units are up to 256 rows wide, not 224
+constexpr int UNIT_SLOTS = 16;             // more than the units whose stages are in flight
+constexpr int INFO_INTS = 2 * UNIT_SLOTS + 8;
 constexpr int SMEM_LIMIT = 227 * 1024 - 1024;  // (behind the alignment to 1024 bytes)
 constexpr int TMEM_COLS = 512;
 constexpr int GROUP_M = 8;
@@ -76,14 +78,19 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 constexpr unsigned long long kDrainLimitNs = 200000000ull;
 
 constexpr int stage_k(int op) { return op == OP_BF16 ? 64 : 128; }   // elements of K per stage
-constexpr int max_bn(int op) { return op == OP_BF16 ? 256 : 224; }   // columns of an accumulator
+constexpr int MAX_BN = 256;                // columns of an accumulator
+// a warp's transposing box: 32 rows x 32 bf16, backward 32 x 64
+constexpr int staging_box(int kind) { return 32 * (kind == KIND_BACKWARD ? 128 : 64); }
 constexpr int num_threads(int op, int kind) {
   return 32 * (2 + EPI_WARPS + (op == OP_BLOCKS ? SCALE_WARPS : kind == KIND_BACKWARD ? 1 : 0));
 }
-constexpr int fixed_bytes(int op) {
-  return EPI_WARPS * STAGING_BOX + (op == OP_BLOCKS ? SF_STAGES * SF_BYTES : 0) + NUM_BARS * 8 + 16;
+constexpr int fixed_bytes(int op, int kind) {
+  return EPI_WARPS * staging_box(kind) + (op == OP_BLOCKS ? SF_STAGES * SF_BYTES : 0) + NUM_BARS * 8 + 16 + INFO_INTS * 4;
 }
-constexpr int SF_TMEM = 448;               // first column of the scales: two slots of 16
+// First column of the scales: two slots of 16.  Below them are two accumulators, 224 columns
+// apart, or 192 where units are wider than 224: those share 64 columns, and a unit starts
+// when the epilogue has read these, which it does first.
+constexpr int SF_TMEM = 448;
 
 // Instruction descriptors.  kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 (bits 7-9,
 // 10-12 = 1); kind::mxf8f6f4: bits 4-5 / 29-30 which byte of the scales' words B / A
@@ -113,7 +120,6 @@ struct GroupArgs {
   int choose;               // a narrower cap may be chosen from the groups' sizes
   int band_n;               // units across N that are swept together
   int num_kb;               // stages of K of out
-  int accs;                 // accumulators: 2, or 1 where a unit is wider than half of TMEM allows
   int stages, stage_bytes;  // stage_bytes: with room for bn_cap / 2 rows of x
 };
 
@@ -187,15 +193,14 @@ QFFN_DEVI uint32_t pack2(uint64_t v) {
 QFFN_DEVI uint4 pack8(const uint64_t (&v)[4]) { return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3])); }
 
 // The table of units in shared memory: off[0 .. G] the offsets (within 0 .. M, none below
-// the one before it), first[0
-// .. G] the number of the first unit of out of each group; backward: order[0 .. G - 1] the
-// groups, those with rows (`busy` of them) first.
+// the one before it), first[0 .. G] the number of the first unit of out of each group; backward:
+// order[0 .. G - 1] the groups, those with rows first.
 struct Table {
   const int* off;
   const int* first;
   const int* order;
+  int G;
   int cap;            // most rows of a unit
-  int busy;
 };
 struct Unit {
   int group;
@@ -225,7 +230,7 @@ struct Cursor {
 // which the issuing thread left the tensor cores without work.)
 QFFN_DEVI Unit rows_unit(int u, Cursor& c, const Table& t, const GroupArgs& a) {
   if (u >= c.next) {
-    int lo = c.group + 1, hi = a.G - 1;      // the last group whose first unit is u or before
+    int lo = c.group + 1, hi = t.G - 1;      // the last group whose first unit is u or before
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (t.first[mid] <= u) lo = mid;
@@ -306,26 +311,29 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     grouped_kernel(const __grid_constant__ Maps maps, const GroupArgs args) {
   constexpr bool BACKWARD = KIND == KIND_BACKWARD;
   const uint32_t stage = uint32_t(args.stage_bytes);
-  constexpr int ACC_COLS = max_bn(OP);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t ring = smem_u32(smem);
   uint8_t* sStaging = smem + args.stages * args.stage_bytes;
-  uint8_t* sScales = sStaging + EPI_WARPS * STAGING_BOX;
+  uint8_t* sScales = sStaging + EPI_WARPS * staging_box(KIND);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sScales + (OP == OP_BLOCKS ? SF_STAGES * SF_BYTES : 0));
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* table_off = reinterpret_cast<int*>(tmem_slot + 4);
+  int* units_bn = reinterpret_cast<int*>(tmem_slot + 4);   // of the units in flight: width (of dw: negative), rows
+  int* units_rows = units_bn + UNIT_SLOTS;
+  int* one = units_rows + UNIT_SLOTS;                  // the table of one group of all rows: off, first, order
+  int* chosen = one + 5;                               // the cap, groups with rows
+  int* table_off = one + 8;
   int* table_first = table_off + args.G + 1;
   int* table_order = table_first + args.G + 1;         // backward
-  int* found = table_order + (BACKWARD ? args.G : 0);  // the cap's costs, groups with rows
+  int* found = table_order + (BACKWARD ? args.G : 0);  // a number per epilogue warp
   const uint32_t bar0 = smem_u32(bars);
   // full[s] (leader): both CTAs' loads of stage s landed; empty[s]: the MMAs
   // reading stage s are done; tfull[a]: accumulator a is complete; tempty[a]
   // (leader): both CTAs' epilogue warps have read it; drain: all MMAs done;
   // sfull[s] (leader): both CTAs' scales of stage s are written; sempty[s]: copied;
   // backward, a stage of dw with rows behind its group: tail[s]: this CTA's loads landed,
-  // cleared[s] (leader): both CTAs have cleared those rows
+  // cleared[s] (leader): both CTAs have cleared those rows; table: this CTA's table is there
   auto full_bar = [&](int s) { return bar0 + 8u * uint32_t(s); };
   auto empty_bar = [&](int s) { return bar0 + 8u * uint32_t(MAX_STAGES + s); };
   auto tfull_bar = [&](int a) { return bar0 + 8u * uint32_t(2 * MAX_STAGES + a); };
@@ -334,6 +342,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   auto sfull_bar = [&](int s) { return bar0 + 8u * uint32_t(2 * MAX_STAGES + 5 + s); };
   auto tail_bar = [&](int s) { return bar0 + 8u * uint32_t(2 * MAX_STAGES + 5 + 2 * SF_STAGES + s); };
   auto cleared_bar = [&](int s) { return bar0 + 8u * uint32_t(3 * MAX_STAGES + 5 + 2 * SF_STAGES + s); };
+  const uint32_t table_bar = bar0 + 8u * uint32_t(4 * MAX_STAGES + 5 + 2 * SF_STAGES);
   auto sempty_bar = [&](int s) { return bar0 + 8u * uint32_t(2 * MAX_STAGES + 5 + SF_STAGES + s); };
 
   const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -350,6 +359,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       mbar_init(tempty_bar(a), 2 * EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
+    mbar_init(table_bar, 1);
     if (OP == OP_BLOCKS)
       for (int s = 0; s < SF_STAGES; ++s) {
         mbar_init(sfull_bar(s), 2);
@@ -361,12 +371,12 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         mbar_init(cleared_bar(s), 2);
       }
     *abort_flag = 0;
+    one[0] = one[2] = one[4] = 0;
+    one[1] = args.M;
+    one[3] = (args.M + args.bn_cap - 1) / args.bn_cap * args.tiles_n;
     mbar_init_fence();
   }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&maps.w);
-    tma_prefetch_desc(&maps.x[0]);
-  }
+  if (warp == 0 && lane >= 8 && lane < (BACKWARD ? 15 : 13)) tma_prefetch_desc(&maps.w + (lane - 8));
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(TMEM_COLS)
@@ -377,15 +387,27 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   cluster_sync_all();      // both CTAs' barriers exist before either signals the other's
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_wait();              // nothing in global memory is touched before the preceding kernel is done
-  const uint16_t* const bias_row = behind_wait(args.bias);
-  pdl_trigger();
-  for (int i = threadIdx.x; i <= args.G; i += num_threads(OP, KIND))
-    table_off[i] = args.offsets != nullptr ? min(max(args.offsets[i], 0), args.M) : i == 0 ? 0 : args.M;
-  __syncthreads();
-  if (args.offsets != nullptr) {
+  // The table.  Without offsets it is that of one group, and every role looks up its first unit
+  // ahead of the wait for the preceding kernel.  With them the epilogue's warps make it behind
+  // that wait, and the other roles have meanwhile looked a unit of one group up: the first
+  // instructions of a kernel come from L2, and a first lookup takes 2000 cycles where the next
+  // takes 350 (4531 x 2048 x 1536 without offsets 17.2 us, so STARTA).  Nothing in global memory is touched
+  // before the preceding kernel is done.
+  const bool grouped = args.offsets != nullptr;
+  Table table{one, one + 2, one + 4, 1, args.bn_cap};
+  int rows_units = BACKWARD && args.out == nullptr ? 0 : one[3];   // units of out, then those of dw
+  int num_units = rows_units;
+  int busy = 0;                            // backward: groups with rows
+  Cursor cursor;
+  if (grouped && warp >= 2 && warp < 2 + EPI_WARPS) {
+    constexpr int THREADS = 32 * EPI_WARPS;
+    const int t = int(threadIdx.x) - 64, w = warp - 2;
+    auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); };
+    pdl_wait();
+    for (int i = t; i <= args.G; i += THREADS) table_off[i] = min(max(args.offsets[i], 0), args.M);
+    sync();
     // an offset below one before it counts as that one, so that no two groups claim a row
-    if (warp == 0) {
+    if (w == 0) {
       int top = 0;
       for (int base = 0; base <= args.G; base += 32) {
         const int i = base + lane;
@@ -399,87 +421,107 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         top = __shfl_sync(0xffffffffu, v, 31);
       }
     }
-    __syncthreads();
-  }
-  Table table{table_off, table_first, table_order, args.bn_cap, 0};
-  if (!BACKWARD && args.choose != 0) {
-    // Where the widest units make few rounds: the width whose units take the least time, their
-    // rounds by a stage's cycles, 117 + 1.55 bn and 288 at least (see linear.cu); one width per
-    // warp.  (Not for more: narrower units keep less in flight.)
-    const int parts = (args.bn_cap >> 5) - warp;
-    if (warp < 8) {
+    sync();
+    int cap = args.bn_cap;
+    if (!BACKWARD && args.choose != 0) {
+      // Where the widest units make few rounds: the width whose units take the least time, their
+      // rounds by a stage's cycles, 117 + 1.55 bn and 288 at least (see linear.cu); one width per
+      // warp.  (Not for more: narrower units keep less in flight.)
+      const int parts = (args.bn_cap >> 5) - w;
       int n = 0;
       for (int i = lane; i < args.G && parts > 0; i += 32) n += (((group_rows(table_off, i) + 31) >> 5) + parts - 1) / parts;
       n = int(__reduce_add_sync(0xffffffffu, unsigned(n)));
       const int64_t rounds = (int64_t(n) * args.tiles_n + num_pairs - 1) / num_pairs;
       const int64_t cost = rounds * max(288, 117 + 31 * (32 * parts) / 20);
-      if (lane == 0) found[warp] = parts > 0 && (warp > 0 || rounds <= 3) ? int(min(cost, int64_t(0x7FFFFFFE))) : warp > 0 ? 0x7FFFFFFF : -1;
+      if (lane == 0) found[w] = parts > 0 && (w > 0 || rounds <= 3) ? int(min(cost, int64_t(0x7FFFFFFE))) : w > 0 ? 0x7FFFFFFF : -1;
+      sync();
+      int best = 0;
+      for (int i = 1; i < EPI_WARPS; ++i)
+        if (found[i] < found[best]) best = i;
+      cap -= 32 * best;
     }
-    __syncthreads();
-    int best = 0;
-    for (int i = 1; i < 8; ++i)
-      if (found[i] < found[best]) best = i;
-    table.cap -= 32 * best;
-  }
-  if (warp == 0) {
-    int total = 0;
-    for (int base = 0; base < args.G; base += 32) {
-      const int i = base + lane;
-      int n = i < args.G ? (group_rows(table_off, i) + table.cap - 1) / table.cap * args.tiles_n : 0;
+    if (w == 0) {
+      int total = 0;
+      for (int base = 0; base < args.G; base += 32) {
+        const int i = base + lane;
+        int n = i < args.G ? (group_rows(table_off, i) + cap - 1) / cap * args.tiles_n : 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int below = __shfl_up_sync(0xffffffffu, n, o);
-        if (lane >= o) n += below;
-      }
-      if (i < args.G) table_first[i + 1] = total + n;
-      total += __shfl_sync(0xffffffffu, n, 31);
-    }
-    if (lane == 0) table_first[0] = 0;
-  }
-  if (BACKWARD) {
-    // the groups in the order of their weight gradients: the longest first, up to 256 of them
-    // (each counts those before it); more as they come, those without rows last
-    if (args.G <= 256) {
-      const int i = int(threadIdx.x), n = i < args.G ? group_rows(table_off, i) : 0;
-      if (i < args.G) {
-        int at = 0;
-#pragma unroll 4
-        for (int j = 0; j < args.G; ++j) {
-          const int m = group_rows(table_off, j);
-          at += m > n || (m == n && j < i) ? 1 : 0;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int below = __shfl_up_sync(0xffffffffu, n, o);
+          if (lane >= o) n += below;
         }
-        table_order[at] = i;
+        if (i < args.G) table_first[i + 1] = total + n;
+        total += __shfl_sync(0xffffffffu, n, 31);
       }
-      table.busy = __syncthreads_count(n > 0);
-    } else {
-      if (warp == 1) {
-        int busy = 0;
+      if (lane == 0) {
+        table_first[0] = 0;
+        chosen[0] = cap;
+      }
+    }
+    if (BACKWARD) {
+      // the groups in the order of their weight gradients: the longest first, up to 256 of them
+      // (each counts those before it); more as they come, those without rows last
+      if (args.G <= THREADS) {
+        const int n = t < args.G ? group_rows(table_off, t) : 0;
+        if (t < args.G) {
+          int at = 0;
+#pragma unroll 4
+          for (int j = 0; j < args.G; ++j) {
+            const int m = group_rows(table_off, j);
+            at += m > n || (m == n && j < t) ? 1 : 0;
+          }
+          table_order[at] = t;
+        }
+        const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+        if (lane == 0) found[w] = __popc(some);
+      } else if (w == 1) {
+        int before_all = 0;
         for (int base = 0; base < args.G; base += 32) {
           const int i = base + lane;
           const bool rows = i < args.G && group_rows(table_off, i) > 0;
           const uint32_t some = __ballot_sync(0xffffffffu, rows);
-          const int before = busy + __popc(some & ((1u << lane) - 1u));
+          const int before = before_all + __popc(some & ((1u << lane) - 1u));
           if (i < args.G) table_order[rows ? before : args.G - 1 - (i - before)] = i;
-          busy += __popc(some);
+          before_all += __popc(some);
         }
-        if (lane == 0) found[8] = busy;
+        if (lane < EPI_WARPS) found[lane] = lane == 0 ? before_all : 0;
       }
-      __syncthreads();
-      table.busy = found[8];
+      sync();
+      if (t == 0) {
+        int n = 0;
+        for (int i = 0; i < EPI_WARPS; ++i) n += found[i];
+        chosen[1] = n;
+      }
     }
+    sync();
+    if (t == 0) mbar_arrive(table_bar);
   }
-  __syncthreads();
-
-  // Units: of out (rows_units of them), then of dw.  This pair's in round r:
-  const int rows_units = BACKWARD && args.out == nullptr ? 0 : table_first[args.G];
-  const int num_units = rows_units + (BACKWARD ? table.busy * args.tiles_r * args.tiles_n : 0);
+  // Behind the preceding kernel, with the table (false: the wait for it ran out).
+  auto start = [&]() -> bool {
+    pdl_wait();
+    pdl_trigger();
+    if (!grouped) return true;
+    if (!mbar_wait(table_bar, 0, abort_flag)) {
+      num_units = 0;
+      return false;
+    }
+    table = Table{table_off, table_first, table_order, args.G, chosen[0]};
+    cursor = Cursor{};
+    if (BACKWARD) busy = chosen[1];
+    rows_units = BACKWARD && args.out == nullptr ? 0 : table_first[args.G];
+    num_units = rows_units + (BACKWARD ? busy * args.tiles_r * args.tiles_n : 0);
+    return true;
+  };
+  // This pair's units in round r.
   auto number = [&](int r) { return r * num_pairs + pair; };
-  Cursor cursor;
   auto unit_at = [&](int u) {
     return BACKWARD && u >= rows_units ? weight_unit(u - rows_units, table, args) : rows_unit(u, cursor, table, args);
   };
   // stages of K of a unit
-  auto stages_of = [&](const Unit& u, bool weight) { return weight ? (u.rows + 63) / 64 : args.num_kb; };
+  auto stages_of = [&](int rows, bool weight) { return weight ? (rows + 63) / 64 : args.num_kb; };
+  // the accumulators' distance, and whether they share columns
+  auto sharing = [&] { return OP == OP_BLOCKS && table.cap > 224; };
+  auto acc_columns = [&] { return OP == OP_BF16 ? MAX_BN : table.cap > 224 ? 192 : 224; };
 
   if (warp == 0) {
     if (elect_one()) {
@@ -488,14 +530,29 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       uint32_t tails = 0, tail_parity = 0;   // stages whose tail barrier was armed, and its phase now
       int s = 0;
       bool ok = true;
-      for (int r = 0, un = number(0); ok && un < num_units; un = number(++r)) {
-        const Unit u = unit_at(un);
+      bool begun = false;
+      for (int r = 0, un = number(0); ok; un = number(++r)) {
+        if (begun && un >= num_units) break;
+        const Unit u = unit_at(begun || !grouped ? un : 0);
+        if (!begun) {
+          ok = start();
+          begun = true;
+          if (grouped) {
+            --r;
+            continue;
+          }
+          if (un >= num_units) break;
+        }
         const bool weight = BACKWARD && un >= rows_units;
+        if (rank == 0) {                     // for the issuer (published by the arrival on the first stage's barrier)
+          units_bn[r % UNIT_SLOTS] = weight ? -u.bn : u.bn;
+          if (BACKWARD) units_rows[r % UNIT_SLOTS] = u.rows;
+        }
         const int row_w = u.nb * (2 * BM) + int(rank) * BM;      // of the 256-row operand
         const int half = u.bn / 2;
         const int row_x = (weight ? u.kb * 256 : u.row0) + int(rank) * half;
         const uint32_t stage_tx = 2u * uint32_t(OP_BYTES + half * ROW_BYTES);
-        const int num = stages_of(u, weight);
+        const int num = stages_of(u.rows, weight);
         for (int kb = 0; kb < num; ++kb) {
           if (!mbar_wait(empty_bar(s), ph ^ 1u, abort_flag)) { ok = false; break; }
           const int k0 = kb * stage_k(OP);
@@ -561,19 +618,20 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       // ------------------------------------------------------------ MMA issuer (leader)
       int s = 0, local = 0, chunk = 0;
       uint32_t ph = 0, cleared_parity = 0;
-      bool ok = true;
+      bool ok = start();
+      const bool shared = sharing();
+      const int acc_cols = acc_columns();
       for (int un = number(0); ok && un < num_units; un = number(++local)) {
-        const int acc = local & (args.accs - 1);
-        const uint32_t aph = uint32_t(local >> (args.accs - 1)) & 1u;
-        const Unit u = unit_at(un);          // (while the MMAs before run)
-        const bool weight = BACKWARD && un >= rows_units;
-        if (!mbar_wait_cluster_bounded(tempty_bar(acc), aph ^ 1u, abort_flag, &g_status, kWaitLimitNs)) break;
+        const int acc = local & 1;
+        if (!mbar_wait(full_bar(s), ph, abort_flag)) break;
+        const int width = units_bn[local % UNIT_SLOTS], rows = BACKWARD ? units_rows[local % UNIT_SLOTS] : 0;
+        const bool weight = BACKWARD && width < 0;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + uint32_t(acc * ACC_COLS);
-        const uint32_t idesc = idesc_for(OP, BACKWARD, weight, u.bn);
-        const int num = stages_of(u, weight);
+        const uint32_t d_tmem = tmem_base + uint32_t(acc * acc_cols);
+        const uint32_t idesc = idesc_for(OP, BACKWARD, weight, weight ? -width : width);
+        const int num = stages_of(rows, weight);
         uint32_t sf = 0;                     // TMEM columns of the current scales
-        bool ready = false;                  // the next stage was there before this one's MMAs were issued
+        bool ready = true;                   // the next stage was there before this one's MMAs were issued
         for (int kb = 0; kb < num; ++kb) {
           if (OP == OP_BLOCKS && (kb & 3) == 0) {
             const int ss = chunk % SF_STAGES;
@@ -591,12 +649,21 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
             ++chunk;
           }
           if (!ready && !mbar_wait(full_bar(s), ph, abort_flag)) { ok = false; break; }
-          if (weight && rows_to_clear(u.rows - kb * 64)) {
+          if (weight && rows_to_clear(rows - kb * 64)) {
             if (!mbar_wait_cluster_bounded(cleared_bar(s), (cleared_parity >> s) & 1u, abort_flag, &g_status, kWaitLimitNs)) {
               ok = false;
               break;
             }
             cleared_parity ^= 1u << s;
+          }
+          if (kb == 0) {
+            // the accumulator has been read, or, where it shares columns with that of the unit
+            // before, that unit's share of them (a warp that says so has read the one before)
+            const int of = shared ? local - 1 : local - 2;
+            if (of >= 0 && !mbar_wait_cluster_bounded(tempty_bar(of & 1), uint32_t(of >> 1) & 1u, abort_flag, &g_status, kWaitLimitNs)) {
+              ok = false;
+              break;
+            }
           }
           tc_fence_after();
           const uint32_t a0 = ring + uint32_t(s) * stage, b0 = a0 + uint32_t(OP_BYTES), empty = empty_bar(s);
@@ -614,7 +681,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
           } else if (weight) {
 #pragma unroll
             for (int i = 0; i < STEPS; ++i)
-              if (kb * 64 + 16 * i < u.rows) mma_pair_f16(d_tmem, step_desc<true>(a0, i), step_desc<true>(b0, i), idesc, uint32_t(kb | i));
+              if (kb * 64 + 16 * i < rows) mma_pair_f16(d_tmem, step_desc<true>(a0, i), step_desc<true>(b0, i), idesc, uint32_t(kb | i));
           } else {
 #pragma unroll
             for (int i = 0; i < STEPS; ++i)
@@ -640,32 +707,71 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     const int mine = warp - (2 + EPI_WARPS);
     const bool whole = ((reinterpret_cast<uintptr_t>(args.x_scale) | reinterpret_cast<uintptr_t>(args.w_scale) | uintptr_t(args.blocks)) & 3u) == 0;
     const int chunks = (args.num_kb + 3) / 4;          // of a unit
-    auto word = [&](const uint8_t* p, int left) {
-      if (whole) return *reinterpret_cast<const uint32_t*>(p);
+    // Four bytes at p, of which the first `left` exist: one word where all are aligned, else out
+    // of the two aligned words around them where both lie within the scales.
+    auto aligned = [](const uint8_t* p) { return reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3)); };
+    auto inside = [&](const uint8_t* p, const uint8_t* base, const uint8_t* end) {
+      const uint8_t* const q = reinterpret_cast<const uint8_t*>(aligned(p));
+      return q >= base && q + 8 <= end;
+    };
+    auto joined = [&](const uint8_t* p) {
+      return __funnelshift_r(aligned(p)[0], aligned(p)[1], 8u * uint32_t(reinterpret_cast<uintptr_t>(p) & 3u));
+    };
+    auto bytes = [](const uint8_t* p, int left) {
       uint32_t v = p[0];
       if (left > 1) v |= uint32_t(p[1]) << 8;
       if (left > 2) v |= uint32_t(p[2]) << 16;
       if (left > 3) v |= uint32_t(p[3]) << 24;
       return v;
     };
+    const uint8_t* const xs_end = args.x_scale + size_t(args.M) * size_t(args.blocks);
+    const uint8_t* const ws_end = args.w_scale + size_t(args.G) * size_t(args.n_blocks) * size_t(args.blocks);
     const uint32_t dst = smem_u32(sScales) + uint32_t(mine * SF_BYTES + lane * 16);
     int c = mine;
     uint32_t fills = 0;
     bool ok = true;
-    for (int r = 0, un = number(0); ok && un < num_units; un = number(++r), c -= chunks) {
-      if (c >= chunks) continue;
-      const Unit u = unit_at(un);
+    bool begun = false;
+    for (int r = 0, un = number(0); ok; un = number(++r)) {
+      if (begun && un >= num_units) break;
+      if (begun && c >= chunks) {
+        c -= chunks;
+        continue;
+      }
+      const Unit u = unit_at(begun || !grouped ? un : 0);
+      if (!begun) {
+        ok = __all_sync(0xffffffffu, start());
+        begun = true;
+        if (grouped || c >= chunks) {
+          --r;
+          continue;
+        }
+        if (un >= num_units) break;
+      }
       const int block_w = min(u.nb * 2 + int(rank), args.n_blocks - 1);
       const uint8_t* const ws = args.w_scale + (size_t(u.group) * size_t(args.n_blocks) + size_t(block_w)) * size_t(args.blocks);
       for (; c < chunks; c += SCALE_WARPS) {
         const int left = args.blocks - 4 * c;
-        const uint32_t w = word(ws + size_t(4 * c), left);
-        uint32_t x[8];
+        const uint8_t* const wp = ws + size_t(4 * c);
+        const uint8_t* xp[8];
+        bool within = inside(wp, args.w_scale, ws_end);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          x[i] = 0u;
-          if (32 * i < u.bn)
-            x[i] = word(args.x_scale + size_t(min(u.row0 + 32 * i + lane, args.M - 1)) * size_t(args.blocks) + size_t(4 * c), left);
+          xp[i] = args.x_scale + size_t(min(u.row0 + 32 * i + lane, args.M - 1)) * size_t(args.blocks) + size_t(4 * c);
+          within = within && (32 * i >= u.bn || inside(xp[i], args.x_scale, xs_end));
+        }
+        uint32_t w, x[8];
+        if (whole) {
+          w = aligned(wp)[0];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? aligned(xp[i])[0] : 0u;
+        } else if (__all_sync(0xffffffffu, within)) {
+          w = joined(wp);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? joined(xp[i]) : 0u;
+        } else {
+          w = bytes(wp, left);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? bytes(xp[i], left) : 0u;
         }
         ok = __all_sync(0xffffffffu, mbar_wait(sempty_bar(mine), (fills & 1u) ^ 1u, abort_flag));
         if (!ok) break;
@@ -677,6 +783,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         if (lane == 0) mbar_arrive_remote(map_to_rank(sfull_bar(mine), 0));
         ++fills;
       }
+      c -= chunks;
     }
     // the issuer's last arrival on this stage reaches this CTA
     if (ok && fills > 0) mbar_wait(sempty_bar(mine), (fills & 1u) ^ 1u, abort_flag, false, kDrainLimitNs);
@@ -688,10 +795,11 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     // is its bytes 128 r ..).
     uint32_t parity = 0;
     int s = 0;
+    __all_sync(0xffffffffu, start());
     for (int r = 0, un = number(0); un < num_units; un = number(++r)) {
       const bool weight = un >= rows_units;
       const Unit u = weight ? unit_at(un) : Unit{};
-      const int num = stages_of(u, weight), live = u.rows - (num - 1) * 64;
+      const int num = stages_of(u.rows, weight), live = u.rows - (num - 1) * 64;
       s = (s + num - 1) % args.stages;
       if (weight && rows_to_clear(live)) {
         if (!__all_sync(0xffffffffu, mbar_wait(tail_bar(s), (parity >> s) & 1u, abort_flag))) break;
@@ -715,7 +823,11 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     // that of the global accesses, 16 bytes per lane (see linear.cu).
     constexpr int WG = EPI_WARPS / 4;
     const int q = warp & 3, wg = (warp - 2) >> 2;
-    const uint32_t box = smem_u32(sStaging + (q * WG + wg) * STAGING_BOX);
+    const uint32_t box = smem_u32(sStaging + (q * WG + wg) * staging_box(KIND));
+    start();
+    const uint16_t* const bias_row = behind_wait(args.bias);
+    const bool shared = sharing();
+    const int acc_cols = acc_columns();
     int local = 0, un = number(0);
     {
       // out: the lanes are columns of the output, the accumulator's columns its rows, 32 at a
@@ -731,15 +843,16 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       const uint32_t block8 = box + uint32_t(lane & 7) * 64u + (uint32_t((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
       const size_t step = size_t(8) * size_t(args.N);
       for (; un < rows_units; un = number(++local)) {
-        const int acc = local & (args.accs - 1);
-        const uint32_t aph = uint32_t(local >> (args.accs - 1)) & 1u;
+        const int acc = local & 1;
+        const uint32_t aph = uint32_t(local >> 1) & 1u;
         const Unit u = unit_at(un);
         const int row_end = min(u.begin + u.rows, u.row0 + u.bn);
         const int col0 = u.nb * (2 * BM) + int(rank) * BM + q * 32, col = col0 + ch * 8;
-        const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * ACC_COLS);
-        const int groups = u.bn / 32;
+        const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * acc_cols);
+        // this warp's groups are g0, g0 + by, ..; the columns that the accumulators share first
+        const int groups = u.bn / 32, by = shared && acc == 0 ? -WG : WG, g0 = by > 0 ? wg : groups - 1 - wg;
         // (a quarter of the lanes past the last column has none)
-        const int share = (groups + WG - 1) / WG, g0 = wg * share, g1 = col0 < args.N ? min(groups, g0 + share) : 0;
+        const int count = col0 < args.N ? (groups - wg + WG - 1) / WG : 0;
         const size_t at = size_t(u.row0 + sub) * size_t(args.N) + size_t(col);
         const int rows_here = col < args.N ? row_end - u.row0 - sub : 0;   // group g: rows 8 i < rows_here - 32 g
         float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};      // of columns sub, 8 + sub, ..
@@ -750,7 +863,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         }
         uint4 next_in[4];                    // what is added, requested a group ahead
         auto request = [&](int g) {
-          const int left = g < g1 ? rows_here - 32 * g : 0;
+          const int left = g >= 0 && g < groups ? rows_here - 32 * g : 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             next_in[i] = make_uint4(0, 0, 0, 0);
@@ -760,18 +873,18 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         if (!BACKWARD && args.in != nullptr) {
           // the first group's are requested here, the others' set out for L2
           if ((ch & 1) == 0)
-            for (int g = g0 + 1; g < g1; ++g) {
+            for (int k = 1, g = g0 + by; k < count; ++k, g += by) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 if (8 * i < rows_here - 32 * g) prefetch_l2(args.in + (at + size_t(4 * g + i) * step));
             }
-          request(g0);
+          if (count > 0) request(g0);
         }
         if (!mbar_wait(tfull_bar(acc), aph, abort_flag)) { un = num_units; break; }
         tc_fence_after();
-        const bool awaited = number(local + args.accs) < num_units;   // another unit takes this accumulator
-        auto loaded = [&](int g) {
-          if (g + 1 >= g1) {
+        const bool awaited = number(local + (shared ? 1 : 2)) < num_units;   // another unit waits for this accumulator
+        auto loaded = [&](int k) {
+          if (k == (shared ? 0 : count - 1)) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0 && awaited) mbar_arrive_remote_relaxed(map_to_rank(tempty_bar(acc), 0));
@@ -801,7 +914,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) sts16(turn16 + 512u * i, next_in[i]);
             __syncwarp();
-            request(g + 1);
+            request(g + by);
           }
 #pragma unroll
           for (int c = 0; c < 4; ++c) {      // rows 8 c .. of the group, four blocks of columns
@@ -827,15 +940,15 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
           leave(g);
         };
         auto unit = [&](auto extras) {
-          for (int g = g0; g < g1; ++g) {
+          for (int k = 0, g = g0; k < count; ++k, g += by) {
             uint32_t lo[16], hi[16];
             issue(g, lo, hi);
             tmem_wait_ld16(lo, hi);
-            loaded(g);
+            loaded(k);
             process(extras, g, lo, hi);
           }
         };
-        if (g0 >= g1) loaded(g0);            // (a unit with fewer groups than warps)
+        if (count <= 0) loaded(shared ? 0 : count - 1);   // (a unit with fewer groups than warps)
         else if (!BACKWARD && (args.in != nullptr || args.bias != nullptr)) unit(Flag<!BACKWARD>{});
         else unit(Flag<false>{});
       }
@@ -882,9 +995,9 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         }
       }
       for (; un < num_units; un = number(++local)) {
-        const int acc = local & (args.accs - 1);
-        const uint32_t aph = uint32_t(local >> (args.accs - 1)) & 1u;
-        const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * ACC_COLS);
+        const int acc = local & 1;
+        const uint32_t aph = uint32_t(local >> 1) & 1u;
+        const uint32_t tbase = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc * acc_cols);
         const int next = number(local + 1);
         const bool awaited = number(local + 2) < num_units;
         const Part p_next = part_of(unit_at(next < num_units ? next : un));
@@ -940,7 +1053,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       // the gradient of a matrix without rows is zero, or what it was when adding
       if (args.in == nullptr && *abort_flag == 0) {
         const int per_group = args.tiles_r * args.tiles_n;
-        for (int e = table.busy * per_group + pair; e < args.G * per_group; e += num_pairs) {
+        for (int e = busy * per_group + pair; e < args.G * per_group; e += num_pairs) {
           const Part z = part_of(weight_unit(e, table, args));
 #pragma unroll
           for (int k = 0; k < GROUPS; ++k) {
@@ -1006,18 +1119,16 @@ cudaError_t max_pairs(int* pairs) {
 // `units`: no fewer than the kernel will find
 template <int OP, int KIND>
 cudaError_t launch(const Maps& m, GroupArgs a, int64_t units, int pairs, cudaStream_t s) {
-  const int table = (KIND == KIND_BACKWARD ? 12 : 8) * (a.G + 1) + 48;
-  const bool wide = a.bn_cap > max_bn(OP);
-  a.accs = wide ? 1 : 2;
+  const int table = (KIND == KIND_BACKWARD ? 12 : 8) * (a.G + 1) + 4 * EPI_WARPS;
   // (narrow units: more stages, whose loads' latency is what bounds them; 512 x 4096 x 2048
   // with six stages 11.3 us, with eight 10.7)
   a.stage_bytes = OP_BYTES + a.bn_cap / 2 * ROW_BYTES;
-  a.stages = (SMEM_LIMIT - fixed_bytes(OP) - table) / a.stage_bytes;
+  a.stages = (SMEM_LIMIT - fixed_bytes(OP, KIND) - table) / a.stage_bytes;
   if (a.stages > MAX_STAGES) a.stages = MAX_STAGES;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * unsigned(units < pairs ? units : pairs));
   cfg.blockDim = dim3(num_threads(OP, KIND));
-  cfg.dynamicSmemBytes = size_t(a.stages * a.stage_bytes + fixed_bytes(OP) + table + 1024);
+  cfg.dynamicSmemBytes = size_t(a.stages * a.stage_bytes + fixed_bytes(OP, KIND) + table + 1024);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1034,34 +1145,30 @@ cudaError_t launch(const Maps& m, GroupArgs a, int64_t units, int pairs, cudaStr
 int ceil_div(int64_t a, int64_t b) { return int((a + b - 1) / b); }
 
 // One group's rows are cut so that its units fill the SM pairs in the fewest and
-// narrowest rounds, a stage taking 117 + 1.55 bn cycles and 288 at least (see linear.cu).
-// With one unit per pair at most, E4M3 needs no second accumulator and takes 256 rows
-// too.  `cycles`: of a stage of K in all rounds.
+// narrowest rounds, a stage taking 117 + 1.55 bn cycles and 288 at least (see linear.cu);
+// E4M3 units wider than 224, which start when the one before has been read in part, 700 more.
+// `cycles`: of all rounds.
 struct Cut {
   int bn;
   int64_t cycles;
 };
-Cut cut_rows(int op, int64_t M, int tiles_n, int pairs) {
-  const int cap = max_bn(op);
+Cut cut_rows(int op, int64_t M, int tiles_n, int num_kb, int pairs) {
   const int64_t parts = (M + 31) / 32;
-  Cut best{cap, -1};
+  Cut best{MAX_BN, -1};
   for (int64_t tm = (parts + 7) / 8; tm < (parts + 7) / 8 + 8 && tm <= parts; ++tm) {
     const int bn = 32 * int((parts + tm - 1) / tm);
-    const int64_t units = tm * tiles_n;
-    if (bn > cap && units > pairs) continue;
+    const int64_t rounds = (tm * tiles_n + pairs - 1) / pairs;
     const int64_t stage = 117 + 31 * bn / 20;
-    const int64_t cost = (units + pairs - 1) / pairs * (stage > 288 ? stage : 288);
+    const int64_t cost = rounds * (stage > 288 ? stage : 288) * num_kb + (op == OP_BLOCKS && bn > 224 ? (rounds - 1) * 700 : 0);
     if (best.cycles < 0 || cost < best.cycles) best = Cut{bn, cost};
   }
   return best;
 }
-// Most rows of a unit.  Several groups, whose sizes the host does not know: the widest
-// (256 in E4M3 where a pair has one unit at most), or 128 where they have few rows, for the
-// sake of more stages.
-int choose_cap(int op, int64_t G, int64_t M, int tiles_n, int pairs) {
-  if (G == 1) return cut_rows(op, M, tiles_n, pairs).bn;
-  const bool one_round = (M / 256 + (G < M ? G : M)) * tiles_n <= pairs;
-  return M / G < 96 ? 128 : one_round ? 256 : max_bn(op);
+// Most rows of a unit.  Several groups, whose sizes the host does not know: the widest, or 128
+// where they have few rows, for the sake of more stages.
+int choose_cap(int op, int64_t G, int64_t M, int tiles_n, int num_kb, int pairs) {
+  if (G == 1) return cut_rows(op, M, tiles_n, num_kb, pairs).bn;
+  return M / G < 96 ? 128 : op == OP_BLOCKS && num_kb < WIDE_KB ? 224 : MAX_BN;
 }
 
 // out [M, N] from x [M, K] and w [G, N, K].
@@ -1091,9 +1198,9 @@ cudaError_t forward(uint16_t* out, const void* x, const uint8_t* x_scale, const 
   int pairs = 0;
   const cudaError_t e = max_pairs<OP, KIND_FORWARD>(&pairs);
   if (e != cudaSuccess) return e;
-  a.bn_cap = choose_cap(OP, G, M, a.tiles_n, pairs);
-  a.choose = G > 1 && a.bn_cap <= max_bn(OP);
   a.num_kb = ceil_div(K, stage_k(OP));
+  a.bn_cap = choose_cap(OP, G, M, a.tiles_n, a.num_kb, pairs);
+  a.choose = G > 1;
   // bands of about 32 MB of weights where they are the larger operand (see linear.cu)
   const int64_t band = (int64_t(32) << 20) / (2 * BM * K * bytes);
   a.band_n = N <= M / G || band >= a.tiles_n ? a.tiles_n : band < 1 ? 1 : int(band);
@@ -1121,7 +1228,7 @@ cudaError_t backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uin
   a.rows = int(N);
   a.tiles_n = ceil_div(K, 256);
   a.tiles_r = ceil_div(N, 256);
-  a.bn_cap = max_bn(OP_BF16);
+  a.bn_cap = MAX_BN;
   a.num_kb = ceil_div(N, 64);
   const int64_t band = (int64_t(32) << 20) / (2 * BM * N * 2);
   a.band_n = K <= M / G || band >= a.tiles_n ? a.tiles_n : band < 1 ? 1 : int(band);
@@ -1150,8 +1257,8 @@ cudaError_t launch_linear_blocks(uint16_t* out, const uint8_t* x, const uint8_t*
     return launch_few_groups(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
   const int64_t few = few_rows_cycles(M, N, K, false, true, 2048);
   if (few >= 0) {
-    const Cut c = cut_rows(OP_BLOCKS, M, ceil_div(N, 2 * BM), kNumSMsHint / 2);
-    const int64_t here = 8000 + 36 * c.bn + c.cycles * ceil_div(K, 128);
+    const Cut c = cut_rows(OP_BLOCKS, M, ceil_div(N, 2 * BM), ceil_div(K, 128), kNumSMsHint / 2);
+    const int64_t here = 8000 + 36 * c.bn + c.cycles;
     if (20 * few < 23 * here) return launch_few_rows_blocks(out, x, x_scale, w, w_scale, bias, res, M, N, K, s);
   }
   return forward<OP_BLOCKS>(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
@@ -1161,7 +1268,7 @@ cudaError_t launch_linear_blocks(uint16_t* out, const uint8_t* x, const uint8_t*
 // each row of a unit, and the stages.
 int64_t grouped_cycles(int op, int64_t G, int64_t M, int64_t N, int64_t K) {
   const int64_t groups = G < M ? G : M, rows = (M + groups - 1) / groups;
-  const int cap = (M / G < 96 ? 128 : max_bn(op)) / 32;
+  const int cap = (M / G < 96 ? 128 : op == OP_BF16 ? MAX_BN : 224) / 32;
   const int64_t parts = (rows + 31) / 32, tiles = (parts + cap - 1) / cap, bn = 32 * ((parts + tiles - 1) / tiles);
   const int64_t units = groups * tiles * ceil_div(N, 2 * BM), pairs = kNumSMsHint / 2;
   const int64_t stage = 117 + 31 * bn / 20;
