@@ -727,63 +727,62 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     const uint8_t* const xs_end = args.x_scale + size_t(args.M) * size_t(args.blocks);
     const uint8_t* const ws_end = args.w_scale + size_t(args.G) * size_t(args.n_blocks) * size_t(args.blocks);
     const uint32_t dst = smem_u32(sScales) + uint32_t(mine * SF_BYTES + lane * 16);
-    int c = mine;
+    int r = 0, c = mine;
     uint32_t fills = 0;
-    bool ok = true;
-    bool begun = false;
-    for (int r = 0, un = number(0); ok; un = number(++r)) {
-      if (begun && un >= num_units) break;
-      if (begun && c >= chunks) {
-        c -= chunks;
-        continue;
+    bool ok = true, begun = false, fresh = true;
+    Unit u{};
+    while (ok) {
+      for (; c >= chunks; c -= chunks) {
+        ++r;
+        fresh = true;
       }
-      const Unit u = unit_at(begun || !grouped ? un : 0);
-      if (!begun) {
+      const int un = number(r);
+      if ((begun || !grouped) && un >= num_units) break;
+      if (fresh) u = unit_at(begun || !grouped ? un : 0);
+      fresh = false;
+      const int left = args.blocks - 4 * c;
+      const int block_w = min(u.nb * 2 + int(rank), args.n_blocks - 1);
+      const uint8_t* const wp =
+          args.w_scale + (size_t(u.group) * size_t(args.n_blocks) + size_t(block_w)) * size_t(args.blocks) + size_t(4 * c);
+      const uint8_t* xp[8];
+      bool within = inside(wp, args.w_scale, ws_end);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        xp[i] = args.x_scale + size_t(min(u.row0 + 32 * i + lane, args.M - 1)) * size_t(args.blocks) + size_t(4 * c);
+        within = within && (32 * i >= u.bn || inside(xp[i], args.x_scale, xs_end));
+      }
+      if (!begun) {                          // (the addresses ahead of the wait for the preceding kernel)
         ok = __all_sync(0xffffffffu, start());
         begun = true;
-        if (grouped || c >= chunks) {
-          --r;
+        if (grouped) {
+          fresh = true;
           continue;
         }
-        if (un >= num_units) break;
       }
-      const int block_w = min(u.nb * 2 + int(rank), args.n_blocks - 1);
-      const uint8_t* const ws = args.w_scale + (size_t(u.group) * size_t(args.n_blocks) + size_t(block_w)) * size_t(args.blocks);
-      for (; c < chunks; c += SCALE_WARPS) {
-        const int left = args.blocks - 4 * c;
-        const uint8_t* const wp = ws + size_t(4 * c);
-        const uint8_t* xp[8];
-        bool within = inside(wp, args.w_scale, ws_end);
+      uint32_t w, x[8];
+      if (whole) {
+        w = aligned(wp)[0];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          xp[i] = args.x_scale + size_t(min(u.row0 + 32 * i + lane, args.M - 1)) * size_t(args.blocks) + size_t(4 * c);
-          within = within && (32 * i >= u.bn || inside(xp[i], args.x_scale, xs_end));
-        }
-        uint32_t w, x[8];
-        if (whole) {
-          w = aligned(wp)[0];
+        for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? aligned(xp[i])[0] : 0u;
+      } else if (__all_sync(0xffffffffu, within)) {
+        w = joined(wp);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? aligned(xp[i])[0] : 0u;
-        } else if (__all_sync(0xffffffffu, within)) {
-          w = joined(wp);
+        for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? joined(xp[i]) : 0u;
+      } else {
+        w = bytes(wp, left);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? joined(xp[i]) : 0u;
-        } else {
-          w = bytes(wp, left);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? bytes(xp[i], left) : 0u;
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(sempty_bar(mine), (fills & 1u) ^ 1u, abort_flag));
-        if (!ok) break;
-        sts16(dst, make_uint4(w, w, w, w));
-        sts16(dst + 512, make_uint4(x[0], x[1], x[2], x[3]));
-        sts16(dst + 1024, make_uint4(x[4], x[5], x[6], x[7]));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(map_to_rank(sfull_bar(mine), 0));
-        ++fills;
+        for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? bytes(xp[i], left) : 0u;
       }
-      c -= chunks;
+      ok = __all_sync(0xffffffffu, mbar_wait(sempty_bar(mine), (fills & 1u) ^ 1u, abort_flag));
+      if (!ok) break;
+      sts16(dst, make_uint4(w, w, w, w));
+      sts16(dst + 512, make_uint4(x[0], x[1], x[2], x[3]));
+      sts16(dst + 1024, make_uint4(x[4], x[5], x[6], x[7]));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(map_to_rank(sfull_bar(mine), 0));
+      ++fills;
+      c += SCALE_WARPS;
     }
     // the issuer's last arrival on this stage reaches this CTA
     if (ok && fills > 0) mbar_wait(sempty_bar(mine), (fills & 1u) ^ 1u, abort_flag, false, kDrainLimitNs);
