@@ -304,6 +304,7 @@ struct Maps {
   CUtensorMap w;        // the weights [G, rows, cols]
   CUtensorMap x[4];     // rows of x (backward: of dout) in boxes of 128, 64, 32, 16
   CUtensorMap dout_mn, x_mn;   // backward: boxes of 64 rows by 64 values
+  CUtensorMap dw;              // [G, rows, cols] in boxes of 32 rows by 64 values
 };
 
 template <int OP, int KIND>
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     one[3] = (args.M + args.bn_cap - 1) / args.bn_cap * args.tiles_n;
     mbar_init_fence();
   }
-  if (warp == 0 && lane >= 8 && lane < (BACKWARD ? 15 : 13)) tma_prefetch_desc(&maps.w + (lane - 8));
+  if (warp == 0 && lane >= 8 && lane < (BACKWARD ? 16 : 13)) tma_prefetch_desc(&maps.w + (lane - 8));
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "r"(TMEM_COLS)
@@ -961,6 +962,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       const size_t step4 = size_t(4) * size_t(args.N);
       struct Part {
         int col;                             // column of this lane's share of the first 64
+        int row0, box_col, group;            // of the warp's first box
         uint32_t rows;                       // bit i: row sub8 + 4 i exists
         size_t at;
       };
@@ -968,6 +970,9 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         Part p;
         const int row0 = u.nb * (2 * BM) + int(rank) * BM + q * 32;
         p.col = u.kb * 256 + ch8 * 8;
+        p.row0 = row0;
+        p.box_col = u.kb * 256;
+        p.group = u.group;
         p.rows = 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) p.rows |= (row0 + sub8 + 4 * i < args.rows ? 1u : 0u) << i;
@@ -1005,7 +1010,8 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
 #pragma unroll
         for (int k = 0; k < GROUPS; ++k) {
           const int g = wg + k * WG;
-          __syncwarp();                      // the previous group has been read out of the box
+          if (lane == 0) bulk_wait_read_0();   // the previous group has been read out of the box
+          __syncwarp();
           if (args.in != nullptr) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) sts16((turn8 ^ uint32_t((i & 1) << 6)) + 512u * i, in8[k][i]);
@@ -1037,18 +1043,16 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
               sts16(addr, pack8(z));
             }
           }
+          fence_proxy_async_smem();
           __syncwarp();
-          const uint32_t live = p.col + g * 64 < args.N ? p.rows : 0u;
-          uint16_t* const dst = args.dw + (p.at + size_t(g * 64));
-          uint4 o[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = lds16((turn8 ^ uint32_t((i & 1) << 6)) + 512u * i);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if ((live >> i) & 1u) stg16(dst + size_t(i) * step4, o[i]);
+          if (lane == 0 && p.box_col + g * 64 < args.N && p.row0 < args.rows) {
+            tma_store_3d(&maps.dw, box, p.box_col + g * 64, p.row0, p.group);
+            bulk_commit();
+          }
         }
         p = p_next;
       }
+      if (lane == 0) bulk_wait_all();
       // the gradient of a matrix without rows is zero, or what it was when adding
       if (args.in == nullptr && *abort_flag == 0) {
         const int per_group = args.tiles_r * args.tiles_n;
@@ -1214,6 +1218,7 @@ cudaError_t backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uin
   Maps m{};
   bool ok = make_operand_map_3d(&m.w, w, true, G, N, K, K * 2, K * N * 2, 64) &&
             make_operand_map(&m.dout_mn, dout, true, M, N, 64) && make_operand_map(&m.x_mn, x, true, M, K, 64);
+  ok = ok && make_operand_map_3d(&m.dw, dw, true, G, N, K, K * 2, K * N * 2, 32);
   for (int b = 0; ok && b < 4; ++b) ok = make_operand_map(&m.x[b], dout, true, M, N, 128 >> b);
   if (!ok) return cudaErrorInvalidValue;
   GroupArgs a{};

@@ -122,6 +122,13 @@ QFFN_DEVI void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) 
                "r"(x), "r"(y), "r"(src)
                : "memory");
 }
+// The same of a 3-D map.
+QFFN_DEVI void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
 QFFN_DEVI void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Wait until at most one committed store group still reads shared memory.
 QFFN_DEVI void bulk_wait_read_1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
