@@ -228,6 +228,30 @@ def test_grouped_backward(q, G, M, N, K, kind, accumulate):
     assert torch.equal(again, dw)
 
 
+@pytest.mark.parametrize("G,M,N,K", [(1, 3, 8728, 680), (2, 5, 4104, 72), (3, 40, 6152, 136), (1, 1, 16384, 8), (5, 33, 8200, 264)])
+@pytest.mark.parametrize("kind", ["ragged", "one", "gaps"])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_grouped_backward_of_long_rows(q, G, M, N, K, kind, accumulate):
+    """Few rows of dout that are much longer than those of x, written by the kernel just before the call."""
+    off = _sizes(kind, G, M)
+    dout, x, w = _t(1, M, N, std=0.1), _t(2, M, K), _t(3, G, N, K, std=0.1)
+    old = _t(4, G, N, K) if accumulate else None
+    d, xs, ws, o = dout.cuda(), x.cuda(), w.cuda(), off.cuda()
+    dx, dw = _new(M, K), old.cuda() if accumulate else _new(G, N, K)
+    late_d, late_x = torch.zeros_like(d), torch.zeros_like(xs)
+    torch.cuda.synchronize()
+    late_d.copy_(d)
+    late_x.copy_(xs)
+    q.qffn_grouped_linear_backward(dx, dw, late_d, late_x, ws, o, G, M, N, K, accumulate)
+    then = dx.clone(), dw.clone()                                   # (read by the kernel just behind)
+    q.qffn_check_status()
+    want_dx, want_dw, b_dx, b_dw, live = B.grouped_backward(dout.double(), x.double(), w.double(), off,
+                                                            old.double() if accumulate else None)
+    P.check(then[0][live.cuda()], want_dx[live], b_dx[live], "dx")
+    P.check(then[1], want_dw, b_dw, "dw")
+    assert bool(torch.isnan(dx[~live.cuda()]).all())
+
+
 @pytest.mark.parametrize("M", [6, 40, 700])
 def test_grouped_backward_neighbours_do_not_mix(q, M):
     """A group that ends anywhere: what the next one, or no group, holds does not reach its gradients."""

@@ -402,6 +402,9 @@ __global__ void __launch_bounds__(kThreads)
         if (GATED) {
           tma_load_2d(dw, &tmW, fb, k0, n0);
           tma_load_2d(dw + BOX_BYTES / 2, &tmW, fb, k0, args.N + n0);
+        } else if (GROUPED && W_MN) {
+          tma_load_3d(dw, &tmW, fb, n0, k0, group);
+          tma_load_3d(dw + BOX_BYTES / 2, &tmW, fb, n0 + 64, k0, group);
         } else if (GROUPED) {
           tma_load_3d(dw, &tmW, fb, k0, n0, group);
         } else if (W_MN) {
@@ -754,7 +757,8 @@ int grouped_bn(int64_t G, int64_t M) {
 int64_t grouped_clusters(int64_t G, int64_t M, int64_t N) {
   return (N + 127) / 128 * (M / grouped_bn(G, M) + (G < M ? G : M));
 }
-template <int OP>
+// out [M, N] from x [M, K] and w [G, N, K] or, W_MN, [G, K, N].
+template <int OP, bool W_MN = false>
 cudaError_t grouped_product(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w, const uint8_t* w_scale,
                             const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K, cudaStream_t s) {
   FewArgs a{};
@@ -777,9 +781,11 @@ cudaError_t grouped_product(uint16_t* out, const void* x, const uint8_t* x_scale
   CUtensorMap mw, mx;
   const bool bf16 = OP == OP_BF16;
   const int64_t pitch = K * (bf16 ? 2 : 1);
-  if (!make_operand_map_3d(&mw, w, bf16, G, N, K, pitch, N * pitch, 128) || !make_operand_map(&mx, x, bf16, M, K, a.bn))
-    return cudaErrorInvalidValue;
-  return launch<OP, false, EPI_LINEAR, true>(mw, mx, a, clusters, s);
+  const bool ok = (W_MN ? make_operand_map_3d(&mw, w, bf16, G, K, N, N * 2, K * N * 2, 64)
+                        : make_operand_map_3d(&mw, w, bf16, G, N, K, pitch, N * pitch, 128)) &&
+                  make_operand_map(&mx, x, bf16, M, K, a.bn);
+  if (!ok) return cudaErrorInvalidValue;
+  return launch<OP, W_MN, EPI_LINEAR, true>(mw, mx, a, clusters, s);
 }
 }  // namespace
 
@@ -799,6 +805,11 @@ cudaError_t launch_few_rows_grouped(uint16_t* out, const void* x, const uint8_t*
                                     int64_t K, cudaStream_t s) {
   return x_scale != nullptr ? grouped_product<OP_BLOCKS>(out, x, x_scale, w, w_scale, offsets, G, M, N, K, s)
                             : grouped_product<OP_BF16>(out, x, nullptr, w, nullptr, offsets, G, M, N, K, s);
+}
+
+cudaError_t launch_few_rows_grouped_dx(uint16_t* dx, const uint16_t* dout, const uint16_t* w, const int* offsets, int64_t G,
+                                       int64_t M, int64_t N, int64_t K, cudaStream_t s) {
+  return grouped_product<OP_BF16, true>(dx, dout, nullptr, w, nullptr, offsets, G, M, K, N, s);
 }
 
 cudaError_t launch_few_rows_gated(uint16_t* out, const uint16_t* x, const uint16_t* w1, const uint16_t* dh, int act,

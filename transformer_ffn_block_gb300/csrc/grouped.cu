@@ -118,6 +118,7 @@ struct GroupArgs {
   int tiles_r;              // backward: units of 256 across a matrix's rows
   int bn_cap;               // most rows of a unit, a multiple of 32
   int choose;               // a narrower cap may be chosen from the groups' sizes
+  int late_wait;            // does not read the preceding kernel's results (see launch.h)
   int band_n;               // units across N that are swept together
   int num_kb;               // stages of K of out
   int stages, stage_bytes;  // stage_bytes: with room for bn_cap / 2 rows of x
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     constexpr int THREADS = 32 * EPI_WARPS;
     const int t = int(threadIdx.x) - 64, w = warp - 2;
     auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); };
-    pdl_wait();
+    if (!args.late_wait) pdl_wait();
     for (int i = t; i <= args.G; i += THREADS) table_off[i] = min(max(args.offsets[i], 0), args.M);
     sync();
     // an offset below one before it counts as that one, so that no two groups claim a row
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   }
   // Behind the preceding kernel, with the table (false: the wait for it ran out).
   auto start = [&]() -> bool {
-    pdl_wait();
+    if (!args.late_wait) pdl_wait();
     pdl_trigger();
     if (!grouped) return true;
     if (!mbar_wait(table_bar, 0, abort_flag)) {
@@ -1071,6 +1072,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     }
   }
 
+  if (args.late_wait) pdl_wait();    // this kernel is not complete before the preceding one
   // Both CTAs finish together: the leader's MMAs write the peer's TMEM and
   // both CTAs signal barriers of the other.  (Every arrival and copy that the other
   // CTA makes here has been waited for, so the barrier orders no memory.)
@@ -1214,7 +1216,8 @@ cudaError_t forward(uint16_t* out, const void* x, const uint8_t* x_scale, const 
 
 // dx [M, K] (NULL: none) and dw [G, N, K] (+)= from dout [M, N], x [M, K] and w [G, N, K].
 cudaError_t backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uint16_t* x, const uint16_t* w,
-                     const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K, bool accumulate, cudaStream_t s) {
+                     const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K, bool accumulate, bool late_wait,
+                     cudaStream_t s) {
   Maps m{};
   bool ok = make_operand_map_3d(&m.w, w, true, G, N, K, K * 2, K * N * 2, 64) &&
             make_operand_map(&m.dout_mn, dout, true, M, N, 64) && make_operand_map(&m.x_mn, x, true, M, K, 64);
@@ -1225,6 +1228,7 @@ cudaError_t backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uin
   a.out = dx;
   a.dw = dw;
   a.in = accumulate ? dw : nullptr;
+  a.late_wait = late_wait ? 1 : 0;
   a.offsets = offsets;
   a.G = int(G);
   a.M = int(M);
@@ -1303,11 +1307,22 @@ cudaError_t launch_grouped(uint16_t* out, const void* x, const uint8_t* x_scale,
   return forward<OP_BF16>(out, x, nullptr, w, nullptr, nullptr, nullptr, offsets, G, M, N, K, s);
 }
 
+// Both gradients in one launch, unless a unit of dx, whose stages of N follow one another at 480
+// cycles, takes longer than dx by few_rows.cu (N split over a cluster) and dw behind it, beside
+// it where SMs are free: 7000 cycles for the call, 3400 for each round of units.  Measured,
+// us, one launch against two: 3 rows of 8728 x 680 37.2 / 17.0, 2 in each of eight of 4096 x 1024
+// 34.7 / 33.8, 156 in two of 1952 x 1288 15.5 / 17.9, 3 of 680 x 8728 10.2 / 16.7.
 cudaError_t launch_grouped_backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uint16_t* x,
                                     const uint16_t* w, const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K,
                                     bool accumulate, cudaStream_t s) {
   if (M == 0) return accumulate ? cudaSuccess : cudaMemsetAsync(dw, 0, size_t(G) * size_t(N) * size_t(K) * 2, s);
-  return backward(dx, dw, dout, x, w, offsets, G, M, N, K, accumulate, s);
+  const int64_t few = dx != nullptr ? few_rows_grouped_cycles(G, M, K, N, false) : -1;
+  const int64_t units = G * ceil_div(N, 256) * ceil_div(K, 256), pairs = kNumSMsHint / 2;
+  if (few >= 0 && few + 7000 + (units + pairs - 1) / pairs * 3400 < int64_t(ceil_div(N, 64)) * 480) {
+    const cudaError_t e = launch_few_rows_grouped_dx(dx, dout, w, offsets, G, M, N, K, s);
+    return e != cudaSuccess ? e : backward(nullptr, dw, dout, x, w, offsets, G, M, N, K, accumulate, true, s);
+  }
+  return backward(dx, dw, dout, x, w, offsets, G, M, N, K, accumulate, false, s);
 }
 
 cudaError_t grouped_take_status(unsigned int* status) {

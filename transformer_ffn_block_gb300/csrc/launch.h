@@ -194,6 +194,9 @@ int64_t few_rows_grouped_cycles(int64_t G, int64_t M, int64_t N, int64_t K, bool
 cudaError_t launch_few_rows_grouped(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w,
                                     const uint8_t* w_scale, const int* offsets, int64_t G, int64_t M, int64_t N,
                                     int64_t K, cudaStream_t s);
+// The input gradient of launch_grouped: dx [M, K] = dout [M, N] w_g.
+cudaError_t launch_few_rows_grouped_dx(uint16_t* dx, const uint16_t* dout, const uint16_t* w, const int* offsets, int64_t G,
+                                       int64_t M, int64_t N, int64_t K, cudaStream_t s);
 cudaError_t few_rows_take_status(unsigned int* status);
 // Reads and clears the linear kernels' device status word of the current device.
 cudaError_t linear_take_status(unsigned int* status);
