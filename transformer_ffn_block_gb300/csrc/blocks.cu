@@ -89,6 +89,8 @@ QFFN_DEVI void stg8(void* p, uint2 v) { *reinterpret_cast<uint2*>(p) = v; }
 // lanes of a block are in one half warp; a thread takes kFlight of them, all loads in
 // flight at once.  The row of a chunk is a product with `magic` = floor(2^64 / chunks per
 // row) + 1: exact for fewer than 2^44 chunks, as the divisor is at most 2^17.
+// Measured: rows of 8192 x 8192 31.5 us (6.4 TB/s), SwiGLU 8192 x 14336 87.8 us (6.7 TB/s; with
+// scalar arithmetic 123), 37 x 2048 2.3 us, most of it a launch.
 constexpr int kFlight = 4;
 template <bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, SWIGLU ? 4 : 6) rows_kernel(uint16_t* h, uint8_t* q, uint8_t* scale,
@@ -139,7 +141,9 @@ __global__ void __launch_bounds__(kThreads, SWIGLU ? 4 : 6) rows_kernel(uint16_t
 // warp each and no barrier.  Short rows go R at a time, so that a thread has about
 // four loads in flight.
 // FEW: the gain is requested with the row, for calls of few rows, which wait once; else
-// after the sums, from L1, which leaves registers for more rows at a time.
+// after the sums, from L1, which leaves registers for more rows at a time (4096 x 16384 91 us
+// with the gain in registers, 78 from L1).  Measured with a residual: 8192 x 4096 38.7 us (6.1
+// TB/s), 16384 x 1024 21 us (5.6), 1 x 4096 2.1 us.
 template <int V, bool FEW>
 constexpr int rows_at_once() { return FEW || V > 2 ? 1 : V == 2 ? 2 : 4; }
 
@@ -252,6 +256,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (FEW || V <= 2 ? 1024 :
 
 // ------------------------------------------------------------------ weights
 // One CTA per 128 x 128 of matrix blockIdx.z: a thread holds 8 values of each of 8 rows.
+// Measured: 8192 x 8192 38.5 us (5.2 TB/s), once per set of weights.
 __global__ void __launch_bounds__(kThreads) weight_blocks_kernel(uint8_t* q, uint8_t* scale, const uint16_t* w,
                                                                  int64_t rows, int64_t cols, int64_t row_blocks) {
   __shared__ uint32_t red[kThreads / 32];

@@ -27,6 +27,7 @@
 // GROUPED: rows in groups with a matrix each (see grouped.cu), a cluster per (tile of
 // 128 weight rows, tile of rows of one group).  The host launches as many tiles of rows as
 // there can be; a cluster finds its group from the offsets, and one beyond the last ends.
+// With W_MN it is their input gradient.
 //
 // OP_BLOCKS: E4M3 with a power-of-two scale per block of 128, which the tensor cores
 // multiply (grouped.cu says how): two warps write the scales of 512 of K at a time to

@@ -34,8 +34,7 @@
 //   read the scales of 512 of K at a time (one byte per row of x and block, one per
 //   128 weight rows and block), lay them out in shared memory, and the issuing thread
 //   copies them to TMEM (tcgen05.cp) in front of the MMAs that use them.  The tensor
-//   cores then scale for nothing; sums never leave TMEM.  TMEM holds two
-//   accumulators of 224 columns and the scales.
+//   cores then scale for nothing; sums never leave TMEM.
 //
 // Every mbarrier wait is bounded; see gemm_fp8.cu for how a wait that runs out
 // ends the kernel (abort flag, status word, drained copies and MMAs).
@@ -66,7 +65,6 @@ constexpr int MAX_STAGES = 10;
 constexpr int SF_STAGES = SCALE_WARPS;     // stages of scales, 512 of K each, one for each warp that fills them
 constexpr int SF_BYTES = 3 * 512;          // 128 weight rows, 256 rows of x: 4 bytes each
 constexpr int NUM_BARS = 4 * MAX_STAGES + 6 + 2 * SF_STAGES;
-constexpr int WIDE_KB = 16;                // E4M3 groups: stages of K from which units are up to 256 rows wide, not 224
 constexpr int UNIT_SLOTS = 16;             // more than the units whose stages are in flight
 constexpr int INFO_INTS = 2 * UNIT_SLOTS + 8;
 constexpr int SMEM_LIMIT = 227 * 1024 - 1024;  // (behind the alignment to 1024 bytes)
@@ -89,7 +87,9 @@ constexpr int fixed_bytes(int op, int kind) {
 }
 // First column of the scales: two slots of 16.  Below them are two accumulators, 224 columns
 // apart, or 192 where units are wider than 224: those share 64 columns, and a unit starts
-// when the epilogue has read these, which it does first.
+// when the epilogue has read these, which it does first.  (Units of 224 rows at most
+// against 256: 8192 rows in eight groups of 28672 x 4096 692 us / 677, 8192 rows of
+// 4096 x 2048 45.3 / 44.1, of 4096 x 512 20.0 / 20.7.)
 constexpr int SF_TMEM = 448;
 
 // Instruction descriptors.  kind::f16: D fp32 (bits 4-5 = 1), A and B bf16 (bits 7-9,
@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   // ahead of the wait for the preceding kernel.  With them the epilogue's warps make it behind
   // that wait, and the other roles have meanwhile looked a unit of one group up: the first
   // instructions of a kernel come from L2, and a first lookup takes 2000 cycles where the next
-  // takes 350 (4531 x 2048 x 1536 without offsets 17.2 us, so STARTA).  Nothing in global memory is touched
-  // before the preceding kernel is done.
+  // takes 350 (4531 x 2048 x 1536 without offsets 17.2 us, so 15.6).  Nothing in global
+  // memory is touched before the preceding kernel is done.
   const bool grouped = args.offsets != nullptr;
   Table table{one, one + 2, one + 4, 1, args.bn_cap};
   int rows_units = BACKWARD && args.out == nullptr ? 0 : one[3];   // units of out, then those of dw
@@ -1150,30 +1150,28 @@ cudaError_t launch(const Maps& m, GroupArgs a, int64_t units, int pairs, cudaStr
 int ceil_div(int64_t a, int64_t b) { return int((a + b - 1) / b); }
 
 // One group's rows are cut so that its units fill the SM pairs in the fewest and
-// narrowest rounds, a stage taking 117 + 1.55 bn cycles and 288 at least (see linear.cu);
-// E4M3 units wider than 224, which start when the one before has been read in part, 700 more.
+// narrowest rounds, a stage taking 117 + 1.55 bn cycles and 288 at least (see linear.cu).
 // `cycles`: of all rounds.
 struct Cut {
   int bn;
   int64_t cycles;
 };
-Cut cut_rows(int op, int64_t M, int tiles_n, int num_kb, int pairs) {
+Cut cut_rows(int64_t M, int tiles_n, int num_kb, int pairs) {
   const int64_t parts = (M + 31) / 32;
   Cut best{MAX_BN, -1};
   for (int64_t tm = (parts + 7) / 8; tm < (parts + 7) / 8 + 8 && tm <= parts; ++tm) {
     const int bn = 32 * int((parts + tm - 1) / tm);
     const int64_t rounds = (tm * tiles_n + pairs - 1) / pairs;
     const int64_t stage = 117 + 31 * bn / 20;
-    const int64_t cost = rounds * (stage > 288 ? stage : 288) * num_kb + (op == OP_BLOCKS && bn > 224 ? (rounds - 1) * 700 : 0);
+    const int64_t cost = rounds * (stage > 288 ? stage : 288) * num_kb;
     if (best.cycles < 0 || cost < best.cycles) best = Cut{bn, cost};
   }
   return best;
 }
 // Most rows of a unit.  Several groups, whose sizes the host does not know: the widest, or 128
 // where they have few rows, for the sake of more stages.
-int choose_cap(int op, int64_t G, int64_t M, int tiles_n, int num_kb, int pairs) {
-  if (G == 1) return cut_rows(op, M, tiles_n, num_kb, pairs).bn;
-  return M / G < 96 ? 128 : op == OP_BLOCKS && num_kb < WIDE_KB ? 224 : MAX_BN;
+int choose_cap(int64_t G, int64_t M, int tiles_n, int num_kb, int pairs) {
+  return G == 1 ? cut_rows(M, tiles_n, num_kb, pairs).bn : M / G < 96 ? 128 : MAX_BN;
 }
 
 // out [M, N] from x [M, K] and w [G, N, K].
@@ -1204,7 +1202,7 @@ cudaError_t forward(uint16_t* out, const void* x, const uint8_t* x_scale, const 
   const cudaError_t e = max_pairs<OP, KIND_FORWARD>(&pairs);
   if (e != cudaSuccess) return e;
   a.num_kb = ceil_div(K, stage_k(OP));
-  a.bn_cap = choose_cap(OP, G, M, a.tiles_n, a.num_kb, pairs);
+  a.bn_cap = choose_cap(G, M, a.tiles_n, a.num_kb, pairs);
   a.choose = G > 1;
   // bands of about 32 MB of weights where they are the larger operand (see linear.cu)
   const int64_t band = (int64_t(32) << 20) / (2 * BM * K * bytes);
@@ -1252,7 +1250,7 @@ cudaError_t backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uin
 // Which form a block-scaled layer takes.  grouped_few.cu up to 8 rows, and up to 16 and 32
 // while the weights are small: us, it against few_rows.cu: 1 row of 4096 x 14336 13.0 / 13.1, 16
 // of 1024 x 1024 2.2 / 4.4, of 4096 x 4096 6.9 / 7.1, of 8192 x 2048 7.4 / 7.0, 32 of 4096 x 1024
-// 4.3 / 4.4, of 4096 x 4096 11.2 / 7.3.  few_rows.cu up to 512 rows where its estimate is not
+// 4.3 / 4.4, of 4096 x 4096 11.2 / 7.3.  few_rows.cu up to 2048 rows where its estimate is not
 // 1.15 times this file's, 8000 cycles for the call, 36 for each row of a unit and the stages
 // (its few stages of long K overlap better than both formulas say): few_rows.cu against it, 64
 // rows of 4096 x 14336 14.7 / 26, of 4096 x 4096 8.0 / 10.5, 512 of 4096 x 4096 13.4 / 12.5, of 14336 x
@@ -1265,7 +1263,7 @@ cudaError_t launch_linear_blocks(uint16_t* out, const uint8_t* x, const uint8_t*
     return launch_few_groups(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
   const int64_t few = few_rows_cycles(M, N, K, false, true, 2048);
   if (few >= 0) {
-    const Cut c = cut_rows(OP_BLOCKS, M, ceil_div(N, 2 * BM), ceil_div(K, 128), kNumSMsHint / 2);
+    const Cut c = cut_rows(M, ceil_div(N, 2 * BM), ceil_div(K, 128), kNumSMsHint / 2);
     const int64_t here = 8000 + 36 * c.bn + c.cycles;
     if (20 * few < 23 * here) return launch_few_rows_blocks(out, x, x_scale, w, w_scale, bias, res, M, N, K, s);
   }
@@ -1276,7 +1274,7 @@ cudaError_t launch_linear_blocks(uint16_t* out, const uint8_t* x, const uint8_t*
 // each row of a unit, and the stages.
 int64_t grouped_cycles(int op, int64_t G, int64_t M, int64_t N, int64_t K) {
   const int64_t groups = G < M ? G : M, rows = (M + groups - 1) / groups;
-  const int cap = (M / G < 96 ? 128 : op == OP_BF16 ? MAX_BN : 224) / 32;
+  const int cap = (M / G < 96 ? 128 : MAX_BN) / 32;
   const int64_t parts = (rows + 31) / 32, tiles = (parts + cap - 1) / cap, bn = 32 * ((parts + tiles - 1) / tiles);
   const int64_t units = groups * tiles * ceil_div(N, 2 * BM), pairs = kNumSMsHint / 2;
   const int64_t stage = 117 + 31 * bn / 20;
