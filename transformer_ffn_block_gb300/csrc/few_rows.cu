@@ -482,26 +482,31 @@ __global__ void __launch_bounds__(kThreads)
     const int chunks = (kb1 - kb0 + 3) / 4;
     const uint8_t* const wb = args.w_blocks + size_t(group * ((args.N + 127) / 128) + tile) * size_t(args.blocks);
     const bool whole = ((reinterpret_cast<uintptr_t>(args.x_blocks) | reinterpret_cast<uintptr_t>(args.w_blocks) | uintptr_t(args.blocks | kb0)) & 3u) == 0;
-    auto word = [&](const uint8_t* p, int n) {
-      if (whole) return *reinterpret_cast<const uint32_t*>(p);
-      uint32_t v = p[0];
-      if (n > 1) v |= uint32_t(p[1]) << 8;
-      if (n > 2) v |= uint32_t(p[2]) << 16;
-      if (n > 3) v |= uint32_t(p[3]) << 24;
-      return v;
-    };
+    const uint8_t* const xs_end = args.x_blocks + size_t(args.M) * size_t(args.blocks);
+    const uint8_t* const ws_end = args.w_blocks + size_t(args.G > 0 ? args.G : 1) * size_t((args.N + 127) / 128) * size_t(args.blocks);
     bool going = true;
     for (int c = warp - 3; going && c < chunks; c += 2) {
       const int first = kb0 + 4 * c, n = min(4, kb1 - first);
-      const uint32_t word_w = word(wb + first, n);
-      uint32_t word_x[4];
+      const uint8_t* xp[4];
+      bool within = scales_within(wb + first, args.w_blocks, ws_end);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        word_x[i] = 0u;
-        if (32 * i < args.bn) {
-          const size_t row = size_t(min(row0 + 32 * i + lane, args.M - 1));
-          word_x[i] = word(args.x_blocks + row * size_t(args.blocks) + size_t(first), n);
-        }
+        xp[i] = args.x_blocks + size_t(min(row0 + 32 * i + lane, args.M - 1)) * size_t(args.blocks) + size_t(first);
+        within = within && (32 * i >= args.bn || scales_within(xp[i], args.x_blocks, xs_end));
+      }
+      uint32_t word_w, word_x[4];
+      if (whole) {
+        word_w = scales_word(wb + first)[0];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) word_x[i] = 32 * i < args.bn ? scales_word(xp[i])[0] : 0u;
+      } else if (__all_sync(0xffffffffu, within)) {
+        word_w = scales_joined(wb + first);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) word_x[i] = 32 * i < args.bn ? scales_joined(xp[i]) : 0u;
+      } else {
+        word_w = scales_bytes(wb + first, n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) word_x[i] = 32 * i < args.bn ? scales_bytes(xp[i], n) : 0u;
       }
       const int ss = c % kScaleStages;
       going = __all_sync(0xffffffffu, mbar_wait(sempty_bar(ss), (uint32_t(c / kScaleStages) & 1u) ^ 1u, abort_flag));

@@ -709,23 +709,6 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     const int mine = warp - (2 + EPI_WARPS);
     const bool whole = ((reinterpret_cast<uintptr_t>(args.x_scale) | reinterpret_cast<uintptr_t>(args.w_scale) | uintptr_t(args.blocks)) & 3u) == 0;
     const int chunks = (args.num_kb + 3) / 4;          // of a unit
-    // Four bytes at p, of which the first `left` exist: one word where all are aligned, else out
-    // of the two aligned words around them where both lie within the scales.
-    auto aligned = [](const uint8_t* p) { return reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3)); };
-    auto inside = [&](const uint8_t* p, const uint8_t* base, const uint8_t* end) {
-      const uint8_t* const q = reinterpret_cast<const uint8_t*>(aligned(p));
-      return q >= base && q + 8 <= end;
-    };
-    auto joined = [&](const uint8_t* p) {
-      return __funnelshift_r(aligned(p)[0], aligned(p)[1], 8u * uint32_t(reinterpret_cast<uintptr_t>(p) & 3u));
-    };
-    auto bytes = [](const uint8_t* p, int left) {
-      uint32_t v = p[0];
-      if (left > 1) v |= uint32_t(p[1]) << 8;
-      if (left > 2) v |= uint32_t(p[2]) << 16;
-      if (left > 3) v |= uint32_t(p[3]) << 24;
-      return v;
-    };
     const uint8_t* const xs_end = args.x_scale + size_t(args.M) * size_t(args.blocks);
     const uint8_t* const ws_end = args.w_scale + size_t(args.G) * size_t(args.n_blocks) * size_t(args.blocks);
     const uint32_t dst = smem_u32(sScales) + uint32_t(mine * SF_BYTES + lane * 16);
@@ -747,11 +730,11 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       const uint8_t* const wp =
           args.w_scale + (size_t(u.group) * size_t(args.n_blocks) + size_t(block_w)) * size_t(args.blocks) + size_t(4 * c);
       const uint8_t* xp[8];
-      bool within = inside(wp, args.w_scale, ws_end);
+      bool within = scales_within(wp, args.w_scale, ws_end);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         xp[i] = args.x_scale + size_t(min(u.row0 + 32 * i + lane, args.M - 1)) * size_t(args.blocks) + size_t(4 * c);
-        within = within && (32 * i >= u.bn || inside(xp[i], args.x_scale, xs_end));
+        within = within && (32 * i >= u.bn || scales_within(xp[i], args.x_scale, xs_end));
       }
       if (!begun) {                          // (the addresses ahead of the wait for the preceding kernel)
         ok = __all_sync(0xffffffffu, start());
@@ -763,17 +746,17 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       }
       uint32_t w, x[8];
       if (whole) {
-        w = aligned(wp)[0];
+        w = scales_word(wp)[0];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? aligned(xp[i])[0] : 0u;
+        for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? scales_word(xp[i])[0] : 0u;
       } else if (__all_sync(0xffffffffu, within)) {
-        w = joined(wp);
+        w = scales_joined(wp);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? joined(xp[i]) : 0u;
+        for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? scales_joined(xp[i]) : 0u;
       } else {
-        w = bytes(wp, left);
+        w = scales_bytes(wp, left);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? bytes(xp[i], left) : 0u;
+        for (int i = 0; i < 8; ++i) x[i] = 32 * i < u.bn ? scales_bytes(xp[i], left) : 0u;
       }
       ok = __all_sync(0xffffffffu, mbar_wait(sempty_bar(mine), (fills & 1u) ^ 1u, abort_flag));
       if (!ok) break;

@@ -238,4 +238,25 @@ QFFN_DEVI uint32_t bf16x2_absmax(uint32_t m, uint32_t v) {
   return r;
 }
 
+// Four bytes of block scales at any address p, in one word.  Where p is a multiple of four,
+// that word; else out of the two aligned words around p, where both lie within the scales
+// base .. end (scales_within); else byte by byte, the `n` that exist.
+QFFN_DEVI const uint32_t* scales_word(const uint8_t* p) {
+  return reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3));
+}
+QFFN_DEVI bool scales_within(const uint8_t* p, const uint8_t* base, const uint8_t* end) {
+  const uint8_t* const q = reinterpret_cast<const uint8_t*>(scales_word(p));
+  return q >= base && q + 8 <= end;
+}
+QFFN_DEVI uint32_t scales_joined(const uint8_t* p) {
+  return __funnelshift_r(scales_word(p)[0], scales_word(p)[1], 8u * uint32_t(reinterpret_cast<uintptr_t>(p) & 3u));
+}
+QFFN_DEVI uint32_t scales_bytes(const uint8_t* p, int n) {
+  uint32_t v = p[0];
+  if (n > 1) v |= uint32_t(p[1]) << 8;
+  if (n > 2) v |= uint32_t(p[2]) << 16;
+  if (n > 3) v |= uint32_t(p[3]) << 24;
+  return v;
+}
+
 }  // namespace qffn
