@@ -66,7 +66,7 @@ constexpr int SF_STAGES = SCALE_WARPS;     // stages of scales, 512 of K each, o
 constexpr int SF_BYTES = 3 * 512;          // 128 weight rows, 256 rows of x: 4 bytes each
 constexpr int NUM_BARS = 4 * MAX_STAGES + 6 + 2 * SF_STAGES;
 constexpr int UNIT_SLOTS = 16;             // more than the units whose stages are in flight
-constexpr int INFO_INTS = 2 * UNIT_SLOTS + 8;
+constexpr int INFO_INTS = 2 * UNIT_SLOTS + 12;
 constexpr int SMEM_LIMIT = 227 * 1024 - 1024;  // (behind the alignment to 1024 bytes)
 constexpr int TMEM_COLS = 512;
 constexpr int GROUP_M = 8;
@@ -324,8 +324,8 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   int* units_bn = reinterpret_cast<int*>(tmem_slot + 4);   // of the units in flight: width (of dw: negative), rows
   int* units_rows = units_bn + UNIT_SLOTS;
   int* one = units_rows + UNIT_SLOTS;                  // the table of one group of all rows: off, first, order
-  int* chosen = one + 5;                               // the cap, groups with rows
-  int* table_off = one + 8;
+  int* chosen = one + 5;                               // the cap, groups with rows, and see `spare`
+  int* table_off = one + 12;
   int* table_first = table_off + args.G + 1;
   int* table_order = table_first + args.G + 1;         // backward
   int* found = table_order + (BACKWARD ? args.G : 0);  // a number per epilogue warp
@@ -399,7 +399,11 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   Table table{one, one + 2, one + 4, 1, args.bn_cap};
   int rows_units = BACKWARD && args.out == nullptr ? 0 : one[3];   // units of out, then those of dw
   int num_units = rows_units;
-  int busy = 0;                            // backward: groups with rows
+  // backward: groups with rows; this pair's units of out; the `spare` pairs behind the last unit of
+  // out, which have one less of those, take `early` units of dw meanwhile, and the rest of dw goes
+  // round from them on (by turns regardless: 3 rows in five groups of 3080 x 1672 29.8 us, so 26.1; 4459
+  // in seven of 4864 x 320 44.0, so 37.0)
+  int busy = 0, of_out = 0, spare = num_pairs, turn = pair, early = 0, early_all = 0;
   Cursor cursor;
   if (grouped && warp >= 2 && warp < 2 + EPI_WARPS) {
     constexpr int THREADS = 32 * EPI_WARPS;
@@ -493,6 +497,13 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         int n = 0;
         for (int i = 0; i < EPI_WARPS; ++i) n += found[i];
         chosen[1] = n;
+        // a stage of out takes 500 cycles, one of dw 514, and its stores 4000, added to dw twice that
+        const int units = args.out == nullptr ? 0 : table_first[args.G];
+        const int rounds = quick_div(units, num_pairs), over = units - rounds * num_pairs;
+        const int stages = n > 0 ? (group_rows(table_off, table_order[0]) + 63) / 64 : 0;
+        chosen[2] = rounds;
+        chosen[3] = num_pairs - over;
+        chosen[4] = over > 0 ? quick_div(args.num_kb * 500, max(args.in != nullptr ? 8000 : 4000, stages * 514 + 2300)) : 0;
       }
     }
     sync();
@@ -509,13 +520,26 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     }
     table = Table{table_off, table_first, table_order, args.G, chosen[0]};
     cursor = Cursor{};
-    if (BACKWARD) busy = chosen[1];
     rows_units = BACKWARD && args.out == nullptr ? 0 : table_first[args.G];
-    num_units = rows_units + (BACKWARD ? busy * args.tiles_r * args.tiles_n : 0);
+    num_units = rows_units;
+    if (BACKWARD) {
+      busy = chosen[1];
+      num_units += busy * args.tiles_r * args.tiles_n;
+      spare = chosen[3];
+      const int over = num_pairs - spare;
+      of_out = chosen[2] + (pair < over ? 1 : 0);
+      turn = pair < over ? spare + pair : pair - over;
+      early = turn < spare ? chosen[4] : 0;
+      early_all = chosen[4] * spare;
+    }
     return true;
   };
-  // This pair's units in round r.
-  auto number = [&](int r) { return r * num_pairs + pair; };
+  // This pair's unit in round r.
+  auto number = [&](int r) {
+    if (!BACKWARD || r < of_out) return r * num_pairs + pair;
+    const int k = r - of_out;
+    return rows_units + turn + (k < early ? k * spare : early_all + (k - early) * num_pairs);
+  };
   auto unit_at = [&](int u) {
     return BACKWARD && u >= rows_units ? weight_unit(u - rows_units, table, args) : rows_unit(u, cursor, table, args);
   };
