@@ -391,10 +391,11 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   const uint32_t tmem_base = *tmem_slot;
   // The table.  Without offsets it is that of one group, and every role looks up its first unit
   // ahead of the wait for the preceding kernel.  With them the epilogue's warps make it behind
-  // that wait, and the other roles have meanwhile looked a unit of one group up: the first
-  // instructions of a kernel come from L2, and a first lookup takes 2000 cycles where the next
-  // takes 350 (4531 x 2048 x 1536 without offsets 17.2 us, so 15.6).  Nothing in global
-  // memory is touched before the preceding kernel is done.
+  // that wait.  The first instructions of a kernel come from L2 (a first lookup takes 2000
+  // cycles, the next 350), so those warps go through the same code once before, for one group,
+  // and the other roles look one of its units up: pass 0.  (4531 x 2048 x 1536 without offsets
+  // 17.2 us, so 15.6; 10200 rows in 14 groups of 1176 x 1664, E4M3, WARMA.)  Nothing in
+  // global memory is touched before the preceding kernel is done.
   const bool grouped = args.offsets != nullptr;
   Table table{one, one + 2, one + 4, 1, args.bn_cap};
   int rows_units = BACKWARD && args.out == nullptr ? 0 : one[3];   // units of out, then those of dw
@@ -409,120 +410,132 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     constexpr int THREADS = 32 * EPI_WARPS;
     const int t = int(threadIdx.x) - 64, w = warp - 2;
     auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); };
-    if (!args.late_wait) pdl_wait();
-    for (int i = t; i <= args.G; i += THREADS) table_off[i] = min(max(args.offsets[i], 0), args.M);
-    sync();
-    // an offset below one before it counts as that one, so that no two groups claim a row
-    if (w == 0) {
-      int top = 0;
-      for (int base = 0; base <= args.G; base += 32) {
-        const int i = base + lane;
-        int v = i <= args.G ? max(table_off[i], top) : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int below = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v = max(v, below);
-        }
-        if (i <= args.G) table_off[i] = v;
-        top = __shfl_sync(0xffffffffu, v, 31);
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      if (pass == 1) {
+        if (!args.late_wait) pdl_wait();
+        pdl_trigger();
       }
-    }
-    sync();
-    int cap = args.bn_cap;
-    if (!BACKWARD && args.choose != 0) {
-      // Where the widest units make few rounds: the width whose units take the least time, their
-      // rounds by a stage's cycles, 117 + 1.55 bn and 288 at least (see linear.cu); one width per
-      // warp.  (Not for more: narrower units keep less in flight.)
-      const int parts = (args.bn_cap >> 5) - w;
-      int n = 0;
-      for (int i = lane; i < args.G && parts > 0; i += 32) n += (((group_rows(table_off, i) + 31) >> 5) + parts - 1) / parts;
-      n = int(__reduce_add_sync(0xffffffffu, unsigned(n)));
-      const int64_t rounds = (int64_t(n) * args.tiles_n + num_pairs - 1) / num_pairs;
-      const int64_t cost = rounds * max(288, 117 + 31 * (32 * parts) / 20);
-      if (lane == 0) found[w] = parts > 0 && (w > 0 || rounds <= 3) ? int(min(cost, int64_t(0x7FFFFFFE))) : w > 0 ? 0x7FFFFFFF : -1;
+      for (int i = t; i <= args.G; i += THREADS) {
+        int v = i == 0 ? 0 : args.M;
+        if (pass == 1) v = min(max(args.offsets[i], 0), args.M);
+        table_off[i] = v;
+      }
       sync();
-      int best = 0;
-      for (int i = 1; i < EPI_WARPS; ++i)
-        if (found[i] < found[best]) best = i;
-      cap -= 32 * best;
-    }
-    if (w == 0) {
-      int total = 0;
-      for (int base = 0; base < args.G; base += 32) {
-        const int i = base + lane;
-        int n = i < args.G ? (group_rows(table_off, i) + cap - 1) / cap * args.tiles_n : 0;
+      // an offset below one before it counts as that one, so that no two groups claim a row
+      if (w == 0) {
+        int top = 0;
+        for (int base = 0; base <= args.G; base += 32) {
+          const int i = base + lane;
+          int v = i <= args.G ? max(table_off[i], top) : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int below = __shfl_up_sync(0xffffffffu, n, o);
-          if (lane >= o) n += below;
-        }
-        if (i < args.G) table_first[i + 1] = total + n;
-        total += __shfl_sync(0xffffffffu, n, 31);
-      }
-      if (lane == 0) {
-        table_first[0] = 0;
-        chosen[0] = cap;
-      }
-    }
-    if (BACKWARD) {
-      // the groups in the order of their weight gradients: the longest first, up to 256 of them
-      // (each counts those before it); more as they come, those without rows last
-      if (args.G <= THREADS) {
-        const int n = t < args.G ? group_rows(table_off, t) : 0;
-        if (t < args.G) {
-          int at = 0;
-#pragma unroll 4
-          for (int j = 0; j < args.G; ++j) {
-            const int m = group_rows(table_off, j);
-            at += m > n || (m == n && j < t) ? 1 : 0;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int below = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v = max(v, below);
           }
-          table_order[at] = t;
+          if (i <= args.G) table_off[i] = v;
+          top = __shfl_sync(0xffffffffu, v, 31);
         }
-        const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
-        if (lane == 0) found[w] = __popc(some);
-      } else if (w == 1) {
-        int before_all = 0;
+      }
+      sync();
+      int cap = args.bn_cap;
+      if (!BACKWARD && args.choose != 0) {
+        // Where the widest units make few rounds: the width whose units take the least time, their
+        // rounds by a stage's cycles, 117 + 1.55 bn and 288 at least (see linear.cu); one width per
+        // warp.  (Not for more: narrower units keep less in flight.)
+        const int parts = (args.bn_cap >> 5) - w;
+        int n = 0;
+        for (int i = lane; i < args.G && parts > 0; i += 32) n += quick_div(((group_rows(table_off, i) + 31) >> 5) + parts - 1, parts);
+        n = int(__reduce_add_sync(0xffffffffu, unsigned(n)));
+        // (a narrower width has eight times the rounds at most)
+        const int rounds = min(quick_div(n * args.tiles_n + num_pairs - 1, num_pairs), 1000);
+        const int cost = rounds * max(288, 117 + 31 * (32 * parts) / 20);
+        if (lane == 0) found[w] = parts > 0 && (w > 0 || rounds <= 3) ? cost : w > 0 ? 0x7FFFFFFF : -1;
+        sync();
+        int best = 0;
+        for (int i = 1; i < EPI_WARPS; ++i)
+          if (found[i] < found[best]) best = i;
+        cap -= 32 * best;
+      }
+      if (w == 0) {
+        int total = 0;
         for (int base = 0; base < args.G; base += 32) {
           const int i = base + lane;
-          const bool rows = i < args.G && group_rows(table_off, i) > 0;
-          const uint32_t some = __ballot_sync(0xffffffffu, rows);
-          const int before = before_all + __popc(some & ((1u << lane) - 1u));
-          if (i < args.G) table_order[rows ? before : args.G - 1 - (i - before)] = i;
-          before_all += __popc(some);
+          int n = i < args.G ? quick_div(group_rows(table_off, i) + cap - 1, cap) * args.tiles_n : 0;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int below = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += below;
+          }
+          if (i < args.G) table_first[i + 1] = total + n;
+          total += __shfl_sync(0xffffffffu, n, 31);
         }
-        if (lane < EPI_WARPS) found[lane] = lane == 0 ? before_all : 0;
+        if (lane == 0) {
+          table_first[0] = 0;
+          chosen[0] = cap;
+        }
+      }
+      if (BACKWARD) {
+        // the groups in the order of their weight gradients: the longest first, up to 256 of them
+        // (each counts those before it); more as they come, those without rows last
+        if (args.G <= THREADS) {
+          const int n = t < args.G ? group_rows(table_off, t) : 0;
+          if (t < args.G) {
+            int at = 0;
+#pragma unroll 4
+            for (int j = 0; j < args.G; ++j) {
+              const int m = group_rows(table_off, j);
+              at += m > n || (m == n && j < t) ? 1 : 0;
+            }
+            table_order[at] = t;
+          }
+          const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+          if (lane == 0) found[w] = __popc(some);
+        } else if (w == 1) {
+          int before_all = 0;
+          for (int base = 0; base < args.G; base += 32) {
+            const int i = base + lane;
+            const bool rows = i < args.G && group_rows(table_off, i) > 0;
+            const uint32_t some = __ballot_sync(0xffffffffu, rows);
+            const int before = before_all + __popc(some & ((1u << lane) - 1u));
+            if (i < args.G) table_order[rows ? before : args.G - 1 - (i - before)] = i;
+            before_all += __popc(some);
+          }
+          if (lane < EPI_WARPS) found[lane] = lane == 0 ? before_all : 0;
+        }
+        sync();
+        if (t == 0) {
+          int n = 0;
+          for (int i = 0; i < EPI_WARPS; ++i) n += found[i];
+          chosen[1] = n;
+          // a stage of out takes 500 cycles, one of dw 514, and its stores 4000, added to dw twice that
+          const int units = args.out == nullptr ? 0 : table_first[args.G];
+          const int rounds = quick_div(units, num_pairs), over = units - rounds * num_pairs;
+          const int stages = n > 0 ? (group_rows(table_off, table_order[0]) + 63) / 64 : 0;
+          chosen[2] = rounds;
+          chosen[3] = num_pairs - over;
+          chosen[4] = over > 0 ? quick_div(args.num_kb * 500, max(args.in != nullptr ? 8000 : 4000, stages * 514 + 2300)) : 0;
+        }
       }
       sync();
-      if (t == 0) {
-        int n = 0;
-        for (int i = 0; i < EPI_WARPS; ++i) n += found[i];
-        chosen[1] = n;
-        // a stage of out takes 500 cycles, one of dw 514, and its stores 4000, added to dw twice that
-        const int units = args.out == nullptr ? 0 : table_first[args.G];
-        const int rounds = quick_div(units, num_pairs), over = units - rounds * num_pairs;
-        const int stages = n > 0 ? (group_rows(table_off, table_order[0]) + 63) / 64 : 0;
-        chosen[2] = rounds;
-        chosen[3] = num_pairs - over;
-        chosen[4] = over > 0 ? quick_div(args.num_kb * 500, max(args.in != nullptr ? 8000 : 4000, stages * 514 + 2300)) : 0;
-      }
     }
-    sync();
     if (t == 0) mbar_arrive(table_bar);
   }
-  // Behind the preceding kernel, with the table (false: the wait for it ran out).
-  auto start = [&]() -> bool {
-    if (!args.late_wait) pdl_wait();
-    pdl_trigger();
+  // Takes the table, in pass 0 that of one group (false: the wait for it ran out).
+  auto start = [&](int pass) -> bool {
     if (!grouped) return true;
-    if (!mbar_wait(table_bar, 0, abort_flag)) {
+    // (the parity of the phase before the first has passed)
+    if (!mbar_wait(table_bar, uint32_t(pass ^ 1), abort_flag)) {
       num_units = 0;
       return false;
     }
-    table = Table{table_off, table_first, table_order, args.G, chosen[0]};
+    const bool real = pass == 1;
+    table = Table{real ? table_off : one, real ? table_first : one + 2, real ? table_order : one + 4, real ? args.G : 1,
+                  real ? chosen[0] : args.bn_cap};
     cursor = Cursor{};
-    rows_units = BACKWARD && args.out == nullptr ? 0 : table_first[args.G];
+    rows_units = BACKWARD && args.out == nullptr ? 0 : table.first[table.G];
     num_units = rows_units;
-    if (BACKWARD) {
+    if (BACKWARD && real) {
       busy = chosen[1];
       num_units += busy * args.tiles_r * args.tiles_n;
       spare = chosen[3];
@@ -533,6 +546,14 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       early_all = chosen[4] * spare;
     }
     return true;
+  };
+  // Ends pass 0, behind which global memory may be read, and gives the next (2: under way).
+  auto next_pass = [&](int pass) {
+    if (pass == 0) {
+      if (!args.late_wait) pdl_wait();
+      pdl_trigger();
+    }
+    return grouped && pass == 0 ? 1 : 2;
   };
   // This pair's unit in round r.
   auto number = [&](int r) {
@@ -556,18 +577,15 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       uint32_t tails = 0, tail_parity = 0;   // stages whose tail barrier was armed, and its phase now
       int s = 0;
       bool ok = true;
-      bool begun = false;
-      for (int r = 0, un = number(0); ok; un = number(++r)) {
-        if (begun && un >= num_units) break;
-        const Unit u = unit_at(begun || !grouped ? un : 0);
-        if (!begun) {
-          ok = start();
-          begun = true;
-          if (grouped) {
-            --r;
-            continue;
-          }
-          if (un >= num_units) break;
+      int pass = 0;
+      for (int r = 0; ok; ++r) {
+        if (pass < 2 && !start(pass)) break;
+        const int un = number(r);
+        if ((pass > 0 || !grouped) && un >= num_units) break;
+        const Unit u = unit_at(pass > 0 || !grouped ? un : 0);
+        if (pass < 2 && (pass = next_pass(pass)) == 1) {
+          --r;
+          continue;
         }
         const bool weight = BACKWARD && un >= rows_units;
         if (rank == 0) {                     // for the issuer (published by the arrival on the first stage's barrier)
@@ -644,7 +662,9 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       // ------------------------------------------------------------ MMA issuer (leader)
       int s = 0, local = 0, chunk = 0;
       uint32_t ph = 0, cleared_parity = 0;
-      bool ok = start();
+      start(0);
+      next_pass(0);                        // (a bounded wait begins behind the preceding kernel)
+      bool ok = start(1);
       const bool shared = sharing();
       const int acc_cols = acc_columns();
       for (int un = number(0); ok && un < num_units; un = number(++local)) {
@@ -738,16 +758,22 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     const uint32_t dst = smem_u32(sScales) + uint32_t(mine * SF_BYTES + lane * 16);
     int r = 0, c = mine;
     uint32_t fills = 0;
-    bool ok = true, begun = false, fresh = true;
+    bool ok = true, fresh = true;
+    int pass = 0;
     Unit u{};
     while (ok) {
       for (; c >= chunks; c -= chunks) {
         ++r;
         fresh = true;
       }
+      if (pass < 2) {
+        ok = __all_sync(0xffffffffu, start(pass));
+        if (!ok) break;
+        fresh = true;
+      }
       const int un = number(r);
-      if ((begun || !grouped) && un >= num_units) break;
-      if (fresh) u = unit_at(begun || !grouped ? un : 0);
+      if ((pass > 0 || !grouped) && un >= num_units) break;
+      if (fresh) u = unit_at(pass > 0 || !grouped ? un : 0);
       fresh = false;
       const int left = args.blocks - 4 * c;
       const int block_w = min(u.nb * 2 + int(rank), args.n_blocks - 1);
@@ -760,13 +786,9 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         xp[i] = args.x_scale + size_t(min(u.row0 + 32 * i + lane, args.M - 1)) * size_t(args.blocks) + size_t(4 * c);
         within = within && (32 * i >= u.bn || scales_within(xp[i], args.x_scale, xs_end));
       }
-      if (!begun) {                          // (the addresses ahead of the wait for the preceding kernel)
-        ok = __all_sync(0xffffffffu, start());
-        begun = true;
-        if (grouped) {
-          fresh = true;
-          continue;
-        }
+      if (pass < 2) {                        // (the addresses ahead of the wait for the preceding kernel)
+        pass = next_pass(pass);
+        if (pass == 1) continue;
       }
       uint32_t w, x[8];
       if (whole) {
@@ -803,7 +825,8 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     // is its bytes 128 r ..).
     uint32_t parity = 0;
     int s = 0;
-    __all_sync(0xffffffffu, start());
+    next_pass(0);
+    __all_sync(0xffffffffu, start(1));
     for (int r = 0, un = number(0); un < num_units; un = number(++r)) {
       const bool weight = un >= rows_units;
       const Unit u = weight ? unit_at(un) : Unit{};
@@ -832,7 +855,8 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     constexpr int WG = EPI_WARPS / 4;
     const int q = warp & 3, wg = (warp - 2) >> 2;
     const uint32_t box = smem_u32(sStaging + (q * WG + wg) * staging_box(KIND));
-    start();
+    start(1);
+    if (!grouped) pdl_wait();
     const uint16_t* const bias_row = behind_wait(args.bias);
     const bool shared = sharing();
     const int acc_cols = acc_columns();
