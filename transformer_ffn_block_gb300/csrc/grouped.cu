@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   // that wait.  The first instructions of a kernel come from L2 (a first lookup takes 2000
   // cycles, the next 350), so those warps go through the same code once before, for one group,
   // and the other roles look one of its units up: pass 0.  (4531 x 2048 x 1536 without offsets
-  // 17.2 us, so 15.6; 10200 rows in 14 groups of 1176 x 1664, E4M3, WARMA.)  Nothing in
+  // 17.2 us, so 15.6; 10200 rows in 14 groups of 1176 x 1664, E4M3, 26.1 us, so 25.7.)  Nothing in
   // global memory is touched before the preceding kernel is done.
   const bool grouped = args.offsets != nullptr;
   Table table{one, one + 2, one + 4, 1, args.bn_cap};
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       sts16(dst + 1024, make_uint4(x[4], x[5], x[6], x[7]));
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(map_to_rank(sfull_bar(mine), 0));
+      if (lane == 0) mbar_arrive_remote_cta(map_to_rank(sfull_bar(mine), 0));
       ++fills;
       c += SCALE_WARPS;
     }
@@ -842,7 +842,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(map_to_rank(cleared_bar(s), 0));
+        if (lane == 0) mbar_arrive_remote_cta(map_to_rank(cleared_bar(s), 0));
       }
       s = s + 1 == args.stages ? 0 : s + 1;
     }
