@@ -117,7 +117,6 @@ struct GroupArgs {
   int tiles_n;              // units of 256 across a row of N
   int tiles_r;              // backward: units of 256 across a matrix's rows
   int bn_cap;               // most rows of a unit, a multiple of 32
-  int choose;               // a narrower cap may be chosen from the groups' sizes
   int late_wait;            // does not read the preceding kernel's results (see launch.h)
   int band_n;               // units across N that are swept together
   int num_kb;               // stages of K of out
@@ -194,11 +193,13 @@ QFFN_DEVI uint32_t pack2(uint64_t v) {
 QFFN_DEVI uint4 pack8(const uint64_t (&v)[4]) { return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3])); }
 
 // The table of units in shared memory: off[0 .. G] the offsets (within 0 .. M, none below
-// the one before it), first[0 .. G] the number of the first unit of out of each group; backward:
-// order[0 .. G - 1] the groups, those with rows first.
+// the one before it), first[0 .. G] the number of the first unit of out of each group,
+// shape[0 .. G - 1] how its rows are cut; backward: order[0 .. G - 1] the groups, those with
+// rows first.
 struct Table {
   const int* off;
   const int* first;
+  const int* shape;
   const int* order;
   int G;
   int cap;            // most rows of a unit
@@ -222,6 +223,13 @@ QFFN_DEVI int quick_div(int n, int d) {
   return q;
 }
 
+// A group's rows in 32s, spread evenly over tiles of `cap` 32s at most: the tiles (4 bits up)
+// and the 32s of the narrowest.
+QFFN_DEVI int shape_of(int rows, int cap) {
+  const int parts = (rows + 31) >> 5, tiles = quick_div(parts + cap - 1, cap);
+  return tiles << 4 | (tiles > 0 ? quick_div(parts, tiles) : 0);
+}
+
 // The group of the last unit that a thread looked up: its first unit and the next group's, its
 // rows in 32s spread over tm tiles, `wider` of `least` + 1 and the others of `least`.
 struct Cursor {
@@ -242,10 +250,10 @@ QFFN_DEVI Unit rows_unit(int u, Cursor& c, const Table& t, const GroupArgs& a) {
     c.next = t.first[lo + 1];
     c.begin = t.off[lo];
     c.rows = group_rows(t.off, lo);
-    const int parts = (c.rows + 31) >> 5, cap = t.cap >> 5;
-    c.tm = parts <= cap ? 1 : quick_div(parts + cap - 1, cap);
-    c.least = c.tm == 1 ? parts : quick_div(parts, c.tm);
-    c.wider = parts - c.least * c.tm;
+    const int shape = t.shape[lo];
+    c.tm = shape >> 4;
+    c.least = shape & 15;
+    c.wider = ((c.rows + 31) >> 5) - c.least * c.tm;
   }
   Unit r;
   r.group = c.group;
@@ -323,11 +331,12 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* units_bn = reinterpret_cast<int*>(tmem_slot + 4);   // of the units in flight: width (of dw: negative), rows
   int* units_rows = units_bn + UNIT_SLOTS;
-  int* one = units_rows + UNIT_SLOTS;                  // the table of one group of all rows: off, first, order
-  int* chosen = one + 5;                               // the cap, groups with rows, and see `spare`
+  int* one = units_rows + UNIT_SLOTS;                  // the table of one group of all rows: off, first, order, shape
+  int* chosen = one + 6;                               // the cap, groups with rows, and see `spare`
   int* table_off = one + 12;
   int* table_first = table_off + args.G + 1;
-  int* table_order = table_first + args.G + 1;         // backward
+  int* table_shape = table_first + args.G + 1;
+  int* table_order = table_shape + args.G;             // backward
   int* found = table_order + (BACKWARD ? args.G : 0);  // a number per epilogue warp
   const uint32_t bar0 = smem_u32(bars);
   // full[s] (leader): both CTAs' loads of stage s landed; empty[s]: the MMAs
@@ -375,7 +384,8 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     *abort_flag = 0;
     one[0] = one[2] = one[4] = 0;
     one[1] = args.M;
-    one[3] = (args.M + args.bn_cap - 1) / args.bn_cap * args.tiles_n;
+    one[5] = shape_of(args.M, args.bn_cap >> 5);
+    one[3] = (one[5] >> 4) * args.tiles_n;
     mbar_init_fence();
   }
   if (warp == 0 && lane >= 8 && lane < (BACKWARD ? 16 : 13)) tma_prefetch_desc(&maps.w + (lane - 8));
@@ -391,13 +401,12 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   const uint32_t tmem_base = *tmem_slot;
   // The table.  Without offsets it is that of one group, and every role looks up its first unit
   // ahead of the wait for the preceding kernel.  With them the epilogue's warps make it behind
-  // that wait.  The first instructions of a kernel come from L2 (a first lookup takes 2000
-  // cycles, the next 350), so those warps go through the same code once before, for one group,
-  // and the other roles look one of its units up: pass 0.  (4531 x 2048 x 1536 without offsets
-  // 17.2 us, so 15.6; 10200 rows in 14 groups of 1176 x 1664, E4M3, 26.1 us, so 25.7.)  Nothing in
-  // global memory is touched before the preceding kernel is done.
+  // that wait; the other roles have meanwhile looked up a unit of one group (pass 0): the first
+  // instructions of a kernel come from L2, and a first lookup takes 2000 cycles where the next
+  // takes 350 (4531 x 2048 x 1536 without offsets 17.2 us, so 15.6).  Nothing in global memory
+  // is touched before the preceding kernel is done.
   const bool grouped = args.offsets != nullptr;
-  Table table{one, one + 2, one + 4, 1, args.bn_cap};
+  Table table{one, one + 2, one + 5, one + 4, 1, args.bn_cap};
   int rows_units = BACKWARD && args.out == nullptr ? 0 : one[3];   // units of out, then those of dw
   int num_units = rows_units;
   // backward: groups with rows; this pair's units of out; the `spare` pairs behind the last unit of
@@ -410,115 +419,119 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
     constexpr int THREADS = 32 * EPI_WARPS;
     const int t = int(threadIdx.x) - 64, w = warp - 2;
     auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); };
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-      if (pass == 1) {
-        if (!args.late_wait) pdl_wait();
-        pdl_trigger();
-      }
-      for (int i = t; i <= args.G; i += THREADS) {
-        int v = i == 0 ? 0 : args.M;
-        if (pass == 1) v = min(max(args.offsets[i], 0), args.M);
-        table_off[i] = v;
-      }
-      sync();
-      // an offset below one before it counts as that one, so that no two groups claim a row
-      if (w == 0) {
-        int top = 0;
-        for (int base = 0; base <= args.G; base += 32) {
-          const int i = base + lane;
-          int v = i <= args.G ? max(table_off[i], top) : 0;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int below = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v = max(v, below);
-          }
-          if (i <= args.G) table_off[i] = v;
-          top = __shfl_sync(0xffffffffu, v, 31);
+    if (!args.late_wait) pdl_wait();
+    pdl_trigger();
+    for (int i = t; i <= args.G; i += THREADS)
+      table_first[i] = min(max(args.offsets[i], 0), args.M);   // (as they are)
+    sync();
+    // An offset below one before it counts as that one, so that no two groups claim a row.
+    // Where the widest units make few rounds, the width whose units take the least time is
+    // chosen, their rounds by a stage's cycles, 117 + 1.55 bn and 288 at least (see linear.cu);
+    // one width per warp.  (Not for more: narrower units keep less in flight.)
+    const int parts = (args.bn_cap >> 5) - w;
+    if (w == 0 || (!BACKWARD && parts > 0)) {
+      int top = 0, n = 0;
+      for (int base = 0; base < args.G; base += 32) {
+        const int i = base + lane;
+        int lo = 0, hi = 0;
+        if (i < args.G) {
+          lo = max(table_first[i], top);
+          hi = max(table_first[i + 1], top);
         }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int below = __shfl_up_sync(0xffffffffu, lo, o);
+          if (lane >= o) lo = max(lo, below);
+        }
+        hi = max(hi, lo);
+        if (w == 0 && i < args.G) {
+          table_off[i] = lo;
+          if (i == args.G - 1) table_off[args.G] = hi;
+        }
+        if (!BACKWARD && i < args.G) n += quick_div(((hi - lo + 31) >> 5) + parts - 1, parts);
+        top = __shfl_sync(0xffffffffu, hi, 31);
       }
-      sync();
-      int cap = args.bn_cap;
-      if (!BACKWARD && args.choose != 0) {
-        // Where the widest units make few rounds: the width whose units take the least time, their
-        // rounds by a stage's cycles, 117 + 1.55 bn and 288 at least (see linear.cu); one width per
-        // warp.  (Not for more: narrower units keep less in flight.)
-        const int parts = (args.bn_cap >> 5) - w;
-        int n = 0;
-        for (int i = lane; i < args.G && parts > 0; i += 32) n += quick_div(((group_rows(table_off, i) + 31) >> 5) + parts - 1, parts);
+      if (!BACKWARD) {
         n = int(__reduce_add_sync(0xffffffffu, unsigned(n)));
         // (a narrower width has eight times the rounds at most)
         const int rounds = min(quick_div(n * args.tiles_n + num_pairs - 1, num_pairs), 1000);
         const int cost = rounds * max(288, 117 + 31 * (32 * parts) / 20);
-        if (lane == 0) found[w] = parts > 0 && (w > 0 || rounds <= 3) ? cost : w > 0 ? 0x7FFFFFFF : -1;
-        sync();
-        int best = 0;
-        for (int i = 1; i < EPI_WARPS; ++i)
-          if (found[i] < found[best]) best = i;
-        cap -= 32 * best;
+        if (lane == 0) found[w] = w > 0 || rounds <= 3 ? cost : -1;
       }
-      if (w == 0) {
-        int total = 0;
+    } else if (!BACKWARD && lane == 0) {
+      found[w] = 0x7FFFFFFF;
+    }
+    sync();
+    int best = 0;
+    if (!BACKWARD)
+      for (int i = 1; i < EPI_WARPS; ++i)
+        if (found[i] < found[best]) best = i;
+    if (w == best) {
+      const int cap = (args.bn_cap >> 5) - best;
+      int total = 0;
+      for (int base = 0; base < args.G; base += 32) {
+        const int i = base + lane;
+        const int shape = i < args.G ? shape_of(group_rows(table_off, i), cap) : 0;
+        int n = (shape >> 4) * args.tiles_n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int below = __shfl_up_sync(0xffffffffu, n, o);
+          if (lane >= o) n += below;
+        }
+        if (i < args.G) {
+          table_shape[i] = shape;
+          table_first[i + 1] = total + n;
+        }
+        total += __shfl_sync(0xffffffffu, n, 31);
+      }
+      if (lane == 0) {
+        table_first[0] = 0;
+        chosen[0] = 32 * cap;
+      }
+    }
+    if (BACKWARD) {
+      // the groups in the order of their weight gradients: the longest first, up to 256 of them
+      // (each counts those before it); more as they come, those without rows last
+      if (args.G <= THREADS) {
+        const int n = t < args.G ? group_rows(table_off, t) : 0;
+        if (t < args.G) {
+          int at = 0;
+#pragma unroll 4
+          for (int j = 0; j < args.G; ++j) {
+            const int m = group_rows(table_off, j);
+            at += m > n || (m == n && j < t) ? 1 : 0;
+          }
+          table_order[at] = t;
+        }
+        const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+        if (lane == 0) found[w] = __popc(some);
+      } else if (w == 1) {
+        int before_all = 0;
         for (int base = 0; base < args.G; base += 32) {
           const int i = base + lane;
-          int n = i < args.G ? quick_div(group_rows(table_off, i) + cap - 1, cap) * args.tiles_n : 0;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int below = __shfl_up_sync(0xffffffffu, n, o);
-            if (lane >= o) n += below;
-          }
-          if (i < args.G) table_first[i + 1] = total + n;
-          total += __shfl_sync(0xffffffffu, n, 31);
+          const bool rows = i < args.G && group_rows(table_off, i) > 0;
+          const uint32_t some = __ballot_sync(0xffffffffu, rows);
+          const int before = before_all + __popc(some & ((1u << lane) - 1u));
+          if (i < args.G) table_order[rows ? before : args.G - 1 - (i - before)] = i;
+          before_all += __popc(some);
         }
-        if (lane == 0) {
-          table_first[0] = 0;
-          chosen[0] = cap;
-        }
-      }
-      if (BACKWARD) {
-        // the groups in the order of their weight gradients: the longest first, up to 256 of them
-        // (each counts those before it); more as they come, those without rows last
-        if (args.G <= THREADS) {
-          const int n = t < args.G ? group_rows(table_off, t) : 0;
-          if (t < args.G) {
-            int at = 0;
-#pragma unroll 4
-            for (int j = 0; j < args.G; ++j) {
-              const int m = group_rows(table_off, j);
-              at += m > n || (m == n && j < t) ? 1 : 0;
-            }
-            table_order[at] = t;
-          }
-          const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
-          if (lane == 0) found[w] = __popc(some);
-        } else if (w == 1) {
-          int before_all = 0;
-          for (int base = 0; base < args.G; base += 32) {
-            const int i = base + lane;
-            const bool rows = i < args.G && group_rows(table_off, i) > 0;
-            const uint32_t some = __ballot_sync(0xffffffffu, rows);
-            const int before = before_all + __popc(some & ((1u << lane) - 1u));
-            if (i < args.G) table_order[rows ? before : args.G - 1 - (i - before)] = i;
-            before_all += __popc(some);
-          }
-          if (lane < EPI_WARPS) found[lane] = lane == 0 ? before_all : 0;
-        }
-        sync();
-        if (t == 0) {
-          int n = 0;
-          for (int i = 0; i < EPI_WARPS; ++i) n += found[i];
-          chosen[1] = n;
-          // a stage of out takes 500 cycles, one of dw 514, and its stores 4000, added to dw twice that
-          const int units = args.out == nullptr ? 0 : table_first[args.G];
-          const int rounds = quick_div(units, num_pairs), over = units - rounds * num_pairs;
-          const int stages = n > 0 ? (group_rows(table_off, table_order[0]) + 63) / 64 : 0;
-          chosen[2] = rounds;
-          chosen[3] = num_pairs - over;
-          chosen[4] = over > 0 ? quick_div(args.num_kb * 500, max(args.in != nullptr ? 8000 : 4000, stages * 514 + 2300)) : 0;
-        }
+        if (lane < EPI_WARPS) found[lane] = lane == 0 ? before_all : 0;
       }
       sync();
+      if (t == 0) {
+        int n = 0;
+        for (int i = 0; i < EPI_WARPS; ++i) n += found[i];
+        chosen[1] = n;
+        // a stage of out takes 500 cycles, one of dw 514, and its stores 4000, added to dw twice that
+        const int units = args.out == nullptr ? 0 : table_first[args.G];
+        const int rounds = quick_div(units, num_pairs), over = units - rounds * num_pairs;
+        const int stages = n > 0 ? (group_rows(table_off, table_order[0]) + 63) / 64 : 0;
+        chosen[2] = rounds;
+        chosen[3] = num_pairs - over;
+        chosen[4] = over > 0 ? quick_div(args.num_kb * 500, max(args.in != nullptr ? 8000 : 4000, stages * 514 + 2300)) : 0;
+      }
     }
+    sync();
     if (t == 0) mbar_arrive(table_bar);
   }
   // Takes the table, in pass 0 that of one group (false: the wait for it ran out).
@@ -530,8 +543,8 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       return false;
     }
     const bool real = pass == 1;
-    table = Table{real ? table_off : one, real ? table_first : one + 2, real ? table_order : one + 4, real ? args.G : 1,
-                  real ? chosen[0] : args.bn_cap};
+    table = Table{real ? table_off : one,       real ? table_first : one + 2, real ? table_shape : one + 5,
+                  real ? table_order : one + 4, real ? args.G : 1,            real ? chosen[0] : args.bn_cap};
     cursor = Cursor{};
     rows_units = BACKWARD && args.out == nullptr ? 0 : table.first[table.G];
     num_units = rows_units;
@@ -779,13 +792,17 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       const int block_w = min(u.nb * 2 + int(rank), args.n_blocks - 1);
       const uint8_t* const wp =
           args.w_scale + (size_t(u.group) * size_t(args.n_blocks) + size_t(block_w)) * size_t(args.blocks) + size_t(4 * c);
+      // (rows behind the last count as that one; the addresses do not descend)
+      const uint8_t* const last = args.x_scale + size_t(args.M - 1) * size_t(args.blocks) + size_t(4 * c);
       const uint8_t* xp[8];
-      bool within = scales_within(wp, args.w_scale, ws_end);
+      xp[0] = args.x_scale + size_t(min(u.row0 + lane, args.M - 1)) * size_t(args.blocks) + size_t(4 * c);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        xp[i] = args.x_scale + size_t(min(u.row0 + 32 * i + lane, args.M - 1)) * size_t(args.blocks) + size_t(4 * c);
-        within = within && (32 * i >= u.bn || scales_within(xp[i], args.x_scale, xs_end));
+      for (int i = 1; i < 8; ++i) {
+        const uint8_t* const p = xp[i - 1] + 32 * args.blocks;
+        xp[i] = 32 * i >= u.bn ? xp[i - 1] : p < last ? p : last;
       }
+      const bool within = scales_within(wp, args.w_scale, ws_end) && scales_within(xp[0], args.x_scale, xs_end) &&
+                          scales_within(xp[7], args.x_scale, xs_end);
       if (pass < 2) {                        // (the addresses ahead of the wait for the preceding kernel)
         pass = next_pass(pass);
         if (pass == 1) continue;
@@ -1155,7 +1172,7 @@ cudaError_t max_pairs(int* pairs) {
 // `units`: no fewer than the kernel will find
 template <int OP, int KIND>
 cudaError_t launch(const Maps& m, GroupArgs a, int64_t units, int pairs, cudaStream_t s) {
-  const int table = (KIND == KIND_BACKWARD ? 12 : 8) * (a.G + 1) + 4 * EPI_WARPS;
+  const int table = (KIND == KIND_BACKWARD ? 16 : 12) * (a.G + 1) + 4 * EPI_WARPS;
   // (narrow units: more stages, whose loads' latency is what bounds them; 512 x 4096 x 2048
   // with six stages 11.3 us, with eight 10.7)
   a.stage_bytes = OP_BYTES + a.bn_cap / 2 * ROW_BYTES;
@@ -1234,12 +1251,11 @@ cudaError_t forward(uint16_t* out, const void* x, const uint8_t* x_scale, const 
   if (e != cudaSuccess) return e;
   a.num_kb = ceil_div(K, stage_k(OP));
   a.bn_cap = choose_cap(G, M, a.tiles_n, a.num_kb, pairs);
-  a.choose = G > 1;
   // bands of about 32 MB of weights where they are the larger operand (see linear.cu)
   const int64_t band = (int64_t(32) << 20) / (2 * BM * K * bytes);
   a.band_n = N <= M / G || band >= a.tiles_n ? a.tiles_n : band < 1 ? 1 : int(band);
   // (a cap chosen on the device is 32 at least)
-  const int64_t units = (M / (a.choose ? 32 : a.bn_cap) + (G < M ? G : M)) * a.tiles_n;
+  const int64_t units = (M / (offsets != nullptr ? 32 : a.bn_cap) + (G < M ? G : M)) * a.tiles_n;
   return launch<OP, KIND_FORWARD>(m, a, units, pairs, s);
 }
 
