@@ -763,6 +763,21 @@ int grouped_bn(int64_t G, int64_t M) {
 int64_t grouped_clusters(int64_t G, int64_t M, int64_t N) {
   return (N + 127) / 128 * (M / grouped_bn(G, M) + (G < M ? G : M));
 }
+// Those that have rows where the groups are of average size.
+int64_t expected_clusters(int64_t G, int64_t M, int64_t N) {
+  const int64_t groups = G < M ? G : M, bn = grouped_bn(G, M);
+  return (N + 127) / 128 * groups * ((M / groups + bn - 1) / bn);
+}
+// K is split for all of them, or for the expected ones where each part has 20 stages: the
+// others take their turns too, some 2 us (184 rows in 15 groups of 152 x 11648 in parts of two 15.2
+// us, of four 10.4; 400 in eight of 512 x 2048 7.2 and 10.0).
+cudaError_t grouped_split(int64_t G, int64_t M, int64_t N, int num_kb, int* splits) {
+  int all = 1;
+  cudaError_t e = split_k(int(grouped_clusters(G, M, N)), num_kb, &all);
+  if (e == cudaSuccess) e = split_k(int(expected_clusters(G, M, N)), num_kb, splits);
+  if (*splits > all && num_kb < 20 * *splits) *splits = all;
+  return e;
+}
 // out [M, N] from x [M, K] and w [G, N, K] or, W_MN, [G, K, N].
 template <int OP, bool W_MN = false>
 cudaError_t grouped_product(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w, const uint8_t* w_scale,
@@ -781,9 +796,9 @@ cudaError_t grouped_product(uint16_t* out, const void* x, const uint8_t* x_scale
   a.tiles_m = int(M / a.bn + (G < M ? G : M));
   a.num_kb = int((K + stage_k(OP) - 1) / stage_k(OP));
   const int clusters = int(grouped_clusters(G, M, N));
-  const cudaError_t e = split_k(clusters, a.num_kb, &a.splits);
+  const cudaError_t e = grouped_split(G, M, N, a.num_kb, &a.splits);
   if (e != cudaSuccess) return e;
-  size_cta(a, clusters, OP);
+  size_cta(a, int(expected_clusters(G, M, N)), OP);
   CUtensorMap mw, mx;
   const bool bf16 = OP == OP_BF16;
   const int64_t pitch = K * (bf16 ? 2 : 1);
@@ -795,15 +810,17 @@ cudaError_t grouped_product(uint16_t* out, const void* x, const uint8_t* x_scale
 }
 }  // namespace
 
-// The estimate of few_rows_cycles for groups of rows; 1500 cycles more for the search.
+// An estimate as few_rows_cycles for groups of rows of average size, fitted to 60 of 2 to 3000
+// rows in 1 to 64 groups, in E4M3 and bf16: 7800 for the call, per round of clusters 500 for
+// each stage and 34 for each row of a tile, 1500 for an exchange.
 int64_t few_rows_grouped_cycles(int64_t G, int64_t M, int64_t N, int64_t K, bool fp8) {
-  const int64_t clusters = grouped_clusters(G, M, N);
-  if (clusters > 4 * kNumSMsHint) return -1;
+  if (grouped_clusters(G, M, N) > 4 * kNumSMsHint) return -1;
+  const int64_t clusters = expected_clusters(G, M, N);
   const int num_kb = int((K + stage_k(fp8 ? OP_E4M3 : OP_BF16) - 1) / stage_k(fp8 ? OP_E4M3 : OP_BF16));
   int splits = 1;
-  if (split_k(int(clusters), num_kb, &splits) != cudaSuccess) return -1;
+  if (grouped_split(G, M, N, num_kb, &splits) != cudaSuccess) return -1;
   const int64_t rounds = (clusters * splits + kNumSMsHint - 1) / kNumSMsHint;
-  return 7200 + rounds * (((num_kb + splits - 1) / splits) * 500 + 39 * grouped_bn(G, M)) + (splits > 1 ? 3900 : 0);
+  return 7800 + rounds * (((num_kb + splits - 1) / splits) * 500 + 34 * grouped_bn(G, M)) + (splits > 1 ? 1500 : 0);
 }
 
 cudaError_t launch_few_rows_grouped(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w,

@@ -1199,27 +1199,26 @@ int ceil_div(int64_t a, int64_t b) { return int((a + b - 1) / b); }
 
 // One group's rows are cut so that its units fill the SM pairs in the fewest and
 // narrowest rounds, a stage taking 117 + 1.55 bn cycles and 288 at least (see linear.cu).
-// `cycles`: of all rounds.
-struct Cut {
-  int bn;
-  int64_t cycles;
-};
-Cut cut_rows(int64_t M, int tiles_n, int num_kb, int pairs) {
+int cut_rows(int64_t M, int tiles_n, int pairs) {
   const int64_t parts = (M + 31) / 32;
-  Cut best{MAX_BN, -1};
+  int best = MAX_BN;
+  int64_t least = -1;
   for (int64_t tm = (parts + 7) / 8; tm < (parts + 7) / 8 + 8 && tm <= parts; ++tm) {
     const int bn = 32 * int((parts + tm - 1) / tm);
     const int64_t rounds = (tm * tiles_n + pairs - 1) / pairs;
     const int64_t stage = 117 + 31 * bn / 20;
-    const int64_t cost = rounds * (stage > 288 ? stage : 288) * num_kb;
-    if (best.cycles < 0 || cost < best.cycles) best = Cut{bn, cost};
+    const int64_t cost = rounds * (stage > 288 ? stage : 288);
+    if (least < 0 || cost < least) {
+      best = bn;
+      least = cost;
+    }
   }
   return best;
 }
 // Most rows of a unit.  Several groups, whose sizes the host does not know: the widest, or 128
 // where they have few rows, for the sake of more stages.
-int choose_cap(int64_t G, int64_t M, int tiles_n, int num_kb, int pairs) {
-  return G == 1 ? cut_rows(M, tiles_n, num_kb, pairs).bn : M / G < 96 ? 128 : MAX_BN;
+int choose_cap(int64_t G, int64_t M, int tiles_n, int pairs) {
+  return G == 1 ? cut_rows(M, tiles_n, pairs) : M / G < 96 ? 128 : MAX_BN;
 }
 
 // out [M, N] from x [M, K] and w [G, N, K].
@@ -1250,7 +1249,7 @@ cudaError_t forward(uint16_t* out, const void* x, const uint8_t* x_scale, const 
   const cudaError_t e = max_pairs<OP, KIND_FORWARD>(&pairs);
   if (e != cudaSuccess) return e;
   a.num_kb = ceil_div(K, stage_k(OP));
-  a.bn_cap = choose_cap(G, M, a.tiles_n, a.num_kb, pairs);
+  a.bn_cap = choose_cap(G, M, a.tiles_n, pairs);
   // bands of about 32 MB of weights where they are the larger operand (see linear.cu)
   const int64_t band = (int64_t(32) << 20) / (2 * BM * K * bytes);
   a.band_n = N <= M / G || band >= a.tiles_n ? a.tiles_n : band < 1 ? 1 : int(band);
@@ -1294,38 +1293,43 @@ cudaError_t backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uin
 
 }  // namespace
 
+// An estimate of a call's SM cycles behind its start and end, beside those of few_rows.cu: 9 for
+// each row of a unit, and the stages at 117 + 1.55 bn and 440 at least.
+int64_t unit_cycles(int64_t units, int64_t bn, int64_t num_kb) {
+  const int64_t pairs = kNumSMsHint / 2, stage = 117 + 31 * bn / 20;
+  return 9 * bn + (units + pairs - 1) / pairs * num_kb * (stage > 440 ? stage : 440);
+}
+
 // Which form a block-scaled layer takes.  grouped_few.cu up to 8 rows, and up to 16 and 32
-// while the weights are small: us, it against few_rows.cu: 1 row of 4096 x 14336 13.0 / 13.1, 16
-// of 1024 x 1024 2.2 / 4.4, of 4096 x 4096 6.9 / 7.1, of 8192 x 2048 7.4 / 7.0, 32 of 4096 x 1024
-// 4.3 / 4.4, of 4096 x 4096 11.2 / 7.3.  few_rows.cu up to 2048 rows where its estimate is not
-// 1.15 times this file's, 8000 cycles for the call, 36 for each row of a unit and the stages
-// (its few stages of long K overlap better than both formulas say): few_rows.cu against it, 64
-// rows of 4096 x 14336 14.7 / 26, of 4096 x 4096 8.0 / 10.5, 512 of 4096 x 4096 13.4 / 12.5, of 14336 x
-// 4096 39 / 30, of 2048 x 14336 20 / 26.
+// while the weights are small: us, it against few_rows.cu and this file: 1 row of 4096 x 14336
+// 13.0 / 13.1 / 24, 9 of 3136 x 624 3.1 / 5.0 / 4.4, 15 of 632 x 2272 3.6 / 5.2 / 6.9, 16 of 4096 x
+// 4096 6.9 / 7.1 / 9.4, 10 of 1144 x 10960 8.3 / 6.9 / 20, 26 of 184 x 256 3.1 / 4.4 / 3.9, 22 of 6888
+// x 512 5.9 / 4.7 / 4.1.  few_rows.cu up to 4096 rows where nine tenths of its estimate are below
+// this file's, 5000 cycles for the call (the pair chosen on 70 sizes of 9 to 4000 rows is 0.3%
+// behind the better form on average): few_rows.cu against this, 64 rows of 4096 x 14336 14.6 / 24,
+// of 4096 x 4096 7.3 / 9.5, 256 of 4096 x 4096 10.6 / 10.5, 512 of 4096 x 4096 13.7 / 11.1, of 2048 x
+// 14336 21 / 25, 1700 of 152 x 11088 15 / 27, 2427 of 632 x 10016 25 / 21.
 cudaError_t launch_linear_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
                                  const uint8_t* w_scale, const uint16_t* bias, const uint16_t* res, int64_t M, int64_t N,
                                  int64_t K, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
-  if (M <= 8 || (M <= 16 && N * K <= (int64_t(1) << 23)) || (M <= 32 && K <= 1024 && N * K <= (int64_t(1) << 22)))
+  if (M <= 8 || (M <= 16 && N * K <= (int64_t(1) << 23)) || (M <= 32 && N * K <= (int64_t(1) << 18)))
     return launch_few_groups(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
-  const int64_t few = few_rows_cycles(M, N, K, false, true, 2048);
+  const int64_t few = few_rows_cycles(M, N, K, false, true, 4096);
   if (few >= 0) {
-    const Cut c = cut_rows(M, ceil_div(N, 2 * BM), ceil_div(K, 128), kNumSMsHint / 2);
-    const int64_t here = 8000 + 36 * c.bn + c.cycles;
-    if (20 * few < 23 * here) return launch_few_rows_blocks(out, x, x_scale, w, w_scale, bias, res, M, N, K, s);
+    const int tiles_n = ceil_div(N, 2 * BM), bn = cut_rows(M, tiles_n, kNumSMsHint / 2);
+    const int64_t here = 5000 + unit_cycles(int64_t(ceil_div(M, bn)) * tiles_n, bn, ceil_div(K, 128));
+    if (9 * few < 10 * here) return launch_few_rows_blocks(out, x, x_scale, w, w_scale, bias, res, M, N, K, s);
   }
   return forward<OP_BLOCKS>(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
 }
 
-// What forward() takes for groups of the average size, in SM cycles: 10500 for the call, 36 for
-// each row of a unit, and the stages.
+// The same for groups of the average size, with 9000 cycles for the call.
 int64_t grouped_cycles(int op, int64_t G, int64_t M, int64_t N, int64_t K) {
   const int64_t groups = G < M ? G : M, rows = (M + groups - 1) / groups;
   const int cap = (M / G < 96 ? 128 : MAX_BN) / 32;
   const int64_t parts = (rows + 31) / 32, tiles = (parts + cap - 1) / cap, bn = 32 * ((parts + tiles - 1) / tiles);
-  const int64_t units = groups * tiles * ceil_div(N, 2 * BM), pairs = kNumSMsHint / 2;
-  const int64_t stage = 117 + 31 * bn / 20;
-  return 10500 + 36 * bn + (units + pairs - 1) / pairs * ceil_div(K, stage_k(op)) * (stage > 288 ? stage : 288);
+  return 9000 + unit_cycles(groups * tiles * ceil_div(N, 2 * BM), bn, ceil_div(K, stage_k(op)));
 }
 
 // grouped_few.cu: up to 32 rows and 8 per group on average, while it has a few thousand CTAs
@@ -1333,11 +1337,11 @@ int64_t grouped_cycles(int op, int64_t G, int64_t M, int64_t N, int64_t K) {
 // rows of 4096 x 2048 7.5 / 10.6, of 14336 x 4096 36 / 39, 16 rows of one of four of 2048 x 2048 8.0
 // / 9.7, 32 of one 13.6 / 9.7; E4M3 2 rows of 4096 x 2048 5.9 / 9.1, 3 rows in each of 64 of 4096
 // x 2048 109 / 82.
-// few_rows.cu where its estimate is the lower, in E4M3 (whose start costs this file more) below
-// 1.4 times: it against this file: bf16 277 rows in each of two of 144 x 3840 9.4 / 16.1, 500 in
-// each of two of 256 x 2048 8.4 / 10.9, 60 in each of four of 4096 x 2048 19 / 14.6; E4M3 9 rows of
-// 248 x 10288 6.8 / 21, 4 in each of ten of 2728 x 2048 12.1 / 15.2, 2 in each of 64 of 512 x 1024 9.1
-// / 12.3, 300 in each of two of 4096 x 4096 19.7 / 15.3.
+// few_rows.cu where its estimate is the lower (on 60 sizes, 1.6% in E4M3 and 1.0% in bf16 behind
+// the better form on average).  It against this file: E4M3 184 rows in 15 groups of 152 x 11648
+// 10.9 / 21.6, 196 in seven of 1264 x 8016 18.1 / 19.5, 40 in ten of 2728 x 2048 12.8 / 13.9, 1235 in
+// one of 2376 x 2672 21.7 / 13.5, 2268 in six of 2656 x 288 15.4 / 9.4; bf16 the first 15.1 /
+// 34.7, 554 in two of 144 x 3840 9.7 / 15.6, 600 in two of 4096 x 4096 32 / 22.
 cudaError_t launch_grouped(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w, const uint8_t* w_scale,
                            const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K, cudaStream_t s) {
   if (M == 0) return cudaSuccess;
@@ -1346,7 +1350,7 @@ cudaError_t launch_grouped(uint16_t* out, const void* x, const uint8_t* x_scale,
     return launch_few_groups(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, s);
   const int64_t few = few_rows_grouped_cycles(G, M, N, K, fp8);
   const int64_t here = grouped_cycles(fp8 ? OP_BLOCKS : OP_BF16, G, M, N, K);
-  if (few >= 0 && 5 * few < (fp8 ? 7 : 5) * here)
+  if (few >= 0 && few < here)
     return launch_few_rows_grouped(out, x, x_scale, w, w_scale, offsets, G, M, N, K, s);
   if (fp8) return forward<OP_BLOCKS>(out, x, x_scale, w, w_scale, nullptr, nullptr, offsets, G, M, N, K, s);
   return forward<OP_BF16>(out, x, nullptr, w, nullptr, nullptr, nullptr, offsets, G, M, N, K, s);
