@@ -252,6 +252,29 @@ def test_grouped_backward_of_long_rows(q, G, M, N, K, kind, accumulate):
     assert bool(torch.isnan(dx[~live.cuda()]).all())
 
 
+@pytest.mark.parametrize("M", [17, 9000])
+def test_most_groups(q, M):
+    """4096 groups, the most: both products and the gradients, against the group of each row."""
+    G, N, K = 4096, 40, 48
+    off = _sizes("ragged", G, M)
+    x, dout, w = _t(1, M, K), _t(2, M, N, std=0.1), _t(3, G, N, K, std=0.1)
+    xq, xs, xv = _records(q, x, 1)
+    wq, ws, wv = _records(q, w, 128)
+    o, one, two = off.cuda(), _new(M, N), _new(M, N)
+    q.qffn_grouped_linear(one, x.cuda(), w.cuda(), o, G, M, N, K)
+    q.qffn_grouped_linear_fp8_blocks(two, xq, xs, wq, ws, o, G, M, N, K)
+    dx, dw = _new(M, K), _new(G, N, K)
+    q.qffn_grouped_linear_backward(dx, dw, dout.cuda(), x.cuda(), w.cuda(), o, G, M, N, K, False)
+    q.qffn_check_status()
+    want, bound, live = B.grouped(x.double(), w.double(), off)
+    P.check(one[live.cuda()], want[live], bound[live], "bf16")
+    want, bound, live = B.grouped(xv, wv, off)
+    P.check(two[live.cuda()], want[live], bound[live], "E4M3")
+    want_dx, want_dw, b_dx, b_dw, live = B.grouped_backward(dout.double(), x.double(), w.double(), off, None)
+    P.check(dx[live.cuda()], want_dx[live], b_dx[live], "dx")
+    P.check(dw, want_dw, b_dw, "dw")
+
+
 @pytest.mark.parametrize("M", [6, 40, 700])
 def test_grouped_backward_neighbours_do_not_mix(q, M):
     """A group that ends anywhere: what the next one, or no group, holds does not reach its gradients."""
