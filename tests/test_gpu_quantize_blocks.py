@@ -119,6 +119,13 @@ def test_rmsnorm(q, N, C, residual):
     B.check_blocks(*d, want, 2 * NORM_REL, "codes")
 
 
+@pytest.mark.parametrize("C", [528, 784, 1296, 2064, 4112, 6144, 6160, 8208, 10240, 10256, 12304, 14336, 14352, 16384])
+@pytest.mark.parametrize("few", [False, True])
+def test_rmsnorm_of_every_width(q, C, few):
+    """Rows on both sides of each number of threads, in calls of few rows and of many."""
+    test_rmsnorm(q, 5 if few else 5_100_000 // C, C, True)
+
+
 def test_rmsnorm_in_place_and_zero_rows(q):
     N, C = 20, 528
     x, res = _t(1, N, C), _t(2, N, C)
