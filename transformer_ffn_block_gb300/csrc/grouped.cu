@@ -537,8 +537,9 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
   // Takes the table, in pass 0 that of one group (false: the wait for it ran out).
   auto start = [&](int pass) -> bool {
     if (!grouped) return true;
-    // (the parity of the phase before the first has passed)
-    if (!mbar_wait(table_bar, uint32_t(pass ^ 1), abort_flag)) {
+    // (pass 0 reads the table of one group, there since the cluster's barrier, and waits for
+    // nothing: the real table's barrier completes one phase in a launch, which may be over)
+    if (pass == 1 && !mbar_wait(table_bar, 0, abort_flag)) {
       num_units = 0;
       return false;
     }
