@@ -158,6 +158,13 @@ QFFN_DEVI bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag
   return mbar_wait_bounded(bar, parity, abort_flag, &g_status, honour_abort, limit);
 }
 
+// Hands this CTA's shared memory over to the thread of the leader that waits on the leader's `bar`
+// (the writes are ordered before it by fence_proxy_async_smem() and __syncwarp()).
+QFFN_DEVI void hand_over(uint32_t bar, uint32_t rank) {
+  if (rank == 0) mbar_arrive(bar);
+  else mbar_arrive_remote(map_to_rank(bar, 0));
+}
+
 QFFN_DEVI void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // Sixteen lanes by 32 columns of TMEM at each of two addresses, without waiting
@@ -829,7 +836,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
       sts16(dst + 1024, make_uint4(x[4], x[5], x[6], x[7]));
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote_cta(map_to_rank(sfull_bar(mine), 0));
+      if (lane == 0) hand_over(sfull_bar(mine), rank);
       ++fills;
       c += SCALE_WARPS;
     }
@@ -860,7 +867,7 @@ __global__ void __launch_bounds__(num_threads(OP, KIND), 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote_cta(map_to_rank(cleared_bar(s), 0));
+        if (lane == 0) hand_over(cleared_bar(s), rank);
       }
       s = s + 1 == args.stages ? 0 : s + 1;
     }

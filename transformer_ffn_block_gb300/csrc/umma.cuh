@@ -80,13 +80,6 @@ QFFN_DEVI void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// Release at CTA scope: for handing over shared memory of this CTA that this SM's tensor
-// core reads (the threads' writes are ordered before it by fence_proxy_async_smem()).  The
-// release at cluster scope takes 1600 to 2000 cycles.
-QFFN_DEVI void mbar_arrive_remote_cta(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
 // 2-D tile load whose completion is signalled on a barrier of either CTA of
 // the pair (`bar` is a shared::cluster address).
 QFFN_DEVI void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
