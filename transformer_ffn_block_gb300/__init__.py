@@ -182,7 +182,7 @@ def _load_torch():
         _BF16.update((torch.bfloat16, torch.int16, torch.uint16))
         _F32.add(torch.float32)
         _E4M3.update((torch.float8_e4m3fn, torch.uint8))
-        _E8M0.update((torch.float8_e8m0fnu, torch.uint8))
+        _E8M0.update((getattr(torch, "float8_e8m0fnu", torch.uint8), torch.uint8))   # (not in every torch)
         _I32.add(torch.int32)
         if torch.cuda.is_available():
             torch.cuda.init()
