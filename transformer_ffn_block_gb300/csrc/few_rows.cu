@@ -675,9 +675,12 @@ int few_rows_bn(int64_t M) {
 }
 }  // namespace
 
-// Up to 512 rows: an estimate in SM cycles, fitted to measurements of 64 to 512
-// rows: 5700 for the call, per round of clusters 500 for each stage and 39 for
-// each row of a tile, 3900 for an exchange (beyond: -1).  Measured in us, here against
+// Up to `max_rows` rows (beyond: -1): an estimate in SM cycles, 5700 for the call, per
+// round of clusters 500 for each stage and 39 for each row of a tile, 3900 for an
+// exchange.  Fitted to 64 to 512 rows of the forms without block scales; with them, for
+// which it is asked up to 4096 rows, calls take 6150, 520, 37 and 1300 (11% rms on 70 sizes of 9
+// to 4000 rows), near enough that the choice by it (launch_linear_blocks) is 0.3%
+// behind the better form on average.  Measured in us, here against
 // linear.cu's forms: 64 rows of 2048 x 2048 6.9 / 8.2, of 4096 x 4096 10.6 / 12.9, of 4096 x
 // 14336 23.3 / 28.4, of 4096 x 1024 6.7 / 6.2, of 14336 x 4096 23.1 / 22.3, 128 rows of
 // 4096 x 4096 13.4 / 13.8, of 2048 x 2048 9.1 / 8.2, 256 rows of 14336 x 4096 33 / 27.5.

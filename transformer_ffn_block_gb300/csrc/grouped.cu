@@ -1302,7 +1302,9 @@ cudaError_t backward(uint16_t* dx, uint16_t* dw, const uint16_t* dout, const uin
 }  // namespace
 
 // An estimate of a call's SM cycles behind its start and end, beside those of few_rows.cu: 9 for
-// each row of a unit, and the stages at 117 + 1.55 bn and 440 at least.
+// each row of a unit, and the stages at 117 + 1.55 bn and 440 at least.  (Fitted to whole calls of
+// one round of units or a few, whose stages wait for their loads; cut_rows compares widths by the
+// 288 that a stage takes in a long unit.)
 int64_t unit_cycles(int64_t units, int64_t bn, int64_t num_kb) {
   const int64_t pairs = kNumSMsHint / 2, stage = 117 + 31 * bn / 20;
   return 9 * bn + (units + pairs - 1) / pairs * num_kb * (stage > 440 ? stage : 440);
@@ -1310,12 +1312,12 @@ int64_t unit_cycles(int64_t units, int64_t bn, int64_t num_kb) {
 
 // Which form a block-scaled layer takes.  grouped_few.cu up to 8 rows, and up to 16 and 32
 // while the weights are small: us, it against few_rows.cu and this file: 1 row of 4096 x 14336
-// 13.0 / 13.1 / 24, 9 of 3136 x 624 3.1 / 5.0 / 4.4, 15 of 632 x 2272 3.6 / 5.2 / 6.9, 16 of 4096 x
-// 4096 6.9 / 7.1 / 9.4, 10 of 1144 x 10960 8.3 / 6.9 / 20, 26 of 184 x 256 3.1 / 4.4 / 3.9, 22 of 6888
-// x 512 5.9 / 4.7 / 4.1.  few_rows.cu up to 4096 rows where nine tenths of its estimate are below
-// this file's, 5000 cycles for the call (the pair chosen on 70 sizes of 9 to 4000 rows is 0.3%
-// behind the better form on average): few_rows.cu against this, 64 rows of 4096 x 14336 14.6 / 24,
-// of 4096 x 4096 7.3 / 9.5, 256 of 4096 x 4096 10.6 / 10.5, 512 of 4096 x 4096 13.7 / 11.1, of 2048 x
+// 13.3 / 13.3 / 25, 9 of 3136 x 624 2.9 / 4.5 / 4.6, 15 of 632 x 2272 3.5 / 5.0 / 6.5, 16 of 4096 x
+// 4096 7.0 / 7.2 / 10.5, 10 of 1144 x 10960 8.6 / 6.9 / 20, 26 of 184 x 256 2.7 / 3.9 / 3.8, 22 of 6888
+// x 512 5.7 / 4.2 / 4.0.  few_rows.cu up to 4096 rows where nine tenths of its estimate are below
+// this file's, 6000 cycles for the call (the pair chosen on 70 sizes of 9 to 4000 rows is 0.3%
+// behind the better form on average): few_rows.cu against this, 64 rows of 4096 x 14336 14.4 / 25,
+// of 4096 x 4096 8.2 / 10.6, 256 of 4096 x 4096 10.7 / 10.5, 512 of 4096 x 4096 13.7 / 11.5, of 2048 x
 // 14336 21 / 25, 1700 of 152 x 11088 15 / 27, 2427 of 632 x 10016 25 / 21.
 cudaError_t launch_linear_blocks(uint16_t* out, const uint8_t* x, const uint8_t* x_scale, const uint8_t* w,
                                  const uint8_t* w_scale, const uint16_t* bias, const uint16_t* res, int64_t M, int64_t N,
@@ -1326,7 +1328,7 @@ cudaError_t launch_linear_blocks(uint16_t* out, const uint8_t* x, const uint8_t*
   const int64_t few = few_rows_cycles(M, N, K, false, true, 4096);
   if (few >= 0) {
     const int tiles_n = ceil_div(N, 2 * BM), bn = cut_rows(M, tiles_n, kNumSMsHint / 2);
-    const int64_t here = 5000 + unit_cycles(int64_t(ceil_div(M, bn)) * tiles_n, bn, ceil_div(K, 128));
+    const int64_t here = 6000 + unit_cycles(int64_t(ceil_div(M, bn)) * tiles_n, bn, ceil_div(K, 128));
     if (9 * few < 10 * here) return launch_few_rows_blocks(out, x, x_scale, w, w_scale, bias, res, M, N, K, s);
   }
   return forward<OP_BLOCKS>(out, x, x_scale, w, w_scale, bias, res, nullptr, 1, M, N, K, s);
@@ -1343,12 +1345,12 @@ int64_t grouped_cycles(int op, int64_t G, int64_t M, int64_t N, int64_t K) {
 // grouped_few.cu: up to 32 rows and 8 per group on average, while it has a few thousand CTAs
 // (each costs 1.6 ns in E4M3).  Measured, us, it against this file: bf16 2 rows, 2 groups with
 // rows of 4096 x 2048 7.5 / 10.6, of 14336 x 4096 36 / 39, 16 rows of one of four of 2048 x 2048 8.0
-// / 9.7, 32 of one 13.6 / 9.7; E4M3 2 rows of 4096 x 2048 5.9 / 9.1, 3 rows in each of 64 of 4096
-// x 2048 109 / 82.
-// few_rows.cu where its estimate is the lower (on 60 sizes, 1.6% in E4M3 and 1.0% in bf16 behind
+// / 9.7, 32 of one 13.6 / 9.7; E4M3 a row in each of two of 4096 x 2048 5.6 / 8.0, three in each
+// of 64 of 4096 x 2048 114 / 84.
+// few_rows.cu where its estimate is the lower (on 60 sizes, 2.3% in E4M3 and 1.1% in bf16 behind
 // the better form on average).  It against this file: E4M3 184 rows in 15 groups of 152 x 11648
-// 10.9 / 21.6, 196 in seven of 1264 x 8016 18.1 / 19.5, 40 in ten of 2728 x 2048 12.8 / 13.9, 1235 in
-// one of 2376 x 2672 21.7 / 13.5, 2268 in six of 2656 x 288 15.4 / 9.4; bf16 the first 15.1 /
+// 10.8 / 22.5, 196 in seven of 1264 x 8016 17.8 / 20.6, 40 in ten of 2728 x 2048 12.8 / 14.8, 1235 in
+// one of 2376 x 2672 21.8 / 13.9, 2268 in six of 2656 x 288 15.2 / 10.0; bf16 the first 15.1 /
 // 34.7, 554 in two of 144 x 3840 9.7 / 15.6, 600 in two of 4096 x 4096 32 / 22.
 cudaError_t launch_grouped(uint16_t* out, const void* x, const uint8_t* x_scale, const void* w, const uint8_t* w_scale,
                            const int* offsets, int64_t G, int64_t M, int64_t N, int64_t K, cudaStream_t s) {
