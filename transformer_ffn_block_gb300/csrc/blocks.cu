@@ -143,7 +143,8 @@ __global__ void __launch_bounds__(kThreads, SWIGLU ? 4 : 6) rows_kernel(uint16_t
 // FEW: the gain is requested with the row, for calls of few rows, which wait once; else
 // after the sums, from L1, which leaves registers for more rows at a time (4096 x 16384 91 us
 // with the gain in registers, 78 from L1).  Measured with a residual: 8192 x 4096 38.7 us (6.1
-// TB/s), 16384 x 1024 21 us (5.6), 1 x 4096 2.1 us.
+// TB/s), 16384 x 1024 21 us (5.6), 1 x 4096 2.1 us; without one, with half the loads in flight,
+// 8192 x 4096 20.4 us (4.9).
 template <int V, bool FEW>
 constexpr int rows_at_once() { return FEW || V > 2 ? 1 : V == 2 ? 2 : 4; }
 
